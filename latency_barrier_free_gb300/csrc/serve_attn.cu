@@ -1,0 +1,730 @@
+// serve_attn.cu -- attention over the 4-bit cache (rra_serve.h).
+//
+// A row is one query of one head.  With K' the codes (exact in binary16) and a
+// scale per 32 channels,
+//     s = sum_g scale_g (q_g . K'_g),   out = sum_keys (p scale_g) V'_g,
+// so the matrix instructions take codes as they are, and a scale costs one
+// multiply-add per score and group (K) or one multiply per weight and group (V).
+//
+// Work is split by keys.  A segment is the rows of one request and KV head
+// that fit the instructions (8 NT); its tiles are 32 keys each.  All
+// segments' tiles in a row are cut into equal runs, one per CTA, so that
+// ragged batches and single long requests load every SM alike.  A segment
+// that several CTAs share is joined by whichever finishes last, in the order
+// of the CTAs.
+//
+// Inside a CTA every warp walks its own tiles (every kWarps-th of the run) and
+// keeps its own ring of bulk copies in flight; warps meet only at the end of a
+// segment.
+#include <math.h>
+
+#include <algorithm>
+
+#include "cluster_prims.cuh"
+#include "kernel_attrs.h"
+#include "serve_common.cuh"
+
+namespace rra {
+
+constexpr int kAttnTile = 32;      // keys of one step of a warp
+constexpr int kAttnMaxCtas = 512;  // CTAs a workspace has room for
+constexpr int kAttnMinRun = 4;     // tiles a CTA takes at least
+constexpr uint32_t kAttnSpins = 1u << 22;  // tries of a wait before it gives up
+constexpr float kAttnSlack = 4.f;  // log2 of how far weights may pass 1 before the maximum moves
+
+// Start of the workspace: status word, then a counter for each CTA, then two
+// partial results for each CTA: maximum and sum of every row, then the rows.
+struct AttnWorkspace {
+    uint32_t status;
+    uint32_t pad[63];
+    uint32_t arrived[kAttnMaxCtas];
+    uint32_t pad_end[1024 - 64 - kAttnMaxCtas];
+};
+static_assert(sizeof(AttnWorkspace) == 4096, "the part of the workspace that starts as zero");
+constexpr int kAttnMaxRows = 16;
+
+struct AttnParams {
+    rra_kv_attention_args_t a;
+    float scale_log2;
+    int32_t group;  // query heads of a KV head
+};
+
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *(const uint32_t*)&h;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :
+                 : "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+// The queries and keys of request b, clamped to the buffers.
+struct AttnRequest {
+    int32_t q0, qn;       // first query token, how many
+    int32_t kv;           // keys
+    int32_t first_tile;   // tile of the first key that any query sees
+    int32_t tiles;        // tiles of one segment, at least one
+    int32_t chunks;       // segments of a KV head
+};
+template <int kRows>
+__device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int b) {
+    const rra_kv_attention_args_t& a = p.a;
+    AttnRequest r;
+    const int most_q = (int)a.tokens;
+    r.q0 = min(max(a.cu_q[b], 0), most_q);
+    r.qn = max(0, min(a.cu_q[b + 1], most_q) - r.q0);
+    const int64_t room = (int64_t)a.table_pages * a.cache.page_tokens;
+    r.kv = (int)min((int64_t)max(a.kv_len[b], 0), room);
+    int first = 0;
+    if (a.window > 0) first = (int)max((int64_t)0, (int64_t)r.kv - r.qn - a.window + 1);
+    r.first_tile = first / kAttnTile;
+    r.tiles = max(1, (r.kv + kAttnTile - 1) / kAttnTile - r.first_tile);
+    r.chunks = (int)(((int64_t)r.qn * p.group + kRows - 1) / kRows);
+    return r;
+}
+
+// A segment: rows of chunk c of KV head h of request b; tiles begin..end in
+// the row of all segments' tiles.
+struct AttnSegment {
+    AttnRequest r;
+    int32_t b, h, c;
+    int64_t begin, end;
+};
+template <int kRows>
+__device__ __forceinline__ void attn_next(const AttnParams& p, AttnSegment& s) {
+    if (++s.c >= s.r.chunks) {
+        s.c = 0;
+        if (++s.h == p.a.cache.kv_heads) {
+            s.h = 0;
+            do {
+                if (++s.b >= p.a.requests) {
+                    s.begin = s.end = INT64_MAX;
+                    return;
+                }
+                s.r = attn_request<kRows>(p, s.b);
+            } while (s.r.chunks == 0);
+        }
+    }
+    s.begin = s.end;
+    s.end += s.r.tiles;
+}
+
+template <int D, int NT, int kWarps, int kStages>
+struct AttnShape {
+    using B = KvBlock<D>;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kStage = 2 * B::kBytes;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kJoin = kWarps * 8 * D * 4;           // rows of one n-tile from every warp
+    static constexpr int kStats = kWarps * kRows * 2 * 4;      // maximum and sum of each row
+    static constexpr int kBars = kWarps * kStages * 8;
+    static constexpr int kFixed = kRing + kJoin + kStats + kBars;
+    static constexpr int kPartial = kRows * (D + 2);           // floats of one partial result
+    static size_t smem(int requests) { return (size_t)kFixed + 8 * ((size_t)requests + 1); }
+};
+
+template <int D, int NT, int kWarps, int kStages>
+__global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = AttnShape<D, NT, kWarps, kStages>;
+    using B = KvBlock<D>;
+    constexpr int J = B::kGroups, kRows = Sh::kRows;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int64_t warp_sum[kWarps];
+    __shared__ uint32_t is_last;
+    const rra_kv_attention_args_t& a = p.a;
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    float* const join = (float*)(smem + Sh::kRing);
+    float* const stats = (float*)(smem + Sh::kRing + Sh::kJoin);
+    int64_t* const sums = (int64_t*)(smem + Sh::kFixed);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * Sh::kStage);
+    const uint32_t bars = smem_u32(smem) + (uint32_t)(Sh::kRing + Sh::kJoin + Sh::kStats + warp * kStages * 8);
+    AttnWorkspace* const ws = (AttnWorkspace*)a.workspace;
+    float* const partials = (float*)(ws + 1);
+
+    pdl_release_early();
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    __syncwarp();
+    pdl_wait();
+
+    // running sums of the requests' tiles
+    int64_t total = 0;
+    for (int b0 = 0; b0 < a.requests; b0 += Sh::kThreads) {
+        const int b = b0 + tid;
+        int64_t v = 0;
+        if (b < a.requests) {
+            const AttnRequest r = attn_request<kRows>(p, b);
+            v = (int64_t)r.tiles * r.chunks * a.cache.kv_heads;
+        }
+        int64_t inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        int64_t before = total, all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += warp_sum[w];
+            all += warp_sum[w];
+        }
+        if (b < a.requests) sums[b] = before + inc - v;
+        total += all;
+        __syncthreads();
+    }
+    if (tid == 0) sums[a.requests] = total;
+    __syncthreads();
+    int64_t run = (total + gridDim.x - 1) / gridDim.x;
+    run = run < kAttnMinRun ? kAttnMinRun : run;
+    const int64_t w0 = (int64_t)blockIdx.x * run;
+    const int64_t w1 = w0 + run < total ? w0 + run : total;
+    if (w0 >= w1) return;
+
+    // this CTA's first segment
+    AttnSegment seg;
+    {
+        int low = 0, high = a.requests;
+        while (high - low > 1) {
+            const int mid = (low + high) >> 1;
+            if (sums[mid] <= w0) low = mid;
+            else high = mid;
+        }
+        seg.b = low;
+        seg.r = attn_request<kRows>(p, low);
+        const int64_t i = (w0 - sums[low]) / seg.r.tiles;
+        seg.h = (int)(i / seg.r.chunks);
+        seg.c = (int)(i % seg.r.chunks);
+        seg.begin = sums[low] + i * seg.r.tiles;
+        seg.end = seg.begin + seg.r.tiles;
+    }
+
+    // ---- copies: the tiles w0 + warp, + kWarps, ... in a ring of kStages ----
+    AttnSegment from = seg;         // segment of the next tile to copy
+    int64_t next = w0 + warp;       // that tile
+    int64_t held_to = next;         // tiles whose pages the lanes hold: up to here, lane i tile next + i * kWarps at load
+    int held_at = 0;                // lane that holds the next tile's pages
+    int page0 = -1, page1 = -1;
+    int put = 0;                    // stage of the next copy
+    uint32_t issued = 0;            // parity of the number of copies of each stage
+    uint32_t valid = 0;             // which blocks of each stage were copied, 2 bits a stage
+    const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
+    auto copy_next = [&]() {
+        if (next >= w1) return;
+        while (next >= from.end) {
+            attn_next<kRows>(p, from);
+            held_to = next;
+        }
+        if (next >= held_to) {  // pages of this warp's next 32 tiles of the segment
+            const int64_t mine = next + (int64_t)lane * kWarps;
+            page0 = page1 = -1;
+            if (mine < from.end && mine < w1) {
+                const int key = (from.r.first_tile + (int)(mine - from.begin)) * kAttnTile;
+                const int32_t* row = a.block_table + from.b * a.table_stride;
+                if (key < from.r.kv) page0 = row[key / ps];
+                if (key + kKvBlockTokens < from.r.kv) page1 = row[(key + kKvBlockTokens) / ps];
+            }
+            held_to = next + 32 * kWarps;
+            held_at = 0;
+        }
+        const int p0 = __shfl_sync(0xffffffffu, page0, held_at), p1 = __shfl_sync(0xffffffffu, page1, held_at);
+        const bool ok0 = p0 >= 0 && p0 < a.cache.num_pages, ok1 = p1 >= 0 && p1 < a.cache.num_pages;
+        valid = (valid & ~(3u << (2 * put))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * put);
+        if (lane == 0) {
+            const uint32_t bar = bars + 8 * put, dst = ring + put * Sh::kStage;
+            mbar_expect_tx(bar, ((ok0 ? 1u : 0u) + (ok1 ? 1u : 0u)) * (uint32_t)B::kBytes);
+            const int block0 = (from.r.first_tile + (int)(next - from.begin)) * 2;
+            const char* const pool = (const char*)a.cache.pages;
+            if (ok0)
+                bulk_g2s(dst, pool + (((int64_t)p0 * a.cache.kv_heads + from.h) * blocks + block0 % blocks) * B::kBytes,
+                         B::kBytes, bar);
+            if (ok1)
+                bulk_g2s(dst + B::kBytes,
+                         pool + (((int64_t)p1 * a.cache.kv_heads + from.h) * blocks + (block0 + 1) % blocks) * B::kBytes,
+                         B::kBytes, bar);
+        }
+        issued ^= 1u << put;
+        ++held_at;
+        next += kWarps;
+        put = put + 1 == kStages ? 0 : put + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) copy_next();
+
+    int64_t w = w0 + warp;
+    int take = 0;
+    uint32_t phase = 0;
+    bool dead = false;  // a wait ran out: no more copies, no more sums
+
+    while (seg.begin < w1) {
+        const int64_t stop = seg.end < w1 ? seg.end : w1;
+        const int rows = seg.r.qn * p.group;
+        // ---- queries of the segment as B operands, each row scaled to [1, 2) by a power of two ----
+        uint32_t q[NT][J][2][2];
+        float factor[NT][2];            // of columns 2 t, 2 t + 1: softmax scale times that power
+        int first_key[NT][2], end_key[NT][2];
+        int all_first = 0, all_end = INT32_MAX, any_first = INT32_MAX, any_end = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = seg.c * kRows + 8 * n + g;
+            float most = 0.f;
+            uint2 raw[J][2];
+            if (row < rows) {
+                const __nv_bfloat16* x = (const __nv_bfloat16*)a.q + (seg.r.q0 + row / p.group) * a.q_token_stride +
+                                         (seg.h * p.group + row % p.group) * a.q_head_stride;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) raw[j][s] = *(const uint2*)(x + 32 * j + 4 * (2 * t + s));
+            } else {
+#pragma unroll
+                for (int j = 0; j < J; ++j) raw[j][0] = raw[j][1] = make_uint2(0u, 0u);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)),
+                                                 fabsf(__uint_as_float(v[k] & 0xffff0000u))));
+                }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 : 0;
+            e = min(max(e, -120), 120);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        q[n][j][s][k] = pack_half2(__uint_as_float(v[k] << 16) * down,
+                                                   __uint_as_float(v[k] & 0xffff0000u) * down);
+                }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                factor[n][k] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + k) * 4);
+                const int r = seg.c * kRows + 8 * n + 2 * t + k;
+                int lo = 0, hi = 0;
+                if (r < rows) {
+                    const int pos = seg.r.kv - seg.r.qn + r / p.group;
+                    hi = a.causal ? max(0, min(seg.r.kv, pos + 1)) : seg.r.kv;
+                    lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)pos - a.window + 1) : 0;
+                    all_first = max(all_first, lo);
+                    all_end = min(all_end, hi);
+                    any_first = min(any_first, lo);
+                    any_end = max(any_end, hi);
+                }
+                first_key[n][k] = lo;
+                end_key[n][k] = hi;
+            }
+        }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            all_first = max(all_first, __shfl_xor_sync(0xffffffffu, all_first, o));
+            all_end = min(all_end, __shfl_xor_sync(0xffffffffu, all_end, o));
+            any_first = min(any_first, __shfl_xor_sync(0xffffffffu, any_first, o));
+            any_end = max(any_end, __shfl_xor_sync(0xffffffffu, any_end, o));
+        }
+
+        float m[NT][2], l[NT][2];
+        float acc[J][2][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[j][i][n][k] = 0.f;
+
+        // ---- tiles ----
+#pragma unroll 1
+        for (; w < stop; w += kWarps) {
+            const uint32_t bar = bars + 8 * take, tile = ring + take * Sh::kStage;
+            if (!dead) {
+                uint32_t tries = 0;
+                while (!mbar_try_wait(bar, (phase >> take) & 1u))
+                    if (++tries > kAttnSpins) {
+                        dead = true;
+                        if (lane == 0) atomicCAS(&ws->status, 0u, (uint32_t)RRA_ERR_TIMEOUT);
+                        break;
+                    }
+                dead = __any_sync(0xffffffffu, dead);
+            }
+            phase ^= 1u << take;
+            const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
+            const int key0 = (seg.r.first_tile + (int)(w - seg.begin)) * kAttnTile;
+            if (have != 0u) {
+                const bool whole = have == 3u && key0 >= all_first && key0 + kAttnTile <= all_end;
+                float s[2][NT][4];
+                // keys of this lane's score rows: block row (g >> 1) + 4 (g & 1), and 8 above
+                const int krow = (g >> 1) + 4 * (g & 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t base = tile + i * B::kBytes;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) s[i][n][k] = 0.f;
+                    uint32_t k0[J], k1[J], s0[J / 2], s1[J / 2];
+                    lds_words<J>(base + krow * B::kRow + t * 4 * J, k0);
+                    lds_words<J>(base + (krow + 8) * B::kRow + t * 4 * J, k1);
+                    lds_words<J / 2>(base + B::kScaleK + krow * B::kScaleRow, s0);
+                    lds_words<J / 2>(base + B::kScaleK + (krow + 8) * B::kScaleRow, s1);
+                    // word s * J/2 + j/2 holds, for group j (bytes 2 (j & 1), + 1), channels 32 j + 4 (2 t + s) + 0..3
+#pragma unroll
+                    for (int jj = 0; jj < J / 2; ++jj) {
+                        uint32_t x[2][4], y[2][4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            from_e2m1x8(k0[h * (J / 2) + jj], x[h]);
+                            from_e2m1x8(k1[h * (J / 2) + jj], y[h]);
+                        }
+                        const float2 f0 = __half22float2(*(const __half2*)&s0[jj]), f1 = __half22float2(*(const __half2*)&s1[jj]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    mma_f16(c, x[h][2 * e], y[h][2 * e], x[h][2 * e + 1], y[h][2 * e + 1],
+                                            q[n][2 * jj + e][h][0], q[n][2 * jj + e][h][1]);
+                                const float u = e ? f0.y : f0.x, v = e ? f1.y : f1.x;
+                                s[i][n][0] = fmaf(u, c[0], s[i][n][0]);
+                                s[i][n][1] = fmaf(u, c[1], s[i][n][1]);
+                                s[i][n][2] = fmaf(v, c[2], s[i][n][2]);
+                                s[i][n][3] = fmaf(v, c[3], s[i][n][3]);
+                            }
+                    }
+                }
+                // ---- scores in units of log2, masked; does any pass the running maximum? ----
+                bool passes = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float x = s[i][n][k] * factor[n][k & 1];
+                            if (!whole) {
+                                const int key = key0 + 16 * i + krow + 8 * (k >> 1);
+                                const bool seen = (have >> i & 1u) && key >= first_key[n][k & 1] && key < end_key[n][k & 1];
+                                x = seen ? x : -INFINITY;
+                            }
+                            s[i][n][k] = x;
+                            passes |= x > m[n][k & 1] + kAttnSlack;
+                        }
+                if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float top = fmaxf(fmaxf(s[0][n][k], s[0][n][k + 2]), fmaxf(s[1][n][k], s[1][n][k + 2]));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            top = fmaxf(top, m[n][k]);
+                            const float by = top == -INFINITY ? 1.f : exp2_fast(m[n][k] - top);
+                            m[n][k] = top;
+                            l[n][k] *= by;
+#pragma unroll
+                            for (int j = 0; j < J; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    acc[j][i][n][k] *= by;
+                                    acc[j][i][n][k + 2] *= by;
+                                }
+                        }
+                }
+                // ---- weights, and their products with the values ----
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t b0[NT], b1[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float top = m[n][k & 1];
+                            e[k] = exp2_fast(s[i][n][k] - (top == -INFINITY ? 0.f : top));
+                            l[n][k & 1] += e[k];
+                        }
+                        b0[n] = transpose8(pack_half2(e[0], e[1]));  // head g, keys t and t + 4
+                        b1[n] = transpose8(pack_half2(e[2], e[3]));  // head g, keys t + 8 and t + 12
+                    }
+                    if (!(have >> i & 1u)) continue;
+                    const uint32_t base = tile + i * B::kBytes;
+                    uint32_t v[4][J / 2], sv[4][J / 2];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        lds_words<J / 2>(base + B::kV + (t + 4 * r) * B::kRow + g * 2 * J, v[r]);
+                        lds_words<J / 2>(base + B::kScaleV + (t + 4 * r) * B::kScaleRow, sv[r]);
+                        if (!whole) {  // what no row sees may never have been written
+                            const int key = key0 + 16 * i + t + 4 * r;
+                            if (key < any_first || key >= any_end)
+#pragma unroll
+                                for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int jj = 0; jj < J / 2; ++jj) {
+                        // nibbles of two keys side by side: even channels in lo, odd ones in hi
+                        uint32_t x[2][4], y[2][4];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t u = v[2 * r][jj], z = v[2 * r + 1][jj];
+                            from_e2m1x8((u & 0x0f0f0f0fu) | ((z << 4) & 0xf0f0f0f0u), x[r]);
+                            from_e2m1x8(((u >> 4) & 0x0f0f0f0fu) | (z & 0xf0f0f0f0u), y[r]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t sel = e ? 0x7632u : 0x5410u;
+                            const uint32_t w0s = __byte_perm(sv[0][jj], sv[1][jj], sel), w1s = __byte_perm(sv[2][jj], sv[3][jj], sel);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const uint32_t p0 = mul_half2(b0[n], w0s), p1 = mul_half2(b1[n], w1s);
+#pragma unroll
+                                for (int d = 0; d < 2; ++d)
+                                    mma_f16(acc[2 * jj + e][d][n], x[0][2 * e + d], y[0][2 * e + d], x[1][2 * e + d],
+                                            y[1][2 * e + d], p0, p1);
+                            }
+                        }
+                    }
+                }
+            }
+            take = take + 1 == kStages ? 0 : take + 1;
+            __syncwarp();  // every lane has read the stage
+            if (!dead) copy_next();
+        }
+
+        // ---- join the warps, one n-tile at a time ----
+        const bool alone = seg.begin >= w0 && seg.end <= w1;
+        float* const partial = partials + ((int64_t)blockIdx.x * 2 + (seg.begin >= w0 ? 1 : 0)) * Sh::kPartial;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float sum = l[n][k];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (g == 0) {
+                    stats[(warp * kRows + 8 * n + 2 * t + k) * 2] = m[n][k];
+                    stats[(warp * kRows + 8 * n + 2 * t + k) * 2 + 1] = sum;
+                }
+            }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    *(float4*)(join + (warp * 8 + 2 * t + k) * D + 32 * j + 4 * g) =
+                        make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]);
+            __syncthreads();
+            for (int i = tid; i < 8 * D / 4; i += Sh::kThreads) {
+                const int r = i / (D / 4), d = i % (D / 4) * 4;
+                const int row = seg.c * kRows + 8 * n + r;
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) top = fmaxf(top, stats[(x * kRows + 8 * n + r) * 2]);
+                const float off = top == -INFINITY ? 0.f : top;
+                float sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) {
+                    const float2 st = *(const float2*)(stats + (x * kRows + 8 * n + r) * 2);
+                    const float by = exp2_fast(st.x - off);
+                    const float4 v = *(const float4*)(join + (x * 8 + r) * D + d);
+                    sum = fmaf(st.y, by, sum);
+                    o.x = fmaf(v.x, by, o.x);
+                    o.y = fmaf(v.y, by, o.y);
+                    o.z = fmaf(v.z, by, o.z);
+                    o.w = fmaf(v.w, by, o.w);
+                }
+                if (!alone) {
+                    *(float4*)(partial + 2 * kRows + (8 * n + r) * D + d) = o;
+                    if (d == 0) *(float2*)(partial + 2 * (8 * n + r)) = make_float2(top, sum);
+                } else if (row < rows) {
+                    const int token = seg.r.q0 + row / p.group, head = seg.h * p.group + row % p.group;
+                    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+                    *(uint2*)((__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride + d) =
+                        make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+                    if (a.lse != nullptr && d == 0)
+                        a.lse[(int64_t)token * a.q_heads + head] = (off + log2f(sum)) * 0.693147180559945309f;
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- join the CTAs that share the segment: the last to arrive adds them in order ----
+        if (!alone) {
+            const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) is_last = atomicAdd(&ws->arrived[i0], 1u) == (uint32_t)(i1 - i0) ? 1u : 0u;
+            __syncthreads();
+            if (is_last != 0u) {
+                __threadfence();
+                for (int i = tid; i < kRows * D / 4; i += Sh::kThreads) {
+                    const int r = i / (D / 4), d = i % (D / 4) * 4;
+                    const int row = seg.c * kRows + r;
+                    if (row >= rows) continue;
+                    float top = -INFINITY, sum = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int64_t step = 2 * Sh::kPartial;
+                    const float* const base = partials + (int64_t)i0 * step;
+#pragma unroll 4
+                    for (int x = i0; x <= i1; ++x) {
+                        const float* const src = base + (x - i0) * step + (x == i0 ? Sh::kPartial : 0);
+                        const float2 st = __ldcg((const float2*)(src + 2 * r));
+                        const float4 v = __ldcg((const float4*)(src + 2 * kRows + r * D + d));
+                        const float now = fmaxf(top, st.x), off = now == -INFINITY ? 0.f : now;
+                        const float keep = exp2_fast(top - off), by = exp2_fast(st.x - off);
+                        top = now;
+                        sum = sum * keep + st.y * by;
+                        o.x = o.x * keep + v.x * by;
+                        o.y = o.y * keep + v.y * by;
+                        o.z = o.z * keep + v.z * by;
+                        o.w = o.w * keep + v.w * by;
+                    }
+                    const int token = seg.r.q0 + row / p.group, head = seg.h * p.group + row % p.group;
+                    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+                    *(uint2*)((__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride + d) =
+                        make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+                    if (a.lse != nullptr && d == 0)
+                        a.lse[(int64_t)token * a.q_heads + head] =
+                            ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.693147180559945309f;
+                }
+                if (tid == 0) ws->arrived[i0] = 0u;
+            }
+            __syncthreads();
+        }
+        attn_next<kRows>(p, seg);
+    }
+    // Copies in flight at this point: none, or those that a wait gave up on.
+    if (dead)
+        for (int i = 0; i < kStages; ++i)
+            for (uint32_t tries = 0; tries < kAttnSpins && !mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u); ++tries) {}
+}
+
+template <int D, int NT, int kWarps, int kStages>
+static rra_status_t attn_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
+    using Sh = AttnShape<D, NT, kWarps, kStages>;
+    const void* k = (const void*)kv_attention_kernel<D, NT, kWarps, kStages>;
+    static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 1024, "shared memory");
+    if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
+        cudaGetLastError();
+        return RRA_ERR_CUDA;
+    }
+    void* args[] = {(void*)&p};
+    return serve_launch(k, dim3((unsigned)ctas), Sh::kThreads, Sh::smem(p.a.requests), 1, stream, args);
+}
+
+static bool attn_args_ok(const rra_kv_attention_args_t* a) {
+    if (a == nullptr || !kv_cache_ok(a->cache) || a->reserved != 0) return false;
+    const int hk = a->cache.kv_heads;
+    if (a->requests < 0 || a->requests > RRA_SERVE_MAX_REQUESTS || a->tokens < 0 || a->tokens > INT32_MAX / 2 ||
+        a->q_heads < 1 || a->q_heads % hk != 0 || a->table_pages < 0 || a->table_stride < a->table_pages ||
+        a->max_q < 0 || a->max_kv < 0 || a->window < 0 || !isfinite(a->scale))
+        return false;
+    // the rows of one KV head, and the keys of one request, are counted in 32 bits
+    if (a->tokens * (a->q_heads / hk) > INT32_MAX / 2 || (int64_t)a->table_pages * a->cache.page_tokens > INT32_MAX / 2)
+        return false;
+    if (!strides_ok(a->q_token_stride, a->q_head_stride, a->q_heads, a->cache.head_dim, 2) ||
+        !strides_ok(a->out_token_stride, a->out_head_stride, a->q_heads, a->cache.head_dim, 2) || !aligned16(a->q) ||
+        !aligned16(a->out) || ((uintptr_t)a->workspace & 255) != 0)
+        return false;
+    if (a->requests == 0 || a->tokens == 0) return true;
+    return a->q != nullptr && a->out != nullptr && a->cu_q != nullptr && a->kv_len != nullptr &&
+           (a->block_table != nullptr || a->table_pages == 0) && a->workspace != nullptr;
+}
+
+}  // namespace rra
+
+extern "C" {
+
+size_t rra_kv_attention_workspace_bytes(int head_dim) {
+    if (head_dim != 64 && head_dim != 128) return 0;
+    return sizeof(rra::AttnWorkspace) +
+           (size_t)rra::kAttnMaxCtas * 2 * rra::kAttnMaxRows * ((size_t)head_dim + 2) * sizeof(float);
+}
+
+rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
+    if (name == nullptr || !rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)std::max(args->max_q, 1) * (args->q_heads / args->cache.kv_heads);
+    *name = rows <= 8 ? "kv_attention_kernel<8 rows>" : "kv_attention_kernel<16 rows>";
+    return RRA_OK;
+}
+
+rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t stream) {
+    if (!rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
+    if (args->requests == 0 || args->tokens == 0) return RRA_OK;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return RRA_ERR_CUDA;
+    }
+    rra::AttnParams p;
+    p.a = *args;
+    p.scale_log2 = (float)(args->scale * 1.4426950408889634);
+    p.group = args->q_heads / args->cache.kv_heads;
+    const int64_t rows = (int64_t)std::max(args->max_q, 1) * p.group;
+    const int ctas = std::min(sms, rra::kAttnMaxCtas);
+    if (args->cache.head_dim == 128)
+        return rows <= 8 ? rra::attn_launch<128, 1, 8, 4>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 4>(p, ctas, stream);
+    return rows <= 8 ? rra::attn_launch<64, 1, 8, 4>(p, ctas, stream) : rra::attn_launch<64, 2, 8, 4>(p, ctas, stream);
+}
+
+}  // extern "C"

@@ -47,6 +47,8 @@ SYMBOLS = [
     "rra_allreduce_static",
     "rra_reduce_scatter", "rra_all_gather", "rra_broadcast", "rra_reduce",
     "rra_allreduce_residual",
+    "rra_slot_map", "rra_qk_norm_rope", "rra_kv_page_bytes", "rra_kv_append", "rra_kv_read", "rra_kv_attention",
+    "rra_kv_attention_workspace_bytes", "rra_kv_attention_plan",
 ]
 
 # The collectives besides AllReduce (all through distributed shared memory).
