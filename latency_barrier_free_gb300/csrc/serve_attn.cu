@@ -8,14 +8,13 @@
 //
 // Work is split by keys.  A segment is the rows of one request and KV head
 // that fit the instructions (8 NT); its tiles are 32 keys each.  All
-// segments' tiles in a row are cut into equal runs, one per CTA, so that
-// ragged batches and single long requests load every SM alike.  A segment
-// that several CTAs share is joined by whichever finishes last, in the order
-// of the CTAs.
-//
-// Inside a CTA every warp walks its own tiles (every kWarps-th of the run) and
-// keeps its own ring of bulk copies in flight; warps meet only at the end of a
-// segment.
+// segments' tiles in a row are cut into equal runs, one per warp, so that
+// ragged batches and single long requests load every scheduler alike.  A warp
+// walks its run with its own ring of bulk copies in flight and no barrier: what
+// it finds whole it writes out itself.  Of its first and last segment it may
+// have a piece only; those are joined once, at the end of the CTA, and across
+// CTAs by whichever finishes last, in the order of the runs.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -28,7 +27,8 @@ namespace rra {
 
 constexpr int kAttnTile = 32;      // keys of one step of a warp
 constexpr int kAttnMaxCtas = 512;  // CTAs a workspace has room for
-constexpr int kAttnMinRun = 4;     // tiles a CTA takes at least
+constexpr int kAttnMinRun = 2;     // tiles a warp takes at least
+constexpr int kAttnSegmentCost = 2;  // what starting and ending a segment costs, in tiles
 constexpr uint32_t kAttnSpins = 1u << 22;  // tries of a wait before it gives up
 constexpr float kAttnSlack = 4.f;  // log2 of how far weights may pass 1 before the maximum moves
 
@@ -55,6 +55,14 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same, from zero.
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -116,8 +124,8 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int b) 
     return r;
 }
 
-// A segment: rows of chunk c of KV head h of request b; tiles begin..end in
-// the row of all segments' tiles.
+// A segment: rows of chunk c of KV head h of request b.  In the row of all
+// segments it takes begin..end: first its cost, then its tiles.
 struct AttnSegment {
     AttnRequest r;
     int32_t b, h, c;
@@ -139,8 +147,16 @@ __device__ __forceinline__ void attn_next(const AttnParams& p, AttnSegment& s) {
         }
     }
     s.begin = s.end;
-    s.end += s.r.tiles;
+    s.end += s.r.tiles + kAttnSegmentCost;
 }
+
+// What a warp, or a CTA, has of a segment that others share.
+struct AttnPiece {
+    int32_t b, h, c;
+    int32_t flags;       // kHas, kStarts, kEnds
+    int64_t begin, end;  // the whole segment
+};
+enum { kHas = 1, kStarts = 2, kEnds = 4 };
 
 template <int D, int NT, int kWarps, int kStages>
 struct AttnShape {
@@ -148,14 +164,39 @@ struct AttnShape {
     static constexpr int kRows = 8 * NT;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStage = 2 * B::kBytes;
-    static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kJoin = kWarps * 8 * D * 4;           // rows of one n-tile from every warp
-    static constexpr int kStats = kWarps * kRows * 2 * 4;      // maximum and sum of each row
+    static constexpr int kPartial = kRows * (D + 2);           // floats of a piece: maximum and sum of each row, rows
+    static constexpr int kRing = kWarps * kStages * kStage;    // a warp's last piece goes where its ring was
+    static constexpr int kHeads = kWarps * kPartial * 4;       // a warp's first piece
     static constexpr int kBars = kWarps * kStages * 8;
-    static constexpr int kFixed = kRing + kJoin + kStats + kBars;
-    static constexpr int kPartial = kRows * (D + 2);           // floats of one partial result
+    static constexpr int kFixed = kRing + kHeads + kBars;
+    static_assert(kStages * kStage >= kPartial * 4, "a piece fits the ring");
     static size_t smem(int requests) { return (size_t)kFixed + 8 * ((size_t)requests + 1); }
 };
+
+// out and lse of one row (four channels) from sums: maximum top (in units of log2), sum, o.
+__device__ __forceinline__ void attn_store(const AttnParams& p, int q0, int h, int row, int d, float top, float sum,
+                                           float4 o, bool with_lse) {
+    const rra_kv_attention_args_t& a = p.a;
+    const int64_t token = q0 + row / p.group;
+    const int head = h * p.group + row % p.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: 0
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *(uint2*)((__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride + d) =
+        make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+    if (with_lse && a.lse != nullptr) a.lse[token * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
+}
+
+// Adds a piece's row (maximum and sum st, four channels v) to the running one.
+__device__ __forceinline__ void attn_add(float& top, float& sum, float4& o, float2 st, float4 v) {
+    const float now = fmaxf(top, st.x);
+    const float keep = exp2_fast(top - now), by = exp2_fast(st.x - now);
+    top = now;
+    sum = sum * keep + st.y * by;
+    o.x = o.x * keep + v.x * by;
+    o.y = o.y * keep + v.y * by;
+    o.z = o.z * keep + v.z * by;
+    o.w = o.w * keep + v.w * by;
+}
 
 template <int D, int NT, int kWarps, int kStages>
 __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __grid_constant__ AttnParams p) {
@@ -164,15 +205,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     constexpr int J = B::kGroups, kRows = Sh::kRows;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t warp_sum[kWarps];
+    __shared__ AttnPiece pieces[2 * kWarps];
     __shared__ uint32_t is_last;
     const rra_kv_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    float* const join = (float*)(smem + Sh::kRing);
-    float* const stats = (float*)(smem + Sh::kRing + Sh::kJoin);
     int64_t* const sums = (int64_t*)(smem + Sh::kFixed);
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * Sh::kStage);
-    const uint32_t bars = smem_u32(smem) + (uint32_t)(Sh::kRing + Sh::kJoin + Sh::kStats + warp * kStages * 8);
+    const uint32_t bars = smem_u32(smem) + (uint32_t)(Sh::kRing + Sh::kHeads + warp * kStages * 8);
+    // piece i of warp w (0 its first, 1 its last segment): statistics of the rows, then the rows
+    auto piece_at = [&](int w, int i) {
+        return (float*)(i == 0 ? smem + Sh::kRing + w * Sh::kPartial * 4 : smem + w * kStages * Sh::kStage);
+    };
     AttnWorkspace* const ws = (AttnWorkspace*)a.workspace;
     float* const partials = (float*)(ws + 1);
 
@@ -182,18 +226,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
+        pieces[2 * warp].flags = pieces[2 * warp + 1].flags = 0;
     }
     __syncwarp();
     pdl_wait();
 
-    // running sums of the requests' tiles
+    // running sums of the requests' segments
     int64_t total = 0;
     for (int b0 = 0; b0 < a.requests; b0 += Sh::kThreads) {
         const int b = b0 + tid;
         int64_t v = 0;
         if (b < a.requests) {
             const AttnRequest r = attn_request<kRows>(p, b);
-            v = (int64_t)r.tiles * r.chunks * a.cache.kv_heads;
+            v = (int64_t)(r.tiles + kAttnSegmentCost) * r.chunks * a.cache.kv_heads;
         }
         int64_t inc = v;
 #pragma unroll
@@ -215,454 +260,467 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     }
     if (tid == 0) sums[a.requests] = total;
     __syncthreads();
-    int64_t run = (total + gridDim.x - 1) / gridDim.x;
-    run = run < kAttnMinRun ? kAttnMinRun : run;
-    const int64_t w0 = (int64_t)blockIdx.x * run;
-    const int64_t w1 = w0 + run < total ? w0 + run : total;
-    if (w0 >= w1) return;
+    int64_t run = (total + (int64_t)gridDim.x * kWarps - 1) / ((int64_t)gridDim.x * kWarps);
+    run = run < kAttnMinRun + kAttnSegmentCost ? kAttnMinRun + kAttnSegmentCost : run;
+    const int64_t cta_run = run * kWarps;
+    if ((int64_t)blockIdx.x * cta_run >= total) return;
+    const int64_t r0 = (int64_t)blockIdx.x * cta_run + warp * run;
+    const int64_t r1 = r0 + run < total ? r0 + run : total;
 
-    // this CTA's first segment
-    AttnSegment seg;
-    {
-        int low = 0, high = a.requests;
-        while (high - low > 1) {
-            const int mid = (low + high) >> 1;
-            if (sums[mid] <= w0) low = mid;
-            else high = mid;
-        }
-        seg.b = low;
-        seg.r = attn_request<kRows>(p, low);
-        const int64_t i = (w0 - sums[low]) / seg.r.tiles;
-        seg.h = (int)(i / seg.r.chunks);
-        seg.c = (int)(i % seg.r.chunks);
-        seg.begin = sums[low] + i * seg.r.tiles;
-        seg.end = seg.begin + seg.r.tiles;
-    }
-
-    // ---- copies: the tiles w0 + warp, + kWarps, ... in a ring of kStages ----
-    AttnSegment from = seg;         // segment of the next tile to copy
-    int64_t next = w0 + warp;       // that tile
-    int64_t held_to = next;         // tiles whose pages the lanes hold: up to here, lane i tile next + i * kWarps at load
-    int held_at = 0;                // lane that holds the next tile's pages
-    int page0 = -1, page1 = -1;
-    int put = 0;                    // stage of the next copy
-    uint32_t issued = 0;            // parity of the number of copies of each stage
-    uint32_t valid = 0;             // which blocks of each stage were copied, 2 bits a stage
-    const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
-    auto copy_next = [&]() {
-        if (next >= w1) return;
-        while (next >= from.end) {
-            attn_next<kRows>(p, from);
-            held_to = next;
-        }
-        if (next >= held_to) {  // pages of this warp's next 32 tiles of the segment
-            const int64_t mine = next + (int64_t)lane * kWarps;
-            page0 = page1 = -1;
-            if (mine < from.end && mine < w1) {
-                const int key = (from.r.first_tile + (int)(mine - from.begin)) * kAttnTile;
-                const int32_t* row = a.block_table + from.b * a.table_stride;
-                if (key < from.r.kv) page0 = row[key / ps];
-                if (key + kKvBlockTokens < from.r.kv) page1 = row[(key + kKvBlockTokens) / ps];
+    if (r0 < r1) {
+        // this warp's first segment
+        AttnSegment seg;
+        {
+            int low = 0, high = a.requests;
+            while (high - low > 1) {
+                const int mid = (low + high) >> 1;
+                if (sums[mid] <= r0) low = mid;
+                else high = mid;
             }
-            held_to = next + 32 * kWarps;
-            held_at = 0;
+            seg.b = low;
+            seg.r = attn_request<kRows>(p, low);
+            const int each = seg.r.tiles + kAttnSegmentCost;
+            const int64_t i = (r0 - sums[low]) / each;
+            seg.h = (int)(i / seg.r.chunks);
+            seg.c = (int)(i % seg.r.chunks);
+            seg.begin = sums[low] + i * each;
+            seg.end = seg.begin + each;
         }
-        const int p0 = __shfl_sync(0xffffffffu, page0, held_at), p1 = __shfl_sync(0xffffffffu, page1, held_at);
-        const bool ok0 = p0 >= 0 && p0 < a.cache.num_pages, ok1 = p1 >= 0 && p1 < a.cache.num_pages;
-        valid = (valid & ~(3u << (2 * put))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * put);
-        if (lane == 0) {
-            const uint32_t bar = bars + 8 * put, dst = ring + put * Sh::kStage;
-            mbar_expect_tx(bar, ((ok0 ? 1u : 0u) + (ok1 ? 1u : 0u)) * (uint32_t)B::kBytes);
-            const int block0 = (from.r.first_tile + (int)(next - from.begin)) * 2;
-            const char* const pool = (const char*)a.cache.pages;
-            if (ok0)
-                bulk_g2s(dst, pool + (((int64_t)p0 * a.cache.kv_heads + from.h) * blocks + block0 % blocks) * B::kBytes,
-                         B::kBytes, bar);
-            if (ok1)
-                bulk_g2s(dst + B::kBytes,
-                         pool + (((int64_t)p1 * a.cache.kv_heads + from.h) * blocks + (block0 + 1) % blocks) * B::kBytes,
-                         B::kBytes, bar);
-        }
-        issued ^= 1u << put;
-        ++held_at;
-        next += kWarps;
-        put = put + 1 == kStages ? 0 : put + 1;
-    };
+        auto first_tile = [&](const AttnSegment& s) {
+            const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - kAttnSegmentCost;
+            return (int)(from > 0 ? from : 0);
+        };
+        auto end_tile = [&](const AttnSegment& s) {
+            const int64_t to = (s.end < r1 ? s.end : r1) - s.begin - kAttnSegmentCost;
+            return (int)(to > 0 ? to : 0);
+        };
+
+        // ---- copies, kStages tiles ahead.  Lane i holds the places of the run's next tiles but i. ----
+        AttnSegment from = seg;             // segment of the next tile to copy
+        int next = first_tile(seg), from_end = end_tile(seg);  // that tile, and the end of the run in its segment
+        int held = 0, held_end = 0;         // lane that holds the next tile, lanes that hold one
+        const char* src0 = nullptr;
+        const char* src1 = nullptr;
+        uint32_t ok0 = 0, ok1 = 0;          // which lanes' blocks exist
+        int put = 0;                        // stage of the next copy
+        uint32_t issued = 0;                // parity of the number of copies of each stage
+        uint32_t valid = 0;                 // which blocks of each stage were copied, 2 bits a stage
+        const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
+        auto copy_next = [&]() {
+            while (next >= from_end) {
+                if (from.end >= r1) return;
+                attn_next<kRows>(p, from);
+                next = first_tile(from);
+                from_end = end_tile(from);
+                held = held_end = 0;
+            }
+            if (held >= held_end) {
+                const int key = (from.r.first_tile + next + lane) * kAttnTile;
+                const int32_t* const row = a.block_table + from.b * a.table_stride;
+                src0 = src1 = nullptr;
+                auto place = [&](int k) -> const char* {
+                    if (next + lane >= from_end || k >= from.r.kv) return nullptr;
+                    const int i = k / ps, page = row[i];
+                    if (page < 0 || page >= a.cache.num_pages) return nullptr;
+                    return (const char*)a.cache.pages +
+                           (((int64_t)page * a.cache.kv_heads + from.h) * blocks + (k - i * ps) / kKvBlockTokens) * B::kBytes;
+                };
+                src0 = place(key);
+                src1 = place(key + kKvBlockTokens);
+                ok0 = __ballot_sync(0xffffffffu, src0 != nullptr);
+                ok1 = __ballot_sync(0xffffffffu, src1 != nullptr);
+                held = 0;
+                held_end = min(32, from_end - next);
+            }
+            if (lane == held) {
+                const uint32_t bar = bars + 8 * put, dst = ring + put * Sh::kStage;
+                const bool h0 = src0 != nullptr, h1 = src1 != nullptr;
+                mbar_expect_tx(bar, ((h0 ? 1u : 0u) + (h1 ? 1u : 0u)) * (uint32_t)B::kBytes);
+                if (h0 && src1 == src0 + B::kBytes) {
+                    bulk_g2s(dst, src0, 2 * B::kBytes, bar);
+                } else {
+                    if (h0) bulk_g2s(dst, src0, B::kBytes, bar);
+                    if (h1) bulk_g2s(dst + B::kBytes, src1, B::kBytes, bar);
+                }
+            }
+            valid = (valid & ~(3u << (2 * put))) | ((ok0 >> held & 1u) | (ok1 >> held & 1u) << 1) << (2 * put);
+            issued ^= 1u << put;
+            ++held;
+            ++next;
+            put = put + 1 == kStages ? 0 : put + 1;
+        };
 #pragma unroll 1
-    for (int i = 0; i < kStages; ++i) copy_next();
+        for (int i = 0; i < kStages; ++i) copy_next();
 
-    int64_t w = w0 + warp;
-    int take = 0;
-    uint32_t phase = 0;
-    bool dead = false;  // a wait ran out: no more copies, no more sums
+        int take = 0;
+        uint32_t phase = 0;
+        bool dead = false;  // a wait ran out: no more copies, no more sums
 
-    while (seg.begin < w1) {
-        const int64_t stop = seg.end < w1 ? seg.end : w1;
-        const int rows = seg.r.qn * p.group;
-        // ---- queries of the segment as B operands, each row scaled to [1, 2) by a power of two ----
-        uint32_t q[NT][J][2][2];
-        float factor[NT][2];            // of columns 2 t, 2 t + 1: softmax scale times that power
-        int first_key[NT][2], end_key[NT][2];
-        int all_first = 0, all_end = INT32_MAX, any_first = INT32_MAX, any_end = 0;
+        while (true) {
+            const int rows = seg.r.qn * p.group;
+            const int tile0 = first_tile(seg), tile1 = end_tile(seg);
+            // ---- queries of the segment as B operands, each row scaled to [1, 2) by a power of two ----
+            uint32_t q[NT][J][2][2];
+            float factor[NT][2];  // of columns 2 t, 2 t + 1: |softmax scale| times that power, above 0
+            int first_key[NT][2], end_key[NT][2];
+            int all_first = 0, all_end = INT32_MAX, any_first = INT32_MAX, any_end = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = seg.c * kRows + 8 * n + g;
-            float most = 0.f;
-            uint2 raw[J][2];
-            if (row < rows) {
-                const __nv_bfloat16* x = (const __nv_bfloat16*)a.q + (seg.r.q0 + row / p.group) * a.q_token_stride +
-                                         (seg.h * p.group + row % p.group) * a.q_head_stride;
+            for (int n = 0; n < NT; ++n) {
+                const int row = seg.c * kRows + 8 * n + g;
+                float most = 0.f;
+                uint2 raw[J][2];
+                if (row < rows && tile0 < tile1) {
+                    const __nv_bfloat16* x = (const __nv_bfloat16*)a.q + (seg.r.q0 + row / p.group) * a.q_token_stride +
+                                             (seg.h * p.group + row % p.group) * a.q_head_stride;
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) raw[j][s] = *(const uint2*)(x + 32 * j + 4 * (2 * t + s));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) raw[j][0] = raw[j][1] = make_uint2(0u, 0u);
+                }
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) raw[j][s] = *(const uint2*)(x + 32 * j + 4 * (2 * t + s));
-            } else {
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
 #pragma unroll
-                for (int j = 0; j < J; ++j) raw[j][0] = raw[j][1] = make_uint2(0u, 0u);
+                        for (int k = 0; k < 2; ++k)
+                            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)),
+                                                     fabsf(__uint_as_float(v[k] & 0xffff0000u))));
+                    }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 : 0;
+                e = min(max(e, -120), 120);
+                float f = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23);
+                float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                if (p.scale_log2 < 0.f) down = -down;
+                if (f == 0.f) f = 1.f, down = 0.f;  // every score is 0
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            q[n][j][s][k] = pack_half2(__uint_as_float(v[k] << 16) * down,
+                                                       __uint_as_float(v[k] & 0xffff0000u) * down);
+                    }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    factor[n][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
+                    const int r = seg.c * kRows + 8 * n + 2 * t + k;
+                    int lo = 0, hi = 0;
+                    if (r < rows) {
+                        const int pos = seg.r.kv - seg.r.qn + r / p.group;
+                        hi = a.causal ? max(0, min(seg.r.kv, pos + 1)) : seg.r.kv;
+                        lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)pos - a.window + 1) : 0;
+                        all_first = max(all_first, lo);
+                        all_end = min(all_end, hi);
+                        any_first = min(any_first, lo);
+                        any_end = max(any_end, hi);
+                    }
+                    first_key[n][k] = lo;
+                    end_key[n][k] = hi;
+                }
             }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                all_first = max(all_first, __shfl_xor_sync(0xffffffffu, all_first, o));
+                all_end = min(all_end, __shfl_xor_sync(0xffffffffu, all_end, o));
+                any_first = min(any_first, __shfl_xor_sync(0xffffffffu, any_first, o));
+                any_end = max(any_end, __shfl_xor_sync(0xffffffffu, any_end, o));
+            }
+
+            // Maximum m, the score that moves it, sum l; -FLT_MAX stands for no key yet.  m is one of the scores, and
+            // weights are 2^((s - m) factor): with s factor - m factor, rounded apart, huge scores would overflow.
+            float m[NT][2], limit[NT][2], l[NT][2];
+            float acc[J][2][NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) m[n][k] = limit[n][k] = -FLT_MAX, l[n][k] = 0.f;
 #pragma unroll
             for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)),
-                                                 fabsf(__uint_as_float(v[k] & 0xffff0000u))));
-                }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 : 0;
-            e = min(max(e, -120), 120);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        q[n][j][s][k] = pack_half2(__uint_as_float(v[k] << 16) * down,
-                                                   __uint_as_float(v[k] & 0xffff0000u) * down);
-                }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                factor[n][k] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + k) * 4);
-                const int r = seg.c * kRows + 8 * n + 2 * t + k;
-                int lo = 0, hi = 0;
-                if (r < rows) {
-                    const int pos = seg.r.kv - seg.r.qn + r / p.group;
-                    hi = a.causal ? max(0, min(seg.r.kv, pos + 1)) : seg.r.kv;
-                    lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)pos - a.window + 1) : 0;
-                    all_first = max(all_first, lo);
-                    all_end = min(all_end, hi);
-                    any_first = min(any_first, lo);
-                    any_end = max(any_end, hi);
-                }
-                first_key[n][k] = lo;
-                end_key[n][k] = hi;
-            }
-        }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            all_first = max(all_first, __shfl_xor_sync(0xffffffffu, all_first, o));
-            all_end = min(all_end, __shfl_xor_sync(0xffffffffu, all_end, o));
-            any_first = min(any_first, __shfl_xor_sync(0xffffffffu, any_first, o));
-            any_end = max(any_end, __shfl_xor_sync(0xffffffffu, any_end, o));
-        }
-
-        float m[NT][2], l[NT][2];
-        float acc[J][2][NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[j][i][n][k] = 0.f;
-
-        // ---- tiles ----
-#pragma unroll 1
-        for (; w < stop; w += kWarps) {
-            const uint32_t bar = bars + 8 * take, tile = ring + take * Sh::kStage;
-            if (!dead) {
-                uint32_t tries = 0;
-                while (!mbar_try_wait(bar, (phase >> take) & 1u))
-                    if (++tries > kAttnSpins) {
-                        dead = true;
-                        if (lane == 0) atomicCAS(&ws->status, 0u, (uint32_t)RRA_ERR_TIMEOUT);
-                        break;
-                    }
-                dead = __any_sync(0xffffffffu, dead);
-            }
-            phase ^= 1u << take;
-            const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
-            const int key0 = (seg.r.first_tile + (int)(w - seg.begin)) * kAttnTile;
-            if (have != 0u) {
-                const bool whole = have == 3u && key0 >= all_first && key0 + kAttnTile <= all_end;
-                float s[2][NT][4];
-                // keys of this lane's score rows: block row (g >> 1) + 4 (g & 1), and 8 above
-                const int krow = (g >> 1) + 4 * (g & 1);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t base = tile + i * B::kBytes;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) s[i][n][k] = 0.f;
-                    uint32_t k0[J], k1[J], s0[J / 2], s1[J / 2];
-                    lds_words<J>(base + krow * B::kRow + t * 4 * J, k0);
-                    lds_words<J>(base + (krow + 8) * B::kRow + t * 4 * J, k1);
-                    lds_words<J / 2>(base + B::kScaleK + krow * B::kScaleRow, s0);
-                    lds_words<J / 2>(base + B::kScaleK + (krow + 8) * B::kScaleRow, s1);
-                    // word s * J/2 + j/2 holds, for group j (bytes 2 (j & 1), + 1), channels 32 j + 4 (2 t + s) + 0..3
-#pragma unroll
-                    for (int jj = 0; jj < J / 2; ++jj) {
-                        uint32_t x[2][4], y[2][4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            from_e2m1x8(k0[h * (J / 2) + jj], x[h]);
-                            from_e2m1x8(k1[h * (J / 2) + jj], y[h]);
-                        }
-                        const float2 f0 = __half22float2(*(const __half2*)&s0[jj]), f1 = __half22float2(*(const __half2*)&s1[jj]);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    mma_f16(c, x[h][2 * e], y[h][2 * e], x[h][2 * e + 1], y[h][2 * e + 1],
-                                            q[n][2 * jj + e][h][0], q[n][2 * jj + e][h][1]);
-                                const float u = e ? f0.y : f0.x, v = e ? f1.y : f1.x;
-                                s[i][n][0] = fmaf(u, c[0], s[i][n][0]);
-                                s[i][n][1] = fmaf(u, c[1], s[i][n][1]);
-                                s[i][n][2] = fmaf(v, c[2], s[i][n][2]);
-                                s[i][n][3] = fmaf(v, c[3], s[i][n][3]);
-                            }
-                    }
-                }
-                // ---- scores in units of log2, masked; does any pass the running maximum? ----
-                bool passes = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float x = s[i][n][k] * factor[n][k & 1];
-                            if (!whole) {
-                                const int key = key0 + 16 * i + krow + 8 * (k >> 1);
-                                const bool seen = (have >> i & 1u) && key >= first_key[n][k & 1] && key < end_key[n][k & 1];
-                                x = seen ? x : -INFINITY;
-                            }
-                            s[i][n][k] = x;
-                            passes |= x > m[n][k & 1] + kAttnSlack;
+                        for (int k = 0; k < 4; ++k) acc[j][i][n][k] = 0.f;
+
+            // ---- tiles ----
+#pragma unroll 1
+            for (int tl = tile0; tl < tile1; ++tl) {
+                const uint32_t bar = bars + 8 * take, tile = ring + take * Sh::kStage;
+                if (!dead) {
+                    uint32_t tries = 0;
+                    while (!mbar_try_wait(bar, (phase >> take) & 1u))
+                        if (++tries > kAttnSpins) {
+                            dead = true;
+                            if (lane == 0) atomicCAS(&ws->status, 0u, (uint32_t)RRA_ERR_TIMEOUT);
+                            break;
                         }
-                if (__any_sync(0xffffffffu, passes)) {
+                    dead = __any_sync(0xffffffffu, dead);
+                }
+                phase ^= 1u << take;
+                const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
+                const int key0 = (seg.r.first_tile + tl) * kAttnTile;
+                if (have != 0u) {
+                    const bool whole = have == 3u && key0 >= all_first && key0 + kAttnTile <= all_end;
+                    float s[2][NT][4];
+                    // keys of this lane's score rows: block row (g >> 1) + 4 (g & 1), and 8 above
+                    const int krow = (g >> 1) + 4 * (g & 1);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t base = tile + i * B::kBytes;
+                        uint32_t k0[J], k1[J], s0[J / 2], s1[J / 2];
+                        lds_words<J>(base + krow * B::kRow + t * 4 * J, k0);
+                        lds_words<J>(base + (krow + 8) * B::kRow + t * 4 * J, k1);
+                        lds_words<J / 2>(base + B::kScaleK + krow * B::kScaleRow, s0);
+                        lds_words<J / 2>(base + B::kScaleK + (krow + 8) * B::kScaleRow, s1);
+                        // word s * J/2 + j/2 holds, for group j (bytes 2 (j & 1), + 1), channels 32 j + 4 (2 t + s) + 0..3
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float top = fmaxf(fmaxf(s[0][n][k], s[0][n][k + 2]), fmaxf(s[1][n][k], s[1][n][k + 2]));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                            top = fmaxf(top, m[n][k]);
-                            const float by = top == -INFINITY ? 1.f : exp2_fast(m[n][k] - top);
-                            m[n][k] = top;
-                            l[n][k] *= by;
+                        for (int jj = 0; jj < J / 2; ++jj) {
+                            uint32_t x[2][4], y[2][4];
 #pragma unroll
-                            for (int j = 0; j < J; ++j)
+                            for (int h = 0; h < 2; ++h) {
+                                from_e2m1x8(k0[h * (J / 2) + jj], x[h]);
+                                from_e2m1x8(k1[h * (J / 2) + jj], y[h]);
+                            }
+                            const float2 f0 = __half22float2(*(const __half2*)&s0[jj]), f1 = __half22float2(*(const __half2*)&s1[jj]);
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    acc[j][i][n][k] *= by;
-                                    acc[j][i][n][k + 2] *= by;
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    float c[4];
+                                    const uint32_t(*qj)[2] = q[n][2 * jj + e];
+                                    mma_f16_first(c, x[0][2 * e], y[0][2 * e], x[0][2 * e + 1], y[0][2 * e + 1], qj[0][0], qj[0][1]);
+                                    mma_f16(c, x[1][2 * e], y[1][2 * e], x[1][2 * e + 1], y[1][2 * e + 1], qj[1][0], qj[1][1]);
+                                    const float u = e ? f0.y : f0.x, v = e ? f1.y : f1.x;
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float w = k < 2 ? u : v;
+                                        s[i][n][k] = jj + e == 0 ? w * c[k] : fmaf(w, c[k], s[i][n][k]);
+                                    }
                                 }
                         }
-                }
-                // ---- weights, and their products with the values ----
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t b0[NT], b1[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float e[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float top = m[n][k & 1];
-                            e[k] = exp2_fast(s[i][n][k] - (top == -INFINITY ? 0.f : top));
-                            l[n][k & 1] += e[k];
-                        }
-                        b0[n] = transpose8(pack_half2(e[0], e[1]));  // head g, keys t and t + 4
-                        b1[n] = transpose8(pack_half2(e[2], e[3]));  // head g, keys t + 8 and t + 12
                     }
-                    if (!(have >> i & 1u)) continue;
-                    const uint32_t base = tile + i * B::kBytes;
-                    uint32_t v[4][J / 2], sv[4][J / 2];
+                    // ---- does a score pass the running maximum? ----
+                    bool passes = false;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        lds_words<J / 2>(base + B::kV + (t + 4 * r) * B::kRow + g * 2 * J, v[r]);
-                        lds_words<J / 2>(base + B::kScaleV + (t + 4 * r) * B::kScaleRow, sv[r]);
-                        if (!whole) {  // what no row sees may never have been written
-                            const int key = key0 + 16 * i + t + 4 * r;
-                            if (key < any_first || key >= any_end)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                                for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = 0u;
-                        }
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (!whole) {
+                                    const int key = key0 + 16 * i + krow + 8 * (k >> 1);
+                                    const bool seen = (have >> i & 1u) && key >= first_key[n][k & 1] && key < end_key[n][k & 1];
+                                    s[i][n][k] = seen ? s[i][n][k] : -INFINITY;
+                                }
+                                passes |= s[i][n][k] > limit[n][k & 1];
+                            }
+                    if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float top = fmaxf(fmaxf(s[0][n][k], s[0][n][k + 2]), fmaxf(s[1][n][k], s[1][n][k + 2]));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                                top = fmaxf(top, m[n][k]);
+                                const float by = exp2_fast((m[n][k] - top) * factor[n][k]);
+                                m[n][k] = top;
+                                limit[n][k] = top + __fdividef(kAttnSlack, factor[n][k]);
+                                l[n][k] *= by;
+#pragma unroll
+                                for (int j = 0; j < J; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        acc[j][i][n][k] *= by;
+                                        acc[j][i][n][k + 2] *= by;
+                                    }
+                            }
                     }
+                    // ---- weights, and their products with the values ----
 #pragma unroll
-                    for (int jj = 0; jj < J / 2; ++jj) {
-                        // nibbles of two keys side by side: even channels in lo, odd ones in hi
-                        uint32_t x[2][4], y[2][4];
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t b0[NT], b1[NT];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t u = v[2 * r][jj], z = v[2 * r + 1][jj];
-                            from_e2m1x8((u & 0x0f0f0f0fu) | ((z << 4) & 0xf0f0f0f0u), x[r]);
-                            from_e2m1x8(((u >> 4) & 0x0f0f0f0fu) | (z & 0xf0f0f0f0u), y[r]);
+                        for (int n = 0; n < NT; ++n) {
+                            float e[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                e[k] = exp2_fast((s[i][n][k] - m[n][k & 1]) * factor[n][k & 1]);
+                                l[n][k & 1] += e[k];
+                            }
+                            b0[n] = transpose8(pack_half2(e[0], e[1]));  // head g, keys t and t + 4
+                            b1[n] = transpose8(pack_half2(e[2], e[3]));  // head g, keys t + 8 and t + 12
+                        }
+                        if (!(have >> i & 1u)) continue;
+                        const uint32_t base = tile + i * B::kBytes;
+                        uint32_t v[4][J / 2], sv[4][J / 2];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            lds_words<J / 2>(base + B::kV + (t + 4 * r) * B::kRow + g * 2 * J, v[r]);
+                            lds_words<J / 2>(base + B::kScaleV + (t + 4 * r) * B::kScaleRow, sv[r]);
+                            if (!whole) {  // what no row sees may never have been written
+                                const int key = key0 + 16 * i + t + 4 * r;
+                                if (key < any_first || key >= any_end)
+#pragma unroll
+                                    for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = 0u;
+                            }
                         }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t sel = e ? 0x7632u : 0x5410u;
-                            const uint32_t w0s = __byte_perm(sv[0][jj], sv[1][jj], sel), w1s = __byte_perm(sv[2][jj], sv[3][jj], sel);
+                        for (int jj = 0; jj < J / 2; ++jj) {
+                            // nibbles of two keys side by side: even channels in x, odd ones in y
+                            uint32_t x[2][4], y[2][4];
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                const uint32_t p0 = mul_half2(b0[n], w0s), p1 = mul_half2(b1[n], w1s);
+                            for (int r = 0; r < 2; ++r) {
+                                const uint32_t u = v[2 * r][jj], z = v[2 * r + 1][jj];
+                                from_e2m1x8((u & 0x0f0f0f0fu) | ((z << 4) & 0xf0f0f0f0u), x[r]);
+                                from_e2m1x8(((u >> 4) & 0x0f0f0f0fu) | (z & 0xf0f0f0f0u), y[r]);
+                            }
 #pragma unroll
-                                for (int d = 0; d < 2; ++d)
-                                    mma_f16(acc[2 * jj + e][d][n], x[0][2 * e + d], y[0][2 * e + d], x[1][2 * e + d],
-                                            y[1][2 * e + d], p0, p1);
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t sel = e ? 0x7632u : 0x5410u;
+                                const uint32_t w0s = __byte_perm(sv[0][jj], sv[1][jj], sel), w1s = __byte_perm(sv[2][jj], sv[3][jj], sel);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const uint32_t p0 = mul_half2(b0[n], w0s), p1 = mul_half2(b1[n], w1s);
+#pragma unroll
+                                    for (int d = 0; d < 2; ++d)
+                                        mma_f16(acc[2 * jj + e][d][n], x[0][2 * e + d], y[0][2 * e + d], x[1][2 * e + d],
+                                                y[1][2 * e + d], p0, p1);
+                                }
                             }
                         }
                     }
                 }
+                take = take + 1 == kStages ? 0 : take + 1;
+                __syncwarp();  // every lane has read the stage
+                if (!dead) copy_next();
             }
-            take = take + 1 == kStages ? 0 : take + 1;
-            __syncwarp();  // every lane has read the stage
-            if (!dead) copy_next();
-        }
 
-        // ---- join the warps, one n-tile at a time ----
-        const bool alone = seg.begin >= w0 && seg.end <= w1;
-        float* const partial = partials + ((int64_t)blockIdx.x * 2 + (seg.begin >= w0 ? 1 : 0)) * Sh::kPartial;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float sum = l[n][k];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                if (g == 0) {
-                    stats[(warp * kRows + 8 * n + 2 * t + k) * 2] = m[n][k];
-                    stats[(warp * kRows + 8 * n + 2 * t + k) * 2 + 1] = sum;
-                }
+            // ---- the segment's end in this run: written out if whole, else kept as a piece ----
+            const bool starts = seg.begin >= r0, ends = seg.end <= r1;
+            const int which = starts ? 1 : 0;
+            float* const piece = piece_at(warp, which);
+            if (!(starts && ends)) {
+                if (which == 1 && dead)  // the ring must be quiet before it is written
+                    for (int i = 0; i < kStages; ++i)
+                        for (uint32_t tries = 0; tries < kAttnSpins && !mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u); ++tries) {}
+                __syncwarp();
+                if (lane == 0)
+                    pieces[2 * warp + which] =
+                        AttnPiece{seg.b, seg.h, seg.c, kHas | (starts ? kStarts : 0) | (ends ? kEnds : 0), seg.begin, seg.end};
             }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+                for (int k = 0; k < 2; ++k) {
+                    float sum = l[n][k];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    const int r = 8 * n + 2 * t + k, row = seg.c * kRows + r;
+                    const float top = m[n][k] * factor[n][k];  // in units of log2
+                    if (!(starts && ends) && g == 0) *(float2*)(piece + 2 * r) = make_float2(top, sum);
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    *(float4*)(join + (warp * 8 + 2 * t + k) * D + 32 * j + 4 * g) =
-                        make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]);
-            __syncthreads();
-            for (int i = tid; i < 8 * D / 4; i += Sh::kThreads) {
-                const int r = i / (D / 4), d = i % (D / 4) * 4;
-                const int row = seg.c * kRows + 8 * n + r;
-                float top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) top = fmaxf(top, stats[(x * kRows + 8 * n + r) * 2]);
-                const float off = top == -INFINITY ? 0.f : top;
-                float sum = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float2 st = *(const float2*)(stats + (x * kRows + 8 * n + r) * 2);
-                    const float by = exp2_fast(st.x - off);
-                    const float4 v = *(const float4*)(join + (x * 8 + r) * D + d);
-                    sum = fmaf(st.y, by, sum);
-                    o.x = fmaf(v.x, by, o.x);
-                    o.y = fmaf(v.y, by, o.y);
-                    o.z = fmaf(v.z, by, o.z);
-                    o.w = fmaf(v.w, by, o.w);
-                }
-                if (!alone) {
-                    *(float4*)(partial + 2 * kRows + (8 * n + r) * D + d) = o;
-                    if (d == 0) *(float2*)(partial + 2 * (8 * n + r)) = make_float2(top, sum);
-                } else if (row < rows) {
-                    const int token = seg.r.q0 + row / p.group, head = seg.h * p.group + row % p.group;
-                    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-                    *(uint2*)((__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride + d) =
-                        make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
-                    if (a.lse != nullptr && d == 0)
-                        a.lse[(int64_t)token * a.q_heads + head] = (off + log2f(sum)) * 0.693147180559945309f;
-                }
-            }
-            __syncthreads();
-        }
-
-        // ---- join the CTAs that share the segment: the last to arrive adds them in order ----
-        if (!alone) {
-            const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) is_last = atomicAdd(&ws->arrived[i0], 1u) == (uint32_t)(i1 - i0) ? 1u : 0u;
-            __syncthreads();
-            if (is_last != 0u) {
-                __threadfence();
-                for (int i = tid; i < kRows * D / 4; i += Sh::kThreads) {
-                    const int r = i / (D / 4), d = i % (D / 4) * 4;
-                    const int row = seg.c * kRows + r;
-                    if (row >= rows) continue;
-                    float top = -INFINITY, sum = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const int64_t step = 2 * Sh::kPartial;
-                    const float* const base = partials + (int64_t)i0 * step;
-#pragma unroll 4
-                    for (int x = i0; x <= i1; ++x) {
-                        const float* const src = base + (x - i0) * step + (x == i0 ? Sh::kPartial : 0);
-                        const float2 st = __ldcg((const float2*)(src + 2 * r));
-                        const float4 v = __ldcg((const float4*)(src + 2 * kRows + r * D + d));
-                        const float now = fmaxf(top, st.x), off = now == -INFINITY ? 0.f : now;
-                        const float keep = exp2_fast(top - off), by = exp2_fast(st.x - off);
-                        top = now;
-                        sum = sum * keep + st.y * by;
-                        o.x = o.x * keep + v.x * by;
-                        o.y = o.y * keep + v.y * by;
-                        o.z = o.z * keep + v.z * by;
-                        o.w = o.w * keep + v.w * by;
+                    for (int j = 0; j < J; ++j) {
+                        const float4 o = make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]);
+                        const int d = 32 * j + 4 * g;
+                        if (!(starts && ends)) *(float4*)(piece + 2 * kRows + r * D + d) = o;
+                        else if (row < rows) attn_store(p, seg.r.q0, seg.h, row, d, top, sum, o, d == 0);
                     }
-                    const int token = seg.r.q0 + row / p.group, head = seg.h * p.group + row % p.group;
-                    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-                    *(uint2*)((__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride + d) =
-                        make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
-                    if (a.lse != nullptr && d == 0)
-                        a.lse[(int64_t)token * a.q_heads + head] =
-                            ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.693147180559945309f;
                 }
-                if (tid == 0) ws->arrived[i0] = 0u;
-            }
-            __syncthreads();
+            if (seg.end >= r1) break;
+            attn_next<kRows>(p, seg);
         }
-        attn_next<kRows>(p, seg);
+        // Copies in flight at this point: none, or those that a wait gave up on.
+        if (dead)
+            for (int i = 0; i < kStages; ++i)
+                for (uint32_t tries = 0; tries < kAttnSpins && !mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u); ++tries) {}
     }
-    // Copies in flight at this point: none, or those that a wait gave up on.
-    if (dead)
-        for (int i = 0; i < kStages; ++i)
-            for (uint32_t tries = 0; tries < kAttnSpins && !mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u); ++tries) {}
+    __syncthreads();
+
+    // ---- join the CTA's pieces.  A chain is the pieces of one segment, in order; its first piece leads. ----
+    constexpr int kItems = kRows * D / 4;
+    int first_piece = 0;
+    while (first_piece < 2 * kWarps && !(pieces[first_piece].flags & kHas)) ++first_piece;
+    for (int item = tid; item < 2 * kWarps * kItems; item += Sh::kThreads) {
+        const int lead = item / kItems, i = item % kItems;
+        if (!(pieces[lead].flags & kHas) || !(lead == first_piece || (pieces[lead].flags & kStarts))) continue;
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float top = -FLT_MAX, sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool ends = false;
+        for (int x = lead; x < 2 * kWarps && !ends; ++x) {
+            const int flags = pieces[x].flags;
+            if (!(flags & kHas)) continue;
+            const float* const src = piece_at(x >> 1, x & 1);
+            attn_add(top, sum, o, *(const float2*)(src + 2 * r), *(const float4*)(src + 2 * kRows + r * D + d));
+            ends = flags & kEnds;
+        }
+        const bool starts = pieces[lead].flags & kStarts;
+        if (starts && ends) {
+            const AttnRequest rq = attn_request<kRows>(p, pieces[lead].b);
+            const int row = pieces[lead].c * kRows + r;
+            if (row < rq.qn * p.group) attn_store(p, rq.q0, pieces[lead].h, row, d, top, sum, o, d == 0);
+        } else {
+            float* const dst = partials + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * Sh::kPartial;
+            *(float4*)(dst + 2 * kRows + r * D + d) = o;
+            if (d == 0) *(float2*)(dst + 2 * r) = make_float2(top, sum);
+        }
+    }
+
+    // ---- join the CTAs that share a segment: the last to arrive adds them in order ----
+    int last_lead = 2 * kWarps - 1;  // leader of the last chain
+    while (last_lead > first_piece && (pieces[last_lead].flags & (kHas | kStarts)) != (kHas | kStarts)) --last_lead;
+    const int64_t cta0 = (int64_t)blockIdx.x * cta_run, cta1 = cta0 + cta_run;
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+        const int lead = turn == 0 ? first_piece : last_lead;
+        if (lead >= 2 * kWarps || (turn == 1 && last_lead == first_piece)) continue;
+        const AttnPiece pc = pieces[lead];
+        if (!(pc.flags & kHas) || (pc.begin >= cta0 && pc.end <= cta1)) continue;
+        const int i0 = (int)(pc.begin / cta_run), i1 = (int)((pc.end - 1) / cta_run);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) is_last = atomicAdd(&ws->arrived[i0], 1u) == (uint32_t)(i1 - i0) ? 1u : 0u;
+        __syncthreads();
+        if (is_last == 0u) continue;
+        __threadfence();
+        const AttnRequest rq = attn_request<kRows>(p, pc.b);
+        for (int i = tid; i < kItems; i += Sh::kThreads) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            const int row = pc.c * kRows + r;
+            if (row >= rq.qn * p.group) continue;
+            float top = -FLT_MAX, sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int64_t kStep = 2 * Sh::kPartial;
+            const float* const base = partials + (int64_t)i0 * kStep;
+#pragma unroll 4
+            for (int x = i0; x <= i1; ++x) {
+                const float* const src = base + (x - i0) * kStep + (x == i0 ? Sh::kPartial : 0);
+                attn_add(top, sum, o, __ldcg((const float2*)(src + 2 * r)), __ldcg((const float4*)(src + 2 * kRows + r * D + d)));
+            }
+            attn_store(p, rq.q0, pc.h, row, d, top, sum, o, d == 0);
+        }
+        if (tid == 0) ws->arrived[i0] = 0u;
+        __syncthreads();
+    }
 }
 
 template <int D, int NT, int kWarps, int kStages>
 static rra_status_t attn_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
     using Sh = AttnShape<D, NT, kWarps, kStages>;
     const void* k = (const void*)kv_attention_kernel<D, NT, kWarps, kStages>;
-    static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 1024, "shared memory");
+    static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 2048, "shared memory");
     if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
@@ -723,8 +781,8 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     const int64_t rows = (int64_t)std::max(args->max_q, 1) * p.group;
     const int ctas = std::min(sms, rra::kAttnMaxCtas);
     if (args->cache.head_dim == 128)
-        return rows <= 8 ? rra::attn_launch<128, 1, 8, 4>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 4>(p, ctas, stream);
-    return rows <= 8 ? rra::attn_launch<64, 1, 8, 4>(p, ctas, stream) : rra::attn_launch<64, 2, 8, 4>(p, ctas, stream);
+        return rows <= 8 ? rra::attn_launch<128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 2>(p, ctas, stream);
+    return rows <= 8 ? rra::attn_launch<64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<64, 2, 8, 4>(p, ctas, stream);
 }
 
 }  // extern "C"
