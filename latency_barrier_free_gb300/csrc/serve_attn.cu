@@ -186,16 +186,14 @@ __device__ __forceinline__ void attn_store(const AttnParams& p, int q0, int h, i
     if (with_lse && a.lse != nullptr) a.lse[token * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
 }
 
-// Adds a piece's row (maximum and sum st, four channels v) to the running one.
-__device__ __forceinline__ void attn_add(float& top, float& sum, float4& o, float2 st, float4 v) {
-    const float now = fmaxf(top, st.x);
-    const float keep = exp2_fast(top - now), by = exp2_fast(st.x - now);
-    top = now;
-    sum = sum * keep + st.y * by;
-    o.x = o.x * keep + v.x * by;
-    o.y = o.y * keep + v.y * by;
-    o.z = o.z * keep + v.z * by;
-    o.w = o.w * keep + v.w * by;
+// Adds a piece's row (maximum and sum st, four channels v) to sums whose maximum is top.
+__device__ __forceinline__ void attn_add(float top, float& sum, float4& o, float2 st, float4 v) {
+    const float by = exp2_fast(st.x - top);
+    sum = fmaf(st.y, by, sum);
+    o.x = fmaf(v.x, by, o.x);
+    o.y = fmaf(v.y, by, o.y);
+    o.z = fmaf(v.z, by, o.z);
+    o.w = fmaf(v.w, by, o.w);
 }
 
 template <int D, int NT, int kWarps, int kStages>
@@ -295,6 +293,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             return (int)(to > 0 ? to : 0);
         };
 
+        // Queries of a segment, as they are; loaded ahead of the copies that the lanes set up meanwhile.
+        uint2 raw[NT][J][2];
+        auto load_queries = [&]() {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = seg.c * kRows + 8 * n + g;
+                const bool live = row < seg.r.qn * p.group && first_tile(seg) < end_tile(seg);
+                const int i = row / p.group;
+                const __nv_bfloat16* x = (const __nv_bfloat16*)a.q + (seg.r.q0 + i) * a.q_token_stride +
+                                         (seg.h * p.group + row - i * p.group) * a.q_head_stride;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        raw[n][j][s] = live ? *(const uint2*)(x + 32 * j + 4 * (2 * t + s)) : make_uint2(0u, 0u);
+            }
+        };
+        load_queries();
+
         // ---- copies, kStages tiles ahead.  Lane i holds the places of the run's next tiles but i. ----
         AttnSegment from = seg;             // segment of the next tile to copy
         int next = first_tile(seg), from_end = end_tile(seg);  // that tile, and the end of the run in its segment
@@ -307,14 +324,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         uint32_t valid = 0;                 // which blocks of each stage were copied, 2 bits a stage
         const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
         auto copy_next = [&]() {
-            while (next >= from_end) {
-                if (from.end >= r1) return;
-                attn_next<kRows>(p, from);
-                next = first_tile(from);
-                from_end = end_tile(from);
-                held = held_end = 0;
-            }
             if (held >= held_end) {
+                while (next >= from_end) {
+                    if (from.end >= r1) return;
+                    attn_next<kRows>(p, from);
+                    next = first_tile(from);
+                    from_end = end_tile(from);
+                }
                 const int key = (from.r.first_tile + next + lane) * kAttnTile;
                 const int32_t* const row = a.block_table + from.b * a.table_stride;
                 src0 = src1 = nullptr;
@@ -331,6 +347,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 ok1 = __ballot_sync(0xffffffffu, src1 != nullptr);
                 held = 0;
                 held_end = min(32, from_end - next);
+                next += held_end;
             }
             if (lane == held) {
                 const uint32_t bar = bars + 8 * put, dst = ring + put * Sh::kStage;
@@ -346,7 +363,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             valid = (valid & ~(3u << (2 * put))) | ((ok0 >> held & 1u) | (ok1 >> held & 1u) << 1) << (2 * put);
             issued ^= 1u << put;
             ++held;
-            ++next;
             put = put + 1 == kStages ? 0 : put + 1;
         };
 #pragma unroll 1
@@ -366,25 +382,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             int all_first = 0, all_end = INT32_MAX, any_first = INT32_MAX, any_end = 0;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int row = seg.c * kRows + 8 * n + g;
                 float most = 0.f;
-                uint2 raw[J][2];
-                if (row < rows && tile0 < tile1) {
-                    const __nv_bfloat16* x = (const __nv_bfloat16*)a.q + (seg.r.q0 + row / p.group) * a.q_token_stride +
-                                             (seg.h * p.group + row % p.group) * a.q_head_stride;
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) raw[j][s] = *(const uint2*)(x + 32 * j + 4 * (2 * t + s));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < J; ++j) raw[j][0] = raw[j][1] = make_uint2(0u, 0u);
-                }
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
+                        const uint32_t v[2] = {raw[n][j][s].x, raw[n][j][s].y};
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)),
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint32_t v[2] = {raw[j][s].x, raw[j][s].y};
+                        const uint32_t v[2] = {raw[n][j][s].x, raw[n][j][s].y};
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             q[n][j][s][k] = pack_half2(__uint_as_float(v[k] << 16) * down,
@@ -467,20 +470,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 }
                 phase ^= 1u << take;
                 const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
-                const int key0 = (seg.r.first_tile + tl) * kAttnTile;
-                if (have != 0u) {
-                    const bool whole = have == 3u && key0 >= all_first && key0 + kAttnTile <= all_end;
-                    float s[2][NT][4];
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {  // blocks of 16 keys
+                    if (!(have >> i & 1u)) continue;
+                    const uint32_t base = tile + i * B::kBytes;
+                    const int key0 = (seg.r.first_tile + tl) * kAttnTile + kKvBlockTokens * i;
                     // keys of this lane's score rows: block row (g >> 1) + 4 (g & 1), and 8 above
                     const int krow = (g >> 1) + 4 * (g & 1);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t base = tile + i * B::kBytes;
+                    float s[NT][4];
+                    {
                         uint32_t k0[J], k1[J], s0[J / 2], s1[J / 2];
                         lds_words<J>(base + krow * B::kRow + t * 4 * J, k0);
-                        lds_words<J>(base + (krow + 8) * B::kRow + t * 4 * J, k1);
-                        lds_words<J / 2>(base + B::kScaleK + krow * B::kScaleRow, s0);
-                        lds_words<J / 2>(base + B::kScaleK + (krow + 8) * B::kScaleRow, s1);
+                        lds_words<J>(base + krow * B::kRow + t * 4 * J + 8 * B::kRow, k1);
+                        lds_words<J / 2>(base + krow * B::kScaleRow + B::kScaleK, s0);
+                        lds_words<J / 2>(base + krow * B::kScaleRow + B::kScaleK + 8 * B::kScaleRow, s1);
                         // word s * J/2 + j/2 holds, for group j (bytes 2 (j & 1), + 1), channels 32 j + 4 (2 t + s) + 0..3
 #pragma unroll
                         for (int jj = 0; jj < J / 2; ++jj) {
@@ -503,32 +506,40 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) {
                                         const float w = k < 2 ? u : v;
-                                        s[i][n][k] = jj + e == 0 ? w * c[k] : fmaf(w, c[k], s[i][n][k]);
+                                        s[n][k] = jj + e == 0 ? w * c[k] : fmaf(w, c[k], s[n][k]);
                                     }
                                 }
                         }
                     }
-                    // ---- does a score pass the running maximum? ----
-                    bool passes = false;
+                    if (!(key0 >= all_first && key0 + kKvBlockTokens <= all_end)) {
+                        // Scores of keys that a row does not see, and the scales of keys that no row sees: their
+                        // memory may never have been written.  The store goes where a copy comes next, hence the fence.
+                        if (lane < kKvBlockTokens && (key0 + lane < any_first || key0 + lane >= any_end))
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                            for (int jj = 0; jj < J / 2; ++jj)
+                                asm volatile("st.shared.u32 [%0], %1;" : : "r"(base + B::kScaleV + lane * B::kScaleRow + 4 * jj), "r"(0u) : "memory");
+                        fence_proxy_async_smem();
+                        __syncwarp();
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                if (!whole) {
-                                    const int key = key0 + 16 * i + krow + 8 * (k >> 1);
-                                    const bool seen = (have >> i & 1u) && key >= first_key[n][k & 1] && key < end_key[n][k & 1];
-                                    s[i][n][k] = seen ? s[i][n][k] : -INFINITY;
-                                }
-                                passes |= s[i][n][k] > limit[n][k & 1];
+                                const int key = key0 + krow + 8 * (k >> 1);
+                                s[n][k] = key >= first_key[n][k & 1] && key < end_key[n][k & 1] ? s[n][k] : -INFINITY;
                             }
+                    }
+                    // ---- does a score pass the running maximum? ----
+                    bool passes = false;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) passes |= fmaxf(s[n][k], s[n][k + 2]) > limit[n][k];
                     if (__any_sync(0xffffffffu, passes)) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                float top = fmaxf(fmaxf(s[0][n][k], s[0][n][k + 2]), fmaxf(s[1][n][k], s[1][n][k + 2]));
+                                float top = fmaxf(s[n][k], s[n][k + 2]);
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -540,63 +551,52 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
 #pragma unroll
                                 for (int j = 0; j < J; ++j)
 #pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
-                                        acc[j][i][n][k] *= by;
-                                        acc[j][i][n][k + 2] *= by;
+                                    for (int d = 0; d < 2; ++d) {
+                                        acc[j][d][n][k] *= by;
+                                        acc[j][d][n][k + 2] *= by;
                                     }
                             }
                     }
                     // ---- weights, and their products with the values ----
+                    uint32_t b0[NT], b1[NT];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t b0[NT], b1[NT];
+                    for (int n = 0; n < NT; ++n) {
+                        float e[4];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float e[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                e[k] = exp2_fast((s[i][n][k] - m[n][k & 1]) * factor[n][k & 1]);
-                                l[n][k & 1] += e[k];
-                            }
-                            b0[n] = transpose8(pack_half2(e[0], e[1]));  // head g, keys t and t + 4
-                            b1[n] = transpose8(pack_half2(e[2], e[3]));  // head g, keys t + 8 and t + 12
+                        for (int k = 0; k < 4; ++k) {
+                            e[k] = exp2_fast((s[n][k] - m[n][k & 1]) * factor[n][k & 1]);
+                            l[n][k & 1] += e[k];
                         }
-                        if (!(have >> i & 1u)) continue;
-                        const uint32_t base = tile + i * B::kBytes;
-                        uint32_t v[4][J / 2], sv[4][J / 2];
+                        b0[n] = transpose8(pack_half2(e[0], e[1]));  // head g, keys t and t + 4
+                        b1[n] = transpose8(pack_half2(e[2], e[3]));  // head g, keys t + 8 and t + 12
+                    }
+                    uint32_t v[4][J / 2], sv[4][J / 2];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            lds_words<J / 2>(base + B::kV + (t + 4 * r) * B::kRow + g * 2 * J, v[r]);
-                            lds_words<J / 2>(base + B::kScaleV + (t + 4 * r) * B::kScaleRow, sv[r]);
-                            if (!whole) {  // what no row sees may never have been written
-                                const int key = key0 + 16 * i + t + 4 * r;
-                                if (key < any_first || key >= any_end)
+                    for (int r = 0; r < 4; ++r) {
+                        lds_words<J / 2>(base + t * B::kRow + g * 2 * J + B::kV + 4 * r * B::kRow, v[r]);
+                        lds_words<J / 2>(base + t * B::kScaleRow + B::kScaleV + 4 * r * B::kScaleRow, sv[r]);
+                    }
 #pragma unroll
-                                    for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = 0u;
-                            }
+                    for (int jj = 0; jj < J / 2; ++jj) {
+                        // nibbles of two keys side by side: even channels in x, odd ones in y
+                        uint32_t x[2][4], y[2][4];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t u = v[2 * r][jj], z = v[2 * r + 1][jj];
+                            from_e2m1x8((u & 0x0f0f0f0fu) | ((z << 4) & 0xf0f0f0f0u), x[r]);
+                            from_e2m1x8(((u >> 4) & 0x0f0f0f0fu) | (z & 0xf0f0f0f0u), y[r]);
                         }
 #pragma unroll
-                        for (int jj = 0; jj < J / 2; ++jj) {
-                            // nibbles of two keys side by side: even channels in x, odd ones in y
-                            uint32_t x[2][4], y[2][4];
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t sel = e ? 0x7632u : 0x5410u;
+                            const uint32_t w0s = __byte_perm(sv[0][jj], sv[1][jj], sel), w1s = __byte_perm(sv[2][jj], sv[3][jj], sel);
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const uint32_t u = v[2 * r][jj], z = v[2 * r + 1][jj];
-                                from_e2m1x8((u & 0x0f0f0f0fu) | ((z << 4) & 0xf0f0f0f0u), x[r]);
-                                from_e2m1x8(((u >> 4) & 0x0f0f0f0fu) | (z & 0xf0f0f0f0u), y[r]);
-                            }
+                            for (int n = 0; n < NT; ++n) {
+                                const uint32_t p0 = mul_half2(b0[n], w0s), p1 = mul_half2(b1[n], w1s);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t sel = e ? 0x7632u : 0x5410u;
-                                const uint32_t w0s = __byte_perm(sv[0][jj], sv[1][jj], sel), w1s = __byte_perm(sv[2][jj], sv[3][jj], sel);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    const uint32_t p0 = mul_half2(b0[n], w0s), p1 = mul_half2(b1[n], w1s);
-#pragma unroll
-                                    for (int d = 0; d < 2; ++d)
-                                        mma_f16(acc[2 * jj + e][d][n], x[0][2 * e + d], y[0][2 * e + d], x[1][2 * e + d],
-                                                y[1][2 * e + d], p0, p1);
-                                }
+                                for (int d = 0; d < 2; ++d)
+                                    mma_f16(acc[2 * jj + e][d][n], x[0][2 * e + d], y[0][2 * e + d], x[1][2 * e + d],
+                                            y[1][2 * e + d], p0, p1);
                             }
                         }
                     }
@@ -640,6 +640,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 }
             if (seg.end >= r1) break;
             attn_next<kRows>(p, seg);
+            load_queries();
         }
         // Copies in flight at this point: none, or those that a wait gave up on.
         if (dead)
@@ -649,24 +650,30 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     __syncthreads();
 
     // ---- join the CTA's pieces.  A chain is the pieces of one segment, in order; its first piece leads. ----
-    constexpr int kItems = kRows * D / 4;
-    int first_piece = 0;
-    while (first_piece < 2 * kWarps && !(pieces[first_piece].flags & kHas)) ++first_piece;
-    for (int item = tid; item < 2 * kWarps * kItems; item += Sh::kThreads) {
-        const int lead = item / kItems, i = item % kItems;
-        if (!(pieces[lead].flags & kHas) || !(lead == first_piece || (pieces[lead].flags & kStarts))) continue;
+    constexpr int kItems = kRows * D / 4;  // four channels of a row each
+    static_assert(2 * kWarps <= 32 && kItems % 32 == 0, "a lane for each piece, a warp in one chain");
+    const int my_flags = lane < 2 * kWarps ? pieces[lane].flags : 0;
+    const uint32_t has = __ballot_sync(0xffffffffu, (my_flags & kHas) != 0);
+    if (has == 0u) return;
+    const uint32_t leads = __ballot_sync(0xffffffffu, (my_flags & kStarts) != 0) | (has & -has);
+    const int chains = __popc(leads);
+    for (int item = tid; item < chains * kItems; item += Sh::kThreads) {
+        const int i = item % kItems;
+        uint32_t left = leads;
+        for (int skip = item / kItems; skip > 0; --skip) left &= left - 1u;
+        const int lead = __ffs((int)left) - 1;
+        const uint32_t later = leads & ~((2u << lead) - 1u);
+        const uint32_t chain = has & ~((1u << lead) - 1u) & (later != 0u ? (later & -later) - 1u : 0xffffffffu);
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float top = -FLT_MAX, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool ends = false;
-        for (int x = lead; x < 2 * kWarps && !ends; ++x) {
-            const int flags = pieces[x].flags;
-            if (!(flags & kHas)) continue;
-            const float* const src = piece_at(x >> 1, x & 1);
+        for (uint32_t x = chain; x != 0u; x &= x - 1u) top = fmaxf(top, piece_at((__ffs((int)x) - 1) >> 1, (__ffs((int)x) - 1) & 1)[2 * r]);
+#pragma unroll 4
+        for (uint32_t x = chain; x != 0u; x &= x - 1u) {
+            const float* const src = piece_at((__ffs((int)x) - 1) >> 1, (__ffs((int)x) - 1) & 1);
             attn_add(top, sum, o, *(const float2*)(src + 2 * r), *(const float4*)(src + 2 * kRows + r * D + d));
-            ends = flags & kEnds;
         }
-        const bool starts = pieces[lead].flags & kStarts;
+        const int starts = pieces[lead].flags & kStarts, ends = pieces[31 - __clz((int)chain)].flags & kEnds;
         if (starts && ends) {
             const AttnRequest rq = attn_request<kRows>(p, pieces[lead].b);
             const int row = pieces[lead].c * kRows + r;
@@ -679,15 +686,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     }
 
     // ---- join the CTAs that share a segment: the last to arrive adds them in order ----
-    int last_lead = 2 * kWarps - 1;  // leader of the last chain
-    while (last_lead > first_piece && (pieces[last_lead].flags & (kHas | kStarts)) != (kHas | kStarts)) --last_lead;
     const int64_t cta0 = (int64_t)blockIdx.x * cta_run, cta1 = cta0 + cta_run;
 #pragma unroll 1
     for (int turn = 0; turn < 2; ++turn) {
-        const int lead = turn == 0 ? first_piece : last_lead;
-        if (lead >= 2 * kWarps || (turn == 1 && last_lead == first_piece)) continue;
+        const int lead = turn == 0 ? __ffs((int)leads) - 1 : 31 - __clz((int)leads);  // first chain, last chain
+        if (turn == 1 && chains == 1) break;
         const AttnPiece pc = pieces[lead];
-        if (!(pc.flags & kHas) || (pc.begin >= cta0 && pc.end <= cta1)) continue;
+        if (pc.begin >= cta0 && pc.end <= cta1) continue;
         const int i0 = (int)(pc.begin / cta_run), i1 = (int)((pc.end - 1) / cta_run);
         __threadfence();
         __syncthreads();
@@ -696,18 +701,40 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         if (is_last == 0u) continue;
         __threadfence();
         const AttnRequest rq = attn_request<kRows>(p, pc.b);
+        // the parts' maxima and sums go where the pieces were
+        constexpr int64_t kStep = 2 * Sh::kPartial;
+        const float* const base = partials + (int64_t)i0 * kStep;
+        const int parts = i1 - i0 + 1;
+        float2* const stats = (float2*)smem;  // [parts][kRows]: maximum, sum
+        static_assert(kAttnMaxCtas * kRows * 8 <= Sh::kRing + Sh::kHeads, "statistics fit");
+        auto part_at = [&](int x) { return base + x * kStep + (x == 0 ? Sh::kPartial : 0); };
+        for (int x = tid; x < parts * kRows; x += Sh::kThreads)
+            stats[x] = __ldcg((const float2*)(part_at(x / kRows) + 2 * (x % kRows)));
+        __syncthreads();
         for (int i = tid; i < kItems; i += Sh::kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             const int row = pc.c * kRows + r;
             if (row >= rq.qn * p.group) continue;
             float top = -FLT_MAX, sum = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int64_t kStep = 2 * Sh::kPartial;
-            const float* const base = partials + (int64_t)i0 * kStep;
-#pragma unroll 4
-            for (int x = i0; x <= i1; ++x) {
-                const float* const src = base + (x - i0) * kStep + (x == i0 ? Sh::kPartial : 0);
-                attn_add(top, sum, o, __ldcg((const float2*)(src + 2 * r)), __ldcg((const float4*)(src + 2 * kRows + r * D + d)));
+            constexpr int kAhead = 16;
+#pragma unroll 1
+            for (int x0 = 0; x0 < parts; x0 += kAhead) {
+                float4 v[kAhead];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x)
+                    if (x0 + x < parts) v[x] = __ldcg((const float4*)(part_at(x0 + x) + 2 * kRows + r * D + d));
+                float now = top;
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x)
+                    if (x0 + x < parts) now = fmaxf(now, stats[(x0 + x) * kRows + r].x);
+                const float keep = exp2_fast(top - now);
+                top = now;
+                sum *= keep;
+                o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x)
+                    if (x0 + x < parts) attn_add(top, sum, o, stats[(x0 + x) * kRows + r], v[x]);
             }
             attn_store(p, rq.q0, pc.h, row, d, top, sum, o, d == 0);
         }
