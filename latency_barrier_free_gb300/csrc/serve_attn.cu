@@ -46,7 +46,9 @@ constexpr int kAttnMaxRows = 16;
 struct AttnParams {
     rra_kv_attention_args_t a;
     float scale_log2;
-    int32_t group;  // query heads of a KV head
+    int32_t group;   // query heads of a KV head
+    int32_t room;    // keys that a row of the table has pages for
+    int32_t window;  // a.window, at most 2^30
 };
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -114,13 +116,10 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int b) 
     const int most_q = (int)a.tokens;
     r.q0 = min(max(a.cu_q[b], 0), most_q);
     r.qn = max(0, min(a.cu_q[b + 1], most_q) - r.q0);
-    const int64_t room = (int64_t)a.table_pages * a.cache.page_tokens;
-    r.kv = (int)min((int64_t)max(a.kv_len[b], 0), room);
-    int first = 0;
-    if (a.window > 0) first = (int)max((int64_t)0, (int64_t)r.kv - r.qn - a.window + 1);
-    r.first_tile = first / kAttnTile;
+    r.kv = min(max(a.kv_len[b], 0), p.room);
+    r.first_tile = (p.window > 0 ? max(0, r.kv - r.qn - p.window + 1) : 0) / kAttnTile;
     r.tiles = max(1, (r.kv + kAttnTile - 1) / kAttnTile - r.first_tile);
-    r.chunks = (int)(((int64_t)r.qn * p.group + kRows - 1) / kRows);
+    r.chunks = (r.qn * p.group + kRows - 1) / kRows;
     return r;
 }
 
@@ -132,7 +131,7 @@ struct AttnSegment {
     int64_t begin, end;
 };
 template <int kRows>
-__device__ __forceinline__ void attn_next(const AttnParams& p, AttnSegment& s) {
+__device__ __noinline__ void attn_next(const AttnParams& p, AttnSegment& s) {  // out of line: once a segment, in two places
     if (++s.c >= s.r.chunks) {
         s.c = 0;
         if (++s.h == p.a.cache.kv_heads) {
@@ -173,17 +172,19 @@ struct AttnShape {
     static size_t smem(int requests) { return (size_t)kFixed + 8 * ((size_t)requests + 1); }
 };
 
-// out and lse of one row (four channels) from sums: maximum top (in units of log2), sum, o.
-__device__ __forceinline__ void attn_store(const AttnParams& p, int q0, int h, int row, int d, float top, float sum,
-                                           float4 o, bool with_lse) {
+// Where row's channels go, and its sum's reciprocal; writes its lse (maximum top in units of log2).
+__device__ __forceinline__ __nv_bfloat16* attn_row(const AttnParams& p, int q0, int h, int row, float top, float sum,
+                                                   bool with_lse, float& inv) {
     const rra_kv_attention_args_t& a = p.a;
-    const int64_t token = q0 + row / p.group;
-    const int head = h * p.group + row % p.group;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: 0
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    *(uint2*)((__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride + d) =
-        make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
+    const int i = row / p.group, head = h * p.group + row - i * p.group;
+    const int64_t token = q0 + i;
+    inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: 0
     if (with_lse && a.lse != nullptr) a.lse[token * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
+    return (__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride;
+}
+__device__ __forceinline__ void attn_store(__nv_bfloat16* to, float4 o, float inv) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *(uint2*)to = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
 }
 
 // Adds a piece's row (maximum and sum st, four channels v) to sums whose maximum is top.
@@ -258,14 +259,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     }
     if (tid == 0) sums[a.requests] = total;
     __syncthreads();
-    int64_t run = (total + (int64_t)gridDim.x * kWarps - 1) / ((int64_t)gridDim.x * kWarps);
-    run = run < kAttnMinRun + kAttnSegmentCost ? kAttnMinRun + kAttnSegmentCost : run;
-    const int64_t cta_run = run * kWarps;
+    // Little work is spread over the SMs first, four warps each: a warp that shares its scheduler takes longer for
+    // a tile, and the smallest batches are all latency.
+    int64_t run = kAttnMinRun + kAttnSegmentCost;
+    int warps = kWarps;
+    if (total <= run * 4 * (int64_t)gridDim.x) {
+        warps = 4;
+    } else if (total > run * kWarps * (int64_t)gridDim.x) {
+        run = (total + (int64_t)gridDim.x * kWarps - 1) / ((int64_t)gridDim.x * kWarps);
+    }
+    const int64_t cta_run = run * warps;
     if ((int64_t)blockIdx.x * cta_run >= total) return;
     const int64_t r0 = (int64_t)blockIdx.x * cta_run + warp * run;
     const int64_t r1 = r0 + run < total ? r0 + run : total;
 
-    if (r0 < r1) {
+    if (r0 < r1 && warp < warps) {
         // this warp's first segment
         AttnSegment seg;
         {
@@ -278,10 +286,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             seg.b = low;
             seg.r = attn_request<kRows>(p, low);
             const int each = seg.r.tiles + kAttnSegmentCost;
-            const int64_t i = (r0 - sums[low]) / each;
-            seg.h = (int)(i / seg.r.chunks);
-            seg.c = (int)(i % seg.r.chunks);
-            seg.begin = sums[low] + i * each;
+            const int i = (int)((r0 - sums[low]) / each);
+            seg.h = i / seg.r.chunks;
+            seg.c = i - seg.h * seg.r.chunks;
+            seg.begin = sums[low] + (int64_t)i * each;
             seg.end = seg.begin + each;
         }
         auto first_tile = [&](const AttnSegment& s) {
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     if (r < rows) {
                         const int pos = seg.r.kv - seg.r.qn + r / p.group;
                         hi = a.causal ? max(0, min(seg.r.kv, pos + 1)) : seg.r.kv;
-                        lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)pos - a.window + 1) : 0;
+                        lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
                         all_first = max(all_first, lo);
                         all_end = min(all_end, hi);
                         any_first = min(any_first, lo);
@@ -629,13 +637,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int r = 8 * n + 2 * t + k, row = seg.c * kRows + r;
                     const float top = m[n][k] * factor[n][k];  // in units of log2
-                    if (!(starts && ends) && g == 0) *(float2*)(piece + 2 * r) = make_float2(top, sum);
+                    if (!(starts && ends)) {
+                        if (g == 0) *(float2*)(piece + 2 * r) = make_float2(top, sum);
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        const float4 o = make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]);
-                        const int d = 32 * j + 4 * g;
-                        if (!(starts && ends)) *(float4*)(piece + 2 * kRows + r * D + d) = o;
-                        else if (row < rows) attn_store(p, seg.r.q0, seg.h, row, d, top, sum, o, d == 0);
+                        for (int j = 0; j < J; ++j)
+                            *(float4*)(piece + 2 * kRows + r * D + 32 * j + 4 * g) =
+                                make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]);
+                    } else if (row < rows) {
+                        float inv;
+                        __nv_bfloat16* const to = attn_row(p, seg.r.q0, seg.h, row, top, sum, g == 0, inv) + 4 * g;
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            attn_store(to + 32 * j,
+                                       make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]), inv);
                     }
                 }
             if (seg.end >= r1) break;
@@ -667,8 +681,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float top = -FLT_MAX, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (uint32_t x = chain; x != 0u; x &= x - 1u) top = fmaxf(top, piece_at((__ffs((int)x) - 1) >> 1, (__ffs((int)x) - 1) & 1)[2 * r]);
-#pragma unroll 4
+#pragma unroll 1
         for (uint32_t x = chain; x != 0u; x &= x - 1u) {
             const float* const src = piece_at((__ffs((int)x) - 1) >> 1, (__ffs((int)x) - 1) & 1);
             attn_add(top, sum, o, *(const float2*)(src + 2 * r), *(const float4*)(src + 2 * kRows + r * D + d));
@@ -677,7 +692,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         if (starts && ends) {
             const AttnRequest rq = attn_request<kRows>(p, pieces[lead].b);
             const int row = pieces[lead].c * kRows + r;
-            if (row < rq.qn * p.group) attn_store(p, rq.q0, pieces[lead].h, row, d, top, sum, o, d == 0);
+            if (row < rq.qn * p.group) {
+                float inv;
+                __nv_bfloat16* const to = attn_row(p, rq.q0, pieces[lead].h, row, top, sum, d == 0, inv);
+                attn_store(to + d, o, inv);
+            }
         } else {
             float* const dst = partials + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * Sh::kPartial;
             *(float4*)(dst + 2 * kRows + r * D + d) = o;
@@ -736,7 +755,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 for (int x = 0; x < kAhead; ++x)
                     if (x0 + x < parts) attn_add(top, sum, o, stats[(x0 + x) * kRows + r], v[x]);
             }
-            attn_store(p, rq.q0, pc.h, row, d, top, sum, o, d == 0);
+            float inv;
+            __nv_bfloat16* const to = attn_row(p, rq.q0, pc.h, row, top, sum, d == 0, inv);
+            attn_store(to + d, o, inv);
         }
         if (tid == 0) ws->arrived[i0] = 0u;
         __syncthreads();
@@ -763,8 +784,8 @@ static bool attn_args_ok(const rra_kv_attention_args_t* a) {
         a->q_heads < 1 || a->q_heads % hk != 0 || a->table_pages < 0 || a->table_stride < a->table_pages ||
         a->max_q < 0 || a->max_kv < 0 || a->window < 0 || !isfinite(a->scale))
         return false;
-    // the rows of one KV head, and the keys of one request, are counted in 32 bits
-    if (a->tokens * (a->q_heads / hk) > INT32_MAX / 2 || (int64_t)a->table_pages * a->cache.page_tokens > INT32_MAX / 2)
+    // rows, and the keys of one request, are counted in 32 bits
+    if (a->tokens * a->q_heads > INT32_MAX / 2 || (int64_t)a->table_pages * a->cache.page_tokens > INT32_MAX / 2)
         return false;
     if (!strides_ok(a->q_token_stride, a->q_head_stride, a->q_heads, a->cache.head_dim, 2) ||
         !strides_ok(a->out_token_stride, a->out_head_stride, a->q_heads, a->cache.head_dim, 2) || !aligned16(a->q) ||
@@ -805,6 +826,8 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     p.a = *args;
     p.scale_log2 = (float)(args->scale * 1.4426950408889634);
     p.group = args->q_heads / args->cache.kv_heads;
+    p.room = args->table_pages * args->cache.page_tokens;
+    p.window = std::min(args->window, 1 << 30);
     const int64_t rows = (int64_t)std::max(args->max_q, 1) * p.group;
     const int ctas = std::min(sms, rra::kAttnMaxCtas);
     if (args->cache.head_dim == 128)
