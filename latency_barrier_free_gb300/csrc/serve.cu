@@ -13,16 +13,14 @@ namespace rra {
 // running sums in shared memory; then the cluster shares the pages to push,
 // the pages to pop and the tokens to place, each found by binary search in the
 // sums.  The cluster barrier between the pushes and the pops is the only
-// synchronisation, and also separates all reads of the lengths from the writes
-// that may go to the same buffers.
+// synchronisation between CTAs, and also separates all reads of the lengths
+// from the writes that may go to the same buffers.  It is all latency: lengths,
+// then pages, then the stack, a round trip to L2 each (64 requests decoding
+// move 2 KB).
 constexpr int kSlotThreads = 1024;
 constexpr int kSlotMaxCluster = 16;
-
-struct SlotSums {  // running sums before request b, [requests + 1]
-    int32_t* back;    // pages pushed
-    int32_t* fresh;   // pages popped
-    int32_t* tokens;  // new tokens
-};
+constexpr int kSlotAhead = 8;   // loads of a row in flight
+constexpr int kSlotRun = 4;     // neighbouring tokens of a thread
 
 // Index of the last entry of sums[0..n] (ascending, sums[0] = 0) that is <= x, below n.
 __device__ __forceinline__ int owner_of(const int32_t* sums, int n, int x) {
@@ -67,144 +65,165 @@ __device__ __forceinline__ void block_sums3(int v[3], int tot[3], int32_t (*part
 
 // Lengths as used: none below 0, and no sum of the new ones past 32 bits.
 constexpr int kSlotMost = (1 << 30) - 1;
-__device__ __forceinline__ int held_of(const rra_slot_map_args_t& a, int b) {
-    return min(max(a.seq_len[b], 0), kSlotMost);
-}
-__device__ __forceinline__ int added_to(const rra_slot_map_args_t& a, int b) {
-    return min(a.new_len[b], kSlotMost / a.requests);
-}
-__device__ __forceinline__ int pages_for(int tokens, int page_tokens) {
-    return tokens > 0 ? (tokens - 1) / page_tokens + 1 : 0;
+
+struct SlotParams {
+    rra_slot_map_args_t a;
+    Divisor by_page;
+    int32_t most_new;  // of one request
+    bool wide;         // slots and positions take 16-byte stores
+};
+
+__device__ __forceinline__ int pages_for(const SlotParams& p, int tokens) {
+    return tokens > 0 ? p.by_page(tokens - 1) + 1 : 0;
 }
 
-__global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_constant__ rra_slot_map_args_t a) {
+// Calls f(page, lane's rank in order) for a row's first `held` valid entries, 32 * kSlotAhead at a time; whole warps.
+template <typename F>
+__device__ __forceinline__ int valid_pages(const rra_slot_map_args_t& a, int b, int held, F&& f) {
+    const int lane = threadIdx.x & 31;
+    const int32_t* const row = a.block_table + b * a.table_stride;
+    int count = 0;
+    for (int i0 = 0; i0 < held; i0 += 32 * kSlotAhead) {
+        int page[kSlotAhead];
+#pragma unroll
+        for (int k = 0; k < kSlotAhead; ++k) page[k] = i0 + 32 * k + lane < held ? row[i0 + 32 * k + lane] : -1;
+#pragma unroll
+        for (int k = 0; k < kSlotAhead; ++k) {
+            const bool good = page[k] >= 0 && page[k] < a.num_pages;
+            const uint32_t who = __ballot_sync(0xffffffffu, good);
+            if (good) f(page[k], count + __popc(who & ((1u << lane) - 1u)));
+            count += __popc(who);
+        }
+    }
+    return count;
+}
+
+__global__ void __launch_bounds__(kSlotThreads, 1) slot_map_kernel(const __grid_constant__ SlotParams p) {
     extern __shared__ int32_t sums_mem[];
     __shared__ int32_t part[3][32];
     __shared__ int32_t over_total;
     pdl_release_early();
+    const rra_slot_map_args_t& a = p.a;
     const int n = a.requests;
-    const SlotSums s{sums_mem, sums_mem + (n + 1), sums_mem + 2 * (n + 1)};
-    const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
-    const int lane = tid & 31;
+    // before request b: pages pushed, pages popped, new tokens; and the tokens that it holds
+    int32_t* const back = sums_mem;
+    int32_t* const fresh = back + (n + 1);
+    int32_t* const tokens = fresh + (n + 1);
+    int32_t* const holds = tokens + (n + 1);
+    const int tid = (int)threadIdx.x, nt = (int)blockDim.x, lane = tid & 31;
     const int me = (int)blockIdx.x * nt + tid, all = (int)gridDim.x * nt;
     if (tid == 0) over_total = 0;
     pdl_wait();
-
-    // pages that come back, for each request that ends: valid entries of its row
-    for (int b = tid; b < n; b += nt) s.back[b] = 0;
-    __syncthreads();
-    for (int b0 = (tid >> 5) * 32; b0 < n; b0 += nt) {
-        const int b = b0 + lane;
-        const bool ends = b < n && a.new_len[b] < 0;
-        uint32_t todo = __ballot_sync(0xffffffffu, ends);
-        while (todo != 0u) {
-            const int e = b0 + __ffs((int)todo) - 1;
-            todo &= todo - 1;
-            const int held = min(pages_for(held_of(a, e), a.page_tokens), a.table_pages);
-            int count = 0;
-            for (int i = lane; i - lane < held; i += 32) {
-                const int page = i < held ? a.block_table[e * a.table_stride + i] : -1;
-                count += __popc(__ballot_sync(0xffffffffu, page >= 0 && page < a.num_pages));
-            }
-            if (lane == 0) s.back[e] = count;
-        }
-    }
-    __syncthreads();
+    const int count = min(max(a.free_count[0], 0), a.num_pages);
 
     // running sums over the requests
     int base[3] = {0, 0, 0};
     for (int b0 = 0; b0 < n; b0 += nt) {
         const int b = b0 + tid;
-        int v[3] = {0, 0, 0}, tot[3];
+        int add = 0, held = 0;
         if (b < n) {
-            const int add = added_to(a, b);
-            const int held = add < 0 ? 0 : held_of(a, b);
-            const int first = pages_for(held, a.page_tokens);
-            const int last = add > 0 ? pages_for(held + add, a.page_tokens) : first;
-            v[0] = s.back[b];
+            add = min(a.new_len[b], p.most_new);
+            held = min(max(a.seq_len[b], 0), kSlotMost);
+        }
+        int v[3] = {0, 0, 0}, tot[3];
+        // pages that come back: valid entries of the row of a request that ends, found by the whole warp
+        for (uint32_t todo = __ballot_sync(0xffffffffu, add < 0); todo != 0u; todo &= todo - 1u) {
+            const int who = __ffs((int)todo) - 1;
+            const int rows = min(pages_for(p, __shfl_sync(0xffffffffu, held, who)), a.table_pages);
+            const int c = valid_pages(a, b - lane + who, rows, [](int, int) {});
+            if (lane == who) v[0] = c;
+        }
+        if (add >= 0) {
+            const int first = pages_for(p, held), last = add > 0 ? pages_for(p, held + add) : first;
             v[1] = max(0, min(last, a.table_pages) - first);
-            v[2] = max(add, 0);
+            v[2] = add;
             const int over = last - max(first, a.table_pages);
             if (over > 0) atomicAdd(&over_total, over);
         }
         block_sums3(v, tot, part);
         if (b < n) {
-            s.back[b] = base[0] + v[0];
-            s.fresh[b] = base[1] + v[1];
-            s.tokens[b] = base[2] + v[2];
+            back[b] = base[0] + v[0];
+            fresh[b] = base[1] + v[1];
+            tokens[b] = base[2] + v[2];
+            holds[b] = held;
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) base[k] += tot[k];
     }
     if (tid == 0) {
-        s.back[n] = base[0];
-        s.fresh[n] = base[1];
-        s.tokens[n] = base[2];
+        back[n] = base[0];
+        fresh[n] = base[1];
+        tokens[n] = base[2];
     }
-    const int count = min(max(a.free_count[0], 0), a.num_pages);
     __syncthreads();
 
     // push: a warp per request that ends
     if (base[0] > 0) {
         for (int b = me >> 5; b < n; b += all >> 5) {
-            if (s.back[b + 1] == s.back[b]) continue;
-            const int held = min(pages_for(held_of(a, b), a.page_tokens), a.table_pages);
-            int at = count + s.back[b];
-            for (int i = lane; i - lane < held; i += 32) {
-                const int page = i < held ? a.block_table[b * a.table_stride + i] : -1;
-                const bool good = page >= 0 && page < a.num_pages;
-                const uint32_t who = __ballot_sync(0xffffffffu, good);
-                const int to = at + __popc(who & ((1u << lane) - 1u));
-                if (good && to < a.num_pages) a.free_pages[to] = page;
-                at += __popc(who);
-            }
+            if (back[b + 1] == back[b]) continue;
+            const int at = count + back[b];
+            valid_pages(a, b, min(pages_for(p, holds[b]), a.table_pages), [&](int page, int rank) {
+                if (at + rank < a.num_pages) a.free_pages[at + rank] = page;
+            });
         }
     }
     const int top = min(count + base[0], a.num_pages);
 
+    // Lengths: what becomes of a request that ends is known from new_len, which nothing overwrites.
     if (gridDim.x > 1) cluster_sync();
     else __syncthreads();
+    for (int b = me; b <= n; b += all) {
+        a.cu_new[b] = tokens[b];
+        if (b < n) a.kv_len[b] = a.new_len[b] < 0 ? 0 : holds[b] + tokens[b + 1] - tokens[b];
+    }
 
     // pop: new entries of the tables
     for (int i = me; i < base[1]; i += all) {
-        const int b = owner_of(s.fresh, n, i);
-        const int at = pages_for(held_of(a, b), a.page_tokens) + i - s.fresh[b];
+        const int b = owner_of(fresh, n, i);
+        const int at = pages_for(p, holds[b]) + i - fresh[b];
         a.block_table[b * a.table_stride + at] = i < top ? a.free_pages[top - 1 - i] : -1;
     }
-    // place: slots and positions of the new tokens
-    for (int64_t t = me; t < a.tokens; t += all) {
-        int64_t slot = -1;
-        int pos = 0;
-        if (t < base[2]) {
-            const int b = owner_of(s.tokens, n, (int)t);
-            const int held = held_of(a, b);
-            pos = held + ((int)t - s.tokens[b]);
-            const int at = pos / a.page_tokens, first = pages_for(held, a.page_tokens);
-            if (at < a.table_pages) {
-                int page;
-                if (at < first) {
-                    page = a.block_table[b * a.table_stride + at];
-                } else {
-                    const int i = s.fresh[b] + at - first;
-                    page = i < top ? a.free_pages[top - 1 - i] : -1;
+    // place: slots and positions of kSlotRun new tokens
+    for (int64_t t0 = (int64_t)me * kSlotRun; t0 < a.tokens; t0 += (int64_t)all * kSlotRun) {
+        int64_t slot[kSlotRun];
+        int pos[kSlotRun], page[kSlotRun];
+        int b = t0 < base[2] ? owner_of(tokens, n, (int)t0) : 0;
+#pragma unroll
+        for (int k = 0; k < kSlotRun; ++k) {
+            const int64_t t = t0 + k;
+            pos[k] = 0;
+            page[k] = -1;
+            if (t < base[2] && t < a.tokens) {
+                while (tokens[b + 1] <= (int)t) ++b;
+                const int held = holds[b];
+                pos[k] = held + ((int)t - tokens[b]);
+                const int at = p.by_page(pos[k]), first = pages_for(p, held);
+                if (at < a.table_pages) {
+                    const int i = fresh[b] + at - first;
+                    if (at < first) page[k] = a.block_table[b * a.table_stride + at];
+                    else if (i < top) page[k] = a.free_pages[top - 1 - i];
                 }
-                if (page >= 0) slot = (int64_t)page * a.page_tokens + pos % a.page_tokens;
             }
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+#pragma unroll
+        for (int k = 0; k < kSlotRun; ++k)
+            slot[k] = page[k] >= 0 ? (int64_t)page[k] * a.page_tokens + (pos[k] - p.by_page(pos[k]) * a.page_tokens) : -1;
+        if (p.wide && t0 + kSlotRun <= a.tokens) {
+            *(longlong2*)(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+            *(longlong2*)(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+            *(int4*)(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSlotRun; ++k)
+                if (t0 + k < a.tokens) {
+                    a.slots[t0 + k] = slot[k];
+                    a.positions[t0 + k] = pos[k];
+                }
+        }
     }
-    for (int b = me; b <= n; b += all) a.cu_new[b] = s.tokens[b];
     if (me == 0) {
         a.free_left[0] = max(0, top - base[1]);
         a.pages_short[0] = max(0, base[1] - top) + over_total;
-    }
-    // kv_len last: it may be seq_len, which the other CTAs read above
-    if (gridDim.x > 1) cluster_sync();
-    else __syncthreads();
-    for (int b = me; b < n; b += all) {
-        const int add = added_to(a, b);
-        a.kv_len[b] = add < 0 ? 0 : held_of(a, b) + add;
     }
 }
 
@@ -212,8 +231,8 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
 // Eight channels a chunk.  A thread owns the two chunks that rotate with each
 // other (channels j.. and j + rot/2.., or a chunk and its neighbour), so the
 // rotation needs no exchange; head_dim / 16 threads, padded to a power of two,
-// share a row and add its squares by shuffles.  A thread keeps its cosines and
-// sines for kRopeHeads heads of one token.
+// share a row and add its squares by shuffles.  A thread has kRopeHeads heads of
+// one token in flight and keeps its cosines and sines for them.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float* x);
 template <>
@@ -251,18 +270,53 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
     *(uint4*)p = v;
 }
 
-constexpr int kRopeThreads = 256;
-
 template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ rra_qk_norm_rope_args_t a,
-                                                                    int lanes, int heads_each, int units) {
+struct Raw8;  // eight channels as they are in memory
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void get(const float* p) { a = __ldcs((const float4*)p), b = __ldcs((const float4*)p + 1); }
+    __device__ __forceinline__ void to(float* x) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void get(const __nv_bfloat16* p) { v = __ldcs((const uint4*)p); }
+    __device__ __forceinline__ void to(float* x) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeHeads = 4;  // heads of a thread, where there are enough
+
+struct RopeParams {
+    rra_qk_norm_rope_args_t a;
+    Divisor by_units;  // units of a token: kHeads heads each
+    int32_t lanes_log2;
+    int32_t items;     // tokens * units
+};
+
+template <typename T, int kHeads>
+__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams r) {
+    const rra_qk_norm_rope_args_t& a = r.a;
     pdl_release_early();
-    const int pair = (int)threadIdx.x % lanes;             // this thread's pair of chunks
-    const int64_t item = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) / lanes;
-    const int64_t t = item / units;
-    const int h0 = (int)(item % units) * heads_each;
+    const int lanes = 1 << r.lanes_log2;
+    const int pair = (int)threadIdx.x & (lanes - 1);       // this thread's pair of chunks
+    const int64_t at = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> r.lanes_log2;
+    const int item = (int)(at < r.items ? at : r.items - 1);
+    const int t = r.by_units(item);
+    const int h0 = (item - t * r.by_units.d) * kHeads;
     const int pairs = a.head_dim / 16, turning = a.rot / 16;
-    const bool mine = pair < pairs && t < a.tokens;
+    const bool mine = pair < pairs && at < r.items;
     int c0, c1;  // first channels of the two chunks
     if (!a.interleaved && pair < turning) {
         c0 = pair * 8;
@@ -271,7 +325,19 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
         c0 = pair * 16;
         c1 = c0 + 8;
     }
+    const int heads = a.q_heads + a.k_heads;
     pdl_wait();
+    Raw8<T> raw[kHeads][2];
+#pragma unroll
+    for (int e = 0; e < kHeads; ++e) {
+        const int h = h0 + e;
+        if (mine && h < heads) {
+            const T* x = h < a.q_heads ? (const T*)a.q + t * a.q_token_stride + h * a.q_head_stride
+                                       : (const T*)a.k + t * a.k_token_stride + (h - a.q_heads) * a.k_head_stride;
+            raw[e][0].get(x + c0);
+            raw[e][1].get(x + c1);
+        }
+    }
     float cs[8], sn[8];
     const bool turns = mine && pair < turning;
     if (turns) {
@@ -284,32 +350,25 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fffffff);
         }
     }
-    const int heads = a.q_heads + a.k_heads;
     const bool normed = a.q_weight != nullptr || a.k_weight != nullptr;
-    for (int e = 0; e < heads_each; ++e) {  // the same count in every thread: they exchange sums
-        const int h = min(h0 + e, heads - 1);  // past the end the last head again, not stored
-        const bool live = mine && h0 + e < heads;
-        const bool is_q = h < a.q_heads;
-        const int hh = is_q ? h : h - a.q_heads;
-        const T* x = is_q ? (const T*)a.q + t * a.q_token_stride + hh * a.q_head_stride
-                          : (const T*)a.k + t * a.k_token_stride + hh * a.k_head_stride;
-        T* y = is_q ? (T*)a.q_out + t * a.q_out_token_stride + hh * a.q_out_head_stride
-                    : (T*)a.k_out + t * a.k_out_token_stride + hh * a.k_out_head_stride;
-        const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-        float u[8], v[8];
-        if (mine) {
-            load8(x + c0, u);
-            load8(x + c1, v);
+    const float eps = (float)a.eps, each = 1.f / (float)a.head_dim;
+#pragma unroll
+    for (int e = 0; e < kHeads; ++e) {
+        const int h = h0 + e;
+        const bool live = mine && h < heads, is_q = h < a.q_heads;
+        float u[8] = {}, v[8] = {};
+        if (live) {
+            raw[e][0].to(u);
+            raw[e][1].to(v);
         }
         if (normed) {
             float sq = 0.f;
-            if (mine) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sq = fmaf(u[i], u[i], fmaf(v[i], v[i], sq));
-            }
+            for (int i = 0; i < 8; ++i) sq = fmaf(u[i], u[i], fmaf(v[i], v[i], sq));
             for (int o = lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            const float inv = rsqrtf(sq / (float)a.head_dim + (float)a.eps);
-            if (mine && w != nullptr) {
+            const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
+            if (live && w != nullptr) {
+                const float inv = rsqrtf(fmaf(sq, each, eps));
                 float wu[8], wv[8];
                 load8(w + c0, wu);
                 load8(w + c1, wv);
@@ -331,48 +390,41 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = u[2 * i], q = u[2 * i + 1], r = v[2 * i], z = v[2 * i + 1];
+                    const float p = u[2 * i], q = u[2 * i + 1], x = v[2 * i], z = v[2 * i + 1];
                     u[2 * i] = p * cs[i] - q * sn[i];
                     u[2 * i + 1] = q * cs[i] + p * sn[i];
-                    v[2 * i] = r * cs[4 + i] - z * sn[4 + i];
-                    v[2 * i + 1] = z * cs[4 + i] + r * sn[4 + i];
+                    v[2 * i] = x * cs[4 + i] - z * sn[4 + i];
+                    v[2 * i + 1] = z * cs[4 + i] + x * sn[4 + i];
                 }
             }
         }
         if (live) {
+            T* y = is_q ? (T*)a.q_out + t * a.q_out_token_stride + h * a.q_out_head_stride
+                        : (T*)a.k_out + t * a.k_out_token_stride + (h - a.q_heads) * a.k_out_head_stride;
             store8(y + c0, u);
             store8(y + c1, v);
         }
     }
 }
 
-// ================================================ the 4-bit cache: write ====
-// A row (one token, head, K or V) is head_dim / 8 threads: thread m holds the
-// channels of one 4-byte word of the row's codes, that is four channels of two
-// neighbouring groups, so a row's codes leave as one coalesced run.  A group's
-// maximum is taken over its eight threads.
+// ======================================= the 4-bit cache: write and read ====
+// A row (one token, head, K or V) is head_dim / 8 threads of eight neighbouring
+// channels, so values move in 16-byte vectors and a group's maximum is taken
+// over four threads.  In the row's codes those eight channels are two half
+// words (four channels each) that belong to different words; thread 4 j + u
+// (group j) swaps one of them with its neighbour in group j ^ 1, after which
+// each holds a whole word and the row's codes leave as one coalesced run.
+// Bound by the values' traffic; a thread has kKvRows rows in flight.
 constexpr int kKvThreads = 256;
+constexpr int kKvRows = 4;
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float* x);
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, float* x) {
-    const float4 v = *(const float4*)p;
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-    const uint2 v = *(const uint2*)p;
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float* x) { *(float4*)p = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *(uint2*)p = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
-}
+struct KvTokensParams {
+    rra_kv_tokens_args_t a;
+    Divisor by_heads;  // K and V of every head: 2 * kv_heads
+    Divisor by_page;   // blocks of a page
+    int32_t rows;      // tokens * 2 * kv_heads
+    int32_t stride;    // rows between those of a thread
+};
 
 // Two values as e2m1, `lo` in the low nibble: nearest, ties to even, saturating.
 __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
@@ -380,101 +432,146 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
     asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Address of the head's block and token row of a slot; null if the slot is outside the cache.
-template <int D>
-__device__ __forceinline__ char* kv_block(const rra_kv_cache_t& c, int64_t slot, int head, int& row) {
-    if (slot < 0 || slot >= c.num_pages * c.page_tokens) return nullptr;
-    const int64_t page = slot / c.page_tokens;
-    const int in = (int)(slot - page * c.page_tokens);
-    row = in % kKvBlockTokens;
-    const int blocks = c.page_tokens / kKvBlockTokens;
-    return (char*)c.pages + ((page * c.kv_heads + head) * blocks + in / kKvBlockTokens) * KvBlock<D>::kBytes;
+
+// x / d as far as its rounding to e2m1 goes, `by` being 1 / d rounded.
+template <typename T>
+__device__ __forceinline__ float quotient(float x, float d, float by);
+template <>
+__device__ __forceinline__ float quotient<float>(float x, float d, float) {
+    return __fdiv_rn(x, d);
+}
+// bfloat16 values (8 bits) over a scale of 11 bits are a midpoint of two codes (3 bits) or at least 2^-14 of it away, so
+// the product with the reciprocal (within 2^-22), rounded to 18 bits, lies on the same side, or on the midpoint itself.
+// The rounded division took 2.5 times the instructions of the rest of the write.
+template <>
+__device__ __forceinline__ float quotient<__nv_bfloat16>(float x, float, float by) {
+    return __uint_as_float((__float_as_uint(x * by) + 0x20u) & 0xffffffc0u);
+}
+
+// Row i of a call: its token, head, whether it is V, and its block and row there; block < 0 if the slot is outside.
+struct KvRow {
+    int32_t token, head, row;
+    bool is_v;
+    int64_t block;
+};
+__device__ __forceinline__ KvRow kv_row(const KvTokensParams& p, int i) {
+    KvRow r;
+    const rra_kv_cache_t& c = p.a.cache;
+    r.token = p.by_heads(i);
+    const int in = i - r.token * p.by_heads.d;
+    r.head = in >> 1;
+    r.is_v = in & 1;
+    const int64_t slot = __ldg(p.a.slots + r.token);
+    r.row = (int)(slot & (kKvBlockTokens - 1));
+    r.block = -1;
+    if (slot >= 0 && slot < c.num_pages * c.page_tokens) {
+        const int at = (int)(slot / kKvBlockTokens), page = p.by_page(at);
+        r.block = ((int64_t)page * c.kv_heads + r.head) * p.by_page.d + (at - page * p.by_page.d);
+    }
+    return r;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ rra_kv_tokens_args_t a) {
+__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ KvTokensParams p) {
     using B = KvBlock<D>;
-    constexpr int kLanes = D / 8, kHalf = B::kGroups / 2;
+    constexpr int kLanes = D / 8;
+    const rra_kv_tokens_args_t& a = p.a;
     pdl_release_early();
-    const int m = (int)threadIdx.x % kLanes;
-    const int c = m / kHalf, j = m % kHalf * 2;
-    const int64_t row_id = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) / kLanes;
-    const int64_t th = row_id >> 1;  // K and V of one token and head sit side by side
-    const bool is_v = row_id & 1;
-    const int64_t t = th / a.cache.kv_heads;
-    const int h = (int)(th - t * a.cache.kv_heads);
+    const int m = (int)threadIdx.x % kLanes, j = m >> 2, u = m & 3;
+    const int first = ((int)blockIdx.x * kKvThreads + (int)threadIdx.x) / kLanes;
     pdl_wait();
-    int row = 0;
-    char* const block = t < a.tokens ? kv_block<D>(a.cache, a.slots[t], h, row) : nullptr;
-    float x[2][4] = {};
-    if (block != nullptr) {
-        const T* p = is_v ? (const T*)a.v + t * a.v_token_stride + h * a.v_head_stride
-                          : (const T*)a.k + t * a.k_token_stride + h * a.k_head_stride;
-        load4(p + kKvGroup * j + 4 * c, x[0]);
-        load4(p + kKvGroup * (j + 1) + 4 * c, x[1]);
-    }
-    float s[2];
+    KvRow row[kKvRows];
+    Raw8<T> raw[kKvRows];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int k = 0; k < kKvRows; ++k) {
+        const int i = first + k * p.stride;
+        row[k].block = -1;
+        if (first < p.stride && i < p.rows) row[k] = kv_row(p, i);
+        if (row[k].block >= 0) {
+            const KvRow& r = row[k];
+            raw[k].get(r.is_v ? (const T*)a.v + r.token * a.v_token_stride + r.head * a.v_head_stride + 8 * m
+                              : (const T*)a.k + r.token * a.k_token_stride + r.head * a.k_head_stride + 8 * m);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kKvRows; ++k) {
+        const KvRow& r = row[k];
+        float x[8] = {};
+        if (r.block >= 0) raw[k].to(x);
         float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[g][i] = x[g][i] == x[g][i] ? x[g][i] : 0.f;  // NaN is stored as 0
-            most = fmaxf(most, fabsf(x[g][i]));
+        for (int i = 0; i < 8; ++i) {
+            x[i] = x[i] == x[i] ? x[i] : 0.f;  // NaN is stored as 0
+            most = fmaxf(most, fabsf(x[i]));
         }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const __half s = __float2half_rn(fminf(fmaxf(most * (1.f / 6.f), 6.103515625e-05f), 2048.f));
+        const float d = __half2float(s), by = __frcp_rn(d);
+        uint32_t half[2];  // channels 0..3 and 4..7
 #pragma unroll
-        for (int o = kHalf; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        s[g] = fminf(fmaxf(most * (1.f / 6.f), 6.103515625e-05f), 2048.f);
+        for (int h = 0; h < 2; ++h)
+            half[h] = to_e2m1x2(quotient<T>(x[4 * h], d, by), quotient<T>(x[4 * h + 1], d, by)) |
+                      to_e2m1x2(quotient<T>(x[4 * h + 2], d, by), quotient<T>(x[4 * h + 3], d, by)) << 8;
+        // even groups keep their first half and get their neighbour's, odd ones the second
+        const bool odd = j & 1;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? half[0] : half[1], 4);
+        const uint32_t word = odd ? got | half[1] << 16 : half[0] | got << 16;
+        if (r.block >= 0) {
+            char* const block = (char*)a.cache.pages + r.block * B::kBytes;
+            const int c = 2 * u + (odd ? 1 : 0);
+            *(uint32_t*)(block + (r.is_v ? B::kV : 0) + r.row * B::kRow + (c * B::kGroups + (j & ~1)) * 2) = word;
+            if (u == 0) *(__half*)(block + (r.is_v ? B::kScaleV : B::kScaleK) + r.row * B::kScaleRow + 2 * j) = s;
+        }
     }
-    if (block == nullptr) return;
-    const __half2 sh = __floats2half2_rn(s[0], s[1]);
-    const float2 sf = __half22float2(sh);
-    uint32_t word = 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const float d = g ? sf.y : sf.x;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)  // the division decides ties as written down, so it is the rounded one
-            word |= to_e2m1x2(__fdiv_rn(x[g][2 * i], d), __fdiv_rn(x[g][2 * i + 1], d)) << (16 * g + 8 * i);
-    }
-    *(uint32_t*)(block + (is_v ? B::kV : 0) + row * B::kRow + 4 * m) = word;
-    if (c == 0) *(__half2*)(block + (is_v ? B::kScaleV : B::kScaleK) + row * B::kScaleRow + 2 * j) = sh;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ rra_kv_tokens_args_t a) {
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvTokensParams p) {
     using B = KvBlock<D>;
-    constexpr int kLanes = D / 8, kHalf = B::kGroups / 2;
+    constexpr int kLanes = D / 8;
+    const rra_kv_tokens_args_t& a = p.a;
     pdl_release_early();
-    const int m = (int)threadIdx.x % kLanes;
-    const int c = m / kHalf, j = m % kHalf * 2;
-    const int64_t row_id = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) / kLanes;
-    const int64_t th = row_id >> 1;
-    const bool is_v = row_id & 1;
-    const int64_t t = th / a.cache.kv_heads;
-    const int h = (int)(th - t * a.cache.kv_heads);
+    const int m = (int)threadIdx.x % kLanes, j = m >> 2, u = m & 3;
+    const int first = ((int)blockIdx.x * kKvThreads + (int)threadIdx.x) / kLanes;
     pdl_wait();
-    if (t >= a.tokens) return;
-    int row = 0;
-    const char* const block = kv_block<D>(a.cache, a.slots[t], h, row);
-    float x[2][4] = {};
-    if (block != nullptr) {
-        const uint32_t word = *(const uint32_t*)(block + (is_v ? B::kV : 0) + row * B::kRow + 4 * m);
-        const __half2 sh = *(const __half2*)(block + (is_v ? B::kScaleV : B::kScaleK) + row * B::kScaleRow + 2 * j);
+    KvRow row[kKvRows];
+    uint32_t word[kKvRows];
+    __half scale[kKvRows];
+    const bool odd = j & 1;
+#pragma unroll
+    for (int k = 0; k < kKvRows; ++k) {
+        const int i = first + k * p.stride;
+        row[k].block = -1;
+        row[k].token = -1;
+        if (first < p.stride && i < p.rows) row[k] = kv_row(p, i);
+        word[k] = 0u;
+        scale[k] = __ushort_as_half(0);
+        if (row[k].block >= 0) {
+            const KvRow& r = row[k];
+            const char* const block = (const char*)a.cache.pages + r.block * B::kBytes;
+            word[k] = *(const uint32_t*)(block + (r.is_v ? B::kV : 0) + r.row * B::kRow + ((2 * u + (odd ? 1 : 0)) * B::kGroups + (j & ~1)) * 2);
+            scale[k] = *(const __half*)(block + (r.is_v ? B::kScaleV : B::kScaleK) + r.row * B::kScaleRow + 2 * j);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kKvRows; ++k) {
+        const KvRow& r = row[k];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? word[k] & 0xffffu : word[k] >> 16, 4);
         uint32_t v[4];
-        from_e2m1x8(word, v);
+        from_e2m1x8(odd ? got | (word[k] & 0xffff0000u) : (word[k] & 0xffffu) | got << 16, v);
+        const float d = __half2float(scale[k]);
+        float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*(const __half2*)&v[i]);
-            const float d = i < 2 ? __low2float(sh) : __high2float(sh);
-            x[i >> 1][(i & 1) * 2] = f.x * d;
-            x[i >> 1][(i & 1) * 2 + 1] = f.y * d;
+            x[2 * i] = f.x * d;
+            x[2 * i + 1] = f.y * d;
         }
+        if (r.token >= 0)
+            store8(r.is_v ? (T*)a.v + r.token * a.v_token_stride + r.head * a.v_head_stride + 8 * m
+                          : (T*)a.k + r.token * a.k_token_stride + r.head * a.k_head_stride + 8 * m, x);
     }
-    T* p = is_v ? (T*)a.v + t * a.v_token_stride + h * a.v_head_stride
-                : (T*)a.k + t * a.k_token_stride + h * a.k_head_stride;
-    store4(p + kKvGroup * j + 4 * c, x[0]);
-    store4(p + kKvGroup * (j + 1) + 4 * c, x[1]);
 }
 
 static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream, bool append) {
@@ -488,9 +585,16 @@ static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream
         return RRA_ERR_INVALID_ARG;
     if (a->tokens == 0) return RRA_OK;
     if (a->k == nullptr || a->v == nullptr || a->slots == nullptr) return RRA_ERR_INVALID_ARG;
-    const int64_t threads = a->tokens * c.kv_heads * 2 * (c.head_dim / 8);
-    const int64_t blocks = (threads + kKvThreads - 1) / kKvThreads;
-    if (a->tokens > (INT64_MAX >> 24) || blocks > INT32_MAX) return RRA_ERR_INVALID_ARG;
+    if (a->tokens > INT32_MAX / 64 / c.kv_heads) return RRA_ERR_INVALID_ARG;  // rows' threads are counted in 32 bits
+    KvTokensParams p;
+    p.a = *a;
+    p.by_heads = Divisor(2 * c.kv_heads);
+    p.by_page = Divisor(c.page_tokens / kKvBlockTokens);
+    p.rows = (int)(a->tokens * 2 * c.kv_heads);
+    // few rows: one a thread, so that every SM has some
+    const int per_cta = kKvThreads / (c.head_dim / 8);
+    p.stride = p.rows >= 4096 ? (p.rows + kKvRows - 1) / kKvRows : p.rows;
+    const int blocks = (p.stride + per_cta - 1) / per_cta;
     const void* k;
     if (append)
         k = elem == 4 ? (c.head_dim == 64 ? (const void*)kv_append_kernel<float, 64> : (const void*)kv_append_kernel<float, 128>)
@@ -500,7 +604,7 @@ static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream
         k = elem == 4 ? (c.head_dim == 64 ? (const void*)kv_read_kernel<float, 64> : (const void*)kv_read_kernel<float, 128>)
                       : (c.head_dim == 64 ? (const void*)kv_read_kernel<__nv_bfloat16, 64>
                                           : (const void*)kv_read_kernel<__nv_bfloat16, 128>);
-    void* args[] = {(void*)a};
+    void* args[] = {(void*)&p};
     return serve_launch(k, dim3((unsigned)blocks), kKvThreads, 0, 1, stream, args);
 }
 
@@ -523,15 +627,21 @@ rra_status_t rra_slot_map(const rra_slot_map_args_t* args, rra_stream_t stream) 
     if ((a.num_pages > 0 && a.free_pages == nullptr) || (a.tokens > 0 && (a.slots == nullptr || a.positions == nullptr)))
         return RRA_ERR_INVALID_ARG;
     const void* k = (const void*)rra::slot_map_kernel;
-    const size_t smem = 3 * sizeof(int32_t) * ((size_t)a.requests + 1);
-    if (rra::configure_cluster_kernel(k, 3 * (int)sizeof(int32_t) * (RRA_SERVE_MAX_REQUESTS + 1)) != cudaSuccess) {
+    const size_t smem = 4 * sizeof(int32_t) * ((size_t)a.requests + 1);
+    if (rra::configure_cluster_kernel(k, 4 * (int)sizeof(int32_t) * (RRA_SERVE_MAX_REQUESTS + 1)) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
-    const int64_t items = a.tokens + a.requests;
+    rra::SlotParams p;
+    p.a = a;
+    p.by_page = rra::Divisor(a.page_tokens);
+    p.most_new = rra::kSlotMost / (a.requests > 0 ? a.requests : 1);
+    p.wide = rra::aligned16(a.slots) && rra::aligned16(a.positions);
+    // as many CTAs as have two runs of tokens a thread
+    const int64_t items = a.tokens / rra::kSlotRun + a.requests;
     int ctas = 1;
     while (ctas < rra::kSlotMaxCluster && (int64_t)ctas * rra::kSlotThreads * 2 < items) ctas *= 2;
-    void* kargs[] = {(void*)args};
+    void* kargs[] = {(void*)&p};
     return rra::serve_launch(k, dim3((unsigned)ctas), rra::kSlotThreads, smem, ctas, stream, kargs);
 }
 
@@ -557,17 +667,22 @@ rra_status_t rra_qk_norm_rope(const rra_qk_norm_rope_args_t* args, rra_stream_t 
     if (a.rot > 0 && (a.cos == nullptr || a.sin == nullptr || a.positions == nullptr || !rra::aligned16(a.cos) ||
                       !rra::aligned16(a.sin)))
         return RRA_ERR_INVALID_ARG;
-    int lanes = 1;
-    while (lanes < a.head_dim / 16) lanes *= 2;
     const int heads = a.q_heads + a.k_heads;
-    const int heads_each = a.tokens * heads >= 16384 ? 4 : 1;
-    int units = (heads + heads_each - 1) / heads_each;
-    const int64_t threads = a.tokens * units * lanes;
-    const int64_t blocks = (threads + rra::kRopeThreads - 1) / rra::kRopeThreads;
-    if (blocks > INT32_MAX) return RRA_ERR_INVALID_ARG;
-    int each = heads_each;
-    void* kargs[] = {(void*)args, &lanes, &each, &units};
-    const void* k = elem == 4 ? (const void*)rra::qk_norm_rope_kernel<float> : (const void*)rra::qk_norm_rope_kernel<__nv_bfloat16>;
+    if (a.q_heads > INT32_MAX / 4 || a.k_heads > INT32_MAX / 4 || a.tokens > INT32_MAX / 2 / heads) return RRA_ERR_INVALID_ARG;
+    rra::RopeParams r;
+    r.a = a;
+    r.lanes_log2 = 0;
+    while (1 << r.lanes_log2 < a.head_dim / 16) ++r.lanes_log2;
+    const bool many = a.tokens * heads >= 16384;
+    const int each = many ? rra::kRopeHeads : 1, units = (heads + each - 1) / each;
+    r.by_units = rra::Divisor(units);
+    r.items = (int)(a.tokens * units);
+    const int64_t blocks = (((int64_t)r.items << r.lanes_log2) + rra::kRopeThreads - 1) / rra::kRopeThreads;
+    void* kargs[] = {(void*)&r};
+    const void* k = elem == 4 ? (many ? (const void*)rra::qk_norm_rope_kernel<float, rra::kRopeHeads>
+                                      : (const void*)rra::qk_norm_rope_kernel<float, 1>)
+                              : (many ? (const void*)rra::qk_norm_rope_kernel<__nv_bfloat16, rra::kRopeHeads>
+                                      : (const void*)rra::qk_norm_rope_kernel<__nv_bfloat16, 1>);
     return rra::serve_launch(k, dim3((unsigned)blocks), rra::kRopeThreads, 0, 1, stream, kargs);
 }
 

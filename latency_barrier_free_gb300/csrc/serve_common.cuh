@@ -36,10 +36,25 @@ __device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t* out) {
         : "r"(w));
 }
 
+// Blocks of all pages and heads are counted in 32 bits (2^31 of them would be terabytes).
 inline bool kv_cache_ok(const rra_kv_cache_t& c) {
     return c.pages != nullptr && ((uintptr_t)c.pages & 15) == 0 && c.num_pages >= 0 && c.num_pages <= INT32_MAX &&
-           c.reserved == 0 && rra_kv_page_bytes(c.page_tokens, c.kv_heads, c.head_dim) != 0;
+           c.reserved == 0 && rra_kv_page_bytes(c.page_tokens, c.kv_heads, c.head_dim) != 0 &&
+           c.num_pages * (c.page_tokens / kKvBlockTokens) <= INT32_MAX / c.kv_heads;
 }
+
+// Division of 0 <= x < 2^31 by a divisor the host knows: x * ceil(2^(31 + s) / d) >> (31 + s) with 2^s >= d is exact,
+// since the factor's excess is below d <= 2^s, so the product's is below x / 2^31 < 1 part in d.
+struct Divisor {
+    uint32_t factor, shift;
+    int32_t d;
+    Divisor() = default;
+    explicit Divisor(int32_t by) : factor(0), shift(31), d(by) {
+        while (shift < 62 && (int64_t)1 << (shift - 31) < by) ++shift;
+        factor = (uint32_t)((((uint64_t)1 << shift) + (uint64_t)by - 1) / (uint64_t)by);
+    }
+    __device__ __forceinline__ int operator()(int x) const { return (int)(((uint64_t)(uint32_t)x * factor) >> shift); }
+};
 
 // Rows of `heads` heads: both strides hold whole 16-byte vectors, and one
 // head's channels do not run into the next.
