@@ -300,13 +300,14 @@ constexpr int kRopeHeads = 4;  // heads of a thread, where there are enough
 
 struct RopeParams {
     rra_qk_norm_rope_args_t a;
-    Divisor by_units;  // units of a token: kHeads heads each
+    Divisor by_units;  // units of a token: kHeads heads of q, or of k
+    int32_t q_units;
     int32_t lanes_log2;
     int32_t items;     // tokens * units
 };
 
 template <typename T, int kHeads>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams r) {
+__global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 3 : 4) qk_norm_rope_kernel(const __grid_constant__ RopeParams r) {
     const rra_qk_norm_rope_args_t& a = r.a;
     pdl_release_early();
     const int lanes = 1 << r.lanes_log2;
@@ -314,9 +315,12 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
     const int64_t at = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> r.lanes_log2;
     const int item = (int)(at < r.items ? at : r.items - 1);
     const int t = r.by_units(item);
-    const int h0 = (item - t * r.by_units.d) * kHeads;
+    const int unit = item - t * r.by_units.d;
+    const bool is_q = unit < r.q_units;
+    const int h0 = (is_q ? unit : unit - r.q_units) * kHeads;
     const int pairs = a.head_dim / 16, turning = a.rot / 16;
     const bool mine = pair < pairs && at < r.items;
+    const int live = mine ? min(kHeads, (is_q ? a.q_heads : a.k_heads) - h0) : 0;  // heads of this thread
     int c0, c1;  // first channels of the two chunks
     if (!a.interleaved && pair < turning) {
         c0 = pair * 8;
@@ -325,20 +329,19 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
         c0 = pair * 16;
         c1 = c0 + 8;
     }
-    const int heads = a.q_heads + a.k_heads;
+    const int64_t head_stride = is_q ? a.q_head_stride : a.k_head_stride;
+    const T* x = (is_q ? (const T*)a.q + t * a.q_token_stride : (const T*)a.k + t * a.k_token_stride) + h0 * head_stride;
+    const T* const w = (const T*)(is_q ? a.q_weight : a.k_weight);
     pdl_wait();
     Raw8<T> raw[kHeads][2];
 #pragma unroll
-    for (int e = 0; e < kHeads; ++e) {
-        const int h = h0 + e;
-        if (mine && h < heads) {
-            const T* x = h < a.q_heads ? (const T*)a.q + t * a.q_token_stride + h * a.q_head_stride
-                                       : (const T*)a.k + t * a.k_token_stride + (h - a.q_heads) * a.k_head_stride;
+    for (int e = 0; e < kHeads; ++e)
+        if (e < live) {
             raw[e][0].get(x + c0);
             raw[e][1].get(x + c1);
+            x += head_stride;
         }
-    }
-    float cs[8], sn[8];
+    float cs[8], sn[8], wu[8], wv[8];
     const bool turns = mine && pair < turning;
     if (turns) {
         const int64_t p = a.positions[t];
@@ -350,33 +353,31 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fffffff);
         }
     }
-    const bool normed = a.q_weight != nullptr || a.k_weight != nullptr;
+    if (mine && w != nullptr) {
+        load8(w + c0, wu);
+        load8(w + c1, wv);
+    }
     const float eps = (float)a.eps, each = 1.f / (float)a.head_dim;
+    const int64_t out_stride = is_q ? a.q_out_head_stride : a.k_out_head_stride;
+    T* y = (is_q ? (T*)a.q_out + t * a.q_out_token_stride : (T*)a.k_out + t * a.k_out_token_stride) + h0 * out_stride;
 #pragma unroll
     for (int e = 0; e < kHeads; ++e) {
-        const int h = h0 + e;
-        const bool live = mine && h < heads, is_q = h < a.q_heads;
         float u[8] = {}, v[8] = {};
-        if (live) {
+        if (e < live) {
             raw[e][0].to(u);
             raw[e][1].to(v);
         }
-        if (normed) {
-            float sq = 0.f;
+        float sq = 0.f;  // exchanged by every thread, whether its heads are normed or not
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sq = fmaf(u[i], u[i], fmaf(v[i], v[i], sq));
-            for (int o = lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-            if (live && w != nullptr) {
-                const float inv = rsqrtf(fmaf(sq, each, eps));
-                float wu[8], wv[8];
-                load8(w + c0, wu);
-                load8(w + c1, wv);
+        for (int i = 0; i < 8; ++i) sq = fmaf(u[i], u[i], fmaf(v[i], v[i], sq));
+        for (int o = lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        if (e >= live) continue;
+        if (w != nullptr) {
+            const float inv = rsqrtf(fmaf(sq, each, eps));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    u[i] = u[i] * inv * wu[i];
-                    v[i] = v[i] * inv * wv[i];
-                }
+            for (int i = 0; i < 8; ++i) {
+                u[i] = u[i] * inv * wu[i];
+                v[i] = v[i] * inv * wv[i];
             }
         }
         if (turns) {
@@ -390,40 +391,39 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = u[2 * i], q = u[2 * i + 1], x = v[2 * i], z = v[2 * i + 1];
+                    const float p = u[2 * i], q = u[2 * i + 1], z0 = v[2 * i], z1 = v[2 * i + 1];
                     u[2 * i] = p * cs[i] - q * sn[i];
                     u[2 * i + 1] = q * cs[i] + p * sn[i];
-                    v[2 * i] = x * cs[4 + i] - z * sn[4 + i];
-                    v[2 * i + 1] = z * cs[4 + i] + x * sn[4 + i];
+                    v[2 * i] = z0 * cs[4 + i] - z1 * sn[4 + i];
+                    v[2 * i + 1] = z1 * cs[4 + i] + z0 * sn[4 + i];
                 }
             }
         }
-        if (live) {
-            T* y = is_q ? (T*)a.q_out + t * a.q_out_token_stride + h * a.q_out_head_stride
-                        : (T*)a.k_out + t * a.k_out_token_stride + (h - a.q_heads) * a.k_out_head_stride;
-            store8(y + c0, u);
-            store8(y + c1, v);
-        }
+        store8(y + c0, u);
+        store8(y + c1, v);
+        y += out_stride;
     }
 }
 
 // ======================================= the 4-bit cache: write and read ====
-// A row (one token, head, K or V) is head_dim / 8 threads of eight neighbouring
-// channels, so values move in 16-byte vectors and a group's maximum is taken
-// over four threads.  In the row's codes those eight channels are two half
-// words (four channels each) that belong to different words; thread 4 j + u
-// (group j) swaps one of them with its neighbour in group j ^ 1, after which
-// each holds a whole word and the row's codes leave as one coalesced run.
-// Bound by the values' traffic; a thread has kKvRows rows in flight.
+// The K and V rows of a token and head are head_dim / 8 threads of eight
+// neighbouring channels, so values move in 16-byte vectors and a group's
+// maximum is taken over four threads.  In a row's codes those eight channels
+// are two half words (four channels each) that belong to different words;
+// thread 4 j + u (group j) swaps one of them with its neighbour in group j ^ 1,
+// after which each holds a whole word and the row's codes leave as one
+// coalesced run.  Bound by the values' traffic as long as the arithmetic (about
+// seven instructions a value) stays under it; a thread has kKvPairs pairs of
+// rows in flight.
 constexpr int kKvThreads = 256;
-constexpr int kKvRows = 4;
+constexpr int kKvPairs = 2;
 
 struct KvTokensParams {
     rra_kv_tokens_args_t a;
-    Divisor by_heads;  // K and V of every head: 2 * kv_heads
+    Divisor by_heads;
     Divisor by_page;   // blocks of a page
-    int32_t rows;      // tokens * 2 * kv_heads
-    int32_t stride;    // rows between those of a thread
+    int32_t pairs;     // tokens * kv_heads
+    int32_t stride;    // pairs between those of a thread
 };
 
 // Two values as e2m1, `lo` in the low nibble: nearest, ties to even, saturating.
@@ -432,41 +432,86 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
     asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The codes of four values over their scale d (by = 1 / d, rounded).
+__device__ __forceinline__ uint32_t codes4(const float* y) {
+    return to_e2m1x2(y[0], y[1]) | to_e2m1x2(y[2], y[3]) << 8;
+}
 
-// x / d as far as its rounding to e2m1 goes, `by` being 1 / d rounded.
+// Eight channels of a row being written: the group's part of the maximum, and the codes of channels 0..3 and 4..7.
 template <typename T>
-__device__ __forceinline__ float quotient(float x, float d, float by);
+struct KvWrite;
 template <>
-__device__ __forceinline__ float quotient<float>(float x, float d, float) {
-    return __fdiv_rn(x, d);
-}
-// bfloat16 values (8 bits) over a scale of 11 bits are a midpoint of two codes (3 bits) or at least 2^-14 of it away, so
-// the product with the reciprocal (within 2^-22), rounded to 18 bits, lies on the same side, or on the midpoint itself.
-// The rounded division took 2.5 times the instructions of the rest of the write.
+struct KvWrite<float> {
+    Raw8<float> raw;
+    __device__ __forceinline__ void clean() {  // NaN is stored as 0
+        float* const x = (float*)&raw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] : 0.f;
+    }
+    __device__ __forceinline__ float most() const {
+        float x[8], m = 0.f;
+        raw.to(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+        return m;
+    }
+    __device__ __forceinline__ void codes(float d, float, uint32_t half[2]) const {
+        float x[8];
+        raw.to(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], d);
+        half[0] = codes4(x);
+        half[1] = codes4(x + 4);
+    }
+};
+// bfloat16 values (8 bits) over a scale of 11 bits are a midpoint of two codes (a multiple of 1/4 of at most 3 bits) or at
+// least 2^-14 of it away.  x / d enters the rounding as x * (1 / d), within 2^-24 of it, put on a grid of 2^-19 by adding
+// and taking off 24 (so that sums lie in [16, 32)): what was a midpoint is one again, and nothing else becomes one.  The
+// rounded division took more instructions than all the rest (16384 tokens, 8 heads of 128: 40 us against 21 us).
 template <>
-__device__ __forceinline__ float quotient<__nv_bfloat16>(float x, float, float by) {
-    return __uint_as_float((__float_as_uint(x * by) + 0x20u) & 0xffffffc0u);
-}
+struct KvWrite<__nv_bfloat16> {
+    Raw8<__nv_bfloat16> raw;
+    __device__ __forceinline__ void clean() {
+        // a sum of the eight that is NaN shows that one is (or that infinities cancelled): rare, then look at each
+        const __nv_bfloat162* w = (const __nv_bfloat162*)&raw;
+        const __nv_bfloat162 sum = __hadd2(__hadd2(w[0], w[1]), __hadd2(w[2], w[3]));
+        if (__low2float(sum) + __high2float(sum) == __low2float(sum) + __high2float(sum)) return;
+        uint16_t* const x = (uint16_t*)&raw;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((x[i] & 0x7fff) > 0x7f80) x[i] = 0;
+    }
+    __device__ __forceinline__ float most() const {
+        const __nv_bfloat162* w = (const __nv_bfloat162*)&raw;
+        const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(w[0]), __habs2(w[1])), __hmax2(__habs2(w[2]), __habs2(w[3])));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ void codes(float, float by, uint32_t half[2]) const {
+        float x[8];
+        raw.to(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = copysignf(__fadd_rn(__fmaf_rn(fabsf(x[i]), by, 24.f), -24.f), x[i]);
+        half[0] = codes4(x);
+        half[1] = codes4(x + 4);
+    }
+};
 
-// Row i of a call: its token, head, whether it is V, and its block and row there; block < 0 if the slot is outside.
-struct KvRow {
+// Pair i of a call: its token and head, and where its block and row are; block < 0 if the slot is outside.
+struct KvPair {
     int32_t token, head, row;
-    bool is_v;
     int64_t block;
 };
-__device__ __forceinline__ KvRow kv_row(const KvTokensParams& p, int i) {
-    KvRow r;
+__device__ __forceinline__ KvPair kv_pair(const KvTokensParams& p, int i) {
+    KvPair r;
     const rra_kv_cache_t& c = p.a.cache;
     r.token = p.by_heads(i);
-    const int in = i - r.token * p.by_heads.d;
-    r.head = in >> 1;
-    r.is_v = in & 1;
+    r.head = i - r.token * p.by_heads.d;
     const int64_t slot = __ldg(p.a.slots + r.token);
-    r.row = (int)(slot & (kKvBlockTokens - 1));
+    r.row = (int)slot & (kKvBlockTokens - 1);
     r.block = -1;
-    if (slot >= 0 && slot < c.num_pages * c.page_tokens) {
+    if ((uint64_t)slot < (uint64_t)(c.num_pages * c.page_tokens)) {
         const int at = (int)(slot / kKvBlockTokens), page = p.by_page(at);
-        r.block = ((int64_t)page * c.kv_heads + r.head) * p.by_page.d + (at - page * p.by_page.d);
+        r.block = (page * c.kv_heads + r.head) * p.by_page.d + (at - page * p.by_page.d);
     }
     return r;
 }
@@ -480,48 +525,44 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
     const int m = (int)threadIdx.x % kLanes, j = m >> 2, u = m & 3;
     const int first = ((int)blockIdx.x * kKvThreads + (int)threadIdx.x) / kLanes;
     pdl_wait();
-    KvRow row[kKvRows];
-    Raw8<T> raw[kKvRows];
+    KvPair pair[kKvPairs];
+    KvWrite<T> in[kKvPairs][2];
 #pragma unroll
-    for (int k = 0; k < kKvRows; ++k) {
+    for (int k = 0; k < kKvPairs; ++k) {
         const int i = first + k * p.stride;
-        row[k].block = -1;
-        if (first < p.stride && i < p.rows) row[k] = kv_row(p, i);
-        if (row[k].block >= 0) {
-            const KvRow& r = row[k];
-            raw[k].get(r.is_v ? (const T*)a.v + r.token * a.v_token_stride + r.head * a.v_head_stride + 8 * m
-                              : (const T*)a.k + r.token * a.k_token_stride + r.head * a.k_head_stride + 8 * m);
+        pair[k].block = -1;
+        if (first < p.stride && i < p.pairs) pair[k] = kv_pair(p, i);
+        if (pair[k].block >= 0) {
+            const KvPair& r = pair[k];
+            in[k][0].raw.get((const T*)a.k + r.token * a.k_token_stride + r.head * a.k_head_stride + 8 * m);
+            in[k][1].raw.get((const T*)a.v + r.token * a.v_token_stride + r.head * a.v_head_stride + 8 * m);
+        } else {
+            in[k][0] = in[k][1] = KvWrite<T>{};
         }
     }
+    const bool odd = j & 1;
+    const int word_at = ((2 * u + (odd ? 1 : 0)) * B::kGroups + (j & ~1)) * 2;
 #pragma unroll
-    for (int k = 0; k < kKvRows; ++k) {
-        const KvRow& r = row[k];
-        float x[8] = {};
-        if (r.block >= 0) raw[k].to(x);
-        float most = 0.f;
+    for (int k = 0; k < kKvPairs; ++k) {
+        char* const block = (char*)a.cache.pages + pair[k].block * B::kBytes;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = x[i] == x[i] ? x[i] : 0.f;  // NaN is stored as 0
-            most = fmaxf(most, fabsf(x[i]));
-        }
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        const __half s = __float2half_rn(fminf(fmaxf(most * (1.f / 6.f), 6.103515625e-05f), 2048.f));
-        const float d = __half2float(s), by = __frcp_rn(d);
-        uint32_t half[2];  // channels 0..3 and 4..7
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            half[h] = to_e2m1x2(quotient<T>(x[4 * h], d, by), quotient<T>(x[4 * h + 1], d, by)) |
-                      to_e2m1x2(quotient<T>(x[4 * h + 2], d, by), quotient<T>(x[4 * h + 3], d, by)) << 8;
-        // even groups keep their first half and get their neighbour's, odd ones the second
-        const bool odd = j & 1;
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? half[0] : half[1], 4);
-        const uint32_t word = odd ? got | half[1] << 16 : half[0] | got << 16;
-        if (r.block >= 0) {
-            char* const block = (char*)a.cache.pages + r.block * B::kBytes;
-            const int c = 2 * u + (odd ? 1 : 0);
-            *(uint32_t*)(block + (r.is_v ? B::kV : 0) + r.row * B::kRow + (c * B::kGroups + (j & ~1)) * 2) = word;
-            if (u == 0) *(__half*)(block + (r.is_v ? B::kScaleV : B::kScaleK) + r.row * B::kScaleRow + 2 * j) = s;
+        for (int v = 0; v < 2; ++v) {
+            KvWrite<T>& x = in[k][v];
+            x.clean();
+            float most = x.most();
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const __half s = __float2half_rn(fminf(fmaxf(most * (1.f / 6.f), 6.103515625e-05f), 2048.f));
+            const float d = __half2float(s);
+            uint32_t half[2];
+            x.codes(d, __frcp_rn(d), half);
+            // even groups keep their first half and get their neighbour's, odd ones the second
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? half[0] : half[1], 4);
+            const uint32_t word = odd ? got | half[1] << 16 : half[0] | got << 16;
+            if (pair[k].block >= 0) {
+                *(uint32_t*)(block + v * B::kV + pair[k].row * B::kRow + word_at) = word;
+                if (u == 0) *(__half*)(block + (v ? B::kScaleV : B::kScaleK) + pair[k].row * B::kScaleRow + 2 * j) = s;
+            }
         }
     }
 }
@@ -534,44 +575,48 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
     pdl_release_early();
     const int m = (int)threadIdx.x % kLanes, j = m >> 2, u = m & 3;
     const int first = ((int)blockIdx.x * kKvThreads + (int)threadIdx.x) / kLanes;
-    pdl_wait();
-    KvRow row[kKvRows];
-    uint32_t word[kKvRows];
-    __half scale[kKvRows];
     const bool odd = j & 1;
+    const int word_at = ((2 * u + (odd ? 1 : 0)) * B::kGroups + (j & ~1)) * 2;
+    pdl_wait();
+    KvPair pair[kKvPairs];
+    uint32_t word[kKvPairs][2];
+    __half scale[kKvPairs][2];
 #pragma unroll
-    for (int k = 0; k < kKvRows; ++k) {
+    for (int k = 0; k < kKvPairs; ++k) {
         const int i = first + k * p.stride;
-        row[k].block = -1;
-        row[k].token = -1;
-        if (first < p.stride && i < p.rows) row[k] = kv_row(p, i);
-        word[k] = 0u;
-        scale[k] = __ushort_as_half(0);
-        if (row[k].block >= 0) {
-            const KvRow& r = row[k];
-            const char* const block = (const char*)a.cache.pages + r.block * B::kBytes;
-            word[k] = *(const uint32_t*)(block + (r.is_v ? B::kV : 0) + r.row * B::kRow + ((2 * u + (odd ? 1 : 0)) * B::kGroups + (j & ~1)) * 2);
-            scale[k] = *(const __half*)(block + (r.is_v ? B::kScaleV : B::kScaleK) + r.row * B::kScaleRow + 2 * j);
+        pair[k].block = pair[k].token = -1;
+        if (first < p.stride && i < p.pairs) pair[k] = kv_pair(p, i);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            word[k][v] = 0u;
+            scale[k][v] = __ushort_as_half(0);
+            if (pair[k].block >= 0) {
+                const char* const block = (const char*)a.cache.pages + pair[k].block * B::kBytes;
+                word[k][v] = *(const uint32_t*)(block + v * B::kV + pair[k].row * B::kRow + word_at);
+                scale[k][v] = *(const __half*)(block + (v ? B::kScaleV : B::kScaleK) + pair[k].row * B::kScaleRow + 2 * j);
+            }
         }
     }
 #pragma unroll
-    for (int k = 0; k < kKvRows; ++k) {
-        const KvRow& r = row[k];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? word[k] & 0xffffu : word[k] >> 16, 4);
-        uint32_t v[4];
-        from_e2m1x8(odd ? got | (word[k] & 0xffff0000u) : (word[k] & 0xffffu) | got << 16, v);
-        const float d = __half2float(scale[k]);
-        float x[8];
+    for (int k = 0; k < kKvPairs; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*(const __half2*)&v[i]);
-            x[2 * i] = f.x * d;
-            x[2 * i + 1] = f.y * d;
+        for (int v = 0; v < 2; ++v) {
+            const uint32_t mine = word[k][v];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? mine & 0xffffu : mine >> 16, 4);
+            uint32_t f[4];
+            from_e2m1x8(odd ? got | (mine & 0xffff0000u) : (mine & 0xffffu) | got << 16, f);
+            const float d = __half2float(scale[k][v]);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 y = __half22float2(*(const __half2*)&f[i]);
+                x[2 * i] = y.x * d;
+                x[2 * i + 1] = y.y * d;
+            }
+            if (pair[k].token >= 0)
+                store8(v ? (T*)a.v + pair[k].token * a.v_token_stride + pair[k].head * a.v_head_stride + 8 * m
+                         : (T*)a.k + pair[k].token * a.k_token_stride + pair[k].head * a.k_head_stride + 8 * m, x);
         }
-        if (r.token >= 0)
-            store8(r.is_v ? (T*)a.v + r.token * a.v_token_stride + r.head * a.v_head_stride + 8 * m
-                          : (T*)a.k + r.token * a.k_token_stride + r.head * a.k_head_stride + 8 * m, x);
-    }
 }
 
 static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream, bool append) {
@@ -585,15 +630,15 @@ static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream
         return RRA_ERR_INVALID_ARG;
     if (a->tokens == 0) return RRA_OK;
     if (a->k == nullptr || a->v == nullptr || a->slots == nullptr) return RRA_ERR_INVALID_ARG;
-    if (a->tokens > INT32_MAX / 64 / c.kv_heads) return RRA_ERR_INVALID_ARG;  // rows' threads are counted in 32 bits
+    if (a->tokens > INT32_MAX / 32 / c.kv_heads) return RRA_ERR_INVALID_ARG;  // threads are counted in 32 bits
     KvTokensParams p;
     p.a = *a;
-    p.by_heads = Divisor(2 * c.kv_heads);
+    p.by_heads = Divisor(c.kv_heads);
     p.by_page = Divisor(c.page_tokens / kKvBlockTokens);
-    p.rows = (int)(a->tokens * 2 * c.kv_heads);
-    // few rows: one a thread, so that every SM has some
+    p.pairs = (int)(a->tokens * c.kv_heads);
+    // few pairs: one a thread, so that every SM has some
     const int per_cta = kKvThreads / (c.head_dim / 8);
-    p.stride = p.rows >= 4096 ? (p.rows + kKvRows - 1) / kKvRows : p.rows;
+    p.stride = p.pairs >= 8192 ? (p.pairs + kKvPairs - 1) / kKvPairs : p.pairs;
     const int blocks = (p.stride + per_cta - 1) / per_cta;
     const void* k;
     if (append)
@@ -674,7 +719,9 @@ rra_status_t rra_qk_norm_rope(const rra_qk_norm_rope_args_t* args, rra_stream_t 
     r.lanes_log2 = 0;
     while (1 << r.lanes_log2 < a.head_dim / 16) ++r.lanes_log2;
     const bool many = a.tokens * heads >= 16384;
-    const int each = many ? rra::kRopeHeads : 1, units = (heads + each - 1) / each;
+    const int each = many ? rra::kRopeHeads : 1;
+    r.q_units = (a.q_heads + each - 1) / each;
+    const int units = r.q_units + (a.k_heads + each - 1) / each;
     r.by_units = rra::Divisor(units);
     r.items = (int)(a.tokens * units);
     const int64_t blocks = (((int64_t)r.items << r.lanes_log2) + rra::kRopeThreads - 1) / rra::kRopeThreads;
