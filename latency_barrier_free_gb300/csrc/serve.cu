@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kSlotThreads, 1) slot_map_kernel(const __grid_
 // Eight channels a chunk.  A thread owns the two chunks that rotate with each
 // other (channels j.. and j + rot/2.., or a chunk and its neighbour), so the
 // rotation needs no exchange; head_dim / 16 threads, padded to a power of two,
-// share a row and add its squares by shuffles.  A thread has kRopeHeads heads of
+// share a row and add its squares by shuffles.  A thread has several heads of
 // one token in flight and keeps its cosines and sines for them.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float* x);
@@ -251,12 +251,13 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, flo
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
+// Streaming stores: at sizes that pass L2 a result is not read before it has left (8192 tokens rotated: 57 -> 50 us).
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float* x);
 template <>
 __device__ __forceinline__ void store8<float>(float* p, const float* x) {
-    *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
-    *(float4*)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    __stcs((float4*)p, make_float4(x[0], x[1], x[2], x[3]));
+    __stcs((float4*)(p + 4), make_float4(x[4], x[5], x[6], x[7]));
 }
 template <>
 __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
@@ -267,7 +268,7 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
         const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         w[i] = *(const uint32_t*)&h;
     }
-    *(uint4*)p = v;
+    __stcs((uint4*)p, v);
 }
 
 template <typename T>
@@ -295,8 +296,11 @@ struct Raw8<__nv_bfloat16> {
     }
 };
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;  // heads of a thread, where there are enough
+// 128 bytes of a thread in flight (8192 tokens of 72 heads of 128, bfloat16: 4 heads in blocks of 256 took 66 us, 8 heads
+// 57 us, and in blocks of 128, whose starts hide each other better, 56 us).
+constexpr int kRopeThreads = 128;
+template <typename T>
+constexpr int kRopeHeads = 16 / (int)sizeof(T);  // heads of a thread, where there are enough
 
 struct RopeParams {
     rra_qk_norm_rope_args_t a;
@@ -306,8 +310,10 @@ struct RopeParams {
     int32_t items;     // tokens * units
 };
 
-template <typename T, int kHeads>
-__global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 3 : 4) qk_norm_rope_kernel(const __grid_constant__ RopeParams r) {
+// With weights w, cosine c and sine s of the pair (x, y), and inv = 1 / sqrt(mean of squares + eps), the result is
+// inv * (x (w_x c) - y (w_y s)) and inv * (y (w_y c) + x (w_x s)): the four products are the same for all of a thread's heads.
+template <typename T, int kHeads, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 4 : 8) qk_norm_rope_kernel(const __grid_constant__ RopeParams r) {
     const rra_qk_norm_rope_args_t& a = r.a;
     pdl_release_early();
     const int lanes = 1 << r.lanes_log2;
@@ -321,8 +327,9 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 3 : 4) qk_norm_rope
     const int pairs = a.head_dim / 16, turning = a.rot / 16;
     const bool mine = pair < pairs && at < r.items;
     const int live = mine ? min(kHeads, (is_q ? a.q_heads : a.k_heads) - h0) : 0;  // heads of this thread
+    const bool turns = mine && pair < turning;
     int c0, c1;  // first channels of the two chunks
-    if (!a.interleaved && pair < turning) {
+    if (!kInterleaved && pair < turning) {
         c0 = pair * 8;
         c1 = c0 + a.rot / 2;
     } else {
@@ -333,6 +340,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 3 : 4) qk_norm_rope
     const T* x = (is_q ? (const T*)a.q + t * a.q_token_stride : (const T*)a.k + t * a.k_token_stride) + h0 * head_stride;
     const T* const w = (const T*)(is_q ? a.q_weight : a.k_weight);
     pdl_wait();
+    const int64_t position = turns ? a.positions[t] : 0;
     Raw8<T> raw[kHeads][2];
 #pragma unroll
     for (int e = 0; e < kHeads; ++e)
@@ -341,68 +349,74 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 3 : 4) qk_norm_rope
             raw[e][1].get(x + c1);
             x += head_stride;
         }
-    float cs[8], sn[8], wu[8], wv[8];
-    const bool turns = mine && pair < turning;
+    // channel i of a chunk pairs with channel i of the other, or with its neighbour in its own
+    constexpr auto first = [](int i) { return kInterleaved ? 2 * i : i; };
+    constexpr auto second = [](int i) { return kInterleaved ? 2 * i + 1 : i + 8; };
+    float by[16], cross[16];  // what a channel is multiplied with, and what its partner is
+#pragma unroll
+    for (int i = 0; i < 16; ++i) by[i] = 1.f, cross[i] = 0.f;
+    if (mine && w != nullptr) {
+        load8(w + c0, by);
+        load8(w + c1, by + 8);
+    }
     if (turns) {
-        const int64_t p = a.positions[t];
-        if (p >= 0 && p < a.max_position) {
-            load8(a.cos + p * (a.rot / 2) + pair * 8, cs);
-            load8(a.sin + p * (a.rot / 2) + pair * 8, sn);
+        float cs[8], sn[8];
+        if (position >= 0 && position < a.max_position) {
+            load8(a.cos + position * (a.rot / 2) + pair * 8, cs);
+            load8(a.sin + position * (a.rot / 2) + pair * 8, sn);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fffffff);
         }
-    }
-    if (mine && w != nullptr) {
-        load8(w + c0, wu);
-        load8(w + c1, wv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cross[first(i)] = -by[second(i)] * sn[i];
+            cross[second(i)] = by[first(i)] * sn[i];
+            by[first(i)] *= cs[i];
+            by[second(i)] *= cs[i];
+        }
     }
     const float eps = (float)a.eps, each = 1.f / (float)a.head_dim;
     const int64_t out_stride = is_q ? a.q_out_head_stride : a.k_out_head_stride;
     T* y = (is_q ? (T*)a.q_out + t * a.q_out_token_stride : (T*)a.k_out + t * a.k_out_token_stride) + h0 * out_stride;
 #pragma unroll
     for (int e = 0; e < kHeads; ++e) {
-        float u[8] = {}, v[8] = {};
+        float u[16];
         if (e < live) {
             raw[e][0].to(u);
-            raw[e][1].to(v);
+            raw[e][1].to(u + 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = 0.f;
         }
         float sq = 0.f;  // exchanged by every thread, whether its heads are normed or not
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(u[i], u[i], fmaf(v[i], v[i], sq));
+        for (int i = 0; i < 16; ++i) sq = fmaf(u[i], u[i], sq);
         for (int o = lanes >> 1; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        if (e >= live) continue;
-        if (w != nullptr) {
-            const float inv = rsqrtf(fmaf(sq, each, eps));
+        const float inv = w != nullptr ? rsqrtf(fmaf(sq, each, eps)) : 1.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                u[i] = u[i] * inv * wu[i];
-                v[i] = v[i] * inv * wv[i];
+        for (int i = 0; i < 8; ++i) {
+            const float p = u[first(i)], q = u[second(i)];
+            float to_p = p * by[first(i)], to_q = q * by[second(i)];
+            if (turns) {  // not with zeros: an infinity beside a channel that does not turn is none of its business
+                to_p = fmaf(q, cross[first(i)], to_p);
+                to_q = fmaf(p, cross[second(i)], to_q);
             }
+            u[first(i)] = to_p * inv;
+            u[second(i)] = to_q * inv;
         }
-        if (turns) {
-            if (!a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = u[i], q = v[i];
-                    u[i] = p * cs[i] - q * sn[i];
-                    v[i] = q * cs[i] + p * sn[i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = u[2 * i], q = u[2 * i + 1], z0 = v[2 * i], z1 = v[2 * i + 1];
-                    u[2 * i] = p * cs[i] - q * sn[i];
-                    u[2 * i + 1] = q * cs[i] + p * sn[i];
-                    v[2 * i] = z0 * cs[4 + i] - z1 * sn[4 + i];
-                    v[2 * i + 1] = z1 * cs[4 + i] + z0 * sn[4 + i];
-                }
-            }
+        if (e < live) {
+            store8(y + c0, u);
+            store8(y + c1, u + 8);
+            y += out_stride;
         }
-        store8(y + c0, u);
-        store8(y + c1, v);
-        y += out_stride;
     }
+}
+
+template <typename T>
+static const void* rope_kernel(bool many, bool interleaved) {
+    if (many) return interleaved ? (const void*)qk_norm_rope_kernel<T, kRopeHeads<T>, true> : (const void*)qk_norm_rope_kernel<T, kRopeHeads<T>, false>;
+    return interleaved ? (const void*)qk_norm_rope_kernel<T, 1, true> : (const void*)qk_norm_rope_kernel<T, 1, false>;
 }
 
 // ======================================= the 4-bit cache: write and read ====
@@ -413,10 +427,10 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads > 1 ? 3 : 4) qk_norm_rope
 // thread 4 j + u (group j) swaps one of them with its neighbour in group j ^ 1,
 // after which each holds a whole word and the row's codes leave as one
 // coalesced run.  Bound by the values' traffic as long as the arithmetic (about
-// seven instructions a value) stays under it; a thread has kKvPairs pairs of
-// rows in flight.
-constexpr int kKvThreads = 256;
-constexpr int kKvPairs = 2;
+// seven instructions a value) stays under it; a thread has up to
+// kKvPairs pairs of rows in flight.
+constexpr int kKvThreads = 128;
+constexpr int kKvPairs = 2;  // where there are enough; one otherwise (16 tokens: 3.0 against 3.6 us for both calls)
 
 struct KvTokensParams {
     rra_kv_tokens_args_t a;
@@ -516,7 +530,7 @@ __device__ __forceinline__ KvPair kv_pair(const KvTokensParams& p, int i) {
     return r;
 }
 
-template <typename T, int D>
+template <typename T, int D, int kPairs>
 __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ KvTokensParams p) {
     using B = KvBlock<D>;
     constexpr int kLanes = D / 8;
@@ -525,10 +539,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
     const int m = (int)threadIdx.x % kLanes, j = m >> 2, u = m & 3;
     const int first = ((int)blockIdx.x * kKvThreads + (int)threadIdx.x) / kLanes;
     pdl_wait();
-    KvPair pair[kKvPairs];
-    KvWrite<T> in[kKvPairs][2];
+    KvPair pair[kPairs];
+    KvWrite<T> in[kPairs][2];
 #pragma unroll
-    for (int k = 0; k < kKvPairs; ++k) {
+    for (int k = 0; k < kPairs; ++k) {
         const int i = first + k * p.stride;
         pair[k].block = -1;
         if (first < p.stride && i < p.pairs) pair[k] = kv_pair(p, i);
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
     const bool odd = j & 1;
     const int word_at = ((2 * u + (odd ? 1 : 0)) * B::kGroups + (j & ~1)) * 2;
 #pragma unroll
-    for (int k = 0; k < kKvPairs; ++k) {
+    for (int k = 0; k < kPairs; ++k) {
         char* const block = (char*)a.cache.pages + pair[k].block * B::kBytes;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
@@ -567,7 +581,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int kPairs>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvTokensParams p) {
     using B = KvBlock<D>;
     constexpr int kLanes = D / 8;
@@ -578,11 +592,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
     const bool odd = j & 1;
     const int word_at = ((2 * u + (odd ? 1 : 0)) * B::kGroups + (j & ~1)) * 2;
     pdl_wait();
-    KvPair pair[kKvPairs];
-    uint32_t word[kKvPairs][2];
-    __half scale[kKvPairs][2];
+    KvPair pair[kPairs];
+    uint32_t word[kPairs][2];
+    __half scale[kPairs][2];
 #pragma unroll
-    for (int k = 0; k < kKvPairs; ++k) {
+    for (int k = 0; k < kPairs; ++k) {
         const int i = first + k * p.stride;
         pair[k].block = pair[k].token = -1;
         if (first < p.stride && i < p.pairs) pair[k] = kv_pair(p, i);
@@ -598,7 +612,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
         }
     }
 #pragma unroll
-    for (int k = 0; k < kKvPairs; ++k)
+    for (int k = 0; k < kPairs; ++k)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             const uint32_t mine = word[k][v];
@@ -619,6 +633,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
         }
 }
 
+template <typename T, int D>
+static const void* kv_tokens_kernel(bool append, bool many) {
+    if (append) return many ? (const void*)kv_append_kernel<T, D, kKvPairs> : (const void*)kv_append_kernel<T, D, 1>;
+    return many ? (const void*)kv_read_kernel<T, D, kKvPairs> : (const void*)kv_read_kernel<T, D, 1>;
+}
+
 static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream, bool append) {
     if (a == nullptr || !kv_cache_ok(a->cache) || a->tokens < 0 || a->reserved != 0) return RRA_ERR_INVALID_ARG;
     if (a->dtype != RRA_FP32 && a->dtype != RRA_BF16) return RRA_ERR_INVALID_ARG;
@@ -636,19 +656,13 @@ static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream
     p.by_heads = Divisor(c.kv_heads);
     p.by_page = Divisor(c.page_tokens / kKvBlockTokens);
     p.pairs = (int)(a->tokens * c.kv_heads);
-    // few pairs: one a thread, so that every SM has some
     const int per_cta = kKvThreads / (c.head_dim / 8);
-    p.stride = p.pairs >= 8192 ? (p.pairs + kKvPairs - 1) / kKvPairs : p.pairs;
+    const bool many = p.pairs >= 8192;
+    p.stride = many ? (p.pairs + kKvPairs - 1) / kKvPairs : p.pairs;
     const int blocks = (p.stride + per_cta - 1) / per_cta;
-    const void* k;
-    if (append)
-        k = elem == 4 ? (c.head_dim == 64 ? (const void*)kv_append_kernel<float, 64> : (const void*)kv_append_kernel<float, 128>)
-                      : (c.head_dim == 64 ? (const void*)kv_append_kernel<__nv_bfloat16, 64>
-                                          : (const void*)kv_append_kernel<__nv_bfloat16, 128>);
-    else
-        k = elem == 4 ? (c.head_dim == 64 ? (const void*)kv_read_kernel<float, 64> : (const void*)kv_read_kernel<float, 128>)
-                      : (c.head_dim == 64 ? (const void*)kv_read_kernel<__nv_bfloat16, 64>
-                                          : (const void*)kv_read_kernel<__nv_bfloat16, 128>);
+    const void* k = elem == 4 ? (c.head_dim == 64 ? kv_tokens_kernel<float, 64>(append, many) : kv_tokens_kernel<float, 128>(append, many))
+                              : (c.head_dim == 64 ? kv_tokens_kernel<__nv_bfloat16, 64>(append, many)
+                                                  : kv_tokens_kernel<__nv_bfloat16, 128>(append, many));
     void* args[] = {(void*)&p};
     return serve_launch(k, dim3((unsigned)blocks), kKvThreads, 0, 1, stream, args);
 }
@@ -719,17 +733,14 @@ rra_status_t rra_qk_norm_rope(const rra_qk_norm_rope_args_t* args, rra_stream_t 
     r.lanes_log2 = 0;
     while (1 << r.lanes_log2 < a.head_dim / 16) ++r.lanes_log2;
     const bool many = a.tokens * heads >= 16384;
-    const int each = many ? rra::kRopeHeads : 1;
+    const int each = !many ? 1 : elem == 4 ? rra::kRopeHeads<float> : rra::kRopeHeads<__nv_bfloat16>;
     r.q_units = (a.q_heads + each - 1) / each;
     const int units = r.q_units + (a.k_heads + each - 1) / each;
     r.by_units = rra::Divisor(units);
     r.items = (int)(a.tokens * units);
     const int64_t blocks = (((int64_t)r.items << r.lanes_log2) + rra::kRopeThreads - 1) / rra::kRopeThreads;
     void* kargs[] = {(void*)&r};
-    const void* k = elem == 4 ? (many ? (const void*)rra::qk_norm_rope_kernel<float, rra::kRopeHeads>
-                                      : (const void*)rra::qk_norm_rope_kernel<float, 1>)
-                              : (many ? (const void*)rra::qk_norm_rope_kernel<__nv_bfloat16, rra::kRopeHeads>
-                                      : (const void*)rra::qk_norm_rope_kernel<__nv_bfloat16, 1>);
+    const void* k = elem == 4 ? rra::rope_kernel<float>(many, a.interleaved != 0) : rra::rope_kernel<__nv_bfloat16>(many, a.interleaved != 0);
     return rra::serve_launch(k, dim3((unsigned)blocks), rra::kRopeThreads, 0, 1, stream, kargs);
 }
 
