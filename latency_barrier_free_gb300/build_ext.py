@@ -19,8 +19,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librra.so")
 
 SOURCES = ["kernels.cu", "cluster.cu", "coll.cu", "fused.cu", "rra_api.cu", "probes.cu", "rra_static.cu", "serve.cu",
-           "serve_attn.cu"]
-HEADERS = ["prims.cuh", "cluster_prims.cuh", "rra_internal.h", "placement.h", "kernel_attrs.h", "serve_common.cuh"]
+           "serve_attn.cu", "serve_prefill.cu"]
+HEADERS = ["prims.cuh", "cluster_prims.cuh", "rra_internal.h", "placement.h", "kernel_attrs.h", "serve_common.cuh",
+           "serve_attn.cuh"]
 PUBLIC_HEADERS = ["rra.h", "rra_probe.h", "rra_static.h", "rra_device.cuh", "rra_serve.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

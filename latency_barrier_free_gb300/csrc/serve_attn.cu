@@ -14,42 +14,17 @@
 // it finds whole it writes out itself.  Of its first and last segment it may
 // have a piece only; those are joined once, at the end of the CTA, and across
 // CTAs by whichever finishes last, in the order of the runs.
-#include <float.h>
-#include <math.h>
-
 #include <algorithm>
 
-#include "cluster_prims.cuh"
-#include "kernel_attrs.h"
-#include "serve_common.cuh"
+#include "serve_attn.cuh"
 
 namespace rra {
 
 constexpr int kAttnTile = 32;      // keys of one step of a warp
-constexpr int kAttnMaxCtas = 512;  // CTAs a workspace has room for
 constexpr int kAttnMinRun = 2;     // tiles a warp takes at least
 constexpr int kAttnSegmentCost = 2;  // what starting and ending a segment costs, in tiles
-constexpr uint32_t kAttnSpins = 1u << 22;  // tries of a wait before it gives up
 constexpr float kAttnSlack = 4.f;  // log2 of how far weights may pass 1 before the maximum moves
 
-// Start of the workspace: status word, then a counter for each CTA, then two
-// partial results for each CTA: maximum and sum of every row, then the rows.
-struct AttnWorkspace {
-    uint32_t status;
-    uint32_t pad[63];
-    uint32_t arrived[kAttnMaxCtas];
-    uint32_t pad_end[1024 - 64 - kAttnMaxCtas];
-};
-static_assert(sizeof(AttnWorkspace) == 4096, "the part of the workspace that starts as zero");
-constexpr int kAttnMaxRows = 16;
-
-struct AttnParams {
-    rra_kv_attention_args_t a;
-    float scale_log2;
-    int32_t group;   // query heads of a KV head
-    int32_t room;    // keys that a row of the table has pages for
-    int32_t window;  // a.window, at most 2^30
-};
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -70,15 +45,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *(const uint32_t*)&h;
 }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -111,12 +77,11 @@ struct AttnRequest {
 };
 template <int kRows>
 __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int b) {
-    const rra_kv_attention_args_t& a = p.a;
+    const AttnLengths n = attn_lengths(p, b);
     AttnRequest r;
-    const int most_q = (int)a.tokens;
-    r.q0 = min(max(a.cu_q[b], 0), most_q);
-    r.qn = max(0, min(a.cu_q[b + 1], most_q) - r.q0);
-    r.kv = min(max(a.kv_len[b], 0), p.room);
+    r.q0 = n.q0;
+    r.qn = n.qn;
+    r.kv = n.kv;
     r.first_tile = (p.window > 0 ? max(0, r.kv - r.qn - p.window + 1) : 0) / kAttnTile;
     r.tiles = max(1, (r.kv + kAttnTile - 1) / kAttnTile - r.first_tile);
     r.chunks = (r.qn * p.group + kRows - 1) / kRows;
@@ -171,21 +136,6 @@ struct AttnShape {
     static_assert(kStages * kStage >= kPartial * 4, "a piece fits the ring");
     static size_t smem(int requests) { return (size_t)kFixed + 8 * ((size_t)requests + 1); }
 };
-
-// Where row's channels go, and its sum's reciprocal; writes its lse (maximum top in units of log2).
-__device__ __forceinline__ __nv_bfloat16* attn_row(const AttnParams& p, int q0, int h, int row, float top, float sum,
-                                                   bool with_lse, float& inv) {
-    const rra_kv_attention_args_t& a = p.a;
-    const int i = row / p.group, head = h * p.group + row - i * p.group;
-    const int64_t token = q0 + i;
-    inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: 0
-    if (with_lse && a.lse != nullptr) a.lse[token * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
-    return (__nv_bfloat16*)a.out + token * a.out_token_stride + head * a.out_head_stride;
-}
-__device__ __forceinline__ void attn_store(__nv_bfloat16* to, float4 o, float inv) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    *(uint2*)to = make_uint2(*(const uint32_t*)&x, *(const uint32_t*)&y);
-}
 
 // Adds a piece's row (maximum and sum st, four channels v) to sums whose maximum is top.
 __device__ __forceinline__ void attn_add(float top, float& sum, float4& o, float2 st, float4 v) {
@@ -376,6 +326,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) copy_next();
 
+        auto drain = [&]() {  // waits for every copy, but no longer than a wait may take
+            const uint64_t start = globaltimer_ns();
+#pragma unroll 1
+            for (int i = 0; i < kStages; ++i)
+                while (!mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u))
+                    if (globaltimer_ns() - start > kAttnWaitNs) break;
+        };
         int take = 0;
         uint32_t phase = 0;
         bool dead = false;  // a wait ran out: no more copies, no more sums
@@ -403,12 +360,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 : 0;
-                e = min(max(e, -120), 120);
-                float f = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23);
-                float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                if (p.scale_log2 < 0.f) down = -down;
-                if (f == 0.f) f = 1.f, down = 0.f;  // every score is 0
+                float f, down;
+                attn_row_scale(p, most, down, f);
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -466,16 +419,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
 #pragma unroll 1
             for (int tl = tile0; tl < tile1; ++tl) {
                 const uint32_t bar = bars + 8 * take, tile = ring + take * Sh::kStage;
-                if (!dead) {
-                    uint32_t tries = 0;
-                    while (!mbar_try_wait(bar, (phase >> take) & 1u))
-                        if (++tries > kAttnSpins) {
-                            dead = true;
-                            if (lane == 0) atomicCAS(&ws->status, 0u, (uint32_t)RRA_ERR_TIMEOUT);
-                            break;
-                        }
-                    dead = __any_sync(0xffffffffu, dead);
-                }
+                if (!dead)
+                    dead = __any_sync(0xffffffffu, !mbar_try_wait(bar, phase >> take & 1u) && !attn_wait_slow(bar, phase >> take & 1u, ws));
                 phase ^= 1u << take;
                 const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
 #pragma unroll 1
@@ -619,9 +564,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             const int which = starts ? 1 : 0;
             float* const piece = piece_at(warp, which);
             if (!(starts && ends)) {
-                if (which == 1 && dead)  // the ring must be quiet before it is written
-                    for (int i = 0; i < kStages; ++i)
-                        for (uint32_t tries = 0; tries < kAttnSpins && !mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u); ++tries) {}
+                if (which == 1 && dead) drain();  // the ring must be quiet before it is written
                 __syncwarp();
                 if (lane == 0)
                     pieces[2 * warp + which] =
@@ -656,10 +599,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             attn_next<kRows>(p, seg);
             load_queries();
         }
-        // Copies in flight at this point: none, or those that a wait gave up on.
-        if (dead)
-            for (int i = 0; i < kStages; ++i)
-                for (uint32_t tries = 0; tries < kAttnSpins && !mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u); ++tries) {}
+        if (dead) drain();  // copies in flight at this point: none, or those that a wait gave up on
     }
     __syncthreads();
 
@@ -802,14 +742,16 @@ extern "C" {
 
 size_t rra_kv_attention_workspace_bytes(int head_dim) {
     if (head_dim != 64 && head_dim != 128) return 0;
-    return sizeof(rra::AttnWorkspace) +
-           (size_t)rra::kAttnMaxCtas * 2 * rra::kAttnMaxRows * ((size_t)head_dim + 2) * sizeof(float);
+    const size_t decode = (size_t)rra::kAttnMaxCtas * 2 * rra::kAttnMaxRows * ((size_t)head_dim + 2) * sizeof(float);
+    return sizeof(rra::AttnWorkspace) + std::max(decode, rra::prefill_partial_bytes(head_dim));
 }
 
 rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
     if (name == nullptr || !rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
     const int64_t rows = (int64_t)std::max(args->max_q, 1) * (args->q_heads / args->cache.kv_heads);
-    *name = rows <= 8 ? "kv_attention_kernel<8 rows>" : "kv_attention_kernel<16 rows>";
+    *name = rows <= 8    ? "kv_attention_kernel<8 rows>"
+            : rows <= 32 ? "kv_attention_kernel<16 rows>"
+                         : "kv_attention_prompt_kernel";
     return RRA_OK;
 }
 
@@ -829,6 +771,7 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     p.room = args->table_pages * args->cache.page_tokens;
     p.window = std::min(args->window, 1 << 30);
     const int64_t rows = (int64_t)std::max(args->max_q, 1) * p.group;
+    if (rows > 32) return rra::launch_prefill(p, sms, stream);
     const int ctas = std::min(sms, rra::kAttnMaxCtas);
     if (args->cache.head_dim == 128)
         return rows <= 8 ? rra::attn_launch<128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 2>(p, ctas, stream);

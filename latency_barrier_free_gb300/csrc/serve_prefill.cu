@@ -1,0 +1,774 @@
+// serve_prefill.cu -- attention over the 4-bit cache for prompts: many queries
+// of a request at once (rra_serve.h), on the tensor cores' own memory.
+//
+// A row is one query of one head.  A CTA takes a segment: TILES x 128 rows of
+// one request and KV head, and walks the keys that any of them sees, 128 at a
+// time.  Four warps unpack a tile of the cache: V as binary16 (code * scale,
+// rounded to 11 bits), K as two binary16 numbers whose sum is code * scale
+// exactly (codes of 3 * 2^i times an 11-bit scale have 13 bits), so that scores
+// keep the accuracy of their binary32 accumulation; the second costs half as
+// much again in tensor work.  One thread issues
+//     S_i = Q_i K_hi^T + Q_i K_lo^T,   O_i += P_i V      (tcgen05.mma, sums in TMEM)
+// and a warpgroup for each tile i turns S_i into weights P_i, in place: a thread
+// has a row, so maxima and sums need no exchange.  While one tile's scores are
+// exponentiated the other's products run.
+//
+// The weights are taken against the maximum so far, before this tile's is known:
+// where it does not pass the old one by more than 2^kSlack (nearly always, after
+// a row's first keys), one pass over the scores is enough, and O is not touched.
+//
+// Work is cut into equal runs of key tiles, one per CTA, as in serve_attn.cu;
+// what a run has of a segment it shares goes to the workspace, and the last CTA
+// to arrive adds the parts in order.
+#include <algorithm>
+#include <type_traits>
+
+#include "serve_attn.cuh"
+
+namespace rra {
+
+constexpr int kPromptKeys = 128;       // keys of a tile
+constexpr int kPromptRows = 128;       // rows of a tile: the TMEM lanes
+constexpr int kPromptMinRun = 4;       // key tiles a CTA takes at least
+constexpr int kPromptSegmentCost = 2;  // what starting and ending a segment costs, in key tiles
+constexpr int kPromptMaxCtas = 192;    // CTAs that the workspace has room for
+constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 before the maximum moves
+static_assert(kPromptMaxCtas * 2 <= kAttnMaxCtas, "a counter for each tile of a CTA's last segment");
+
+template <int D, int TILES>
+struct PromptShape {
+    using B = KvBlock<D>;
+    static constexpr int kRows = TILES * kPromptRows;
+    static constexpr int kPanel = 128 * 128;            // 128 rows of 64 binary16, swizzled in 128 bytes
+    static constexpr int kTile = D / 64 * kPanel;       // 128 rows of D binary16
+    static constexpr int kK = TILES * kTile;            // after the queries: K, high and low parts
+    static constexpr int kV = kK + 2 * kTile;           // two stages of V
+    static constexpr int kSums = kV + 2 * kTile;        // running sums of the requests' chunks
+    static constexpr int kSoftmaxWarps = 4 * TILES;
+    static constexpr int kWarps = kSoftmaxWarps + 4 + 1;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
+    static constexpr int kPart = kPromptRows * (D + 2);      // floats of a part: rows in columns of 4 channels, statistics
+    static size_t smem(int requests) { return 1024 + kSums + 4 * ((size_t)requests + 1); }
+};
+
+// ------------------------------------------------------------- tcgen05 ----
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t panel_stride) {
+    // start, leading dimension (panels of 64, for the operand whose rows are keys), stride of 8 rows, 128-byte swizzle
+    return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)((panel_stride >> 4) & 0x3fffu) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// binary32 sums of binary16 products, 128 rows, n columns; b_keys: B's rows are the summed index
+constexpr uint32_t mma_desc(int n, bool b_keys) {
+    return 1u << 4 | (b_keys ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 : : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add ? 1 : 0) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 : : "r"(d), "r"(a), "l"(b), "r"(desc), "r"(add ? 1 : 0) : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" : : "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        :
+        : "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+          "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+          "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" : : "r"(bar) : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" : : "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// a * b - c, rounded once: with c the rounded product, what its rounding lost
+__device__ __forceinline__ uint32_t half2_rest(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c ^ 0x80008000u));
+    return r;
+}
+
+// --------------------------------------------------------- work as a row ----
+// Chunk c of request b: its rows' key tiles.
+struct PromptItem {
+    int32_t first_tile, tiles;
+};
+template <int kRows>
+__device__ __forceinline__ PromptItem prompt_item(const AttnParams& p, const AttnLengths& n, int c) {
+    const int rows = n.qn * p.group, last = min(rows, (c + 1) * kRows) - 1;
+    const int end = p.a.causal ? max(0, n.kv - n.qn + last / p.group + 1) : n.kv;
+    const int first = p.window > 0 ? max(0, n.kv - n.qn + c * kRows / p.group - p.window + 1) : 0;
+    PromptItem t;
+    t.first_tile = first / kPromptKeys;
+    t.tiles = max(1, (end + kPromptKeys - 1) / kPromptKeys - t.first_tile);
+    return t;
+}
+template <int kRows>
+__device__ __forceinline__ int prompt_chunks(const AttnParams& p, const AttnLengths& n) {
+    return (n.qn * p.group + kRows - 1) / kRows;
+}
+
+// A segment: chunk c of request b, KV head h, at begin..end of the row of all segments: first its cost, then its tiles.
+struct PromptSegment {
+    AttnLengths n;
+    int32_t b, c, h, chunks, first_tile;
+    int64_t begin, end;
+};
+template <int kRows>
+__device__ __noinline__ void prompt_load(const AttnParams& p, PromptSegment& s) {
+    s.n = attn_lengths(p, s.b);
+    s.chunks = prompt_chunks<kRows>(p, s.n);
+    const PromptItem t = prompt_item<kRows>(p, s.n, s.c);
+    s.first_tile = t.first_tile;
+    s.end = s.begin + t.tiles + kPromptSegmentCost;
+}
+template <int kRows>
+__device__ __noinline__ void prompt_next(const AttnParams& p, PromptSegment& s) {
+    s.begin = s.end;
+    if (++s.c >= s.chunks) {
+        s.c = 0;
+        do {
+            if (++s.b == p.a.requests) s.b = 0, ++s.h;
+            s.n = attn_lengths(p, s.b);
+        } while (s.n.qn == 0 && s.h < p.a.cache.kv_heads);  // some request has queries: there is a segment
+    }
+    prompt_load<kRows>(p, s);
+}
+
+// Exclusive sum over the block, and the total.
+template <int kWarps>
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t& total, int64_t* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += part[w];
+        total += part[w];
+    }
+    return before + inc - v;
+}
+
+template <int D, int TILES>
+__global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attention_prompt_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = PromptShape<D, TILES>;
+    using B = KvBlock<D>;
+    constexpr int J = B::kGroups;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ __align__(8) uint64_t bar_mem[3 * TILES + 2 * TILES + 2 + 4 + 4 + 1];
+    __shared__ int64_t part[Sh::kWarps];
+    __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile uint32_t arrived[TILES];
+    __shared__ PromptSegment start;
+    const rra_kv_attention_args_t& a = p.a;
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    int32_t* const chunk_sums = (int32_t*)(raw_smem + (smem - smem_u32(raw_smem)) + Sh::kSums);
+    AttnWorkspace* const ws = (AttnWorkspace*)a.workspace;
+    float* const parts = (float*)(ws + 1);
+
+    const uint32_t bars = smem_u32(bar_mem);
+    const uint32_t q_full = bars, s_full = q_full + 8 * TILES, p_full = s_full + 8 * TILES, o_full = p_full + 8 * TILES,
+                   joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 8, v_full = k_empty + 8,
+                   v_empty = v_full + 16, seen_full = v_empty + 16, drained = seen_full + 32;
+    pdl_release_early();
+    if (tid == 0) {
+        for (int i = 0; i < TILES; ++i) {
+            mbar_init(q_full + 8 * i, kPromptRows);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, kPromptRows);
+            mbar_init(o_full + 8 * i, 1);
+            mbar_init(joined + 8 * i, kPromptRows);
+        }
+        mbar_init(k_full, 128);
+        mbar_init(k_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(v_full + 8 * i, 128);
+            mbar_init(v_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(seen_full + 8 * i, 4);
+        mbar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    pdl_wait();
+
+    // ---- this CTA's run: chunks of the requests, then the chunks' tiles, the same for every head ----
+    int64_t total_chunks = 0;
+    for (int b0 = 0; b0 < a.requests; b0 += Sh::kThreads) {
+        const int b = b0 + tid;
+        int64_t all;
+        const int64_t at = block_sum<Sh::kWarps>(b < a.requests ? prompt_chunks<Sh::kRows>(p, attn_lengths(p, b)) : 0, all, part);
+        if (b < a.requests) chunk_sums[b] = (int32_t)(total_chunks + at);
+        total_chunks += all;
+    }
+    if (tid == 0) chunk_sums[a.requests] = (int32_t)total_chunks;
+    __syncthreads();
+    auto owner = [&](int n, int& b, int& c) {
+        int low = 0, high = a.requests;
+        while (high - low > 1) {
+            const int mid = (low + high) >> 1;
+            if (chunk_sums[mid] <= n) low = mid;
+            else high = mid;
+        }
+        b = low;
+        c = n - chunk_sums[low];
+    };
+    auto cost_of = [&](int n) {
+        int b, c;
+        owner(n, b, c);
+        return prompt_item<Sh::kRows>(p, attn_lengths(p, b), c).tiles + kPromptSegmentCost;
+    };
+    int64_t per_head = 0;
+    for (int n0 = 0; n0 < total_chunks; n0 += Sh::kThreads) {
+        int64_t all;
+        block_sum<Sh::kWarps>(n0 + tid < total_chunks ? cost_of(n0 + tid) : 0, all, part);
+        per_head += all;
+    }
+    const int64_t total = per_head * a.cache.kv_heads;
+    int64_t run = (total + gridDim.x - 1) / gridDim.x;
+    run = run < kPromptMinRun + kPromptSegmentCost ? kPromptMinRun + kPromptSegmentCost : run;
+    const int64_t r0 = (int64_t)blockIdx.x * run, r1 = r0 + run < total ? r0 + run : total;
+    if (r0 >= r1) return;
+    {
+        const int64_t h = r0 / per_head, w = r0 - h * per_head;
+        int64_t before = 0;
+        for (int n0 = 0; n0 < total_chunks && before <= w; n0 += Sh::kThreads) {
+            int64_t all;
+            const int n = n0 + tid, cost = n < total_chunks ? cost_of(n) : 0;
+            const int64_t at = before + block_sum<Sh::kWarps>(cost, all, part);
+            if (at <= w && w < at + cost) {
+                owner(n, start.b, start.c);
+                start.h = (int)h;
+                start.begin = h * per_head + at;
+            }
+            before += all;
+        }
+    }
+    if (warp == Sh::kWarps - 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = tmem_base;
+    PromptSegment seg = start;
+    prompt_load<Sh::kRows>(p, seg);
+    auto first_of = [&](const PromptSegment& s) {
+        const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - kPromptSegmentCost;
+        return (int)(from > 0 ? from : 0);
+    };
+    auto end_of = [&](const PromptSegment& s) {
+        const int64_t to = (s.end < r1 ? s.end : r1) - s.begin - kPromptSegmentCost;
+        return (int)(to > 0 ? to : 0);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u) || attn_wait_slow(bar, parity & 1u, ws));
+    };
+
+    uint32_t n = 0;   // key tiles of this run so far
+    uint32_t sn = 0;  // segments so far that had tiles
+    bool ok = true;
+    if (warp < Sh::kSoftmaxWarps) {
+        // =============================== softmax: a thread has a row ====
+        const int i = warp >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
+        const uint32_t s_at = lanes + 128 * i, o_at = lanes + 128 * (TILES + i);
+        uint32_t joins = 0;
+        while (ok) {
+            const int t0 = first_of(seg), t1 = end_of(seg);
+            const int all_rows = seg.n.qn * p.group, r = seg.c * Sh::kRows + i * kPromptRows + row;
+            const bool live = r < all_rows;
+            float m = -FLT_MAX, limit = -FLT_MAX, l = 0.f, factor = 1.f;
+            if (t0 < t1) {
+                // ---- the row's query, scaled, into shared memory; the keys that it sees ----
+                int lo = 0, hi = 0;
+                {
+                    uint4 x[D / 8];
+                    const int tok = live ? r / p.group : 0;
+                    if (live) {
+                        const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (seg.n.q0 + tok) * a.q_token_stride +
+                                                   (seg.h * p.group + r - tok * p.group) * a.q_head_stride;
+#pragma unroll
+                        for (int k = 0; k < D / 8; ++k) x[k] = *((const uint4*)src + k);
+                        const int pos = seg.n.kv - seg.n.qn + tok;
+                        hi = a.causal ? max(0, min(seg.n.kv, pos + 1)) : seg.n.kv;
+                        lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 8; ++k) x[k] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    float most = 0.f, down;
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) {
+                        const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
+                    }
+                    attn_row_scale(p, most, down, factor);
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) {
+                        const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            h[e] = pack_half2(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+                        sts_v4(smem + i * Sh::kTile + (k >> 3) * Sh::kPanel + row * 128 + (((k & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(q_full + 8 * i);
+
+                const uint64_t factor2 = pair2(factor, factor);
+                for (int tl = t0; tl < t1 && ok; ++tl, ++n) {
+                    ok = wait(seen_full + 8 * (n & 3), n >> 2) && wait(s_full + 8 * i, n);
+                    if (!ok) break;
+                    tc_after_sync();
+                    const int key0 = (seg.first_tile + tl) * kPromptKeys;
+                    const volatile uint32_t* const words = seen_words[n & 3];
+                    const uint4 seen = make_uint4(words[0], words[1], words[2], words[3]);
+                    const bool whole = __all_sync(0xffffffffu, key0 >= lo && key0 + kPromptKeys <= hi) &&
+                                       (seen.x & seen.y & seen.z & seen.w) == 0xffffffffu;
+                    uint32_t w[64];   // the weights, two a word
+                    float top, sum;
+                    auto weigh = [&]() {
+                        top = -FLT_MAX;
+                        const uint64_t off = pair2(-m, -m);
+                        uint64_t sum2 = pair2(0.f, 0.f);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t v[32];
+                            tc_ld32(s_at + 32 * q, v);
+                            tc_wait_ld();
+                            if (!whole) {
+                                const uint32_t here = q == 0 ? seen.x : q == 1 ? seen.y : q == 2 ? seen.z : seen.w;
+                                // keys lo..hi of these 32, as bits
+                                const int from = min(max(lo - key0 - 32 * q, 0), 32), to = min(max(hi - key0 - 32 * q, 0), 32);
+                                const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
+                                const uint32_t mask = here & below & (from == 32 ? 0u : 0xffffffffu << from);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!(mask >> k & 1u)) v[k] = __float_as_uint(-INFINITY);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
+                                top = fmaxf(top, fmaxf(x, y));
+                                float e0, e1;
+                                split2(mul2(add2(pair2(x, y), off), factor2), e0, e1);
+                                e0 = exp2_fast(e0);
+                                e1 = exp2_fast(e1);
+                                sum2 = add2(sum2, pair2(e0, e1));
+                                w[16 * q + k / 2] = pack_half2(e0, e1);
+                            }
+                        }
+                        float a0, a1;
+                        split2(sum2, a0, a1);
+                        sum = a0 + a1;
+                    };
+                    weigh();
+                    if (__any_sync(0xffffffffu, top > limit)) {
+                        // a maximum moved: scale what was summed, weigh again
+                        const float now = top > limit ? top : m;
+                        const float by = exp2_fast((m - now) * factor);
+                        m = now;
+                        limit = now + __fdividef(kPromptSlack, factor);
+                        l *= by;
+                        if (tl > t0) {
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t v[32];
+                                tc_ld32(o_at + 32 * q, v);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * by);
+                                tc_st32(o_at + 32 * q, v);
+                            }
+                        }
+                        weigh();
+                    }
+                    l += sum;
+                    tc_st32(s_at, w);
+                    tc_st32(s_at + 32, w + 32);
+                    tc_wait_st();
+                    tc_before_sync();
+                    mbar_arrive(p_full + 8 * i);
+                }
+                if (ok) ok = wait(o_full + 8 * i, sn);
+                if (!ok) break;
+                tc_after_sync();
+                ++sn;
+            }
+            // ---- the segment's end in this run ----
+            const bool starts = seg.begin >= r0, ends = seg.end <= r1;
+            const float top = m * factor;
+            if (starts && ends) {
+                float inv = 0.f;
+                __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, top, l, true, inv) : nullptr;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t v[32];
+                    tc_ld32(o_at + 32 * q, v);
+                    tc_wait_ld();
+                    if (live)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint4 u;
+                            uint32_t* const h = (uint32_t*)&u;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(v[k + 2 * e]) * inv,
+                                                                               __uint_as_float(v[k + 2 * e + 1]) * inv);
+                                h[e] = *(const uint32_t*)&z;
+                            }
+                            *(uint4*)(to + 32 * q + k) = u;
+                        }
+                }
+            } else {
+                float4* const mine = (float4*)(parts + (((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * TILES + i) * Sh::kPart);
+                if (t0 < t1) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t v[32];
+                        tc_ld32(o_at + 32 * q, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mine[(8 * q + k) * kPromptRows + row] =
+                                make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
+                                            __uint_as_float(v[4 * k + 3]));
+                    }
+                }
+                ((float2*)(mine + D / 4 * kPromptRows))[row] = make_float2(top, l);
+                // ---- the last CTA to arrive adds the parts in order ----
+                const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
+                __threadfence();
+                mbar_arrive(joined + 8 * i);
+                ok = wait(joined + 8 * i, joins++);
+                if (ok && row == 0) arrived[i] = atomicAdd(&ws->arrived[i0 * TILES + i], 1u);
+                mbar_arrive(joined + 8 * i);
+                ok = ok && wait(joined + 8 * i, joins);
+                ++joins;
+                if (!ok) break;
+                if (arrived[i] == (uint32_t)(i1 - i0)) {
+                    __threadfence();
+                    auto part_of = [&](int x) {
+                        return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPart);
+                    };
+                    float best = -FLT_MAX, sum = 0.f;
+                    for (int x = i0; x <= i1; ++x) best = fmaxf(best, __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row).x);
+                    for (int x = i0; x <= i1; ++x) {
+                        const float2 st = __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row);
+                        sum += st.y * exp2_fast(st.x - best);
+                    }
+                    float inv = 0.f;
+                    __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, best, sum, true, inv) : nullptr;
+#pragma unroll 1
+                    for (int d = 0; d < D / 4; d += 8) {
+                        float4 o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                        for (int x = i0; x <= i1; ++x) {
+                            const float4* const src = part_of(x);
+                            const float2 st = __ldcg((const float2*)(src + D / 4 * kPromptRows) + row);
+                            if (st.y == 0.f) continue;  // nothing seen there; its rows may not have been written
+                            const float by = exp2_fast(st.x - best);
+                            float4 v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (d + k) * kPromptRows + row);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                o[k].x = fmaf(v[k].x, by, o[k].x);
+                                o[k].y = fmaf(v[k].y, by, o[k].y);
+                                o[k].z = fmaf(v[k].z, by, o[k].z);
+                                o[k].w = fmaf(v[k].w, by, o[k].w);
+                            }
+                        }
+                        if (live)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) attn_store(to + 4 * (d + k), o[k], inv);
+                    }
+                    if (row == 0) ws->arrived[i0 * TILES + i] = 0u;
+                }
+            }
+            if (seg.end >= r1) break;
+            tc_before_sync();
+            prompt_next<Sh::kRows>(p, seg);
+        }
+    } else if (warp < Sh::kSoftmaxWarps + 4) {
+        // =============================== unpacking: a thread has a key ====
+        const int key_in = tid - 32 * Sh::kSoftmaxWarps;
+        const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
+        constexpr int kLoads = D / 32;  // 16-byte loads of a row of codes
+        struct Row {
+            uint4 k[kLoads], v[kLoads];
+            uint32_t ks[J / 2], vs[J / 2];
+            bool there;
+        };
+        // the segment and tile after the one in hand: what is loaded next
+        PromptSegment ahead = seg;
+        int next = first_of(ahead), next_end = end_of(ahead);
+        bool more = true;
+        int page = -1;  // of this thread's key in that tile
+        int key = 0;
+        auto settle = [&]() {  // moves to a segment that has a tile left in this run
+            while (more && next >= next_end) {
+                if (ahead.end >= r1) {
+                    more = false;
+                    break;
+                }
+                prompt_next<Sh::kRows>(p, ahead);
+                next = first_of(ahead);
+                next_end = end_of(ahead);
+            }
+        };
+        auto find_page = [&]() {
+            settle();
+            page = -1;
+            if (!more) return;
+            key = (ahead.first_tile + next) * kPromptKeys + key_in;
+            if (key < ahead.n.kv) page = a.block_table[ahead.b * a.table_stride + key / ps];
+        };
+        auto load_row = [&](Row& x) {  // the row of the tile that find_page() looked up, then the page of the one after
+            x.there = page >= 0 && page < a.cache.num_pages;
+            if (x.there) {
+                const int in = key - key / ps * ps;
+                const char* const block = (const char*)a.cache.pages +
+                                          (((int64_t)page * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
+                const int rr = in % kKvBlockTokens;
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    x.k[k] = *((const uint4*)(block + rr * B::kRow) + k);
+                    x.v[k] = *((const uint4*)(block + B::kV + rr * B::kRow) + k);
+                }
+#pragma unroll
+                for (int k = 0; k < J / 2; ++k) {
+                    x.ks[k] = *((const uint32_t*)(block + B::kScaleK + rr * B::kScaleRow) + k);
+                    x.vs[k] = *((const uint32_t*)(block + B::kScaleV + rr * B::kScaleRow) + k);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) x.k[k] = x.v[k] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int k = 0; k < J / 2; ++k) x.ks[k] = x.vs[k] = 0u;
+            }
+            if (more) ++next;
+            find_page();
+        };
+        // A row's codes as binary16 into its place of a swizzled tile; with kRest the part that rounding lost into `rest`.
+        const uint32_t row_at = key_in * 128;
+        auto unpack = [&](const uint4* codes, const uint32_t* scales, uint32_t to, uint32_t rest, auto with_rest) {
+            uint32_t wd[4 * kLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) wd[4 * k] = codes[k].x, wd[4 * k + 1] = codes[k].y, wd[4 * k + 2] = codes[k].z, wd[4 * k + 3] = codes[k].w;
+            // word c * J/2 + jh: channels 4 c.. of group 2 jh in its low half, of group 2 jh + 1 in its high one
+#pragma unroll
+            for (int c = 0; c < 8; c += 2)
+#pragma unroll
+                for (int jh = 0; jh < J / 2; ++jh) {
+                    uint32_t x[4], y[4];
+                    from_e2m1x8(wd[c * (J / 2) + jh], x);
+                    from_e2m1x8(wd[(c + 1) * (J / 2) + jh], y);
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        const uint32_t s2 = __byte_perm(scales[jh], 0u, jj ? 0x3232u : 0x1010u);
+                        const uint32_t v[4] = {x[2 * jj], x[2 * jj + 1], y[2 * jj], y[2 * jj + 1]};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = half2_mul(v[e], s2);
+                        const uint32_t at = jh * Sh::kPanel + row_at + ((((jj * 4 + c / 2)) ^ (key_in & 7)) << 4);
+                        sts_v4(to + at, h[0], h[1], h[2], h[3]);
+                        if constexpr (decltype(with_rest)::value) {
+                            uint32_t g[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) g[e] = half2_rest(v[e], s2, h[e]);
+                            sts_v4(rest + at, g[0], g[1], g[2], g[3]);
+                        }
+                    }
+                }
+        };
+        Row row[2];
+        find_page();
+        if (more) load_row(row[0]);
+        int64_t left = 0;  // tiles of this run
+        for (PromptSegment s = seg;;) {
+            left += max(0, end_of(s) - first_of(s));
+            if (s.end >= r1) break;
+            prompt_next<Sh::kRows>(p, s);
+        }
+        auto step = [&](Row& now, Row& then) {
+            if ((int64_t)n + 1 < left) load_row(then);
+            const uint32_t there = __ballot_sync(0xffffffffu, now.there);
+            if (lane == 0) {
+                seen_words[n & 3][warp & 3] = there;
+                mbar_arrive(seen_full + 8 * (n & 3));
+            }
+            if (n >= 1) ok = wait(k_empty, n - 1);
+            if (!ok) return;
+            unpack(now.k, now.ks, smem + Sh::kK, smem + Sh::kK + Sh::kTile, std::true_type{});
+            fence_proxy_async_smem();
+            mbar_arrive(k_full);
+            if (n >= 2) ok = wait(v_empty + 8 * (n & 1), (n >> 1) - 1);
+            if (!ok) return;
+            unpack(now.v, now.vs, smem + Sh::kV + (n & 1) * Sh::kTile, 0u, std::false_type{});
+            fence_proxy_async_smem();
+            mbar_arrive(v_full + 8 * (n & 1));
+            ++n;
+        };
+        while (ok && (int64_t)n < left) {
+            step(row[0], row[1]);
+            if (ok && (int64_t)n < left) step(row[1], row[0]);
+        }
+    } else {
+        // =============================== products: one thread issues ====
+        const uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
+        auto scores = [&](int i) {  // S_i = Q_i K^T, both parts of K
+            if (lane == 0) {
+#pragma unroll
+                for (int part2 = 0; part2 < 2; ++part2)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k >> 2) * Sh::kPanel + (k & 3) * 32;
+                        tc_mma(tmem + 128 * i, tile_desc(smem + i * Sh::kTile + at, 16),
+                               tile_desc(smem + Sh::kK + part2 * Sh::kTile + at, 16), kQk, part2 + k > 0);
+                    }
+                tc_commit(s_full + 8 * i);
+                if (i == TILES - 1) tc_commit(k_empty);
+            }
+            __syncwarp();
+        };
+        while (ok) {
+            const int t0 = first_of(seg), t1 = end_of(seg);
+            if (t0 < t1) {
+                for (int i = 0; i < TILES && ok; ++i) {
+                    ok = wait(q_full + 8 * i, sn) && (i > 0 || wait(k_full, n));
+                    if (!ok) break;
+                    tc_after_sync();
+                    scores(i);
+                }
+                for (int tl = t0; tl < t1 && ok; ++tl, ++n) {
+                    ok = wait(v_full + 8 * (n & 1), n >> 1);
+                    for (int i = 0; i < TILES && ok; ++i) {
+                        ok = wait(p_full + 8 * i, n);
+                        if (!ok) break;
+                        tc_after_sync();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < kPromptKeys / 16; ++k)
+                                tc_mma_ts(tmem + 128 * (TILES + i), tmem + 128 * i + 8 * k,
+                                          tile_desc(smem + Sh::kV + (n & 1) * Sh::kTile + k * 2048, Sh::kPanel), kPv, tl > t0 || k > 0);
+                            if (i == TILES - 1) tc_commit(v_empty + 8 * (n & 1));
+                            if (tl + 1 == t1) tc_commit(o_full + 8 * i);
+                        }
+                        __syncwarp();
+                        if (tl + 1 < t1) {
+                            if (i == 0) {
+                                ok = wait(k_full, n + 1);
+                                if (!ok) break;
+                                tc_after_sync();
+                            }
+                            scores(i);
+                        }
+                    }
+                }
+                ++sn;
+            }
+            if (seg.end >= r1) break;
+            prompt_next<Sh::kRows>(p, seg);
+        }
+        // nothing is in flight when TMEM goes back
+        if (lane == 0) tc_commit(drained);
+        __syncwarp();
+        wait(drained, 0);
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == Sh::kWarps - 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" : : "r"(tmem), "r"(Sh::kColumns) : "memory");
+}
+
+template <int D, int TILES>
+static rra_status_t prompt_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
+    using Sh = PromptShape<D, TILES>;
+    const void* k = (const void*)kv_attention_prompt_kernel<D, TILES>;
+    static_assert(1024 + Sh::kSums + 4 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 2048, "shared memory");
+    if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
+        cudaGetLastError();
+        return RRA_ERR_CUDA;
+    }
+    void* args[] = {(void*)&p};
+    return serve_launch(k, dim3((unsigned)ctas), Sh::kThreads, Sh::smem(p.a.requests), 1, stream, args);
+}
+
+size_t prefill_partial_bytes(int head_dim) {
+    return (size_t)kPromptMaxCtas * 2 * 2 * kPromptRows * ((size_t)head_dim + 2) * sizeof(float);
+}
+
+rra_status_t launch_prefill(const AttnParams& p, int sms, rra_stream_t stream) {
+    const int ctas = std::min(sms, kPromptMaxCtas);
+    const bool two = (int64_t)p.a.max_q * p.group > kPromptRows;
+    if (p.a.cache.head_dim == 128) return two ? prompt_launch<128, 2>(p, ctas, stream) : prompt_launch<128, 1>(p, ctas, stream);
+    return two ? prompt_launch<64, 2>(p, ctas, stream) : prompt_launch<64, 1>(p, ctas, stream);
+}
+
+}  // namespace rra
