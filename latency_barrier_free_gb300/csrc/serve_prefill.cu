@@ -53,24 +53,30 @@ struct PromptShape {
 };
 
 // ------------------------------------------------------------- tcgen05 ----
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t panel_stride) {
-    // start, leading dimension (panels of 64, for the operand whose rows are keys), stride of 8 rows, 128-byte swizzle
-    return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)((panel_stride >> 4) & 0x3fffu) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// A tile in shared memory as an operand.  Low word: start and, for the operand whose rows are keys, the distance of its
+// panels of 64 columns, in 16 bytes; a step along the tile adds to the start.  High word: 8 rows apart by 1024 bytes,
+// 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t addr, uint32_t panels) { return addr >> 4 | panels >> 4 << 16; }
+constexpr uint32_t kTileDescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
 // binary32 sums of binary16 products, 128 rows, n columns; b_keys: B's rows are the summed index
 constexpr uint32_t mma_desc(int n, bool b_keys) {
     return 1u << 4 | (b_keys ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 : : "r"(d), "l"(a), "l"(b), "r"(desc), "r"(add ? 1 : 0) : "memory");
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+                 "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+                 : : "r"(d), "r"(a), "r"(b), "r"(desc), "r"(add ? 1 : 0), "r"(kTileDescHigh) : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 : : "r"(d), "r"(a), "l"(b), "r"(desc), "r"(add ? 1 : 0) : "memory");
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+                 : : "r"(d), "r"(a), "r"(b), "r"(desc), "r"(add ? 1 : 0), "r"(kTileDescHigh) : "memory");
+}
+// One lane of the warp, the same for every call.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" : : "r"(bar) : "memory");
@@ -681,16 +687,17 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         }
     } else {
         // =============================== products: one thread issues ====
-        const uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
+        constexpr uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
+        const uint32_t q_desc = tile_desc(smem, 16), k_desc = tile_desc(smem + Sh::kK, 16), v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
+        constexpr uint32_t kStep = Sh::kTile >> 4;  // from one tile to the next, in a descriptor
         auto scores = [&](int i) {  // S_i = Q_i K^T, both parts of K
-            if (lane == 0) {
+            if (elected()) {
 #pragma unroll
                 for (int part2 = 0; part2 < 2; ++part2)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = (k >> 2) * Sh::kPanel + (k & 3) * 32;
-                        tc_mma(tmem + 128 * i, tile_desc(smem + i * Sh::kTile + at, 16),
-                               tile_desc(smem + Sh::kK + part2 * Sh::kTile + at, 16), kQk, part2 + k > 0);
+                        constexpr auto at = [](int x) { return (uint32_t)((x >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
+                        tc_mma(tmem + 128 * i, q_desc + i * kStep + at(k), k_desc + part2 * kStep + at(k), kQk, part2 + k > 0);
                     }
                 tc_commit(s_full + 8 * i);
                 if (i == TILES - 1) tc_commit(k_empty);
@@ -712,11 +719,11 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                         ok = wait(p_full + 8 * i, n);
                         if (!ok) break;
                         tc_after_sync();
-                        if (lane == 0) {
+                        if (elected()) {
+                            const uint32_t v_at = v_desc + (n & 1) * kStep;
 #pragma unroll
                             for (int k = 0; k < kPromptKeys / 16; ++k)
-                                tc_mma_ts(tmem + 128 * (TILES + i), tmem + 128 * i + 8 * k,
-                                          tile_desc(smem + Sh::kV + (n & 1) * Sh::kTile + k * 2048, Sh::kPanel), kPv, tl > t0 || k > 0);
+                                tc_mma_ts(tmem + 128 * (TILES + i), tmem + 128 * i + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
                             if (i == TILES - 1) tc_commit(v_empty + 8 * (n & 1));
                             if (tl + 1 == t1) tc_commit(o_full + 8 * i);
                         }
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             prompt_next<Sh::kRows>(p, seg);
         }
         // nothing is in flight when TMEM goes back
-        if (lane == 0) tc_commit(drained);
+        if (elected()) tc_commit(drained);
         __syncwarp();
         wait(drained, 0);
     }
