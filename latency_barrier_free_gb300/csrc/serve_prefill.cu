@@ -13,9 +13,12 @@
 // has a row, so maxima and sums need no exchange.  While one tile's scores are
 // exponentiated the other's products run.
 //
-// The weights are taken against the maximum so far, before this tile's is known:
-// where it does not pass the old one by more than 2^kSlack (nearly always, after
-// a row's first keys), one pass over the scores is enough, and O is not touched.
+// The maximum that weights are taken against moves only when a score passes it by
+// more than kPromptSlack (in units of log2); then O is scaled, in TMEM, which is
+// rare after a row's first keys.  The code of every role is kept small (loops
+// over 32 columns, one place for each product): four kinds of warps share the
+// instruction cache, and with twice the code the issuing thread alone cost a
+// third of the time.
 //
 // Work is cut into equal runs of key tiles, one per CTA, as in serve_attn.cu;
 // what a run has of a segment it shares goes to the workspace, and the last CTA
@@ -44,8 +47,12 @@ struct PromptShape {
     static constexpr int kK = TILES * kTile;            // after the queries: K, high and low parts
     static constexpr int kV = kK + 2 * kTile;           // two stages of V
     static constexpr int kSums = kV + 2 * kTile;        // running sums of the requests' chunks
+    // Warps: softmax (a warp reaches the TMEM lanes of its number modulo 4), then the one that issues the products, then
+    // four that unpack.  Warps that are alike modulo 4 share a scheduler: the issuing one has only softmax warps beside it.
     static constexpr int kSoftmaxWarps = 4 * TILES;
-    static constexpr int kWarps = kSoftmaxWarps + 4 + 1;
+    static constexpr int kIssue = kSoftmaxWarps;
+    static constexpr int kUnpack = kSoftmaxWarps + 1;  // and on: + 0, 1, 2 and 4
+    static constexpr int kWarps = kSoftmaxWarps + 6;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
     static constexpr int kPart = kPromptRows * (D + 2);      // floats of a part: rows in columns of 4 channels, statistics
@@ -107,6 +114,14 @@ __device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* v) {
           "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(a)
         : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+        :
+        : "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
+        : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" : : "r"(bar) : "memory");
 }
@@ -136,9 +151,8 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
 }
 // a * b - c, rounded once: with c the rounded product, what its rounding lost
 __device__ __forceinline__ uint32_t half2_rest(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c ^ 0x80008000u));
-    return r;
+    const __half2 r = __hfma2(*(const __half2*)&a, *(const __half2*)&b, __hneg2(*(const __half2*)&c));
+    return *(const uint32_t*)&r;
 }
 
 // --------------------------------------------------------- work as a row ----
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             before += all;
         }
     }
-    if (warp == Sh::kWarps - 1) {
+    if (warp == Sh::kIssue) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -391,56 +405,36 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     tc_after_sync();
                     const int key0 = (seg.first_tile + tl) * kPromptKeys;
                     const volatile uint32_t* const words = seen_words[n & 3];
-                    const uint4 seen = make_uint4(words[0], words[1], words[2], words[3]);
                     const bool whole = __all_sync(0xffffffffu, key0 >= lo && key0 + kPromptKeys <= hi) &&
-                                       (seen.x & seen.y & seen.z & seen.w) == 0xffffffffu;
-                    uint32_t w[64];   // the weights, two a word
-                    float top, sum;
-                    auto weigh = [&]() {
-                        top = -FLT_MAX;
-                        const uint64_t off = pair2(-m, -m);
-                        uint64_t sum2 = pair2(0.f, 0.f);
+                                       (words[0] & words[1] & words[2] & words[3]) == 0xffffffffu;
+                    // ---- the row's largest score; scores that it does not see go back as -inf ----
+                    float top = -FLT_MAX;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[32];
+                        tc_ld32(s_at + 32 * q, v);
+                        tc_wait_ld();
+                        if (!whole) {
+                            // keys lo..hi of these 32, as bits, and of them those that are there
+                            const int from = min(max(lo - key0 - 32 * q, 0), 32), to = min(max(hi - key0 - 32 * q, 0), 32);
+                            const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
+                            const uint32_t mask = words[q] & below & (from == 32 ? 0u : 0xffffffffu << from);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t v[32];
-                            tc_ld32(s_at + 32 * q, v);
-                            tc_wait_ld();
-                            if (!whole) {
-                                const uint32_t here = q == 0 ? seen.x : q == 1 ? seen.y : q == 2 ? seen.z : seen.w;
-                                // keys lo..hi of these 32, as bits
-                                const int from = min(max(lo - key0 - 32 * q, 0), 32), to = min(max(hi - key0 - 32 * q, 0), 32);
-                                const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
-                                const uint32_t mask = here & below & (from == 32 ? 0u : 0xffffffffu << from);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!(mask >> k & 1u)) v[k] = __float_as_uint(-INFINITY);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
-                                top = fmaxf(top, fmaxf(x, y));
-                                float e0, e1;
-                                split2(mul2(add2(pair2(x, y), off), factor2), e0, e1);
-                                e0 = exp2_fast(e0);
-                                e1 = exp2_fast(e1);
-                                sum2 = add2(sum2, pair2(e0, e1));
-                                w[16 * q + k / 2] = pack_half2(e0, e1);
-                            }
+                            for (int k = 0; k < 32; ++k) v[k] = mask >> k & 1u ? v[k] : 0xff800000u;
+                            tc_st32(s_at + 32 * q, v);
                         }
-                        float a0, a1;
-                        split2(sum2, a0, a1);
-                        sum = a0 + a1;
-                    };
-                    weigh();
-                    if (__any_sync(0xffffffffu, top > limit)) {
-                        // a maximum moved: scale what was summed, weigh again
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                    }
+                    if (!whole) tc_wait_st();
+                    if (__any_sync(0xffffffffu, top > limit)) {  // a maximum moves: scale what was summed
                         const float now = top > limit ? top : m;
                         const float by = exp2_fast((m - now) * factor);
                         m = now;
                         limit = now + __fdividef(kPromptSlack, factor);
                         l *= by;
                         if (tl > t0) {
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
                                 uint32_t v[32];
                                 tc_ld32(o_at + 32 * q, v);
@@ -450,11 +444,29 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                                 tc_st32(o_at + 32 * q, v);
                             }
                         }
-                        weigh();
                     }
-                    l += sum;
-                    tc_st32(s_at, w);
-                    tc_st32(s_at + 32, w + 32);
+                    // ---- weights, over scores already read ----
+                    const uint64_t off = pair2(-m, -m);
+                    uint64_t sum2 = pair2(0.f, 0.f);
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[32];
+                        tc_ld32(s_at + 32 * q, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float e0, e1;
+                            split2(mul2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), off), factor2), e0, e1);
+                            e0 = exp2_fast(e0);
+                            e1 = exp2_fast(e1);
+                            sum2 = add2(sum2, pair2(e0, e1));
+                            v[k / 2] = pack_half2(e0, e1);
+                        }
+                        tc_st16(s_at + 16 * q, v);
+                    }
+                    float a0, a1;
+                    split2(sum2, a0, a1);
+                    l += a0 + a1;
                     tc_wait_st();
                     tc_before_sync();
                     mbar_arrive(p_full + 8 * i);
@@ -561,9 +573,9 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             tc_before_sync();
             prompt_next<Sh::kRows>(p, seg);
         }
-    } else if (warp < Sh::kSoftmaxWarps + 4) {
+    } else if (warp != Sh::kIssue && warp != Sh::kUnpack + 3) {
         // =============================== unpacking: a thread has a key ====
-        const int key_in = tid - 32 * Sh::kSoftmaxWarps;
+        const int unpacker = warp == Sh::kUnpack + 4 ? 3 : warp - Sh::kUnpack, key_in = 32 * unpacker + lane;
         const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
         constexpr int kLoads = D / 32;  // 16-byte loads of a row of codes
         struct Row {
@@ -653,39 +665,37 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     }
                 }
         };
-        Row row[2];
-        find_page();
-        if (more) load_row(row[0]);
         int64_t left = 0;  // tiles of this run
         for (PromptSegment s = seg;;) {
             left += max(0, end_of(s) - first_of(s));
             if (s.end >= r1) break;
             prompt_next<Sh::kRows>(p, s);
         }
-        auto step = [&](Row& now, Row& then) {
+        Row then;
+        find_page();
+        if (more) load_row(then);
+#pragma unroll 1
+        while ((int64_t)n < left) {
+            const Row now = then;
             if ((int64_t)n + 1 < left) load_row(then);
             const uint32_t there = __ballot_sync(0xffffffffu, now.there);
             if (lane == 0) {
-                seen_words[n & 3][warp & 3] = there;
+                seen_words[n & 3][unpacker] = there;
                 mbar_arrive(seen_full + 8 * (n & 3));
             }
             if (n >= 1) ok = wait(k_empty, n - 1);
-            if (!ok) return;
+            if (!ok) break;
             unpack(now.k, now.ks, smem + Sh::kK, smem + Sh::kK + Sh::kTile, std::true_type{});
             fence_proxy_async_smem();
             mbar_arrive(k_full);
             if (n >= 2) ok = wait(v_empty + 8 * (n & 1), (n >> 1) - 1);
-            if (!ok) return;
+            if (!ok) break;
             unpack(now.v, now.vs, smem + Sh::kV + (n & 1) * Sh::kTile, 0u, std::false_type{});
             fence_proxy_async_smem();
             mbar_arrive(v_full + 8 * (n & 1));
             ++n;
-        };
-        while (ok && (int64_t)n < left) {
-            step(row[0], row[1]);
-            if (ok && (int64_t)n < left) step(row[1], row[0]);
         }
-    } else {
+    } else if (warp == Sh::kIssue) {
         // =============================== products: one thread issues ====
         constexpr uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
         const uint32_t q_desc = tile_desc(smem, 16), k_desc = tile_desc(smem + Sh::kK, 16), v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
@@ -707,36 +717,36 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);
             if (t0 < t1) {
-                for (int i = 0; i < TILES && ok; ++i) {
-                    ok = wait(q_full + 8 * i, sn) && (i > 0 || wait(k_full, n));
-                    if (!ok) break;
-                    tc_after_sync();
-                    scores(i);
-                }
-                for (int tl = t0; tl < t1 && ok; ++tl, ++n) {
-                    ok = wait(v_full + 8 * (n & 1), n >> 1);
+#pragma unroll 1
+                for (int tl = t0 - 1; tl < t1 && ok; ++tl) {  // products of tile tl, scores of the next
+                    const bool values = tl >= t0, next = tl + 1 < t1;
+                    const uint32_t v_at = v_desc + (n & 1) * kStep;
+                    if (values) ok = wait(v_full + 8 * (n & 1), n >> 1);
+#pragma unroll 1
                     for (int i = 0; i < TILES && ok; ++i) {
-                        ok = wait(p_full + 8 * i, n);
+                        ok = values ? wait(p_full + 8 * i, n) : wait(q_full + 8 * i, sn);
                         if (!ok) break;
                         tc_after_sync();
-                        if (elected()) {
-                            const uint32_t v_at = v_desc + (n & 1) * kStep;
+                        if (values) {
+                            if (elected()) {
 #pragma unroll
-                            for (int k = 0; k < kPromptKeys / 16; ++k)
-                                tc_mma_ts(tmem + 128 * (TILES + i), tmem + 128 * i + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
-                            if (i == TILES - 1) tc_commit(v_empty + 8 * (n & 1));
-                            if (tl + 1 == t1) tc_commit(o_full + 8 * i);
+                                for (int k = 0; k < kPromptKeys / 16; ++k)
+                                    tc_mma_ts(tmem + 128 * (TILES + i), tmem + 128 * i + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
+                                if (i == TILES - 1) tc_commit(v_empty + 8 * (n & 1));
+                                if (!next) tc_commit(o_full + 8 * i);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
-                        if (tl + 1 < t1) {
+                        if (next) {
                             if (i == 0) {
-                                ok = wait(k_full, n + 1);
+                                ok = wait(k_full, values ? n + 1 : n);
                                 if (!ok) break;
                                 tc_after_sync();
                             }
                             scores(i);
                         }
                     }
+                    if (values) ++n;
                 }
                 ++sn;
             }
@@ -750,7 +760,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     }
     tc_before_sync();
     __syncthreads();
-    if (warp == Sh::kWarps - 1)
+    if (warp == Sh::kIssue)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" : : "r"(tmem), "r"(Sh::kColumns) : "memory");
 }
 
