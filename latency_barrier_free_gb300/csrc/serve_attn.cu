@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             const uint64_t start = globaltimer_ns();
 #pragma unroll 1
             for (int i = 0; i < kStages; ++i)
-                while (!mbar_try_wait(bars + 8 * i, (issued >> i & 1u) ^ 1u))
+                while (!attn_try(bars + 8 * i, (issued >> i & 1u) ^ 1u))
                     if (globaltimer_ns() - start > kAttnWaitNs) break;
         };
         int take = 0;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             for (int tl = tile0; tl < tile1; ++tl) {
                 const uint32_t bar = bars + 8 * take, tile = ring + take * Sh::kStage;
                 if (!dead)
-                    dead = __any_sync(0xffffffffu, !mbar_try_wait(bar, phase >> take & 1u) && !attn_wait_slow(bar, phase >> take & 1u, ws));
+                    dead = __any_sync(0xffffffffu, !attn_try(bar, phase >> take & 1u) && !attn_wait_slow(bar, phase >> take & 1u, ws));
                 phase ^= 1u << take;
                 const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
 #pragma unroll 1

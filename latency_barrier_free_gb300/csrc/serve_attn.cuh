@@ -24,13 +24,23 @@ struct AttnWorkspace {
     uint32_t pad_end[1024 - 64 - kAttnMaxCtas];
 };
 static_assert(sizeof(AttnWorkspace) == 4096, "the part of the workspace that starts as zero");
-// The rest of a wait whose first try found its barrier's phase open.  Gives up after kAttnWaitNs, or soon after another
-// wait did, and says so in the status word.
+// One try of a wait on a barrier of this CTA: returns when its phase is done, or after about kAttnTryNs.  Acquire in the
+// CTA only: at cluster scope every try also drops the L1 cache.
+constexpr uint32_t kAttnTryNs = 20000;
+__device__ __forceinline__ bool attn_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kAttnTryNs)
+        : "memory");
+    return done != 0;
+}
+// The rest of a wait whose first try did not see the phase done.  Gives up after kAttnWaitNs, or soon after another wait
+// did, and says so in the status word.
 static __device__ __noinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity, AttnWorkspace* ws) {
     const uint64_t start = globaltimer_ns();
-    for (uint32_t spins = 1;; ++spins) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((spins & 15u) != 0u) continue;
+    while (!attn_try(bar, parity)) {
         const uint64_t waited = globaltimer_ns() - start;
         if (waited > kAttnWaitNs) {
             atomicCAS(&ws->status, 0u, (uint32_t)RRA_ERR_TIMEOUT);
@@ -38,6 +48,7 @@ static __device__ __noinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity
         }
         if (waited > kStatusAfterNs && ld_relaxed_u32(&ws->status) != 0u) return false;
     }
+    return true;
 }
 
 struct AttnParams {

@@ -44,19 +44,21 @@ struct PromptShape {
     static constexpr int kRows = TILES * kPromptRows;
     static constexpr int kPanel = 128 * 128;            // 128 rows of 64 binary16, swizzled in 128 bytes
     static constexpr int kTile = D / 64 * kPanel;       // 128 rows of D binary16
-    static constexpr int kK = TILES * kTile;            // after the queries: K, high and low parts
-    static constexpr int kV = kK + 2 * kTile;           // two stages of V
-    static constexpr int kSums = kV + 2 * kTile;        // running sums of the requests' chunks
-    // Warps: softmax (a warp reaches the TMEM lanes of its number modulo 4), then the one that issues the products, then
-    // four that unpack.  Warps that are alike modulo 4 share a scheduler: the issuing one has only softmax warps beside it.
+    static constexpr int kK = TILES * kTile;            // after the queries: two stages of K, high and low parts
+    static constexpr int kV = kK + 4 * kTile;           // V
+    static constexpr int kEnd = kV + kTile;
+    static constexpr int kSums = kK;                    // before any tile: running sums of the requests' chunks
+    static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
+    // Warps: softmax (a warp reaches the TMEM lanes of its number modulo 4), then four that unpack, then one for each tile
+    // that issues its products: one for both left the tensor cores idle for 300 to 500 cycles between products.
     static constexpr int kSoftmaxWarps = 4 * TILES;
-    static constexpr int kIssue = kSoftmaxWarps;
-    static constexpr int kUnpack = kSoftmaxWarps + 1;  // and on: + 0, 1, 2 and 4
-    static constexpr int kWarps = kSoftmaxWarps + 6;
+    static constexpr int kUnpack = kSoftmaxWarps;
+    static constexpr int kIssue = kUnpack + 4;
+    static constexpr int kWarps = kIssue + TILES;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
     static constexpr int kPart = kPromptRows * (D + 2);      // floats of a part: rows in columns of 4 channels, statistics
-    static size_t smem(int requests) { return 1024 + kSums + 4 * ((size_t)requests + 1); }
+    static constexpr int kSmem = 1024 + kEnd;
 };
 
 // ------------------------------------------------------------- tcgen05 ----
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     using B = KvBlock<D>;
     constexpr int J = B::kGroups;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t bar_mem[3 * TILES + 2 * TILES + 2 + 4 + 4 + 1];
+    __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 4 + 2 + 4 + 1];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
     __shared__ uint32_t tmem_base;
@@ -246,8 +248,8 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
 
     const uint32_t bars = smem_u32(bar_mem);
     const uint32_t q_full = bars, s_full = q_full + 8 * TILES, p_full = s_full + 8 * TILES, o_full = p_full + 8 * TILES,
-                   joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 8, v_full = k_empty + 8,
-                   v_empty = v_full + 16, seen_full = v_empty + 16, drained = seen_full + 32;
+                   joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 16, v_full = k_empty + 16,
+                   v_empty = v_full + 8, seen_full = v_empty + 8, drained = seen_full + 32, turn = drained + 8;
     pdl_release_early();
     if (tid == 0) {
         for (int i = 0; i < TILES; ++i) {
@@ -256,15 +258,16 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             mbar_init(p_full + 8 * i, kPromptRows);
             mbar_init(o_full + 8 * i, 1);
             mbar_init(joined + 8 * i, kPromptRows);
+            mbar_init(turn + 8 * i, 1);
         }
-        mbar_init(k_full, 128);
-        mbar_init(k_empty, 1);
+        mbar_init(v_full, 128);
+        mbar_init(v_empty, TILES);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(v_full + 8 * i, 128);
-            mbar_init(v_empty + 8 * i, 1);
+            mbar_init(k_full + 8 * i, 128);
+            mbar_init(k_empty + 8 * i, TILES);
         }
         for (int i = 0; i < 4; ++i) mbar_init(seen_full + 8 * i, 4);
-        mbar_init(drained, 1);
+        mbar_init(drained, TILES);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         return (int)(to > 0 ? to : 0);
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u) || attn_wait_slow(bar, parity & 1u, ws));
+        return __all_sync(0xffffffffu, attn_try(bar, parity & 1u) || attn_wait_slow(bar, parity & 1u, ws));
     };
 
     uint32_t n = 0;   // key tiles of this run so far
@@ -409,11 +412,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                                        (words[0] & words[1] & words[2] & words[3]) == 0xffffffffu;
                     // ---- the row's largest score; scores that it does not see go back as -inf ----
                     float top = -FLT_MAX;
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t v[32];
-                        tc_ld32(s_at + 32 * q, v);
-                        tc_wait_ld();
+                    auto largest = [&](int q, uint32_t* v) {
                         if (!whole) {
                             // keys lo..hi of these 32, as bits, and of them those that are there
                             const int from = min(max(lo - key0 - 32 * q, 0), 32), to = min(max(hi - key0 - 32 * q, 0), 32);
@@ -425,6 +424,17 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                         }
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                    };
+                    uint32_t v0[32], v1[32];  // 32 columns in hand, 32 on their way
+                    tc_ld32(s_at, v0);
+#pragma unroll 1
+                    for (int q = 0; q < 4; q += 2) {
+                        tc_wait_ld();
+                        tc_ld32(s_at + 32 * (q + 1), v1);
+                        largest(q, v0);
+                        tc_wait_ld();
+                        if (q == 0) tc_ld32(s_at + 64, v0);
+                        largest(q + 1, v1);
                     }
                     if (!whole) tc_wait_st();
                     if (__any_sync(0xffffffffu, top > limit)) {  // a maximum moves: scale what was summed
@@ -448,11 +458,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     // ---- weights, over scores already read ----
                     const uint64_t off = pair2(-m, -m);
                     uint64_t sum2 = pair2(0.f, 0.f);
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t v[32];
-                        tc_ld32(s_at + 32 * q, v);
-                        tc_wait_ld();
+                    auto weigh = [&](int q, uint32_t* v) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
                             float e0, e1;
@@ -463,6 +469,16 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                             v[k / 2] = pack_half2(e0, e1);
                         }
                         tc_st16(s_at + 16 * q, v);
+                    };
+                    tc_ld32(s_at, v0);
+#pragma unroll 1
+                    for (int q = 0; q < 4; q += 2) {
+                        tc_wait_ld();
+                        tc_ld32(s_at + 32 * (q + 1), v1);
+                        weigh(q, v0);
+                        tc_wait_ld();
+                        if (q == 0) tc_ld32(s_at + 64, v0);
+                        weigh(q + 1, v1);
                     }
                     float a0, a1;
                     split2(sum2, a0, a1);
@@ -573,15 +589,18 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             tc_before_sync();
             prompt_next<Sh::kRows>(p, seg);
         }
-    } else if (warp != Sh::kIssue && warp != Sh::kUnpack + 3) {
+    } else if (warp < Sh::kIssue) {
         // =============================== unpacking: a thread has a key ====
-        const int unpacker = warp == Sh::kUnpack + 4 ? 3 : warp - Sh::kUnpack, key_in = 32 * unpacker + lane;
+        const int unpacker = warp - Sh::kUnpack, key_in = 32 * unpacker + lane;
         const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
         constexpr int kLoads = D / 32;  // 16-byte loads of a row of codes
-        struct Row {
-            uint4 k[kLoads], v[kLoads];
-            uint32_t ks[J / 2], vs[J / 2];
-            bool there;
+        struct Codes {  // of a row, and its scales
+            uint4 c[kLoads];
+            uint32_t s[J / 2];
+        };
+        struct Place {  // a key's block and row; null if it is not there
+            const char* block;
+            int row;
         };
         // the segment and tile after the one in hand: what is loaded next
         PromptSegment ahead = seg;
@@ -607,50 +626,43 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             key = (ahead.first_tile + next) * kPromptKeys + key_in;
             if (key < ahead.n.kv) page = a.block_table[ahead.b * a.table_stride + key / ps];
         };
-        auto load_row = [&](Row& x) {  // the row of the tile that find_page() looked up, then the page of the one after
-            x.there = page >= 0 && page < a.cache.num_pages;
-            if (x.there) {
+        auto next_place = [&]() {  // of the tile that find_page() looked up, then the page of the one after
+            Place x{nullptr, 0};
+            if (page >= 0 && page < a.cache.num_pages) {
                 const int in = key - key / ps * ps;
-                const char* const block = (const char*)a.cache.pages +
-                                          (((int64_t)page * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
-                const int rr = in % kKvBlockTokens;
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    x.k[k] = *((const uint4*)(block + rr * B::kRow) + k);
-                    x.v[k] = *((const uint4*)(block + B::kV + rr * B::kRow) + k);
-                }
-#pragma unroll
-                for (int k = 0; k < J / 2; ++k) {
-                    x.ks[k] = *((const uint32_t*)(block + B::kScaleK + rr * B::kScaleRow) + k);
-                    x.vs[k] = *((const uint32_t*)(block + B::kScaleV + rr * B::kScaleRow) + k);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) x.k[k] = x.v[k] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int k = 0; k < J / 2; ++k) x.ks[k] = x.vs[k] = 0u;
+                x.block = (const char*)a.cache.pages + (((int64_t)page * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
+                x.row = in % kKvBlockTokens;
             }
             if (more) ++next;
             find_page();
+            return x;
+        };
+        auto load = [&](Codes& x, const Place& at, int codes, int scales) {
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+                x.c[k] = at.block != nullptr ? *((const uint4*)(at.block + codes + at.row * B::kRow) + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < J / 2; ++k)
+                x.s[k] = at.block != nullptr ? *((const uint32_t*)(at.block + scales + at.row * B::kScaleRow) + k) : 0u;
         };
         // A row's codes as binary16 into its place of a swizzled tile; with kRest the part that rounding lost into `rest`.
         const uint32_t row_at = key_in * 128;
-        auto unpack = [&](const uint4* codes, const uint32_t* scales, uint32_t to, uint32_t rest, auto with_rest) {
+        auto unpack = [&](const Codes& x, uint32_t to, uint32_t rest, auto with_rest) {
             uint32_t wd[4 * kLoads];
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) wd[4 * k] = codes[k].x, wd[4 * k + 1] = codes[k].y, wd[4 * k + 2] = codes[k].z, wd[4 * k + 3] = codes[k].w;
+            for (int k = 0; k < kLoads; ++k) wd[4 * k] = x.c[k].x, wd[4 * k + 1] = x.c[k].y, wd[4 * k + 2] = x.c[k].z, wd[4 * k + 3] = x.c[k].w;
             // word c * J/2 + jh: channels 4 c.. of group 2 jh in its low half, of group 2 jh + 1 in its high one
 #pragma unroll
             for (int c = 0; c < 8; c += 2)
 #pragma unroll
                 for (int jh = 0; jh < J / 2; ++jh) {
-                    uint32_t x[4], y[4];
-                    from_e2m1x8(wd[c * (J / 2) + jh], x);
-                    from_e2m1x8(wd[(c + 1) * (J / 2) + jh], y);
+                    uint32_t even[4], odd[4];
+                    from_e2m1x8(wd[c * (J / 2) + jh], even);
+                    from_e2m1x8(wd[(c + 1) * (J / 2) + jh], odd);
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj) {
-                        const uint32_t s2 = __byte_perm(scales[jh], 0u, jj ? 0x3232u : 0x1010u);
-                        const uint32_t v[4] = {x[2 * jj], x[2 * jj + 1], y[2 * jj], y[2 * jj + 1]};
+                        const uint32_t s2 = __byte_perm(x.s[jh], 0u, jj ? 0x3232u : 0x1010u);
+                        const uint32_t v[4] = {even[2 * jj], even[2 * jj + 1], odd[2 * jj], odd[2 * jj + 1]};
                         uint32_t h[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) h[e] = half2_mul(v[e], s2);
@@ -671,86 +683,106 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             if (s.end >= r1) break;
             prompt_next<Sh::kRows>(p, s);
         }
-        Row then;
-        find_page();
-        if (more) load_row(then);
-#pragma unroll 1
-        while ((int64_t)n < left) {
-            const Row now = then;
-            if ((int64_t)n + 1 < left) load_row(then);
-            const uint32_t there = __ballot_sync(0xffffffffu, now.there);
+        // K is unpacked a tile ahead of V: its two stages are free before V's one
+        auto unpack_k = [&](uint32_t tile, const Codes& x, bool here) {
+            const uint32_t there = __ballot_sync(0xffffffffu, here);
             if (lane == 0) {
-                seen_words[n & 3][unpacker] = there;
-                mbar_arrive(seen_full + 8 * (n & 3));
+                seen_words[tile & 3][unpacker] = there;
+                mbar_arrive(seen_full + 8 * (tile & 3));
             }
-            if (n >= 1) ok = wait(k_empty, n - 1);
-            if (!ok) break;
-            unpack(now.k, now.ks, smem + Sh::kK, smem + Sh::kK + Sh::kTile, std::true_type{});
+            if (tile >= 2) ok = wait(k_empty + 8 * (tile & 1), (tile >> 1) - 1);
+            if (!ok) return;
+            const uint32_t to = smem + Sh::kK + (tile & 1) * 2 * Sh::kTile;
+            unpack(x, to, to + Sh::kTile, std::true_type{});
             fence_proxy_async_smem();
-            mbar_arrive(k_full);
-            if (n >= 2) ok = wait(v_empty + 8 * (n & 1), (n >> 1) - 1);
-            if (!ok) break;
-            unpack(now.v, now.vs, smem + Sh::kV + (n & 1) * Sh::kTile, 0u, std::false_type{});
-            fence_proxy_async_smem();
-            mbar_arrive(v_full + 8 * (n & 1));
-            ++n;
+            mbar_arrive(k_full + 8 * (tile & 1));
+        };
+        Codes k_now, v_now;   // K of tile n, V of tile n - 1
+        Place place{nullptr, 0};  // of tile n
+        find_page();
+        if (left > 0) {
+            place = next_place();
+            load(k_now, place, 0, B::kScaleK);
         }
-    } else if (warp == Sh::kIssue) {
-        // =============================== products: one thread issues ====
-        constexpr uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
-        const uint32_t q_desc = tile_desc(smem, 16), k_desc = tile_desc(smem + Sh::kK, 16), v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
-        constexpr uint32_t kStep = Sh::kTile >> 4;  // from one tile to the next, in a descriptor
-        auto scores = [&](int i) {  // S_i = Q_i K^T, both parts of K
-            if (elected()) {
-#pragma unroll
-                for (int part2 = 0; part2 < 2; ++part2)
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        constexpr auto at = [](int x) { return (uint32_t)((x >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
-                        tc_mma(tmem + 128 * i, q_desc + i * kStep + at(k), k_desc + part2 * kStep + at(k), kQk, part2 + k > 0);
-                    }
-                tc_commit(s_full + 8 * i);
-                if (i == TILES - 1) tc_commit(k_empty);
+#pragma unroll 1
+        for (int64_t tile = 0; ok && tile <= left && left > 0; ++tile) {
+            Codes k_then, v_then;
+            const bool here = place.block != nullptr;
+            if (tile < left) load(v_then, place, B::kV, B::kScaleV);
+            if (tile + 1 < left) {
+                place = next_place();
+                load(k_then, place, 0, B::kScaleK);
             }
-            __syncwarp();
+            if (tile < left) unpack_k((uint32_t)tile, k_now, here);
+            if (ok && tile > 0) {  // V of the tile before
+                if (tile > 1) ok = wait(v_empty, (uint32_t)tile - 2);
+                if (!ok) break;
+                unpack(v_now, smem + Sh::kV, 0u, std::false_type{});
+                fence_proxy_async_smem();
+                mbar_arrive(v_full);
+            }
+            k_now = k_then;
+            v_now = v_then;
+        }
+    } else {
+        // =============================== products of tile i: one thread issues ====
+        const int i = warp - Sh::kIssue;
+        constexpr uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
+        const uint32_t q_desc = tile_desc(smem + i * Sh::kTile, 16), k_desc = tile_desc(smem + Sh::kK, 16),
+                       v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
+        constexpr uint32_t kStep = Sh::kTile >> 4;  // from one tile to the next, in a descriptor
+        const uint32_t s_at = tmem + 128 * i, o_at = tmem + 128 * (TILES + i);
+        // The tiles' warps take turns: left alone they fall into step, and products and softmax of both alternate instead
+        // of overlapping (394 us against 3xx us).
+        uint32_t turns = 0;
+        auto my_turn = [&]() {
+            return TILES == 1 || (i == 0 && turns == 0) || wait(turn + 8 * i, i == 0 ? turns - 1 : turns);
         };
         while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);
             if (t0 < t1) {
 #pragma unroll 1
-                for (int tl = t0 - 1; tl < t1 && ok; ++tl) {  // products of tile tl, scores of the next
+                for (int tl = t0 - 1; tl < t1; ++tl) {  // products of tile tl, scores of the next
                     const bool values = tl >= t0, next = tl + 1 < t1;
-                    const uint32_t v_at = v_desc + (n & 1) * kStep;
-                    if (values) ok = wait(v_full + 8 * (n & 1), n >> 1);
-#pragma unroll 1
-                    for (int i = 0; i < TILES && ok; ++i) {
-                        ok = values ? wait(p_full + 8 * i, n) : wait(q_full + 8 * i, sn);
+                    if (values) {
+                        ok = wait(v_full, n) && wait(p_full + 8 * i, n) && my_turn();
                         if (!ok) break;
                         tc_after_sync();
-                        if (values) {
-                            if (elected()) {
+                        if (elected()) {  // O_i += P_i V
 #pragma unroll
-                                for (int k = 0; k < kPromptKeys / 16; ++k)
-                                    tc_mma_ts(tmem + 128 * (TILES + i), tmem + 128 * i + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
-                                if (i == TILES - 1) tc_commit(v_empty + 8 * (n & 1));
-                                if (!next) tc_commit(o_full + 8 * i);
-                            }
-                            __syncwarp();
+                            for (int k = 0; k < kPromptKeys / 16; ++k)
+                                tc_mma_ts(o_at, s_at + 8 * k, v_desc + k * (2048 >> 4), kPv, tl > t0 || k > 0);
+                            tc_commit(v_empty);
+                            if (!next) tc_commit(o_full + 8 * i);
                         }
-                        if (next) {
-                            if (i == 0) {
-                                ok = wait(k_full, values ? n + 1 : n);
-                                if (!ok) break;
-                                tc_after_sync();
-                            }
-                            scores(i);
-                        }
+                        __syncwarp();
+                        ++n;
+                    } else {
+                        ok = wait(q_full + 8 * i, sn) && my_turn();
                     }
-                    if (values) ++n;
+                    if (ok && next) {
+                        ok = wait(k_full + 8 * (n & 1), n >> 1);
+                        if (!ok) break;
+                        tc_after_sync();
+                        const uint32_t k_at = k_desc + (n & 1) * 2 * kStep;
+                        if (elected()) {  // S_i = Q_i K^T, both parts of K
+#pragma unroll
+                            for (int k = 0; k < 2 * (D / 16); ++k) {
+                                constexpr auto at = [](int x) { return (uint32_t)((x % (D / 16) >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
+                                tc_mma(s_at, q_desc + at(k), k_at + k / (D / 16) * kStep + at(k), kQk, k > 0);
+                            }
+                            tc_commit(s_full + 8 * i);
+                            tc_commit(k_empty + 8 * (n & 1));
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    ++turns;
+                    if (TILES == 2 && lane == 0) mbar_arrive(turn + 8 * (1 - i));
                 }
                 ++sn;
             }
-            if (seg.end >= r1) break;
+            if (!ok || seg.end >= r1) break;
             prompt_next<Sh::kRows>(p, seg);
         }
         // nothing is in flight when TMEM goes back
@@ -768,13 +800,13 @@ template <int D, int TILES>
 static rra_status_t prompt_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
     using Sh = PromptShape<D, TILES>;
     const void* k = (const void*)kv_attention_prompt_kernel<D, TILES>;
-    static_assert(1024 + Sh::kSums + 4 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 2048, "shared memory");
-    if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
+    static_assert(Sh::kSmem <= 227 * 1024 - 1024, "shared memory");
+    if (configure_cluster_kernel(k, Sh::kSmem) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
     void* args[] = {(void*)&p};
-    return serve_launch(k, dim3((unsigned)ctas), Sh::kThreads, Sh::smem(p.a.requests), 1, stream, args);
+    return serve_launch(k, dim3((unsigned)ctas), Sh::kThreads, Sh::kSmem, 1, stream, args);
 }
 
 size_t prefill_partial_bytes(int head_dim) {
