@@ -38,7 +38,7 @@ __device__ __forceinline__ bool attn_try(uint32_t bar, uint32_t parity) {
 }
 // The rest of a wait whose first try did not see the phase done.  Gives up after kAttnWaitNs, or soon after another wait
 // did, and says so in the status word.
-static __device__ __noinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity, AttnWorkspace* ws) {
+__device__ __forceinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity, AttnWorkspace* ws) {
     const uint64_t start = globaltimer_ns();
     while (!attn_try(bar, parity)) {
         const uint64_t waited = globaltimer_ns() - start;

@@ -51,10 +51,18 @@ struct PromptShape {
     static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
     // Warps: softmax (a warp reaches the TMEM lanes of its number modulo 4), then four that unpack, then one for each tile
     // that issues its products: one for both left the tensor cores idle for 300 to 500 cycles between products.
+    // Whole warpgroups, for the registers: a softmax thread holds all 128 scores of its row (read back from TMEM in two
+    // passes instead, their latency alone took 1200 cycles a tile).  The shares of a warpgroup's thread are those that
+    // the launch gives (65536 over all threads, a multiple of 8), taken from the issuing one for the softmax.
     static constexpr int kSoftmaxWarps = 4 * TILES;
     static constexpr int kUnpack = kSoftmaxWarps;
     static constexpr int kIssue = kUnpack + 4;
-    static constexpr int kWarps = kIssue + TILES;
+    static constexpr int kWarps = kIssue + 4;
+    static constexpr int kLaunchRegs = 65536 / (32 * kWarps) / 8 * 8;
+    static constexpr int kSoftmaxRegs = TILES == 2 ? 184 : 216;
+    static constexpr int kUnpackRegs = TILES == 2 ? 104 : 168;
+    static constexpr int kIssueRegs = TILES == 2 ? 40 : 120;
+    static_assert(TILES * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= (TILES + 2) * kLaunchRegs, "what the launch has");
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
     static constexpr int kPart = kPromptRows * (D + 2);      // floats of a part: rows in columns of 4 channels, statistics
@@ -80,6 +88,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, ui
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
                  : : "r"(d), "r"(a), "r"(b), "r"(desc), "r"(add ? 1 : 0), "r"(kTileDescHigh) : "memory");
+}
+// This warpgroup's registers a thread, from what it was launched with.
+template <int N, int FROM>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (N > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" : : "n"(N));
+    if constexpr (N < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" : : "n"(N));
 }
 // One lane of the warp, the same for every call.
 __device__ __forceinline__ bool elected() {
@@ -115,6 +129,13 @@ __device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* v) {
           "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
           "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(a)
         : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
 }
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t* v) {
     asm volatile(
@@ -184,7 +205,7 @@ struct PromptSegment {
     int64_t begin, end;
 };
 template <int kRows>
-__device__ __noinline__ void prompt_load(const AttnParams& p, PromptSegment& s) {
+__device__ __forceinline__ void prompt_load(const AttnParams& p, PromptSegment& s) {
     s.n = attn_lengths(p, s.b);
     s.chunks = prompt_chunks<kRows>(p, s.n);
     const PromptItem t = prompt_item<kRows>(p, s.n, s.c);
@@ -192,7 +213,7 @@ __device__ __noinline__ void prompt_load(const AttnParams& p, PromptSegment& s) 
     s.end = s.begin + t.tiles + kPromptSegmentCost;
 }
 template <int kRows>
-__device__ __noinline__ void prompt_next(const AttnParams& p, PromptSegment& s) {
+__device__ __forceinline__ void prompt_next(const AttnParams& p, PromptSegment& s) {
     s.begin = s.end;
     if (++s.c >= s.chunks) {
         s.c = 0;
@@ -352,6 +373,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     bool ok = true;
     if (warp < Sh::kSoftmaxWarps) {
         // =============================== softmax: a thread has a row ====
+        set_registers<Sh::kSoftmaxRegs, Sh::kLaunchRegs>();
         const int i = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
         const uint32_t s_at = lanes + 128 * i, o_at = lanes + 128 * (TILES + i);
@@ -410,33 +432,26 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     const volatile uint32_t* const words = seen_words[n & 3];
                     const bool whole = __all_sync(0xffffffffu, key0 >= lo && key0 + kPromptKeys <= hi) &&
                                        (words[0] & words[1] & words[2] & words[3]) == 0xffffffffu;
-                    // ---- the row's largest score; scores that it does not see go back as -inf ----
-                    float top = -FLT_MAX;
-                    auto largest = [&](int q, uint32_t* v) {
-                        if (!whole) {
+                    uint32_t v[128];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_ld32(s_at + 32 * q, v + 32 * q);
+                    tc_wait_ld();
+                    if (!whole) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
                             // keys lo..hi of these 32, as bits, and of them those that are there
                             const int from = min(max(lo - key0 - 32 * q, 0), 32), to = min(max(hi - key0 - 32 * q, 0), 32);
                             const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
                             const uint32_t mask = words[q] & below & (from == 32 ? 0u : 0xffffffffu << from);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = mask >> k & 1u ? v[k] : 0xff800000u;
-                            tc_st32(s_at + 32 * q, v);
+                            for (int k = 0; k < 32; ++k) v[32 * q + k] = mask >> k & 1u ? v[32 * q + k] : 0xff800000u;
                         }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                    };
-                    uint32_t v0[32], v1[32];  // 32 columns in hand, 32 on their way
-                    tc_ld32(s_at, v0);
-#pragma unroll 1
-                    for (int q = 0; q < 4; q += 2) {
-                        tc_wait_ld();
-                        tc_ld32(s_at + 32 * (q + 1), v1);
-                        largest(q, v0);
-                        tc_wait_ld();
-                        if (q == 0) tc_ld32(s_at + 64, v0);
-                        largest(q + 1, v1);
                     }
-                    if (!whole) tc_wait_st();
+                    float tops[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll
+                    for (int k = 0; k < 128; k += 2)
+                        tops[k >> 1 & 3] = fmaxf(tops[k >> 1 & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     if (__any_sync(0xffffffffu, top > limit)) {  // a maximum moves: scale what was summed
                         const float now = top > limit ? top : m;
                         const float by = exp2_fast((m - now) * factor);
@@ -445,43 +460,34 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                         l *= by;
                         if (tl > t0) {
 #pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t v[32];
-                                tc_ld32(o_at + 32 * q, v);
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tc_ld16(o_at + 16 * q, o);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * by);
-                                tc_st32(o_at + 32 * q, v);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                                tc_st16(o_at + 16 * q, o);
                             }
                         }
                     }
-                    // ---- weights, over scores already read ----
+                    // ---- weights, where the scores were ----
                     const uint64_t off = pair2(-m, -m);
-                    uint64_t sum2 = pair2(0.f, 0.f);
-                    auto weigh = [&](int q, uint32_t* v) {
+                    uint64_t sums[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int k = 64 * q; k < 64 * q + 64; k += 2) {
                             float e0, e1;
                             split2(mul2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), off), factor2), e0, e1);
                             e0 = exp2_fast(e0);
                             e1 = exp2_fast(e1);
-                            sum2 = add2(sum2, pair2(e0, e1));
+                            sums[k >> 1 & 1] = add2(sums[k >> 1 & 1], pair2(e0, e1));
                             v[k / 2] = pack_half2(e0, e1);
                         }
-                        tc_st16(s_at + 16 * q, v);
-                    };
-                    tc_ld32(s_at, v0);
-#pragma unroll 1
-                    for (int q = 0; q < 4; q += 2) {
-                        tc_wait_ld();
-                        tc_ld32(s_at + 32 * (q + 1), v1);
-                        weigh(q, v0);
-                        tc_wait_ld();
-                        if (q == 0) tc_ld32(s_at + 64, v0);
-                        weigh(q + 1, v1);
+                        tc_st32(s_at + 32 * q, v + 32 * q);
                     }
                     float a0, a1;
-                    split2(sum2, a0, a1);
+                    split2(add2(sums[0], sums[1]), a0, a1);
                     l += a0 + a1;
                     tc_wait_st();
                     tc_before_sync();
@@ -591,6 +597,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         }
     } else if (warp < Sh::kIssue) {
         // =============================== unpacking: a thread has a key ====
+        set_registers<Sh::kUnpackRegs, Sh::kLaunchRegs>();
         const int unpacker = warp - Sh::kUnpack, key_in = 32 * unpacker + lane;
         const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
         constexpr int kLoads = D / 32;  // 16-byte loads of a row of codes
@@ -726,7 +733,9 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         }
     } else {
         // =============================== products of tile i: one thread issues ====
+        set_registers<Sh::kIssueRegs, Sh::kLaunchRegs>();
         const int i = warp - Sh::kIssue;
+        ok = i < TILES;  // the warpgroup's other warps have nothing to do
         constexpr uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
         const uint32_t q_desc = tile_desc(smem + i * Sh::kTile, 16), k_desc = tile_desc(smem + Sh::kK, 16),
                        v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
@@ -786,9 +795,11 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             prompt_next<Sh::kRows>(p, seg);
         }
         // nothing is in flight when TMEM goes back
-        if (elected()) tc_commit(drained);
-        __syncwarp();
-        wait(drained, 0);
+        if (i < TILES) {
+            if (elected()) tc_commit(drained);
+            __syncwarp();
+            wait(drained, 0);
+        }
     }
     tc_before_sync();
     __syncthreads();
@@ -805,6 +816,12 @@ static rra_status_t prompt_launch(const AttnParams& p, int ctas, rra_stream_t st
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
+    // The shares of the registers are of what the launch has: a build that launches with fewer would wait for them forever.
+    static const bool enough = [k] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, k) == cudaSuccess && f.numRegs == Sh::kLaunchRegs;
+    }();
+    if (!enough) return RRA_ERR_CUDA;
     void* args[] = {(void*)&p};
     return serve_launch(k, dim3((unsigned)ctas), Sh::kThreads, Sh::kSmem, 1, stream, args);
 }
