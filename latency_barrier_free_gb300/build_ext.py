@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "librra.so")
+NATIVE = os.path.join(HERE, "_serve.so")  # the Python binding of rra_serve.h
 
 SOURCES = ["kernels.cu", "cluster.cu", "coll.cu", "fused.cu", "rra_api.cu", "probes.cu", "rra_static.cu", "serve.cu",
            "serve_attn.cu", "serve_prefill.cu"]
@@ -37,16 +39,26 @@ def nvcc() -> str:
 
 
 def _newest_input() -> float:
-    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["serve_bind.c"]]
     files += [os.path.join(INCLUDE, f) for f in PUBLIC_HEADERS]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_native() -> None:
+    tmp = NATIVE + ".tmp%d" % os.getpid()
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "serve_bind.c"), "-o", tmp, "-ldl"]
+    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if p.returncode != 0:
+        raise RuntimeError("gcc failed on serve_bind.c\n" + p.stdout.decode(errors="replace"))
+    os.replace(tmp, NATIVE)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link; returns the path of librra.so.  Skips work when the
     library is newer than every source."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _newest_input() for f in (LIB, NATIVE)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -69,6 +81,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(text, file=sys.stderr)
     if errors:
         raise RuntimeError("nvcc failed\n" + "\n".join(errors))
+    _build_native()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)

@@ -499,3 +499,51 @@ def test_attention_of_many_requests(serve, max_q):
     for b in list(range(0, n, 37)) + [17, n - 1]:
         want, _, mean, dots = ref.attention(qn[b:b + 1], kn[at[b]:at[b + 1]], vn[at[b]:at[b + 1]], int(kv[b]), d ** -0.5, True, 0)
         check_out(got[b:b + 1], want, mean, dots, d, int(kv[b]))
+
+
+# -------------------------------------------------- the binding's refusals --
+def test_binding_refuses_what_does_not_fit(serve):
+    """Wrong types, shapes, strides and places raise before anything is launched."""
+    from latency_barrier_free_gb300 import rra
+
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    cache = cache_of(serve, 4, 16, 2, 64)
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    good = [bf(3, 2, 64), bf(3, 2, 64), slots]
+    cache.append(*good)
+    for n, bad in ((0, bf(3, 2, 32)), (0, bf(2, 2, 64)), (1, bf(3, 2, 64).float()), (0, bf(3, 2, 64).cpu()),
+                   (0, bf(3, 64, 2).transpose(1, 2)), (2, i32(3)), (2, slots.cpu()), (1, bf(6, 64)), (2, slots.expand(3, 3)[:, 1])):
+        args = list(good)
+        args[n] = bad
+        with pytest.raises(ValueError):
+            cache.append(*args)
+    with pytest.raises(TypeError):
+        cache.append(bf(3, 2, 64).double(), bf(3, 2, 64), slots)
+    with pytest.raises(rra.RraError):  # a stride that is no multiple of 16 bytes
+        cache.append(bf(3, 2 * 64 + 1)[:, :128].view(3, 2, 64), good[1], slots)
+    q, table, cu, kv = bf(2, 4, 64), i32(2, 3), i32(3), i32(2)
+    kw = dict(max_q=1, max_kv=8)
+    cache.attention(q, bf(2, 4, 64), cu, kv, table, **kw)
+    for args, more in (((q, bf(2, 4, 32), cu, kv, table), {}), ((bf(2, 3, 64), bf(2, 3, 64), cu, kv, table), {}),
+                       ((q, q.float(), cu, kv, table), {}), ((q, bf(2, 4, 64), i32(2), kv, table), {}),
+                       ((q, bf(2, 4, 64), cu, kv, i32(3, 3)), {}), ((q, bf(2, 4, 64), cu, kv, table.t()), {}),
+                       ((q, bf(2, 4, 64), cu, kv.long(), table), {}), ((q, bf(2, 4, 64), cu, kv, table), {"lse": bf(2, 4)}),
+                       ((q, bf(2, 4, 64), cu, kv, table), {"lse": torch.zeros(7, device="cuda")})):
+        with pytest.raises(ValueError):
+            cache.attention(*args, **kw, **more)
+    with pytest.raises(rra.RraError):
+        cache.attention(q, bf(2, 4, 64), cu, kv, table, max_q=-1, max_kv=8)
+    k, c = bf(2, 1, 64), torch.zeros(9, 32, device="cuda")
+    ok = [q, k, None, bf(64), c, c, i32(2), bf(2, 4, 64), bf(2, 1, 64)]
+    serve.qk_norm_rope(*ok)
+    for n, bad in ((1, bf(3, 1, 64)), (2, bf(63)), (3, bf(64).float()), (4, torch.zeros(8, 32, device="cuda")), (6, i32(1)),
+                   (6, slots), (7, bf(2, 3, 64)), (8, bf(2, 1, 64).cpu()), (5, c.cpu())):
+        args = list(ok)
+        args[n] = bad
+        with pytest.raises(ValueError):
+            serve.qk_norm_rope(*args)
+    with pytest.raises(ValueError):
+        serve.KvCache(torch.zeros(100, dtype=torch.uint8, device="cuda"), 16, 2, 64)
+    assert cache.plan_kernel(8, 1, max_q=1, max_kv=10) == "kv_attention_kernel<8 rows>"
+    assert cache.status() == 0
