@@ -21,8 +21,8 @@
 namespace rra {
 
 constexpr int kAttnTile = 32;      // keys of one step of a warp
-constexpr int kAttnMinRun = 2;     // tiles a warp takes at least
-constexpr int kAttnSegmentCost = 2;  // what starting and ending a segment costs, in tiles
+constexpr int kAttnMinRun = 1;     // tiles a warp takes at least
+constexpr int kAttnSegmentCost = 4;  // what starting and ending a segment costs, in tiles
 constexpr float kAttnSlack = 4.f;  // log2 of how far weights may pass 1 before the maximum moves
 
 
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     __syncthreads();
     // Little work is spread over the SMs first, four warps each: a warp that shares its scheduler takes longer for
     // a tile, and the smallest batches are all latency.
-    int64_t run = kAttnMinRun + kAttnSegmentCost;
+    int64_t run = kAttnMinRun;
     int warps = kWarps;
     if (total <= run * 4 * (int64_t)gridDim.x) {
         warps = 4;
@@ -653,47 +653,49 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         const AttnPiece pc = pieces[lead];
         if (pc.begin >= cta0 && pc.end <= cta1) continue;
         const int i0 = (int)(pc.begin / cta_run), i1 = (int)((pc.end - 1) / cta_run);
-        __threadfence();
         __syncthreads();
-        if (tid == 0) is_last = atomicAdd(&ws->arrived[i0], 1u) == (uint32_t)(i1 - i0) ? 1u : 0u;
+        if (tid == 0) {
+            __threadfence();  // of the whole CTA's part: the barrier comes before it
+            is_last = atomicAdd(&ws->arrived[i0], 1u) == (uint32_t)(i1 - i0) ? 1u : 0u;
+            __threadfence();
+        }
         __syncthreads();
         if (is_last == 0u) continue;
-        __threadfence();
         const AttnRequest rq = attn_request<kRows>(p, pc.b);
-        // the parts' maxima and sums go where the pieces were
         constexpr int64_t kStep = 2 * Sh::kPartial;
         const float* const base = partials + (int64_t)i0 * kStep;
         const int parts = i1 - i0 + 1;
-        float2* const stats = (float2*)smem;  // [parts][kRows]: maximum, sum
-        static_assert(kAttnMaxCtas * kRows * 8 <= Sh::kRing + Sh::kHeads, "statistics fit");
-        auto part_at = [&](int x) { return base + x * kStep + (x == 0 ? Sh::kPartial : 0); };
-        for (int x = tid; x < parts * kRows; x += Sh::kThreads)
-            stats[x] = __ldcg((const float2*)(part_at(x / kRows) + 2 * (x % kRows)));
-        __syncthreads();
         for (int i = tid; i < kItems; i += Sh::kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             const int row = pc.c * kRows + r;
             if (row >= rq.qn * p.group) continue;
             float top = -FLT_MAX, sum = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 16;
+            constexpr int kAhead = 20;  // parts in flight: a round trip to L2 each otherwise
 #pragma unroll 1
             for (int x0 = 0; x0 < parts; x0 += kAhead) {
+                float2 st[kAhead];
                 float4 v[kAhead];
+                const float* src = base + x0 * kStep + (x0 == 0 ? Sh::kPartial : 0);
 #pragma unroll
-                for (int x = 0; x < kAhead; ++x)
-                    if (x0 + x < parts) v[x] = __ldcg((const float4*)(part_at(x0 + x) + 2 * kRows + r * D + d));
+                for (int x = 0; x < kAhead; ++x) {
+                    st[x] = make_float2(-FLT_MAX, 0.f);
+                    v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x0 + x < parts) {
+                        st[x] = __ldcg((const float2*)(src + 2 * r));
+                        v[x] = __ldcg((const float4*)(src + 2 * kRows + r * D + d));
+                    }
+                    src += x0 + x == 0 ? kStep - Sh::kPartial : kStep;
+                }
                 float now = top;
 #pragma unroll
-                for (int x = 0; x < kAhead; ++x)
-                    if (x0 + x < parts) now = fmaxf(now, stats[(x0 + x) * kRows + r].x);
+                for (int x = 0; x < kAhead; ++x) now = fmaxf(now, st[x].x);
                 const float keep = exp2_fast(top - now);
                 top = now;
                 sum *= keep;
                 o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-                for (int x = 0; x < kAhead; ++x)
-                    if (x0 + x < parts) attn_add(top, sum, o, stats[(x0 + x) * kRows + r], v[x]);
+                for (int x = 0; x < kAhead; ++x) attn_add(top, sum, o, st[x], v[x]);
             }
             float inv;
             __nv_bfloat16* const to = attn_row(p, rq.q0, pc.h, row, top, sum, d == 0, inv);
@@ -771,7 +773,7 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     p.room = args->table_pages * args->cache.page_tokens;
     p.window = std::min(args->window, 1 << 30);
     const int64_t rows = (int64_t)std::max(args->max_q, 1) * p.group;
-    if (rows > 32) return rra::launch_prefill(p, sms, stream);
+    if (rows > 48) return rra::launch_prefill(p, sms, stream);
     const int ctas = std::min(sms, rra::kAttnMaxCtas);
     if (args->cache.head_dim == 128)
         return rows <= 8 ? rra::attn_launch<128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 2>(p, ctas, stream);
