@@ -15,6 +15,7 @@
 // have a piece only; those are joined once, at the end of the CTA, and across
 // CTAs by whichever finishes last, in the order of the runs.
 #include <algorithm>
+#include <cmath>
 
 #include "serve_attn.cuh"
 
@@ -76,8 +77,7 @@ struct AttnRequest {
     int32_t chunks;       // segments of a KV head
 };
 template <int kRows>
-__device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int b) {
-    const AttnLengths n = attn_lengths(p, b);
+__device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, const AttnLengths& n) {
     AttnRequest r;
     r.q0 = n.q0;
     r.qn = n.qn;
@@ -95,8 +95,9 @@ struct AttnSegment {
     int32_t b, h, c;
     int64_t begin, end;
 };
+// `known`: the first requests' lengths, n of them, in shared memory.
 template <int kRows>
-__device__ __noinline__ void attn_next(const AttnParams& p, AttnSegment& s) {  // out of line: once a segment, in two places
+__device__ __noinline__ void attn_next(const AttnParams& p, const AttnLengths* known, int n, AttnSegment& s) {  // out of line: once a segment, in two places
     if (++s.c >= s.r.chunks) {
         s.c = 0;
         if (++s.h == p.a.cache.kv_heads) {
@@ -106,7 +107,7 @@ __device__ __noinline__ void attn_next(const AttnParams& p, AttnSegment& s) {  /
                     s.begin = s.end = INT64_MAX;
                     return;
                 }
-                s.r = attn_request<kRows>(p, s.b);
+                s.r = attn_request<kRows>(p, s.b < n ? known[s.b] : attn_lengths(p, s.b));
             } while (s.r.chunks == 0);
         }
     }
@@ -114,10 +115,16 @@ __device__ __noinline__ void attn_next(const AttnParams& p, AttnSegment& s) {  /
     s.end += s.r.tiles + kAttnSegmentCost;
 }
 
+// x / y, which fits 32 bits; mostly x does too, and then the division is a short one.
+__device__ __forceinline__ int quotient(int64_t x, int64_t y) {
+    if (((uint64_t)x | (uint64_t)y) >> 32 == 0) return (int)((uint32_t)x / (uint32_t)y);
+    return (int)(x / y);
+}
+
 // What a warp, or a CTA, has of a segment that others share.
 struct AttnPiece {
-    int32_t b, h, c;
-    int32_t flags;       // kHas, kStarts, kEnds
+    int32_t q0, rows, h, c;  // the request's first query token and number of rows
+    int32_t flags;           // kHas, kStarts, kEnds
     int64_t begin, end;  // the whole segment
 };
 enum { kHas = 1, kStarts = 2, kEnds = 4 };
@@ -155,6 +162,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t warp_sum[kWarps];
     __shared__ AttnPiece pieces[2 * kWarps];
+    __shared__ AttnLengths known[Sh::kThreads];
+    __shared__ float2 joined[2 * kWarps][kRows];  // maximum and sum of a chain's rows
     __shared__ uint32_t is_last;
     const rra_kv_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -186,7 +195,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         const int b = b0 + tid;
         int64_t v = 0;
         if (b < a.requests) {
-            const AttnRequest r = attn_request<kRows>(p, b);
+            const AttnLengths n = attn_lengths(p, b);
+            if (b0 == 0) known[tid] = n;
+            const AttnRequest r = attn_request<kRows>(p, n);
             v = (int64_t)(r.tiles + kAttnSegmentCost) * r.chunks * a.cache.kv_heads;
         }
         int64_t inc = v;
@@ -234,9 +245,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 else high = mid;
             }
             seg.b = low;
-            seg.r = attn_request<kRows>(p, low);
+            seg.r = attn_request<kRows>(p, low < Sh::kThreads ? known[low] : attn_lengths(p, low));
             const int each = seg.r.tiles + kAttnSegmentCost;
-            const int i = (int)((r0 - sums[low]) / each);
+            const int i = quotient(r0 - sums[low], each);
             seg.h = i / seg.r.chunks;
             seg.c = i - seg.h * seg.r.chunks;
             seg.begin = sums[low] + (int64_t)i * each;
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             for (int n = 0; n < NT; ++n) {
                 const int row = seg.c * kRows + 8 * n + g;
                 const bool live = row < seg.r.qn * p.group && first_tile(seg) < end_tile(seg);
-                const int i = row / p.group;
+                const int i = p.by_group(row);
                 const __nv_bfloat16* x = (const __nv_bfloat16*)a.q + (seg.r.q0 + i) * a.q_token_stride +
                                          (seg.h * p.group + row - i * p.group) * a.q_head_stride;
 #pragma unroll
@@ -285,7 +296,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             if (held >= held_end) {
                 while (next >= from_end) {
                     if (from.end >= r1) return;
-                    attn_next<kRows>(p, from);
+                    attn_next<kRows>(p, known, Sh::kThreads, from);
                     next = first_tile(from);
                     from_end = end_tile(from);
                 }
@@ -294,7 +305,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 src0 = src1 = nullptr;
                 auto place = [&](int k) -> const char* {
                     if (next + lane >= from_end || k >= from.r.kv) return nullptr;
-                    const int i = k / ps, page = row[i];
+                    const int i = p.by_page(k), page = row[i];
                     if (page < 0 || page >= a.cache.num_pages) return nullptr;
                     return (const char*)a.cache.pages +
                            (((int64_t)page * a.cache.kv_heads + from.h) * blocks + (k - i * ps) / kKvBlockTokens) * B::kBytes;
@@ -378,7 +389,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     const int r = seg.c * kRows + 8 * n + 2 * t + k;
                     int lo = 0, hi = 0;
                     if (r < rows) {
-                        const int pos = seg.r.kv - seg.r.qn + r / p.group;
+                        const int pos = seg.r.kv - seg.r.qn + p.by_group(r);
                         hi = a.causal ? max(0, min(seg.r.kv, pos + 1)) : seg.r.kv;
                         lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
                         all_first = max(all_first, lo);
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 __syncwarp();
                 if (lane == 0)
                     pieces[2 * warp + which] =
-                        AttnPiece{seg.b, seg.h, seg.c, kHas | (starts ? kStarts : 0) | (ends ? kEnds : 0), seg.begin, seg.end};
+                        AttnPiece{seg.r.q0, rows, seg.h, seg.c, kHas | (starts ? kStarts : 0) | (ends ? kEnds : 0), seg.begin, seg.end};
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -596,7 +607,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     }
                 }
             if (seg.end >= r1) break;
-            attn_next<kRows>(p, seg);
+            attn_next<kRows>(p, known, Sh::kThreads, seg);
             load_queries();
         }
         if (dead) drain();  // copies in flight at this point: none, or those that a wait gave up on
@@ -611,36 +622,62 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     if (has == 0u) return;
     const uint32_t leads = __ballot_sync(0xffffffffu, (my_flags & kStarts) != 0) | (has & -has);
     const int chains = __popc(leads);
+    auto chain_of = [&](int lead) {
+        const uint32_t later = leads & ~((2u << lead) - 1u);
+        return has & ~((1u << lead) - 1u) & (later != 0u ? (later & -later) - 1u : 0xffffffffu);
+    };
+    // A warp takes a row, a lane a piece: a piece's maximum becomes its weight.
+    for (int r = warp; r < kRows; r += kWarps) {
+        float* const mine = piece_at(lane >> 1, lane & 1) + 2 * r;
+        const float2 st = has >> lane & 1u ? *(const float2*)mine : make_float2(-FLT_MAX, 0.f);
+#pragma unroll 1
+        for (uint32_t left = leads; left != 0u; left &= left - 1u) {
+            const int lead = __ffs((int)left) - 1;
+            const bool in = chain_of(lead) >> lane & 1u;
+            float top = in ? st.x : -FLT_MAX;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float by = exp2_fast(st.x - top);
+            float sum = in ? st.y * by : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (in) *mine = by;
+            if (lane == lead) joined[lead][r] = make_float2(top, sum);
+        }
+    }
+    __syncthreads();
     for (int item = tid; item < chains * kItems; item += Sh::kThreads) {
         const int i = item % kItems;
         uint32_t left = leads;
         for (int skip = item / kItems; skip > 0; --skip) left &= left - 1u;
         const int lead = __ffs((int)left) - 1;
-        const uint32_t later = leads & ~((2u << lead) - 1u);
-        const uint32_t chain = has & ~((1u << lead) - 1u) & (later != 0u ? (later & -later) - 1u : 0xffffffffu);
+        const uint32_t chain = chain_of(lead);
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float top = -FLT_MAX, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (uint32_t x = chain; x != 0u; x &= x - 1u) top = fmaxf(top, piece_at((__ffs((int)x) - 1) >> 1, (__ffs((int)x) - 1) & 1)[2 * r]);
-#pragma unroll 1
+#pragma unroll 4
         for (uint32_t x = chain; x != 0u; x &= x - 1u) {
-            const float* const src = piece_at((__ffs((int)x) - 1) >> 1, (__ffs((int)x) - 1) & 1);
-            attn_add(top, sum, o, *(const float2*)(src + 2 * r), *(const float4*)(src + 2 * kRows + r * D + d));
+            const int at = __ffs((int)x) - 1;
+            const float* const src = piece_at(at >> 1, at & 1);
+            const float by = src[2 * r];
+            const float4 v = *(const float4*)(src + 2 * kRows + r * D + d);
+            o.x = fmaf(v.x, by, o.x);
+            o.y = fmaf(v.y, by, o.y);
+            o.z = fmaf(v.z, by, o.z);
+            o.w = fmaf(v.w, by, o.w);
         }
+        const float2 st = joined[lead][r];
         const int starts = pieces[lead].flags & kStarts, ends = pieces[31 - __clz((int)chain)].flags & kEnds;
         if (starts && ends) {
-            const AttnRequest rq = attn_request<kRows>(p, pieces[lead].b);
             const int row = pieces[lead].c * kRows + r;
-            if (row < rq.qn * p.group) {
+            if (row < pieces[lead].rows) {
                 float inv;
-                __nv_bfloat16* const to = attn_row(p, rq.q0, pieces[lead].h, row, top, sum, d == 0, inv);
+                __nv_bfloat16* const to = attn_row(p, pieces[lead].q0, pieces[lead].h, row, st.x, st.y, d == 0, inv);
                 attn_store(to + d, o, inv);
             }
         } else {
             float* const dst = partials + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * Sh::kPartial;
             *(float4*)(dst + 2 * kRows + r * D + d) = o;
-            if (d == 0) *(float2*)(dst + 2 * r) = make_float2(top, sum);
+            if (d == 0) *(float2*)(dst + 2 * r) = st;
         }
     }
 
@@ -652,7 +689,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         if (turn == 1 && chains == 1) break;
         const AttnPiece pc = pieces[lead];
         if (pc.begin >= cta0 && pc.end <= cta1) continue;
-        const int i0 = (int)(pc.begin / cta_run), i1 = (int)((pc.end - 1) / cta_run);
+        const int i0 = quotient(pc.begin, cta_run), i1 = quotient(pc.end - 1, cta_run);
         __syncthreads();
         if (tid == 0) {
             __threadfence();  // of the whole CTA's part: the barrier comes before it
@@ -661,14 +698,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         }
         __syncthreads();
         if (is_last == 0u) continue;
-        const AttnRequest rq = attn_request<kRows>(p, pc.b);
         constexpr int64_t kStep = 2 * Sh::kPartial;
         const float* const base = partials + (int64_t)i0 * kStep;
         const int parts = i1 - i0 + 1;
         for (int i = tid; i < kItems; i += Sh::kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             const int row = pc.c * kRows + r;
-            if (row >= rq.qn * p.group) continue;
+            if (row >= pc.rows) continue;
             float top = -FLT_MAX, sum = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             constexpr int kAhead = 20;  // parts in flight: a round trip to L2 each otherwise
@@ -698,7 +734,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 for (int x = 0; x < kAhead; ++x) attn_add(top, sum, o, st[x], v[x]);
             }
             float inv;
-            __nv_bfloat16* const to = attn_row(p, rq.q0, pc.h, row, top, sum, d == 0, inv);
+            __nv_bfloat16* const to = attn_row(p, pc.q0, pc.h, row, top, sum, d == 0, inv);
             attn_store(to + d, o, inv);
         }
         if (tid == 0) ws->arrived[i0] = 0u;
@@ -710,7 +746,7 @@ template <int D, int NT, int kWarps, int kStages>
 static rra_status_t attn_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
     using Sh = AttnShape<D, NT, kWarps, kStages>;
     const void* k = (const void*)kv_attention_kernel<D, NT, kWarps, kStages>;
-    static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 2048, "shared memory");
+    static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 10240, "shared memory");
     if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
@@ -738,6 +774,29 @@ static bool attn_args_ok(const rra_kv_attention_args_t* a) {
            (a->block_table != nullptr || a->table_pages == 0) && a->workspace != nullptr;
 }
 
+// Which kernel: the one with the shortest time by what was measured of each, for the sizes that the caller expects (every
+// kernel is right for every call).  Times in microseconds, work in tiles of the busiest of 152 SMs:
+//   8 or 16 rows     8.5 or 11 + a chunk's tiles of 32 keys at 0.125 or 0.2 (head_dim 128), 0.085 or 0.135 (64)
+//   128 or 256 rows  8 or 11 + tiles of 128 keys at 2.7 or 3.2, 1.9 or 2.0, + joining the parts of a segment, 2 or 1.1 each
+// (e.g. 8 requests, 64 heads over 8 of 128, 4096 keys: 4 queries 38.6, 34.6, 54.8, 64.8 us; 8: 67, 56, 55, 66; 32: 223, 180,
+// 79, 74; 32768 keys, 64 queries: 3246, 2462, 1084, 690.)
+enum AttnKernel { kRows8, kRows16, kPrompt128, kPrompt256 };
+static AttnKernel attn_kernel_of(const rra_kv_attention_args_t& a) {
+    const bool big = a.cache.head_dim == 128;
+    const double sms = 152;
+    const double rows = (double)std::max(a.max_q, 1) * (a.q_heads / a.cache.kv_heads);
+    const double seen = a.window > 0 ? std::min((double)a.max_kv, (double)a.window + a.max_q) : (double)a.max_kv;
+    const double heads = (double)std::max(a.requests, 1) * a.cache.kv_heads;
+    auto chunks = [&](double n) { return std::ceil(rows / n); };
+    auto few = [&](double n, double fixed, double tile) { return fixed + heads * chunks(n) * (std::ceil(seen / kAttnTile) + kAttnSegmentCost) / sms * tile; };
+    auto many = [&](double n, double fixed, double tile) {
+        const double tiles = std::ceil(seen / 128), run = std::max(6.0, heads * chunks(n) * (tiles + 2) / sms);
+        return fixed + (heads * chunks(n) <= sms ? std::min(tiles, run) : run) * tile + (tiles > run ? tiles / run * (big ? 2 : 1.1) : 0);
+    };
+    const double t[4] = {few(8, 8.5, big ? 0.125 : 0.085), few(16, 11, big ? 0.2 : 0.135), many(128, 8, big ? 2.7 : 1.9), many(256, 11, big ? 3.2 : 2.0)};
+    return (AttnKernel)(std::min_element(t, t + 4) - t);
+}
+
 }  // namespace rra
 
 extern "C" {
@@ -750,10 +809,9 @@ size_t rra_kv_attention_workspace_bytes(int head_dim) {
 
 rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
     if (name == nullptr || !rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
-    const int64_t rows = (int64_t)std::max(args->max_q, 1) * (args->q_heads / args->cache.kv_heads);
-    *name = rows <= 8    ? "kv_attention_kernel<8 rows>"
-            : rows <= 32 ? "kv_attention_kernel<16 rows>"
-                         : "kv_attention_prompt_kernel";
+    static const char* const names[] = {"kv_attention_kernel<8 rows>", "kv_attention_kernel<16 rows>",
+                                        "kv_attention_prompt_kernel<128 rows>", "kv_attention_prompt_kernel<256 rows>"};
+    *name = names[rra::attn_kernel_of(*args)];
     return RRA_OK;
 }
 
@@ -770,14 +828,17 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     p.a = *args;
     p.scale_log2 = (float)(args->scale * 1.4426950408889634);
     p.group = args->q_heads / args->cache.kv_heads;
+    p.by_group = rra::Divisor(p.group);
+    p.by_page = rra::Divisor(args->cache.page_tokens);
     p.room = args->table_pages * args->cache.page_tokens;
     p.window = std::min(args->window, 1 << 30);
-    const int64_t rows = (int64_t)std::max(args->max_q, 1) * p.group;
-    if (rows > 48) return rra::launch_prefill(p, sms, stream);
+    const rra::AttnKernel kernel = rra::attn_kernel_of(*args);
+    if (kernel == rra::kPrompt128 || kernel == rra::kPrompt256)
+        return rra::launch_prefill(p, kernel == rra::kPrompt256 ? 2 : 1, sms, stream);
     const int ctas = std::min(sms, rra::kAttnMaxCtas);
     if (args->cache.head_dim == 128)
-        return rows <= 8 ? rra::attn_launch<128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 2>(p, ctas, stream);
-    return rows <= 8 ? rra::attn_launch<64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<64, 2, 8, 4>(p, ctas, stream);
+        return kernel == rra::kRows8 ? rra::attn_launch<128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 2>(p, ctas, stream);
+    return kernel == rra::kRows8 ? rra::attn_launch<64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<64, 2, 8, 4>(p, ctas, stream);
 }
 
 }  // extern "C"

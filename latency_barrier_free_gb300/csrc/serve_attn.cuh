@@ -55,6 +55,7 @@ struct AttnParams {
     rra_kv_attention_args_t a;
     float scale_log2;
     int32_t group;   // query heads of a KV head
+    Divisor by_group, by_page;
     int32_t room;    // keys that a row of the table has pages for
     int32_t window;  // a.window, at most 2^30
 };
@@ -72,7 +73,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ __nv_bfloat16* attn_row(const AttnParams& p, int q0, int h, int row, float top, float sum,
                                                    bool with_lse, float& inv) {
     const rra_kv_attention_args_t& a = p.a;
-    const int i = row / p.group, head = h * p.group + row - i * p.group;
+    const int i = p.by_group(row), head = h * p.group + row - i * p.group;
     const int64_t token = q0 + i;
     inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: 0
     if (with_lse && a.lse != nullptr) a.lse[token * a.q_heads + head] = (top + log2f(sum)) * 0.693147180559945309f;
@@ -108,8 +109,8 @@ __device__ __forceinline__ void attn_row_scale(const AttnParams& p, float most, 
     if (factor == 0.f) factor = 1.f, down = 0.f;  // every score is 0
 }
 
-// Prompts (serve_prefill.cu).
-rra_status_t launch_prefill(const AttnParams& p, int sms, rra_stream_t stream);
+// Prompts (serve_prefill.cu): `tiles` (1 or 2) of 128 rows a CTA.
+rra_status_t launch_prefill(const AttnParams& p, int tiles, int sms, rra_stream_t stream);
 size_t prefill_partial_bytes(int head_dim);
 
 }  // namespace rra

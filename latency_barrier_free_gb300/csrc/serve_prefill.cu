@@ -186,8 +186,8 @@ struct PromptItem {
 template <int kRows>
 __device__ __forceinline__ PromptItem prompt_item(const AttnParams& p, const AttnLengths& n, int c) {
     const int rows = n.qn * p.group, last = min(rows, (c + 1) * kRows) - 1;
-    const int end = p.a.causal ? max(0, n.kv - n.qn + last / p.group + 1) : n.kv;
-    const int first = p.window > 0 ? max(0, n.kv - n.qn + c * kRows / p.group - p.window + 1) : 0;
+    const int end = p.a.causal ? max(0, n.kv - n.qn + p.by_group(last) + 1) : n.kv;
+    const int first = p.window > 0 ? max(0, n.kv - n.qn + p.by_group(c * kRows) - p.window + 1) : 0;
     PromptItem t;
     t.first_tile = first / kPromptKeys;
     t.tiles = max(1, (end + kPromptKeys - 1) / kPromptKeys - t.first_tile);
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 int lo = 0, hi = 0;
                 {
                     uint4 x[D / 8];
-                    const int tok = live ? r / p.group : 0;
+                    const int tok = live ? p.by_group(r) : 0;
                     if (live) {
                         const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (seg.n.q0 + tok) * a.q_token_stride +
                                                    (seg.h * p.group + r - tok * p.group) * a.q_head_stride;
@@ -554,8 +554,11 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     auto part_of = [&](int x) {
                         return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPart);
                     };
+                    constexpr int kAhead = 6, kWide = 4;  // parts, and columns of four channels, in flight
                     float best = -FLT_MAX, sum = 0.f;
+#pragma unroll 8
                     for (int x = i0; x <= i1; ++x) best = fmaxf(best, __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row).x);
+#pragma unroll 8
                     for (int x = i0; x <= i1; ++x) {
                         const float2 st = __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row);
                         sum += st.y * exp2_fast(st.x - best);
@@ -563,30 +566,40 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     float inv = 0.f;
                     __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, best, sum, true, inv) : nullptr;
 #pragma unroll 1
-                    for (int d = 0; d < D / 4; d += 8) {
-                        float4 o[8];
+                    for (int d = 0; d < D / 4; d += kWide) {
+                        float4 o[kWide];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < kWide; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-                        for (int x = i0; x <= i1; ++x) {
-                            const float4* const src = part_of(x);
-                            const float2 st = __ldcg((const float2*)(src + D / 4 * kPromptRows) + row);
-                            if (st.y == 0.f) continue;  // nothing seen there; its rows may not have been written
-                            const float by = exp2_fast(st.x - best);
-                            float4 v[8];
+                        for (int x0 = i0; x0 <= i1; x0 += kAhead) {
+                            float by[kAhead];
+                            float4 v[kAhead][kWide];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (d + k) * kPromptRows + row);
+                            for (int x = 0; x < kAhead; ++x) {
+                                by[x] = 0.f;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                o[k].x = fmaf(v[k].x, by, o[k].x);
-                                o[k].y = fmaf(v[k].y, by, o[k].y);
-                                o[k].z = fmaf(v[k].z, by, o[k].z);
-                                o[k].w = fmaf(v[k].w, by, o[k].w);
+                                for (int k = 0; k < kWide; ++k) v[x][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (x0 + x > i1) continue;
+                                const float4* const src = part_of(x0 + x);
+                                const float2 st = __ldcg((const float2*)(src + D / 4 * kPromptRows) + row);
+                                if (st.y == 0.f) continue;  // nothing seen there; its rows may not have been written
+                                by[x] = exp2_fast(st.x - best);
+#pragma unroll
+                                for (int k = 0; k < kWide; ++k) v[x][k] = __ldcg(src + (d + k) * kPromptRows + row);
                             }
+#pragma unroll
+                            for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+                                for (int k = 0; k < kWide; ++k) {
+                                    o[k].x = fmaf(v[x][k].x, by[x], o[k].x);
+                                    o[k].y = fmaf(v[x][k].y, by[x], o[k].y);
+                                    o[k].z = fmaf(v[x][k].z, by[x], o[k].z);
+                                    o[k].w = fmaf(v[x][k].w, by[x], o[k].w);
+                                }
                         }
                         if (live)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) attn_store(to + 4 * (d + k), o[k], inv);
+                            for (int k = 0; k < kWide; ++k) attn_store(to + 4 * (d + k), o[k], inv);
                     }
                     if (row == 0) ws->arrived[i0 * TILES + i] = 0u;
                 }
@@ -631,12 +644,12 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             page = -1;
             if (!more) return;
             key = (ahead.first_tile + next) * kPromptKeys + key_in;
-            if (key < ahead.n.kv) page = a.block_table[ahead.b * a.table_stride + key / ps];
+            if (key < ahead.n.kv) page = a.block_table[ahead.b * a.table_stride + p.by_page(key)];
         };
         auto next_place = [&]() {  // of the tile that find_page() looked up, then the page of the one after
             Place x{nullptr, 0};
             if (page >= 0 && page < a.cache.num_pages) {
-                const int in = key - key / ps * ps;
+                const int in = key - p.by_page(key) * ps;
                 x.block = (const char*)a.cache.pages + (((int64_t)page * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
                 x.row = in % kKvBlockTokens;
             }
@@ -830,11 +843,10 @@ size_t prefill_partial_bytes(int head_dim) {
     return (size_t)kPromptMaxCtas * 2 * 2 * kPromptRows * ((size_t)head_dim + 2) * sizeof(float);
 }
 
-rra_status_t launch_prefill(const AttnParams& p, int sms, rra_stream_t stream) {
+rra_status_t launch_prefill(const AttnParams& p, int tiles, int sms, rra_stream_t stream) {
     const int ctas = std::min(sms, kPromptMaxCtas);
-    const bool two = (int64_t)p.a.max_q * p.group > kPromptRows;
-    if (p.a.cache.head_dim == 128) return two ? prompt_launch<128, 2>(p, ctas, stream) : prompt_launch<128, 1>(p, ctas, stream);
-    return two ? prompt_launch<64, 2>(p, ctas, stream) : prompt_launch<64, 1>(p, ctas, stream);
+    if (p.a.cache.head_dim == 128) return tiles == 2 ? prompt_launch<128, 2>(p, ctas, stream) : prompt_launch<128, 1>(p, ctas, stream);
+    return tiles == 2 ? prompt_launch<64, 2>(p, ctas, stream) : prompt_launch<64, 1>(p, ctas, stream);
 }
 
 }  // namespace rra
