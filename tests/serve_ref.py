@@ -148,3 +148,22 @@ def slot_map(seq, new, table, free, count, ps, tokens):
         cu.append(cu[-1] + add)
     pad = max(0, tokens - len(slots))
     return (kv, cu, (slots + [-1] * pad)[:tokens], (positions + [0] * pad)[:tokens], top, short)
+
+
+def leave_zeros():
+    """Overwrites what the allocator keeps with zeros, for tests that come later.  These tests fill tables with -1 and pages
+    with NaN patterns; the sentinel AllReduces take a buffer of all-ones for data that has not arrived, and tests enqueue them
+    on buffers straight from the allocator."""
+    import gc
+
+    import torch
+
+    gc.collect()
+    torch.cuda.synchronize()
+    for size in (1 << 20, 2 << 20):  # its pools of small and of large blocks
+        before, kept = torch.cuda.memory_reserved(), []
+        while torch.cuda.memory_reserved() == before:
+            kept.append(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+        del kept
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()

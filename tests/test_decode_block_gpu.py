@@ -24,7 +24,8 @@ def example():
     __graft_entry__.build()
     import decode_block
 
-    return decode_block
+    yield decode_block
+    ref.leave_zeros()
 
 
 def f64(t):

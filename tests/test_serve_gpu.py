@@ -17,6 +17,8 @@ def _built():
     import __graft_entry__
 
     __graft_entry__.build()
+    yield
+    ref.leave_zeros()
 
 
 @pytest.fixture(scope="module")
@@ -178,7 +180,7 @@ def test_qk_norm_rope(serve, t, hq, hk, d, rot, interleaved, dtype, case):
 
 
 # ------------------------------------------------------------- the cache --
-def cache_of(serve, num_pages, ps, hk, d, fill=0xFF):
+def cache_of(serve, num_pages, ps, hk, d, fill=0x7F):
     """Pages that were never written hold `fill`: as scales, NaN."""
     pages = torch.full((num_pages, serve.kv_page_bytes(ps, hk, d)), fill, dtype=torch.uint8, device="cuda")
     return serve.KvCache(pages, ps, hk, d)
