@@ -39,20 +39,23 @@ def nvcc() -> str:
 
 
 def _newest_input() -> float:
-    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["serve_bind.c"]]
+    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["serve_bind.cpp"]]
     files += [os.path.join(INCLUDE, f) for f in PUBLIC_HEADERS]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
 
-def _build_native() -> None:
-    tmp = NATIVE + ".tmp%d" % os.getpid()
-    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "serve_bind.c"), "-o", tmp, "-ldl"]
-    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if p.returncode != 0:
-        raise RuntimeError("gcc failed on serve_bind.c\n" + p.stdout.decode(errors="replace"))
-    os.replace(tmp, NATIVE)
+def _native_command(out: str) -> list:
+    """The compiler's command for _serve.so, against the installed torch (for its tensors' types and the current stream)."""
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(at, "include"),
+               os.path.join(at, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            *("-I" + i for i in include), os.path.join(CSRC, "serve_bind.cpp"), "-o", out, "-L" + os.path.join(at, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl", "-Wl,-rpath," + os.path.join(at, "lib")]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -71,6 +74,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    native = NATIVE + ".tmp%d" % os.getpid()
+    procs.append(("serve_bind.cpp", subprocess.Popen(_native_command(native), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     errors = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -81,13 +86,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(text, file=sys.stderr)
     if errors:
         raise RuntimeError("nvcc failed\n" + "\n".join(errors))
-    _build_native()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if p.returncode != 0:
         raise RuntimeError("link failed:\n" + p.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    os.replace(native, NATIVE)
     return LIB
 
 

@@ -3,7 +3,7 @@
 Page bookkeeping, head norms with position rotation, a key/value cache held in
 4 bits, and the attention over it: what a tensor-parallel rank runs around its
 AllReduces.  As in rra.py this is argument checking and marshalling only (in
-_serve.so, csrc/serve_bind.c); every call enqueues one kernel of librra.so on the
+_serve.so, csrc/serve_bind.cpp); every call enqueues one kernel of librra.so on the
 current stream (or `stream`), and there is no fallback.
 """
 from __future__ import annotations
@@ -26,8 +26,6 @@ _ROPE = struct.Struct("9P10qd6i")
 _TOKENS = struct.Struct("Pq4i3P5q2i")
 _ATTN = struct.Struct("Pq4i7P6qd8i")
 _CACHE = struct.Struct("Pq4i")
-
-_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 
 _WORKSPACE_HEAD = 4096  # bytes of the workspace that a call expects to be zero
 
@@ -64,7 +62,7 @@ class _Native:
         loader = importlib.machinery.ExtensionFileLoader("_serve", NATIVE_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serve", loader))
         loader.exec_module(module)
-        module.init(rra.LIB_PATH, _F32, _BF16, _I32, _I64, torch._C._cuda_getCurrentRawStream)
+        module.init(rra.LIB_PATH)
         _native = module
         return getattr(module, name)
 
