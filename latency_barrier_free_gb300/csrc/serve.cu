@@ -101,7 +101,7 @@ __device__ __forceinline__ int valid_pages(const rra_slot_map_args_t& a, int b, 
 __global__ void __launch_bounds__(kSlotThreads, 1) slot_map_kernel(const __grid_constant__ SlotParams p) {
     extern __shared__ int32_t sums_mem[];
     __shared__ int32_t part[3][32];
-    __shared__ int32_t over_total;
+    __shared__ int32_t over_total, endings;
     pdl_release_early();
     const rra_slot_map_args_t& a = p.a;
     const int n = a.requests;
@@ -110,42 +110,52 @@ __global__ void __launch_bounds__(kSlotThreads, 1) slot_map_kernel(const __grid_
     int32_t* const fresh = back + (n + 1);
     int32_t* const tokens = fresh + (n + 1);
     int32_t* const holds = tokens + (n + 1);
+    uint16_t* const ending = (uint16_t*)(holds + (n + 1));  // the requests that end, in any order
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, lane = tid & 31;
     const int me = (int)blockIdx.x * nt + tid, all = (int)gridDim.x * nt;
-    if (tid == 0) over_total = 0;
+    if (tid == 0) over_total = endings = 0;
+    __syncthreads();
     pdl_wait();
     const int count = min(max(a.free_count[0], 0), a.num_pages);
+
+    // Lengths, once; holds[b] is the complement for a request that ends.
+    for (int b = tid; b < n; b += nt) {
+        const int add = min(a.new_len[b], p.most_new), held = min(max(a.seq_len[b], 0), kSlotMost);
+        holds[b] = add < 0 ? ~held : held;
+        tokens[b] = max(add, 0);
+        back[b] = 0;
+        if (add < 0) ending[atomicAdd(&endings, 1)] = (uint16_t)b;
+    }
+    __syncthreads();
+    // pages that come back: valid entries of the rows of requests that end, a warp each
+    for (int e = tid >> 5; e < endings; e += nt >> 5) {
+        const int b = ending[e];
+        const int c = valid_pages(a, b, min(pages_for(p, ~holds[b]), a.table_pages), [](int, int) {});
+        if (lane == 0) back[b] = c;
+    }
+    if (endings > 0) __syncthreads();
 
     // running sums over the requests
     int base[3] = {0, 0, 0};
     for (int b0 = 0; b0 < n; b0 += nt) {
         const int b = b0 + tid;
-        int add = 0, held = 0;
-        if (b < n) {
-            add = min(a.new_len[b], p.most_new);
-            held = min(max(a.seq_len[b], 0), kSlotMost);
-        }
         int v[3] = {0, 0, 0}, tot[3];
-        // pages that come back: valid entries of the row of a request that ends, found by the whole warp
-        for (uint32_t todo = __ballot_sync(0xffffffffu, add < 0); todo != 0u; todo &= todo - 1u) {
-            const int who = __ffs((int)todo) - 1;
-            const int rows = min(pages_for(p, __shfl_sync(0xffffffffu, held, who)), a.table_pages);
-            const int c = valid_pages(a, b - lane + who, rows, [](int, int) {});
-            if (lane == who) v[0] = c;
-        }
-        if (add >= 0) {
-            const int first = pages_for(p, held), last = add > 0 ? pages_for(p, held + add) : first;
-            v[1] = max(0, min(last, a.table_pages) - first);
-            v[2] = add;
-            const int over = last - max(first, a.table_pages);
-            if (over > 0) atomicAdd(&over_total, over);
+        if (b < n) {
+            const int held = holds[b], add = tokens[b];
+            v[0] = back[b];
+            if (held >= 0) {
+                const int first = pages_for(p, held), last = add > 0 ? pages_for(p, held + add) : first;
+                v[1] = max(0, min(last, a.table_pages) - first);
+                v[2] = add;
+                const int over = last - max(first, a.table_pages);
+                if (over > 0) atomicAdd(&over_total, over);
+            }
         }
         block_sums3(v, tot, part);
         if (b < n) {
             back[b] = base[0] + v[0];
             fresh[b] = base[1] + v[1];
             tokens[b] = base[2] + v[2];
-            holds[b] = held;
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) base[k] += tot[k];
@@ -157,31 +167,27 @@ __global__ void __launch_bounds__(kSlotThreads, 1) slot_map_kernel(const __grid_
     }
     __syncthreads();
 
-    // push: a warp per request that ends
-    if (base[0] > 0) {
-        for (int b = me >> 5; b < n; b += all >> 5) {
-            if (back[b + 1] == back[b]) continue;
-            const int at = count + back[b];
-            valid_pages(a, b, min(pages_for(p, holds[b]), a.table_pages), [&](int page, int rank) {
-                if (at + rank < a.num_pages) a.free_pages[at + rank] = page;
-            });
-        }
+    // push: a warp of the cluster per request that ends
+    for (int e = me >> 5; e < endings; e += all >> 5) {
+        const int b = ending[e], at = count + back[b];
+        valid_pages(a, b, min(pages_for(p, ~holds[b]), a.table_pages), [&](int page, int rank) {
+            if (at + rank < a.num_pages) a.free_pages[at + rank] = page;
+        });
     }
     const int top = min(count + base[0], a.num_pages);
 
-    // Lengths: what becomes of a request that ends is known from new_len, which nothing overwrites.
     if (gridDim.x > 1) cluster_sync();
     else __syncthreads();
     for (int b = me; b <= n; b += all) {
         a.cu_new[b] = tokens[b];
-        if (b < n) a.kv_len[b] = a.new_len[b] < 0 ? 0 : holds[b] + tokens[b + 1] - tokens[b];
+        if (b < n) a.kv_len[b] = holds[b] < 0 ? 0 : holds[b] + tokens[b + 1] - tokens[b];
     }
 
     // pop: new entries of the tables
     for (int i = me; i < base[1]; i += all) {
+        const int page = i < top ? a.free_pages[top - 1 - i] : -1;
         const int b = owner_of(fresh, n, i);
-        const int at = pages_for(p, holds[b]) + i - fresh[b];
-        a.block_table[b * a.table_stride + at] = i < top ? a.free_pages[top - 1 - i] : -1;
+        a.block_table[b * a.table_stride + pages_for(p, holds[b]) + i - fresh[b]] = page;
     }
     // place: slots and positions of kSlotRun new tokens
     for (int64_t t0 = (int64_t)me * kSlotRun; t0 < a.tokens; t0 += (int64_t)all * kSlotRun) {
@@ -686,8 +692,8 @@ rra_status_t rra_slot_map(const rra_slot_map_args_t* args, rra_stream_t stream) 
     if ((a.num_pages > 0 && a.free_pages == nullptr) || (a.tokens > 0 && (a.slots == nullptr || a.positions == nullptr)))
         return RRA_ERR_INVALID_ARG;
     const void* k = (const void*)rra::slot_map_kernel;
-    const size_t smem = 4 * sizeof(int32_t) * ((size_t)a.requests + 1);
-    if (rra::configure_cluster_kernel(k, 4 * (int)sizeof(int32_t) * (RRA_SERVE_MAX_REQUESTS + 1)) != cudaSuccess) {
+    const size_t smem = 18 * ((size_t)a.requests + 1);
+    if (rra::configure_cluster_kernel(k, 18 * (RRA_SERVE_MAX_REQUESTS + 1)) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
@@ -700,8 +706,9 @@ rra_status_t rra_slot_map(const rra_slot_map_args_t* args, rra_stream_t stream) 
     const int64_t items = a.tokens / rra::kSlotRun + a.requests;
     int ctas = 1;
     while (ctas < rra::kSlotMaxCluster && (int64_t)ctas * rra::kSlotThreads * 2 < items) ctas *= 2;
+    const int threads = items <= 512 ? 256 : rra::kSlotThreads;  // fewer warps meet sooner
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kSlotThreads, smem, ctas, stream, kargs);
+    return rra::serve_launch(k, dim3((unsigned)ctas), threads, smem, ctas, stream, kargs);
 }
 
 rra_status_t rra_qk_norm_rope(const rra_qk_norm_rope_args_t* args, rra_stream_t stream) {
