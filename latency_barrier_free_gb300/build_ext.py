@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "librra.so")
 NATIVE = os.path.join(HERE, "_serve.so")  # the Python binding of rra_serve.h
 
 SOURCES = ["kernels.cu", "cluster.cu", "coll.cu", "fused.cu", "rra_api.cu", "probes.cu", "rra_static.cu", "serve.cu",
-           "serve_attn.cu", "serve_prefill.cu"]
+           "serve_attn.cu", "serve_prefill.cu", "serve_attn_team.cu"]
 HEADERS = ["prims.cuh", "cluster_prims.cuh", "rra_internal.h", "placement.h", "kernel_attrs.h", "serve_common.cuh",
            "serve_attn.cuh", "serve_attn_rows.cuh"]
 PUBLIC_HEADERS = ["rra.h", "rra_probe.h", "rra_static.h", "rra_device.cuh", "rra_serve.h"]

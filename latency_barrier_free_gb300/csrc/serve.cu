@@ -167,9 +167,12 @@ __global__ void __launch_bounds__(kSlotThreads, 1) slot_map_kernel(const __grid_
     }
     __syncthreads();
 
-    // push: a warp of the cluster per request that ends
-    for (int e = me >> 5; e < endings; e += all >> 5) {
-        const int b = ending[e], at = count + back[b];
+    // push: a warp of the cluster per request that ends (by number where there are several CTAs: their lists' orders differ)
+    const bool one = gridDim.x == 1;
+    for (int i = me >> 5; i < (one || endings == 0 ? endings : n); i += all >> 5) {
+        const int b = one ? ending[i] : i;
+        if (holds[b] >= 0) continue;
+        const int at = count + back[b];
         valid_pages(a, b, min(pages_for(p, ~holds[b]), a.table_pages), [&](int page, int rank) {
             if (at + rank < a.num_pages) a.free_pages[at + rank] = page;
         });

@@ -16,7 +16,6 @@
 
 namespace rra {
 
-constexpr int kAttnTile = 32;      // keys of one step of a warp
 constexpr int kAttnMinRun = 1;     // tiles a warp takes at least
 constexpr int kAttnSegmentCost = 4;  // what starting and ending a segment costs, in tiles
 
@@ -513,26 +512,36 @@ static bool attn_args_ok(const rra_kv_attention_args_t* a) {
 }
 
 // Which kernel: the one with the shortest time by what was measured of each, for the sizes that the caller expects (every
-// kernel is right for every call).  Times in microseconds, work in tiles of the busiest of 152 SMs:
-//   8 or 16 rows     8.5 or 11 + a chunk's tiles of 32 keys at 0.125 or 0.2 (head_dim 128), 0.085 or 0.135 (64)
-//   128 or 256 rows  8 or 11 + tiles of 128 keys at 2.7 or 3.2, 1.9 or 2.0, + joining the parts of a segment, 2 or 1.1 each
-// (e.g. 8 requests, 64 heads over 8 of 128, 4096 keys: 4 queries 38.6, 34.6, 54.8, 64.8 us; 8: 67, 56, 55, 66; 32: 223, 180,
-// 79, 74; 32768 keys, 64 queries: 3246, 2462, 1084, 690.)
-enum AttnKernel { kRows8, kRows16, kPrompt128, kPrompt256 };
+// kernel is right for every call).  Times in microseconds, for heads of 128 (64); work on the busiest of 152 SMs:
+//   8 or 16 rows     11.5 or 14 (9.5 or 12) + a chunk's tiles of 32 keys at 0.125 or 0.2 (0.085 or 0.135)
+//   128 or 256 rows  8 or 11 + tiles of 128 keys at 2.7 or 3.2 (1.9 or 2.0), + joining a segment's parts, 2 (1.1) each
+//   8 rows, a cluster of 1, 2, 4, 8 CTAs   3.5 to 4.4 + a warp's tiles of 32 keys at 0.83 (0.64), times 1.1 (0.7) for each
+//                    CTA on an SM
+// (64 heads over 8 of 128, 8 requests, 4096 keys: 4 queries 38.6, 34.6, 54.8, 64.8 us; 8: 67, 56, 55, 66; 32: 223, 180, 79,
+// 74; 32768 keys, 64 queries: 3246, 2462, 1084, 690.  1 request and query, 500 keys: 8.1 us against 6.7, 5.6, 4.8, 5.0 in
+// clusters; 8000 keys: 13.8 against 57, 31, 17.8, 11.0; 32000: 19.6 against 31.5 in clusters of 8.)
+enum AttnKernel { kRows8, kRows16, kPrompt128, kPrompt256, kTeam1, kTeam2, kTeam4, kTeam8 };
 static AttnKernel attn_kernel_of(const rra_kv_attention_args_t& a) {
     const bool big = a.cache.head_dim == 128;
     const double sms = 152;
     const double rows = (double)std::max(a.max_q, 1) * (a.q_heads / a.cache.kv_heads);
     const double seen = a.window > 0 ? std::min((double)a.max_kv, (double)a.window + a.max_q) : (double)a.max_kv;
-    const double heads = (double)std::max(a.requests, 1) * a.cache.kv_heads;
-    auto chunks = [&](double n) { return std::ceil(rows / n); };
-    auto few = [&](double n, double fixed, double tile) { return fixed + heads * chunks(n) * (std::ceil(seen / kAttnTile) + kAttnSegmentCost) / sms * tile; };
+    const double heads = (double)std::max(a.requests, 1) * a.cache.kv_heads, tiles = std::max(1.0, std::ceil(seen / kAttnTile));
+    auto segments = [&](double n) { return heads * std::ceil(rows / n); };
+    auto few = [&](double n, double fixed, double tile) { return fixed + segments(n) * (tiles + kAttnSegmentCost) / sms * tile; };
     auto many = [&](double n, double fixed, double tile) {
-        const double tiles = std::ceil(seen / 128), run = std::max(6.0, heads * chunks(n) * (tiles + 2) / sms);
-        return fixed + (heads * chunks(n) <= sms ? std::min(tiles, run) : run) * tile + (tiles > run ? tiles / run * (big ? 2 : 1.1) : 0);
+        const double of = std::ceil(seen / 128), run = std::max(6.0, segments(n) * (of + 2) / sms);
+        return fixed + (segments(n) <= sms ? std::min(of, run) : run) * tile + (of > run ? of / run * (big ? 2 : 1.1) : 0);
     };
-    const double t[4] = {few(8, 8.5, big ? 0.125 : 0.085), few(16, 11, big ? 0.2 : 0.135), many(128, 8, big ? 2.7 : 1.9), many(256, 11, big ? 3.2 : 2.0)};
-    return (AttnKernel)(std::min_element(t, t + 4) - t);
+    auto team = [&](double size, double fixed) {
+        const double ctas = segments(8) * size;
+        if (ctas > 16 * sms) return 1e30;
+        return fixed + std::ceil(tiles / (kTeamWarps * size)) * (big ? 0.83 : 0.64) * std::max(1.0, (big ? 1.1 : 0.7) * ctas / sms);
+    };
+    const double t[8] = {few(8, big ? 11.5 : 9.5, big ? 0.125 : 0.085), few(16, big ? 14 : 12, big ? 0.2 : 0.135), many(128, 8, big ? 2.7 : 1.9),
+                         many(256, 11, big ? 3.2 : 2.0),   team(1, 3.5),                   team(2, 4.0),
+                         team(4, 4.1),                     team(8, 4.4)};
+    return (AttnKernel)(std::min_element(t, t + 8) - t);
 }
 
 }  // namespace rra
@@ -548,7 +557,9 @@ size_t rra_kv_attention_workspace_bytes(int head_dim) {
 rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
     if (name == nullptr || !rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
     static const char* const names[] = {"kv_attention_kernel<8 rows>", "kv_attention_kernel<16 rows>",
-                                        "kv_attention_prompt_kernel<128 rows>", "kv_attention_prompt_kernel<256 rows>"};
+                                        "kv_attention_prompt_kernel<128 rows>", "kv_attention_prompt_kernel<256 rows>",
+                                        "kv_attention_team_kernel<1 CTA>", "kv_attention_team_kernel<2 CTAs>",
+                                        "kv_attention_team_kernel<4 CTAs>", "kv_attention_team_kernel<8 CTAs>"};
     *name = names[rra::attn_kernel_of(*args)];
     return RRA_OK;
 }
@@ -571,6 +582,8 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     p.room = args->table_pages * args->cache.page_tokens;
     p.window = std::min(args->window, 1 << 30);
     const rra::AttnKernel kernel = rra::attn_kernel_of(*args);
+    if (kernel >= rra::kTeam1)
+        return rra::launch_team(p, (int)(((int64_t)std::max(args->max_q, 1) * p.group + 7) / 8), 1 << (kernel - rra::kTeam1), stream);
     if (kernel == rra::kPrompt128 || kernel == rra::kPrompt256)
         return rra::launch_prefill(p, kernel == rra::kPrompt256 ? 2 : 1, sms, stream);
     const int ctas = std::min(sms, rra::kAttnMaxCtas);

@@ -11,6 +11,8 @@
 
 namespace rra {
 
+constexpr int kAttnTile = 32;      // keys of one step of a warp
+constexpr int kTeamWarps = 4;      // warps of a CTA of serve_attn_team.cu: one for each scheduler, a tile is a chain of latencies
 constexpr int kAttnMaxCtas = 512;  // CTAs a workspace has room for
 constexpr uint64_t kAttnWaitNs = 1000000000;  // a wait gives up after this long
 constexpr int kAttnMaxRows = 16;
@@ -109,6 +111,8 @@ __device__ __forceinline__ void attn_row_scale(const AttnParams& p, float most, 
     if (factor == 0.f) factor = 1.f, down = 0.f;  // every score is 0
 }
 
+// Few requests (serve_attn_team.cu): clusters of `size` CTAs (at most 8), `chunks` of them for a request and KV head.
+rra_status_t launch_team(const AttnParams& p, int chunks, int size, rra_stream_t stream);
 // Prompts (serve_prefill.cu): `tiles` (1 or 2) of 128 rows a CTA.
 rra_status_t launch_prefill(const AttnParams& p, int tiles, int sms, rra_stream_t stream);
 size_t prefill_partial_bytes(int head_dim);

@@ -359,6 +359,41 @@ def test_attention(serve, case):
         assert (out.float() - first.float()).abs().max() <= 0.02 * max(1.0, first.float().abs().max())
 
 
+def plans(cache, hq, requests):
+    """Hints that lead to each of the kernels."""
+    found = {}
+    for max_q in (1, 2, 8, 32, 256, 10 ** 4, 10 ** 6):
+        for max_kv in [0] + [2 ** i for i in range(5, 27)]:
+            found.setdefault(cache.plan_kernel(hq, requests, max_q=max_q, max_kv=max_kv), (max_q, max_kv))
+    return found
+
+
+@pytest.mark.parametrize("case", sorted(CASES))
+def test_every_kernel_is_right_for_every_call(serve, case):
+    """What the caller expects decides which kernel runs, not what it computes."""
+    hq, hk, d, ps, new, kv, causal, window = CASES[case]
+    cache, q, cu, kv_d, table, keys = build(serve, case)
+    kinds = plans(cache, hq, len(new))
+    assert {n.split("<")[0] for n in kinds} == {"kv_attention_kernel", "kv_attention_team_kernel", "kv_attention_prompt_kernel"}
+    assert len(kinds) >= 7, sorted(kinds)
+    wants = [ref.attention(f64(q[at:at + n]), k, v, length, d ** -0.5, causal, window)
+             for at, n, length, (k, v) in zip(np.cumsum([0] + new), new, kv, keys)]
+    for name, (max_q, max_kv) in kinds.items():
+        out, lse = torch.full_like(q, 7.0), torch.full((q.shape[0], hq), 7.0, device="cuda")
+        cache.attention(q, out, cu, kv_d, dev(table), max_q=max_q, max_kv=max_kv, causal=causal, window=window, lse=lse)
+        torch.cuda.synchronize()
+        at = 0
+        for n, length, (want, want_lse, mean, dots) in zip(new, kv, wants):
+            check_out(f64(out[at:at + n]), want, mean, dots, d, length)
+            got, empty = f64(lse[at:at + n]), np.isneginf(want_lse)
+            assert np.array_equal(np.isneginf(got), empty), name
+            tol = score_error(dots, d) + (length + 64) * U32 + 4 * U32 * np.abs(np.where(empty, 0, want_lse))
+            assert (np.abs(got[~empty] - want_lse[~empty]) <= tol[~empty]).all(), name
+            at += n
+        assert (out[at:] == 7).all()
+    assert cache.status() == 0
+
+
 @pytest.mark.parametrize("case", ["a chunk of a prompt", "drafted tokens", "a longer prompt"])
 def test_attention_hints_do_not_decide_what_is_computed(serve, case):
     hq, hk, d, ps, new, kv, causal, window = CASES[case]
@@ -547,5 +582,5 @@ def test_binding_refuses_what_does_not_fit(serve):
             serve.qk_norm_rope(*args)
     with pytest.raises(ValueError):
         serve.KvCache(torch.zeros(100, dtype=torch.uint8, device="cuda"), 16, 2, 64)
-    assert cache.plan_kernel(8, 1, max_q=1, max_kv=10) == "kv_attention_kernel<8 rows>"
+    assert cache.plan_kernel(8, 1, max_q=1, max_kv=10) == "kv_attention_team_kernel<1 CTA>"
     assert cache.status() == 0
