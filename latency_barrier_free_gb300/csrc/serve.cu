@@ -445,22 +445,28 @@ struct KvTokensParams {
     rra_kv_tokens_args_t a;
     Divisor by_heads;
     Divisor by_page;   // blocks of a page
+    int64_t room;      // slots of the cache
     int32_t pairs;     // tokens * kv_heads
     int32_t stride;    // pairs between those of a thread
 };
 
-// Two values as e2m1, `lo` in the low nibble: nearest, ties to even, saturating.
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+// The codes of eight values over their scale, the first in the low nibble: nearest e2m1, ties to even, saturating.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* y) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return r;
 }
-// The codes of four values over their scale d (by = 1 / d, rounded).
-__device__ __forceinline__ uint32_t codes4(const float* y) {
-    return to_e2m1x2(y[0], y[1]) | to_e2m1x2(y[2], y[3]) << 8;
+// (x, y) * by + 24 - 24 of two values in one instruction each, every step rounded to nearest.
+__device__ __forceinline__ void on_grid(float& x, float& y, float by) {
+    asm("{\n\t.reg .b64 v, b, c;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+        "fma.rn.f32x2 v, v, b, c;\n\tmov.b64 c, {%4, %4};\n\tadd.rn.f32x2 v, v, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(x), "+f"(y) : "f"(by), "f"(24.f), "f"(-24.f));
 }
 
-// Eight channels of a row being written: the group's part of the maximum, and the codes of channels 0..3 and 4..7.
+// Eight channels of a row being written: the group's part of the maximum, and the codes.
 template <typename T>
 struct KvWrite;
 template <>
@@ -478,19 +484,19 @@ struct KvWrite<float> {
         for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
         return m;
     }
-    __device__ __forceinline__ void codes(float d, float, uint32_t half[2]) const {
+    __device__ __forceinline__ uint32_t codes(float d) const {
         float x[8];
         raw.to(x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], d);
-        half[0] = codes4(x);
-        half[1] = codes4(x + 4);
+        return to_e2m1x8(x);
     }
 };
 // bfloat16 values (8 bits) over a scale of 11 bits are a midpoint of two codes (a multiple of 1/4 of at most 3 bits) or at
-// least 2^-14 of it away.  x / d enters the rounding as x * (1 / d), within 2^-24 of it, put on a grid of 2^-19 by adding
-// and taking off 24 (so that sums lie in [16, 32)): what was a midpoint is one again, and nothing else becomes one.  The
-// rounded division took more instructions than all the rest (16384 tokens, 8 heads of 128: 40 us against 21 us).
+// least 2^-14 of it away.  x / d enters the rounding as x * (1 / d), within 2^-23 of it, put on a grid of 2^-19 by adding
+// and taking off 24 (so that sums of what does not saturate lie in [16, 32)): what was a midpoint, 5 at most, is one
+// again, and nothing else becomes one.  The
+// rounded division took more instructions than all the rest (16384 tokens, 8 heads of 128: 40 us against 21 us; now 19).
 template <>
 struct KvWrite<__nv_bfloat16> {
     Raw8<__nv_bfloat16> raw;
@@ -509,13 +515,15 @@ struct KvWrite<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(w[0]), __habs2(w[1])), __hmax2(__habs2(w[2]), __habs2(w[3])));
         return fmaxf(__low2float(m), __high2float(m));
     }
-    __device__ __forceinline__ void codes(float, float by, uint32_t half[2]) const {
-        float x[8];
+    __device__ __forceinline__ uint32_t codes(float d) const {
+        float x[8], by;
         raw.to(x);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(d));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = copysignf(__fadd_rn(__fmaf_rn(fabsf(x[i]), by, 24.f), -24.f), x[i]);
-        half[0] = codes4(x);
-        half[1] = codes4(x + 4);
+        for (int i = 0; i < 8; i += 2) on_grid(x[i], x[i + 1], by);
+        // a zero has its value's sign
+        const uint32_t low = __byte_perm(raw.v.x, raw.v.y, 0x7351), high = __byte_perm(raw.v.z, raw.v.w, 0x7351);
+        return to_e2m1x8(x) | (__byte_perm(low, high, 0x5410) >> 4 & 0x08080808u) | (__byte_perm(low, high, 0x7632) & 0x80808080u);
     }
 };
 
@@ -532,8 +540,8 @@ __device__ __forceinline__ KvPair kv_pair(const KvTokensParams& p, int i) {
     const int64_t slot = __ldg(p.a.slots + r.token);
     r.row = (int)slot & (kKvBlockTokens - 1);
     r.block = -1;
-    if ((uint64_t)slot < (uint64_t)(c.num_pages * c.page_tokens)) {
-        const int at = (int)(slot / kKvBlockTokens), page = p.by_page(at);
+    if ((uint64_t)slot < (uint64_t)p.room) {
+        const int at = (int)((uint64_t)slot / kKvBlockTokens), page = p.by_page(at);
         r.block = (page * c.kv_heads + r.head) * p.by_page.d + (at - page * p.by_page.d);
     }
     return r;
@@ -577,11 +585,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const __half s = __float2half_rn(fminf(fmaxf(most * (1.f / 6.f), 6.103515625e-05f), 2048.f));
             const float d = __half2float(s);
-            uint32_t half[2];
-            x.codes(d, __frcp_rn(d), half);
+            const uint32_t codes = x.codes(d);
             // even groups keep their first half and get their neighbour's, odd ones the second
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? half[0] : half[1], 4);
-            const uint32_t word = odd ? got | half[1] << 16 : half[0] | got << 16;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? codes : codes >> 16, 4);
+            const uint32_t word = __byte_perm(codes, got, odd ? 0x3254 : 0x5410);
             if (pair[k].block >= 0) {
                 *(uint32_t*)(block + v * B::kV + pair[k].row * B::kRow + word_at) = word;
                 if (u == 0) *(__half*)(block + (v ? B::kScaleV : B::kScaleK) + pair[k].row * B::kScaleRow + 2 * j) = s;
@@ -664,6 +671,7 @@ static rra_status_t kv_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream
     p.a = *a;
     p.by_heads = Divisor(c.kv_heads);
     p.by_page = Divisor(c.page_tokens / kKvBlockTokens);
+    p.room = c.num_pages * c.page_tokens;
     p.pairs = (int)(a->tokens * c.kv_heads);
     const int per_cta = kKvThreads / (c.head_dim / 8);
     const bool many = p.pairs >= 8192;
