@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     __shared__ AttnPiece pieces[2 * kWarps];
     __shared__ AttnLengths known[Sh::kThreads];
     __shared__ float2 joined[2 * kWarps][kRows];  // maximum and sum of a chain's rows
-    __shared__ uint32_t is_last;
+    __shared__ int2 chain[2 * kWarps];  // its lead, its pieces
+    __shared__ int2 to_join[2];         // first CTA and number of CTAs of the first and last segment, 0 unless this one joins them
     const rra_kv_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -359,56 +360,75 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     if (has == 0u) return;
     const uint32_t leads = __ballot_sync(0xffffffffu, (my_flags & kStarts) != 0) | (has & -has);
     const int chains = __popc(leads);
-    auto chain_of = [&](int lead) {
-        const uint32_t later = leads & ~((2u << lead) - 1u);
-        return has & ~((1u << lead) - 1u) & (later != 0u ? (later & -later) - 1u : 0xffffffffu);
-    };
-    // A warp takes a row, a lane a piece: a piece's maximum becomes its weight.
-    for (int r = warp; r < kRows; r += kWarps) {
-        float* const mine = piece_at(lane >> 1, lane & 1) + 2 * r;
-        const float2 st = has >> lane & 1u ? *(const float2*)mine : make_float2(-FLT_MAX, 0.f);
-#pragma unroll 1
-        for (uint32_t left = leads; left != 0u; left &= left - 1u) {
-            const int lead = __ffs((int)left) - 1;
-            const bool in = chain_of(lead) >> lane & 1u;
-            float top = in ? st.x : -FLT_MAX;
+    {
+        // the lanes of this lane's chain, from its lead to the one before the next lead
+        const uint32_t until = (2u << lane) - 1u, later = leads & ~until;
+        const int lead = 31 - __clz((int)(leads & until | 1u)), last = later != 0u ? __ffs((int)later) - 2 : 31;
+        if (warp == kWarps - 1 && leads >> lane & 1u)
+            chain[__popc(leads & until) - 1] = make_int2(lane, (int)(has & ~((1u << lane) - 1u) & ((2u << last) - 1u)));
+        // A warp takes a row, a lane a piece: a piece's maximum becomes its weight.
+        for (int r = warp; r < kRows; r += kWarps) {
+            const bool mine = has >> lane & 1u;
+            float* const at = piece_at(lane >> 1, lane & 1) + 2 * r;
+            const float2 st = mine ? *(const float2*)at : make_float2(-FLT_MAX, 0.f);
+            float top = st.x;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 1; o < 32; o <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, top, o);
+                if (lane - o >= lead) top = fmaxf(top, up);
+            }
+            top = __shfl_sync(0xffffffffu, top, last);
             const float by = exp2_fast(st.x - top);
-            float sum = in ? st.y * by : 0.f;
+            float sum = mine ? st.y * by : 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (in) *mine = by;
-            if (lane == lead) joined[lead][r] = make_float2(top, sum);
+            for (int o = 1; o < 32; o <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane - o >= lead) sum += up;
+            }
+            sum = __shfl_sync(0xffffffffu, sum, last);
+            if (mine) *at = by;
+            if (leads >> lane & 1u) joined[lane][r] = make_float2(top, sum);
         }
     }
     __syncthreads();
     for (int item = tid; item < chains * kItems; item += Sh::kThreads) {
-        const int i = item % kItems;
-        uint32_t left = leads;
-        for (int skip = item / kItems; skip > 0; --skip) left &= left - 1u;
-        const int lead = __ffs((int)left) - 1;
-        const uint32_t chain = chain_of(lead);
+        const int i = item % kItems, lead = chain[item / kItems].x;
+        const uint32_t members = (uint32_t)chain[item / kItems].y;
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (uint32_t x = chain; x != 0u; x &= x - 1u) {
-            const int at = __ffs((int)x) - 1;
-            const float* const src = piece_at(at >> 1, at & 1);
-            const float by = src[2 * r];
-            const float4 v = *(const float4*)(src + 2 * kRows + r * D + d);
-            o.x = fmaf(v.x, by, o.x);
-            o.y = fmaf(v.y, by, o.y);
-            o.z = fmaf(v.z, by, o.z);
-            o.w = fmaf(v.w, by, o.w);
+        constexpr int kAhead = 4;
+#pragma unroll 1
+        for (uint32_t x = members; x != 0u;) {
+            float by[kAhead];
+            float4 v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                by[k] = 0.f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x != 0u) {
+                    const int at = __ffs((int)x) - 1;
+                    const float* const src = piece_at(at >> 1, at & 1);
+                    by[k] = src[2 * r];
+                    v[k] = *(const float4*)(src + 2 * kRows + r * D + d);
+                }
+                x &= x - 1u;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                o.x = fmaf(v[k].x, by[k], o.x);
+                o.y = fmaf(v[k].y, by[k], o.y);
+                o.z = fmaf(v[k].z, by[k], o.z);
+                o.w = fmaf(v[k].w, by[k], o.w);
+            }
         }
         const float2 st = joined[lead][r];
-        const int starts = pieces[lead].flags & kStarts, ends = pieces[31 - __clz((int)chain)].flags & kEnds;
+        const AttnPiece& pc = pieces[lead];
+        const int starts = pc.flags & kStarts, ends = pieces[31 - __clz((int)members)].flags & kEnds;
         if (starts && ends) {
-            const int row = pieces[lead].c * kRows + r;
-            if (row < pieces[lead].rows) {
+            const int row = pc.c * kRows + r;
+            if (row < pc.rows) {
                 float inv;
-                __nv_bfloat16* const to = attn_row(p, pieces[lead].q0, pieces[lead].h, row, st.x, st.y, d == 0, inv);
+                __nv_bfloat16* const to = attn_row(p, pc.q0, pc.h, row, st.x, st.y, d == 0, inv);
                 attn_store(to + d, o, inv);
             }
         } else {
@@ -418,64 +438,68 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         }
     }
 
-    // ---- join the CTAs that share a segment: the last to arrive adds them in order ----
+    // ---- join the CTAs that share a segment, the CTA's first chain's or its last's: the last to arrive adds them in order ----
     const int64_t cta0 = (int64_t)blockIdx.x * cta_run, cta1 = cta0 + cta_run;
-#pragma unroll 1
-    for (int turn = 0; turn < 2; ++turn) {
-        const int lead = turn == 0 ? __ffs((int)leads) - 1 : 31 - __clz((int)leads);  // first chain, last chain
-        if (turn == 1 && chains == 1) break;
-        const AttnPiece pc = pieces[lead];
-        if (pc.begin >= cta0 && pc.end <= cta1) continue;
-        const int i0 = quotient(pc.begin, cta_run), i1 = quotient(pc.end - 1, cta_run);
-        __syncthreads();
-        if (tid == 0) {
+    const int ends_at[2] = {__ffs((int)leads) - 1, 31 - __clz((int)leads)};
+    bool shared[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        shared[k] = (k == 0 || chains > 1) && (pieces[ends_at[k]].begin < cta0 || pieces[ends_at[k]].end > cta1);
+    if (!shared[0] && !shared[1]) return;
+    __syncthreads();
+    if (tid < 2) {
+        int i0 = 0, parts = 0;
+        if (shared[tid]) {
+            const AttnPiece& pc = pieces[ends_at[tid]];
+            i0 = quotient(pc.begin, cta_run);
+            parts = quotient(pc.end - 1, cta_run) - i0 + 1;
             __threadfence();  // of the whole CTA's part: the barrier comes before it
-            is_last = atomicAdd(&ws->arrived[i0], 1u) == (uint32_t)(i1 - i0) ? 1u : 0u;
+            if (atomicAdd(&ws->arrived[i0], 1u) != (uint32_t)(parts - 1)) parts = 0;
+            else ws->arrived[i0] = 0u;
             __threadfence();
         }
-        __syncthreads();
-        if (is_last == 0u) continue;
+        to_join[tid] = make_int2(i0, parts);
+    }
+    __syncthreads();
+    for (int item = tid; item < 2 * kItems; item += Sh::kThreads) {
+        const int i = item % kItems, parts = to_join[item / kItems].y;
+        const AttnPiece& pc = pieces[item < kItems ? ends_at[0] : ends_at[1]];
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        const int row = pc.c * kRows + r;
+        if (parts == 0 || row >= pc.rows) continue;
         constexpr int64_t kStep = 2 * Sh::kPartial;
-        const float* const base = partials + (int64_t)i0 * kStep;
-        const int parts = i1 - i0 + 1;
-        for (int i = tid; i < kItems; i += Sh::kThreads) {
-            const int r = i / (D / 4), d = i % (D / 4) * 4;
-            const int row = pc.c * kRows + r;
-            if (row >= pc.rows) continue;
-            float top = -FLT_MAX, sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 20;  // parts in flight: a round trip to L2 each otherwise
+        const float* const base = partials + (int64_t)to_join[item / kItems].x * kStep;
+        float top = -FLT_MAX, sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAhead = 20;  // parts in flight: a round trip to L2 each otherwise
 #pragma unroll 1
-            for (int x0 = 0; x0 < parts; x0 += kAhead) {
-                float2 st[kAhead];
-                float4 v[kAhead];
-                const float* src = base + x0 * kStep + (x0 == 0 ? Sh::kPartial : 0);
+        for (int x0 = 0; x0 < parts; x0 += kAhead) {
+            float2 st[kAhead];
+            float4 v[kAhead];
+            const float* src = base + x0 * kStep + (x0 == 0 ? Sh::kPartial : 0);
 #pragma unroll
-                for (int x = 0; x < kAhead; ++x) {
-                    st[x] = make_float2(-FLT_MAX, 0.f);
-                    v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (x0 + x < parts) {
-                        st[x] = __ldcg((const float2*)(src + 2 * r));
-                        v[x] = __ldcg((const float4*)(src + 2 * kRows + r * D + d));
-                    }
-                    src += x0 + x == 0 ? kStep - Sh::kPartial : kStep;
+            for (int x = 0; x < kAhead; ++x) {
+                st[x] = make_float2(-FLT_MAX, 0.f);
+                v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x0 + x < parts) {
+                    st[x] = __ldcg((const float2*)(src + 2 * r));
+                    v[x] = __ldcg((const float4*)(src + 2 * kRows + r * D + d));
                 }
-                float now = top;
-#pragma unroll
-                for (int x = 0; x < kAhead; ++x) now = fmaxf(now, st[x].x);
-                const float keep = exp2_fast(top - now);
-                top = now;
-                sum *= keep;
-                o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
-#pragma unroll
-                for (int x = 0; x < kAhead; ++x) attn_add(top, sum, o, st[x], v[x]);
+                src += x0 + x == 0 ? kStep - Sh::kPartial : kStep;
             }
-            float inv;
-            __nv_bfloat16* const to = attn_row(p, pc.q0, pc.h, row, top, sum, d == 0, inv);
-            attn_store(to + d, o, inv);
+            float now = top;
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) now = fmaxf(now, st[x].x);
+            const float keep = exp2_fast(top - now);
+            top = now;
+            sum *= keep;
+            o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) attn_add(top, sum, o, st[x], v[x]);
         }
-        if (tid == 0) ws->arrived[i0] = 0u;
-        __syncthreads();
+        float inv;
+        __nv_bfloat16* const to = attn_row(p, pc.q0, pc.h, row, top, sum, d == 0, inv);
+        attn_store(to + d, o, inv);
     }
 }
 
