@@ -33,7 +33,9 @@ namespace rra {
 constexpr int kPromptKeys = 128;       // keys of a tile
 constexpr int kPromptRows = 128;       // rows of a tile: the TMEM lanes
 constexpr int kPromptMinRun = 4;       // key tiles a CTA takes at least
-constexpr int kPromptSegmentCost = 2;  // what starting and ending a segment costs, in key tiles
+// What starting and ending a segment costs, in key tiles (3 requests of 1024 queries, 64 heads over 8 of 128, up to 8192 keys:
+// 2, 3, 4 and 5 took 327, 299, 280 and 283 us: with less, a CTA that gets the shortest segments ends last).
+constexpr int kPromptSegmentCost = 4;
 constexpr int kPromptMaxCtas = 192;    // CTAs that the workspace has room for
 constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 before the maximum moves
 static_assert(kPromptMaxCtas * 2 <= kAttnMaxCtas, "a counter for each tile of a CTA's last segment");
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     using B = KvBlock<D>;
     constexpr int J = B::kGroups;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 4 + 2 + 4 + 1];
+    __shared__ __align__(8) uint64_t bar_mem[5 * TILES + 4 + 2 + 4 + 1];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
     __shared__ uint32_t tmem_base;
@@ -268,27 +270,28 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     float* const parts = (float*)(ws + 1);
 
     const uint32_t bars = smem_u32(bar_mem);
-    const uint32_t q_full = bars, s_full = q_full + 8 * TILES, p_full = s_full + 8 * TILES, o_full = p_full + 8 * TILES,
-                   joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 16, v_full = k_empty + 16,
-                   v_empty = v_full + 8, seen_full = v_empty + 8, drained = seen_full + 32, turn = drained + 8;
+    // q_full[i], pv_full[i]: what the next products of tile i wait for, with their turn; s_full[i], o_full[i]: done
+    const uint32_t q_full = bars, s_full = q_full + 8 * TILES, pv_full = s_full + 8 * TILES, o_full = pv_full + 8 * TILES,
+                   joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 16, v_empty = k_empty + 16,
+                   seen_full = v_empty + 16, drained = seen_full + 32;
+    constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
     if (tid == 0) {
         for (int i = 0; i < TILES; ++i) {
-            mbar_init(q_full + 8 * i, kPromptRows);
+            mbar_init(q_full + 8 * i, kPromptRows + kTurn);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, kPromptRows);
+            mbar_init(pv_full + 8 * i, kPromptRows + 128 + kTurn);
             mbar_init(o_full + 8 * i, 1);
             mbar_init(joined + 8 * i, kPromptRows);
-            mbar_init(turn + 8 * i, 1);
         }
-        mbar_init(v_full, 128);
-        mbar_init(v_empty, TILES);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(v_empty + 8 * i, TILES);
             mbar_init(k_full + 8 * i, 128);
             mbar_init(k_empty + 8 * i, TILES);
         }
         for (int i = 0; i < 4; ++i) mbar_init(seen_full + 8 * i, 4);
         mbar_init(drained, TILES);
+        if (kTurn) mbar_arrive(q_full);  // the first turn
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     l += a0 + a1;
                     tc_wait_st();
                     tc_before_sync();
-                    mbar_arrive(p_full + 8 * i);
+                    mbar_arrive(pv_full + 8 * i);
                 }
                 if (ok) ok = wait(o_full + 8 * i, sn);
                 if (!ok) break;
@@ -609,24 +612,25 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             prompt_next<Sh::kRows>(p, seg);
         }
     } else if (warp < Sh::kIssue) {
-        // =============================== unpacking: a thread has a key ====
+        // =============================== unpacking: a thread has half a row of two keys, 64 apart ====
+        // so that either half of V's keys is unpacked, and its products begin, by itself
         set_registers<Sh::kUnpackRegs, Sh::kLaunchRegs>();
-        const int unpacker = warp - Sh::kUnpack, key_in = 32 * unpacker + lane;
+        const int unpacker = warp - Sh::kUnpack, side = unpacker >> 1, key_in = 32 * (unpacker & 1) + lane;
         const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
-        constexpr int kLoads = D / 32;  // 16-byte loads of a row of codes
-        struct Codes {  // of a row, and its scales
+        constexpr int kLoads = D / 64;  // 16-byte loads of half a row of codes
+        struct Codes {  // of half a row, and the row's scales
             uint4 c[kLoads];
             uint32_t s[J / 2];
         };
-        struct Place {  // a key's block and row; null if it is not there
-            const char* block;
-            int row;
+        struct Places {  // the keys' blocks; null if they are not there
+            const char* block[2];
         };
+        const int row = key_in % kKvBlockTokens;  // of both keys in their blocks: tiles and pages are whole blocks
         // the segment and tile after the one in hand: what is loaded next
         PromptSegment ahead = seg;
         int next = first_of(ahead), next_end = end_of(ahead);
         bool more = true;
-        int page = -1;  // of this thread's key in that tile
+        int pages[2] = {-1, -1};  // of this thread's keys in that tile
         int key = 0;
         auto settle = [&]() {  // moves to a segment that has a tile left in this run
             while (more && next >= next_end) {
@@ -639,41 +643,51 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 next_end = end_of(ahead);
             }
         };
-        auto find_page = [&]() {
+        auto find_pages = [&]() {
             settle();
-            page = -1;
+            pages[0] = pages[1] = -1;
             if (!more) return;
             key = (ahead.first_tile + next) * kPromptKeys + key_in;
-            if (key < ahead.n.kv) page = a.block_table[ahead.b * a.table_stride + p.by_page(key)];
+            const int32_t* const of = a.block_table + ahead.b * a.table_stride;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (key + 64 * x < ahead.n.kv) pages[x] = of[p.by_page(key + 64 * x)];
         };
-        auto next_place = [&]() {  // of the tile that find_page() looked up, then the page of the one after
-            Place x{nullptr, 0};
-            if (page >= 0 && page < a.cache.num_pages) {
-                const int in = key - p.by_page(key) * ps;
-                x.block = (const char*)a.cache.pages + (((int64_t)page * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
-                x.row = in % kKvBlockTokens;
+        auto next_places = [&]() {  // of the tile that find_pages() looked up, then the pages of the one after
+            Places at;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                at.block[x] = nullptr;
+                if (pages[x] >= 0 && pages[x] < a.cache.num_pages) {
+                    const int k = key + 64 * x, in = k - p.by_page(k) * ps;
+                    at.block[x] = (const char*)a.cache.pages + (((int64_t)pages[x] * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
+                }
             }
             if (more) ++next;
-            find_page();
-            return x;
+            find_pages();
+            return at;
         };
-        auto load = [&](Codes& x, const Place& at, int codes, int scales) {
+        auto load = [&](Codes (&x)[2], const Places& at, int codes, int scales) {
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k)
-                x.c[k] = at.block != nullptr ? *((const uint4*)(at.block + codes + at.row * B::kRow) + k) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i) {
+                const bool here = at.block[i] != nullptr;
 #pragma unroll
-            for (int k = 0; k < J / 2; ++k)
-                x.s[k] = at.block != nullptr ? *((const uint32_t*)(at.block + scales + at.row * B::kScaleRow) + k) : 0u;
+                for (int k = 0; k < kLoads; ++k)
+                    x[i].c[k] = here ? *((const uint4*)(at.block[i] + codes + row * B::kRow + side * (B::kRow / 2)) + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int k = 0; k < J / 2; ++k)
+                    x[i].s[k] = here ? *((const uint32_t*)(at.block[i] + scales + row * B::kScaleRow) + k) : 0u;
+            }
         };
-        // A row's codes as binary16 into its place of a swizzled tile; with kRest the part that rounding lost into `rest`.
+        // Half a row's codes as binary16 into their place of a swizzled tile; with_rest the part that rounding lost into `rest`.
         const uint32_t row_at = key_in * 128;
         auto unpack = [&](const Codes& x, uint32_t to, uint32_t rest, auto with_rest) {
             uint32_t wd[4 * kLoads];
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) wd[4 * k] = x.c[k].x, wd[4 * k + 1] = x.c[k].y, wd[4 * k + 2] = x.c[k].z, wd[4 * k + 3] = x.c[k].w;
-            // word c * J/2 + jh: channels 4 c.. of group 2 jh in its low half, of group 2 jh + 1 in its high one
+            // word (c - 4 side) * J/2 + jh: channels 4 c.. of group 2 jh in its low half, of group 2 jh + 1 in its high one
 #pragma unroll
-            for (int c = 0; c < 8; c += 2)
+            for (int c = 0; c < 4; c += 2)
 #pragma unroll
                 for (int jh = 0; jh < J / 2; ++jh) {
                     uint32_t even[4], odd[4];
@@ -686,7 +700,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                         uint32_t h[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) h[e] = half2_mul(v[e], s2);
-                        const uint32_t at = jh * Sh::kPanel + row_at + ((((jj * 4 + c / 2)) ^ (key_in & 7)) << 4);
+                        const uint32_t at = jh * Sh::kPanel + row_at + (((jj * 4 + 2 * side + c / 2) ^ (key_in & 7)) << 4);
                         sts_v4(to + at, h[0], h[1], h[2], h[3]);
                         if constexpr (decltype(with_rest)::value) {
                             uint32_t g[4];
@@ -697,6 +711,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     }
                 }
         };
+        constexpr uint32_t kHalf = 64 * 128;  // from a tile's first key to its 65th
         int64_t left = 0;  // tiles of this run
         for (PromptSegment s = seg;;) {
             left += max(0, end_of(s) - first_of(s));
@@ -704,45 +719,47 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             prompt_next<Sh::kRows>(p, s);
         }
         // K is unpacked a tile ahead of V: its two stages are free before V's one
-        auto unpack_k = [&](uint32_t tile, const Codes& x, bool here) {
-            const uint32_t there = __ballot_sync(0xffffffffu, here);
-            if (lane == 0) {
-                seen_words[tile & 3][unpacker] = there;
-                mbar_arrive(seen_full + 8 * (tile & 3));
-            }
-            if (tile >= 2) ok = wait(k_empty + 8 * (tile & 1), (tile >> 1) - 1);
-            if (!ok) return;
-            const uint32_t to = smem + Sh::kK + (tile & 1) * 2 * Sh::kTile;
-            unpack(x, to, to + Sh::kTile, std::true_type{});
-            fence_proxy_async_smem();
-            mbar_arrive(k_full + 8 * (tile & 1));
-        };
-        Codes k_now, v_now;   // K of tile n, V of tile n - 1
-        Place place{nullptr, 0};  // of tile n
-        find_page();
+        Codes k[2], v[2];        // K of tile n, V of tile n - 1
+        Places here = {{nullptr, nullptr}};  // of tile n
+        find_pages();
         if (left > 0) {
-            place = next_place();
-            load(k_now, place, 0, B::kScaleK);
+            here = next_places();
+            load(k, here, 0, B::kScaleK);
         }
 #pragma unroll 1
         for (int64_t tile = 0; ok && tile <= left && left > 0; ++tile) {
-            Codes k_then, v_then;
-            const bool here = place.block != nullptr;
-            if (tile < left) load(v_then, place, B::kV, B::kScaleV);
-            if (tile + 1 < left) {
-                place = next_place();
-                load(k_then, place, 0, B::kScaleK);
-            }
-            if (tile < left) unpack_k((uint32_t)tile, k_now, here);
-            if (ok && tile > 0) {  // V of the tile before
-                if (tile > 1) ok = wait(v_empty, (uint32_t)tile - 2);
+            const Places now = here;
+            const uint32_t t = (uint32_t)tile, stage = t & 1;
+            if (tile < left) {
+                const uint32_t there = __ballot_sync(0xffffffffu, (side == 0 ? now.block[0] : now.block[1]) != nullptr);
+                if (lane == 0) {
+                    seen_words[t & 3][unpacker] = there;
+                    mbar_arrive(seen_full + 8 * (t & 3));
+                }
+                if (tile >= 2) ok = wait(k_empty + 8 * stage, (t >> 1) - 1);
                 if (!ok) break;
-                unpack(v_now, smem + Sh::kV, 0u, std::false_type{});
+                const uint32_t to = smem + Sh::kK + stage * 2 * Sh::kTile;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) unpack(k[i], to + i * kHalf, to + Sh::kTile + i * kHalf, std::true_type{});
                 fence_proxy_async_smem();
-                mbar_arrive(v_full);
+                mbar_arrive(k_full + 8 * stage);
+                if (tile + 1 < left) {
+                    here = next_places();
+                    load(k, here, 0, B::kScaleK);
+                }
             }
-            k_now = k_then;
-            v_now = v_then;
+            if (tile > 0) {  // V of the tile before
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (tile > 1) ok = wait(v_empty + 8 * i, t - 2);
+                    if (!ok) break;
+                    unpack(v[i], smem + Sh::kV + i * kHalf, 0u, std::false_type{});
+                }
+                if (!ok) break;
+                fence_proxy_async_smem();
+                for (int i = 0; i < TILES; ++i) mbar_arrive(pv_full + 8 * i);
+            }
+            if (tile < left) load(v, now, B::kV, B::kScaleV);
         }
     } else {
         // =============================== products of tile i: one thread issues ====
@@ -755,11 +772,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         constexpr uint32_t kStep = Sh::kTile >> 4;  // from one tile to the next, in a descriptor
         const uint32_t s_at = tmem + 128 * i, o_at = tmem + 128 * (TILES + i);
         // The tiles' warps take turns: left alone they fall into step, and products and softmax of both alternate instead
-        // of overlapping (394 us against 3xx us).
-        uint32_t turns = 0;
-        auto my_turn = [&]() {
-            return TILES == 1 || (i == 0 && turns == 0) || wait(turn + 8 * i, i == 0 ? turns - 1 : turns);
-        };
+        // of overlapping (394 us against 330 us).
         while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);
             if (t0 < t1) {
@@ -767,20 +780,25 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 for (int tl = t0 - 1; tl < t1; ++tl) {  // products of tile tl, scores of the next
                     const bool values = tl >= t0, next = tl + 1 < t1;
                     if (values) {
-                        ok = wait(v_full, n) && wait(p_full + 8 * i, n) && my_turn();
+                        ok = wait(pv_full + 8 * i, n);
                         if (!ok) break;
                         tc_after_sync();
                         if (elected()) {  // O_i += P_i V
 #pragma unroll
-                            for (int k = 0; k < kPromptKeys / 16; ++k)
+                            for (int k = 0; k < kPromptKeys / 16; ++k) {
                                 tc_mma_ts(o_at, s_at + 8 * k, v_desc + k * (2048 >> 4), kPv, tl > t0 || k > 0);
-                            tc_commit(v_empty);
-                            if (!next) tc_commit(o_full + 8 * i);
+                                if (k == kPromptKeys / 32 - 1) tc_commit(v_empty);
+                            }
+                            tc_commit(v_empty + 8);
+                            if (!next) {
+                                tc_commit(o_full + 8 * i);
+                                if (kTurn) mbar_arrive(i == 0 ? pv_full + 8 : q_full);
+                            }
                         }
                         __syncwarp();
                         ++n;
                     } else {
-                        ok = wait(q_full + 8 * i, sn) && my_turn();
+                        ok = wait(q_full + 8 * i, sn);
                     }
                     if (ok && next) {
                         ok = wait(k_full + 8 * (n & 1), n >> 1);
@@ -793,14 +811,13 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                                 constexpr auto at = [](int x) { return (uint32_t)((x % (D / 16) >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
                                 tc_mma(s_at, q_desc + at(k), k_at + k / (D / 16) * kStep + at(k), kQk, k > 0);
                             }
+                            if (kTurn) mbar_arrive(i == 1 ? pv_full : values ? pv_full + 8 : q_full + 8);
                             tc_commit(s_full + 8 * i);
                             tc_commit(k_empty + 8 * (n & 1));
                         }
                         __syncwarp();
                     }
                     if (!ok) break;
-                    ++turns;
-                    if (TILES == 2 && lane == 0) mbar_arrive(turn + 8 * (1 - i));
                 }
                 ++sn;
             }
