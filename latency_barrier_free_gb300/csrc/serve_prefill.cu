@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     __shared__ int64_t part[Sh::kWarps];
     __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
     __shared__ uint32_t tmem_base;
-    __shared__ volatile uint32_t arrived[TILES];
+    __shared__ volatile uint32_t arrived[2][TILES];  // of the run's first and last segment
     __shared__ PromptSegment start;
     const rra_kv_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -504,6 +504,19 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             // ---- the segment's end in this run ----
             const bool starts = seg.begin >= r0, ends = seg.end <= r1;
             const float top = m * factor;
+            auto put = [&](__nv_bfloat16* to, const float* o, float inv) {  // 32 channels
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    uint4 u;
+                    uint32_t* const w = (uint32_t*)&u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
+                        w[e] = *(const uint32_t*)&z;
+                    }
+                    *(uint4*)(to + k) = u;
+                }
+            };
             if (starts && ends) {
                 float inv = 0.f;
                 __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, top, l, true, inv) : nullptr;
@@ -512,99 +525,87 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     uint32_t v[32];
                     tc_ld32(o_at + 32 * q, v);
                     tc_wait_ld();
-                    if (live)
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            uint4 u;
-                            uint32_t* const h = (uint32_t*)&u;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(v[k + 2 * e]) * inv,
-                                                                               __uint_as_float(v[k + 2 * e + 1]) * inv);
-                                h[e] = *(const uint32_t*)&z;
-                            }
-                            *(uint4*)(to + 32 * q + k) = u;
-                        }
+                    if (live) put(to + 32 * q, (const float*)v, inv);
                 }
             } else {
-                float4* const mine = (float4*)(parts + (((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * TILES + i) * Sh::kPart);
-                if (t0 < t1) {
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t v[32];
-                        tc_ld32(o_at + 32 * q, v);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mine[(8 * q + k) * kPromptRows + row] =
-                                make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
-                                            __uint_as_float(v[4 * k + 3]));
-                    }
-                }
-                ((float2*)(mine + D / 4 * kPromptRows))[row] = make_float2(top, l);
-                // ---- the last CTA to arrive adds the parts in order ----
+                // The last CTA to arrive adds the parts in order; its own, if it finds all others there, from where it is.
                 const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
-                __threadfence();
-                mbar_arrive(joined + 8 * i);
-                ok = wait(joined + 8 * i, joins++);
-                if (ok && row == 0) arrived[i] = atomicAdd(&ws->arrived[i0 * TILES + i], 1u);
-                mbar_arrive(joined + 8 * i);
-                ok = ok && wait(joined + 8 * i, joins);
-                ++joins;
+                uint32_t* const count = &ws->arrived[i0 * TILES + i];
+                volatile uint32_t& others = arrived[starts ? 1 : 0][i];
+                auto meet = [&]() {
+                    mbar_arrive(joined + 8 * i);
+                    return wait(joined + 8 * i, joins++);
+                };
+                if (row == 0) others = ld_acquire_u32(count);
+                ok = meet();
                 if (!ok) break;
-                if (arrived[i] == (uint32_t)(i1 - i0)) {
+                int mine = (int)blockIdx.x;
+                if (others != (uint32_t)(i1 - i0)) {
+                    mine = -1;
+                    float4* const to = (float4*)(parts + (((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * TILES + i) * Sh::kPart);
+                    if (t0 < t1) {
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t v[32];
+                            tc_ld32(o_at + 32 * q, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                to[(8 * q + k) * kPromptRows + row] =
+                                    make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
+                                                __uint_as_float(v[4 * k + 3]));
+                        }
+                    }
+                    ((float2*)(to + D / 4 * kPromptRows))[row] = make_float2(top, l);
+                    __threadfence();
+                    ok = meet();
+                    if (ok && row == 0) others = atomicAdd(count, 1u);
+                    ok = ok && meet();
+                    if (!ok) break;
+                }
+                if (others == (uint32_t)(i1 - i0)) {
                     __threadfence();
                     auto part_of = [&](int x) {
                         return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPart);
                     };
-                    constexpr int kAhead = 6, kWide = 4;  // parts, and columns of four channels, in flight
+                    auto stats_of = [&](int x) {
+                        return x == mine ? make_float2(top, l) : __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row);
+                    };
                     float best = -FLT_MAX, sum = 0.f;
-#pragma unroll 8
-                    for (int x = i0; x <= i1; ++x) best = fmaxf(best, __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row).x);
-#pragma unroll 8
+#pragma unroll 4
+                    for (int x = i0; x <= i1; ++x) best = fmaxf(best, stats_of(x).x);
+#pragma unroll 4
                     for (int x = i0; x <= i1; ++x) {
-                        const float2 st = __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row);
+                        const float2 st = stats_of(x);
                         sum += st.y * exp2_fast(st.x - best);
                     }
                     float inv = 0.f;
                     __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, best, sum, true, inv) : nullptr;
 #pragma unroll 1
-                    for (int d = 0; d < D / 4; d += kWide) {
-                        float4 o[kWide];
+                    for (int q = 0; q < D / 32; ++q) {
+                        float o[32];
 #pragma unroll
-                        for (int k = 0; k < kWide; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
 #pragma unroll 1
-                        for (int x0 = i0; x0 <= i1; x0 += kAhead) {
-                            float by[kAhead];
-                            float4 v[kAhead][kWide];
+                        for (int x = i0; x <= i1; ++x) {
+                            const float2 st = stats_of(x);
+                            uint32_t v[32];
+                            if (x == mine) {
+                                tc_ld32(o_at + 32 * q, v);
+                                tc_wait_ld();
+                            } else {
 #pragma unroll
-                            for (int x = 0; x < kAhead; ++x) {
-                                by[x] = 0.f;
-#pragma unroll
-                                for (int k = 0; k < kWide; ++k) v[x][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (x0 + x > i1) continue;
-                                const float4* const src = part_of(x0 + x);
-                                const float2 st = __ldcg((const float2*)(src + D / 4 * kPromptRows) + row);
-                                if (st.y == 0.f) continue;  // nothing seen there; its rows may not have been written
-                                by[x] = exp2_fast(st.x - best);
-#pragma unroll
-                                for (int k = 0; k < kWide; ++k) v[x][k] = __ldcg(src + (d + k) * kPromptRows + row);
+                                for (int k = 0; k < 8; ++k) *(float4*)(v + 4 * k) = __ldcg(part_of(x) + (8 * q + k) * kPromptRows + row);
                             }
+                            if (st.y != 0.f) {  // else nothing was seen there, and its channels may not have been written
+                                const float by = exp2_fast(st.x - best);
 #pragma unroll
-                            for (int x = 0; x < kAhead; ++x)
-#pragma unroll
-                                for (int k = 0; k < kWide; ++k) {
-                                    o[k].x = fmaf(v[x][k].x, by[x], o[k].x);
-                                    o[k].y = fmaf(v[x][k].y, by[x], o[k].y);
-                                    o[k].z = fmaf(v[x][k].z, by[x], o[k].z);
-                                    o[k].w = fmaf(v[x][k].w, by[x], o[k].w);
-                                }
+                                for (int k = 0; k < 32; ++k) o[k] = fmaf(__uint_as_float(v[k]), by, o[k]);
+                            }
                         }
-                        if (live)
-#pragma unroll
-                            for (int k = 0; k < kWide; ++k) attn_store(to + 4 * (d + k), o[k], inv);
+                        if (live) put(to + 32 * q, o, inv);
                     }
-                    if (row == 0) ws->arrived[i0 * TILES + i] = 0u;
+                    if (row == 0) *count = 0u;
                 }
             }
             if (seg.end >= r1) break;
