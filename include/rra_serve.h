@@ -151,7 +151,8 @@ rra_status_t rra_qk_norm_rope(const rra_qk_norm_rope_args_t* args, rra_stream_t 
  * 6.  So the cache resolves values from 3e-5 to 12288; NaN is stored as 0,
  * infinities as the largest code.
  *
- * page_tokens: a multiple of 16, 16..4096.  head_dim: 64 or 128. */
+ * page_tokens: a multiple of 16, 16..4096.  head_dim: 64 or 128.  The cache has
+ * up to 2^31 - 1 blocks (num_pages * page_tokens / 16 * kv_heads). */
 typedef struct {
     void* pages;                /* [num_pages][rra_kv_page_bytes()], 16-byte aligned */
     int64_t num_pages;
@@ -197,10 +198,14 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  *     s_j = scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
  *     lse = log sum_j exp(s_j).
  * A query that sees no key gets out = 0 and lse = -inf.  Products accumulate
- * in binary32; the softmax's maximum, sum and weights are binary32, a weight
- * is rounded to binary16 (11 bits) for its product with the values; out is
- * rounded to bfloat16 once.  The result does not depend on timing: partial
- * results of a split request are joined in a fixed order.
+ * in binary32; the softmax's maximum, sum and weights are binary32; out is
+ * rounded to bfloat16 once.  A query is scaled by a power of two to [1, 2) and
+ * then binary16 (its 8 bits fit).  Scores take every key exactly: code times
+ * scale, 13 bits, as two products.  For the sum over values binary16 (11 bits)
+ * holds: for few queries, weight times scale, the codes being exact; in the
+ * kernel for prompts, the weight, and code times scale apart.  The result does
+ * not depend on timing: partial results of a split request are joined in a
+ * fixed order.
  *   q, out bfloat16 [tokens][q_heads][head_dim], strides in elements, channels
  *   adjacent, pointers 16-byte aligned, strides multiples of 8; out may not
  *   overlap q.  lse NULL or binary32 [tokens][q_heads], contiguous.
@@ -214,7 +219,8 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  *   Its first 32-bit word is a status: RRA_OK, or RRA_ERR_TIMEOUT if a wait for
  *   the kernel's own copies ran out (results are then not valid); the
  *   caller clears it.
- * requests 0..RRA_SERVE_MAX_REQUESTS; q_heads a multiple of kv_heads. */
+ * requests 0..RRA_SERVE_MAX_REQUESTS; q_heads a multiple of kv_heads; tokens *
+ * q_heads and table_pages * page_tokens up to 2^30 - 1. */
 typedef struct {
     rra_kv_cache_t cache;
     const void* q;
@@ -244,8 +250,12 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
  * (0 if not supported); independent of the batch. */
 size_t rra_kv_attention_workspace_bytes(int head_dim);
 
-/* The kernel that rra_kv_attention launches for these arguments, as a
- * profiler's launch list names it (host arithmetic only). */
+/* The kernel that rra_kv_attention launches for these arguments (host
+ * arithmetic only): its name in a profiler's launch list, then the form in
+ * angle brackets, "kv_attention_kernel<8 rows>" or <16 rows> (few queries, the
+ * batch's keys in equal runs), "kv_attention_team_kernel<1 CTA>", <2 CTAs>,
+ * <4 CTAs>, <8 CTAs> (few requests, a cluster for each 8 rows) or
+ * "kv_attention_prompt_kernel<128 rows>", <256 rows>. */
 rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name);
 
 #ifdef __cplusplus

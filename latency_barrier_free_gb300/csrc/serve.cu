@@ -15,8 +15,10 @@ namespace rra {
 // sums.  The cluster barrier between the pushes and the pops is the only
 // synchronisation between CTAs, and also separates all reads of the lengths
 // from the writes that may go to the same buffers.  It is all latency: lengths,
-// then pages, then the stack, a round trip to L2 each (64 requests decoding
-// move 2 KB).
+// then pages, then the stack, a round trip to L2 each (64 requests that decode:
+// 2 KB in 4.4 us; 1000 requests with 65536 new tokens, one in 16 ending: 0.9 MB
+// in 12.0 us, of which scan and counting take a third, the push and the barrier
+// a quarter).
 constexpr int kSlotThreads = 1024;
 constexpr int kSlotMaxCluster = 16;
 constexpr int kSlotAhead = 8;   // loads of a row in flight
@@ -306,7 +308,7 @@ struct Raw8<__nv_bfloat16> {
 };
 
 // 128 bytes of a thread in flight (8192 tokens of 72 heads of 128, bfloat16: 4 heads in blocks of 256 took 66 us, 8 heads
-// 57 us, and in blocks of 128, whose starts hide each other better, 56 us).
+// 57 us, and in blocks of 128, whose starts hide each other better, 56 us; with streaming stores 50 us, 6.1 TB/s).
 constexpr int kRopeThreads = 128;
 template <typename T>
 constexpr int kRopeHeads = 16 / (int)sizeof(T);  // heads of a thread, where there are enough
@@ -435,11 +437,14 @@ static const void* rope_kernel(bool many, bool interleaved) {
 // are two half words (four channels each) that belong to different words;
 // thread 4 j + u (group j) swaps one of them with its neighbour in group j ^ 1,
 // after which each holds a whole word and the row's codes leave as one
-// coalesced run.  Bound by the values' traffic as long as the arithmetic (about
-// seven instructions a value) stays under it; a thread has up to
-// kKvPairs pairs of rows in flight.
+// coalesced run.  Bound by the values' traffic and, in the write, by nearly as
+// much arithmetic; a thread has up to kKvPairs pairs of rows in flight.  16384
+// tokens of 8 heads of 128, bfloat16: written in 17.6 us (4.9 TB/s), read back
+// in 13.4 (6.4 TB/s).
 constexpr int kKvThreads = 128;
-constexpr int kKvPairs = 2;  // where there are enough; one otherwise (16 tokens: 3.0 against 3.6 us for both calls)
+// Where there are enough; one otherwise (16384 tokens of 8 heads of 128, written and read: 31.0 us, with one pair 36.3; 16 tokens:
+// 3.9 us, with one pair 2.9).
+constexpr int kKvPairs = 2;
 
 struct KvTokensParams {
     rra_kv_tokens_args_t a;
@@ -496,7 +501,7 @@ struct KvWrite<float> {
 // least 2^-14 of it away.  x / d enters the rounding as x * (1 / d), within 2^-23 of it, put on a grid of 2^-19 by adding
 // and taking off 24 (so that sums of what does not saturate lie in [16, 32)): what was a midpoint, 5 at most, is one
 // again, and nothing else becomes one.  The
-// rounded division took more instructions than all the rest (16384 tokens, 8 heads of 128: 40 us against 21 us; now 19).
+// rounded division took more instructions than all the rest (16384 tokens, 8 heads of 128: 40 us against 21 us; with two values an instruction 17.6).
 template <>
 struct KvWrite<__nv_bfloat16> {
     Raw8<__nv_bfloat16> raw;
@@ -713,11 +718,12 @@ rra_status_t rra_slot_map(const rra_slot_map_args_t* args, rra_stream_t stream) 
     p.by_page = rra::Divisor(a.page_tokens);
     p.most_new = rra::kSlotMost / (a.requests > 0 ? a.requests : 1);
     p.wide = rra::aligned16(a.slots) && rra::aligned16(a.positions);
-    // as many CTAs as have two runs of tokens a thread
+    // as many CTAs as have two runs of tokens a thread (1000 requests, 65536 tokens: 43 us with one CTA, 23, 16 and 12 us with
+    // 4, 8 and 16); fewer warps meet sooner (64 requests, 64 tokens: 4.4 us with 256 threads, 5.1 with 1024)
     const int64_t items = a.tokens / rra::kSlotRun + a.requests;
     int ctas = 1;
     while (ctas < rra::kSlotMaxCluster && (int64_t)ctas * rra::kSlotThreads * 2 < items) ctas *= 2;
-    const int threads = items <= 512 ? 256 : rra::kSlotThreads;  // fewer warps meet sooner
+    const int threads = items <= 512 ? 256 : rra::kSlotThreads;
     void* kargs[] = {(void*)&p};
     return rra::serve_launch(k, dim3((unsigned)ctas), threads, smem, ctas, stream, kargs);
 }
@@ -750,6 +756,8 @@ rra_status_t rra_qk_norm_rope(const rra_qk_norm_rope_args_t* args, rra_stream_t 
     r.a = a;
     r.lanes_log2 = 0;
     while (1 << r.lanes_log2 < a.head_dim / 16) ++r.lanes_log2;
+    // heads of a thread, where the SMs stay full (4 tokens of 72 heads: 1.5 us with one a thread, 3.1 with eight; 1021 of 12: the
+    // same; 8192 of 72: 66 us and 50)
     const bool many = a.tokens * heads >= 16384;
     const int each = !many ? 1 : elem == 4 ? rra::kRopeHeads<float> : rra::kRopeHeads<__nv_bfloat16>;
     r.q_units = (a.q_heads + each - 1) / each;
