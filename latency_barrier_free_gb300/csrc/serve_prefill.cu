@@ -788,45 +788,37 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
 #pragma unroll 1
                 for (int tl = t0 - 1; tl < t1; ++tl) {  // products of tile tl, scores of the next
                     const bool values = tl >= t0, next = tl + 1 < t1;
-                    if (values) {
-                        ok = wait(pv_full + 8 * i, n);
-                        if (!ok) break;
-                        tc_after_sync();
-                        if (elected()) {  // O_i += P_i V
+                    const uint32_t then = n + (values ? 1 : 0);  // the tile whose scores come next
+                    // K is ready long before: first its wait, so that nothing comes between the products
+                    ok = (!next || wait(k_full + 8 * (then & 1), then >> 1)) && (values ? wait(pv_full + 8 * i, n) : wait(q_full + 8 * i, sn));
+                    if (!ok) break;
+                    tc_after_sync();
+                    const uint32_t k_at = k_desc + (then & 1) * 2 * kStep;
+                    if (elected()) {
+                        if (values) {  // O_i += P_i V
 #pragma unroll
                             for (int k = 0; k < kPromptKeys / 16; ++k) {
                                 tc_mma_ts(o_at, s_at + 8 * k, v_desc + k * (2048 >> 4), kPv, tl > t0 || k > 0);
                                 if (k == kPromptKeys / 32 - 1) tc_commit(v_empty);
                             }
                             tc_commit(v_empty + 8);
-                            if (!next) {
-                                tc_commit(o_full + 8 * i);
-                                if (kTurn) mbar_arrive(i == 0 ? pv_full + 8 : q_full);
-                            }
                         }
-                        __syncwarp();
-                        ++n;
-                    } else {
-                        ok = wait(q_full + 8 * i, sn);
-                    }
-                    if (ok && next) {
-                        ok = wait(k_full + 8 * (n & 1), n >> 1);
-                        if (!ok) break;
-                        tc_after_sync();
-                        const uint32_t k_at = k_desc + (n & 1) * 2 * kStep;
-                        if (elected()) {  // S_i = Q_i K^T, both parts of K
+                        if (next) {  // S_i = Q_i K^T, both parts of K
 #pragma unroll
                             for (int k = 0; k < 2 * (D / 16); ++k) {
                                 constexpr auto at = [](int x) { return (uint32_t)((x % (D / 16) >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
                                 tc_mma(s_at, q_desc + at(k), k_at + k / (D / 16) * kStep + at(k), kQk, k > 0);
                             }
-                            if (kTurn) mbar_arrive(i == 1 ? pv_full : values ? pv_full + 8 : q_full + 8);
                             tc_commit(s_full + 8 * i);
-                            tc_commit(k_empty + 8 * (n & 1));
+                            tc_commit(k_empty + 8 * (then & 1));
+                            if (kTurn) mbar_arrive(i == 1 ? pv_full : values ? pv_full + 8 : q_full + 8);
+                        } else {
+                            tc_commit(o_full + 8 * i);
+                            if (kTurn) mbar_arrive(i == 0 ? pv_full + 8 : q_full);
                         }
-                        __syncwarp();
                     }
-                    if (!ok) break;
+                    __syncwarp();
+                    n = then;
                 }
                 ++sn;
             }
