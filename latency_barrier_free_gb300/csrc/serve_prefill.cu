@@ -69,8 +69,8 @@ struct PromptShape {
     static constexpr int kWarps = kIssue + 4;
     static constexpr int kLaunchRegs = 65536 / (32 * kWarps) / 8 * 8;
     static constexpr int kSoftmaxRegs = TILES == 2 ? 184 : 216;
-    static constexpr int kUnpackRegs = TILES == 2 ? 104 : 168;
-    static constexpr int kIssueRegs = TILES == 2 ? 40 : 120;
+    static constexpr int kUnpackRegs = TILES == 2 ? 88 : 168;
+    static constexpr int kIssueRegs = TILES == 2 ? 56 : 120;
     static_assert(TILES * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= (TILES + 2) * kLaunchRegs, "what the launch has");
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
@@ -263,9 +263,10 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     using B = KvBlock<D>;
     constexpr int J = B::kGroups;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t bar_mem[5 * TILES + 4 + 2 + 4 + 1];
+    __shared__ __align__(8) uint64_t bar_mem[5 * TILES + 4 + 2 + 4 + 1 + 8];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
+    __shared__ volatile int32_t places[4][9];  // of four tiles: the cache's blocks of its keys (-1: none), and how many keys there are
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t arrived[2][TILES];  // of the run's first and last segment
     __shared__ PromptSegment start;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     // q_full[i], pv_full[i]: what the next products of tile i wait for, with their turn; s_full[i], o_full[i]: done
     const uint32_t q_full = bars, s_full = q_full + 8 * TILES, pv_full = s_full + 8 * TILES, o_full = pv_full + 8 * TILES,
                    joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 16, v_empty = k_empty + 16,
-                   seen_full = v_empty + 16, drained = seen_full + 32;
+                   seen_full = v_empty + 16, drained = seen_full + 32, place_full = drained + 8, place_empty = place_full + 32;
     constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
     if (tid == 0) {
@@ -296,7 +297,11 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             mbar_init(k_full + 8 * i, 128);
             mbar_init(k_empty + 8 * i, TILES);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(seen_full + 8 * i, 4);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(seen_full + 8 * i, 4);
+            mbar_init(place_full + 8 * i, 1);
+            mbar_init(place_empty + 8 * i, 4);
+        }
         mbar_init(drained, TILES);
         if (kTurn) mbar_arrive(q_full);  // the first turn
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -624,7 +629,6 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         // so that either half of V's keys is unpacked, and its products begin, by itself
         set_registers<Sh::kUnpackRegs, Sh::kLaunchRegs>();
         const int unpacker = warp - Sh::kUnpack, side = unpacker >> 1, key_in = 32 * (unpacker & 1) + lane;
-        const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
         constexpr int kLoads = D / 64;  // 16-byte loads of half a row of codes
         struct Codes {  // of half a row, and the row's scales
             uint4 c[kLoads];
@@ -634,45 +638,17 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             const char* block[2];
         };
         const int row = key_in % kKvBlockTokens;  // of both keys in their blocks: tiles and pages are whole blocks
-        // the segment and tile after the one in hand: what is loaded next
-        PromptSegment ahead = seg;
-        int next = first_of(ahead), next_end = end_of(ahead);
-        bool more = true;
-        int pages[2] = {-1, -1};  // of this thread's keys in that tile
-        int key = 0;
-        auto settle = [&]() {  // moves to a segment that has a tile left in this run
-            while (more && next >= next_end) {
-                if (ahead.end >= r1) {
-                    more = false;
-                    break;
-                }
-                prompt_next<Sh::kRows>(p, ahead);
-                next = first_of(ahead);
-                next_end = end_of(ahead);
-            }
-        };
-        auto find_pages = [&]() {
-            settle();
-            pages[0] = pages[1] = -1;
-            if (!more) return;
-            key = (ahead.first_tile + next) * kPromptKeys + key_in;
-            const int32_t* const of = a.block_table + ahead.b * a.table_stride;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (key + 64 * x < ahead.n.kv) pages[x] = of[p.by_page(key + 64 * x)];
-        };
-        auto next_places = [&]() {  // of the tile that find_pages() looked up, then the pages of the one after
+        auto places_of = [&](uint32_t t) {
             Places at;
+            ok = wait(place_full + 8 * (t & 3), t >> 2);
+            const volatile int32_t* const from = places[t & 3];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                at.block[x] = nullptr;
-                if (pages[x] >= 0 && pages[x] < a.cache.num_pages) {
-                    const int k = key + 64 * x, in = k - p.by_page(k) * ps;
-                    at.block[x] = (const char*)a.cache.pages + (((int64_t)pages[x] * a.cache.kv_heads + ahead.h) * blocks + in / kKvBlockTokens) * B::kBytes;
-                }
+                const int block = from[(key_in + 64 * x) / kKvBlockTokens];
+                at.block[x] = ok && block >= 0 && key_in + 64 * x < from[8] ? (const char*)a.cache.pages + (int64_t)block * B::kBytes : nullptr;
             }
-            if (more) ++next;
-            find_pages();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(place_empty + 8 * (t & 3));
             return at;
         };
         auto load = [&](Codes (&x)[2], const Places& at, int codes, int scales) {
@@ -729,9 +705,8 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         // K is unpacked a tile ahead of V: its two stages are free before V's one
         Codes k[2], v[2];        // K of tile n, V of tile n - 1
         Places here = {{nullptr, nullptr}};  // of tile n
-        find_pages();
         if (left > 0) {
-            here = next_places();
+            here = places_of(0);
             load(k, here, 0, B::kScaleK);
         }
 #pragma unroll 1
@@ -752,7 +727,8 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 fence_proxy_async_smem();
                 mbar_arrive(k_full + 8 * stage);
                 if (tile + 1 < left) {
-                    here = next_places();
+                    here = places_of(t + 1);
+                    if (!ok) break;
                     load(k, here, 0, B::kScaleK);
                 }
             }
@@ -773,7 +749,31 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         // =============================== products of tile i: one thread issues ====
         set_registers<Sh::kIssueRegs, Sh::kLaunchRegs>();
         const int i = warp - Sh::kIssue;
-        ok = i < TILES;  // the warpgroup's other warps have nothing to do
+        if (i == 2) {
+            // =============================== another warp looks up pages, up to four tiles ahead of the unpacking ====
+            const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
+            uint32_t t = 0;
+            for (PromptSegment s = seg; ok;) {
+                const int end = end_of(s);
+                for (int tl = first_of(s); ok && tl < end; ++tl, ++t) {
+                    const int key0 = (s.first_tile + tl) * kPromptKeys, key = key0 + kKvBlockTokens * lane;
+                    int block = -1;
+                    if (lane < kPromptKeys / kKvBlockTokens && key < s.n.kv) {
+                        const int at = p.by_page(key), page = a.block_table[s.b * a.table_stride + at];
+                        if (page >= 0 && page < a.cache.num_pages) block = (page * a.cache.kv_heads + s.h) * blocks + (key - at * ps) / kKvBlockTokens;
+                    }
+                    if (t >= 4) ok = wait(place_empty + 8 * (t & 3), (t >> 2) - 1);
+                    if (!ok) break;
+                    if (lane < kPromptKeys / kKvBlockTokens) places[t & 3][lane] = block;
+                    if (lane == 0) places[t & 3][8] = min(kPromptKeys, s.n.kv - key0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(place_full + 8 * (t & 3));
+                }
+                if (s.end >= r1) break;
+                prompt_next<Sh::kRows>(p, s);
+            }
+        }
+        ok = i < TILES;
         constexpr uint32_t kQk = mma_desc(kPromptKeys, false), kPv = mma_desc(D, true);
         const uint32_t q_desc = tile_desc(smem + i * Sh::kTile, 16), k_desc = tile_desc(smem + Sh::kK, 16),
                        v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
