@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int r = 8 * n + 2 * t + k, row = seg.c * kRows + r;
-                    const float top = att.m[n][k] * att.factor[n][k];  // in units of log2
+                    // in units of log2; of a row that saw nothing the factor must not make it infinite
+                    const float top = fmaxf(att.m[n][k] * att.factor[n][k], -FLT_MAX);
                     if (!(starts && ends)) {
                         if (g == 0) *(float2*)(piece + 2 * r) = make_float2(top, sum);
 #pragma unroll

@@ -491,6 +491,41 @@ def test_attention_of_queries_of_any_size(serve, size, new):
         check_out(np.where(sharp[..., None], want, got), want, mean, dots, d, kv)
 
 
+@pytest.mark.parametrize("d,hk,group", [(128, 3, 2), (64, 2, 7)])
+def test_large_queries_that_see_no_key(serve, d, hk, group):
+    """Rows before the first key, in segments that warps and CTAs share, where the scale of a row is above 1."""
+    hq, ps, new, kv = hk * group, 48, [0, 50, 402], [1, 2, 402]
+    rng = np.random.default_rng(21)
+    num = sum(-(-n // ps) for n in kv)
+    cache = cache_of(serve, num, ps, hk, d)
+    table = np.zeros((3, -(-max(kv) // ps)), np.int32)
+    keys, used = [], 0
+    for b, n in enumerate(kv):
+        held = -(-n // ps)
+        table[b, :held] = np.arange(used, used + held)
+        used += held
+        slots = dev(table[b, np.arange(n) // ps].astype(np.int64) * ps + np.arange(n) % ps)
+        k, v = (dev(rng.standard_normal((n, hk, d)).astype(np.float32) * 0.01) for _ in range(2))
+        cache.append(k, v, slots)
+        cache.read(slots, k, v)
+        keys.append((f64(k), f64(v)))
+    q = dev(rng.standard_normal((sum(new), hq, d)) * 100, torch.bfloat16)
+    cu = dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    for name, (max_q, max_kv) in plans(cache, hq, 3).items():
+        out, lse = torch.full_like(q, 7.0), torch.full((q.shape[0], hq), 7.0, device="cuda")
+        cache.attention(q, out, cu, dev(np.array(kv, np.int32)), dev(table), max_q=max_q, max_kv=max_kv, lse=lse)
+        torch.cuda.synchronize()
+        assert cache.status() == 0
+        for b in (1, 2):
+            rows = slice(int(cu[b]), int(cu[b + 1]))
+            want, want_lse, mean, dots = ref.attention(f64(q[rows]), *keys[b], kv[b], d ** -0.5, True, 0)
+            empty = np.isneginf(want_lse)
+            assert empty[:48].all() == (b == 1)
+            assert np.array_equal(np.isneginf(f64(lse[rows])), empty), name
+            assert (f64(out[rows])[empty] == 0).all(), name
+            check_out(f64(out[rows]), want, mean, dots, d, kv[b])
+
+
 def test_attention_nan_query_stays_in_its_row(serve):
     for case in ("drafted tokens", "a longer prompt"):
         hq, hk, d, ps, new, kv, causal, window = CASES[case]
