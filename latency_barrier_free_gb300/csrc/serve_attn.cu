@@ -547,11 +547,11 @@ static bool attn_args_ok(const rra_kv_attention_args_t* a) {
 // kernel is right for every call).  Times in microseconds, for heads of 128 (64); work on the busiest of 152 SMs:
 //   8 or 16 rows     11.5 or 14 (9.5 or 12) + a chunk's tiles of 32 keys at 0.125 or 0.2 (0.085 or 0.135)
 //   128 or 256 rows  8 or 11 + tiles of 128 keys at 2.7 or 3.2 (1.9 or 2.0), + joining a segment's parts, 2 (1.1) each
-//                    (short segments included: in long ones a tile of 256 rows takes 2.3)
+//                    (short segments included: in long ones a tile of 256 rows takes 2.1)
 //   8 rows, a cluster of 1, 2, 4, 8 CTAs   3.5 to 4.4 + a warp's tiles of 32 keys at 0.83 (0.64), times 1.1 (0.7) for each
 //                    CTA on an SM
-// (64 heads over 8 of 128, 8 requests, 4096 keys: 4 queries 37.0, 32.9, 50.4, 57.8 us; 8: 64, 53, 51, 59; 32: 216, 172, 81,
-// 62; 32768 keys, 64 queries: 3185, 2376, 888, 615.  1 request and query, 500 keys: 8.1 us against 6.7, 5.6, 4.8, 5.0 in
+// (64 heads over 8 of 128, 8 requests, 4096 keys: 4 queries 37.1, 32.7, 51.5, 56.1 us; 8: 64, 53, 52, 57; 32: 217, 172, 80,
+// 58; 32768 keys, 64 queries: 3207, 2376, 932, 525.  1 request and query, 500 keys: 8.1 us against 6.7, 5.6, 4.8, 5.0 in
 // clusters; 8000 keys: 13.8 against 57, 31, 17.8, 11.0; 32000: 19.6 against 31.5 in clusters of 8.)
 enum AttnKernel { kRows8, kRows16, kPrompt128, kPrompt256, kTeam1, kTeam2, kTeam4, kTeam8 };
 static AttnKernel attn_kernel_of(const rra_kv_attention_args_t& a) {

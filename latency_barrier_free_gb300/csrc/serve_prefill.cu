@@ -25,11 +25,13 @@
 // to arrive adds the parts in order.
 //
 // 3 requests of up to 1024 queries and 8192 keys, 64 heads over 8 of 128: 261
-// GFLOP in 272.5 us, 958 TFLOP/s, or 1437 with the second part of K; the tensor
-// pipe is busy 62 % of the time.  Per 256 rows and 128 keys that is about 4500
-// cycles, of which products at their full rate would take 3072: queries, keys
-// and the unpacking warps' stores share the bandwidth of shared memory, and each
-// of the four waits between products and softmax costs 200 to 400 cycles.
+// GFLOP in 259.5 us, 1006 TFLOP/s, or 1509 with the second part of K.  Per 256
+// rows and 128 keys that is about 4200 cycles, of which products at their full
+// rate would take 3072.  Longest is the chain of one tile: its values' and next
+// scores' products (1536 cycles alone, 1750 beside the stores and reads of the
+// rest), a wait of 250, its softmax (2000: reading the scores, their maximum, and
+// 128 exponentials a thread take about as long each).  TMEM has no room for the
+// next scores beside the weights, so only the other tile fills the gap.
 #include <algorithm>
 #include <type_traits>
 
@@ -40,8 +42,8 @@ namespace rra {
 constexpr int kPromptKeys = 128;       // keys of a tile
 constexpr int kPromptRows = 128;       // rows of a tile: the TMEM lanes
 constexpr int kPromptMinRun = 4;       // key tiles a CTA takes at least
-// What starting and ending a segment costs, in key tiles (3 requests of 1024 queries, 64 heads over 8 of 128, up to 8192 keys:
-// 2, 3, 4 and 5 took 327, 299, 280 and 283 us: with less, a CTA that gets the shortest segments ends last).
+// What starting and ending a segment costs, in key tiles (3 requests of up to 1024 queries and 8192 keys, 64 heads over 8 of 128:
+// 2, 3, 4, 5 and 6 take 304, 276, 259, 262 and 265 us: with less, a CTA that gets the shortest segments ends last).
 constexpr int kPromptSegmentCost = 4;
 constexpr int kPromptMaxCtas = 192;    // CTAs that the workspace has room for
 constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 before the maximum moves
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         constexpr uint32_t kStep = Sh::kTile >> 4;  // from one tile to the next, in a descriptor
         const uint32_t s_at = tmem + 128 * i, o_at = tmem + 128 * (TILES + i);
         // The tiles' warps take turns: left alone they fall into step, and products and softmax of both alternate instead
-        // of overlapping (394 us against 330 us).  The turn arrives at the barrier that the warp waits on for its
+        // of overlapping (394 us against 330 us, measured when the rest was slower).  The turn arrives at the barrier that the warp waits on for its
         // operands: each further wait cost it 200 to 400 cycles (with two more, for halves of P and V: 381 us).
         while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);

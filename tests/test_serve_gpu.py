@@ -234,6 +234,31 @@ def test_quantisation_error_is_half_a_step(serve):
     assert (np.abs(g - y) <= step * (1 + 2.0 ** -9)).all()
 
 
+@pytest.mark.parametrize("exponent", [-9, 0, 5])
+def test_every_bfloat16_rounds_as_its_quotient(serve, exponent):
+    """Every value of eight binades under every largest value of its group: midpoints of codes are among them."""
+    binade = (1 + np.arange(128) / 128) * 2.0 ** exponent
+    values = np.concatenate([binade * 2.0 ** -k for k in range(8)])
+    rows = []
+    for most in binade:
+        x = values[values <= most]
+        x = np.concatenate([x, -x])
+        x = np.concatenate([x, np.zeros(-len(x) % 31)]).reshape(-1, 31)
+        rows.append(np.concatenate([np.full((len(x), 1), most), x], 1))
+    rows = np.concatenate(rows)
+    rows = np.concatenate([rows, np.zeros((len(rows) % 2, 32))]).reshape(-1, 1, 64)
+    cache = cache_of(serve, -(-len(rows) // 16), 16, 1, 64)
+    k, slots = dev(rows, torch.bfloat16), torch.arange(len(rows), device="cuda")
+    assert np.array_equal(f64(k), rows)
+    cache.append(k, -k, slots)
+    got = [torch.empty(rows.shape, device="cuda") for _ in range(2)]
+    cache.read(slots, *got)
+    want = ref.dequantise(*ref.quantise(rows.astype(np.float32)))
+    for g, sign in zip(got, (1, -1)):
+        assert np.array_equal(sign * f64(g), want)
+        assert np.array_equal(np.signbit(f64(g)), np.signbit(sign * want))
+
+
 def test_cache_beyond_4_gib(serve):
     """Pages whose byte offsets pass 32 bits."""
     hk, d, ps = 8, 128, 64
