@@ -61,7 +61,8 @@ struct PromptShape {
     static constexpr int kSums = kK;                    // before any tile: running sums of the requests' chunks
     static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
     // Warps: softmax (a warp reaches the TMEM lanes of its number modulo 4), then four that unpack, then one for each tile
-    // that issues its products: one for both left the tensor cores idle for 300 to 500 cycles between products.
+    // that issues its products: one for both left the tensor cores idle for 300 to 500 cycles between products.  Of the two
+    // left in the last warpgroup one looks up pages.
     // Whole warpgroups, for the registers: a softmax thread holds all 128 scores of its row (read back from TMEM in two
     // passes instead, their latency alone took 1200 cycles a tile).  The shares of a warpgroup's thread are those that
     // the launch gives (65536 over all threads, a multiple of 8), taken from the issuing one for the softmax.
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         }
     } else if (warp < Sh::kIssue) {
         // =============================== unpacking: a thread has half a row of two keys, 64 apart ====
-        // so that either half of V's keys is unpacked, and its products begin, by itself
+        // so that a half of V's keys is unpacked while products still read the other
         set_registers<Sh::kUnpackRegs, Sh::kLaunchRegs>();
         const int unpacker = warp - Sh::kUnpack, side = unpacker >> 1, key_in = 32 * (unpacker & 1) + lane;
         constexpr int kLoads = D / 64;  // 16-byte loads of half a row of codes
@@ -753,6 +754,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         const int i = warp - Sh::kIssue;
         if (i == 2) {
             // =============================== another warp looks up pages, up to four tiles ahead of the unpacking ====
+            // (by the unpacking warps themselves, lookups and addresses took a quarter of a tile's time: 270 us against 259)
             const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
             uint32_t t = 0;
             for (PromptSegment s = seg; ok;) {
