@@ -14,7 +14,7 @@
 // heads over 8 of 128, one query each: 131071 keys of one request, 151 MB, take
 // 36.4 us (4.15 TB/s): 3.4 us to the first copy (lengths, page numbers, pages),
 // 24.7 us of stream at 6.1 TB/s, then the joins.  64 ragged requests, 175 MB:
-// 43.7 us (4.0 TB/s).  Half the instructions are the unpacking of codes, and the
+// 43.5 us (4.0 TB/s).  Half the instructions are the unpacking of codes, and the
 // ALU pipe is half busy; four schedulers need the three warps each.
 #include <algorithm>
 #include <cmath>

@@ -25,7 +25,7 @@
 // to arrive adds the parts in order.
 //
 // 3 requests of up to 1024 queries and 8192 keys, 64 heads over 8 of 128: 261
-// GFLOP in 259.5 us, 1006 TFLOP/s, or 1509 with the second part of K.  Per 256
+// GFLOP in 259 us, 1008 TFLOP/s, or 1512 with the second part of K.  Per 256
 // rows and 128 keys that is about 4200 cycles, of which products at their full
 // rate would take 3072.  Longest is the chain of one tile: its values' and next
 // scores' products (1536 cycles alone, 1750 beside the stores and reads of the
@@ -72,8 +72,8 @@ struct PromptShape {
     static constexpr int kWarps = kIssue + 4;
     static constexpr int kLaunchRegs = 65536 / (32 * kWarps) / 8 * 8;
     static constexpr int kSoftmaxRegs = TILES == 2 ? 184 : 216;
-    static constexpr int kUnpackRegs = TILES == 2 ? 88 : 168;
-    static constexpr int kIssueRegs = TILES == 2 ? 56 : 120;
+    static constexpr int kUnpackRegs = TILES == 2 ? 96 : 168;
+    static constexpr int kIssueRegs = TILES == 2 ? 48 : 120;
     static_assert(TILES * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= (TILES + 2) * kLaunchRegs, "what the launch has");
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
