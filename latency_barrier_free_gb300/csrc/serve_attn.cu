@@ -12,9 +12,9 @@
 //
 // Bound by the pages' bytes in the middle and by latency at both ends.  64
 // heads over 8 of 128, one query each: 131071 keys of one request, 151 MB, take
-// 36.4 us (4.15 TB/s): 3.4 us to the first copy (lengths, page numbers, pages),
-// 24.7 us of stream at 6.1 TB/s, then the joins.  64 ragged requests, 175 MB:
-// 43.5 us (4.0 TB/s).  Half the instructions are the unpacking of codes, and the
+// 37.3 us (4.05 TB/s): 3.4 us to the first copy (lengths, page numbers, pages),
+// 25 us of stream at 6 TB/s, then the joins.  64 ragged requests, 175 MB:
+// 44.5 us (3.9 TB/s).  Half the instructions are the unpacking of codes, and the
 // ALU pipe is half busy; four schedulers need the three warps each.
 #include <algorithm>
 #include <cmath>
@@ -335,8 +335,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int r = 8 * n + 2 * t + k, row = seg.c * kRows + r;
-                    // in units of log2; of a row that saw nothing the factor must not make it infinite
-                    const float top = fmaxf(att.m[n][k] * att.factor[n][k], -FLT_MAX);
+                    const float top = att.top(n, k);
                     if (!(starts && ends)) {
                         if (g == 0) *(float2*)(piece + 2 * r) = make_float2(top, sum);
 #pragma unroll

@@ -7,8 +7,8 @@
 // barriers: against serve_attn.cu there is no scan of the batch before the first
 // copy, and no fence, counter and round trip to L2 after the last key.  What
 // remains is lengths, page numbers, pages: three round trips, one after another.
-// 8 heads over 1 of 128: 2000 keys in 5.4 us (the other kernel: 9.7).  24
-// requests of up to 5 queries, 14 heads over 2 of 64, a window of 1000: 10.4 us.
+// 8 heads over 1 of 128: 2000 keys in 5.5 us (the other kernel: 9.7).  24
+// requests of up to 5 queries, 14 heads over 2 of 64, a window of 1000: 10.8 us.
 #include "serve_attn_rows.cuh"
 
 namespace rra {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 3) kv_attention_team_kernel(c
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int r = 2 * t + k;
-            if (g == 0) *(float2*)(part + 2 * r) = make_float2(att.m[0][k] * att.factor[0][k], sum);
+            if (g == 0) *(float2*)(part + 2 * r) = make_float2(att.top(0, k), sum);
 #pragma unroll
             for (int j = 0; j < B::kGroups; ++j) *(float4*)(part + 16 + r * D + 32 * j + 4 * g) = att.output(j, 0, k);
         }

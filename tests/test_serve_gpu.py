@@ -516,6 +516,31 @@ def test_attention_of_queries_of_any_size(serve, size, new):
         check_out(np.where(sharp[..., None], want, got), want, mean, dots, d, kv)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("values", ["small", "small, then large", "large"])
+def test_weights_far_below_one(serve, d, values):
+    """Thousands of keys in one run whose weights are far below the largest: weight times scale keeps its bits."""
+    rng = np.random.default_rng(31)
+    hq, hk, ps, kv = 8, 1, 64, 9000
+    cache = cache_of(serve, -(-kv // ps), ps, hk, d)
+    size = np.full((kv, 1, 1), 2e-4)
+    if values != "small":
+        size[0 if values == "large" else 5000:] = 3000.0
+    k, v = (dev((rng.standard_normal((kv, hk, d)) * x).astype(np.float32)) for x in (1.0, size))
+    slots = torch.arange(kv, device="cuda")
+    cache.append(k, v, slots)
+    cache.read(slots, k, v)
+    q = dev(rng.standard_normal((1, hq, d)) * 4, torch.bfloat16)
+    table = torch.arange(-(-kv // ps), dtype=torch.int32, device="cuda")[None]
+    want, want_lse, mean, dots = ref.attention(f64(q), f64(k), f64(v), kv, d ** -0.5, True, 0)
+    for name, (max_q, max_kv) in plans(cache, hq, 1).items():
+        out, lse = torch.empty_like(q), torch.empty(1, hq, device="cuda")
+        cache.attention(q, out, dev(np.array([0, 1], np.int32)), dev(np.array([kv], np.int32)), table, max_q=max_q, max_kv=max_kv, lse=lse)
+        torch.cuda.synchronize()
+        check_out(f64(out), want, mean, dots, d, kv)
+        assert (np.abs(f64(lse) - want_lse) <= score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)).all(), name
+
+
 @pytest.mark.parametrize("d,hk,group", [(128, 3, 2), (64, 2, 7)])
 def test_large_queries_that_see_no_key(serve, d, hk, group):
     """Rows before the first key, in segments that warps and CTAs share, where the scale of a row is above 1."""
