@@ -204,9 +204,9 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  * scale, 13 bits, as two products.  For the sum over values binary16 (11 bits)
  * holds: for few queries, weight times scale (times 2^10 while scales are below
  * 2, against its underflow), the codes being exact; in the
- * kernel for prompts, the weight, and code times scale apart.  The result does
- * not depend on timing: partial results of a split request are joined in a
- * fixed order.
+ * kernel for prompts, the weight (times 2^7), and code times scale apart.  The
+ * result does not depend on timing: partial results of a split request are
+ * joined in a fixed order.
  *   q, out bfloat16 [tokens][q_heads][head_dim], strides in elements, channels
  *   adjacent, pointers 16-byte aligned, strides multiples of 8; out may not
  *   overlap q.  lse NULL or binary32 [tokens][q_heads], contiguous.

@@ -47,6 +47,10 @@ constexpr int kPromptMinRun = 4;       // key tiles a CTA takes at least
 constexpr int kPromptSegmentCost = 4;
 constexpr int kPromptMaxCtas = 192;    // CTAs that the workspace has room for
 constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 before the maximum moves
+// Weights enter their product with the values as binary16, which has few bits left below 2^-14 and none below 2^-25, while a
+// row's sum counts them whole.  So they are taken 2^kPromptLift times as large: 2^(8 + 7) fits.  (131072 keys of one run, each
+// 2^-25.3 of the largest: without it their share, 0.3 % of the values' size, was missing.)
+constexpr float kPromptLift = 7.f, kPromptUnlift = 1.f / 128;
 static_assert(kPromptMaxCtas * 2 <= kAttnMaxCtas, "a counter for each tile of a CTA's last segment");
 
 template <int D, int TILES>
@@ -174,9 +178,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 fence_proxy_async_smem();
                 mbar_arrive(q_full + 8 * i);
 
-                const uint64_t factor2 = pair2(factor, factor);
+                const uint64_t factor2 = pair2(factor, factor), lift2 = pair2(kPromptLift, kPromptLift);
                 for (int tl = t0; tl < t1 && ok; ++tl, ++n) {
                     ok = wait(seen_full + 8 * (n & 3), n >> 2) && wait(s_full + 8 * i, n);
                     if (!ok) break;
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
 #pragma unroll
                         for (int k = 64 * q; k < 64 * q + 64; k += 2) {
                             float e0, e1;
-                            split2(mul2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), off), factor2), e0, e1);
+                            split2(fma2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), off), factor2, lift2), e0, e1);
                             e0 = exp2_fast(e0);
                             e1 = exp2_fast(e1);
                             sums[k >> 1 & 1] = add2(sums[k >> 1 & 1], pair2(e0, e1));
@@ -519,6 +523,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             // ---- the segment's end in this run ----
             const bool starts = seg.begin >= r0, ends = seg.end <= r1;
             const float top = m * factor;
+            l *= kPromptUnlift;  // O stays lifted until it is divided by its sum
             auto put = [&](__nv_bfloat16* to, const float* o, float inv) {  // 32 channels
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
@@ -535,6 +540,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             if (starts && ends) {
                 float inv = 0.f;
                 __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, top, l, true, inv) : nullptr;
+                inv *= kPromptUnlift;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
@@ -596,6 +602,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     }
                     float inv = 0.f;
                     __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, best, sum, true, inv) : nullptr;
+                    inv *= kPromptUnlift;
 #pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         float o[32];

@@ -1,0 +1,52 @@
+"""Attention over the 4-bit cache where its kernels' numbers and paths reach
+their ends, against plain references in 64 bits: through every kernel that a call
+may be given."""
+import numpy as np
+import pytest
+
+import serve_ref as ref
+from test_serve_gpu import U8, U16, U32, _built, cache_of, dev, f64, plans, score_error, serve  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def one_request(serve, k, v, ps=64):  # noqa: F811
+    """A cache that holds the keys and values k, v [kv, hk, d], their values as they are held, and its row of pages."""
+    kv, hk, d = k.shape
+    pages = -(-kv // ps)
+    cache = cache_of(serve, pages, ps, hk, d)
+    k, v, slots = dev(k.astype(np.float32)), dev(v.astype(np.float32)), torch.arange(kv, device="cuda")
+    cache.append(k, v, slots)
+    cache.read(slots, k, v)
+    return cache, f64(k), f64(v), torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("below", [20.2, 24.6, 25.3, 28.0])
+def test_many_weights_far_below_the_largest(serve, below, d):  # noqa: F811
+    """One key outweighs each of the 131071 others by 2^below; together they still count.  So many requests over the same
+    pages that some have all keys in one run."""
+    kv, hq, requests = 131072, 8, 160
+    k, v = np.zeros((kv, 1, d)), np.ones((kv, 1, d))
+    k[0], v[0] = 1.0, 0.0
+    cache, k, v, table = one_request(serve, k, v)
+    q = dev(np.full((requests, hq, d), 1.0), torch.bfloat16)
+    scale = below * np.log(2) / k[0].sum()
+    want, want_lse, mean, dots = ref.attention(f64(q[:1]), k, v, kv, scale, True, 0)
+    assert want[0, 0, 0] > 2.0 ** -13
+    # A weight is rounded to binary16, to 11 bits or, of small numbers, to a multiple of 2^-24: of weights taken at least
+    # 2^7 times as large as they are against the largest, so within 2^-32 of that.
+    lost = kv * 2.0 ** -32 * np.abs(v).max()
+    tol = U8 * np.abs(want) + (1 + U8) * ((2 * U16 + 2 * score_error(dots, d) + (kv + 64) * U32)[..., None] * mean + lost)
+    kinds = plans(cache, hq, requests)
+    assert {n.split("<")[0] for n in kinds} == {"kv_attention_kernel", "kv_attention_team_kernel", "kv_attention_prompt_kernel"}
+    for name, (max_q, max_kv) in kinds.items():
+        out, lse = torch.empty_like(q), torch.empty(requests, hq, device="cuda")
+        cache.attention(q, out, torch.arange(requests + 1, dtype=torch.int32, device="cuda"),
+                        torch.full((requests,), kv, dtype=torch.int32, device="cuda"), table.repeat(requests, 1), max_q=max_q,
+                        max_kv=max_kv, scale=scale, lse=lse)
+        torch.cuda.synchronize()
+        assert cache.status() == 0
+        assert (np.abs(f64(out) - want) <= tol).all(), (name, f64(out).min(), f64(out).max(), want[0, 0, 0])
+        assert (np.abs(f64(lse) - want_lse) <= score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)).all(), name
