@@ -202,9 +202,9 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  * rounded to bfloat16 once.  A query is scaled by a power of two to [1, 2) and
  * then binary16 (its 8 bits fit).  Scores take every key exactly: code times
  * scale, 13 bits, as two products.  For the sum over values binary16 (11 bits)
- * holds: for few queries, weight times scale (times 2^10 while scales are below
- * 2, against its underflow), the codes being exact; in the
- * kernel for prompts, the weight (times 2^7), and code times scale apart.  The
+ * holds: for few queries, the weight (times 2^10, against its underflow) and the
+ * weight times scale, the codes being exact; in the kernel for prompts, the
+ * weight (times 2^7), and code times scale apart.  The
  * result does not depend on timing: partial results of a split request are
  * joined in a fixed order.
  *   q, out bfloat16 [tokens][q_heads][head_dim], strides in elements, channels

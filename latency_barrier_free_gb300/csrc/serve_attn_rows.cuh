@@ -17,12 +17,13 @@
 namespace rra {
 
 constexpr float kAttnSlack = 4.f;  // log2 of how far weights may pass 1 before the maximum moves
-// A weight times a value's scale is rounded to binary16, which has few bits left below 2^-14.  So weights are taken 2^kAttnLift
-// times as large while every scale is below 2 (values below 12), which one bit of a scale tells: 2^(4 + 10) * 2 fits, and so does
-// 2^4 times the largest scale, 2048, after that.  (60000 keys, values of 2e-4, queries of 4: the result's error 0.2 %, without
-// it 1 %; 64 ragged requests take 2 % longer.)
+// A weight, and a weight times a value's scale, is rounded to binary16, which has few bits left below 2^-14 and none below
+// 2^-25.  So weights are taken 2^kAttnLift times as large, and scales are brought below 2 by a power of two, which the sums
+// get back at the segment's end: 2^(4 + 10) * 2 fits.  Scales below 2 (values below 12) need no such power; one bit of a scale
+// tells, and the rest is done where a maximum moves.  (60000 keys, values of 2e-4, queries of 4: the result's error 0.2 %, with no lift 1 %; 64 ragged requests take 2 %
+// longer.)
 constexpr float kAttnLift = 10.f;
-constexpr uint32_t kAttnLarge = 0x40004000u;  // in two scales
+constexpr uint32_t kAttnLarge = 0x40004000u;  // a bit of two scales each that are 2 or more
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -78,15 +79,15 @@ struct AttnRows {
     // weights are 2^((s - m) factor): with s factor - m factor, rounded apart, huge scores would overflow.
     float m[NT][2], limit[NT][2], l[NT][2];
     float acc[J][2][NT][4];
-    float lift;                     // kAttnLift and
-    uint32_t large;                 // kAttnLarge, or 0 and 0 after a scale that is
+    float grown;                    // what scales are divided by, and so the sums too short by: 1, or 2^k with all scales below 2^(k + 1)
+    uint32_t large;                 // bits of scales that need a look: kAttnLarge, or all once they are divided
 
     // Of column 2 t + k of n-tile n: the maximum that sum and channels go with, in units of log2.  Of a row that saw
     // nothing the factor must not make it infinite.
-    __device__ __forceinline__ float top(int n, int k) const { return fmaxf(m[n][k] * factor[n][k], -FLT_MAX) - lift; }
+    __device__ __forceinline__ float top(int n, int k) const { return fmaxf(m[n][k] * factor[n][k], -FLT_MAX) - kAttnLift; }
     // Of column 2 t + k of n-tile n: channels 32 j + 4 g .. + 3 (not divided by the sum)
     __device__ __forceinline__ float4 output(int j, int n, int k) const {
-        return make_float4(acc[j][0][n][k], acc[j][0][n][k + 2], acc[j][1][n][k], acc[j][1][n][k + 2]);
+        return make_float4(acc[j][0][n][k] * grown, acc[j][0][n][k + 2] * grown, acc[j][1][n][k] * grown, acc[j][1][n][k + 2] * grown);
     }
 
     // Rows c * kRows .. of the queries q0 .. q0 + qn and KV head h (none unless `live`).
@@ -167,7 +168,7 @@ struct AttnRows {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) m[n][k] = limit[n][k] = -FLT_MAX, l[n][k] = 0.f;
-        lift = kAttnLift;
+        grown = 1.f;
         large = kAttnLarge;
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -242,45 +243,61 @@ struct AttnRows {
                     s[n][k] = key >= first_key[n][k & 1] && key < end_key[n][k & 1] ? s[n][k] : -INFINITY;
                 }
         }
-        // ---- does a score pass the running maximum, or a scale what the lift allows? ----
+        // ---- does a score pass the running maximum, or a scale what the sums allow? ----
         uint32_t any = 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int jj = 0; jj < J / 2; ++jj) any |= sv[r][jj];
-        bool passes = (any & large) != 0u;
+        bool moves = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) passes |= fmaxf(s[n][k], s[n][k + 2]) > limit[n][k];
-        if (__any_sync(0xffffffffu, passes)) {
+            for (int k = 0; k < 2; ++k) moves |= fmaxf(s[n][k], s[n][k + 2]) > limit[n][k];
+        if (__any_sync(0xffffffffu, moves || (any & large) != 0u)) {
             float down = 1.f;
             if (__any_sync(0xffffffffu, (any & large) != 0u)) {
-                down = exp2_fast(-kAttnLift);
-                lift = 0.f;
-                large = 0u;
+                uint32_t most = 0;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int jj = 0; jj < J / 2; ++jj) most = max(most, max(sv[r][jj] >> 16, sv[r][jj] & 0xffffu));
+                // the power of two at or below the largest scale so far
+                most = __reduce_max_sync(0xffffffffu, most) & 0x7c00u;
+                const float now = fmaxf(grown, __half2float(__ushort_as_half((uint16_t)most)));
+                down = __fdividef(grown, now);
+                grown = now;
+                large = 0xffffffffu;
+                const float by = __fdividef(1.f, now);
+                const uint32_t by2 = pack_half2(by, by);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = mul_half2(sv[r][jj], by2);
             }
+            if (__any_sync(0xffffffffu, moves) || down != 1.f) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float top = fmaxf(s[n][k], s[n][k + 2]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    top = fmaxf(top, m[n][k]);
-                    const float by = exp2_fast((m[n][k] - top) * factor[n][k]) * down;
-                    m[n][k] = top;
-                    limit[n][k] = top + __fdividef(kAttnSlack, factor[n][k]);
-                    l[n][k] *= by;
+                    for (int k = 0; k < 2; ++k) {
+                        float top = fmaxf(s[n][k], s[n][k + 2]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        top = fmaxf(top, m[n][k]);
+                        const float by = exp2_fast((m[n][k] - top) * factor[n][k]);
+                        m[n][k] = top;
+                        limit[n][k] = top + __fdividef(kAttnSlack, factor[n][k]);
+                        l[n][k] *= by;
 #pragma unroll
-                    for (int j = 0; j < J; ++j)
+                        for (int j = 0; j < J; ++j)
 #pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-                            acc[j][d][n][k] *= by;
-                            acc[j][d][n][k + 2] *= by;
-                        }
-                }
+                            for (int d = 0; d < 2; ++d) {
+                                acc[j][d][n][k] *= by * down;
+                                acc[j][d][n][k + 2] *= by * down;
+                            }
+                    }
+            }
         }
         // ---- weights, and their products with the values ----
         uint32_t b0[NT], b1[NT];
@@ -289,7 +306,7 @@ struct AttnRows {
             float e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                e[k] = exp2_fast(fmaf(s[n][k] - m[n][k & 1], factor[n][k & 1], lift));
+                e[k] = exp2_fast(fmaf(s[n][k] - m[n][k & 1], factor[n][k & 1], kAttnLift));
                 l[n][k & 1] += e[k];
             }
             b0[n] = transpose8(pack_half2(e[0], e[1]));  // head g, keys t and t + 4

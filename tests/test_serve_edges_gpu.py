@@ -22,19 +22,17 @@ def one_request(serve, k, v, ps=64):  # noqa: F811
     return cache, f64(k), f64(v), torch.arange(pages, dtype=torch.int32, device="cuda")[None]
 
 
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("below", [20.2, 24.6, 25.3, 28.0])
-def test_many_weights_far_below_the_largest(serve, below, d):  # noqa: F811
-    """One key outweighs each of the 131071 others by 2^below; together they still count.  So many requests over the same
-    pages that some have all keys in one run."""
+def check_weights_far_below(serve, below, d, size):  # noqa: F811
+    """One key outweighs each of the 131071 others, whose values are `size`, by 2^below; together they still count.  So many
+    requests over the same pages that some have all keys in one run."""
     kv, hq, requests = 131072, 8, 160
-    k, v = np.zeros((kv, 1, d)), np.ones((kv, 1, d))
+    k, v = np.zeros((kv, 1, d)), np.full((kv, 1, d), size)
     k[0], v[0] = 1.0, 0.0
     cache, k, v, table = one_request(serve, k, v)
     q = dev(np.full((requests, hq, d), 1.0), torch.bfloat16)
     scale = below * np.log(2) / k[0].sum()
     want, want_lse, mean, dots = ref.attention(f64(q[:1]), k, v, kv, scale, True, 0)
-    assert want[0, 0, 0] > 2.0 ** -13
+    assert want[0, 0, 0] > 2.0 ** -13 * size
     # A weight is rounded to binary16, to 11 bits or, of small numbers, to a multiple of 2^-24: of weights taken at least
     # 2^7 times as large as they are against the largest, so within 2^-32 of that.
     lost = kv * 2.0 ** -32 * np.abs(v).max()
@@ -49,4 +47,39 @@ def test_many_weights_far_below_the_largest(serve, below, d):  # noqa: F811
         torch.cuda.synchronize()
         assert cache.status() == 0
         assert (np.abs(f64(out) - want) <= tol).all(), (name, f64(out).min(), f64(out).max(), want[0, 0, 0])
+        assert (np.abs(f64(lse) - want_lse) <= score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)).all(), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("below", [20.2, 24.6, 25.3, 28.0])
+def test_many_weights_far_below_the_largest(serve, below, d):  # noqa: F811
+    check_weights_far_below(serve, below, d, 1.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [20.0, 5000.0])
+def test_many_weights_far_below_the_largest_over_large_values(serve, size, d):  # noqa: F811
+    check_weights_far_below(serve, 25.3, d, size)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sizes", [(1e-3, 3.0, 20.0, 300.0, 12000.0), (12000.0, 40.0, 1e-3), (11.0, 13.0, 11.0, 26.0, 1.0)])
+def test_values_whose_size_changes_along_the_keys(serve, sizes, d):  # noqa: F811
+    """Stretches of a thousand keys with values of one size each; weights of like size."""
+    rng = np.random.default_rng(8)
+    each, hq = 1000, 8
+    kv = each * len(sizes)
+    v = rng.standard_normal((kv, 1, d)) * np.repeat(sizes, each)[:, None, None]
+    cache, k, v, table = one_request(serve, rng.standard_normal((kv, 1, d)), np.clip(v, -12000, 12000))
+    q = dev(rng.standard_normal((1, hq, d)), torch.bfloat16)
+    want, want_lse, mean, dots = ref.attention(f64(q), k, v, kv, d ** -0.5, True, 0)
+    # weights and their products: 11 bits, or multiples of 2^-24 of what is 2^7 times as large against the largest value
+    lost = kv * 2.0 ** -32 * np.abs(v).max()
+    tol = U8 * np.abs(want) + (1 + U8) * ((2 * U16 + 2 * score_error(dots, d) + (kv + 64) * U32)[..., None] * mean + lost)
+    for name, (max_q, max_kv) in plans(cache, hq, 1).items():
+        out, lse = torch.empty_like(q), torch.empty(1, hq, device="cuda")
+        cache.attention(q, out, dev(np.array([0, 1], np.int32)), dev(np.array([kv], np.int32)), table, max_q=max_q, max_kv=max_kv, lse=lse)
+        torch.cuda.synchronize()
+        assert cache.status() == 0
+        assert (np.abs(f64(out) - want) <= tol).all(), name
         assert (np.abs(f64(lse) - want_lse) <= score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)).all(), name
