@@ -20,8 +20,8 @@ constexpr float kAttnSlack = 4.f;  // log2 of how far weights may pass 1 before 
 // A weight, and a weight times a value's scale, is rounded to binary16, which has few bits left below 2^-14 and none below
 // 2^-25.  So weights are taken 2^kAttnLift times as large, and scales are brought below 2 by a power of two, which the sums
 // get back at the segment's end: 2^(4 + 10) * 2 fits.  Scales below 2 (values below 12) need no such power; one bit of a scale
-// tells, and the rest is done where a maximum moves.  (60000 keys, values of 2e-4, queries of 4: the result's error 0.2 %, with no lift 1 %; 64 ragged requests take 2 %
-// longer.)
+// tells, and the rest is done where a maximum moves.  (60000 keys, values of 2e-4, queries of 4: the result's error 0.2 %, with
+// no lift 1 %; 64 ragged requests take 2 % longer; over values of 12 and more 8 % longer again.)
 constexpr float kAttnLift = 10.f;
 constexpr uint32_t kAttnLarge = 0x40004000u;  // a bit of two scales each that are 2 or more
 
@@ -80,6 +80,7 @@ struct AttnRows {
     float m[NT][2], limit[NT][2], l[NT][2];
     float acc[J][2][NT][4];
     float grown;                    // what scales are divided by, and so the sums too short by: 1, or 2^k with all scales below 2^(k + 1)
+    uint32_t shrink;                // 1 / grown, twice
     uint32_t large;                 // bits of scales that need a look: kAttnLarge, or all once they are divided
 
     // Of column 2 t + k of n-tile n: the maximum that sum and channels go with, in units of log2.  Of a row that saw
@@ -169,6 +170,7 @@ struct AttnRows {
 #pragma unroll
             for (int k = 0; k < 2; ++k) m[n][k] = limit[n][k] = -FLT_MAX, l[n][k] = 0.f;
         grown = 1.f;
+        shrink = 0x3c003c00u;
         large = kAttnLarge;
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -256,24 +258,30 @@ struct AttnRows {
             for (int k = 0; k < 2; ++k) moves |= fmaxf(s[n][k], s[n][k + 2]) > limit[n][k];
         if (__any_sync(0xffffffffu, moves || (any & large) != 0u)) {
             float down = 1.f;
-            if (__any_sync(0xffffffffu, (any & large) != 0u)) {
+            if (large != kAttnLarge) {
+                any = 0;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int jj = 0; jj < J / 2; ++jj) any |= sv[r][jj] = mul_half2(sv[r][jj], shrink);
+            }
+            if (__any_sync(0xffffffffu, (any & kAttnLarge) != 0u)) {
                 uint32_t most = 0;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int jj = 0; jj < J / 2; ++jj) most = max(most, max(sv[r][jj] >> 16, sv[r][jj] & 0xffffu));
-                // the power of two at or below the largest scale so far
-                most = __reduce_max_sync(0xffffffffu, most) & 0x7c00u;
-                const float now = fmaxf(grown, __half2float(__ushort_as_half((uint16_t)most)));
-                down = __fdividef(grown, now);
-                grown = now;
-                large = 0xffffffffu;
-                const float by = __fdividef(1.f, now);
-                const uint32_t by2 = pack_half2(by, by);
+                // by the power of two at or below the largest scale, these and all that follow
+                const float up = __half2float(__ushort_as_half((uint16_t)(__reduce_max_sync(0xffffffffu, most) & 0x7c00u)));
+                down = __fdividef(1.f, up);
+                const uint32_t by = pack_half2(down, down);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = mul_half2(sv[r][jj], by2);
+                    for (int jj = 0; jj < J / 2; ++jj) sv[r][jj] = mul_half2(sv[r][jj], by);
+                grown *= up;
+                shrink = mul_half2(shrink, by);
+                large = 0xffffffffu;
             }
             if (__any_sync(0xffffffffu, moves) || down != 1.f) {
 #pragma unroll
