@@ -4,10 +4,11 @@
 // A row is one query of one head.  A CTA takes a segment: TILES x 128 rows of
 // one request and KV head, and walks the keys that any of them sees, 128 at a
 // time.  Four warps unpack a tile of the cache: V as binary16 (code * scale,
-// rounded to 11 bits), K as two binary16 numbers whose sum is code * scale
-// exactly (codes of 3 * 2^i times an 11-bit scale have 13 bits), so that scores
-// keep the accuracy of their binary32 accumulation; the second costs half as
-// much again in tensor work.  One thread issues
+// rounded to 11 bits), K as two binary16 numbers whose sum is 2 * code * scale
+// exactly (codes of 3 * 2^i times an 11-bit scale have 13 bits, and twice the
+// smallest product's last one, 2^-25, is binary16's smallest number), so that
+// scores keep the accuracy of their binary32 accumulation; the second costs half
+// as much again in tensor work.  One thread issues
 //     S_i = Q_i K_hi^T + Q_i K_lo^T,   O_i += P_i V      (tcgen05.mma, sums in TMEM)
 // and a warpgroup for each tile i turns S_i into weights P_i, in place: a thread
 // has a row, so maxima and sums need no exchange.  While one tile's scores are
@@ -432,6 +433,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                             most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
                     }
                     attn_row_scale(p, most, down, factor);
+                    factor *= 0.5f;  // K is held twice as large
 #pragma unroll
                     for (int k = 0; k < D / 8; ++k) {
                         const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -673,7 +675,8 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     x[i].s[k] = here ? *((const uint32_t*)(at.block[i] + scales + row * B::kScaleRow) + k) : 0u;
             }
         };
-        // Half a row's codes as binary16 into their place of a swizzled tile; with_rest the part that rounding lost into `rest`.
+        // Half a row's codes as binary16 into their place of a swizzled tile; with_rest twice as large, and the part that
+        // rounding lost into `rest`.
         const uint32_t row_at = key_in * 128;
         auto unpack = [&](const Codes& x, uint32_t to, uint32_t rest, auto with_rest) {
             uint32_t wd[4 * kLoads];
@@ -685,11 +688,12 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
 #pragma unroll
                 for (int jh = 0; jh < J / 2; ++jh) {
                     uint32_t even[4], odd[4];
+                    const uint32_t s = decltype(with_rest)::value ? half2_mul(x.s[jh], 0x40004000u) : x.s[jh];
                     from_e2m1x8(wd[c * (J / 2) + jh], even);
                     from_e2m1x8(wd[(c + 1) * (J / 2) + jh], odd);
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj) {
-                        const uint32_t s2 = __byte_perm(x.s[jh], 0u, jj ? 0x3232u : 0x1010u);
+                        const uint32_t s2 = __byte_perm(s, 0u, jj ? 0x3232u : 0x1010u);
                         const uint32_t v[4] = {even[2 * jj], even[2 * jj + 1], odd[2 * jj], odd[2 * jj + 1]};
                         uint32_t h[4];
 #pragma unroll

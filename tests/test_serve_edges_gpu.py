@@ -83,3 +83,32 @@ def test_values_whose_size_changes_along_the_keys(serve, sizes, d):  # noqa: F81
         assert cache.status() == 0
         assert (np.abs(f64(out) - want) <= tol).all(), name
         assert (np.abs(f64(lse) - want_lse) <= score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)).all(), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("code", [0.5, 1.5, 3.0])
+def test_scores_of_keys_at_the_smallest_scales(serve, code, d):  # noqa: F811
+    """Scales whose last bit is 2^-24, under queries that make scores of them: a score has every key's bits."""
+    kv, hq = 300, 8
+    s = (1025 + 4 * (np.arange(kv) % 250)) * 2.0 ** -24  # half of one, and 1 1/2, lie between two multiples of 2^-24
+    k = np.repeat((code * s)[:, None], d, 1)
+    k[:, ::32] = (6 * s)[:, None]
+    v = np.random.default_rng(5).standard_normal((kv, 1, d))
+    cache, held, v, table = one_request(serve, k[:, None], v)
+    assert np.array_equal(held[:, 0], k)
+    x = np.full((2, hq, d), 60000.0) * (1 + np.arange(hq) / 16)[None, :, None]
+    x[..., ::32] = 0
+    q = dev(x, torch.bfloat16)
+    scale = 0.2 / code / d ** 0.5
+    want, want_lse, mean, dots = ref.attention(f64(q), held, v, kv, scale, True, 0)
+    assert dots.min() > 3
+    for name, (max_q, max_kv) in plans(cache, hq, 1).items():
+        out, lse = torch.empty_like(q), torch.empty(2, hq, device="cuda")
+        cache.attention(q, out, dev(np.array([0, 2], np.int32)), dev(np.array([kv], np.int32)), table, max_q=max_q, max_kv=max_kv,
+                        scale=scale, lse=lse)
+        torch.cuda.synchronize()
+        assert cache.status() == 0
+        tol = score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)
+        assert (np.abs(f64(lse) - want_lse) <= tol).all(), (name, np.abs(f64(lse) - want_lse).max(), tol.min())
+        e = (2 * U16 + 2 * score_error(dots, d) + (kv + 64) * U32)[..., None]
+        assert (np.abs(f64(out) - want) <= U8 * np.abs(want) + (1 + U8) * e * mean).all(), name
