@@ -218,8 +218,9 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  *   first 4096 zero before its first use; every call leaves it ready for the
  *   next.  Calls that share a workspace are ordered on one stream.
  *   Its first 32-bit word is a status: RRA_OK, or RRA_ERR_TIMEOUT if a wait for
- *   the kernel's own copies ran out (results are then not valid); the
- *   caller clears it.
+ *   the kernel's own copies or products ran out.  The results of that call are
+ *   then not valid, nor are later ones until the caller has set the word to 0,
+ *   in the order of the stream; the rest of the workspace is ready all the same.
  * requests 0..RRA_SERVE_MAX_REQUESTS; q_heads a multiple of kv_heads; tokens *
  * q_heads and table_pages * page_tokens up to 2^30 - 1. */
 typedef struct {

@@ -283,12 +283,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) copy_next();
 
-        auto drain = [&]() {  // waits for every copy, but no longer than a wait may take
-            const uint64_t start = globaltimer_ns();
+        auto drain = [&]() {  // waits for every copy
 #pragma unroll 1
-            for (int i = 0; i < kStages; ++i)
-                while (!attn_try(bars + 8 * i, (issued >> i & 1u) ^ 1u))
-                    if (globaltimer_ns() - start > kAttnWaitNs) break;
+            for (int i = 0; i < kStages; ++i) attn_wait_quiet(bars + 8 * i, (issued >> i & 1u) ^ 1u);
         };
         int take = 0;
         uint32_t phase = 0;

@@ -14,7 +14,14 @@ namespace rra {
 constexpr int kAttnTile = 32;      // keys of one step of a warp
 constexpr int kTeamWarps = 4;      // warps of a CTA of serve_attn_team.cu: one for each scheduler, a tile is a chain of latencies
 constexpr int kAttnMaxCtas = 512;  // CTAs a workspace has room for
-constexpr uint64_t kAttnWaitNs = 1000000000;  // a wait gives up after this long
+// A wait gives up after kAttnWaitNs, one try of it after about kAttnTryNs.  Both are 0 in a build that a test makes, so that
+// waits do run out: what is not done when it is first looked at is given up.
+#ifndef RRA_ATTN_WAIT_NS
+#define RRA_ATTN_WAIT_NS 1000000000
+#define RRA_ATTN_TRY_NS 20000
+#endif
+constexpr uint32_t kAttnWaitNs = RRA_ATTN_WAIT_NS, kAttnTryNs = RRA_ATTN_TRY_NS;
+constexpr uint32_t kAttnQuietNs = 1000000000;  // the same for what must not be in flight any more
 constexpr int kAttnMaxRows = 16;
 
 // Start of the workspace: status word, then a counter for each CTA, then two
@@ -28,14 +35,21 @@ struct AttnWorkspace {
 static_assert(sizeof(AttnWorkspace) == 4096, "the part of the workspace that starts as zero");
 // One try of a wait on a barrier of this CTA: returns when its phase is done, or after about kAttnTryNs.  Acquire in the
 // CTA only: at cluster scope every try also drops the L1 cache.
-constexpr uint32_t kAttnTryNs = 20000;
 __device__ __forceinline__ bool attn_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
+#if RRA_ATTN_TRY_NS == 0
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+#else
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(bar), "r"(parity), "r"(kAttnTryNs)
         : "memory");
+#endif
     return done != 0;
 }
 // The rest of a wait whose first try did not see the phase done.  Gives up after kAttnWaitNs, or soon after another wait
@@ -44,13 +58,20 @@ __device__ __forceinline__ bool attn_wait_slow(uint32_t bar, uint32_t parity, At
     const uint64_t start = globaltimer_ns();
     while (!attn_try(bar, parity)) {
         const uint64_t waited = globaltimer_ns() - start;
-        if (waited > kAttnWaitNs) {
+        if (waited >= kAttnWaitNs) {
             atomicCAS(&ws->status, 0u, (uint32_t)RRA_ERR_TIMEOUT);
             return false;
         }
         if (waited > kStatusAfterNs && ld_relaxed_u32(&ws->status) != 0u) return false;
     }
     return true;
+}
+
+// Waits for what must not be in flight any more: copies and products that a wait gave up on.
+__device__ __forceinline__ void attn_wait_quiet(uint32_t bar, uint32_t parity) {
+    const uint64_t start = globaltimer_ns();
+    while (!attn_try(bar, parity))
+        if (globaltimer_ns() - start > kAttnQuietNs) break;
 }
 
 struct AttnParams {

@@ -207,12 +207,8 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 3) kv_attention_team_kernel(c
         if (size > 1) cluster_sync();  // the parts have been read
         else __syncthreads();
     }
-    if (dead) {  // copies that a wait gave up on: until they are done, but no longer than a wait may take
-        const uint64_t start = globaltimer_ns();
-        for (int i = 0; i < kTeamStages; ++i)
-            while (!attn_try(bars + 8 * i, (issued >> i & 1u) ^ 1u))
-                if (globaltimer_ns() - start > kAttnWaitNs) break;
-    }
+    if (dead)  // copies that a wait gave up on
+        for (int i = 0; i < kTeamStages; ++i) attn_wait_quiet(bars + 8 * i, (issued >> i & 1u) ^ 1u);
 }
 
 rra_status_t launch_team(const AttnParams& p, int chunks, int size, rra_stream_t stream) {

@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     __shared__ volatile int32_t places[4][9];  // of four tiles: the cache's blocks of its keys (-1: none), and how many keys there are
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t arrived[2][TILES];  // of the run's first and last segment
+    __shared__ volatile uint32_t added[2][TILES];    // whether this CTA has counted itself there
     __shared__ PromptSegment start;
     const rra_kv_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
     pdl_release_early();
     if (tid == 0) {
         for (int i = 0; i < TILES; ++i) {
+            added[0][i] = added[1][i] = 0u;
             mbar_init(q_full + 8 * i, kPromptRows + kTurn);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(pv_full + 8 * i, kPromptRows + 128 + kTurn);
@@ -582,7 +584,10 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     ((float2*)(to + D / 4 * kPromptRows))[row] = make_float2(top, l);
                     __threadfence();
                     ok = meet();
-                    if (ok && row == 0) others = atomicAdd(count, 1u);
+                    if (ok && row == 0) {
+                        others = atomicAdd(count, 1u);
+                        added[starts ? 1 : 0][i] = 1u;
+                    }
                     ok = ok && meet();
                     if (!ok) break;
                 }
@@ -636,6 +641,21 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             tc_before_sync();
             prompt_next<Sh::kRows>(p, seg);
         }
+        // A wait ran out: the results are lost, but the counters of the segments from here on have to be zero for the next
+        // call.  So this CTA still counts itself, and whoever is last there clears them.
+        if (!ok && row == 0)
+#pragma unroll 1
+            while (true) {
+                const int which = seg.begin >= r0 ? 1 : 0;
+                if (which == 0 || seg.end > r1) {
+                    const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
+                    uint32_t* const count = &ws->arrived[i0 * TILES + i];
+                    const uint32_t before = added[which][i] != 0u ? arrived[which][i] : atomicAdd(count, 1u);
+                    if (before == (uint32_t)(i1 - i0)) *count = 0u;
+                }
+                if (seg.end >= r1) break;
+                prompt_next<Sh::kRows>(p, seg);
+            }
     } else if (warp < Sh::kIssue) {
         // =============================== unpacking: a thread has half a row of two keys, 64 apart ====
         // so that a half of V's keys is unpacked while products still read the other
@@ -844,7 +864,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         if (i < TILES) {
             if (elected()) tc_commit(drained);
             __syncwarp();
-            wait(drained, 0);
+            attn_wait_quiet(drained, 0);
         }
     }
     tc_before_sync();

@@ -176,3 +176,8 @@ class KvCache:
     def status(self) -> int:
         """Status word of the attention calls so far (0 is fine); synchronises."""
         return int(self._workspace[:4].cpu().view(torch.int32).item())
+
+    def reset(self) -> None:
+        """Sets the status back to 0, in the order of the current stream: after a
+        status that is not, attention() gives valid results from here on."""
+        self._workspace[:_WORKSPACE_HEAD].zero_()

@@ -112,3 +112,80 @@ def test_scores_of_keys_at_the_smallest_scales(serve, code, d):  # noqa: F811
         assert (np.abs(f64(lse) - want_lse) <= tol).all(), (name, np.abs(f64(lse) - want_lse).max(), tol.min())
         e = (2 * U16 + 2 * score_error(dots, d) + (kv + 64) * U32)[..., None]
         assert (np.abs(f64(out) - want) <= U8 * np.abs(want) + (1 + U8) * e * mean).all(), name
+
+
+@pytest.fixture(scope="module")
+def impatient(tmp_path_factory):
+    """The operators built with waits that run out at once."""
+    import ctypes
+    import subprocess
+
+    from latency_barrier_free_gb300 import build_ext as be
+
+    at = tmp_path_factory.mktemp("impatient")
+    units = [f for f in be.SOURCES if f.startswith("serve")]
+    run = [subprocess.Popen([be.nvcc(), *be.ARCH, *be.FLAGS, "-DRRA_ATTN_WAIT_NS=0", "-DRRA_ATTN_TRY_NS=0", "-c",
+                             "%s/%s" % (be.CSRC, f), "-o", str(at / f) + ".o"], stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL)
+           for f in units]
+    assert [p.wait() for p in run] == [0] * len(units)
+    subprocess.run([be.nvcc(), *be.ARCH, "-shared", "-cudart", "static", "-o", str(at / "lib.so"), *(str(at / f) + ".o" for f in units)],
+                   check=True, stdout=subprocess.DEVNULL)
+    lib = ctypes.CDLL(str(at / "lib.so"))
+    lib.rra_kv_attention.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    return lib
+
+
+def arguments(serve, cache, q, out, lse, cu, kv, table, max_q, max_kv):  # noqa: F811
+    """The C structure of an attention call."""
+    s = q.stride(0), q.stride(1), out.stride(0), out.stride(1)
+    return serve._ATTN.pack(*serve._CACHE.unpack(cache._cache), q.data_ptr(), out.data_ptr(), lse.data_ptr(), cu.data_ptr(),
+                            kv.data_ptr(), table.data_ptr(), cache._workspace.data_ptr(), *s, table.stride(0), q.shape[0],
+                            q.shape[2] ** -0.5, kv.numel(), table.shape[1], q.shape[1], max_q, max_kv, 1, 0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_after_a_wait_ran_out_the_next_call_is_right(serve, impatient, d):  # noqa: F811
+    """The call says that its waits ran out, and leaves the workspace as calls expect it."""
+    from latency_barrier_free_gb300 import rra
+
+    hq, hk, ps = 16, 2, 64
+    new, kv = [40, 300, 7, 0] + [1] * 60, [5000, 9000, 300, 10] + [9000] * 60
+    held = [-(-n // ps) for n in kv]
+    cache = cache_of(serve, sum(held), ps, hk, d)
+    table, used = torch.full((len(kv), max(held)), -1, dtype=torch.int32, device="cuda"), 0
+    for b, n in enumerate(held):
+        table[b, :n] = torch.arange(used, used + n, device="cuda")
+        used += n
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    for at in range(0, used * ps, 1 << 16):
+        slots = torch.arange(at, min(at + (1 << 16), used * ps), device="cuda")
+        cache.append(*(torch.randn(len(slots), hk, d, generator=gen, device="cuda") for _ in range(2)), slots)
+    rng, flush = np.random.default_rng(12), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    q = dev(rng.standard_normal((sum(new), hq, d)), torch.bfloat16)
+    cu, kv_d = dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)), dev(np.array(kv, np.int32))
+    head = cache._workspace[:4096].view(torch.int32)
+    stream, ran_out = torch.cuda.current_stream().cuda_stream, set()
+    for name, (max_q, max_kv) in plans(cache, hq, len(new)).items():
+        want, lse = torch.empty_like(q), torch.empty(q.shape[0], hq, device="cuda")
+        out, lse2 = torch.empty_like(want), torch.empty_like(lse)
+        cache.attention(q, want, cu, kv_d, table, max_q=max_q, max_kv=max_kv, lse=lse)
+        assert cache.status() == 0
+        for way in ("the word", "reset()"):
+            for _ in range(20):
+                flush.fill_(0)  # copies come from memory, not from L2
+                args = arguments(serve, cache, q, out, lse2, cu, kv_d, table, max_q, max_kv)
+                assert impatient.rra_kv_attention(args, stream) == rra.OK
+                if cache.status() != 0:
+                    assert cache.status() == rra.ERR_TIMEOUT
+                    ran_out.add(name)
+                assert (head[1:] == 0).all(), name
+            if way == "the word":
+                head[0] = 0
+            else:
+                cache.reset()
+            for _ in range(2):
+                out.fill_(7.0)
+                cache.attention(q, out, cu, kv_d, table, max_q=max_q, max_kv=max_kv, lse=lse2)
+                assert cache.status() == 0 and torch.equal(out, want) and torch.equal(lse2, lse), name
+    # the kernels that count arrivals in the workspace; small ones may find their few copies done
+    assert {"kv_attention_kernel", "kv_attention_prompt_kernel"} <= {n.split("<")[0] for n in ran_out}, ran_out
