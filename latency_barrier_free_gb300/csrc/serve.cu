@@ -542,7 +542,7 @@ __device__ __forceinline__ KvPair kv_pair(const KvTokensParams& p, int i) {
     const rra_kv_cache_t& c = p.a.cache;
     r.token = p.by_heads(i);
     r.head = i - r.token * p.by_heads.d;
-    const int64_t slot = __ldg(p.a.slots + r.token);
+    const int64_t slot = p.a.slots[r.token];  // not through the non-coherent path: written while this grid is resident already
     r.row = (int)slot & (kKvBlockTokens - 1);
     r.block = -1;
     if ((uint64_t)slot < (uint64_t)p.room) {

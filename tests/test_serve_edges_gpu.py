@@ -189,3 +189,44 @@ def test_after_a_wait_ran_out_the_next_call_is_right(serve, impatient, d):  # no
                 assert cache.status() == 0 and torch.equal(out, want) and torch.equal(lse2, lse), name
     # the kernels that count arrivals in the workspace; small ones may find their few copies done
     assert {"kv_attention_kernel", "kv_attention_prompt_kernel"} <= {n.split("<")[0] for n in ran_out}, ran_out
+
+
+@pytest.mark.parametrize("heads", [1, 8])
+def test_steps_back_to_back_over_the_same_slots(serve, heads):  # noqa: F811
+    """slot_map writes the slots that the write right behind it reads, step after step in one buffer, nothing in between."""
+    n, ps, d, steps, width = 48, 16, 64, 60, 12
+    pool = n * width
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    kv, table, cu, pos, short = i32(n), torch.full((n, width), -1, dtype=torch.int32, device="cuda"), i32(n + 1), i32(3 * n), i32(1)
+    order = np.random.default_rng(2).permutation(pool).astype(np.int32)
+    free, left = dev(order), torch.full((1,), pool, dtype=torch.int32, device="cuda")
+    slots = torch.full((3 * n,), -1, dtype=torch.int64, device="cuda")
+    cache = cache_of(serve, pool, ps, heads, d)
+    rng = np.random.default_rng(3)
+    new = rng.integers(0, 4, (steps, n)).astype(np.int32)
+    new_d = dev(new)
+    # the token at position p of request b has the value 2^((7 b + p) % 11) everywhere; its scale, a sixth of that, has 11 bits
+    value = lambda b, p: 2.0 ** ((7 * b + p) % 11)  # noqa: E731
+    x, at = np.zeros((steps, 3 * n, heads, d), np.float32), np.zeros(n, np.int64)
+    for s in range(steps):
+        b = np.repeat(np.arange(n), new[s])
+        p = np.concatenate([np.arange(a, a + m) for a, m in zip(at, new[s])])
+        x[s, :len(b)] = value(b, p)[:, None, None]
+        at += new[s]
+    x = dev(x, torch.bfloat16)
+    torch.cuda.synchronize()
+    for s in range(steps):
+        serve.slot_map(kv, new_d[s], table, free, left, ps, kv_len=kv, cu_new=cu, slots=slots, positions=pos, free_left=left,
+                       pages_short=short)
+        cache.append(x[s], x[s], slots)
+    torch.cuda.synchronize()
+    assert kv.tolist() == at.tolist() and short.item() == 0 and at.max() <= width * ps
+    rows = table.cpu().numpy()
+    b = np.repeat(np.arange(n), at)
+    p = np.concatenate([np.arange(m) for m in at])
+    held = dev(rows[b, p // ps].astype(np.int64) * ps + p % ps)
+    k, v = (torch.empty(len(b), heads, d, device="cuda") for _ in range(2))
+    cache.read(held, k, v)
+    want = np.broadcast_to(value(b, p)[:, None, None], k.shape)
+    assert (np.abs(f64(k) - want) <= 2.0 ** -10 * want).all()
+    assert torch.equal(k, v)
