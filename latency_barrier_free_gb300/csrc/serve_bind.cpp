@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -40,10 +41,17 @@ const at::Tensor& tensor(const char* name, PyObject* o) {
     return THPVariable_Unpack(o);
 }
 
-// A tensor's GPU; refuses what is on none.
+// Refuses a GPU that is not the current one: a kernel would run on that one, with this one's addresses.
+int on_current(int device) {
+    const int now = (int)c10::cuda::current_device();
+    if (device != now) refuse(PyExc_ValueError, "tensors on cuda:%d, but the current GPU is cuda:%d", device, now);
+    return device;
+}
+
+// A tensor's GPU, the current one; refuses what is on none.
 int device_of(const char* name, const at::Tensor& t) {
     if (!t.is_cuda()) refuse(PyExc_ValueError, "%s must be a CUDA tensor", name);
-    return (int)t.get_device();
+    return on_current((int)t.get_device());
 }
 
 void check(const char* name, const at::Tensor& t, at::ScalarType type, int device, bool fine, const char* what) {
@@ -197,7 +205,7 @@ long kv_tokens(PyObject* const* v, Py_ssize_t n, Operator<rra_kv_tokens_args_t> 
     arguments(n, 6);
     rra_kv_tokens_args_t a = {};
     a.cache = cache_of(v[0]);
-    const int dev = integer32(v[1]);
+    const int dev = on_current(integer32(v[1]));
     const at::Tensor &k = tensor("k", v[2]), &slots = tensor("slots", v[4]);
     const at::ScalarType type = k.scalar_type();
     a.dtype = value_dtype(type);
@@ -216,7 +224,7 @@ long kv_attention(PyObject* const* v, Py_ssize_t n) {
     arguments(n, 15);
     rra_kv_attention_args_t a = {};
     a.cache = cache_of(v[0]);
-    const int dev = integer32(v[1]);
+    const int dev = on_current(integer32(v[1]));
     const at::Tensor &q = tensor("q", v[3]), &kv = tensor("kv_len", v[6]);
     if (q.dim() != 3 || q.size(2) != a.cache.head_dim || q.size(1) < 1 || q.size(1) % a.cache.kv_heads != 0 || q.size(1) > INT32_MAX)
         refuse(PyExc_ValueError, "q must be [tokens, heads, %d], heads a multiple of %d", a.cache.head_dim, a.cache.kv_heads);

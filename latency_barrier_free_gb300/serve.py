@@ -4,7 +4,8 @@ Page bookkeeping, head norms with position rotation, a key/value cache held in
 4 bits, and the attention over it: what a tensor-parallel rank runs around its
 AllReduces.  As in rra.py this is argument checking and marshalling only (in
 _serve.so, csrc/serve_bind.cpp); every call enqueues one kernel of librra.so on the
-current stream (or `stream`), and there is no fallback.
+current stream (or `stream`), and there is no fallback.  Tensors are on the current
+GPU; those of another one are refused.
 """
 from __future__ import annotations
 

@@ -230,3 +230,20 @@ def test_steps_back_to_back_over_the_same_slots(serve, heads):  # noqa: F811
     want = np.broadcast_to(value(b, p)[:, None, None], k.shape)
     assert (np.abs(f64(k) - want) <= 2.0 ** -10 * want).all()
     assert torch.equal(k, v)
+
+
+def test_a_gpu_that_is_not_the_current_one_is_refused(serve):  # noqa: F811
+    """Said of the cache's GPU, before any tensor is looked at: one GPU is enough to see it."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = cache_of(serve, 4, 16, 2, 64)
+    other, k, slots = cache._dev + 1, bf(3, 2, 64), torch.zeros(3, dtype=torch.int64, device="cuda")
+    native = serve._native
+    for call in (lambda: native.kv_append(cache._cache, other, k, k, slots, None),
+                 lambda: native.kv_read(cache._cache, other, k, k, slots, None),
+                 lambda: native.kv_attention(cache._cache, other, cache._at, bf(1, 2, 64), bf(1, 2, 64), i32(2), i32(1), i32(1, 4),
+                                             1, 1, 1.0, True, 0, None, None)):
+        with pytest.raises(ValueError, match="the current GPU is cuda:%d" % cache._dev):
+            call()
+    cache.append(k, k, slots)
+    torch.cuda.synchronize()
