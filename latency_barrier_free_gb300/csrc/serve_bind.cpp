@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -219,16 +220,18 @@ long kv_tokens(PyObject* const* v, Py_ssize_t n, Operator<rra_kv_tokens_args_t> 
 long kv_append(PyObject* const* v, Py_ssize_t n) { return kv_tokens(v, n, fn_append); }
 long kv_read(PyObject* const* v, Py_ssize_t n) { return kv_tokens(v, n, fn_read); }
 
-// (cache, device, workspace's address, q, out, cu_q, kv_len, block_table, max_q, max_kv, scale, causal, window, lse, stream)
+// (cache, device, workspace, q, out, cu_q, kv_len, block_table, max_q, max_kv, scale, causal, window, lse, stream, the
+// workspace's own stream)
 long kv_attention(PyObject* const* v, Py_ssize_t n) {
-    arguments(n, 15);
+    arguments(n, 16);
     rra_kv_attention_args_t a = {};
     a.cache = cache_of(v[0]);
     const int dev = on_current(integer32(v[1]));
     const at::Tensor &q = tensor("q", v[3]), &kv = tensor("kv_len", v[6]);
     if (q.dim() != 3 || q.size(2) != a.cache.head_dim || q.size(1) < 1 || q.size(1) % a.cache.kv_heads != 0 || q.size(1) > INT32_MAX)
         refuse(PyExc_ValueError, "q must be [tokens, heads, %d], heads a multiple of %d", a.cache.head_dim, a.cache.kv_heads);
-    a.workspace = (void*)(uintptr_t)integer(v[2]);
+    const at::Tensor& workspace = tensor("workspace", v[2]);
+    a.workspace = workspace.data_ptr();
     a.tokens = q.size(0);
     a.q_heads = (int32_t)q.size(1);
     a.q = rows("q", q, at::kBFloat16, q.sizes(), dev, &a.q_token_stride, &a.q_head_stride);
@@ -245,7 +248,13 @@ long kv_attention(PyObject* const* v, Py_ssize_t n) {
     if (v[13] != Py_None) a.lse = flat<float>("lse", v[13], at::kFloat, a.tokens * a.q_heads, dev);
     if (requests > RRA_SERVE_MAX_REQUESTS) return RRA_ERR_INVALID_ARG;
     a.requests = (int32_t)requests;
-    return fn_attention(&a, stream_of(v[14], dev));
+    const rra_stream_t stream = stream_of(v[14], dev);
+    // The caller does not know the workspace: its memory must not go to another tensor before this call's work is done.  (Of a
+    // stream given by its number nothing is known, not even whether it still exists then: there the caller keeps the cache.)
+    if (stream != (rra_stream_t)PyLong_AsVoidPtr(v[15]) && !PyLong_Check(v[14]))
+        c10::cuda::CUDACachingAllocator::recordStream(workspace.storage().data_ptr(),
+                                                      c10::cuda::getStreamFromExternal((cudaStream_t)stream, (c10::DeviceIndex)dev));
+    return fn_attention(&a, stream);
 }
 
 // ---------------------------------------------------------------- module ----

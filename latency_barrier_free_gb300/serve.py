@@ -118,7 +118,9 @@ class KvCache:
     `pages` is a contiguous uint8 CUDA tensor of whole pages (kv_page_bytes()
     each; their layout stands in rra_serve.h); it needs no initialisation.  The
     object holds the attention's workspace, so its attention() calls are ordered
-    on one stream; append() and read() are not bound to it."""
+    on one stream, any one; append() and read() are not bound to it.  It may go
+    once they are enqueued, but for calls whose stream was given as a number: for
+    those it is kept until their work is done."""
 
     def __init__(self, pages, page_tokens: int, kv_heads: int, head_dim: int):
         lib = _lib()
@@ -132,8 +134,11 @@ class KvCache:
         self._workspace = torch.empty(lib.rra_kv_attention_workspace_bytes(head_dim), dtype=torch.uint8,
                                       device=pages.device)
         self._workspace[:_WORKSPACE_HEAD].zero_()
+        own = torch.cuda.current_stream(self._dev)
+        if not torch.cuda.is_current_stream_capturing():
+            own.synchronize()  # calls on other streams find the zeros
+        self._home = own.cuda_stream
         self._cache = _CACHE.pack(pages.data_ptr(), self.num_pages, self.page_tokens, self.kv_heads, self.head_dim, 0)
-        self._at = self._workspace.data_ptr()
         self._scale = 1.0 / math.sqrt(head_dim)
 
     def append(self, k, v, slots, stream=None) -> None:
@@ -156,15 +161,15 @@ class KvCache:
         and the first kv_len[b] tokens of its row of block_table, its own
         included; max_q and max_kv are what to plan for.  scale defaults to
         1/sqrt(head_dim).  lse: float32 [tokens, q_heads], optional."""
-        st = _native.kv_attention(self._cache, self._dev, self._at, q, out, cu_q, kv_len, block_table, max_q, max_kv,
-                                  self._scale if scale is None else scale, causal, window, lse, stream)
+        st = _native.kv_attention(self._cache, self._dev, self._workspace, q, out, cu_q, kv_len, block_table, max_q, max_kv,
+                                  self._scale if scale is None else scale, causal, window, lse, stream, self._home)
         if st:
             raise rra.RraError(st, "rra_kv_attention")
 
     def plan_kernel(self, q_heads: int, requests: int, *, max_q: int, max_kv: int) -> str:
         """Name of the kernel that attention() launches for so many query heads
         and requests, planned for max_q and max_kv."""
-        some = self._at  # planning reads no memory
+        some = self._workspace.data_ptr()  # planning reads no memory
         d = self.head_dim
         args = _ATTN.pack(*_CACHE.unpack(self._cache), some, some, 0, some, some, some, some, q_heads * d, d, q_heads * d, d, 1,
                           requests, self._scale, requests, 1, q_heads, max_q, max_kv, 1, 0, 0)

@@ -241,9 +241,43 @@ def test_a_gpu_that_is_not_the_current_one_is_refused(serve):  # noqa: F811
     native = serve._native
     for call in (lambda: native.kv_append(cache._cache, other, k, k, slots, None),
                  lambda: native.kv_read(cache._cache, other, k, k, slots, None),
-                 lambda: native.kv_attention(cache._cache, other, cache._at, bf(1, 2, 64), bf(1, 2, 64), i32(2), i32(1), i32(1, 4),
-                                             1, 1, 1.0, True, 0, None, None)):
+                 lambda: native.kv_attention(cache._cache, other, cache._workspace, bf(1, 2, 64), bf(1, 2, 64), i32(2), i32(1),
+                                             i32(1, 4), 1, 1, 1.0, True, 0, None, None, 0)):
         with pytest.raises(ValueError, match="the current GPU is cuda:%d" % cache._dev):
             call()
     cache.append(k, k, slots)
     torch.cuda.synchronize()
+
+
+def test_the_workspace_on_another_stream_than_its_own(serve):  # noqa: F811
+    """Made behind other work on one stream, used on another, and gone before that work is done."""
+    rng = np.random.default_rng(6)
+    kv, hk, hq, d = 3000, 2, 8, 64
+    cache, k, v, table = one_request(serve, rng.standard_normal((kv, hk, d)), rng.standard_normal((kv, hk, d)))
+    q = dev(rng.standard_normal((30, hq, d)), torch.bfloat16)
+    cu, kv_d = dev(np.array([0, 30], np.int32)), dev(np.array([kv], np.int32))
+    away = torch.cuda.Stream()
+    for max_q, max_kv in plans(cache, hq, 1).values():
+        want, out = torch.empty_like(q), torch.zeros_like(q)
+        cache.attention(q, want, cu, kv_d, table, max_q=max_q, max_kv=max_kv)
+        size = cache._workspace.numel()
+        dirt = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        del dirt
+        torch.cuda._sleep(10 ** 7)
+        fresh = serve.KvCache(cache.pages, cache.page_tokens, hk, d)
+        with torch.cuda.stream(away):
+            fresh.attention(q, out, cu, kv_d, table, max_q=max_q, max_kv=max_kv)
+        away.synchronize()
+        assert torch.equal(out, want) and fresh.status() == 0
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(away):
+            torch.cuda._sleep(10 ** 7)
+            fresh.attention(q, out, cu, kv_d, table, max_q=max_q, max_kv=max_kv)
+        at = fresh._workspace.data_ptr()
+        del fresh
+        dirt = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        assert at not in [x.data_ptr() for x in dirt]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
