@@ -180,7 +180,9 @@ class KvCache:
         return name.value.decode()
 
     def status(self) -> int:
-        """Status word of the attention calls so far (0 is fine); synchronises."""
+        """Status word of the attention calls so far (0 is fine), whatever their
+        stream; synchronises with the GPU."""
+        torch.cuda.synchronize(self._dev)
         return int(self._workspace[:4].cpu().view(torch.int32).item())
 
     def reset(self) -> None:

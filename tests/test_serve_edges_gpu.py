@@ -281,3 +281,15 @@ def test_the_workspace_on_another_stream_than_its_own(serve):  # noqa: F811
         assert at not in [x.data_ptr() for x in dirt]
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_status_of_work_on_another_stream(serve):  # noqa: F811
+    cache = cache_of(serve, 1, 16, 1, 64)
+    away = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(away):
+        torch.cuda._sleep(10 ** 7)
+        cache._workspace[:4].view(torch.int32).fill_(5)
+    assert cache.status() == 5
+    cache.reset()
+    assert cache.status() == 0
