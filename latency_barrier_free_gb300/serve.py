@@ -166,13 +166,13 @@ class KvCache:
         if st:
             raise rra.RraError(st, "rra_kv_attention")
 
-    def plan_kernel(self, q_heads: int, requests: int, *, max_q: int, max_kv: int) -> str:
+    def plan_kernel(self, q_heads: int, requests: int, *, max_q: int, max_kv: int, window: int = 0) -> str:
         """Name of the kernel that attention() launches for so many query heads
-        and requests, planned for max_q and max_kv."""
+        and requests and this window, planned for max_q and max_kv."""
         some = self._workspace.data_ptr()  # planning reads no memory
         d = self.head_dim
         args = _ATTN.pack(*_CACHE.unpack(self._cache), some, some, 0, some, some, some, some, q_heads * d, d, q_heads * d, d, 1,
-                          requests, self._scale, requests, 1, q_heads, max_q, max_kv, 1, 0, 0)
+                          requests, self._scale, requests, 1, q_heads, max_q, max_kv, 1, window, 0)
         name = ctypes.c_char_p()
         st = _lib().rra_kv_attention_plan(args, ctypes.byref(name))
         if st:

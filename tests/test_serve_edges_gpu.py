@@ -293,3 +293,89 @@ def test_status_of_work_on_another_stream(serve):  # noqa: F811
     assert cache.status() == 5
     cache.reset()
     assert cache.status() == 0
+
+
+def dense(q, k, v, scale, causal, window):
+    """serve_ref.attention on the GPU: q [n, hq, d], k and v [kv, hk, d], float64.  Returns out, lse, mean |v| under the
+    weights, and the largest sum of |q_i k_i| * |scale|, as numpy arrays."""
+    n, hq, _ = q.shape
+    kv, hk, _ = k.shape
+    if kv == 0:
+        return np.zeros(q.shape), np.full((n, hq), -np.inf), np.zeros(q.shape), np.zeros((n, hq))
+    pos, key = kv - n + torch.arange(n, device="cuda")[:, None], torch.arange(kv, device="cuda")[None]
+    see = torch.ones(n, kv, dtype=torch.bool, device="cuda")
+    if causal:
+        see &= key <= pos
+    if window:
+        see &= key > pos - window
+    g = q.unflatten(1, (hk, -1))
+    s = torch.einsum("nhgd,khd->nhgk", g, k) * scale
+    dots = (torch.einsum("nhgd,khd->nhgk", g.abs(), k.abs()) * abs(scale)).masked_fill(~see[:, None, None], 0).amax(-1)
+    s = s.masked_fill(~see[:, None, None], -torch.inf)
+    lse = s.logsumexp(-1)
+    p = (s - lse.masked_fill(lse == -torch.inf, 0.0)[..., None]).exp()
+    out, mean = (torch.einsum("nhgk,khd->nhgd", p, x) for x in (v, v.abs()))
+    return [x.flatten(1, 2).cpu().numpy() for x in (out, lse, mean, dots)]
+
+
+WINDOWS = {
+    # hq, hk, d, ps, requests, most new tokens, most keys, window, causal, kernels that the window leaves to choose from
+    "many requests, several tiles": (16, 8, 64, 16, 200, 6, 2500, 700, True, {"8 rows", "16 rows", "128 rows", "256 rows", "1 CTA"}),
+    "many requests, several tiles, heads of 128": (16, 8, 128, 48, 200, 6, 2500, 700, True,
+                                                    {"8 rows", "16 rows", "128 rows", "256 rows", "1 CTA"}),
+    "many requests, a narrow window": (16, 8, 64, 64, 400, 3, 900, 100, True, {"8 rows", "16 rows", "128 rows", "256 rows"}),
+    "many requests, a narrow window, heads of 128": (16, 8, 128, 16, 400, 3, 900, 37, True,
+                                                      {"8 rows", "16 rows", "128 rows", "256 rows"}),
+    "prompts": (8, 2, 64, 64, 6, 600, 1500, 333, True, {"128 rows", "256 rows", "1 CTA", "2 CTAs", "4 CTAs"}),
+    "prompts, heads of 128": (8, 2, 128, 16, 6, 600, 1500, 333, True, {"128 rows", "256 rows", "1 CTA", "2 CTAs", "4 CTAs"}),
+    "prompts, not causal": (14, 2, 128, 64, 5, 300, 2200, 1000, False, {"128 rows", "256 rows", "1 CTA"}),
+    "prompts, a window of one key": (8, 2, 64, 16, 6, 400, 900, 1, True, {"128 rows", "256 rows", "1 CTA"}),
+}
+
+
+@pytest.mark.parametrize("case", sorted(WINDOWS))
+def test_windows_through_the_kernels_they_reach(serve, case):  # noqa: F811
+    """The window cuts what is planned for, too: of the hints those are taken that lead to other kernels with it."""
+    hq, hk, d, ps, n, most_new, most_kv, window, causal, want_kinds = WINDOWS[case]
+    rng = np.random.default_rng(14)
+    new = rng.integers(1, most_new + 1, n)
+    kv = np.maximum(rng.integers(0, most_kv + 1, n), np.where(rng.random(n) < 0.8, new, 0))
+    new[n // 2], kv[n // 3], kv[-1] = 0, 0, most_kv
+    held = -(-kv // ps)
+    num = int(held.sum())
+    cache = cache_of(serve, num, ps, hk, d)
+    table, order, used = np.full((n, max(held.max(), 1)), -1, np.int32), rng.permutation(num), 0
+    for b in range(n):
+        table[b, :held[b]] = order[used:used + held[b]]
+        used += held[b]
+    slots = np.concatenate([table[b, np.arange(kv[b]) // ps].astype(np.int64) * ps + np.arange(kv[b]) % ps for b in range(n)])
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    k, v = (torch.randn(len(slots), hk, d, generator=gen, device="cuda") for _ in range(2))
+    cache.append(k, v, dev(slots))
+    cache.read(dev(slots), k, v)
+    q = torch.randn(int(new.sum()), hq, d, generator=gen, device="cuda").bfloat16()
+    cu, at = np.concatenate([[0], np.cumsum(new)]), np.concatenate([[0], np.cumsum(kv)])
+    wants = [dense(q[cu[b]:cu[b + 1]].double(), k[at[b]:at[b + 1]].double(), v[at[b]:at[b + 1]].double(), d ** -0.5, causal, window)
+             for b in range(n)]
+    want, want_lse, mean, dots = (np.concatenate(x) for x in zip(*wants))
+    length = np.repeat(np.minimum(kv, window + new), new)[:, None]
+    kinds = {}
+    for max_q in (1, 2, 8, 32, 64, 128, 256, 1024, 10 ** 4, 10 ** 6):
+        for max_kv in [0] + [2 ** i for i in range(5, 27)]:
+            name = cache.plan_kernel(hq, n, max_q=max_q, max_kv=max_kv, window=window)
+            kinds.setdefault(name.split("<")[1][:-1], (max_q, max_kv))
+    assert want_kinds <= set(kinds)
+    empty = np.isneginf(want_lse)
+    score = score_error(dots, d)
+    tol = U8 * np.abs(want) + (1 + U8) * (2 * U16 + 2 * score + (length + 64) * U32)[..., None] * mean + 1e-30
+    tol_lse = score + (length + 64) * U32 + 4 * U32 * np.abs(np.where(empty, 0, want_lse))
+    cu_d, kv_d, table_d = dev(cu.astype(np.int32)), dev(kv.astype(np.int32)), dev(table)
+    for name, (max_q, max_kv) in kinds.items():
+        out, lse = torch.full_like(q, 7.0), torch.full((len(q), hq), 7.0, device="cuda")
+        cache.attention(q, out, cu_d, kv_d, table_d, max_q=max_q, max_kv=max_kv, causal=causal, window=window, lse=lse)
+        assert cache.status() == 0
+        got, got_lse = f64(out), f64(lse)
+        assert np.array_equal(np.isneginf(got_lse), empty) and (got[empty] == 0).all(), name
+        bad = ~(np.abs(got - want) <= tol)
+        assert not bad.any(), (name, bad.sum())
+        assert (np.abs(got_lse[~empty] - want_lse[~empty]) <= tol_lse[~empty]).all(), name
