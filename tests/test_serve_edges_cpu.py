@@ -2,6 +2,8 @@
 import glob
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -24,3 +26,58 @@ def test_no_operator_reads_through_the_non_coherent_path():
         text = source(name)
         for word in ("__ldg(", "ld.global.nc", "ld_nc", "__restrict__"):
             assert word not in text, (name, word)
+
+
+@pytest.fixture
+def be(tmp_path, monkeypatch):
+    """The build with one small unit, into a folder of its own."""
+    monkeypatch.setattr(build_ext, "SOURCES", ["rra_static.cu"])
+    monkeypatch.setattr(build_ext, "BUILD", str(tmp_path / "_build"))
+    for name, file in (("LIB", "librra.so"), ("NATIVE", "_serve.so"), ("NATIVE_STAMP", "_build/_serve.torch")):
+        monkeypatch.setattr(build_ext, name, str(tmp_path / file), raising=False)
+    return build_ext
+
+
+def test_the_library_builds_without_torch(be, tmp_path):
+    """In a Python that has none."""
+    code = """
+import sys
+class Hidden:
+    def find_spec(self, name, path=None, target=None):
+        if name.split(".")[0] == "torch":
+            raise ModuleNotFoundError("No module named 'torch'", name="torch")
+sys.meta_path.insert(0, Hidden())
+sys.path.insert(0, %r)
+from latency_barrier_free_gb300 import build_ext as be
+be.SOURCES, be.BUILD, be.LIB, be.NATIVE, be.NATIVE_STAMP = ["rra_static.cu"], %r, %r, %r, %r
+print(be.build())
+assert "torch" not in sys.modules
+""" % (build_ext.ROOT, be.BUILD, be.LIB, be.NATIVE, getattr(be, "NATIVE_STAMP", ""))
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+    assert os.path.exists(be.LIB) and not os.path.exists(be.NATIVE) and p.stdout.strip() == be.LIB
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library(be, monkeypatch):
+    bad = os.path.join(os.path.dirname(be.LIB), "bad.cpp")
+    open(bad, "w").write("#error not today\n")
+    monkeypatch.setattr(be, "_native_command", lambda out: ["g++", "-c", bad, "-o", out])
+    with pytest.raises(RuntimeError, match="not today"):
+        be.build()
+    assert os.path.exists(be.LIB) and not os.path.exists(be.NATIVE)
+
+
+def test_the_binding_is_built_again_for_another_torch(be, monkeypatch):
+    built = []
+    monkeypatch.setattr(be, "_native_command", lambda out: built.append(out) or ["touch", out])
+    be.build()
+    be.build()
+    assert len(built) == 1 and os.path.exists(be.NATIVE)
+    before = os.path.getmtime(be.LIB)
+    monkeypatch.setattr(be, "_torch", lambda: "another")
+    be.build()
+    be.build()
+    assert len(built) == 2 and os.path.getmtime(be.LIB) == before
+    monkeypatch.setattr(be, "_torch", lambda: "")
+    be.build(force=True)
+    assert len(built) == 2 and os.path.getmtime(be.LIB) > before
