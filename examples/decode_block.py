@@ -57,21 +57,23 @@ class DecodeBlock:
 
     def step(self, x, new_len, max_q, max_kv):
         """x [tokens, hidden]: the new tokens of every request, in the order of the
-        requests; new_len [requests] int32 on the GPU (negative: the request ends).
-        Returns x plus the block's output."""
+        requests, and padding after them, if any; new_len [requests] int32 on the GPU
+        (negative: the request ends).  Returns x plus the block's output; padding as
+        it was."""
         t, n = x.shape[0], self.kv_len.numel()
         slots, positions = self.slots[:t], self.positions[:t]
         serve.slot_map(self.kv_len, new_len, self.table, self.free, self.free_count, self.page_tokens, kv_len=self.kv_len,
                        cu_new=self.cu, slots=slots, positions=positions, free_left=self.free_count, pages_short=self.short)
+        # zeros: the attention leaves the rows of padding as they are
+        heads = torch.zeros(self.ranks, t, self.hq, self.d, dtype=torch.bfloat16, device="cuda")
         shares = []
         for r in range(self.ranks):
             qkv = (x @ self.wqkv[r]).view(t, self.hq + 2 * self.hk, self.d)
             q, k, v = qkv.split([self.hq, self.hk, self.hk], 1)
             serve.qk_norm_rope(q, k, self.wq, self.wk, self.cos, self.sin, positions, q, k, eps=self.eps)
             self.caches[r].append(k, v, slots)
-            o = torch.empty(t, self.hq, self.d, dtype=torch.bfloat16, device="cuda")
-            self.caches[r].attention(q, o, self.cu[:n + 1], self.kv_len, self.table, max_q=max_q, max_kv=max_kv)
-            shares.append(o.view(t, -1) @ self.wo[r])
+            self.caches[r].attention(q, heads[r], self.cu[:n + 1], self.kv_len, self.table, max_q=max_q, max_kv=max_kv)
+            shares.append(heads[r].view(t, -1) @ self.wo[r])
         outs = [torch.empty_like(x) for _ in range(self.ranks)]
         self.comm.allreduce_residual(shares, [x] * self.ranks, outs)
         return outs[0]

@@ -160,7 +160,8 @@ class KvCache:
         cache (rra_kv_attention).  Request b has the queries cu_q[b]..cu_q[b+1]
         and the first kv_len[b] tokens of its row of block_table, its own
         included; max_q and max_kv are what to plan for.  scale defaults to
-        1/sqrt(head_dim).  lse: float32 [tokens, q_heads], optional."""
+        1/sqrt(head_dim).  lse: float32 [tokens, q_heads], optional.  Rows of out
+        and lse after cu_q[-1], a step's padding, stay as they are."""
         st = _native.kv_attention(self._cache, self._dev, self._workspace, q, out, cu_q, kv_len, block_table, max_q, max_kv,
                                   self._scale if scale is None else scale, causal, window, lse, stream, self._home)
         if st:

@@ -115,3 +115,25 @@ def test_a_decode_step_from_a_graph(example):
     a, b = run(False), run(True)
     assert a[1:] == b[1:] == ([34, 28], 24 - 5, 0)
     assert torch.equal(a[0], b[0])
+
+
+def test_padding_of_a_step_stays_as_it_was(example):
+    """A step of fixed shape with fewer new tokens than rows, over memory that held NaN."""
+    block = example.DecodeBlock(ranks=2, hidden=256, q_heads=8, kv_heads=2, head_dim=64, pages=24, page_tokens=16, max_requests=4,
+                                max_pages=10, max_tokens=64, max_position=512)
+    try:
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        x = torch.randn(40, 256, generator=gen, device="cuda").bfloat16()
+        kv = np.zeros(4, np.int64)
+        for new in ([9, 0, 20, 1], [1, 1, -1, 0]):
+            nan = [torch.full((n,), float("nan"), dtype=torch.bfloat16, device="cuda") for n in (40 * 4 * 64, 40 * 256) for _ in range(8)]
+            del nan
+            y = block.step(x, torch.tensor(new, dtype=torch.int32, device="cuda"), max_q=max(new), max_kv=64)
+            torch.cuda.synchronize()
+            kv = np.array([0 if n < 0 else k + n for k, n in zip(kv, new)])
+            t = sum(max(n, 0) for n in new)
+            assert torch.equal(y[t:], x[t:])
+            want = plain_step(block, x[:t], kv, new)
+            assert np.abs(f64(y[:t]) - want).max() <= 8 * U8 * max(1.0, np.abs(want).max())
+    finally:
+        block.close()
