@@ -238,7 +238,7 @@ typedef struct {
     int64_t out_token_stride, out_head_stride;
     int64_t table_stride;
     int64_t tokens;             /* rows of q and out */
-    double scale;               /* finite; usually 1 / sqrt(head_dim) */
+    double scale;               /* usually 1 / sqrt(head_dim); times log2(e) finite in binary32, as scores are */
     int32_t requests;
     int32_t table_pages;
     int32_t q_heads;

@@ -23,6 +23,7 @@
 
 namespace rra {
 
+constexpr double kLog2E = 1.4426950408889634;
 constexpr int kAttnMinRun = 1;     // tiles a warp takes at least
 constexpr int kAttnSegmentCost = 4;  // what starting and ending a segment costs, in tiles
 
@@ -525,7 +526,7 @@ static bool attn_args_ok(const rra_kv_attention_args_t* a) {
     const int hk = a->cache.kv_heads;
     if (a->requests < 0 || a->requests > RRA_SERVE_MAX_REQUESTS || a->tokens < 0 || a->tokens > INT32_MAX / 2 ||
         a->q_heads < 1 || a->q_heads % hk != 0 || a->table_pages < 0 || a->table_stride < a->table_pages ||
-        a->max_q < 0 || a->max_kv < 0 || a->window < 0 || !isfinite(a->scale))
+        a->max_q < 0 || a->max_kv < 0 || a->window < 0 || !(fabs(a->scale) * kLog2E <= FLT_MAX))
         return false;
     // rows, and the keys of one request, are counted in 32 bits
     if (a->tokens * a->q_heads > INT32_MAX / 2 || (int64_t)a->table_pages * a->cache.page_tokens > INT32_MAX / 2)
@@ -604,7 +605,7 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     }
     rra::AttnParams p;
     p.a = *args;
-    p.scale_log2 = (float)(args->scale * 1.4426950408889634);
+    p.scale_log2 = (float)(args->scale * rra::kLog2E);
     p.group = args->q_heads / args->cache.kv_heads;
     p.by_group = rra::Divisor(p.group);
     p.by_page = rra::Divisor(args->cache.page_tokens);

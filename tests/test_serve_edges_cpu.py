@@ -7,7 +7,8 @@ import sys
 
 import pytest
 
-from latency_barrier_free_gb300 import build_ext
+from latency_barrier_free_gb300 import build_ext, rra
+from test_serve_cpu import FAKE, fields, serve  # noqa: F401
 
 torch = pytest.importorskip("torch")
 
@@ -81,3 +82,16 @@ def test_the_binding_is_built_again_for_another_torch(be, monkeypatch):
     monkeypatch.setattr(be, "_torch", lambda: "")
     be.build(force=True)
     assert len(built) == 2 and os.path.getmtime(be.LIB) > before
+
+
+def test_attention_refuses_a_scale_beyond_binary32(serve):  # noqa: F811
+    """Scores are binary32 and in units of log2."""
+    names = fields("rra_kv_attention_args_t")
+    good = [FAKE, 100, 16, 2, 128, 0] + [FAKE] * 7 + [1024, 128] * 2 + [8, 0, 0.1, 0, 8, 8, 1, 100, 1, 0, 0]
+    assert len(names) == len(good)
+    call = lambda scale: serve._lib().rra_kv_attention(  # noqa: E731
+        serve._ATTN.pack(*good[:names.index("scale")], scale, *good[names.index("scale") + 1:]), 0)
+    for scale in (0.1, -0.1, 0.0, 2.3e38, -2.3e38, 1e-300):  # no tokens, no requests: nothing is launched
+        assert call(scale) == rra.OK
+    for scale in (2.4e38, -2.4e38, 1e39, 1e300, float("inf"), float("nan")):
+        assert call(scale) == rra.ERR_INVALID_ARG
