@@ -212,7 +212,8 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  *   overlap q.  lse NULL or binary32 [tokens][q_heads], contiguous.
  *   Rows of out and lse that no request has (a step's padding after cu_q[B]) stay
  *   as they are: fill them before, if anything reads them.
- *   cu_q values are clamped to [0, tokens], kv_len to [0, table_pages *
+ *   cu_q ascends; where it does not, rows may be computed several times or not at
+ *   all.  Its values are clamped to [0, tokens], kv_len to [0, table_pages *
  *   page_tokens]; keys in pages outside [0, num_pages) are not seen.
  *   max_q, max_kv: the longest query and key counts expected.  They steer the
  *   choice of kernel and its split only: longer requests are still right.

@@ -328,6 +328,9 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         if (b < a.requests) chunk_sums[b] = (int32_t)(total_chunks + at);
         total_chunks += all;
     }
+    // Chunks are counted in 32 bits, which the rows of any batch fit.  More of them are the same rows over and over: cu_q does
+    // not ascend, and there is no result to give.
+    if (total_chunks > INT32_MAX) return;
     if (tid == 0) chunk_sums[a.requests] = (int32_t)total_chunks;
     __syncthreads();
     auto owner = [&](int n, int& b, int& c) {

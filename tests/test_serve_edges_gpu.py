@@ -379,3 +379,22 @@ def test_windows_through_the_kernels_they_reach(serve, case):  # noqa: F811
         bad = ~(np.abs(got - want) <= tol)
         assert not bad.any(), (name, bad.sum())
         assert (np.abs(got_lse[~empty] - want_lse[~empty]) <= tol_lse[~empty]).all(), name
+
+
+def test_query_ranges_that_hold_every_row_thousands_of_times(serve):  # noqa: F811
+    """cu_q that goes up and down over 2^30 rows (of strides that overlap): more row tiles than 32 bits count.  The kernels for
+    prompts leave at once."""
+    hq, d, n, tokens = 64, 64, 4096, 2 ** 24 - 1
+    cache = cache_of(serve, 1, 16, 1, d)
+    x = torch.full((tokens * 8 + hq * d,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = x.clone()
+    q, out = (z.as_strided((tokens, hq, d), (8, d, 1)) for z in (x, y))
+    cu = dev(np.resize(np.array([0, tokens], np.int32), n + 1))
+    kv, table = torch.ones(n, dtype=torch.int32, device="cuda"), torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    kinds = {name: hint for name, hint in plans(cache, hq, n).items() if name.startswith("kv_attention_prompt_kernel")}
+    assert len(kinds) == 2
+    for name, (max_q, max_kv) in kinds.items():
+        assert cache.plan_kernel(hq, n, max_q=max_q, max_kv=max_kv) == name
+        cache.attention(q, out, cu, kv, table, max_q=max_q, max_kv=max_kv)
+        torch.cuda.synchronize()
+        assert cache.status() == 0 and torch.equal(x, y)
