@@ -200,7 +200,8 @@ rra_status_t rra_kv_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
  * A query that sees no key gets out = 0 and lse = -inf.  Products accumulate
  * in binary32; the softmax's maximum, sum and weights are binary32; out is
  * rounded to bfloat16 once.  A query is scaled by a power of two to [1, 2) and
- * then binary16 (its 8 bits fit).  Scores take every key exactly: code times
+ * then binary16: its elements keep their 8 bits down to 2^-17 of its largest, and
+ * those below 2^-25 of it count as 0.  Scores take every key exactly: code times
  * scale, 13 bits, as two products.  For the sum over values binary16 (11 bits)
  * holds: for few queries, the weight (times 2^10, against its underflow) and the
  * weight times scale, the codes being exact; in the kernel for prompts, the

@@ -121,7 +121,7 @@ __device__ __forceinline__ AttnLengths attn_lengths(const AttnParams& p, int b) 
 }
 
 // Queries enter the matrix instructions as binary16, each row scaled to [1, 2) by a power of two (exact but for
-// elements below 2^-14 of the row's largest): `down` is that factor, with the softmax scale's sign, and `factor`, above 0,
+// elements below 2^-17 of the row's largest: the last of a bfloat16's 8 bits is then below 2^-24): `down` is that factor, with the softmax scale's sign, and `factor`, above 0,
 // what scores are multiplied with to be in units of log2.
 __device__ __forceinline__ void attn_row_scale(const AttnParams& p, float most, float& down, float& factor) {
     int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 : 0;

@@ -119,8 +119,8 @@ class KvCache:
     each; their layout stands in rra_serve.h); it needs no initialisation.  The
     object holds the attention's workspace, so its attention() calls are ordered
     on one stream, any one; append() and read() are not bound to it.  It may go
-    once they are enqueued, but for calls whose stream was given as a number: for
-    those it is kept until their work is done."""
+    once they are enqueued, but for calls whose stream was given as a number, which
+    it has to outlive, and for graphs that hold calls."""
 
     def __init__(self, pages, page_tokens: int, kv_heads: int, head_dim: int):
         lib = _lib()

@@ -398,3 +398,56 @@ def test_query_ranges_that_hold_every_row_thousands_of_times(serve):  # noqa: F8
         cache.attention(q, out, cu, kv, table, max_q=max_q, max_kv=max_kv)
         torch.cuda.synchronize()
         assert cache.status() == 0 and torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_with_one_element_far_above_the_rest(serve, d):  # noqa: F811
+    """2^16 times the others, over a channel where no key has anything: the others keep all their bits."""
+    rng = np.random.default_rng(15)
+    kv, hq = 500, 8
+    k = rng.standard_normal((kv, 1, d))
+    k[..., 5] = 0
+    cache, k, v, table = one_request(serve, k, rng.standard_normal((kv, 1, d)))
+    x = rng.uniform(1, 2, (2, hq, d)) * np.where(rng.random((2, hq, d)) < 0.5, -1, 1) * 2.0 ** -16
+    x[..., 5] = 1.5
+    q = dev(x, torch.bfloat16)
+    scale = 2.0 ** 16 / d ** 0.5
+    want, want_lse, mean, dots = ref.attention(f64(q), k, v, kv, scale, True, 0)
+    for name, (max_q, max_kv) in plans(cache, hq, 1).items():
+        out, lse = torch.empty_like(q), torch.empty(2, hq, device="cuda")
+        cache.attention(q, out, dev(np.array([0, 2], np.int32)), dev(np.array([kv], np.int32)), table, max_q=max_q, max_kv=max_kv,
+                        scale=scale, lse=lse)
+        assert cache.status() == 0
+        e = (2 * U16 + 2 * score_error(dots, d) + (kv + 64) * U32)[..., None]
+        assert (np.abs(f64(out) - want) <= U8 * np.abs(want) + (1 + U8) * e * mean).all(), name
+        assert (np.abs(f64(lse) - want_lse) <= score_error(dots, d) + (kv + 64) * U32 + 4 * U32 * np.abs(want_lse)).all(), name
+
+
+def test_every_kernel_from_a_graph_and_on_another_stream(serve):  # noqa: F811
+    """The same bits as enqueued by itself; calls that follow each other over one workspace, replayed."""
+    rng = np.random.default_rng(16)
+    kv, hk, hq, d = 4000, 2, 16, 128
+    cache, _, _, table = one_request(serve, rng.standard_normal((kv, hk, d)), rng.standard_normal((kv, hk, d)))
+    q = dev(rng.standard_normal((200, hq, d)), torch.bfloat16)
+    cu, kv_d = dev(np.array([0, 200], np.int32)), dev(np.array([kv], np.int32))
+    away = torch.cuda.Stream()
+    for name, (max_q, max_kv) in plans(cache, hq, 1).items():
+        want, want_lse = torch.empty_like(q), torch.empty(200, hq, device="cuda")
+        cache.attention(q, want, cu, kv_d, table, max_q=max_q, max_kv=max_kv, lse=want_lse)
+        outs = [(torch.zeros_like(q), torch.zeros_like(want_lse)) for _ in range(3)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(away):
+            cache.attention(q, outs[0][0], cu, kv_d, table, max_q=max_q, max_kv=max_kv, lse=outs[0][1])
+        away.synchronize()
+        assert torch.equal(outs[0][0], want) and torch.equal(outs[0][1], want_lse), name
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for out, lse in outs:
+                cache.attention(q, out, cu, kv_d, table, max_q=max_q, max_kv=max_kv, lse=lse)
+        for _ in range(2):
+            for out, lse in outs:
+                out.zero_(), lse.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(out, want) and torch.equal(lse, want_lse) for out, lse in outs), name
+    assert cache.status() == 0
