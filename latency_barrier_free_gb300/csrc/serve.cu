@@ -439,8 +439,9 @@ static const void* rope_kernel(bool many, bool interleaved) {
 // after which each holds a whole word and the row's codes leave as one
 // coalesced run.  Bound by the values' traffic and, in the write, by nearly as
 // much arithmetic; a thread has up to kKvPairs pairs of rows in flight.  16384
-// tokens of 8 heads of 128, bfloat16: written or read in 17.6 us (4.9 TB/s); the
-// one after the other, with codes still in L2, 31.0 us.
+// tokens of 8 heads of 128, nothing of it in L2: bfloat16 written in 18.5 us, read
+// in 17.7 us (4.6, 4.9 TB/s), binary32 in 30.0 and 30.9 us (5.1, 5.0 TB/s); the one
+// after the other, bfloat16, with codes still in L2, 31.0 us.
 constexpr int kKvThreads = 128;
 // Where there are enough; one otherwise (16384 tokens of 8 heads of 128, written and read: 31.0 us, with one pair 36.3; 16 tokens:
 // 3.9 us, with one pair 2.9).

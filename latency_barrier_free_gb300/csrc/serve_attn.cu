@@ -12,9 +12,9 @@
 //
 // Bound by the pages' bytes in the middle and by latency at both ends.  64
 // heads over 8 of 128, one query each: 131071 keys of one request, 151 MB, take
-// 37.3 us (4.05 TB/s): 3.4 us to the first copy (lengths, page numbers, pages),
+// 37.5 us (4.0 TB/s): 3.4 us to the first copy (lengths, page numbers, pages),
 // 25 us of stream at 6 TB/s, then the joins.  64 ragged requests, 175 MB:
-// 44.5 us (3.9 TB/s).  Half the instructions are the unpacking of codes, and the
+// 44.9 us (3.9 TB/s).  Half the instructions are the unpacking of codes, and the
 // ALU pipe is half busy; four schedulers need the three warps each.
 #include <algorithm>
 #include <cmath>

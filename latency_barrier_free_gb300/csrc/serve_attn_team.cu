@@ -7,7 +7,7 @@
 // barriers: against serve_attn.cu there is no scan of the batch before the first
 // copy, and no fence, counter and round trip to L2 after the last key.  What
 // remains is lengths, page numbers, pages: three round trips, one after another.
-// 8 heads over 1 of 128: 2000 keys in 5.5 us (the other kernel: 9.7).  24
+// 8 heads over 1 of 128: 2000 keys in 5.6 us (the other kernel: 9.7).  24
 // requests of up to 5 queries, 14 heads over 2 of 64, a window of 1000: 10.8 us.
 #include "serve_attn_rows.cuh"
 

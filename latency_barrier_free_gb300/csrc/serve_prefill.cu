@@ -26,7 +26,7 @@
 // to arrive adds the parts in order.
 //
 // 3 requests of up to 1024 queries and 8192 keys, 64 heads over 8 of 128: 261
-// GFLOP in 259 us, 1008 TFLOP/s, or 1512 with the second part of K.  Per 256
+// GFLOP in 259.5 us, 1006 TFLOP/s, or 1509 with the second part of K.  Per 256
 // rows and 128 keys that is about 4200 cycles, of which products at their full
 // rate would take 3072.  Longest is the chain of one tile: its values' and next
 // scores' products (1536 cycles alone, 1750 beside the stores and reads of the
