@@ -34,37 +34,37 @@ LOW, HIGH, LARGEST = -32, 32, 448.0  # exponents, and the largest code
 def listed():
     return [
         # a few short chat turns at once, odd groups of 7 heads, small heads: latency
-        {"name": "prompt, 5 short", "op": "prompt", "requests": 5, "longest": 96, "hq": 14, "hk": 2, "d": 64,
+        {"name": "prompt 5 short", "op": "prompt", "requests": 5, "longest": 96, "hq": 14, "hk": 2, "d": 64,
          "dtype": "bf16", "causal": True, "window": 0},
         # ragged prompts on one of eight tensor-parallel ranks, sliding window, binary16
-        {"name": "prompt, 12 ragged fp16", "op": "prompt", "requests": 12, "longest": 2048, "hq": 8, "hk": 1, "d": 128,
+        {"name": "prompt 12 ragged fp16", "op": "prompt", "requests": 12, "longest": 2048, "hq": 8, "hk": 1, "d": 128,
          "dtype": "fp16", "causal": True, "window": 1000},
         # two long documents, all heads of the [B, 8192] model
-        {"name": "prompt, 2 long", "op": "prompt", "requests": 2, "longest": 8192, "hq": 64, "hk": 8, "d": 128,
+        {"name": "prompt 2 long", "op": "prompt", "requests": 2, "longest": 8192, "hq": 64, "hk": 8, "d": 128,
          "dtype": "bf16", "causal": True, "window": 0},
         # the cache write of a decode step, and what the touched blocks stand for
-        {"name": "store8, 16 tokens", "op": "store8", "requests": 16, "queries": 1, "longest": 4096, "hk": 8, "d": 128,
+        {"name": "store8 16 tokens", "op": "store8", "requests": 16, "queries": 1, "longest": 4096, "hk": 8, "d": 128,
          "ps": 64, "dtype": "bf16"},
         # the cache write of prompts that continue what is there
-        {"name": "store8, 4 prompts", "op": "store8", "requests": 4, "queries": 8192, "longest": 16384, "hk": 8, "d": 128,
+        {"name": "store8 4 prompts", "op": "store8", "requests": 4, "queries": 8192, "longest": 16384, "hk": 8, "d": 128,
          "ps": 64, "dtype": "bf16"},
         # one request on one tensor-parallel rank: latency
-        {"name": "attend8, 1 x 2000", "op": "attend8", "requests": 1, "queries": 1, "longest": 2000, "hq": 8, "hk": 1,
+        {"name": "attend8 1 x 2000", "op": "attend8", "requests": 1, "queries": 1, "longest": 2000, "hq": 8, "hk": 1,
          "d": 128, "ps": 64, "causal": True, "window": 0},
         # a decode batch of 64 ragged requests, all heads, some padding
-        {"name": "attend8, 64 ragged", "op": "attend8", "requests": 64, "queries": 1, "longest": 16384, "hq": 64, "hk": 8,
+        {"name": "attend8 64 ragged", "op": "attend8", "requests": 64, "queries": 1, "longest": 16384, "hq": 64, "hk": 8,
          "d": 128, "ps": 64, "causal": True, "window": 0},
         # prompts in chunks on top of what the cache already holds
-        {"name": "attend8, prompt chunks", "op": "attend8", "requests": 3, "queries": 1024, "longest": 8192, "hq": 64,
+        {"name": "attend8 prompt chunks", "op": "attend8", "requests": 3, "queries": 1024, "longest": 8192, "hq": 64,
          "hk": 8, "d": 128, "ps": 64, "causal": True, "window": 0},
         # one prompt sampled eight times: latency
-        {"name": "fork, 1 into 8", "op": "fork", "requests": 1, "samples": 8, "longest": 1000, "hk": 1, "d": 128, "ps": 64},
+        {"name": "fork 1 into 8", "op": "fork", "requests": 1, "samples": 8, "longest": 1000, "hk": 1, "d": 128, "ps": 64},
         # a batch of prompts, each sampled eight times, whole pages of all heads
-        {"name": "fork, 32 into 8", "op": "fork", "requests": 32, "samples": 8, "longest": 4096, "hk": 8, "d": 128, "ps": 64},
+        {"name": "fork 32 into 8", "op": "fork", "requests": 32, "samples": 8, "longest": 4096, "hk": 8, "d": 128, "ps": 64},
         # a few requests end, odd sizes
-        {"name": "tidy, 9 requests", "op": "tidy", "requests": 9, "longest": 700, "hk": 1, "d": 64, "ps": 16, "moves": 64},
+        {"name": "tidy 9 requests", "op": "tidy", "requests": 9, "longest": 700, "hk": 1, "d": 64, "ps": 16, "moves": 64},
         # a large pool after much traffic, every fourth request ends
-        {"name": "tidy, 500 requests", "op": "tidy", "requests": 500, "longest": 16384, "hk": 2, "d": 128, "ps": 64,
+        {"name": "tidy 500 requests", "op": "tidy", "requests": 500, "longest": 16384, "hk": 2, "d": 128, "ps": 64,
          "moves": 8192},
     ]
 
