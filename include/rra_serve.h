@@ -14,6 +14,10 @@
  *   rra_kv_read       what the cache holds for given tokens, as values
  *   rra_kv_attention  attention over that cache: single tokens, a few drafted
  *                     tokens, chunks of a prompt
+ *   rra_kv8_append, rra_kv8_read, rra_kv8_attention   the same over a cache of 8 bits
+ *   rra_pages_fork, rra_pages_release, rra_pages_compact, rra_pages_copy
+ *                     pages that several requests share: samples of a prompt,
+ *                     their end, holes in the pool closed
  *
  * Rules common to all.  Every call only enqueues work on `stream` (one
  * kernel), never synchronises and allocates nothing, so it can be captured
@@ -263,6 +267,182 @@ size_t rra_kv_attention_workspace_bytes(int head_dim);
  * <4 CTAs>, <8 CTAs> (few requests, a cluster for each 8 rows) or
  * "kv_attention_prompt_kernel<128 rows>", <256 rows>. */
 rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name);
+
+/* ------------------------------------------------------- the 8-bit cache ---
+ * The same calls over a cache of 8 bits (8 + 8 / head_dim with its exponents),
+ * for those to whom 4 bits are too few: the structures above, with pages of
+ * rra_kv8_page_bytes() bytes.  A page: for each KV head, for each 16 of its
+ * page_tokens tokens, a block of 32 * head_dim + 16 bytes:
+ *     K codes [16][head_dim]   V codes [16][head_dim]
+ *     exponent of K, of V (a signed byte each)   14 bytes that nothing uses
+ * A value is code * 2^exponent.  A code is e4m3: sign, 4 bits of exponent, 3 of
+ * mantissa, up to 448, down to 2^-9.  The 16-byte piece i of row r's codes is in
+ * the 128-byte line that row order gives, at i ^ (r & 7) within it for heads of
+ * 128, at i ^ (r & 6) for heads of 64 (two rows a line).
+ *
+ * Writing: a block's exponent, for each head, K and V apart, is the smallest whole
+ * number with max |x| <= 448 * 2^e over its values, within [-32, 32]; code = x *
+ * 2^-e rounded to the nearest e4m3, ties to even, saturating.  Writing the token
+ * at a block's start begins it anew: what it held before goes.  Writing others
+ * keeps what is there and can only raise the exponent; the codes that are there
+ * are then rounded again, to the new unit (a power of two: only those that get
+ * below 2^-6 of it lose bits, at most 2^-10 of it each time).  So a value is within
+ * 2^-4 of itself, or 2^-10 * 2^e for each write that raised e.  NaN is stored as 0;
+ * infinities as the largest code, and do not count for the exponent.
+ *
+ * rra_kv8_append: slots of one block are neighbours in the list, in any order, as
+ * rra_slot_map gives them (slots outside the cache are skipped and do not come
+ * between neighbours).  Where one block's slots come in several places of one
+ * call, its codes and exponents may not belong together.  A slot that occurs
+ * twice gets either token's values, channel by channel.
+ * rra_kv8_read, rra_kv8_attention: as rra_kv_read, rra_kv_attention; every code
+ * and exponent enters exactly.  Codes are binary16 in the products, weights
+ * too, against a maximum of score and exponent together: 2^10 (for prompts 2^7)
+ * times as large, against their underflow, times 2^exponent.  The workspace is
+ * the same. */
+size_t rra_kv8_page_bytes(int page_tokens, int kv_heads, int head_dim);
+rra_status_t rra_kv8_append(const rra_kv_tokens_args_t* args, rra_stream_t stream);
+rra_status_t rra_kv8_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
+rra_status_t rra_kv8_attention(const rra_kv_attention_args_t* args, rra_stream_t stream);
+rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const char** name);
+
+/* ---------------------------------------------------------- shared pages ---
+ * Requests that share pages: samples of one prompt, prompts with a common start.
+ * shared[p] counts the holders of page p beyond the first: 0 for pages that one
+ * request holds or none, never below.  rra_slot_map knows nothing of it: it pops
+ * pages, whose count is 0, and a request's new tokens go behind those it has, so
+ * it needs only that no request shares a page that is not full.  rra_pages_fork
+ * sees to that.  Requests that end are given to rra_pages_release first; it sets
+ * their length to 0, so that rra_slot_map returns nothing for them again.
+ *
+ * Common to the three.  A request of length n holds the first ceil(n /
+ * page_tokens) entries of its row of block_table (at most table_pages).  Lengths
+ * below 0 count as 0.  Entries outside [0, num_pages) are no pages: they are
+ * copied as they are and counted nowhere.  free_pages[0 .. *free_count) is the
+ * stack of rra_slot_map.  Outputs that are named "may be" an input may be the
+ * same buffer; nothing else overlaps.  Each call is one kernel and moves no page:
+ * fork and compact write lists for rra_pages_copy, which is called for the pages
+ * of every layer.
+ *
+ * rra_pages_fork: for i < forks, row target[i] becomes a copy of row source[i]:
+ *   its whole pages are shared (shared + 1 for each), and a page of its own is
+ *   popped, fork by fork, for one that is not full:
+ *     copy_from[i], copy_to[i]   that page and the new one; -1 and -1 if there is
+ *                                nothing to copy
+ *     kv_len                     seq_len, and for the targets their sources'
+ *     *free_left, *pages_short   as in rra_slot_map (entries without a page: -1)
+ *   What a target's row held before is not given back.  Forks whose source or
+ *   target is outside [0, requests) do nothing but write -1.  No row is target of two
+ *   forks, or target and source: what such rows then hold is not defined.
+ *   shared_out may be shared, kv_len may be seq_len, free_left may be free_count. */
+typedef struct {
+    const int32_t* seq_len;     /* [requests] */
+    const int32_t* source;      /* [forks] */
+    const int32_t* target;      /* [forks] */
+    int32_t* block_table;       /* [requests][table_stride], table_pages used */
+    const int32_t* free_pages;  /* [num_pages] */
+    const int32_t* free_count;  /* [1] */
+    const int32_t* shared;      /* [num_pages] */
+    int32_t* kv_len;            /* [requests] */
+    int32_t* shared_out;        /* [num_pages] */
+    int32_t* copy_from;         /* [forks] */
+    int32_t* copy_to;           /* [forks] */
+    int32_t* free_left;         /* [1] */
+    int32_t* pages_short;       /* [1] */
+    int64_t table_stride;
+    int32_t requests;
+    int32_t forks;              /* 0..RRA_SERVE_MAX_REQUESTS */
+    int32_t table_pages;
+    int32_t page_tokens;
+    int32_t num_pages;
+    int32_t reserved;           /* 0 */
+} rra_pages_fork_args_t;
+
+rra_status_t rra_pages_fork(const rra_pages_fork_args_t* args, rra_stream_t stream);
+
+/* rra_pages_release: requests with new_len[b] < 0 end.  Each page that such a
+ *   request holds has one holder less; pages without any are pushed on the stack,
+ *   in ascending order of their numbers (those that would not fit num_pages are
+ *   dropped).  kv_len[b] is 0 for the requests that end, seq_len[b] for the others;
+ *   block_table is not changed.  A page that is listed more often than it has
+ *   holders is pushed once.
+ *   shared_out may be shared, kv_len may be seq_len, free_left may be free_count. */
+typedef struct {
+    const int32_t* seq_len;     /* [requests] */
+    const int32_t* new_len;     /* [requests] */
+    const int32_t* block_table; /* [requests][table_stride], table_pages used */
+    int32_t* free_pages;        /* [num_pages] */
+    const int32_t* free_count;  /* [1] */
+    const int32_t* shared;      /* [num_pages] */
+    int32_t* kv_len;            /* [requests] */
+    int32_t* shared_out;        /* [num_pages] */
+    int32_t* free_left;         /* [1] */
+    int64_t table_stride;
+    int32_t requests;
+    int32_t table_pages;
+    int32_t page_tokens;
+    int32_t num_pages;
+} rra_pages_release_args_t;
+
+rra_status_t rra_pages_release(const rra_pages_release_args_t* args, rra_stream_t stream);
+
+/* rra_pages_compact: moves pages in use to the pool's low end.  Every page that is
+ *   not on the stack is in use, whoever holds it.  The highest page in use goes
+ *   to the lowest free page, the next highest to the next lowest, while that is
+ *   lower and up to max_moves:
+ *     move_from[i], move_to[i]   the moves (i < max_moves; -1 behind the last);
+ *     *move_count                how many
+ *     moved[p]                   page p's new number; -1 for pages that were free
+ *     table_out                  block_table with the new numbers in the entries that requests hold
+ *     free_out, *free_left       the pages that are free now, the lowest on top
+ *     shared_out                 counts, moved along
+ *   With max_moves >= num_pages / 2 the pages in use end up as 0 .. n - 1.  Nothing
+ *   may use the pages between this call and rra_pages_copy's.
+ *   table_out may be block_table (then with the same stride, and other entries are
+ *   not touched; else they are copied), free_out may be free_pages, free_left may
+ *   be free_count, shared_out may be shared. */
+typedef struct {
+    const int32_t* seq_len;     /* [requests] */
+    const int32_t* block_table; /* [requests][table_stride], table_pages used */
+    const int32_t* free_pages;  /* [num_pages] */
+    const int32_t* free_count;  /* [1] */
+    const int32_t* shared;      /* [num_pages] */
+    int32_t* table_out;         /* [requests][table_out_stride] */
+    int32_t* free_out;          /* [num_pages] */
+    int32_t* free_left;         /* [1] */
+    int32_t* shared_out;        /* [num_pages] */
+    int32_t* moved;             /* [num_pages] */
+    int32_t* move_from;         /* [max_moves] */
+    int32_t* move_to;           /* [max_moves] */
+    int32_t* move_count;        /* [1] */
+    int64_t table_stride, table_out_stride;
+    int32_t requests;
+    int32_t table_pages;
+    int32_t page_tokens;
+    int32_t num_pages;
+    int32_t max_moves;
+    int32_t reserved;           /* 0 */
+} rra_pages_compact_args_t;
+
+rra_status_t rra_pages_compact(const rra_pages_compact_args_t* args, rra_stream_t stream);
+
+/* rra_pages_copy: page to[i] of the pool `to_pages` becomes page from[i] of
+ * `from_pages` (which may be the same pool), i < count.  Pairs with either outside
+ * its pool are skipped.  A page that is both read and written, or written twice,
+ * in one call may get a mixture.  page_bytes is a multiple of 16; pages are 16-byte
+ * aligned. */
+typedef struct {
+    const void* from_pages;     /* [from_num][page_bytes] */
+    void* to_pages;             /* [to_num][page_bytes] */
+    const int32_t* from;        /* [count] */
+    const int32_t* to;          /* [count] */
+    int64_t from_num, to_num;
+    int64_t page_bytes;
+    int32_t count;
+    int32_t reserved;           /* 0 */
+} rra_pages_copy_args_t;
+
+rra_status_t rra_pages_copy(const rra_pages_copy_args_t* args, rra_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "serve_attn_rows.cuh"
+#include "serve_attn_rows8.cuh"
 
 namespace rra {
 
@@ -89,9 +89,9 @@ struct AttnPiece {
 };
 enum { kHas = 1, kStarts = 2, kEnds = 4 };
 
-template <int D, int NT, int kWarps, int kStages>
+template <typename F, int D, int NT, int kWarps, int kStages>
 struct AttnShape {
-    using B = KvBlock<D>;
+    using B = typename F::template Block<D>;
     static constexpr int kRows = 8 * NT;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStage = 2 * B::kBytes;
@@ -114,11 +114,11 @@ __device__ __forceinline__ void attn_add(float top, float& sum, float4& o, float
     o.w = fmaf(v.w, by, o.w);
 }
 
-template <int D, int NT, int kWarps, int kStages>
+template <typename F, int D, int NT, int kWarps, int kStages>
 __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = AttnShape<D, NT, kWarps, kStages>;
-    using B = KvBlock<D>;
-    constexpr int J = B::kGroups, kRows = Sh::kRows;
+    using Sh = AttnShape<F, D, NT, kWarps, kStages>;
+    using B = typename F::template Block<D>;
+    constexpr int J = D / 32, kRows = Sh::kRows;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t warp_sum[kWarps];
     __shared__ AttnPiece pieces[2 * kWarps];
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         };
 
         // Queries of a segment, as they are; loaded ahead of the copies that the lanes set up meanwhile.
-        AttnRows<D, NT> att;
+        typename F::template Rows<D, NT> att;
         auto load_queries = [&]() { att.load(p, seg.r.q0, seg.r.qn, seg.h, seg.c, first_tile(seg) < end_tile(seg)); };
         load_queries();
 
@@ -338,15 +338,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                         if (g == 0) *(float2*)(piece + 2 * r) = make_float2(top, sum);
 #pragma unroll
                         for (int j = 0; j < J; ++j)
-                            *(float4*)(piece + 2 * kRows + r * D + 32 * j + 4 * g) =
-                                att.output(j, n, k);
+                            *(float4*)(piece + 2 * kRows + r * D + att.channel(j, g)) = att.output(j, n, k);
                     } else if (row < rows) {
                         float inv;
-                        __nv_bfloat16* const to = attn_row(p, seg.r.q0, seg.h, row, top, sum, g == 0, inv) + 4 * g;
+                        __nv_bfloat16* const to = attn_row(p, seg.r.q0, seg.h, row, top, sum, g == 0, inv);
 #pragma unroll
                         for (int j = 0; j < J; ++j)
-                            attn_store(to + 32 * j,
-                                       att.output(j, n, k), inv);
+                            attn_store(to + att.channel(j, g), att.output(j, n, k), inv);
                     }
                 }
             if (seg.end >= r1) break;
@@ -508,10 +506,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     }
 }
 
-template <int D, int NT, int kWarps, int kStages>
+template <typename F, int D, int NT, int kWarps, int kStages>
 static rra_status_t attn_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
-    using Sh = AttnShape<D, NT, kWarps, kStages>;
-    const void* k = (const void*)kv_attention_kernel<D, NT, kWarps, kStages>;
+    using Sh = AttnShape<F, D, NT, kWarps, kStages>;
+    const void* k = (const void*)kv_attention_kernel<F, D, NT, kWarps, kStages>;
     static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 10240, "shared memory");
     if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
         cudaGetLastError();
@@ -594,7 +592,11 @@ rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const ch
     return RRA_OK;
 }
 
-rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t stream) {
+rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
+    return rra_kv_attention_plan(args, name);
+}
+
+static rra_status_t kv_attention(const rra_kv_attention_args_t* args, int bits, rra_stream_t stream) {
     if (!rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
     if (args->requests == 0 || args->tokens == 0) return RRA_OK;
     int dev = 0, sms = 0;
@@ -613,13 +615,25 @@ rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t 
     p.window = std::min(args->window, 1 << 30);
     const rra::AttnKernel kernel = rra::attn_kernel_of(*args);
     if (kernel >= rra::kTeam1)
-        return rra::launch_team(p, (int)(((int64_t)std::max(args->max_q, 1) * p.group + 7) / 8), 1 << (kernel - rra::kTeam1), stream);
+        return rra::launch_team(p, bits, (int)(((int64_t)std::max(args->max_q, 1) * p.group + 7) / 8), 1 << (kernel - rra::kTeam1), stream);
     if (kernel == rra::kPrompt128 || kernel == rra::kPrompt256)
-        return rra::launch_prefill(p, kernel == rra::kPrompt256 ? 2 : 1, sms, stream);
+        return rra::launch_prefill(p, bits, kernel == rra::kPrompt256 ? 2 : 1, sms, stream);
     const int ctas = std::min(sms, rra::kAttnMaxCtas);
+    using rra::Cache4;
+    using rra::Cache8;
+    const bool eight = kernel == rra::kRows8;
+    if (bits == 8) {
+        if (args->cache.head_dim == 128)
+            return eight ? rra::attn_launch<Cache8, 128, 1, 8, 2>(p, ctas, stream) : rra::attn_launch<Cache8, 128, 2, 6, 2>(p, ctas, stream);
+        return eight ? rra::attn_launch<Cache8, 64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<Cache8, 64, 2, 8, 3>(p, ctas, stream);
+    }
     if (args->cache.head_dim == 128)
-        return kernel == rra::kRows8 ? rra::attn_launch<128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<128, 2, 8, 2>(p, ctas, stream);
-    return kernel == rra::kRows8 ? rra::attn_launch<64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<64, 2, 8, 4>(p, ctas, stream);
+        return eight ? rra::attn_launch<Cache4, 128, 1, 12, 2>(p, ctas, stream) : rra::attn_launch<Cache4, 128, 2, 8, 2>(p, ctas, stream);
+    return eight ? rra::attn_launch<Cache4, 64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<Cache4, 64, 2, 8, 4>(p, ctas, stream);
 }
+
+rra_status_t rra_kv_attention(const rra_kv_attention_args_t* args, rra_stream_t stream) { return kv_attention(args, 4, stream); }
+
+rra_status_t rra_kv8_attention(const rra_kv_attention_args_t* args, rra_stream_t stream) { return kv_attention(args, 8, stream); }
 
 }  // extern "C"

@@ -66,15 +66,52 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
+// The keys that the rows of 2 t, 2 t + 1 of every n-tile see, and those that all, or any, of the rows do.
+template <int NT>
+struct AttnRange {
+    int first_key[NT][2], end_key[NT][2];
+    int all_first, all_end, any_first, any_end;
+
+    __device__ __forceinline__ void clear() { all_first = 0, all_end = INT32_MAX, any_first = INT32_MAX, any_end = 0; }
+    // Row r of the request's `rows`, column 2 t + k of n-tile n.
+    __device__ __forceinline__ void add(const AttnParams& p, int n, int k, int r, int rows, int qn, int kv) {
+        int lo = 0, hi = 0;
+        if (r < rows) {
+            const int pos = kv - qn + p.by_group(r);
+            hi = p.a.causal ? max(0, min(kv, pos + 1)) : kv;
+            lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            all_first = max(all_first, lo);
+            all_end = min(all_end, hi);
+            any_first = min(any_first, lo);
+            any_end = max(any_end, hi);
+        }
+        first_key[n][k] = lo;
+        end_key[n][k] = hi;
+    }
+    __device__ __forceinline__ void meet() {
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            all_first = max(all_first, __shfl_xor_sync(0xffffffffu, all_first, o));
+            all_end = min(all_end, __shfl_xor_sync(0xffffffffu, all_end, o));
+            any_first = min(any_first, __shfl_xor_sync(0xffffffffu, any_first, o));
+            any_end = max(any_end, __shfl_xor_sync(0xffffffffu, any_end, o));
+        }
+    }
+    __device__ __forceinline__ bool sees(int n, int k, int key) const { return key >= first_key[n][k] && key < end_key[n][k]; }
+};
+
 template <int D, int NT>
-struct AttnRows {
+struct AttnRows : AttnRange<NT> {
     using B = KvBlock<D>;
+    using AttnRange<NT>::all_first;
+    using AttnRange<NT>::all_end;
+    using AttnRange<NT>::any_first;
+    using AttnRange<NT>::any_end;
     static constexpr int J = B::kGroups, kRows = 8 * NT;
+    static __device__ __forceinline__ int channel(int j, int g) { return 32 * j + 4 * g; }  // first of output(j)'s, lanes g, t
     uint2 raw[NT][J][2];            // queries as they are: loaded some time before start()
     uint32_t q[NT][J][2][2];        // as B operands, each row scaled to [1, 2) by a power of two
     float factor[NT][2];            // of columns 2 t, 2 t + 1: |softmax scale| times that power, above 0
-    int first_key[NT][2], end_key[NT][2];
-    int all_first, all_end, any_first, any_end;
     // Maximum m, the score that moves it, sum l; -FLT_MAX stands for no key yet.  m is one of the scores, and
     // weights are 2^((s - m) factor): with s factor - m factor, rounded apart, huge scores would overflow.
     float m[NT][2], limit[NT][2], l[NT][2];
@@ -111,7 +148,7 @@ struct AttnRows {
     // After load(): the rows over kv keys, nothing seen yet.
     __device__ __forceinline__ void start(const AttnParams& p, int qn, int kv, int c) {
         const int t = threadIdx.x & 3, rows = qn * p.group;
-        all_first = 0, all_end = INT32_MAX, any_first = INT32_MAX, any_end = 0;
+        this->clear();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float most = 0.f;
@@ -142,28 +179,10 @@ struct AttnRows {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 factor[n][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
-                const int r = c * kRows + 8 * n + 2 * t + k;
-                int lo = 0, hi = 0;
-                if (r < rows) {
-                    const int pos = kv - qn + p.by_group(r);
-                    hi = p.a.causal ? max(0, min(kv, pos + 1)) : kv;
-                    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-                    all_first = max(all_first, lo);
-                    all_end = min(all_end, hi);
-                    any_first = min(any_first, lo);
-                    any_end = max(any_end, hi);
-                }
-                first_key[n][k] = lo;
-                end_key[n][k] = hi;
+                this->add(p, n, k, c * kRows + 8 * n + 2 * t + k, rows, qn, kv);
             }
         }
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            all_first = max(all_first, __shfl_xor_sync(0xffffffffu, all_first, o));
-            all_end = min(all_end, __shfl_xor_sync(0xffffffffu, all_end, o));
-            any_first = min(any_first, __shfl_xor_sync(0xffffffffu, any_first, o));
-            any_end = max(any_end, __shfl_xor_sync(0xffffffffu, any_end, o));
-        }
+        this->meet();
 
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -242,7 +261,7 @@ struct AttnRows {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int key = key0 + krow + 8 * (k >> 1);
-                    s[n][k] = key >= first_key[n][k & 1] && key < end_key[n][k & 1] ? s[n][k] : -INFINITY;
+                    s[n][k] = this->sees(n, k & 1, key) ? s[n][k] : -INFINITY;
                 }
         }
         // ---- does a score pass the running maximum, or a scale what the sums allow? ----
@@ -348,6 +367,15 @@ struct AttnRows {
             }
         }
     }
+};
+
+// The 4-bit cache, to the kernels that take either.
+struct Cache4 {
+    static constexpr int kBits = 4;
+    template <int D>
+    using Block = KvBlock<D>;
+    template <int D, int NT>
+    using Rows = AttnRows<D, NT>;
 };
 
 }  // namespace rra

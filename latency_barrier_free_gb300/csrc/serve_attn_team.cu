@@ -9,15 +9,15 @@
 // remains is lengths, page numbers, pages: three round trips, one after another.
 // 8 heads over 1 of 128: 2000 keys in 5.6 us (the other kernel: 9.7).  24
 // requests of up to 5 queries, 14 heads over 2 of 64, a window of 1000: 10.8 us.
-#include "serve_attn_rows.cuh"
+#include "serve_attn_rows8.cuh"
 
 namespace rra {
 
 constexpr int kTeamStages = 2;
 
-template <int D>
+template <typename F, int D>
 struct TeamShape {
-    using B = KvBlock<D>;
+    using B = typename F::template Block<D>;
     static constexpr int kThreads = 32 * kTeamWarps;
     static constexpr int kStage = 2 * B::kBytes;
     static constexpr int kRing = kTeamWarps * kTeamStages * kStage;
@@ -66,10 +66,10 @@ __device__ __forceinline__ void team_add(int n, F&& get, float& top, float& sum,
 }
 
 // Cluster i: KV head and request of segment i, rows 8 c .. of chunk c, and of chunk c + chunks and so on.
-template <int D>
+template <typename F, int D>
 __global__ void __launch_bounds__(32 * kTeamWarps, 3) kv_attention_team_kernel(const __grid_constant__ AttnParams p, int chunks) {
-    using Sh = TeamShape<D>;
-    using B = KvBlock<D>;
+    using Sh = TeamShape<F, D>;
+    using B = typename F::template Block<D>;
     constexpr int kItems = 8 * D / 4;  // four channels of a row each
     extern __shared__ __align__(128) unsigned char smem[];
     const rra_kv_attention_args_t& a = p.a;
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 3) kv_attention_team_kernel(c
     bool dead = false;  // a wait ran out: no more copies, no more sums
 
     for (int c = c0; c * 8 < rows; c += chunks) {  // the same for every CTA of the cluster
-        AttnRows<D, 1> att;
+        typename F::template Rows<D, 1> att;
         att.load(p, n.q0, n.qn, h, c, t0 < t1);
         // copies, kTeamStages tiles ahead; lane i holds the places of tile `from` + i
         int next = t0, from = t0 - 32;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 3) kv_attention_team_kernel(c
             const int r = 2 * t + k;
             if (g == 0) *(float2*)(part + 2 * r) = make_float2(att.top(0, k), sum);
 #pragma unroll
-            for (int j = 0; j < B::kGroups; ++j) *(float4*)(part + 16 + r * D + 32 * j + 4 * g) = att.output(j, 0, k);
+            for (int j = 0; j < D / 32; ++j) *(float4*)(part + 16 + r * D + att.channel(j, g)) = att.output(j, 0, k);
         }
         __syncthreads();
         for (int i = tid; i < kItems; i += Sh::kThreads) {
@@ -211,16 +211,21 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 3) kv_attention_team_kernel(c
         for (int i = 0; i < kTeamStages; ++i) attn_wait_quiet(bars + 8 * i, (issued >> i & 1u) ^ 1u);
 }
 
-rra_status_t launch_team(const AttnParams& p, int chunks, int size, rra_stream_t stream) {
+template <typename F>
+static rra_status_t team_launch(const AttnParams& p, int chunks, int size, rra_stream_t stream) {
     const bool big = p.a.cache.head_dim == 128;
-    const void* const k = big ? (const void*)kv_attention_team_kernel<128> : (const void*)kv_attention_team_kernel<64>;
-    const int smem = big ? TeamShape<128>::kSmem : TeamShape<64>::kSmem;
+    const void* const k = big ? (const void*)kv_attention_team_kernel<F, 128> : (const void*)kv_attention_team_kernel<F, 64>;
+    const int smem = big ? TeamShape<F, 128>::kSmem : TeamShape<F, 64>::kSmem;
     if (configure_cluster_kernel(k, smem) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
     void* args[] = {(void*)&p, &chunks};
     return serve_launch(k, dim3((unsigned)(p.a.requests * p.a.cache.kv_heads * chunks * size)), 32 * kTeamWarps, (size_t)smem, size, stream, args);
+}
+
+rra_status_t launch_team(const AttnParams& p, int bits, int chunks, int size, rra_stream_t stream) {
+    return bits == 8 ? team_launch<Cache8>(p, chunks, size, stream) : team_launch<Cache4>(p, chunks, size, stream);
 }
 
 }  // namespace rra

@@ -25,6 +25,12 @@ Operator<rra_slot_map_args_t> fn_slot_map;
 Operator<rra_qk_norm_rope_args_t> fn_rope;
 Operator<rra_kv_tokens_args_t> fn_append, fn_read;
 Operator<rra_kv_attention_args_t> fn_attention;
+Operator<rra_kv_tokens_args_t> fn_append8, fn_read8;
+Operator<rra_kv_attention_args_t> fn_attention8;
+Operator<rra_pages_fork_args_t> fn_fork;
+Operator<rra_pages_release_args_t> fn_release;
+Operator<rra_pages_compact_args_t> fn_compact;
+Operator<rra_pages_copy_args_t> fn_copy;
 PyObject* s_cuda_stream;
 
 struct Refused {};  // thrown with a Python exception set
@@ -219,10 +225,20 @@ long kv_tokens(PyObject* const* v, Py_ssize_t n, Operator<rra_kv_tokens_args_t> 
 }
 long kv_append(PyObject* const* v, Py_ssize_t n) { return kv_tokens(v, n, fn_append); }
 long kv_read(PyObject* const* v, Py_ssize_t n) { return kv_tokens(v, n, fn_read); }
+long kv8_append(PyObject* const* v, Py_ssize_t n) { return kv_tokens(v, n, fn_append8); }
+long kv8_read(PyObject* const* v, Py_ssize_t n) { return kv_tokens(v, n, fn_read8); }
+
+// The caller does not know the workspace: its memory must not go to another tensor before this call's work is done.  (Of a
+// stream given by its number nothing is known, not even whether it still exists then: there the caller keeps the cache.)
+void keep_workspace(const at::Tensor& workspace, rra_stream_t stream, PyObject* given, PyObject* home, int dev) {
+    if (stream != (rra_stream_t)PyLong_AsVoidPtr(home) && !PyLong_Check(given))
+        c10::cuda::CUDACachingAllocator::recordStream(workspace.storage().data_ptr(),
+                                                      c10::cuda::getStreamFromExternal((cudaStream_t)stream, (c10::DeviceIndex)dev));
+}
 
 // (cache, device, workspace, q, out, cu_q, kv_len, block_table, max_q, max_kv, scale, causal, window, lse, stream, the
 // workspace's own stream)
-long kv_attention(PyObject* const* v, Py_ssize_t n) {
+long attention(PyObject* const* v, Py_ssize_t n, Operator<rra_kv_attention_args_t> fn) {
     arguments(n, 16);
     rra_kv_attention_args_t a = {};
     a.cache = cache_of(v[0]);
@@ -249,12 +265,109 @@ long kv_attention(PyObject* const* v, Py_ssize_t n) {
     if (requests > RRA_SERVE_MAX_REQUESTS) return RRA_ERR_INVALID_ARG;
     a.requests = (int32_t)requests;
     const rra_stream_t stream = stream_of(v[14], dev);
-    // The caller does not know the workspace: its memory must not go to another tensor before this call's work is done.  (Of a
-    // stream given by its number nothing is known, not even whether it still exists then: there the caller keeps the cache.)
-    if (stream != (rra_stream_t)PyLong_AsVoidPtr(v[15]) && !PyLong_Check(v[14]))
-        c10::cuda::CUDACachingAllocator::recordStream(workspace.storage().data_ptr(),
-                                                      c10::cuda::getStreamFromExternal((cudaStream_t)stream, (c10::DeviceIndex)dev));
-    return fn_attention(&a, stream);
+    keep_workspace(workspace, stream, v[14], v[15], dev);
+    return fn(&a, stream);
+}
+long kv_attention(PyObject* const* v, Py_ssize_t n) { return attention(v, n, fn_attention); }
+long kv8_attention(PyObject* const* v, Py_ssize_t n) { return attention(v, n, fn_attention8); }
+
+// A table whose rows and width are the first one's.
+int32_t* table_like(const char* name, PyObject* o, int64_t requests, int64_t width, int device, int64_t* stride) {
+    const at::Tensor& t = tensor(name, o);
+    check(name, t, at::kInt, device, t.dim() == 2 && t.size(0) == requests && t.size(1) == width && (t.stride(1) == 1 || width <= 1 || requests == 0),
+          "of block_table's sizes with adjacent pages");
+    *stride = requests > 1 ? t.stride(0) : width;
+    return (int32_t*)t.data_ptr();
+}
+
+// What the calls on shared pages begin with: seq_len, the table, the stack, its count, the counts of holders, tokens of a page.
+template <typename Args>
+int pages_of(Args& a, PyObject* seq_len, PyObject* table, PyObject* free_pages, PyObject* free_count, PyObject* shared, PyObject* page_tokens) {
+    const at::Tensor &seq = tensor("seq_len", seq_len), &stack = tensor("free_pages", free_pages);
+    const int dev = device_of("seq_len", seq);
+    if (seq.numel() > RRA_SERVE_MAX_REQUESTS || stack.numel() > INT32_MAX)
+        refuse(PyExc_ValueError, "more than %d requests, or more than 2^31 - 1 pages", RRA_SERVE_MAX_REQUESTS);
+    a.requests = (int32_t)seq.numel();
+    a.num_pages = (int32_t)stack.numel();
+    a.seq_len = flat<int32_t>("seq_len", seq, at::kInt, 0, dev);
+    a.block_table = table_of(table, a.requests, dev, &a.table_stride, &a.table_pages);
+    a.free_pages = flat<int32_t>("free_pages", stack, at::kInt, 0, dev);
+    a.free_count = flat<int32_t>("free_count", free_count, at::kInt, 1, dev);
+    a.shared = flat<int32_t>("shared", shared, at::kInt, a.num_pages, dev);
+    a.page_tokens = integer32(page_tokens);
+    return dev;
+}
+
+// (seq_len, source, target, table, free_pages, free_count, shared, page_tokens, kv_len, shared_out, copy_from, copy_to, free_left,
+// pages_short, stream)
+long pages_fork(PyObject* const* v, Py_ssize_t n) {
+    arguments(n, 15);
+    rra_pages_fork_args_t a = {};
+    const int dev = pages_of(a, v[0], v[3], v[4], v[5], v[6], v[7]);
+    const at::Tensor& source = tensor("source", v[1]);
+    const int64_t forks = source.numel();
+    a.source = flat<int32_t>("source", source, at::kInt, 0, dev);
+    a.target = flat<int32_t>("target", v[2], at::kInt, forks, dev);
+    a.kv_len = flat<int32_t>("kv_len", v[8], at::kInt, a.requests, dev);
+    a.shared_out = flat<int32_t>("shared_out", v[9], at::kInt, a.num_pages, dev);
+    a.copy_from = flat<int32_t>("copy_from", v[10], at::kInt, forks, dev);
+    a.copy_to = flat<int32_t>("copy_to", v[11], at::kInt, forks, dev);
+    a.free_left = flat<int32_t>("free_left", v[12], at::kInt, 1, dev);
+    a.pages_short = flat<int32_t>("pages_short", v[13], at::kInt, 1, dev);
+    if (forks > RRA_SERVE_MAX_REQUESTS) return RRA_ERR_INVALID_ARG;
+    a.forks = (int32_t)forks;
+    return fn_fork(&a, stream_of(v[14], dev));
+}
+
+// (seq_len, new_len, table, free_pages, free_count, shared, page_tokens, kv_len, shared_out, free_left, stream)
+long pages_release(PyObject* const* v, Py_ssize_t n) {
+    arguments(n, 11);
+    rra_pages_release_args_t a = {};
+    const int dev = pages_of(a, v[0], v[2], v[3], v[4], v[5], v[6]);
+    a.new_len = flat<int32_t>("new_len", v[1], at::kInt, a.requests, dev);
+    a.kv_len = flat<int32_t>("kv_len", v[7], at::kInt, a.requests, dev);
+    a.shared_out = flat<int32_t>("shared_out", v[8], at::kInt, a.num_pages, dev);
+    a.free_left = flat<int32_t>("free_left", v[9], at::kInt, 1, dev);
+    return fn_release(&a, stream_of(v[10], dev));
+}
+
+// (seq_len, table, free_pages, free_count, shared, page_tokens, table_out, free_out, shared_out, free_left, moved, move_from, move_to,
+// move_count, stream)
+long pages_compact(PyObject* const* v, Py_ssize_t n) {
+    arguments(n, 15);
+    rra_pages_compact_args_t a = {};
+    const int dev = pages_of(a, v[0], v[1], v[2], v[3], v[4], v[5]);
+    a.table_out = table_like("table_out", v[6], a.requests, a.table_pages, dev, &a.table_out_stride);
+    a.free_out = flat<int32_t>("free_out", v[7], at::kInt, a.num_pages, dev);
+    a.shared_out = flat<int32_t>("shared_out", v[8], at::kInt, a.num_pages, dev);
+    a.free_left = flat<int32_t>("free_left", v[9], at::kInt, 1, dev);
+    a.moved = flat<int32_t>("moved", v[10], at::kInt, a.num_pages, dev);
+    const at::Tensor& from = tensor("move_from", v[11]);
+    a.move_from = flat<int32_t>("move_from", from, at::kInt, 0, dev);
+    a.move_to = flat<int32_t>("move_to", v[12], at::kInt, from.numel(), dev);
+    a.move_count = flat<int32_t>("move_count", v[13], at::kInt, 1, dev);
+    if (from.numel() > INT32_MAX) return RRA_ERR_INVALID_ARG;
+    a.max_moves = (int32_t)from.numel();
+    return fn_compact(&a, stream_of(v[14], dev));
+}
+
+// (pages, the pool that they go to, bytes of a page, from, to, stream)
+long pages_copy(PyObject* const* v, Py_ssize_t n) {
+    arguments(n, 6);
+    rra_pages_copy_args_t a = {};
+    const at::Tensor &pages = tensor("pages", v[0]), &to_pages = tensor("to", v[1]), &from = tensor("source", v[3]);
+    const int dev = device_of("pages", pages);
+    a.page_bytes = integer(v[2]);
+    a.from_pages = flat<void>("pages", pages, at::kByte, 0, dev);
+    a.to_pages = flat<void>("to", to_pages, at::kByte, 0, dev);
+    if (a.page_bytes < 1) return RRA_ERR_INVALID_ARG;
+    a.from_num = pages.numel() / a.page_bytes;
+    a.to_num = to_pages.numel() / a.page_bytes;
+    a.from = flat<int32_t>("source", from, at::kInt, 0, dev);
+    a.to = flat<int32_t>("target", v[4], at::kInt, from.numel(), dev);
+    if (from.numel() > INT32_MAX) return RRA_ERR_INVALID_ARG;
+    a.count = (int32_t)from.numel();
+    return fn_copy(&a, stream_of(v[5], dev));
 }
 
 // ---------------------------------------------------------------- module ----
@@ -274,6 +387,13 @@ long init(PyObject* const* v, Py_ssize_t n) {
     find(fn_append, "rra_kv_append");
     find(fn_read, "rra_kv_read");
     find(fn_attention, "rra_kv_attention");
+    find(fn_append8, "rra_kv8_append");
+    find(fn_read8, "rra_kv8_read");
+    find(fn_attention8, "rra_kv8_attention");
+    find(fn_fork, "rra_pages_fork");
+    find(fn_release, "rra_pages_release");
+    find(fn_compact, "rra_pages_compact");
+    find(fn_copy, "rra_pages_copy");
     return 0;
 }
 
@@ -295,6 +415,9 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef methods[] = {method<init>("init"),           method<slot_map>("slot_map"),  method<qk_norm_rope>("qk_norm_rope"),
                          method<kv_append>("kv_append"), method<kv_read>("kv_read"),    method<kv_attention>("kv_attention"),
+                         method<kv8_append>("kv8_append"), method<kv8_read>("kv8_read"), method<kv8_attention>("kv8_attention"),
+                         method<pages_fork>("pages_fork"), method<pages_release>("pages_release"),
+                         method<pages_compact>("pages_compact"), method<pages_copy>("pages_copy"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

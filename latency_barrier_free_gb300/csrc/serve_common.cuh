@@ -28,6 +28,40 @@ struct KvBlock {
 };
 static_assert(KvBlock<64>::kBytes == 18 * 64 && KvBlock<128>::kBytes == 18 * 128, "18 bytes a channel");
 
+// The same of the 8-bit cache.
+template <int D>
+struct Kv8Block {
+    static constexpr int kV = kKvBlockTokens * D;        // V codes
+    static constexpr int kExponents = 2 * kV;            // of K, of V: a signed byte each
+    static constexpr int kBytes = kExponents + 16;       // 32 D + 16
+    // Offset of 16-byte piece `piece` of row `row` in its codes.  Pieces of a 128-byte line change places so that neither the
+    // lanes that read eight rows (K) nor those that read four rows two apart (V) meet in a bank.
+    static __host__ __device__ constexpr int at(int row, int piece) {
+        const int x = row * (D / 16) + piece;
+        return ((x & ~7) | ((x ^ (D == 128 ? row : row & 6)) & 7)) * 16;
+    }
+};
+static_assert(Kv8Block<64>::kBytes % 16 == 0 && Kv8Block<128>::kBytes == 4112, "blocks of whole bulk copies");
+constexpr int kKv8Low = -32, kKv8High = 32;  // exponents
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The exponents of K and of V from a block's last word but three.
+__device__ __forceinline__ int kv8_exponent(uint32_t w, int v) {
+    return min(max((int)(int8_t)(w >> (8 * v)), kKv8Low), kKv8High);  // clamped: memory that was never written may hold anything
+}
+// Two e4m3 codes, the lower byte in the lower half.
+__device__ __forceinline__ uint32_t from_e4m3x2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+// Four e4m3 codes as two pairs.
+__device__ __forceinline__ void from_e4m3x4(uint32_t w, uint32_t& low, uint32_t& high) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(low), "=r"(high) : "r"(w));
+}
+
 // The four pairs of values of a word of codes, byte i in out[i].
 __device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t* out) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"

@@ -1,0 +1,324 @@
+// serve_kv8.cu -- the writes and reads of the 8-bit cache (rra_serve.h).
+//
+// Write.  A block of 16 tokens and a head shares an exponent, so its tokens have
+// to be looked at together: a warp takes one run of neighbouring tokens of one
+// block, one head, K or V.  A CTA finds the runs that begin among its tokens (a
+// prompt: one in 16; a decode step: each), then its warps share runs x heads x 2.
+// A run's values stay in registers from their maximum to their codes.
+//
+// Read.  A warp's lanes take 8 channels each of a row.
+#include <algorithm>
+
+#include "serve_common.cuh"
+
+namespace rra {
+
+constexpr int kKv8Threads = 256;
+constexpr int kKv8Span = 16;      // tokens of a CTA where there are many
+
+struct Kv8Params {
+    rra_kv_tokens_args_t a;
+    Divisor by_heads;
+    Divisor by_page;   // blocks of a page
+    int64_t room;      // slots of the cache
+    int32_t span;      // tokens of a CTA
+    int32_t heads;     // heads of a CTA
+};
+
+// The block of head h that slot is in.
+template <typename B>
+__device__ __forceinline__ char* kv8_block(const Kv8Params& p, int64_t slot, int h) {
+    const rra_kv_cache_t& c = p.a.cache;
+    const int at = (int)((uint64_t)slot / kKvBlockTokens), page = p.by_page(at);
+    return (char*)c.pages + ((int64_t)(page * c.kv_heads + h) * p.by_page.d + (at - page * p.by_page.d)) * B::kBytes;
+}
+
+// Eight channels as binary32.
+__device__ __forceinline__ void kv8_load(const float* from, float* x) {
+    const float4 a = __ldcs((const float4*)from), b = __ldcs((const float4*)from + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void kv8_load(const __nv_bfloat16* from, float* x) {
+    const uint4 v = __ldcs((const uint4*)from);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void kv8_store(float* to, const float* x) {
+    __stcs((float4*)to, make_float4(x[0], x[1], x[2], x[3]));
+    __stcs((float4*)to + 1, make_float4(x[4], x[5], x[6], x[7]));
+}
+__device__ __forceinline__ void kv8_store(__nv_bfloat16* to, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *(const uint32_t*)&h;
+    }
+    __stcs((uint4*)to, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// The codes of four values, the first in the low byte: nearest e4m3, ties to even, saturating.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// The smallest e with most <= 448 * 2^e = 1.75 * 2^(8 + e), within the limits.
+__device__ __forceinline__ int kv8_exponent_of(float most) {
+    const uint32_t bits = __float_as_uint(most);
+    const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, kKv8Low), kKv8High);  // most = 0 and its neighbours end up at the lower one
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(const __grid_constant__ Kv8Params p) {
+    using B = Kv8Block<D>;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows that a warp takes at once
+    constexpr int kHeld = kKvBlockTokens / kRows;       // rows of a lane
+    __shared__ int64_t slots[kKv8Span + kKvBlockTokens];
+    __shared__ int runs[kKv8Span], count;
+    __shared__ int32_t picks[kKv8Threads / 32][kKvBlockTokens];
+    const rra_kv_tokens_args_t& a = p.a;
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t0 = (int64_t)blockIdx.x * p.span;
+    const int h0 = (int)blockIdx.y * p.heads, heads = min(p.heads, a.cache.kv_heads - h0);
+    pdl_release_early();
+    pdl_wait();
+    // ---- the runs that begin among this CTA's tokens; the slots of those and of 16 more ----
+    if (warp == 0) {
+        const bool mine = lane < p.span && t0 + lane < a.tokens;
+        const int64_t slot = t0 + lane < a.tokens ? a.slots[t0 + lane] : -1;
+        slots[lane] = slot;
+        const bool inside = (uint64_t)slot < (uint64_t)p.room;
+        // the slot before, not counting those that are skipped; -1: none
+        const uint32_t valid = __ballot_sync(0xffffffffu, inside), lower = valid & ((1u << lane) - 1u);
+        int64_t left = __shfl_sync(0xffffffffu, slot, 31 - __clz((int)(lower | 1u)));
+        int64_t earlier = -1;
+        for (int64_t t = t0 - 32; valid != 0u && t > -32; t -= 32) {
+            const int64_t s = t + lane >= 0 ? a.slots[t + lane] : -1;
+            const uint32_t there = __ballot_sync(0xffffffffu, (uint64_t)s < (uint64_t)p.room);
+            if (there == 0u) continue;
+            earlier = __shfl_sync(0xffffffffu, s, 31 - __clz((int)there));
+            break;
+        }
+        if (lower == 0u) left = earlier;
+        const bool begins = mine && inside && (left < 0 || left / kKvBlockTokens != slot / kKvBlockTokens);
+        const uint32_t who = __ballot_sync(0xffffffffu, begins);
+        if (begins) runs[__popc(who & ((1u << lane) - 1u))] = lane;
+        if (lane == 0) count = __popc(who);
+    }
+    __syncthreads();
+    const int items = count * heads * 2;
+    const int sub = lane / kLanes, m = lane % kLanes;  // this lane's row of those that the warp takes at once, and its eight channels
+    for (int item = warp; item < items; item += kKv8Threads / 32) {
+        const int v = item & 1, r = (item >> 1) / heads, h = h0 + (item >> 1) - r * heads;
+        const int first = runs[r];
+        const int64_t in_block = slots[first] / kKvBlockTokens;
+        char* const block = kv8_block<B>(p, slots[first], h);
+        char* const codes = block + v * B::kV;
+        const T* const from = v ? (const T*)a.v + h * a.v_head_stride : (const T*)a.k + h * a.k_head_stride;
+        const int64_t stride = v ? a.v_token_stride : a.k_token_stride;
+        const uint32_t held = *(const uint32_t*)(block + B::kExponents);
+        // The next tokens of the run from `at` on, up to 16, into pick; skipped slots between them do not end it.  Where there
+        // are more (the same slots over and over), `at` becomes the next one's place and `more` true.
+        int32_t* const pick = picks[warp];
+        auto gather = [&](int64_t& at, bool& more) {
+            int n = 0;
+            more = false;
+            __syncwarp();
+            for (;; at += 32) {
+                const int64_t t = at + lane, s = t - t0 < kKv8Span + kKvBlockTokens ? slots[t - t0] : t < a.tokens ? a.slots[t] : -1;
+                const bool valid = (uint64_t)s < (uint64_t)p.room, same = valid && s / kKvBlockTokens == in_block;
+                const uint32_t ends = __ballot_sync(0xffffffffu, (valid && !same) || t >= a.tokens);
+                const uint32_t in = __ballot_sync(0xffffffffu, same) & ((ends & (0u - ends)) - 1u);
+                const int place = n + __popc(in & ((1u << lane) - 1u));
+                const bool mine = in >> lane & 1u;
+                if (mine && place < kKvBlockTokens) pick[place] = (int32_t)t;
+                const uint32_t over = __ballot_sync(0xffffffffu, mine && place == kKvBlockTokens);
+                n += __popc(in);
+                if (over != 0u) {
+                    at += __ffs((int)over) - 1;
+                    more = true;
+                    break;
+                }
+                if (ends != 0u) break;
+            }
+            __syncwarp();
+            return min(n, kKvBlockTokens);
+        };
+        const int64_t run = t0 + first;
+        int64_t next = run;
+        bool repeats;
+        const int length = gather(next, repeats);
+        float x[kHeld][8];
+        uint32_t rows = 0;      // where this lane's tokens go, 4 bits each
+        float most = 0.f;
+        uint32_t starts = 0;    // is the block's first token among them
+        auto take = [&](int n) {  // the tokens in pick: their values, what is largest of them
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int k = i * kRows + sub;
+                if (k < n) {
+                    const int64_t t = pick[k];
+                    kv8_load(from + t * stride + 8 * m, x[i]);
+                    const int row = (int)(t - t0 < kKv8Span + kKvBlockTokens ? slots[t - t0] : a.slots[t]) & (kKvBlockTokens - 1);
+                    rows = (rows & ~(15u << (4 * i))) | (uint32_t)row << (4 * i);
+                    starts |= row == 0 ? 1u : 0u;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) x[i][c] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    x[i][c] = x[i][c] == x[i][c] ? x[i][c] : 0.f;  // NaN is stored as 0
+                    const float size = fabsf(x[i][c]);
+                    if (size < INFINITY) most = fmaxf(most, size);
+                }
+        };
+        take(length);
+        if (repeats) {  // all others are looked at before any is written
+            int64_t at = next;
+            for (bool more = true; more;) take(gather(at, more));
+            at = run;
+            take(gather(at, repeats));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const int old = kv8_exponent(held, v);
+        const bool anew = __any_sync(0xffffffffu, starts != 0u);
+        int e = kv8_exponent_of(most);
+        if (!anew) e = max(e, old);
+        if (!anew && e > old) {  // the codes that are there, in the new unit
+            const float down = two_to(old - e);
+            for (int i = lane; i < D; i += 32) {  // 16 bytes each
+                uint4 c = *((uint4*)codes + i);
+                uint32_t* const w = (uint32_t*)&c;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t low, high;
+                    from_e4m3x4(w[k], low, high);
+                    const float2 y = __half22float2(*(const __half2*)&low), z = __half22float2(*(const __half2*)&high);
+                    w[k] = to_e4m3x4(y.x * down, y.y * down, z.x * down, z.y * down);
+                }
+                *((uint4*)codes + i) = c;
+            }
+            __syncwarp();
+        }
+        const float by = two_to(-e);
+        auto put = [&](int n) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                if (i * kRows + sub >= n) continue;
+                const int row = (int)(rows >> (4 * i)) & 15;
+                *(uint2*)(codes + B::at(row, m >> 1) + 8 * (m & 1)) =
+                    make_uint2(to_e4m3x4(x[i][0] * by, x[i][1] * by, x[i][2] * by, x[i][3] * by),
+                               to_e4m3x4(x[i][4] * by, x[i][5] * by, x[i][6] * by, x[i][7] * by));
+            }
+        };
+        put(length);
+        for (bool more = repeats; more;) {
+            const int n = gather(next, more);
+            take(n);
+            put(n);
+        }
+        if (lane == 0) *(int8_t*)(block + B::kExponents + v) = (int8_t)e;
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kKv8Threads) kv8_read_kernel(const __grid_constant__ Kv8Params p) {
+    using B = Kv8Block<D>;
+    constexpr int kLanes = D / 8;
+    const rra_kv_tokens_args_t& a = p.a;
+    pdl_release_early();
+    const int m = (int)threadIdx.x % kLanes, pair = (int)((blockIdx.x * (uint32_t)kKv8Threads + threadIdx.x) / kLanes);
+    const int t = p.by_heads(pair), h = pair - t * p.by_heads.d;
+    pdl_wait();
+    if (t >= a.tokens) return;
+    const int64_t slot = a.slots[t];
+    float x[2][8];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[v][c] = 0.f;
+    if ((uint64_t)slot < (uint64_t)p.room) {
+        const char* const block = kv8_block<B>(p, slot, h);
+        const int row = (int)slot & (kKvBlockTokens - 1);
+        const uint32_t e = *(const uint32_t*)(block + B::kExponents);
+        uint2 w[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) w[v] = *(const uint2*)(block + v * B::kV + B::at(row, m >> 1) + 8 * (m & 1));
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const float by = two_to(kv8_exponent(e, v));
+            uint32_t f[4];
+            from_e4m3x4(w[v].x, f[0], f[1]);
+            from_e4m3x4(w[v].y, f[2], f[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 y = __half22float2(*(const __half2*)&f[i]);
+                x[v][2 * i] = y.x * by, x[v][2 * i + 1] = y.y * by;
+            }
+        }
+    }
+    kv8_store((T*)a.k + t * a.k_token_stride + h * a.k_head_stride + 8 * m, x[0]);
+    kv8_store((T*)a.v + t * a.v_token_stride + h * a.v_head_stride + 8 * m, x[1]);
+}
+
+static rra_status_t kv8_tokens(const rra_kv_tokens_args_t* a, rra_stream_t stream, bool append) {
+    if (a == nullptr || !kv_cache_ok(a->cache) || a->tokens < 0 || a->reserved != 0) return RRA_ERR_INVALID_ARG;
+    if (a->dtype != RRA_FP32 && a->dtype != RRA_BF16) return RRA_ERR_INVALID_ARG;
+    const int elem = a->dtype == RRA_FP32 ? 4 : 2;
+    const rra_kv_cache_t& c = a->cache;
+    if (!strides_ok(a->k_token_stride, a->k_head_stride, c.kv_heads, c.head_dim, elem) ||
+        !strides_ok(a->v_token_stride, a->v_head_stride, c.kv_heads, c.head_dim, elem) || !aligned16(a->k) || !aligned16(a->v))
+        return RRA_ERR_INVALID_ARG;
+    if (a->tokens == 0) return RRA_OK;
+    if (a->k == nullptr || a->v == nullptr || a->slots == nullptr) return RRA_ERR_INVALID_ARG;
+    if (a->tokens > INT32_MAX / 32 / c.kv_heads) return RRA_ERR_INVALID_ARG;  // threads are counted in 32 bits
+    Kv8Params p;
+    p.a = *a;
+    p.by_heads = Divisor(c.kv_heads);
+    p.by_page = Divisor(c.page_tokens / kKvBlockTokens);
+    p.room = c.num_pages * c.page_tokens;
+    const bool big = c.head_dim == 128;
+    dim3 grid;
+    const void* k;
+    if (append) {
+        // a CTA a token and four heads, a warp a row: where tokens are few each may be a block of its own
+        p.span = a->tokens * c.kv_heads <= 4096 ? 1 : kKv8Span;
+        p.heads = std::min(4, c.kv_heads);
+        grid = dim3((unsigned)((a->tokens + p.span - 1) / p.span), (unsigned)((c.kv_heads + p.heads - 1) / p.heads));
+        k = elem == 4 ? (big ? (const void*)kv8_append_kernel<float, 128> : (const void*)kv8_append_kernel<float, 64>)
+                      : (big ? (const void*)kv8_append_kernel<__nv_bfloat16, 128> : (const void*)kv8_append_kernel<__nv_bfloat16, 64>);
+    } else {
+        const int per_cta = kKv8Threads / (c.head_dim / 8);
+        p.span = p.heads = 1;
+        grid = dim3((unsigned)((a->tokens * c.kv_heads + per_cta - 1) / per_cta));
+        k = elem == 4 ? (big ? (const void*)kv8_read_kernel<float, 128> : (const void*)kv8_read_kernel<float, 64>)
+                      : (big ? (const void*)kv8_read_kernel<__nv_bfloat16, 128> : (const void*)kv8_read_kernel<__nv_bfloat16, 64>);
+    }
+    void* args[] = {(void*)&p};
+    return serve_launch(k, grid, kKv8Threads, 0, 1, stream, args);
+}
+
+}  // namespace rra
+
+extern "C" {
+
+size_t rra_kv8_page_bytes(int page_tokens, int kv_heads, int head_dim) {
+    if (rra_kv_page_bytes(page_tokens, kv_heads, head_dim) == 0) return 0;
+    return (size_t)kv_heads * (size_t)(page_tokens / rra::kKvBlockTokens) * (32u * (size_t)head_dim + 16u);
+}
+
+rra_status_t rra_kv8_append(const rra_kv_tokens_args_t* args, rra_stream_t stream) { return rra::kv8_tokens(args, stream, true); }
+
+rra_status_t rra_kv8_read(const rra_kv_tokens_args_t* args, rra_stream_t stream) { return rra::kv8_tokens(args, stream, false); }
+
+}  // extern "C"

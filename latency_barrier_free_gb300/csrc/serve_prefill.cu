@@ -36,7 +36,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "serve_attn.cuh"
+#include "serve_attn_rows8.cuh"
 
 namespace rra {
 
@@ -54,14 +54,15 @@ constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 bef
 constexpr float kPromptLift = 7.f, kPromptUnlift = 1.f / 128;
 static_assert(kPromptMaxCtas * 2 <= kAttnMaxCtas, "a counter for each tile of a CTA's last segment");
 
-template <int D, int TILES>
+template <typename F, int D, int TILES>
 struct PromptShape {
-    using B = KvBlock<D>;
+    using B = typename F::template Block<D>;
+    static constexpr int kParts = F::kBits == 4 ? 2 : 1;  // of K: high and low, or codes as they are
     static constexpr int kRows = TILES * kPromptRows;
     static constexpr int kPanel = 128 * 128;            // 128 rows of 64 binary16, swizzled in 128 bytes
     static constexpr int kTile = D / 64 * kPanel;       // 128 rows of D binary16
-    static constexpr int kK = TILES * kTile;            // after the queries: two stages of K, high and low parts
-    static constexpr int kV = kK + 4 * kTile;           // V
+    static constexpr int kK = TILES * kTile;            // after the queries: two stages of K, all parts
+    static constexpr int kV = kK + 2 * kParts * kTile;  // V
     static constexpr int kEnd = kV + kTile;
     static constexpr int kSums = kK;                    // before any tile: running sums of the requests' chunks
     static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
@@ -82,7 +83,7 @@ struct PromptShape {
     static_assert(TILES * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= (TILES + 2) * kLaunchRegs, "what the launch has");
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kColumns = TILES == 2 ? 512 : 256;  // of TMEM: S of every tile, then O of every tile
-    static constexpr int kPart = kPromptRows * (D + 2);      // floats of a part: rows in columns of 4 channels, statistics
+    static constexpr int kPartFloats = kPromptRows * (D + 2);  // floats of a part: rows in columns of 4 channels, statistics
     static constexpr int kSmem = 1024 + kEnd;
 };
 
@@ -265,16 +266,18 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t& total, int64_t*
     return before + inc - v;
 }
 
-template <int D, int TILES>
-__global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attention_prompt_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = PromptShape<D, TILES>;
-    using B = KvBlock<D>;
-    constexpr int J = B::kGroups;
+template <typename F, int D, int TILES>
+__global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_attention_prompt_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = PromptShape<F, D, TILES>;
+    using B = typename F::template Block<D>;
+    constexpr int J = D / kKvGroup;
+    constexpr bool kEight = F::kBits == 8;
     extern __shared__ unsigned char raw_smem[];
     __shared__ __align__(8) uint64_t bar_mem[5 * TILES + 4 + 2 + 4 + 1 + 8];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
     __shared__ volatile int32_t places[4][9];  // of four tiles: the cache's blocks of its keys (-1: none), and how many keys there are
+    __shared__ int2 exponents[4][8];  // 8-bit cache: of K and V in the blocks of four tiles
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t arrived[2][TILES];  // of the run's first and last segment
     __shared__ volatile uint32_t added[2][TILES];    // whether this CTA has counted itself there
@@ -410,7 +413,9 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             const int t0 = first_of(seg), t1 = end_of(seg);
             const int all_rows = seg.n.qn * p.group, r = seg.c * Sh::kRows + i * kPromptRows + row;
             const bool live = r < all_rows;
-            float m = -FLT_MAX, limit = -FLT_MAX, l = 0.f, factor = 1.f;
+            constexpr float kNone = kEight ? -0x1p90f : -FLT_MAX;  // no key yet (8 bits: scores are below 2^58, and m enters times 2^32)
+            float m = kNone, limit = kNone, l = 0.f, factor = 1.f;
+            int x = 0;  // 8-bit cache: the exponent that goes with m
             if (t0 < t1) {
                 // ---- the row's query, scaled, into shared memory; the keys that it sees ----
                 int lo = 0, hi = 0;
@@ -438,7 +443,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                             most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
                     }
                     attn_row_scale(p, most, down, factor);
-                    factor *= 0.5f;  // K is held twice as large
+                    if constexpr (!kEight) factor *= 0.5f;  // K is held twice as large
 #pragma unroll
                     for (int k = 0; k < D / 8; ++k) {
                         const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -475,6 +480,81 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
 #pragma unroll
                             for (int k = 0; k < 32; ++k) v[32 * q + k] = mask >> k & 1u ? v[32 * q + k] : 0xff800000u;
                         }
+                    }
+                    if constexpr (kEight) {
+                        // As in serve_attn_rows8.cuh: a block of 16 keys has the exponents k and v; scores are v[] 2^k, weights
+                        // 2^((score - m) factor + v - x), their sum's parts 2^(x - v) as large.
+                        const int2* const ex = exponents[n & 3];
+                        float tops[8], best = 0.f, now = 0.f;  // scores; the largest weight's exponent, its score and x
+                        int at = 0;
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            float top = fmaxf(__uint_as_float(v[16 * b]), __uint_as_float(v[16 * b + 1]));
+#pragma unroll
+                            for (int k = 2; k < 16; ++k) top = fmaxf(top, __uint_as_float(v[16 * b + k]));
+                            tops[b] = top * two_to(ex[b].x);
+                        }
+                        auto find = [&]() {
+                            best = -INFINITY;
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) {
+                                const float up = fmaf(tops[b] - m, factor, (float)(ex[b].y - x));
+                                if (up > best) best = up, now = tops[b], at = ex[b].y;
+                            }
+                        };
+                        find();
+                        if (__any_sync(0xffffffffu, best > kPromptSlack)) {
+                            if (m == kNone && best > kPromptSlack) {  // so far away all weights look alike: again from a key
+                                m = now;
+                                x = at;
+                                find();
+                            }
+                            const bool moves = best > kPromptSlack;
+                            const float by = moves ? exp2_fast(-best) : 1.f;
+                            if (moves) {
+                                l *= exp2_fast((m - now) * factor);
+                                m = now;
+                                x = at;
+                            }
+                            if (tl > t0) {
+#pragma unroll 1
+                                for (int q = 0; q < D / 16; ++q) {
+                                    uint32_t o[16];
+                                    tc_ld16(o_at + 16 * q, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                                    tc_st16(o_at + 16 * q, o);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                            for (int b = 4 * q; b < 4 * q + 4; ++b) {
+                                const int2 e = ex[b];
+                                const float by = factor * two_to(e.x), less = -m * two_to(-e.x), lift = kPromptLift + (float)(e.y - x);
+                                const uint64_t by2 = pair2(by, by), less2 = pair2(less, less), lifts = pair2(lift, lift);
+                                uint64_t sum = pair2(0.f, 0.f);
+#pragma unroll
+                                for (int k = 16 * b; k < 16 * b + 16; k += 2) {
+                                    float e0, e1;
+                                    split2(fma2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), less2), by2, lifts), e0, e1);
+                                    e0 = exp2_fast(e0);
+                                    e1 = exp2_fast(e1);
+                                    sum = add2(sum, pair2(e0, e1));
+                                    v[k / 2] = pack_half2(e0, e1);
+                                }
+                                float a0, a1;
+                                split2(sum, a0, a1);
+                                l = fmaf(a0 + a1, two_to(x - e.y), l);
+                            }
+                            tc_st32(s_at + 32 * q, v + 32 * q);
+                        }
+                        tc_wait_st();
+                        tc_before_sync();
+                        mbar_arrive(pv_full + 8 * i);
+                        continue;
                     }
                     float tops[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
 #pragma unroll
@@ -531,6 +611,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             const bool starts = seg.begin >= r0, ends = seg.end <= r1;
             const float top = m * factor;
             l *= kPromptUnlift;  // O stays lifted until it is divided by its sum
+            const float up = kEight ? two_to(x) : 1.f;  // what O is too small by
             auto put = [&](__nv_bfloat16* to, const float* o, float inv) {  // 32 channels
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
@@ -548,6 +629,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 float inv = 0.f;
                 __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, top, l, true, inv) : nullptr;
                 inv *= kPromptUnlift;
+                if constexpr (kEight) inv *= up;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
@@ -570,13 +652,16 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 int mine = (int)blockIdx.x;
                 if (others != (uint32_t)(i1 - i0)) {
                     mine = -1;
-                    float4* const to = (float4*)(parts + (((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * TILES + i) * Sh::kPart);
+                    float4* const to = (float4*)(parts + (((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * TILES + i) * Sh::kPartFloats);
                     if (t0 < t1) {
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t v[32];
                             tc_ld32(o_at + 32 * q, v);
                             tc_wait_ld();
+                            if constexpr (kEight)
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * up);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 to[(8 * q + k) * kPromptRows + row] =
@@ -597,7 +682,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 if (others == (uint32_t)(i1 - i0)) {
                     __threadfence();
                     auto part_of = [&](int x) {
-                        return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPart);
+                        return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPartFloats);
                     };
                     auto stats_of = [&](int x) {
                         return x == mine ? make_float2(top, l) : __ldcg((const float2*)(part_of(x) + D / 4 * kPromptRows) + row);
@@ -625,6 +710,9 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                             if (x == mine) {
                                 tc_ld32(o_at + 32 * q, v);
                                 tc_wait_ld();
+                                if constexpr (kEight)
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * up);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) *(float4*)(v + 4 * k) = __ldcg(part_of(x) + (8 * q + k) * kPromptRows + row);
@@ -664,10 +752,10 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         // so that a half of V's keys is unpacked while products still read the other
         set_registers<Sh::kUnpackRegs, Sh::kLaunchRegs>();
         const int unpacker = warp - Sh::kUnpack, side = unpacker >> 1, key_in = 32 * (unpacker & 1) + lane;
-        constexpr int kLoads = D / 64;  // 16-byte loads of half a row of codes
+        constexpr int kLoads = D * F::kBits / 256;  // 16-byte loads of half a row of codes
         struct Codes {  // of half a row, and the row's scales
             uint4 c[kLoads];
-            uint32_t s[J / 2];
+            uint32_t s[kEight ? 1 : J / 2];
         };
         struct Places {  // the keys' blocks; null if they are not there
             const char* block[2];
@@ -690,18 +778,41 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool here = at.block[i] != nullptr;
+                if constexpr (kEight) {
+#pragma unroll
+                    for (int k = 0; k < kLoads; ++k)
+                        x[i].c[k] = here ? *(const uint4*)(at.block[i] + codes + B::at(row, side * kLoads + k)) : make_uint4(0u, 0u, 0u, 0u);
+                    x[i].s[0] = 0u;
+                    if (codes == 0 && side == 0 && row == 0 && here) x[i].s[0] = *(const uint32_t*)(at.block[i] + scales);
+                } else {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k)
                     x[i].c[k] = here ? *((const uint4*)(at.block[i] + codes + row * B::kRow + side * (B::kRow / 2)) + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int k = 0; k < J / 2; ++k)
                     x[i].s[k] = here ? *((const uint32_t*)(at.block[i] + scales + row * B::kScaleRow) + k) : 0u;
+                }
             }
         };
         // Half a row's codes as binary16 into their place of a swizzled tile; with_rest twice as large, and the part that
         // rounding lost into `rest`.
         const uint32_t row_at = key_in * 128;
         auto unpack = [&](const Codes& x, uint32_t to, uint32_t rest, auto with_rest) {
+            if constexpr (kEight) {
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int piece = side * kLoads + k;  // 16 channels: two 16-byte pieces of a row of 64
+                    const uint32_t w[4] = {x.c[k].x, x.c[k].y, x.c[k].z, x.c[k].w};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t h[4];
+                        from_e4m3x4(w[2 * e], h[0], h[1]);
+                        from_e4m3x4(w[2 * e + 1], h[2], h[3]);
+                        sts_v4(to + (piece >> 2) * Sh::kPanel + row_at + ((((piece & 3) * 2 + e) ^ (key_in & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    }
+                }
+                return;
+            } else {
             uint32_t wd[4 * kLoads];
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) wd[4 * k] = x.c[k].x, wd[4 * k + 1] = x.c[k].y, wd[4 * k + 2] = x.c[k].z, wd[4 * k + 3] = x.c[k].w;
@@ -731,6 +842,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                         }
                     }
                 }
+            }
         };
         constexpr uint32_t kHalf = 64 * 128;  // from a tile's first key to its 65th
         int64_t left = 0;  // tiles of this run
@@ -740,11 +852,13 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             prompt_next<Sh::kRows>(p, s);
         }
         // K is unpacked a tile ahead of V: its two stages are free before V's one
+        constexpr int kScalesK = [] { if constexpr (kEight) return B::kExponents; else return B::kScaleK; }();
+        constexpr int kScalesV = [] { if constexpr (kEight) return B::kExponents; else return B::kScaleV; }();
         Codes k[2], v[2];        // K of tile n, V of tile n - 1
         Places here = {{nullptr, nullptr}};  // of tile n
         if (left > 0) {
             here = places_of(0);
-            load(k, here, 0, B::kScaleK);
+            load(k, here, 0, kScalesK);
         }
 #pragma unroll 1
         for (int64_t tile = 0; ok && tile <= left && left > 0; ++tile) {
@@ -752,13 +866,20 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
             const uint32_t t = (uint32_t)tile, stage = t & 1;
             if (tile < left) {
                 const uint32_t there = __ballot_sync(0xffffffffu, (side == 0 ? now.block[0] : now.block[1]) != nullptr);
+                if constexpr (kEight) {
+                    if (side == 0 && row == 0)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            exponents[t & 3][key_in / kKvBlockTokens + 4 * i] = make_int2(kv8_exponent(k[i].s[0], 0), kv8_exponent(k[i].s[0], 1));
+                    __syncwarp();
+                }
                 if (lane == 0) {
                     seen_words[t & 3][unpacker] = there;
                     mbar_arrive(seen_full + 8 * (t & 3));
                 }
                 if (tile >= 2) ok = wait(k_empty + 8 * stage, (t >> 1) - 1);
                 if (!ok) break;
-                const uint32_t to = smem + Sh::kK + stage * 2 * Sh::kTile;
+                const uint32_t to = smem + Sh::kK + stage * Sh::kParts * Sh::kTile;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) unpack(k[i], to + i * kHalf, to + Sh::kTile + i * kHalf, std::true_type{});
                 fence_proxy_async_smem();
@@ -766,7 +887,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 if (tile + 1 < left) {
                     here = places_of(t + 1);
                     if (!ok) break;
-                    load(k, here, 0, B::kScaleK);
+                    load(k, here, 0, kScalesK);
                 }
             }
             if (tile > 0) {  // V of the tile before
@@ -780,7 +901,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                 fence_proxy_async_smem();
                 for (int i = 0; i < TILES; ++i) mbar_arrive(pv_full + 8 * i);
             }
-            if (tile < left) load(v, now, B::kV, B::kScaleV);
+            if (tile < left) load(v, now, B::kV, kScalesV);
         }
     } else {
         // =============================== products of tile i: one thread issues ====
@@ -831,7 +952,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                     ok = (!next || wait(k_full + 8 * (then & 1), then >> 1)) && (values ? wait(pv_full + 8 * i, n) : wait(q_full + 8 * i, sn));
                     if (!ok) break;
                     tc_after_sync();
-                    const uint32_t k_at = k_desc + (then & 1) * 2 * kStep;
+                    const uint32_t k_at = k_desc + (then & 1) * Sh::kParts * kStep;
                     if (elected()) {
                         if (values) {  // O_i += P_i V
 #pragma unroll
@@ -841,9 +962,9 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
                             }
                             tc_commit(v_empty + 8);
                         }
-                        if (next) {  // S_i = Q_i K^T, both parts of K
+                        if (next) {  // S_i = Q_i K^T, all parts of K
 #pragma unroll
-                            for (int k = 0; k < 2 * (D / 16); ++k) {
+                            for (int k = 0; k < Sh::kParts * (D / 16); ++k) {
                                 constexpr auto at = [](int x) { return (uint32_t)((x % (D / 16) >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
                                 tc_mma(s_at, q_desc + at(k), k_at + k / (D / 16) * kStep + at(k), kQk, k > 0);
                             }
@@ -876,10 +997,10 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::kThreads, 1) kv_attenti
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" : : "r"(tmem), "r"(Sh::kColumns) : "memory");
 }
 
-template <int D, int TILES>
+template <typename F, int D, int TILES>
 static rra_status_t prompt_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
-    using Sh = PromptShape<D, TILES>;
-    const void* k = (const void*)kv_attention_prompt_kernel<D, TILES>;
+    using Sh = PromptShape<F, D, TILES>;
+    const void* k = (const void*)kv_attention_prompt_kernel<F, D, TILES>;
     static_assert(Sh::kSmem <= 227 * 1024 - 1024, "shared memory");
     if (configure_cluster_kernel(k, Sh::kSmem) != cudaSuccess) {
         cudaGetLastError();
@@ -899,10 +1020,15 @@ size_t prefill_partial_bytes(int head_dim) {
     return (size_t)kPromptMaxCtas * 2 * 2 * kPromptRows * ((size_t)head_dim + 2) * sizeof(float);
 }
 
-rra_status_t launch_prefill(const AttnParams& p, int tiles, int sms, rra_stream_t stream) {
+template <typename F>
+static rra_status_t prefill_launch(const AttnParams& p, int tiles, int ctas, rra_stream_t stream) {
+    if (p.a.cache.head_dim == 128) return tiles == 2 ? prompt_launch<F, 128, 2>(p, ctas, stream) : prompt_launch<F, 128, 1>(p, ctas, stream);
+    return tiles == 2 ? prompt_launch<F, 64, 2>(p, ctas, stream) : prompt_launch<F, 64, 1>(p, ctas, stream);
+}
+
+rra_status_t launch_prefill(const AttnParams& p, int bits, int tiles, int sms, rra_stream_t stream) {
     const int ctas = std::min(sms, kPromptMaxCtas);
-    if (p.a.cache.head_dim == 128) return tiles == 2 ? prompt_launch<128, 2>(p, ctas, stream) : prompt_launch<128, 1>(p, ctas, stream);
-    return tiles == 2 ? prompt_launch<64, 2>(p, ctas, stream) : prompt_launch<64, 1>(p, ctas, stream);
+    return bits == 8 ? prefill_launch<Cache8>(p, tiles, ctas, stream) : prefill_launch<Cache4>(p, tiles, ctas, stream);
 }
 
 }  // namespace rra

@@ -1,8 +1,8 @@
-"""Python binding of the decode-step operators (include/rra_serve.h).
+"""Python binding of the serving operators (include/rra_serve.h).
 
 Page bookkeeping, head norms with position rotation, a key/value cache held in
-4 bits, and the attention over it: what a tensor-parallel rank runs around its
-AllReduces.  As in rra.py this is argument checking and marshalling only (in
+4 or 8 bits, and the attention over it: what a tensor-parallel rank runs around its
+AllReduces; and pages that several requests share.  As in rra.py this is argument checking and marshalling only (in
 _serve.so, csrc/serve_bind.cpp); every call enqueues one kernel of librra.so on the
 current stream (or `stream`), and there is no fallback.  Tensors are on the current
 GPU; those of another one are refused.
@@ -27,6 +27,10 @@ _ROPE = struct.Struct("9P10qd6i")
 _TOKENS = struct.Struct("Pq4i3P5q2i")
 _ATTN = struct.Struct("Pq4i7P6qd8i")
 _CACHE = struct.Struct("Pq4i")
+_FORK = struct.Struct("13Pq6i")
+_RELEASE = struct.Struct("9Pq4i")
+_COMPACT = struct.Struct("13P2q6i")
+_COPY = struct.Struct("4P3q2i")
 
 _WORKSPACE_HEAD = 4096  # bytes of the workspace that a call expects to be zero
 
@@ -41,11 +45,15 @@ def _lib():
         vp = ctypes.c_void_p
         sig = {"rra_slot_map": [vp, vp], "rra_qk_norm_rope": [vp, vp], "rra_kv_append": [vp, vp],
                "rra_kv_read": [vp, vp], "rra_kv_attention": [vp, vp],
-               "rra_kv_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)]}
+               "rra_kv_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)],
+               "rra_kv8_append": [vp, vp], "rra_kv8_read": [vp, vp], "rra_kv8_attention": [vp, vp],
+               "rra_kv8_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)], "rra_pages_fork": [vp, vp],
+               "rra_pages_release": [vp, vp], "rra_pages_compact": [vp, vp], "rra_pages_copy": [vp, vp]}
         for name, args in sig.items():
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, ctypes.c_int
-        lib.rra_kv_page_bytes.argtypes, lib.rra_kv_page_bytes.restype = [ctypes.c_int] * 3, ctypes.c_size_t
+        for fn in (lib.rra_kv_page_bytes, lib.rra_kv8_page_bytes):
+            fn.argtypes, fn.restype = [ctypes.c_int] * 3, ctypes.c_size_t
         lib.rra_kv_attention_workspace_bytes.argtypes = [ctypes.c_int]
         lib.rra_kv_attention_workspace_bytes.restype = ctypes.c_size_t
         _fns = lib
@@ -112,6 +120,53 @@ def kv_page_bytes(page_tokens: int, kv_heads: int, head_dim: int) -> int:
     return n
 
 
+def kv8_page_bytes(page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of the 8-bit cache."""
+    n = _lib().rra_kv8_page_bytes(page_tokens, kv_heads, head_dim)
+    if n == 0:
+        raise rra.RraError(rra.ERR_INVALID_ARG, "rra_kv8_page_bytes")
+    return n
+
+
+def pages_fork(seq_len, source, target, block_table, free_pages, free_count, shared, page_tokens, *, kv_len, shared_out,
+               copy_from, copy_to, free_left, pages_short, stream=None) -> None:
+    """Requests that continue others (rra_pages_fork): row target[i] becomes a copy
+    of row source[i], whose whole pages both share from then on (shared counts a
+    page's holders beyond the first); the last one, if it is not full, gets a page
+    of its own, and copy_from[i], copy_to[i] say what to copy: give them to copy() of
+    the cache of every layer.  All int32; kv_len may be seq_len, shared_out shared,
+    free_left free_count."""
+    st = _native.pages_fork(seq_len, source, target, block_table, free_pages, free_count, shared, page_tokens, kv_len, shared_out,
+                            copy_from, copy_to, free_left, pages_short, stream)
+    if st:
+        raise rra.RraError(st, "rra_pages_fork")
+
+
+def pages_release(seq_len, new_len, block_table, free_pages, free_count, shared, page_tokens, *, kv_len, shared_out, free_left,
+                  stream=None) -> None:
+    """Requests with new_len[b] < 0 end (rra_pages_release): their pages go back on
+    the stack once nobody else holds them, and their kv_len is 0, so that slot_map
+    with the same new_len returns nothing for them again.  kv_len may be seq_len,
+    shared_out shared, free_left free_count."""
+    st = _native.pages_release(seq_len, new_len, block_table, free_pages, free_count, shared, page_tokens, kv_len, shared_out,
+                               free_left, stream)
+    if st:
+        raise rra.RraError(st, "rra_pages_release")
+
+
+def pages_compact(seq_len, block_table, free_pages, free_count, shared, page_tokens, *, table_out, free_out, shared_out, free_left,
+                  moved, move_from, move_to, move_count, stream=None) -> None:
+    """Moves the highest pages in use to the lowest free ones, at most
+    move_from.numel() (rra_pages_compact): new tables, stack and counts, moved[p] the
+    new number of page p (-1: it was free), and the moves (-1 behind the last), which
+    copy() of the cache of every layer carries out.  table_out may be block_table,
+    free_out free_pages, free_left free_count, shared_out shared."""
+    st = _native.pages_compact(seq_len, block_table, free_pages, free_count, shared, page_tokens, table_out, free_out, shared_out,
+                               free_left, moved, move_from, move_to, move_count, stream)
+    if st:
+        raise rra.RraError(st, "rra_pages_compact")
+
+
 class KvCache:
     """A paged key/value cache held in 4 bits, in memory of the caller.
 
@@ -122,13 +177,15 @@ class KvCache:
     once they are enqueued, but for calls whose stream was given as a number, which
     it has to outlive, and for graphs that hold calls."""
 
+    _size = staticmethod(kv_page_bytes)
+
     def __init__(self, pages, page_tokens: int, kv_heads: int, head_dim: int):
         lib = _lib()
-        size = kv_page_bytes(page_tokens, kv_heads, head_dim)
+        size = self._size(page_tokens, kv_heads, head_dim)
         self._dev = _device(pages)
         if pages.dtype is not torch.uint8 or not pages.is_contiguous() or pages.numel() % size:
             raise ValueError("pages must be a contiguous uint8 tensor of whole pages (%d bytes each)" % size)
-        self.pages = pages
+        self.pages, self.page_bytes = pages, size
         self.page_tokens, self.kv_heads, self.head_dim = int(page_tokens), int(kv_heads), int(head_dim)
         self.num_pages = pages.numel() // size
         self._workspace = torch.empty(lib.rra_kv_attention_workspace_bytes(head_dim), dtype=torch.uint8,
@@ -180,6 +237,17 @@ class KvCache:
             raise rra.RraError(st, "rra_kv_attention_plan")
         return name.value.decode()
 
+    def copy(self, source, target, to=None, stream=None) -> None:
+        """Page target[i] becomes a copy of page source[i] (rra_pages_copy; int32, pairs
+        with a number outside the cache are skipped), of this cache or of `to`, a cache
+        of the same kind.  Not ordered with other streams, like append()."""
+        to = self if to is None else to
+        if type(to) is not type(self) or (to.page_tokens, to.kv_heads, to.head_dim) != (self.page_tokens, self.kv_heads, self.head_dim):
+            raise ValueError("pages are copied between caches of one kind, page size and heads")
+        st = _native.pages_copy(self.pages, to.pages, self.page_bytes, source, target, stream)
+        if st:
+            raise rra.RraError(st, "rra_pages_copy")
+
     def status(self) -> int:
         """Status word of the attention calls so far (0 is fine), whatever their
         stream; synchronises with the GPU."""
@@ -190,3 +258,34 @@ class KvCache:
         """Sets the status back to 0, in the order of the current stream: after a
         status that is not, attention() gives valid results from here on."""
         self._workspace[:_WORKSPACE_HEAD].zero_()
+
+
+class KvCache8(KvCache):
+    """The same over a cache held in 8 bits: e4m3 codes, and an exponent for each
+    block of 16 tokens and head (kv8_page_bytes(); layout and rounding stand in
+    rra_serve.h)."""
+
+    _size = staticmethod(kv8_page_bytes)
+
+    def append(self, k, v, slots, stream=None) -> None:
+        """Write k and v [tokens, kv_heads, head_dim] to the slots (int64; negative:
+        skipped).  The slots of one block of 16 are neighbours in the list; the one at
+        a block's start begins it anew, the others keep what it holds, rounded again
+        where they are larger than all before."""
+        st = _native.kv8_append(self._cache, self._dev, k, v, slots, stream)
+        if st:
+            raise rra.RraError(st, "rra_kv8_append")
+
+    def read(self, slots, k, v, stream=None) -> None:
+        """k and v [tokens, kv_heads, head_dim] become the values that the slots hold."""
+        st = _native.kv8_read(self._cache, self._dev, k, v, slots, stream)
+        if st:
+            raise rra.RraError(st, "rra_kv8_read")
+
+    def attention(self, q, out, cu_q, kv_len, block_table, *, max_q: int, max_kv: int, scale=None, causal: bool = True,
+                  window: int = 0, lse=None, stream=None) -> None:
+        """As KvCache.attention, over this cache (rra_kv8_attention)."""
+        st = _native.kv8_attention(self._cache, self._dev, self._workspace, q, out, cu_q, kv_len, block_table, max_q, max_kv,
+                                   self._scale if scale is None else scale, causal, window, lse, stream, self._home)
+        if st:
+            raise rra.RraError(st, "rra_kv8_attention")
