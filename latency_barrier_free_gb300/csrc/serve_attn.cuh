@@ -115,7 +115,7 @@ __device__ __forceinline__ AttnLengths attn_lengths(const AttnParams& p, int b) 
     const int most_q = (int)p.a.tokens;
     AttnLengths r;
     r.q0 = min(max(p.a.cu_q[b], 0), most_q);
-    r.qn = max(0, min(p.a.cu_q[b + 1], most_q) - r.q0);
+    r.qn = max(0, min(max(p.a.cu_q[b + 1], 0), most_q) - r.q0);
     r.kv = min(max(p.a.kv_len[b], 0), p.room);
     return r;
 }
