@@ -15,6 +15,7 @@
  *   rra_kv_attention  attention over that cache: single tokens, a few drafted
  *                     tokens, chunks of a prompt
  *   rra_kv8_append, rra_kv8_read, rra_kv8_attention   the same over a cache of 8 bits
+ *   rra_prompt_attention  attention of whole prompts over their own keys and values
  *   rra_pages_fork, rra_pages_release, rra_pages_compact, rra_pages_copy
  *                     pages that several requests share: samples of a prompt,
  *                     their end, holes in the pool closed
@@ -305,6 +306,59 @@ rra_status_t rra_kv8_append(const rra_kv_tokens_args_t* args, rra_stream_t strea
 rra_status_t rra_kv8_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
 rra_status_t rra_kv8_attention(const rra_kv_attention_args_t* args, rra_stream_t stream);
 rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const char** name);
+
+/* ------------------------------------------------- attention of prompts ---
+ * rra_prompt_attention: attention of whole prompts over their own keys and
+ * values, as the projection gives them, before or beside their way into a cache.
+ * Request b has the tokens cu[b] .. cu[b + 1) of q, k, v and out.  Its token i sees
+ * its token j if
+ *     j <= i (if causal),  j > i - window (if window > 0).
+ * Query head h uses KV head h / (q_heads / kv_heads); formulas, lse and scale as in
+ * rra_kv_attention.  Queries, keys and values enter their products as they are;
+ * products, the softmax's maximum, sum and weights are binary32; for the sum over
+ * values a weight is rounded to the values' type (bfloat16, 8 bits; binary16, 11 bits,
+ * times 2^7 against its underflow), out to it once.  Results do not depend on timing.
+ *   An infinity or NaN makes the rows that see its token infinite or NaN, no others.
+ *   q, out [tokens][q_heads][head_dim], k, v [tokens][kv_heads][head_dim], all
+ *   bfloat16, or binary16 (`half`); strides in elements, multiples of 8, below 2^39;
+ *   channels adjacent; pointers 16-byte aligned; out overlaps nothing.  They may be
+ *   parts of a packed projection.  lse NULL or binary32 [tokens][q_heads], contiguous.
+ *   Rows after cu[B] stay as they are.  head_dim a multiple of 8 up to 128.
+ *   cu ascends; where it does not, rows may be computed several times or not at all.
+ *   Its values are clamped to [0, tokens].
+ *   max_len: the longest prompt expected; it steers the choice of kernel only.
+ *   workspace: rra_prompt_attention_workspace_bytes() bytes, with the rules of
+ *   rra_kv_attention's.
+ * requests 0..RRA_SERVE_MAX_REQUESTS; tokens * q_heads up to 2^30 - 1. */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* lse;
+    const int32_t* cu;          /* [requests + 1] */
+    void* workspace;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int64_t tokens;             /* rows of q, k, v and out */
+    double scale;               /* usually 1 / sqrt(head_dim); times log2(e) finite in binary32, as scores are */
+    int32_t requests;
+    int32_t q_heads, kv_heads;
+    int32_t head_dim;
+    int32_t half;               /* 0: bfloat16, 1: binary16 */
+    int32_t max_len;
+    int32_t causal;
+    int32_t window;             /* 0: no window */
+} rra_prompt_attention_args_t;
+
+rra_status_t rra_prompt_attention(const rra_prompt_attention_args_t* args, rra_stream_t stream);
+size_t rra_prompt_attention_workspace_bytes(void);
+
+/* The kernel that rra_prompt_attention launches for these arguments:
+ * "prompt_attention_kernel<128 rows>" or <256 rows>, a CTA's. */
+rra_status_t rra_prompt_attention_plan(const rra_prompt_attention_args_t* args, const char** name);
 
 /* ---------------------------------------------------------- shared pages ---
  * Requests that share pages: samples of one prompt, prompts with a common start.

@@ -26,9 +26,10 @@ NATIVE = os.path.join(HERE, "_serve.so")  # the Python binding of rra_serve.h
 NATIVE_STAMP = os.path.join(BUILD, "_serve.torch")  # the torch that it was built against
 
 SOURCES = ["kernels.cu", "cluster.cu", "coll.cu", "fused.cu", "rra_api.cu", "probes.cu", "rra_static.cu", "serve.cu",
-           "serve_attn.cu", "serve_prefill.cu", "serve_attn_team.cu", "serve_kv8.cu", "serve_pages.cu"]
+           "serve_attn.cu", "serve_prefill.cu", "serve_attn_team.cu", "serve_kv8.cu", "serve_pages.cu",
+           "serve_prompt.cu"]
 HEADERS = ["prims.cuh", "cluster_prims.cuh", "rra_internal.h", "placement.h", "kernel_attrs.h", "serve_common.cuh",
-           "serve_attn.cuh", "serve_attn_rows.cuh", "serve_attn_rows8.cuh"]
+           "serve_attn.cuh", "serve_attn_rows.cuh", "serve_attn_rows8.cuh", "serve_tc.cuh"]
 PUBLIC_HEADERS = ["rra.h", "rra_probe.h", "rra_static.h", "rra_device.cuh", "rra_serve.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -15,6 +15,9 @@
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "rra_serve.h"
 
 namespace {
@@ -31,6 +34,7 @@ Operator<rra_pages_fork_args_t> fn_fork;
 Operator<rra_pages_release_args_t> fn_release;
 Operator<rra_pages_compact_args_t> fn_compact;
 Operator<rra_pages_copy_args_t> fn_copy;
+Operator<rra_prompt_attention_args_t> fn_prompt;
 PyObject* s_cuda_stream;
 
 struct Refused {};  // thrown with a Python exception set
@@ -271,6 +275,40 @@ long attention(PyObject* const* v, Py_ssize_t n, Operator<rra_kv_attention_args_
 long kv_attention(PyObject* const* v, Py_ssize_t n) { return attention(v, n, fn_attention); }
 long kv8_attention(PyObject* const* v, Py_ssize_t n) { return attention(v, n, fn_attention8); }
 
+// (device, workspace, q, k, v, out, cu, max_len, scale, causal, window, lse, stream, the workspace's own stream)
+long prompt_attention(PyObject* const* v, Py_ssize_t n) {
+    arguments(n, 14);
+    rra_prompt_attention_args_t a = {};
+    const int dev = on_current(integer32(v[0]));
+    const at::Tensor &workspace = tensor("workspace", v[1]), &q = tensor("q", v[2]), &k = tensor("k", v[3]), &cu = tensor("cu", v[6]);
+    const at::ScalarType type = q.scalar_type();
+    if (type != at::kBFloat16 && type != at::kHalf) refuse(PyExc_TypeError, "unsupported dtype (bfloat16, float16)");
+    if (q.dim() != 3 || k.dim() != 3 || k.size(0) != q.size(0) || k.size(2) != q.size(2) || k.size(1) < 1 || q.size(1) < 1 ||
+        q.size(1) % k.size(1) != 0 || q.size(1) > INT32_MAX || q.size(2) > INT32_MAX)
+        refuse(PyExc_ValueError, "q and k must be [tokens, heads, channels] with the same tokens and channels, q's heads a multiple of k's");
+    a.workspace = workspace.data_ptr();
+    a.half = type == at::kHalf;
+    a.tokens = q.size(0);
+    a.q_heads = (int32_t)q.size(1);
+    a.kv_heads = (int32_t)k.size(1);
+    a.head_dim = (int32_t)q.size(2);
+    a.q = rows("q", q, type, q.sizes(), dev, &a.q_token_stride, &a.q_head_stride);
+    a.k = rows("k", k, type, k.sizes(), dev, &a.k_token_stride, &a.k_head_stride);
+    a.v = rows("v", tensor("v", v[4]), type, k.sizes(), dev, &a.v_token_stride, &a.v_head_stride);
+    a.out = rows("out", tensor("out", v[5]), type, q.sizes(), dev, &a.out_token_stride, &a.out_head_stride);
+    a.cu = flat<int32_t>("cu", cu, at::kInt, 1, dev);
+    if (cu.numel() - 1 > RRA_SERVE_MAX_REQUESTS) return RRA_ERR_INVALID_ARG;
+    a.requests = (int32_t)(cu.numel() - 1);
+    a.max_len = integer32(v[7]);
+    a.scale = v[8] == Py_None ? 1.0 / std::sqrt((double)std::max(a.head_dim, 1)) : real(v[8]);
+    a.causal = truth(v[9]);
+    a.window = integer32(v[10]);
+    if (v[11] != Py_None) a.lse = flat<float>("lse", v[11], at::kFloat, a.tokens * a.q_heads, dev);
+    const rra_stream_t stream = stream_of(v[12], dev);
+    keep_workspace(workspace, stream, v[12], v[13], dev);
+    return fn_prompt(&a, stream);
+}
+
 // A table whose rows and width are the first one's.
 int32_t* table_like(const char* name, PyObject* o, int64_t requests, int64_t width, int device, int64_t* stride) {
     const at::Tensor& t = tensor(name, o);
@@ -394,6 +432,7 @@ long init(PyObject* const* v, Py_ssize_t n) {
     find(fn_release, "rra_pages_release");
     find(fn_compact, "rra_pages_compact");
     find(fn_copy, "rra_pages_copy");
+    find(fn_prompt, "rra_prompt_attention");
     return 0;
 }
 
@@ -418,6 +457,7 @@ PyMethodDef methods[] = {method<init>("init"),           method<slot_map>("slot_
                          method<kv8_append>("kv8_append"), method<kv8_read>("kv8_read"), method<kv8_attention>("kv8_attention"),
                          method<pages_fork>("pages_fork"), method<pages_release>("pages_release"),
                          method<pages_compact>("pages_compact"), method<pages_copy>("pages_copy"),
+                         method<prompt_attention>("prompt_attention"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

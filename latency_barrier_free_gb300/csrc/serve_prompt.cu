@@ -1,0 +1,770 @@
+// serve_prompt.cu -- attention of whole prompts over their own keys and values
+// (rra_serve.h), on the tensor cores' own memory.
+//
+// A tile is 128 rows: `group` query heads of one KV head, of 128 / group neighbouring
+// tokens, so that heads share their keys and values and few tokens fill a tile.
+// A CTA takes a segment, TILES tiles of one request and KV head, and walks the
+// keys that any of their rows sees, 128 at a time: queries, keys and values come
+// by TMA, one thread for each tile issues
+//     S_i = Q_i K^T,   O_i += P_i V        (tcgen05.mma, sums in TMEM)
+// and two warpgroups for each tile turn S_i into weights P_i, in place.  Two threads
+// have a row, each half of its columns: alone, a thread would take twice as long
+// from scores to weights, and the tensor cores have nothing but the other tile's
+// products to do meanwhile (TMEM: 128 columns of S and D of O a tile, twice).
+//
+// The maximum that weights are taken against moves only when a score passes it by
+// more than kPromptSlack (in units of log2): one vote of a row's two warps a tile,
+// and only then they exchange maxima and scale O, in TMEM.
+//
+// A value that is infinite or NaN would spoil rows that do not see it: 0 times it
+// is NaN.  So in tiles that some row does not see whole, values are looked over in
+// shared memory; such elements become 0 there, and rows that see them get them at
+// their end.
+//
+// Work is cut into equal runs of key tiles, one per CTA (serve_tc.cuh); what a run
+// has of a segment it shares goes to the workspace, and the last CTA to arrive adds
+// the parts in order.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda.h>
+
+#include "serve_tc.cuh"
+
+namespace rra {
+
+constexpr float kPromptSlack = 8.f;  // log2 of how far weights may pass 1 before the maximum moves
+
+struct PromptParams {
+    CUtensorMap q, k, v;  // [channels][heads][tokens]; boxes of 64 channels, q: group heads of `span` tokens, k, v: 128 tokens
+    rra_prompt_attention_args_t a;
+    float factor;         // |scale| log2(e), above 0
+    float flip;           // what scores are multiplied with first: 1, or -1 or 0 with the scale
+    int32_t heads_of_kv;  // query heads of a KV head
+    int32_t group, parts; // query heads of a tile; tiles for all heads of a KV head (1 up to 128 heads)
+    int32_t span;         // tokens of a tile
+    int32_t window;       // a.window, at most 2^30
+    Divisor by_group, by_parts, by_chunk;  // by_chunk: tokens of a CTA
+};
+
+template <typename T, int D, int TILES>
+struct WholeShape {
+    static constexpr bool kHalf = std::is_same<T, __half>::value;
+    static constexpr float kLift = kHalf ? 7.f : 0.f, kUnlift = kHalf ? 1.f / 128 : 1.f;  // weights are 2^kLift times as large: 2^(8 + 7) fits
+    static constexpr int kPanel = 128 * 128;       // 128 rows of 64 channels, swizzled in 128 bytes
+    static constexpr int kTile = D / 64 * kPanel;
+    static constexpr int kStages = 2;              // of K, and of V
+    static constexpr int kK = TILES * kTile, kV = kK + kStages * kTile, kEnd = kV + kStages * kTile;
+    static constexpr int kSums = kK;               // before any tile: running sums of the requests' chunks
+    static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
+    // Warps: eight of softmax for each tile (a warp reaches the TMEM lanes of its number modulo 4; the second four have the
+    // second halves of the rows), then one for each tile that issues its products, and one for the copies.
+    static constexpr int kSoftmaxWarps = 8 * TILES, kIssue = kSoftmaxWarps, kCopy = kIssue + 2, kWarps = kIssue + 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kSoftmaxRegs = TILES == 2 ? 104 : 184;
+    static constexpr int kIssueRegs = TILES == 2 ? 64 : 128;
+    static_assert(2 * TILES * kSoftmaxRegs + kIssueRegs <= (2 * TILES + 1) * kLaunchRegs, "what the launch has");
+    static constexpr int kColumns = TILES == 2 ? 512 : 256;    // of TMEM: S of every tile, then O of every tile
+    static constexpr int kPartFloats = kPromptRows * (D + 2);  // of a part: rows in columns of 4 channels, statistics
+    static constexpr int kSmem = 1024 + kEnd;
+};
+
+// The work: chunks of TILES * span tokens of every request, for every head (a KV head and the part of its query heads).
+template <int TILES>
+struct WholeWork {
+    const PromptParams& p;
+    __device__ __forceinline__ int requests() const { return p.a.requests; }
+    __device__ __forceinline__ int heads() const { return p.a.kv_heads * p.parts; }
+    __device__ __forceinline__ AttnLengths lengths(int b) const {
+        const int most = (int)p.a.tokens;
+        AttnLengths r;
+        r.q0 = min(max(p.a.cu[b], 0), most);
+        r.kv = r.qn = max(0, min(max(p.a.cu[b + 1], 0), most) - r.q0);
+        return r;
+    }
+    __device__ __forceinline__ int chunks(const AttnLengths& n) const { return n.qn > 0 ? p.by_chunk(n.qn - 1) + 1 : 0; }
+    __device__ __forceinline__ PromptItem item(const AttnLengths& n, int c) const {
+        const int first = c * TILES * p.span, last = min(n.qn, first + TILES * p.span) - 1;
+        return prompt_item(p.window > 0 ? max(0, first - p.window + 1) : 0, p.a.causal ? last + 1 : n.qn);
+    }
+};
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int channel, int head, int token, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        :
+        : "r"(dst), "l"(map), "r"(channel), "r"(head), "r"(token), "r"(bar)
+        : "memory");
+}
+// Two warps meet at barrier `id`; whether any of their threads says so.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(x ? 1u : 0u), "r"(id) : "memory");
+    return any != 0u;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) { return pack_half2(a, b); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t*)&h;
+}
+// Of each half of a word whether it is infinite or NaN: its top bit.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return ((w & (kHalf ? 0x7c007c00u : 0x7f807f80u)) + (kHalf ? 0x04000400u : 0x00800080u)) & 0x80008000u;
+}
+
+// What tiles of a segment some row does not see whole: keys below `from` or from `to` on are in them.
+struct PromptEdge {
+    int from, to;
+    __device__ __forceinline__ bool masks(int key0) const { return key0 < from || key0 + kPromptKeys > to; }
+};
+
+// A row's share of a segment: keys lo .. hi of the key tiles t0 .. t1, those of them that `edge` cuts.
+struct PromptShare {
+    PromptEdge edge;
+    int64_t token0;
+    int kv_head, t0, t1, lo, hi;
+};
+// Adds the row's values that are infinite or NaN to channels c .. end of its output, or of its part, whose channel x is at
+// part[x / 4 * kPromptRows * 4 + x % 4].  Rare, hence out of line and after the rest has been written.
+template <typename T>
+__device__ __noinline__ void add_lost(const PromptParams& p, const PromptShare& s, T* out, float* part, int c, int end) {
+    for (; c < end; ++c) {
+        float sum = 0.f;
+        for (int t = s.t0; t < s.t1; ++t) {
+            const int key0 = t * kPromptKeys;
+            if (!s.edge.masks(key0)) continue;
+            for (int j = max(s.lo, key0); j < min(s.hi, key0 + kPromptKeys); ++j) {
+                const float v = (float)*((const T*)p.a.v + (s.token0 + j) * p.a.v_token_stride + s.kv_head * p.a.v_head_stride + c);
+                if (!(fabsf(v) < INFINITY)) sum += v;
+            }
+        }
+        if (sum == 0.f) continue;
+        if (out != nullptr) out[c] = (T)((float)out[c] + sum);
+        else part[c / 4 * kPromptRows * 4 + c % 4] += sum;
+    }
+}
+
+template <typename T, int D, int TILES>
+__global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+    using Sh = WholeShape<T, D, TILES>;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 4 * Sh::kStages + 1];
+    __shared__ int64_t part[Sh::kWarps];
+    __shared__ uint32_t tmem_base;
+    __shared__ float tops[TILES][2][kPromptRows];      // maxima of the halves of rows, NaN: a wait ran out
+    __shared__ float sums[2][TILES][2][kPromptRows];   // their sums, of every other segment
+    __shared__ volatile int32_t dirty[8];              // of every eighth segment: its number + 1 if values were taken out
+    __shared__ volatile uint32_t arrived[2][TILES];    // of the run's first and last segment
+    __shared__ volatile uint32_t added[2][TILES];      // whether this CTA has counted itself there
+    __shared__ PromptSegment start;
+    const rra_prompt_attention_args_t& a = p.a;
+    const int tid = (int)threadIdx.x, warp = tid >> 5;
+    const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    int32_t* const chunk_sums = (int32_t*)(raw_smem + (smem - smem_u32(raw_smem)) + Sh::kSums);
+    AttnWorkspace* const ws = (AttnWorkspace*)a.workspace;
+    float* const parts = (float*)(ws + 1);
+
+    const uint32_t bars = smem_u32(bar_mem);
+    // q_full[i], pv_full[i]: what the next products of tile i wait for, with their turn; s_full[i], o_full[i]: done
+    const uint32_t q_full = bars, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, pv_full = s_full + 8 * TILES,
+                   o_full = pv_full + 8 * TILES, joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 8 * Sh::kStages,
+                   v_full = k_empty + 8 * Sh::kStages, v_empty = v_full + 8 * Sh::kStages, drained = v_empty + 8 * Sh::kStages;
+    constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
+    pdl_release_early();
+    if (tid == 0) {
+        for (int i = 0; i < TILES; ++i) {
+            added[0][i] = added[1][i] = 0u;
+            mbar_init(q_full + 8 * i, 1 + kTurn);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(pv_full + 8 * i, 2 * kPromptRows + kTurn);
+            mbar_init(o_full + 8 * i, 1);
+            mbar_init(joined + 8 * i, 2 * kPromptRows);
+        }
+        for (int i = 0; i < Sh::kStages; ++i) {
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, TILES);
+            mbar_init(v_full + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, TILES);
+        }
+        for (int i = 0; i < 8; ++i) dirty[i] = 0;
+        mbar_init(drained, TILES);
+        if (kTurn) mbar_arrive(q_full);  // the first turn
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    pdl_wait();
+
+    const WholeWork<TILES> work{p};
+    int64_t r0, r1, run;
+    if (!prompt_run<Sh::kWarps>(work, chunk_sums, part, start, r0, r1, run)) return;
+    if (warp == Sh::kIssue) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_proxy_async_smem();  // the sums were where copies go next
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = tmem_base;
+    PromptSegment seg = start;
+    prompt_load(work, seg);
+    auto first_of = [&](const PromptSegment& s) {
+        const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - kPromptSegmentCost;
+        return (int)(from > 0 ? from : 0);
+    };
+    auto end_of = [&](const PromptSegment& s) {
+        const int64_t to = (s.end < r1 ? s.end : r1) - s.begin - kPromptSegmentCost;
+        return (int)(to > 0 ? to : 0);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, attn_try(bar, parity & 1u) || attn_wait_slow(bar, parity & 1u, ws));
+    };
+
+    uint32_t n = 0;   // key tiles of this run so far
+    uint32_t sn = 0;  // segments so far that had tiles
+    if (warp < Sh::kSoftmaxWarps) {
+        // =============================== softmax: a thread has half a row ====
+        set_registers<Sh::kSoftmaxRegs, Sh::kLaunchRegs>();
+        const int i = warp >> 3, half = warp >> 2 & 1, row = tid & 127;
+        const int id = 1 + 4 * i + (warp & 3);  // barrier of the two warps that have the same rows
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
+        const uint32_t s_at = lanes + 128 * i + 64 * half, p_at = lanes + 128 * i + 32 * half,
+                       o_at = lanes + 128 * (TILES + i) + D / 2 * half;
+        const int tok = p.by_group(row), head_in = row - tok * p.group;  // this row's token and head in the tile
+        const float factor = p.factor;
+        uint32_t joins = 0, count_of_segments = 0;
+        // A wait that runs out makes this warp fail; it leaves only where its partner does too, or either would wait for the
+        // other forever.
+        bool failed = false, over = false, joined_it = false;
+        while (true) {
+            const int t0 = first_of(seg), t1 = end_of(seg);
+            const int kv_head = p.by_parts(seg.h), head0 = (seg.h - kv_head * p.parts) * p.group;  // of the KV head's query heads
+            const int token = (seg.c * TILES + i) * p.span + tok, head = kv_head * p.heads_of_kv + head0 + head_in;
+            const bool live = tok < p.span && token < seg.n.qn && head0 + head_in < p.heads_of_kv;
+            // the keys that this row sees, and which of the segment's tiles some row does not see whole
+            const int lo = live && p.window > 0 ? max(0, token - p.window + 1) : 0;
+            const int hi = !live ? INT32_MAX : a.causal ? token + 1 : seg.n.qn;
+            PromptEdge edge;
+            {
+                const int first = seg.c * TILES * p.span, last = min(seg.n.qn, first + TILES * p.span) - 1;
+                edge.from = p.window > 0 ? max(0, last - p.window + 1) : 0;
+                edge.to = a.causal ? first + 1 : seg.n.qn;
+            }
+            float m = -FLT_MAX, limit = -FLT_MAX, l = 0.f;
+            const uint64_t factor2 = pair2(factor, factor), lift2 = pair2(Sh::kLift, Sh::kLift);
+#pragma unroll 1
+            for (int tl = t0; tl < t1; ++tl, ++n) {
+                failed = failed || !wait(s_full + 8 * i, n);
+                const int key0 = (seg.first_tile + tl) * kPromptKeys;
+                const bool masks = edge.masks(key0);
+                uint32_t v[64];
+                float top = -FLT_MAX;
+                if (!failed) {
+                    tc_after_sync();
+                    tc_ld32(s_at, v);
+                    tc_ld32(s_at + 32, v + 32);
+                    tc_wait_ld();
+                    if (p.flip != 1.f)
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
+                    if (masks) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int at = key0 + 64 * half + 32 * q;
+                            const int from = min(max(lo - at, 0), 32), to = min(max(hi - at, 0), 32);
+                            const uint32_t mask = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & (from == 32 ? 0u : 0xffffffffu << from);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[32 * q + k] = mask >> k & 1u ? v[32 * q + k] : 0xff800000u;
+                        }
+                    }
+                    float most[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll
+                    for (int k = 0; k < 64; k += 2)
+                        most[k >> 1 & 3] = fmaxf(most[k >> 1 & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                }
+                // The partner has read its scores here: weights go where the first half's were.
+                if (pair_any(id, failed || top > limit)) {  // a maximum moves: scale what was summed
+                    tops[i][half][row] = failed ? __int_as_float(0x7fffffff) : top;
+                    pair_any(id, false);
+                    const float other = tops[i][half ^ 1][row];
+                    over = __any_sync(0xffffffffu, failed || other != other);
+                    if (over) break;
+                    top = fmaxf(top, other);
+                    if (__any_sync(0xffffffffu, top > limit)) {
+                        const float now = top > limit ? top : m;
+                        const float by = exp2_fast((m - now) * factor);
+                        m = now;
+                        limit = now + __fdividef(kPromptSlack, factor);
+                        l *= by;
+                        if (tl > t0) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t o[16];
+                                tc_ld16(o_at + 16 * q, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                                tc_st16(o_at + 16 * q, o);
+                            }
+                        }
+                    }
+                }
+                // ---- weights, where the scores were ----
+                const uint64_t off = pair2(-m, -m);
+                uint64_t sum[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    float e0, e1;
+                    split2(fma2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), off), factor2, lift2), e0, e1);
+                    e0 = exp2_fast(e0);
+                    e1 = exp2_fast(e1);
+                    sum[k >> 1 & 1] = add2(sum[k >> 1 & 1], pair2(e0, e1));
+                    v[k / 2] = pack2<T>(e0, e1);
+                }
+                tc_st32(p_at, v);
+                float a0, a1;
+                split2(add2(sum[0], sum[1]), a0, a1);
+                l += a0 + a1;
+                if (masks) {  // values that a row does not see must be finite
+                    const uint32_t stage = n % Sh::kStages;
+                    failed = !wait(v_full + 8 * stage, n / Sh::kStages);
+                    if (!failed)
+#pragma unroll 1
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t at = smem + Sh::kV + stage * Sh::kTile + 16 * (256 * k + 128 * half + row);
+                            uint32_t w[4], bad = 0;
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) bad |= not_finite<Sh::kHalf>(w[e]);
+                            if (bad == 0u) continue;
+                            dirty[sn & 7] = (int32_t)sn + 1;
+                            __threadfence_block();  // whoever finds the 0 finds this
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] &= ~((not_finite<Sh::kHalf>(w[e]) >> 15) * 0xffffu);
+                            sts_v4(at, w[0], w[1], w[2], w[3]);
+                        }
+                    fence_proxy_async_smem();
+                }
+                tc_wait_st();
+                tc_before_sync();
+                if (!failed) mbar_arrive(pv_full + 8 * i);
+            }
+            // ---- the segment's end in this run ----
+            const bool starts = seg.begin >= r0, ends = seg.end <= r1;
+            bool lost = false;
+            if (!over) {
+                if (t0 < t1) {
+                    failed = failed || !wait(o_full + 8 * i, sn);
+                    tc_after_sync();
+                    lost = dirty[sn & 7] == (int32_t)sn + 1;
+                    ++sn;
+                }
+                float(&mine)[2][kPromptRows] = sums[count_of_segments++ & 1][i];
+                mine[half][row] = l;
+                over = pair_any(id, failed);
+                l += mine[half ^ 1][row];
+            }
+            if (over) break;
+            const float top = m * factor;
+            l *= Sh::kUnlift;  // O stays lifted until it is divided by its sum
+            // 32 of this thread's channels, from c on, times inv
+            T* const out = (T*)a.out + (int64_t)(seg.n.q0 + token) * a.out_token_stride + head * a.out_head_stride;
+            auto put = [&](float* o, int c, float inv) {
+                T* const to = out + c;
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    uint4 u;
+                    uint32_t* const w = (uint32_t*)&u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack2<T>(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
+                    if (c + k < a.head_dim) *(uint4*)(to + k) = u;
+                }
+            };
+            // what was taken out of the values comes back, into the output or a part
+            auto add = [&](float* part) {
+                if (!lost || !live) return;
+                const PromptShare share = {edge, seg.n.q0, kv_head, seg.first_tile + t0, seg.first_tile + t1, lo, hi};
+                add_lost<T>(p, share, part == nullptr ? out : nullptr, part, D / 2 * half, min(a.head_dim, D / 2 * (half + 1)));
+            };
+            auto get = [&](int q, float* o) {  // 32 columns of O from its `q`th on
+                tc_ld32(o_at + 32 * q, (uint32_t*)o);
+                tc_wait_ld();
+            };
+            auto statistics = [&](float best, float sum) {
+                if (live && half == 0 && a.lse != nullptr)
+                    a.lse[(int64_t)(seg.n.q0 + token) * a.q_heads + head] = (best + log2f(sum)) * 0.693147180559945309f;
+                return sum == 0.f ? 0.f : Sh::kUnlift / sum;
+            };
+            if (starts && ends) {
+                const float inv = statistics(top, l);
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    float o[32];
+                    get(q, o);
+                    if (live) put(o, D / 2 * half + 32 * q, inv);
+                }
+                add(nullptr);
+            } else {
+                // The last CTA to arrive adds the parts in order; its own, if it finds all others there, from where it is.
+                const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run), which = starts ? 1 : 0;
+                uint32_t* const count = &ws->arrived[i0 * TILES + i];
+                volatile uint32_t& others = arrived[which][i];
+                const bool counts = row == 0 && half == 0;
+                auto meet = [&]() {
+                    mbar_arrive(joined + 8 * i);
+                    return wait(joined + 8 * i, joins++);
+                };
+                auto join = [&]() {
+                    if (counts) others = ld_acquire_u32(count);
+                    if (!meet()) return false;
+                    int mine = (int)blockIdx.x;
+                    constexpr int kColumns4 = D / 4;  // of a part, four channels each
+                    if (others != (uint32_t)(i1 - i0)) {
+                        mine = -1;
+                        float4* const to = (float4*)(parts + (((int64_t)blockIdx.x * 2 + which) * TILES + i) * Sh::kPartFloats);
+                        if (t0 < t1) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 64; ++q) {
+                                float o[32];
+                                get(q, o);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    to[(D / 8 * half + 8 * q + k) * kPromptRows + row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            }
+                            add((float*)(to + row));
+                        }
+                        if (half == 0) ((float2*)(to + kColumns4 * kPromptRows))[row] = make_float2(top, l);
+                        __threadfence();
+                        if (!meet()) return false;
+                        if (counts) {
+                            others = atomicAdd(count, 1u);
+                            added[which][i] = 1u;
+                        }
+                        if (!meet()) return false;
+                    }
+                    if (others != (uint32_t)(i1 - i0)) return true;
+                    __threadfence();
+                    auto part_of = [&](int x) {
+                        return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPartFloats);
+                    };
+                    auto stats_of = [&](int x) {
+                        return x == mine ? make_float2(top, l) : __ldcg((const float2*)(part_of(x) + kColumns4 * kPromptRows) + row);
+                    };
+                    float best = -FLT_MAX, sum = 0.f;
+#pragma unroll 4
+                    for (int x = i0; x <= i1; ++x) best = fmaxf(best, stats_of(x).x);
+#pragma unroll 4
+                    for (int x = i0; x <= i1; ++x) {
+                        const float2 st = stats_of(x);
+                        sum += st.y * exp2_fast(st.x - best);
+                    }
+                    const float inv = statistics(best, sum);
+#pragma unroll 1
+                    for (int q = 0; q < D / 64; ++q) {
+                        float o[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+#pragma unroll 1
+                        for (int x = i0; x <= i1; ++x) {
+                            const float2 st = stats_of(x);
+                            float v[32];
+                            if (x == mine) {
+                                get(q, v);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    *(float4*)(v + 4 * k) = __ldcg(part_of(x) + (D / 8 * half + 8 * q + k) * kPromptRows + row);
+                            }
+                            if (st.y != 0.f) {  // else nothing was seen there, and its channels may not have been written
+                                const float by = exp2_fast(st.x - best);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = fmaf(v[k], by, o[k]);
+                            }
+                        }
+                        if (live) put(o, D / 2 * half + 32 * q, inv);
+                    }
+                    if (mine >= 0) add(nullptr);
+                    if (counts) *count = 0u;
+                    return true;
+                };
+                joined_it = join();
+                over = pair_any(id, !joined_it);
+                if (over) break;
+                joined_it = false;
+            }
+            if (seg.end >= r1) break;
+            tc_before_sync();
+            prompt_next(work, seg);
+        }
+        // A wait ran out: the results are lost, but the counters of the segments from here on have to be zero for the next
+        // call.  So this CTA still counts itself, and whoever is last there clears them.
+        if (over && row == 0 && half == 0)
+#pragma unroll 1
+            while (true) {
+                if (joined_it) {  // but for the one that this thread had already joined, when its partner's wait ran out
+                    joined_it = false;
+                    if (seg.end >= r1) break;
+                    prompt_next(work, seg);
+                }
+                const int which = seg.begin >= r0 ? 1 : 0;
+                if (which == 0 || seg.end > r1) {
+                    const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
+                    uint32_t* const count = &ws->arrived[i0 * TILES + i];
+                    const uint32_t before = added[which][i] != 0u ? arrived[which][i] : atomicAdd(count, 1u);
+                    if (before == (uint32_t)(i1 - i0)) *count = 0u;
+                }
+                if (seg.end >= r1) break;
+                prompt_next(work, seg);
+            }
+    } else if (warp == Sh::kCopy) {
+        // =============================== copies, ahead of the products by the stages ====
+        set_registers<Sh::kIssueRegs, Sh::kLaunchRegs>();
+        const uint32_t q_bytes = (uint32_t)(p.group * p.span) * 128u * (D / 64);
+        bool ok = true;
+        while (ok) {
+            const int t0 = first_of(seg), t1 = end_of(seg);
+            const int kv_head = p.by_parts(seg.h), head = kv_head * p.heads_of_kv + (seg.h - kv_head * p.parts) * p.group;
+            if (t0 < t1) {
+                for (int i = 0; i < TILES && ok; ++i) {
+                    ok = sn == 0 || wait(q_empty + 8 * i, sn - 1);
+                    if (ok && elected()) {
+                        mbar_expect_tx(q_full + 8 * i, q_bytes);
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load(smem + i * Sh::kTile + x * Sh::kPanel, &p.q, 64 * x, head, seg.n.q0 + (seg.c * TILES + i) * p.span, q_full + 8 * i);
+                    }
+                    __syncwarp();
+                }
+                ++sn;
+            }
+#pragma unroll 1
+            for (int tl = t0; tl < t1 && ok; ++tl, ++n) {
+                const uint32_t stage = n % Sh::kStages, turn = n / Sh::kStages;
+                const int token = seg.n.q0 + (seg.first_tile + tl) * kPromptKeys;
+                ok = turn == 0 || wait(k_empty + 8 * stage, turn - 1);
+                if (ok && elected()) {
+                    mbar_expect_tx(k_full + 8 * stage, Sh::kTile);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load(smem + Sh::kK + stage * Sh::kTile + x * Sh::kPanel, &p.k, 64 * x, kv_head, token, k_full + 8 * stage);
+                }
+                __syncwarp();
+                if (!ok) break;
+                ok = turn == 0 || wait(v_empty + 8 * stage, turn - 1);
+                if (ok && elected()) {
+                    mbar_expect_tx(v_full + 8 * stage, Sh::kTile);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load(smem + Sh::kV + stage * Sh::kTile + x * Sh::kPanel, &p.v, 64 * x, kv_head, token, v_full + 8 * stage);
+                }
+                __syncwarp();
+                if (!ok) {  // K of this tile is on its way
+                    attn_wait_quiet(k_full + 8 * stage, turn & 1u);
+                    break;
+                }
+            }
+            if (!ok || seg.end >= r1) break;
+            prompt_next(work, seg);
+        }
+        // No copy is in flight when the CTA ends, also where nobody waited for it.
+        for (int i = 0; i < TILES && sn > 0; ++i) attn_wait_quiet(q_full + 8 * i, (sn - 1) & 1u);
+        for (uint32_t x = n > Sh::kStages ? n - Sh::kStages : 0; x < n; ++x) {
+            attn_wait_quiet(k_full + 8 * (x % Sh::kStages), x / Sh::kStages & 1u);
+            attn_wait_quiet(v_full + 8 * (x % Sh::kStages), x / Sh::kStages & 1u);
+        }
+    } else {
+        // =============================== products of tile i: one thread issues ====
+        set_registers<Sh::kIssueRegs, Sh::kLaunchRegs>();
+        const int i = warp - Sh::kIssue;
+        bool ok = i < TILES;
+        constexpr uint32_t kQk = mma_desc(kPromptKeys, false, !Sh::kHalf), kPv = mma_desc(D, true, !Sh::kHalf);
+        const uint32_t q_desc = tile_desc(smem + i * Sh::kTile, 16), k_desc = tile_desc(smem + Sh::kK, 16),
+                       v_desc = tile_desc(smem + Sh::kV, Sh::kPanel);
+        constexpr uint32_t kStep = Sh::kTile >> 4;  // from one tile to the next, in a descriptor
+        const uint32_t s_at = tmem + 128 * i, o_at = tmem + 128 * (TILES + i);
+        // The tiles' warps take turns, as in serve_prefill.cu.
+        while (ok) {
+            const int t0 = first_of(seg), t1 = end_of(seg);
+            if (t0 < t1) {
+#pragma unroll 1
+                for (int tl = t0 - 1; tl < t1; ++tl) {  // products of tile tl, scores of the next
+                    const bool values = tl >= t0, next = tl + 1 < t1;
+                    const uint32_t then = n + (values ? 1 : 0);  // the tile whose scores come next
+                    // K and V are there long before: first their waits, so that nothing comes between the products
+                    ok = (!next || wait(k_full + 8 * (then % Sh::kStages), then / Sh::kStages)) &&
+                         (!values || wait(v_full + 8 * (n % Sh::kStages), n / Sh::kStages)) &&
+                         (values ? wait(pv_full + 8 * i, n) : wait(q_full + 8 * i, sn));
+                    if (!ok) break;
+                    tc_after_sync();
+                    const uint32_t k_at = k_desc + then % Sh::kStages * kStep, v_at = v_desc + n % Sh::kStages * kStep;
+                    if (elected()) {
+                        if (values) {  // O_i += P_i V
+#pragma unroll
+                            for (int k = 0; k < kPromptKeys / 16; ++k) tc_mma_ts(o_at, s_at + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
+                            tc_commit(v_empty + 8 * (n % Sh::kStages));
+                        }
+                        if (next) {  // S_i = Q_i K^T
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                constexpr auto at = [](int x) { return (uint32_t)((x >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
+                                tc_mma(s_at, q_desc + at(k), k_at + at(k), kQk, k > 0);
+                            }
+                            tc_commit(s_full + 8 * i);
+                            tc_commit(k_empty + 8 * (then % Sh::kStages));
+                            if (tl + 2 == t1) tc_commit(q_empty + 8 * i);
+                            if (kTurn) mbar_arrive(i == 1 ? pv_full : values ? pv_full + 8 : q_full + 8);
+                        } else {
+                            tc_commit(o_full + 8 * i);
+                            if (kTurn) mbar_arrive(i == 0 ? pv_full + 8 : q_full);
+                        }
+                    }
+                    __syncwarp();
+                    n = then;
+                }
+                ++sn;
+            }
+            if (!ok || seg.end >= r1) break;
+            prompt_next(work, seg);
+        }
+        // nothing is in flight when TMEM goes back
+        if (i < TILES) {
+            if (elected()) tc_commit(drained);
+            __syncwarp();
+            attn_wait_quiet(drained, 0);
+        }
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == Sh::kIssue)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" : : "r"(tmem), "r"(Sh::kColumns) : "memory");
+}
+
+// ------------------------------------------------------------------ host ----
+// The driver's function that describes a tensor to the copies; null where there is no driver.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess) cudaGetLastError();
+        return found == cudaDriverEntryPointSuccess ? (EncodeTiled)f : nullptr;
+    }();
+    return fn;
+}
+
+// [tokens][heads][head_dim] of 16-bit values, in boxes of `span` tokens, `group` heads and 64 channels; what lies outside reads as 0.
+static bool prompt_map(CUtensorMap* map, const void* at, bool half, int64_t tokens, int heads, int head_dim, int64_t token_stride,
+                       int64_t head_stride, int group, int span) {
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)span}, steps[3] = {1, 1, 1};
+    return encode(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)at, dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, int TILES>
+static rra_status_t whole_launch(const PromptParams& p, int ctas, rra_stream_t stream) {
+    using Sh = WholeShape<T, D, TILES>;
+    const void* k = (const void*)prompt_attention_kernel<T, D, TILES>;
+    static_assert(Sh::kSmem <= 227 * 1024 - 8192, "shared memory");
+    if (configure_cluster_kernel(k, Sh::kSmem) != cudaSuccess) {
+        cudaGetLastError();
+        return RRA_ERR_CUDA;
+    }
+    // The shares of the registers are of what the launch has: a build that launches with fewer would wait for them forever.
+    static const bool enough = [k] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, k) == cudaSuccess && f.numRegs == Sh::kLaunchRegs;
+    }();
+    if (!enough) return RRA_ERR_CUDA;
+    void* args[] = {(void*)&p};
+    return serve_launch(k, dim3((unsigned)ctas), Sh::kThreads, Sh::kSmem, 1, stream, args);
+}
+
+template <typename T>
+static rra_status_t whole_launch(const PromptParams& p, int tiles, int ctas, rra_stream_t stream) {
+    if (p.a.head_dim > 64) return tiles == 2 ? whole_launch<T, 128, 2>(p, ctas, stream) : whole_launch<T, 128, 1>(p, ctas, stream);
+    return tiles == 2 ? whole_launch<T, 64, 2>(p, ctas, stream) : whole_launch<T, 64, 1>(p, ctas, stream);
+}
+
+static bool prompt_args_ok(const rra_prompt_attention_args_t* a) {
+    if (a == nullptr || a->requests < 0 || a->requests > RRA_SERVE_MAX_REQUESTS || a->tokens < 0 || a->tokens > INT32_MAX / 2 ||
+        a->kv_heads < 1 || a->q_heads < 1 || a->q_heads % a->kv_heads != 0 || a->head_dim < 8 || a->head_dim > 128 || a->head_dim % 8 != 0 ||
+        (a->half != 0 && a->half != 1) || a->max_len < 0 || a->window < 0 || !(fabs(a->scale) * 1.4426950408889634 <= FLT_MAX))
+        return false;
+    if (a->tokens * a->q_heads > INT32_MAX / 2) return false;  // rows are counted in 32 bits
+    const int64_t far = (int64_t)1 << 39;  // the copies' strides are below 2^40 bytes
+    auto fine = [&](const void* at, int64_t token, int64_t head, int heads) {
+        return aligned16(at) && strides_ok(token, head, heads, a->head_dim, 2) && token < far && head < far;
+    };
+    if (!fine(a->q, a->q_token_stride, a->q_head_stride, a->q_heads) || !fine(a->k, a->k_token_stride, a->k_head_stride, a->kv_heads) ||
+        !fine(a->v, a->v_token_stride, a->v_head_stride, a->kv_heads) || !fine(a->out, a->out_token_stride, a->out_head_stride, a->q_heads) ||
+        ((uintptr_t)a->workspace & 255) != 0)
+        return false;
+    if (a->requests == 0 || a->tokens == 0) return true;
+    return a->q != nullptr && a->k != nullptr && a->v != nullptr && a->out != nullptr && a->cu != nullptr && a->workspace != nullptr;
+}
+
+// Tiles of a CTA: two, if the longest prompt fills more than one.
+static int prompt_tiles(const rra_prompt_attention_args_t& a) {
+    const int64_t rows = (int64_t)std::max(a.max_len, 1) * (a.q_heads / a.kv_heads);
+    return rows > kPromptRows ? 2 : 1;
+}
+
+}  // namespace rra
+
+extern "C" {
+
+size_t rra_prompt_attention_workspace_bytes(void) { return sizeof(rra::AttnWorkspace) + rra::prefill_partial_bytes(128); }
+
+rra_status_t rra_prompt_attention_plan(const rra_prompt_attention_args_t* args, const char** name) {
+    if (name == nullptr || !rra::prompt_args_ok(args)) return RRA_ERR_INVALID_ARG;
+    *name = rra::prompt_tiles(*args) == 2 ? "prompt_attention_kernel<256 rows>" : "prompt_attention_kernel<128 rows>";
+    return RRA_OK;
+}
+
+rra_status_t rra_prompt_attention(const rra_prompt_attention_args_t* args, rra_stream_t stream) {
+    if (!rra::prompt_args_ok(args)) return RRA_ERR_INVALID_ARG;
+    const rra_prompt_attention_args_t& a = *args;
+    if (a.requests == 0 || a.tokens == 0) return RRA_OK;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return RRA_ERR_CUDA;
+    }
+    const int tiles = rra::prompt_tiles(a);
+    rra::PromptParams p;
+    p.a = a;
+    p.heads_of_kv = a.q_heads / a.kv_heads;
+    p.parts = (p.heads_of_kv + rra::kPromptRows - 1) / rra::kPromptRows;
+    p.group = (p.heads_of_kv + p.parts - 1) / p.parts;
+    p.span = rra::kPromptRows / p.group;
+    p.window = std::min(a.window, 1 << 30);
+    p.by_group = rra::Divisor(p.group);
+    p.by_parts = rra::Divisor(p.parts);
+    p.by_chunk = rra::Divisor(tiles * p.span);
+    p.factor = (float)(fabs(a.scale) * 1.4426950408889634);
+    p.flip = a.scale > 0 ? 1.f : a.scale < 0 ? -1.f : 0.f;
+    if (p.factor == 0.f) p.factor = 1.f, p.flip = 0.f;  // every score is 0
+    if (!rra::prompt_map(&p.q, a.q, a.half != 0, a.tokens, a.q_heads, a.head_dim, a.q_token_stride, a.q_head_stride, p.group, p.span) ||
+        !rra::prompt_map(&p.k, a.k, a.half != 0, a.tokens, a.kv_heads, a.head_dim, a.k_token_stride, a.k_head_stride, 1, rra::kPromptKeys) ||
+        !rra::prompt_map(&p.v, a.v, a.half != 0, a.tokens, a.kv_heads, a.head_dim, a.v_token_stride, a.v_head_stride, 1, rra::kPromptKeys))
+        return RRA_ERR_CUDA;
+    const int ctas = std::min(sms, rra::kPromptMaxCtas);
+    return a.half != 0 ? rra::whole_launch<__half>(p, tiles, ctas, stream) : rra::whole_launch<__nv_bfloat16>(p, tiles, ctas, stream);
+}
+
+}  // extern "C"

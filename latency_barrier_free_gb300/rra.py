@@ -50,6 +50,7 @@ SYMBOLS = [
     "rra_slot_map", "rra_qk_norm_rope", "rra_kv_page_bytes", "rra_kv_append", "rra_kv_read", "rra_kv_attention",
     "rra_kv_attention_workspace_bytes", "rra_kv_attention_plan",
     "rra_kv8_page_bytes", "rra_kv8_append", "rra_kv8_read", "rra_kv8_attention", "rra_kv8_attention_plan",
+    "rra_prompt_attention", "rra_prompt_attention_workspace_bytes", "rra_prompt_attention_plan",
     "rra_pages_fork", "rra_pages_release", "rra_pages_compact", "rra_pages_copy",
 ]
 

@@ -2,8 +2,9 @@
 
 Page bookkeeping, head norms with position rotation, a key/value cache held in
 4 or 8 bits, and the attention over it: what a tensor-parallel rank runs around its
-AllReduces; and pages that several requests share.  As in rra.py this is argument checking and marshalling only (in
-_serve.so, csrc/serve_bind.cpp); every call enqueues one kernel of librra.so on the
+AllReduces; attention of whole prompts, and pages that several requests share.  As
+in rra.py this is argument checking and marshalling only (in _serve.so,
+csrc/serve_bind.cpp); every call enqueues one kernel of librra.so on the
 current stream (or `stream`), and there is no fallback.  Tensors are on the current
 GPU; those of another one are refused.
 """
@@ -27,6 +28,7 @@ _ROPE = struct.Struct("9P10qd6i")
 _TOKENS = struct.Struct("Pq4i3P5q2i")
 _ATTN = struct.Struct("Pq4i7P6qd8i")
 _CACHE = struct.Struct("Pq4i")
+_PROMPT = struct.Struct("7P9qd8i")
 _FORK = struct.Struct("13Pq6i")
 _RELEASE = struct.Struct("9Pq4i")
 _COMPACT = struct.Struct("13P2q6i")
@@ -47,7 +49,8 @@ def _lib():
                "rra_kv_read": [vp, vp], "rra_kv_attention": [vp, vp],
                "rra_kv_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)],
                "rra_kv8_append": [vp, vp], "rra_kv8_read": [vp, vp], "rra_kv8_attention": [vp, vp],
-               "rra_kv8_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)], "rra_pages_fork": [vp, vp],
+               "rra_kv8_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)], "rra_prompt_attention": [vp, vp],
+               "rra_prompt_attention_plan": [vp, ctypes.POINTER(ctypes.c_char_p)], "rra_pages_fork": [vp, vp],
                "rra_pages_release": [vp, vp], "rra_pages_compact": [vp, vp], "rra_pages_copy": [vp, vp]}
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -56,6 +59,8 @@ def _lib():
             fn.argtypes, fn.restype = [ctypes.c_int] * 3, ctypes.c_size_t
         lib.rra_kv_attention_workspace_bytes.argtypes = [ctypes.c_int]
         lib.rra_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+        lib.rra_prompt_attention_workspace_bytes.argtypes = []
+        lib.rra_prompt_attention_workspace_bytes.restype = ctypes.c_size_t
         _fns = lib
     return _fns
 
@@ -167,7 +172,68 @@ def pages_compact(seq_len, block_table, free_pages, free_count, shared, page_tok
         raise rra.RraError(st, "rra_pages_compact")
 
 
-class KvCache:
+class _Workspace:
+    """What an attention's calls need besides their tensors: memory, with a status word in front."""
+
+    def _allocate(self, size: int, dev: int):
+        self._dev = dev
+        self._workspace = torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", dev))
+        self._workspace[:_WORKSPACE_HEAD].zero_()
+        own = torch.cuda.current_stream(dev)
+        if not torch.cuda.is_current_stream_capturing():
+            own.synchronize()  # calls on other streams find the zeros
+        self._home = own.cuda_stream
+
+    def status(self) -> int:
+        """Status word of the attention calls so far (0 is fine), whatever their
+        stream; synchronises with the GPU."""
+        torch.cuda.synchronize(self._dev)
+        return int(self._workspace[:4].cpu().view(torch.int32).item())
+
+    def reset(self) -> None:
+        """Sets the status back to 0, in the order of the current stream: after a
+        status that is not, attention() gives valid results from here on."""
+        self._workspace[:_WORKSPACE_HEAD].zero_()
+
+
+class PromptAttention(_Workspace):
+    """Attention of whole prompts over their own keys and values.
+
+    The object holds the attention's workspace, on the current GPU: its calls are
+    ordered on one stream, any one.  It may go once they are enqueued, but for calls
+    whose stream was given as a number, which it has to outlive, and for graphs that
+    hold calls."""
+
+    def __init__(self):
+        self._allocate(_lib().rra_prompt_attention_workspace_bytes(), torch.cuda.current_device())
+
+    def attention(self, q, k, v, out, cu, *, max_len: int, scale=None, causal: bool = True, window: int = 0, lse=None,
+                  stream=None) -> None:
+        """out = attention of q [tokens, q_heads, head_dim] over k and v [tokens,
+        kv_heads, head_dim], all bfloat16 or all float16 (rra_prompt_attention): prompt
+        b has the tokens cu[b]..cu[b+1] (int32) of all of them, each of which sees the
+        prompt's tokens up to itself (all of them, unless `causal`), the last `window`
+        of them if that is not 0.  max_len is what to plan for; scale defaults to
+        1/sqrt(head_dim).  lse: float32 [tokens, q_heads], optional.  Rows of out and lse
+        after cu[-1], a step's padding, stay as they are."""
+        st = _native.prompt_attention(self._dev, self._workspace, q, k, v, out, cu, max_len, scale, causal, window, lse, stream,
+                                      self._home)
+        if st:
+            raise rra.RraError(st, "rra_prompt_attention")
+
+    def plan_kernel(self, q_heads: int, kv_heads: int, *, max_len: int) -> str:
+        """Name of the kernel that attention() launches for so many heads, planned for max_len."""
+        some = self._workspace.data_ptr()  # planning reads no memory
+        args = _PROMPT.pack(some, some, some, some, 0, some, some, q_heads * 128, 128, kv_heads * 128, 128, kv_heads * 128, 128,
+                            q_heads * 128, 128, 1, 1.0, 1, q_heads, kv_heads, 128, 0, max_len, 1, 0)
+        name = ctypes.c_char_p()
+        st = _lib().rra_prompt_attention_plan(args, ctypes.byref(name))
+        if st:
+            raise rra.RraError(st, "rra_prompt_attention_plan")
+        return name.value.decode()
+
+
+class KvCache(_Workspace):
     """A paged key/value cache held in 4 bits, in memory of the caller.
 
     `pages` is a contiguous uint8 CUDA tensor of whole pages (kv_page_bytes()
@@ -182,19 +248,13 @@ class KvCache:
     def __init__(self, pages, page_tokens: int, kv_heads: int, head_dim: int):
         lib = _lib()
         size = self._size(page_tokens, kv_heads, head_dim)
-        self._dev = _device(pages)
+        dev = _device(pages)
         if pages.dtype is not torch.uint8 or not pages.is_contiguous() or pages.numel() % size:
             raise ValueError("pages must be a contiguous uint8 tensor of whole pages (%d bytes each)" % size)
         self.pages, self.page_bytes = pages, size
         self.page_tokens, self.kv_heads, self.head_dim = int(page_tokens), int(kv_heads), int(head_dim)
         self.num_pages = pages.numel() // size
-        self._workspace = torch.empty(lib.rra_kv_attention_workspace_bytes(head_dim), dtype=torch.uint8,
-                                      device=pages.device)
-        self._workspace[:_WORKSPACE_HEAD].zero_()
-        own = torch.cuda.current_stream(self._dev)
-        if not torch.cuda.is_current_stream_capturing():
-            own.synchronize()  # calls on other streams find the zeros
-        self._home = own.cuda_stream
+        self._allocate(lib.rra_kv_attention_workspace_bytes(head_dim), dev)
         self._cache = _CACHE.pack(pages.data_ptr(), self.num_pages, self.page_tokens, self.kv_heads, self.head_dim, 0)
         self._scale = 1.0 / math.sqrt(head_dim)
 
@@ -247,17 +307,6 @@ class KvCache:
         st = _native.pages_copy(self.pages, to.pages, self.page_bytes, source, target, stream)
         if st:
             raise rra.RraError(st, "rra_pages_copy")
-
-    def status(self) -> int:
-        """Status word of the attention calls so far (0 is fine), whatever their
-        stream; synchronises with the GPU."""
-        torch.cuda.synchronize(self._dev)
-        return int(self._workspace[:4].cpu().view(torch.int32).item())
-
-    def reset(self) -> None:
-        """Sets the status back to 0, in the order of the current stream: after a
-        status that is not, attention() gives valid results from here on."""
-        self._workspace[:_WORKSPACE_HEAD].zero_()
 
 
 class KvCache8(KvCache):
