@@ -7,14 +7,14 @@
 // keys that any of their rows sees, 128 at a time: queries, keys and values come
 // by TMA, one thread for each tile issues
 //     S_i = Q_i K^T,   O_i += P_i V        (tcgen05.mma, sums in TMEM)
-// and two warpgroups for each tile turn S_i into weights P_i, in place.  Two threads
-// have a row, each half of its columns: alone, a thread would take twice as long
-// from scores to weights, and the tensor cores have nothing but the other tile's
-// products to do meanwhile (TMEM: 128 columns of S and D of O a tile, twice).
+// and two warpgroups for each tile turn S_i into weights P_i, in place.  A warp has
+// 16 rows, four threads a row (the layout of an accumulator of mma): one thread a row
+// would take twice as long from scores to weights, and the tensor cores have nothing
+// but the other tile's products to do meanwhile (TMEM: 128 columns of S and D of O a
+// tile, twice).
 //
 // The maximum that weights are taken against moves only when a score passes it by
-// more than kPromptSlack (in units of log2): one vote of a row's two warps a tile,
-// and only then they exchange maxima and scale O, in TMEM.
+// more than kPromptSlack (in units of log2); only then O is scaled, in TMEM.
 //
 // A value that is infinite or NaN would spoil rows that do not see it: 0 times it
 // is NaN.  So in tiles that some row does not see whole, values are looked over in
@@ -57,8 +57,8 @@ struct WholeShape {
     static constexpr int kK = TILES * kTile, kV = kK + kStages * kTile, kEnd = kV + kStages * kTile;
     static constexpr int kSums = kK;               // before any tile: running sums of the requests' chunks
     static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
-    // Warps: eight of softmax for each tile (a warp reaches the TMEM lanes of its number modulo 4; the second four have the
-    // second halves of the rows), then one for each tile that issues its products, and one for the copies.
+    // Warps: eight of softmax for each tile (a warp reaches the 32 TMEM lanes of its number modulo 4; the first four have the
+    // first 16 of them), then one for each tile that issues its products, and one for the copies.
     static constexpr int kSoftmaxWarps = 8 * TILES, kIssue = kSoftmaxWarps, kCopy = kIssue + 2, kWarps = kIssue + 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
@@ -97,12 +97,60 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "r"(dst), "l"(map), "r"(channel), "r"(head), "r"(token), "r"(bar)
         : "memory");
 }
-// Two warps meet at barrier `id`; whether any of their threads says so.
-__device__ __forceinline__ bool pair_any(int id, bool x) {
-    uint32_t any;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any) : "r"(x ? 1u : 0u), "r"(id) : "memory");
-    return any != 0u;
+// 16 lanes' rows: of 8 (x8: 64) columns a thread has columns 2 t, 2 t + 1 of row g, then of row g + 8 (t = lane % 4, g = lane / 4).
+__device__ __forceinline__ void tc_ld_rows64(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tc_ld_rows32(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tc_st_rows32(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+        :
+        : "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
+        : "memory");
+}
+// 32 columns, of each 4 a thread has column t of row g, then of row g + 8.
+__device__ __forceinline__ void tc_st_weights(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+        :
+        : "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Word j of the four threads of a row goes to thread j: x[i] becomes thread i's word t.
+__device__ __forceinline__ void quad_transpose(uint32_t* x) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+        const bool up = t & o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & o) continue;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + o], o);
+            if (up) x[i] = got;
+            else x[i + o] = got;
+        }
+    }
 }
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -131,11 +179,11 @@ struct PromptShare {
     int64_t token0;
     int kv_head, t0, t1, lo, hi;
 };
-// Adds the row's values that are infinite or NaN to channels c .. end of its output, or of its part, whose channel x is at
-// part[x / 4 * kPromptRows * 4 + x % 4].  Rare, hence out of line and after the rest has been written.
+// Adds the row's values that are infinite or NaN to every fourth channel of its output, or of its part (the row's first
+// thread's first word of it), from c on.  Rare, hence out of line and after the rest has been written.
 template <typename T>
 __device__ __noinline__ void add_lost(const PromptParams& p, const PromptShare& s, T* out, float* part, int c, int end) {
-    for (; c < end; ++c) {
+    for (; c < end; c += 4) {
         float sum = 0.f;
         for (int t = s.t0; t < s.t1; ++t) {
             const int key0 = t * kPromptKeys;
@@ -147,7 +195,7 @@ __device__ __noinline__ void add_lost(const PromptParams& p, const PromptShare& 
         }
         if (sum == 0.f) continue;
         if (out != nullptr) out[c] = (T)((float)out[c] + sum);
-        else part[c / 4 * kPromptRows * 4 + c % 4] += sum;
+        else part[c / 8 * 128 + c % 8 / 2 * 4 + c % 2] += sum;
     }
 }
 
@@ -158,8 +206,6 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 4 * Sh::kStages + 1];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ uint32_t tmem_base;
-    __shared__ float tops[TILES][2][kPromptRows];      // maxima of the halves of rows, NaN: a wait ran out
-    __shared__ float sums[2][TILES][2][kPromptRows];   // their sums, of every other segment
     __shared__ volatile int32_t dirty[8];              // of every eighth segment: its number + 1 if values were taken out
     __shared__ volatile uint32_t arrived[2][TILES];    // of the run's first and last segment
     __shared__ volatile uint32_t added[2][TILES];      // whether this CTA has counted itself there
@@ -231,186 +277,206 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     uint32_t n = 0;   // key tiles of this run so far
     uint32_t sn = 0;  // segments so far that had tiles
     if (warp < Sh::kSoftmaxWarps) {
-        // =============================== softmax: a thread has half a row ====
+        // =============================== softmax: a thread has a quarter of two rows ====
         set_registers<Sh::kSoftmaxRegs, Sh::kLaunchRegs>();
-        const int i = warp >> 3, half = warp >> 2 & 1, row = tid & 127;
-        const int id = 1 + 4 * i + (warp & 3);  // barrier of the two warps that have the same rows
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the TMEM lanes
-        const uint32_t s_at = lanes + 128 * i + 64 * half, p_at = lanes + 128 * i + 32 * half,
-                       o_at = lanes + 128 * (TILES + i) + D / 2 * half;
-        const int tok = p.by_group(row), head_in = row - tok * p.group;  // this row's token and head in the tile
+        const int i = warp >> 3, lane = tid & 31, t = lane & 3, row0 = 32 * (warp & 3) + 16 * (warp >> 2 & 1) + (lane >> 2);
+        const uint32_t lanes = tmem + ((uint32_t)(row0 & ~15) << 16);  // this warp's TMEM lanes
+        const uint32_t s_at = lanes + 128 * i, o_at = lanes + 128 * (TILES + i);
+        int tok[2], head_in[2];  // the rows' token and head in the tile
+#pragma unroll
+        for (int r = 0; r < 2; ++r) tok[r] = p.by_group(row0 + 8 * r), head_in[r] = row0 + 8 * r - tok[r] * p.group;
         const float factor = p.factor;
-        uint32_t joins = 0, count_of_segments = 0;
-        // A wait that runs out makes this warp fail; it leaves only where its partner does too, or either would wait for the
-        // other forever.
-        bool failed = false, over = false, joined_it = false;
-        while (true) {
+        uint32_t joins = 0;
+        bool ok = true;
+        while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);
             const int kv_head = p.by_parts(seg.h), head0 = (seg.h - kv_head * p.parts) * p.group;  // of the KV head's query heads
-            const int token = (seg.c * TILES + i) * p.span + tok, head = kv_head * p.heads_of_kv + head0 + head_in;
-            const bool live = tok < p.span && token < seg.n.qn && head0 + head_in < p.heads_of_kv;
-            // the keys that this row sees, and which of the segment's tiles some row does not see whole
-            const int lo = live && p.window > 0 ? max(0, token - p.window + 1) : 0;
-            const int hi = !live ? INT32_MAX : a.causal ? token + 1 : seg.n.qn;
+            // the keys that the rows see, and which of the segment's tiles some row does not see whole
+            int token[2], lo[2], hi[2];
+            bool live[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                token[r] = (seg.c * TILES + i) * p.span + tok[r];
+                live[r] = tok[r] < p.span && token[r] < seg.n.qn && head0 + head_in[r] < p.heads_of_kv;
+                lo[r] = live[r] && p.window > 0 ? max(0, token[r] - p.window + 1) : 0;
+                hi[r] = !live[r] ? INT32_MAX : a.causal ? token[r] + 1 : seg.n.qn;
+            }
             PromptEdge edge;
             {
                 const int first = seg.c * TILES * p.span, last = min(seg.n.qn, first + TILES * p.span) - 1;
                 edge.from = p.window > 0 ? max(0, last - p.window + 1) : 0;
                 edge.to = a.causal ? first + 1 : seg.n.qn;
             }
-            float m = -FLT_MAX, limit = -FLT_MAX, l = 0.f;
+            float m[2] = {-FLT_MAX, -FLT_MAX}, limit[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
             const uint64_t factor2 = pair2(factor, factor), lift2 = pair2(Sh::kLift, Sh::kLift);
 #pragma unroll 1
             for (int tl = t0; tl < t1; ++tl, ++n) {
-                failed = failed || !wait(s_full + 8 * i, n);
+                ok = wait(s_full + 8 * i, n);
+                if (!ok) break;
+                tc_after_sync();
                 const int key0 = (seg.first_tile + tl) * kPromptKeys;
                 const bool masks = edge.masks(key0);
-                uint32_t v[64];
-                float top = -FLT_MAX;
-                if (!failed) {
-                    tc_after_sync();
-                    tc_ld32(s_at, v);
-                    tc_ld32(s_at + 32, v + 32);
-                    tc_wait_ld();
-                    if (p.flip != 1.f)
+                uint32_t v[64];  // v[4 j + 2 r + e]: row r, key 8 j + 2 t + e
+                tc_ld_rows64(s_at, v);
+                tc_ld_rows64(s_at + 64, v + 32);
+                tc_wait_ld();
+                if (p.flip != 1.f)
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
-                    if (masks) {
+                    for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
+                if (masks) {
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int at = key0 + 64 * half + 32 * q;
-                            const int from = min(max(lo - at, 0), 32), to = min(max(hi - at, 0), 32);
-                            const uint32_t mask = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & (from == 32 ? 0u : 0xffffffffu << from);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[32 * q + k] = mask >> k & 1u ? v[32 * q + k] : 0xff800000u;
-                        }
+                    for (int k = 0; k < 64; ++k) {
+                        const int key = key0 + 8 * (k >> 2) + 2 * t + (k & 1), r = k >> 1 & 1;
+                        if (key < lo[r] || key >= hi[r]) v[k] = 0xff800000u;
                     }
-                    float most[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
-#pragma unroll
-                    for (int k = 0; k < 64; k += 2)
-                        most[k >> 1 & 3] = fmaxf(most[k >> 1 & 3], fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
-                    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
                 }
-                // The partner has read its scores here: weights go where the first half's were.
-                if (pair_any(id, failed || top > limit)) {  // a maximum moves: scale what was summed
-                    tops[i][half][row] = failed ? __int_as_float(0x7fffffff) : top;
-                    pair_any(id, false);
-                    const float other = tops[i][half ^ 1][row];
-                    over = __any_sync(0xffffffffu, failed || other != other);
-                    if (over) break;
-                    top = fmaxf(top, other);
-                    if (__any_sync(0xffffffffu, top > limit)) {
-                        const float now = top > limit ? top : m;
-                        const float by = exp2_fast((m - now) * factor);
-                        m = now;
-                        limit = now + __fdividef(kPromptSlack, factor);
-                        l *= by;
-                        if (tl > t0) {
-#pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t o[16];
-                                tc_ld16(o_at + 16 * q, o);
-                                tc_wait_ld();
+                float top[2] = {-FLT_MAX, -FLT_MAX};
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
-                                tc_st16(o_at + 16 * q, o);
-                            }
+                for (int r = 0; r < 2; ++r) {
+                    float most[2] = {-FLT_MAX, -FLT_MAX};
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        most[j & 1] = max3(most[j & 1], __uint_as_float(v[4 * j + 2 * r]), __uint_as_float(v[4 * j + 2 * r + 1]));
+                    top[r] = fmaxf(most[0], most[1]);
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                }
+                if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {  // a maximum moves: scale what was summed
+                    float by[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float now = top[r] > limit[r] ? top[r] : m[r];
+                        by[r] = exp2_fast((m[r] - now) * factor);
+                        m[r] = now;
+                        limit[r] = now + __fdividef(kPromptSlack, factor);
+                        l[r] *= by[r];
+                    }
+                    if (tl > t0) {
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t o[16];
+                            tc_ld_rows32(o_at + 32 * q, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by[k >> 1 & 1]);
+                            tc_st_rows32(o_at + 32 * q, o);
                         }
                     }
                 }
                 // ---- weights, where the scores were ----
-                const uint64_t off = pair2(-m, -m);
-                uint64_t sum[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
 #pragma unroll
-                for (int k = 0; k < 64; k += 2) {
-                    float e0, e1;
-                    split2(fma2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), off), factor2, lift2), e0, e1);
-                    e0 = exp2_fast(e0);
-                    e1 = exp2_fast(e1);
-                    sum[k >> 1 & 1] = add2(sum[k >> 1 & 1], pair2(e0, e1));
-                    v[k / 2] = pack2<T>(e0, e1);
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[16];
+                    uint64_t sum[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int r = k & 1, at = 32 * q + 2 * k;
+                        float e0, e1;
+                        split2(fma2(add2(pair2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), pair2(-m[r], -m[r])), factor2, lift2), e0, e1);
+                        e0 = exp2_fast(e0);
+                        e1 = exp2_fast(e1);
+                        sum[r] = add2(sum[r], pair2(e0, e1));
+                        w[k] = pack2<T>(e0, e1);
+                    }
+                    tc_st_weights(s_at + 32 * q, w);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float a0, a1;
+                        split2(sum[r], a0, a1);
+                        l[r] += a0 + a1;
+                    }
                 }
-                tc_st32(p_at, v);
-                float a0, a1;
-                split2(add2(sum[0], sum[1]), a0, a1);
-                l += a0 + a1;
                 if (masks) {  // values that a row does not see must be finite
                     const uint32_t stage = n % Sh::kStages;
-                    failed = !wait(v_full + 8 * stage, n / Sh::kStages);
-                    if (!failed)
+                    ok = wait(v_full + 8 * stage, n / Sh::kStages);
+                    if (!ok) break;
 #pragma unroll 1
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t at = smem + Sh::kV + stage * Sh::kTile + 16 * (256 * k + 128 * half + row);
-                            uint32_t w[4], bad = 0;
-                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = smem + Sh::kV + stage * Sh::kTile + 16 * (256 * k + (tid & 255));
+                        uint32_t w[4], bad = 0;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) bad |= not_finite<Sh::kHalf>(w[e]);
-                            if (bad == 0u) continue;
-                            dirty[sn & 7] = (int32_t)sn + 1;
-                            __threadfence_block();  // whoever finds the 0 finds this
+                        for (int e = 0; e < 4; ++e) bad |= not_finite<Sh::kHalf>(w[e]);
+                        if (bad == 0u) continue;
+                        dirty[sn & 7] = (int32_t)sn + 1;
+                        __threadfence_block();  // whoever finds the 0 finds this
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] &= ~((not_finite<Sh::kHalf>(w[e]) >> 15) * 0xffffu);
-                            sts_v4(at, w[0], w[1], w[2], w[3]);
-                        }
+                        for (int e = 0; e < 4; ++e) w[e] &= ~((not_finite<Sh::kHalf>(w[e]) >> 15) * 0xffffu);
+                        sts_v4(at, w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
                     fence_proxy_async_smem();
                 }
                 tc_wait_st();
                 tc_before_sync();
-                if (!failed) mbar_arrive(pv_full + 8 * i);
+                mbar_arrive(pv_full + 8 * i);
             }
+            bool lost = false;
+            if (ok && t0 < t1) {
+                ok = wait(o_full + 8 * i, sn);
+                tc_after_sync();
+                lost = dirty[sn & 7] == (int32_t)sn + 1;
+                ++sn;
+            }
+            if (!ok) break;
             // ---- the segment's end in this run ----
             const bool starts = seg.begin >= r0, ends = seg.end <= r1;
-            bool lost = false;
-            if (!over) {
-                if (t0 < t1) {
-                    failed = failed || !wait(o_full + 8 * i, sn);
-                    tc_after_sync();
-                    lost = dirty[sn & 7] == (int32_t)sn + 1;
-                    ++sn;
-                }
-                float(&mine)[2][kPromptRows] = sums[count_of_segments++ & 1][i];
-                mine[half][row] = l;
-                over = pair_any(id, failed);
-                l += mine[half ^ 1][row];
+            float top[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                top[r] = m[r] * factor;
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                l[r] *= Sh::kUnlift;  // O stays lifted until it is divided by its sum
             }
-            if (over) break;
-            const float top = m * factor;
-            l *= Sh::kUnlift;  // O stays lifted until it is divided by its sum
-            // 32 of this thread's channels, from c on, times inv
-            T* const out = (T*)a.out + (int64_t)(seg.n.q0 + token) * a.out_token_stride + head * a.out_head_stride;
-            auto put = [&](float* o, int c, float inv) {
-                T* const to = out + c;
+            T* out[2];
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    uint4 u;
-                    uint32_t* const w = (uint32_t*)&u;
+            for (int r = 0; r < 2; ++r)
+                out[r] = (T*)a.out + (int64_t)(seg.n.q0 + token[r]) * a.out_token_stride + (kv_head * p.heads_of_kv + head0 + head_in[r]) * a.out_head_stride;
+            // 32 channels of both rows, from c on, times inv: each thread writes 8 of them
+            auto put = [&](const float* o, int c, const float* inv) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = pack2<T>(o[k + 2 * e] * inv, o[k + 2 * e + 1] * inv);
-                    if (c + k < a.head_dim) *(uint4*)(to + k) = u;
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = pack2<T>(o[4 * j + 2 * r] * inv[r], o[4 * j + 2 * r + 1] * inv[r]);
+                    quad_transpose(w);
+                    if (live[r] && c + 8 * t < a.head_dim) *(uint4*)(out[r] + c + 8 * t) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             };
             // what was taken out of the values comes back, into the output or a part
             auto add = [&](float* part) {
-                if (!lost || !live) return;
-                const PromptShare share = {edge, seg.n.q0, kv_head, seg.first_tile + t0, seg.first_tile + t1, lo, hi};
-                add_lost<T>(p, share, part == nullptr ? out : nullptr, part, D / 2 * half, min(a.head_dim, D / 2 * (half + 1)));
+                if (!lost) return;
+                __syncwarp();
+#pragma unroll 1
+                for (int r = 0; r < 2; ++r) {
+                    const PromptShare share = {edge, seg.n.q0, kv_head, seg.first_tile + t0, seg.first_tile + t1, r ? lo[1] : lo[0], r ? hi[1] : hi[0]};
+                    if (r ? live[1] : live[0])
+                        add_lost<T>(p, share, part == nullptr ? (r ? out[1] : out[0]) : nullptr, part == nullptr ? nullptr : part + 2 * r, t, a.head_dim);
+                }
+                __syncwarp();
             };
             auto get = [&](int q, float* o) {  // 32 columns of O from its `q`th on
-                tc_ld32(o_at + 32 * q, (uint32_t*)o);
+                tc_ld_rows32(o_at + 32 * q, (uint32_t*)o);
                 tc_wait_ld();
             };
-            auto statistics = [&](float best, float sum) {
-                if (live && half == 0 && a.lse != nullptr)
-                    a.lse[(int64_t)(seg.n.q0 + token) * a.q_heads + head] = (best + log2f(sum)) * 0.693147180559945309f;
-                return sum == 0.f ? 0.f : Sh::kUnlift / sum;
+            auto statistics = [&](const float* best, const float* sum, float* inv) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (live[r] && t == 0 && a.lse != nullptr)
+                        a.lse[(int64_t)(seg.n.q0 + token[r]) * a.q_heads + kv_head * p.heads_of_kv + head0 + head_in[r]] =
+                            (best[r] + log2f(sum[r])) * 0.693147180559945309f;
+                    inv[r] = sum[r] == 0.f ? 0.f : Sh::kUnlift / sum[r];
+                }
             };
             if (starts && ends) {
-                const float inv = statistics(top, l);
+                float inv[2];
+                statistics(top, l, inv);
 #pragma unroll
-                for (int q = 0; q < D / 64; ++q) {
-                    float o[32];
+                for (int q = 0; q < D / 32; ++q) {
+                    float o[16];
                     get(q, o);
-                    if (live) put(o, D / 2 * half + 32 * q, inv);
+                    put(o, 32 * q, inv);
                 }
                 add(nullptr);
             } else {
@@ -418,88 +484,94 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run), which = starts ? 1 : 0;
                 uint32_t* const count = &ws->arrived[i0 * TILES + i];
                 volatile uint32_t& others = arrived[which][i];
-                const bool counts = row == 0 && half == 0;
+                const bool counts = (tid & 255) == 0;
                 auto meet = [&]() {
                     mbar_arrive(joined + 8 * i);
                     return wait(joined + 8 * i, joins++);
                 };
-                auto join = [&]() {
-                    if (counts) others = ld_acquire_u32(count);
-                    if (!meet()) return false;
-                    int mine = (int)blockIdx.x;
-                    constexpr int kColumns4 = D / 4;  // of a part, four channels each
-                    if (others != (uint32_t)(i1 - i0)) {
-                        mine = -1;
-                        float4* const to = (float4*)(parts + (((int64_t)blockIdx.x * 2 + which) * TILES + i) * Sh::kPartFloats);
-                        if (t0 < t1) {
+                // A part: of each warp, of every 8 channels, four values of each lane; then the rows' statistics.
+                constexpr int kVectors = D / 4 * kPromptRows;
+                auto part_of = [&](int x) {
+                    return (float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPartFloats) + (warp & 7) * (D / 8) * 32 + lane;
+                };
+                auto stats_at = [&](int x, int r) {
+                    return (float2*)((float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPartFloats) + kVectors) + row0 + 8 * r;
+                };
+                if (counts) others = ld_acquire_u32(count);
+                ok = meet();
+                if (!ok) break;
+                int mine = (int)blockIdx.x;
+                if (others != (uint32_t)(i1 - i0)) {
+                    mine = -1;
+                    if (t0 < t1) {
+                        float4* const to = part_of((int)blockIdx.x);
 #pragma unroll 1
-                            for (int q = 0; q < D / 64; ++q) {
-                                float o[32];
-                                get(q, o);
+                        for (int q = 0; q < D / 32; ++q) {
+                            float o[16];
+                            get(q, o);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    to[(D / 8 * half + 8 * q + k) * kPromptRows + row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                            }
-                            add((float*)(to + row));
+                            for (int j = 0; j < 4; ++j) to[(4 * q + j) * 32] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                         }
-                        if (half == 0) ((float2*)(to + kColumns4 * kPromptRows))[row] = make_float2(top, l);
-                        __threadfence();
-                        if (!meet()) return false;
-                        if (counts) {
-                            others = atomicAdd(count, 1u);
-                            added[which][i] = 1u;
-                        }
-                        if (!meet()) return false;
+                        add((float*)(to - t));
                     }
-                    if (others != (uint32_t)(i1 - i0)) return true;
+                    if (t == 0)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) *stats_at((int)blockIdx.x, r) = make_float2(top[r], l[r]);
                     __threadfence();
-                    auto part_of = [&](int x) {
-                        return (const float4*)(parts + (((int64_t)x * 2 + (x == i0 ? 1 : 0)) * TILES + i) * Sh::kPartFloats);
-                    };
-                    auto stats_of = [&](int x) {
-                        return x == mine ? make_float2(top, l) : __ldcg((const float2*)(part_of(x) + kColumns4 * kPromptRows) + row);
-                    };
-                    float best = -FLT_MAX, sum = 0.f;
-#pragma unroll 4
-                    for (int x = i0; x <= i1; ++x) best = fmaxf(best, stats_of(x).x);
-#pragma unroll 4
-                    for (int x = i0; x <= i1; ++x) {
-                        const float2 st = stats_of(x);
-                        sum += st.y * exp2_fast(st.x - best);
+                    ok = meet();
+                    if (ok && counts) {
+                        others = atomicAdd(count, 1u);
+                        added[which][i] = 1u;
                     }
-                    const float inv = statistics(best, sum);
-#pragma unroll 1
-                    for (int q = 0; q < D / 64; ++q) {
-                        float o[32];
+                    ok = ok && meet();
+                    if (!ok) break;
+                }
+                if (others == (uint32_t)(i1 - i0)) {
+                    __threadfence();
+                    auto stats_of = [&](int x, int r) { return x == mine ? make_float2(top[r], l[r]) : __ldcg(stats_at(x, r)); };
+                    float best[2] = {-FLT_MAX, -FLT_MAX}, sum[2] = {0.f, 0.f}, inv[2];
+#pragma unroll 4
+                    for (int x = i0; x <= i1; ++x)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                        for (int r = 0; r < 2; ++r) best[r] = fmaxf(best[r], stats_of(x, r).x);
+#pragma unroll 4
+                    for (int x = i0; x <= i1; ++x)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float2 st = stats_of(x, r);
+                            sum[r] += st.y * exp2_fast(st.x - best[r]);
+                        }
+                    statistics(best, sum, inv);
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        float o[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = 0.f;
 #pragma unroll 1
                         for (int x = i0; x <= i1; ++x) {
-                            const float2 st = stats_of(x);
-                            float v[32];
+                            float v[16];
                             if (x == mine) {
                                 get(q, v);
                             } else {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    *(float4*)(v + 4 * k) = __ldcg(part_of(x) + (D / 8 * half + 8 * q + k) * kPromptRows + row);
+                                for (int j = 0; j < 4; ++j) *(float4*)(v + 4 * j) = __ldcg(part_of(x) + (4 * q + j) * 32);
                             }
-                            if (st.y != 0.f) {  // else nothing was seen there, and its channels may not have been written
-                                const float by = exp2_fast(st.x - best);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = fmaf(v[k], by, o[k]);
+                            for (int r = 0; r < 2; ++r) {
+                                const float2 st = stats_of(x, r);
+                                if (st.y == 0.f) continue;  // nothing was seen there, and its channels may not have been written
+                                const float by = exp2_fast(st.x - best[r]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) o[4 * j + 2 * r + e] = fmaf(v[4 * j + 2 * r + e], by, o[4 * j + 2 * r + e]);
                             }
                         }
-                        if (live) put(o, D / 2 * half + 32 * q, inv);
+                        put(o, 32 * q, inv);
                     }
                     if (mine >= 0) add(nullptr);
                     if (counts) *count = 0u;
-                    return true;
-                };
-                joined_it = join();
-                over = pair_any(id, !joined_it);
-                if (over) break;
-                joined_it = false;
+                }
             }
             if (seg.end >= r1) break;
             tc_before_sync();
@@ -507,14 +579,9 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
         }
         // A wait ran out: the results are lost, but the counters of the segments from here on have to be zero for the next
         // call.  So this CTA still counts itself, and whoever is last there clears them.
-        if (over && row == 0 && half == 0)
+        if (!ok && (tid & 255) == 0)
 #pragma unroll 1
             while (true) {
-                if (joined_it) {  // but for the one that this thread had already joined, when its partner's wait ran out
-                    joined_it = false;
-                    if (seg.end >= r1) break;
-                    prompt_next(work, seg);
-                }
                 const int which = seg.begin >= r0 ? 1 : 0;
                 if (which == 0 || seg.end > r1) {
                     const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
