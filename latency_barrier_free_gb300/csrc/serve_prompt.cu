@@ -17,13 +17,14 @@
 // more than kPromptSlack (in units of log2); only then O is scaled, in TMEM.
 //
 // A value that is infinite or NaN would spoil rows that do not see it: 0 times it
-// is NaN.  So in tiles that some row does not see whole, values are looked over in
-// shared memory; such elements become 0 there, and rows that see them get them at
-// their end.
+// is NaN.  So in tiles that some row does not see whole, a warp looks values over in
+// shared memory before products may read them; such elements become 0 there, and
+// rows that see them get them at their end.
 //
-// Work is cut into equal runs of key tiles, one per CTA (serve_tc.cuh); what a run
-// has of a segment it shares goes to the workspace, and the last CTA to arrive adds
-// the parts in order.
+// Segments are dealt out whole, the longest first, to and fro over the CTAs.  Where
+// that leaves CTAs idle (few long segments) they are cut into equal runs of key
+// tiles, one per CTA (serve_tc.cuh); what a run has of a segment it shares goes to
+// the workspace, and the last CTA to arrive adds the parts in order.
 #include <algorithm>
 #include <cmath>
 
@@ -34,6 +35,12 @@
 namespace rra {
 
 constexpr float kPromptSlack = 8.f;  // log2 of how far weights may pass 1 before the maximum moves
+
+constexpr int kDealRequests = 1024;  // up to so many requests, and chunks of the longest, segments are dealt out: their order
+constexpr int kDealChunks = 8192;    // is found in shared memory
+constexpr int kDealItems = 1024;     // segments of a CTA
+constexpr int kDealChecked = 16;     // with more, the CTAs' shares differ by little
+constexpr int kPromptJoinCost = 8;   // what joining the parts of a segment costs, in key tiles
 
 struct PromptParams {
     CUtensorMap q, k, v;  // [channels][heads][tokens]; boxes of 64 channels, q: group heads of `span` tokens, k, v: 128 tokens
@@ -58,8 +65,8 @@ struct WholeShape {
     static constexpr int kSums = kK;               // before any tile: running sums of the requests' chunks
     static_assert(4 * (RRA_SERVE_MAX_REQUESTS + 1) <= kEnd - kSums, "the sums fit");
     // Warps: eight of softmax for each tile (a warp reaches the 32 TMEM lanes of its number modulo 4; the first four have the
-    // first 16 of them), then one for each tile that issues its products, and one for the copies.
-    static constexpr int kSoftmaxWarps = 8 * TILES, kIssue = kSoftmaxWarps, kCopy = kIssue + 2, kWarps = kIssue + 4;
+    // first 16 of them), then one for each tile that issues its products, one for the copies, and one that looks values over.
+    static constexpr int kSoftmaxWarps = 8 * TILES, kIssue = kSoftmaxWarps, kCopy = kIssue + 2, kLook = kIssue + 3, kWarps = kIssue + 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static constexpr int kSoftmaxRegs = TILES == 2 ? 104 : 184;
@@ -68,6 +75,7 @@ struct WholeShape {
     static constexpr int kColumns = TILES == 2 ? 512 : 256;    // of TMEM: S of every tile, then O of every tile
     static constexpr int kPartFloats = kPromptRows * (D + 2);  // of a part: rows in columns of 4 channels, statistics
     static constexpr int kSmem = 1024 + kEnd;
+    static_assert(20 * kDealRequests + 4 * (kDealChunks + 1) <= kEnd - kSums, "and what dealing out needs");
 };
 
 // The work: chunks of TILES * span tokens of every request, for every head (a KV head and the part of its query heads).
@@ -89,6 +97,88 @@ struct WholeWork {
         return prompt_item(p.window > 0 ? max(0, first - p.window + 1) : 0, p.a.causal ? last + 1 : n.qn);
     }
 };
+
+// Deals the segments out: this CTA's in items[] as (first token, tokens, chunk, head), their number; 0 if there is nothing to
+// do, -1 if the work is better cut into runs.  Segment i of all, by number of chunk from the last down, then by request, those
+// with most chunks first, then by head, goes to CTA i of the first round, to CTA gridDim - 1 - i of the second, and so on:
+// where later chunks see more keys that is the longest first.  scratch: 20 kDealRequests + 4 (kDealChunks + 1) bytes, sums: a
+// word for each warp; the whole block.
+template <int kWarps, typename W>
+__device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int64_t* sums, int4* items) {
+    constexpr int kThreads = 32 * kWarps;
+    const int tid = (int)threadIdx.x, requests = work.requests(), heads = work.heads(), ctas = (int)gridDim.x;
+    if (requests > kDealRequests) return -1;
+    int32_t *const q0 = scratch, *const qn = q0 + kDealRequests, *const chunks = qn + kDealRequests, *const sorted = chunks + kDealRequests,
+                   *const order = sorted + kDealRequests, *const levels = order + kDealRequests;
+    int mine = 0;
+    for (int b = tid; b < requests; b += kThreads) {
+        const AttnLengths n = work.lengths(b);
+        q0[b] = n.q0, qn[b] = n.qn;
+        mine = max(mine, chunks[b] = work.chunks(n));
+    }
+    if (__syncthreads_or(mine > kDealChunks)) return -1;
+    for (int b = tid; b < requests; b += kThreads) {
+        const int c = chunks[b];
+        int rank = 0;
+        for (int x = 0; x < requests; ++x) rank += chunks[x] > c || (chunks[x] == c && x < b);
+        sorted[rank] = c;
+        order[rank] = b;
+    }
+    __syncthreads();
+    // level i is the chunks sorted[0] - 1 - i: how many there are at lower levels
+    const int most = requests > 0 ? sorted[0] : 0;
+    int before = 0;
+    for (int i0 = 0; i0 < most; i0 += kThreads) {
+        const int i = i0 + tid, c = most - 1 - i;
+        int low = 0, high = requests;  // requests with more than c chunks
+        while (i < most && low < high) {
+            const int mid = (low + high) >> 1;
+            if (sorted[mid] > c) low = mid + 1;
+            else high = mid;
+        }
+        int64_t all;
+        const int64_t at = before + block_sum<kWarps>(i < most ? low : 0, all, sums);
+        if (before + all > INT32_MAX / 4) return -1;
+        if (i < most) levels[i] = (int)at;
+        before += (int)all;
+    }
+    if (tid == 0) levels[most] = before;
+    __syncthreads();
+    const int64_t total = (int64_t)before * heads;
+    if (total == 0) return 0;
+    if (total > (int64_t)kDealItems * ctas) return -1;
+    const int rounds = (int)((total + ctas - 1) / ctas);
+    // segment of CTA x in round k
+    auto item = [&](int x, int k, int4& to) {
+        const int at = k * ctas + (k & 1 ? ctas - 1 - x : x);
+        if (at >= total) return false;
+        const int y = at / heads;
+        int low = 0, high = most;
+        while (high - low > 1) {
+            const int mid = (low + high) >> 1;
+            if (levels[mid] <= y) low = mid;
+            else high = mid;
+        }
+        const int b = order[y - levels[low]];
+        to = make_int4(q0[b], qn[b], most - 1 - low, at - y * heads);
+        return true;
+    };
+    if (rounds <= kDealChecked) {
+        int cost = 0;
+        int4 it;
+        for (int k = 0; tid < ctas && k < rounds; ++k)
+            if (item(tid, k, it)) cost += work.item(AttnLengths{it.x, it.y, it.y}, it.z).tiles + kPromptSegmentCost;
+        int64_t all;
+        block_sum<kWarps>(cost, all, sums);
+        if (__syncthreads_or(cost > all / ctas + 2 * kPromptJoinCost)) return -1;
+    }
+    for (int k = tid; k < rounds; k += kThreads) {
+        int4 it;
+        if (item((int)blockIdx.x, k, it)) items[k] = it;
+    }
+    const int last = (rounds - 1) * ctas + (rounds - 1 & 1 ? ctas - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    return last < total ? rounds : rounds - 1;
+}
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int channel, int head, int token, uint32_t bar) {
     asm volatile(
@@ -203,13 +293,14 @@ template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
     using Sh = WholeShape<T, D, TILES>;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 4 * Sh::kStages + 1];
+    __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 5 * Sh::kStages + 1];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int32_t dirty[8];              // of every eighth segment: its number + 1 if values were taken out
     __shared__ volatile uint32_t arrived[2][TILES];    // of the run's first and last segment
     __shared__ volatile uint32_t added[2][TILES];      // whether this CTA has counted itself there
     __shared__ PromptSegment start;
+    __shared__ int4 items[kDealItems];
     const rra_prompt_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, warp = tid >> 5;
     const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
@@ -221,7 +312,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     // q_full[i], pv_full[i]: what the next products of tile i wait for, with their turn; s_full[i], o_full[i]: done
     const uint32_t q_full = bars, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, pv_full = s_full + 8 * TILES,
                    o_full = pv_full + 8 * TILES, joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 8 * Sh::kStages,
-                   v_full = k_empty + 8 * Sh::kStages, v_empty = v_full + 8 * Sh::kStages, drained = v_empty + 8 * Sh::kStages;
+                   v_full = k_empty + 8 * Sh::kStages, v_empty = v_full + 8 * Sh::kStages, v_ready = v_empty + 8 * Sh::kStages, drained = v_ready + 8 * Sh::kStages;
     constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
     if (tid == 0) {
@@ -239,6 +330,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             mbar_init(k_empty + 8 * i, TILES);
             mbar_init(v_full + 8 * i, 1);
             mbar_init(v_empty + 8 * i, TILES);
+            mbar_init(v_ready + 8 * i, 1);
         }
         for (int i = 0; i < 8; ++i) dirty[i] = 0;
         mbar_init(drained, TILES);
@@ -249,8 +341,10 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     pdl_wait();
 
     const WholeWork<TILES> work{p};
-    int64_t r0, r1, run;
-    if (!prompt_run<Sh::kWarps>(work, chunk_sums, part, start, r0, r1, run)) return;
+    int64_t r0 = 0, r1 = INT64_MAX, run = 1;
+    const int dealt = prompt_deal<Sh::kWarps>(work, chunk_sums, part, items);
+    __syncthreads();
+    if (dealt == 0 || (dealt < 0 && !prompt_run<Sh::kWarps>(work, chunk_sums, part, start, r0, r1, run))) return;
     if (warp == Sh::kIssue) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -260,8 +354,32 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = tmem_base;
-    PromptSegment seg = start;
-    prompt_load(work, seg);
+    // Segments: the first, and the next of one; those that are dealt out have a row of their own.
+    auto load = [&](PromptSegment& s, int k) {
+        const int4 it = items[k];
+        s.n = AttnLengths{it.x, it.y, it.y};
+        s.b = k, s.c = it.z, s.h = it.w;
+        const PromptItem t = work.item(s.n, s.c);
+        s.first_tile = t.first_tile;
+        s.begin = 0, s.end = t.tiles + kPromptSegmentCost;
+    };
+    auto next = [&](PromptSegment& s) {
+        if (dealt >= 0) {
+            if (s.b + 1 == dealt) return false;
+            load(s, s.b + 1);
+        } else {
+            if (s.end >= r1) return false;
+            prompt_next(work, s);
+        }
+        return true;
+    };
+    PromptSegment seg;
+    if (dealt >= 0) {
+        load(seg, 0);
+    } else {
+        seg = start;
+        prompt_load(work, seg);
+    }
     auto first_of = [&](const PromptSegment& s) {
         const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - kPromptSegmentCost;
         return (int)(from > 0 ? from : 0);
@@ -272,6 +390,11 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, attn_try(bar, parity & 1u) || attn_wait_slow(bar, parity & 1u, ws));
+    };
+
+    auto edge_of = [&](const PromptSegment& s) {
+        const int first = s.c * TILES * p.span, last = min(s.n.qn, first + TILES * p.span) - 1;
+        return PromptEdge{p.window > 0 ? max(0, last - p.window + 1) : 0, a.causal ? first + 1 : s.n.qn};
     };
 
     uint32_t n = 0;   // key tiles of this run so far
@@ -301,12 +424,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 lo[r] = live[r] && p.window > 0 ? max(0, token[r] - p.window + 1) : 0;
                 hi[r] = !live[r] ? INT32_MAX : a.causal ? token[r] + 1 : seg.n.qn;
             }
-            PromptEdge edge;
-            {
-                const int first = seg.c * TILES * p.span, last = min(seg.n.qn, first + TILES * p.span) - 1;
-                edge.from = p.window > 0 ? max(0, last - p.window + 1) : 0;
-                edge.to = a.causal ? first + 1 : seg.n.qn;
-            }
+            const PromptEdge edge = edge_of(seg);
             float m[2] = {-FLT_MAX, -FLT_MAX}, limit[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
             const uint64_t factor2 = pair2(factor, factor), lift2 = pair2(Sh::kLift, Sh::kLift);
 #pragma unroll 1
@@ -315,7 +433,6 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 if (!ok) break;
                 tc_after_sync();
                 const int key0 = (seg.first_tile + tl) * kPromptKeys;
-                const bool masks = edge.masks(key0);
                 uint32_t v[64];  // v[4 j + 2 r + e]: row r, key 8 j + 2 t + e
                 tc_ld_rows64(s_at, v);
                 tc_ld_rows64(s_at + 64, v + 32);
@@ -323,12 +440,19 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 if (p.flip != 1.f)
 #pragma unroll
                     for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
-                if (masks) {
+                if (edge.masks(key0)) {
+                    // bit j of seen[2 r + e]: whether row r sees key 8 j + 2 t + e
+                    uint32_t seen[4];
+                    bool whole = true;
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        const int key = key0 + 8 * (k >> 2) + 2 * t + (k & 1), r = k >> 1 & 1;
-                        if (key < lo[r] || key >= hi[r]) v[k] = 0xff800000u;
+                    for (int k = 0; k < 4; ++k) {
+                        auto below = [&](int end) { return (1u << min(max((min(end - key0, 2 * kPromptKeys) - 2 * t - (k & 1) + 7) >> 3, 0), 16)) - 1u; };
+                        seen[k] = below(hi[k >> 1]) & ~below(lo[k >> 1]);
+                        whole = whole && seen[k] == 0xffffu;
                     }
+                    if (!__all_sync(0xffffffffu, whole))
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) v[k] = seen[k & 3] >> (k >> 2) & 1u ? v[k] : 0xff800000u;
                 }
                 float top[2] = {-FLT_MAX, -FLT_MAX};
 #pragma unroll
@@ -385,27 +509,6 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                         split2(sum[r], a0, a1);
                         l[r] += a0 + a1;
                     }
-                }
-                if (masks) {  // values that a row does not see must be finite
-                    const uint32_t stage = n % Sh::kStages;
-                    ok = wait(v_full + 8 * stage, n / Sh::kStages);
-                    if (!ok) break;
-#pragma unroll 1
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = smem + Sh::kV + stage * Sh::kTile + 16 * (256 * k + (tid & 255));
-                        uint32_t w[4], bad = 0;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) bad |= not_finite<Sh::kHalf>(w[e]);
-                        if (bad == 0u) continue;
-                        dirty[sn & 7] = (int32_t)sn + 1;
-                        __threadfence_block();  // whoever finds the 0 finds this
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] &= ~((not_finite<Sh::kHalf>(w[e]) >> 15) * 0xffffu);
-                        sts_v4(at, w[0], w[1], w[2], w[3]);
-                    }
-                    __syncwarp();
-                    fence_proxy_async_smem();
                 }
                 tc_wait_st();
                 tc_before_sync();
@@ -472,12 +575,12 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             if (starts && ends) {
                 float inv[2];
                 statistics(top, l, inv);
+                float o[D / 2];
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    float o[16];
-                    get(q, o);
-                    put(o, 32 * q, inv);
-                }
+                for (int q = 0; q < D / 64; ++q) tc_ld_rows64(o_at + 64 * q, (uint32_t*)o + 32 * q);
+                tc_wait_ld();
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) put(o + 16 * q, 32 * q, inv);
                 add(nullptr);
             } else {
                 // The last CTA to arrive adds the parts in order; its own, if it finds all others there, from where it is.
@@ -573,9 +676,8 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                     if (counts) *count = 0u;
                 }
             }
-            if (seg.end >= r1) break;
             tc_before_sync();
-            prompt_next(work, seg);
+            if (!next(seg)) break;
         }
         // A wait ran out: the results are lost, but the counters of the segments from here on have to be zero for the next
         // call.  So this CTA still counts itself, and whoever is last there clears them.
@@ -589,8 +691,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                     const uint32_t before = added[which][i] != 0u ? arrived[which][i] : atomicAdd(count, 1u);
                     if (before == (uint32_t)(i1 - i0)) *count = 0u;
                 }
-                if (seg.end >= r1) break;
-                prompt_next(work, seg);
+                if (!next(seg)) break;
             }
     } else if (warp == Sh::kCopy) {
         // =============================== copies, ahead of the products by the stages ====
@@ -639,14 +740,53 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                     break;
                 }
             }
-            if (!ok || seg.end >= r1) break;
-            prompt_next(work, seg);
+            if (!ok || !next(seg)) break;
         }
         // No copy is in flight when the CTA ends, also where nobody waited for it.
         for (int i = 0; i < TILES && sn > 0; ++i) attn_wait_quiet(q_full + 8 * i, (sn - 1) & 1u);
         for (uint32_t x = n > Sh::kStages ? n - Sh::kStages : 0; x < n; ++x) {
             attn_wait_quiet(k_full + 8 * (x % Sh::kStages), x / Sh::kStages & 1u);
             attn_wait_quiet(v_full + 8 * (x % Sh::kStages), x / Sh::kStages & 1u);
+        }
+    } else if (warp == Sh::kLook) {
+        // =============================== values that some row does not see must be finite ====
+        set_registers<Sh::kIssueRegs, Sh::kLaunchRegs>();
+        for (bool ok = true; ok;) {
+            const int t0 = first_of(seg), t1 = end_of(seg);
+            const PromptEdge edge = edge_of(seg);
+#pragma unroll 1
+            for (int tl = t0; tl < t1; ++tl, ++n) {
+                const uint32_t stage = n % Sh::kStages;
+                ok = wait(v_full + 8 * stage, n / Sh::kStages);
+                if (!ok) break;
+                if (edge.masks((seg.first_tile + tl) * kPromptKeys)) {
+#pragma unroll 1
+                    for (uint32_t k = 0; k < Sh::kTile; k += 8 * 512) {
+                        const uint32_t at = smem + Sh::kV + stage * Sh::kTile + k + 16 * (tid & 31);
+                        uint32_t w[8][4], bad = 0;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[x][0]), "=r"(w[x][1]), "=r"(w[x][2]), "=r"(w[x][3]) : "r"(at + 512 * x));
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) bad |= not_finite<Sh::kHalf>(w[x][e]);
+                        if (bad == 0u) continue;
+                        dirty[sn & 7] = (int32_t)sn + 1;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[x][e] &= ~((not_finite<Sh::kHalf>(w[x][e]) >> 15) * 0xffffu);
+                            sts_v4(at + 512 * x, w[x][0], w[x][1], w[x][2], w[x][3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (elected()) mbar_arrive(v_ready + 8 * stage);
+            }
+            if (t0 < t1) ++sn;
+            if (!ok || !next(seg)) break;
         }
     } else {
         // =============================== products of tile i: one thread issues ====
@@ -664,11 +804,11 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             if (t0 < t1) {
 #pragma unroll 1
                 for (int tl = t0 - 1; tl < t1; ++tl) {  // products of tile tl, scores of the next
-                    const bool values = tl >= t0, next = tl + 1 < t1;
+                    const bool values = tl >= t0, scores = tl + 1 < t1;
                     const uint32_t then = n + (values ? 1 : 0);  // the tile whose scores come next
                     // K and V are there long before: first their waits, so that nothing comes between the products
-                    ok = (!next || wait(k_full + 8 * (then % Sh::kStages), then / Sh::kStages)) &&
-                         (!values || wait(v_full + 8 * (n % Sh::kStages), n / Sh::kStages)) &&
+                    ok = (!scores || wait(k_full + 8 * (then % Sh::kStages), then / Sh::kStages)) &&
+                         (!values || wait(v_ready + 8 * (n % Sh::kStages), n / Sh::kStages)) &&
                          (values ? wait(pv_full + 8 * i, n) : wait(q_full + 8 * i, sn));
                     if (!ok) break;
                     tc_after_sync();
@@ -679,7 +819,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                             for (int k = 0; k < kPromptKeys / 16; ++k) tc_mma_ts(o_at, s_at + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
                             tc_commit(v_empty + 8 * (n % Sh::kStages));
                         }
-                        if (next) {  // S_i = Q_i K^T
+                        if (scores) {  // S_i = Q_i K^T
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
                                 constexpr auto at = [](int x) { return (uint32_t)((x >> 2) * Sh::kPanel + (x & 3) * 32) >> 4; };
@@ -699,8 +839,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 }
                 ++sn;
             }
-            if (!ok || seg.end >= r1) break;
-            prompt_next(work, seg);
+            if (!ok || !next(seg)) break;
         }
         // nothing is in flight when TMEM goes back
         if (i < TILES) {
@@ -746,7 +885,7 @@ template <typename T, int D, int TILES>
 static rra_status_t whole_launch(const PromptParams& p, int ctas, rra_stream_t stream) {
     using Sh = WholeShape<T, D, TILES>;
     const void* k = (const void*)prompt_attention_kernel<T, D, TILES>;
-    static_assert(Sh::kSmem <= 227 * 1024 - 8192, "shared memory");
+    static_assert(Sh::kSmem <= 227 * 1024 - 20480, "shared memory, with the list of segments");
     if (configure_cluster_kernel(k, Sh::kSmem) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
