@@ -13,8 +13,10 @@
 // but the other tile's products to do meanwhile (TMEM: 128 columns of S and D of O a
 // tile, twice).
 //
-// The maximum that weights are taken against moves only when a score passes it by
-// more than kPromptSlack (in units of log2); only then O is scaled, in TMEM.
+// The maximum that weights are taken against is that of a row's first tile, until
+// weights get large: their sum, which is needed anyway, shows it (an earlier form
+// looked for each tile's maximum first, 400 of the 1350 cycles from scores to
+// weights).  Only then the tile's maximum is found, and O scaled, in TMEM.
 //
 // A value that is infinite or NaN would spoil rows that do not see it: 0 times it
 // is NaN.  So in tiles that some row does not see whole, a warp looks values over in
@@ -34,7 +36,6 @@
 
 namespace rra {
 
-constexpr float kPromptSlack = 8.f;  // log2 of how far weights may pass 1 before the maximum moves
 
 constexpr int kDealRequests = 1024;  // up to so many requests, and chunks of the longest, segments are dealt out: their order
 constexpr int kDealChunks = 8192;    // is found in shared memory
@@ -57,7 +58,9 @@ struct PromptParams {
 template <typename T, int D, int TILES>
 struct WholeShape {
     static constexpr bool kHalf = std::is_same<T, __half>::value;
-    static constexpr float kLift = kHalf ? 7.f : 0.f, kUnlift = kHalf ? 1.f / 128 : 1.f;  // weights are 2^kLift times as large: 2^(8 + 7) fits
+    // Weights are 2^kLift times as large as they are; a thread's share of a row in a tile may add up to kMost: more is no
+    // binary16, and sums of large values stay far from binary32's end.
+    static constexpr float kLift = kHalf ? 7.f : 0.f, kUnlift = kHalf ? 1.f / 128 : 1.f, kMost = kHalf ? 32768.f : 1024.f;
     static constexpr int kPanel = 128 * 128;       // 128 rows of 64 channels, swizzled in 128 bytes
     static constexpr int kTile = D / 64 * kPanel;
     static constexpr int kStages = 2;              // of K, and of V
@@ -425,8 +428,9 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 hi[r] = !live[r] ? INT32_MAX : a.causal ? token[r] + 1 : seg.n.qn;
             }
             const PromptEdge edge = edge_of(seg);
-            float m[2] = {-FLT_MAX, -FLT_MAX}, limit[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
-            const uint64_t factor2 = pair2(factor, factor), lift2 = pair2(Sh::kLift, Sh::kLift);
+            // What a row's weights are taken against, in units of log2 (kNone: it has seen no key yet), and their sum.
+            constexpr float kNone = -FLT_MAX;
+            float top[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
 #pragma unroll 1
             for (int tl = t0; tl < t1; ++tl, ++n) {
                 ok = wait(s_full + 8 * i, n);
@@ -454,60 +458,66 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
 #pragma unroll
                         for (int k = 0; k < 64; ++k) v[k] = seen[k & 3] >> (k >> 2) & 1u ? v[k] : 0xff800000u;
                 }
-                float top[2] = {-FLT_MAX, -FLT_MAX};
+                const uint64_t factor2 = pair2(factor, factor);
+                for (bool exact = __any_sync(0xffffffffu, top[0] == kNone || top[1] == kNone);; exact = true) {
+                    if (exact) {
+                        float by[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float most[2] = {-FLT_MAX, -FLT_MAX};
+                        for (int r = 0; r < 2; ++r) {
+                            float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        most[j & 1] = max3(most[j & 1], __uint_as_float(v[4 * j + 2 * r]), __uint_as_float(v[4 * j + 2 * r + 1]));
-                    top[r] = fmaxf(most[0], most[1]);
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                }
-                if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {  // a maximum moves: scale what was summed
-                    float by[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float now = top[r] > limit[r] ? top[r] : m[r];
-                        by[r] = exp2_fast((m[r] - now) * factor);
-                        m[r] = now;
-                        limit[r] = now + __fdividef(kPromptSlack, factor);
-                        l[r] *= by[r];
-                    }
-                    if (tl > t0) {
+                            for (int j = 0; j < 16; ++j)
+                                most[j & 1] = max3(most[j & 1], __uint_as_float(v[4 * j + 2 * r]), __uint_as_float(v[4 * j + 2 * r + 1]));
+                            float now = fmaxf(most[0], most[1]);
+                            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 1));
+                            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 2));
+                            now = fmaxf(top[r], now * factor);  // no key: kNone
+                            by[r] = exp2_fast(top[r] - now);
+                            top[r] = now;
+                            l[r] *= by[r];
+                        }
+                        if (tl > t0 && __any_sync(0xffffffffu, by[0] != 1.f || by[1] != 1.f)) {
 #pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t o[16];
-                            tc_ld_rows32(o_at + 32 * q, o);
-                            tc_wait_ld();
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t o[16];
+                                tc_ld_rows32(o_at + 32 * q, o);
+                                tc_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by[k >> 1 & 1]);
-                            tc_st_rows32(o_at + 32 * q, o);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by[k >> 1 & 1]);
+                                tc_st_rows32(o_at + 32 * q, o);
+                            }
                         }
                     }
-                }
-                // ---- weights, where the scores were ----
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t w[16];
+                    // ---- weights, where the scores were ----
+                    const float less[2] = {top[0] == kNone ? 0.f : Sh::kLift - top[0], top[1] == kNone ? 0.f : Sh::kLift - top[1]};
+                    const uint64_t less2[2] = {pair2(less[0], less[0]), pair2(less[1], less[1])};
                     uint64_t sum[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int r = k & 1, at = 32 * q + 2 * k;
-                        float e0, e1;
-                        split2(fma2(add2(pair2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), pair2(-m[r], -m[r])), factor2, lift2), e0, e1);
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        sum[r] = add2(sum[r], pair2(e0, e1));
-                        w[k] = pack2<T>(e0, e1);
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int r = k & 1, at = 32 * q + 2 * k;
+                            float e0, e1;
+                            split2(fma2(pair2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), factor2, less2[r]), e0, e1);
+                            e0 = exp2_fast(e0);
+                            e1 = exp2_fast(e1);
+                            sum[r] = add2(sum[r], pair2(e0, e1));
+                            w[k] = pack2<T>(e0, e1);
+                        }
+                        tc_st_weights(s_at + 32 * q, w);
                     }
-                    tc_st_weights(s_at + 32 * q, w);
+                    float all[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float a0, a1;
                         split2(sum[r], a0, a1);
-                        l[r] += a0 + a1;
+                        all[r] = a0 + a1;
+                    }
+                    if (exact || !__any_sync(0xffffffffu, all[0] > Sh::kMost || all[1] > Sh::kMost)) {
+                        l[0] += all[0];
+                        l[1] += all[1];
+                        break;
                     }
                 }
                 tc_wait_st();
@@ -524,10 +534,8 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             if (!ok) break;
             // ---- the segment's end in this run ----
             const bool starts = seg.begin >= r0, ends = seg.end <= r1;
-            float top[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                top[r] = m[r] * factor;
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
                 l[r] *= Sh::kUnlift;  // O stays lifted until it is divided by its sum
