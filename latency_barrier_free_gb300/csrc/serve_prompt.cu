@@ -296,7 +296,7 @@ template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
     using Sh = WholeShape<T, D, TILES>;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t bar_mem[6 * TILES + 5 * Sh::kStages + 1];
+    __shared__ __align__(8) uint64_t bar_mem[8 * TILES + 5 * Sh::kStages + 1];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int32_t dirty[8];              // of every eighth segment: its number + 1 if values were taken out
@@ -312,10 +312,12 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     float* const parts = (float*)(ws + 1);
 
     const uint32_t bars = smem_u32(bar_mem);
-    // q_full[i], pv_full[i]: what the next products of tile i wait for, with their turn; s_full[i], o_full[i]: done
+    // q_full[i], pv_half[i]: what the next products of tile i wait for, with their turn; pv_full[i]: the second half of the
+    // weights; s_full[i], half_done[i], o_full[i]: products that are done
     const uint32_t q_full = bars, q_empty = q_full + 8 * TILES, s_full = q_empty + 8 * TILES, pv_full = s_full + 8 * TILES,
                    o_full = pv_full + 8 * TILES, joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 8 * Sh::kStages,
-                   v_full = k_empty + 8 * Sh::kStages, v_empty = v_full + 8 * Sh::kStages, v_ready = v_empty + 8 * Sh::kStages, drained = v_ready + 8 * Sh::kStages;
+                   v_full = k_empty + 8 * Sh::kStages, v_empty = v_full + 8 * Sh::kStages, v_ready = v_empty + 8 * Sh::kStages, pv_half = v_ready + 8 * Sh::kStages, half_done = pv_half + 8 * TILES,
+                   drained = half_done + 8 * TILES;
     constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
     if (tid == 0) {
@@ -324,7 +326,9 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             mbar_init(q_full + 8 * i, 1 + kTurn);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(pv_full + 8 * i, 2 * kPromptRows + kTurn);
+            mbar_init(pv_half + 8 * i, 2 * kPromptRows + kTurn);
+            mbar_init(pv_full + 8 * i, 2 * kPromptRows);
+            mbar_init(half_done + 8 * i, 1);
             mbar_init(o_full + 8 * i, 1);
             mbar_init(joined + 8 * i, 2 * kPromptRows);
         }
@@ -412,6 +416,8 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
 #pragma unroll
         for (int r = 0; r < 2; ++r) tok[r] = p.by_group(row0 + 8 * r), head_in[r] = row0 + 8 * r - tok[r] * p.group;
         const float factor = p.factor;
+        const uint64_t factor2 = pair2(factor, factor);
+        const bool flips = p.flip != 1.f;
         uint32_t joins = 0;
         bool ok = true;
         while (ok) {
@@ -430,7 +436,8 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             const PromptEdge edge = edge_of(seg);
             // What a row's weights are taken against, in units of log2 (kNone: it has seen no key yet), and their sum.
             constexpr float kNone = -FLT_MAX;
-            float top[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+            float top[2] = {kNone, kNone}, less[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // less: what is taken off scores
+            bool fresh = true;  // some row has none
 #pragma unroll 1
             for (int tl = t0; tl < t1; ++tl, ++n) {
                 ok = wait(s_full + 8 * i, n);
@@ -441,10 +448,11 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 tc_ld_rows64(s_at, v);
                 tc_ld_rows64(s_at + 64, v + 32);
                 tc_wait_ld();
-                if (p.flip != 1.f)
+                const bool masks = edge.masks(key0);
+                if (masks || flips) {
+                    if (flips)
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
-                if (edge.masks(key0)) {
+                        for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
                     // bit j of seen[2 r + e]: whether row r sees key 8 j + 2 t + e
                     uint32_t seen[4];
                     bool whole = true;
@@ -458,42 +466,48 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
 #pragma unroll
                         for (int k = 0; k < 64; ++k) v[k] = seen[k & 3] >> (k >> 2) & 1u ? v[k] : 0xff800000u;
                 }
-                const uint64_t factor2 = pair2(factor, factor);
-                for (bool exact = __any_sync(0xffffffffu, top[0] == kNone || top[1] == kNone);; exact = true) {
-                    if (exact) {
-                        float by[2];
+                // The halves of a tile's weights are given away one after the other: products begin with the first.
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float most[2] = {-INFINITY, -INFINITY};
+                for (int q = 0; q < 2; ++q) {
+                    float all[2];
+                    bool exact = fresh;
+                    while (true) {
+                        if (exact && (q == 0 || !fresh)) {  // against the maximum of what has not been given away
+                            float by[2];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                most[j & 1] = max3(most[j & 1], __uint_as_float(v[4 * j + 2 * r]), __uint_as_float(v[4 * j + 2 * r + 1]));
-                            float now = fmaxf(most[0], most[1]);
-                            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 1));
-                            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 2));
-                            now = fmaxf(top[r], now * factor);  // no key: kNone
-                            by[r] = exp2_fast(top[r] - now);
-                            top[r] = now;
-                            l[r] *= by[r];
-                        }
-                        if (tl > t0 && __any_sync(0xffffffffu, by[0] != 1.f || by[1] != 1.f)) {
+                            for (int r = 0; r < 2; ++r) {
+                                float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                                for (int j = 8 * q; j < 16; ++j)
+                                    most[j & 1] = max3(most[j & 1], __uint_as_float(v[4 * j + 2 * r]), __uint_as_float(v[4 * j + 2 * r + 1]));
+                                float now = fmaxf(most[0], most[1]);
+                                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 1));
+                                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 2));
+                                now = fmaxf(top[r], now * factor);  // no key: kNone
+                                by[r] = exp2_fast(top[r] - now);
+                                top[r] = now;
+                                l[r] *= by[r];
+                                less[r] = now == kNone ? 0.f : Sh::kLift - now;
+                            }
+                            if (q == 1) {  // products of the first half are under way
+                                ok = wait(half_done + 8 * i, n);
+                                tc_after_sync();
+                            }
+                            if (ok && (tl > t0 || q == 1) && __any_sync(0xffffffffu, by[0] != 1.f || by[1] != 1.f)) {
 #pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t o[16];
-                                tc_ld_rows32(o_at + 32 * q, o);
-                                tc_wait_ld();
+                                for (int x = 0; x < D / 32; ++x) {
+                                    uint32_t o[16];
+                                    tc_ld_rows32(o_at + 32 * x, o);
+                                    tc_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by[k >> 1 & 1]);
-                                tc_st_rows32(o_at + 32 * q, o);
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by[k >> 1 & 1]);
+                                    tc_st_rows32(o_at + 32 * x, o);
+                                }
                             }
                         }
-                    }
-                    // ---- weights, where the scores were ----
-                    const float less[2] = {top[0] == kNone ? 0.f : Sh::kLift - top[0], top[1] == kNone ? 0.f : Sh::kLift - top[1]};
-                    const uint64_t less2[2] = {pair2(less[0], less[0]), pair2(less[1], less[1])};
-                    uint64_t sum[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                        // ---- weights, where the scores were ----
+                        const uint64_t less2[2] = {pair2(less[0], less[0]), pair2(less[1], less[1])};
+                        uint64_t sum[2] = {pair2(0.f, 0.f), pair2(0.f, 0.f)};
                         uint32_t w[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
@@ -506,23 +520,23 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                             w[k] = pack2<T>(e0, e1);
                         }
                         tc_st_weights(s_at + 32 * q, w);
-                    }
-                    float all[2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float a0, a1;
-                        split2(sum[r], a0, a1);
-                        all[r] = a0 + a1;
+                        for (int r = 0; r < 2; ++r) {
+                            float a0, a1;
+                            split2(sum[r], a0, a1);
+                            all[r] = a0 + a1;
+                        }
+                        if (exact || !__any_sync(0xffffffffu, all[0] > Sh::kMost || all[1] > Sh::kMost)) break;
+                        exact = true;
                     }
-                    if (exact || !__any_sync(0xffffffffu, all[0] > Sh::kMost || all[1] > Sh::kMost)) {
-                        l[0] += all[0];
-                        l[1] += all[1];
-                        break;
-                    }
+                    l[0] += all[0];
+                    l[1] += all[1];
+                    tc_wait_st();
+                    tc_before_sync();
+                    mbar_arrive((q == 0 ? pv_half : pv_full) + 8 * i);
                 }
-                tc_wait_st();
-                tc_before_sync();
-                mbar_arrive(pv_full + 8 * i);
+                if (!ok) break;
+                if (fresh) fresh = __any_sync(0xffffffffu, top[0] == kNone || top[1] == kNone);
             }
             bool lost = false;
             if (ok && t0 < t1) {
@@ -817,16 +831,28 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                     // K and V are there long before: first their waits, so that nothing comes between the products
                     ok = (!scores || wait(k_full + 8 * (then % Sh::kStages), then / Sh::kStages)) &&
                          (!values || wait(v_ready + 8 * (n % Sh::kStages), n / Sh::kStages)) &&
-                         (values ? wait(pv_full + 8 * i, n) : wait(q_full + 8 * i, sn));
+                         (values ? wait(pv_half + 8 * i, n) : wait(q_full + 8 * i, sn));
                     if (!ok) break;
                     tc_after_sync();
                     const uint32_t k_at = k_desc + then % Sh::kStages * kStep, v_at = v_desc + n % Sh::kStages * kStep;
-                    if (elected()) {
-                        if (values) {  // O_i += P_i V
+                    if (values) {  // O_i += P_i V
 #pragma unroll
-                            for (int k = 0; k < kPromptKeys / 16; ++k) tc_mma_ts(o_at, s_at + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
-                            tc_commit(v_empty + 8 * (n % Sh::kStages));
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 1) {
+                                ok = wait(pv_full + 8 * i, n);
+                                tc_after_sync();
+                            }
+                            if (ok && elected()) {
+#pragma unroll
+                                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                                    tc_mma_ts(o_at, s_at + 8 * k, v_at + k * (2048 >> 4), kPv, tl > t0 || k > 0);
+                                tc_commit(h == 0 ? half_done + 8 * i : v_empty + 8 * (n % Sh::kStages));
+                            }
+                            __syncwarp();
                         }
+                        if (!ok) break;
+                    }
+                    if (elected()) {
                         if (scores) {  // S_i = Q_i K^T
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
@@ -836,10 +862,10 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                             tc_commit(s_full + 8 * i);
                             tc_commit(k_empty + 8 * (then % Sh::kStages));
                             if (tl + 2 == t1) tc_commit(q_empty + 8 * i);
-                            if (kTurn) mbar_arrive(i == 1 ? pv_full : values ? pv_full + 8 : q_full + 8);
+                            if (kTurn) mbar_arrive(i == 1 ? pv_half : values ? pv_half + 8 : q_full + 8);
                         } else {
                             tc_commit(o_full + 8 * i);
-                            if (kTurn) mbar_arrive(i == 0 ? pv_full + 8 : q_full);
+                            if (kTurn) mbar_arrive(i == 0 ? pv_half + 8 : q_full);
                         }
                     }
                     __syncwarp();
