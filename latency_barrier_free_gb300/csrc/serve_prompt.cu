@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     __shared__ volatile uint32_t arrived[2][TILES];    // of the run's first and last segment
     __shared__ volatile uint32_t added[2][TILES];      // whether this CTA has counted itself there
     __shared__ PromptSegment start;
+    __shared__ PromptSegment segments[Sh::kWarps];  // each warp's: registers are for scores
     __shared__ int4 items[kDealItems];
     const rra_prompt_attention_args_t& a = p.a;
     const int tid = (int)threadIdx.x, warp = tid >> 5;
@@ -370,22 +371,23 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
         s.first_tile = t.first_tile;
         s.begin = 0, s.end = t.tiles + kPromptSegmentCost;
     };
-    auto next = [&](PromptSegment& s) {
-        if (dealt >= 0) {
-            if (s.b + 1 == dealt) return false;
-            load(s, s.b + 1);
-        } else {
-            if (s.end >= r1) return false;
-            prompt_next(work, s);
-        }
+    auto next = [&](PromptSegment& at) {
+        PromptSegment s = at;
+        if (dealt >= 0 ? s.b + 1 == dealt : s.end >= r1) return false;
+        if (dealt >= 0) load(s, s.b + 1);
+        else prompt_next(work, s);
+        __syncwarp();  // all lanes have read it; they write the same
+        at = s;
+        __syncwarp();
         return true;
     };
-    PromptSegment seg;
-    if (dealt >= 0) {
-        load(seg, 0);
-    } else {
-        seg = start;
-        prompt_load(work, seg);
+    PromptSegment& seg = segments[warp];
+    {
+        PromptSegment s = start;
+        if (dealt >= 0) load(s, 0);
+        else prompt_load(work, s);
+        seg = s;
+        __syncwarp();
     }
     auto first_of = [&](const PromptSegment& s) {
         const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - kPromptSegmentCost;
@@ -422,18 +424,15 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
         bool ok = true;
         while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);
-            const int kv_head = p.by_parts(seg.h), head0 = (seg.h - kv_head * p.parts) * p.group;  // of the KV head's query heads
-            // the keys that the rows see, and which of the segment's tiles some row does not see whole
-            int token[2], lo[2], hi[2];
-            bool live[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                token[r] = (seg.c * TILES + i) * p.span + tok[r];
-                live[r] = tok[r] < p.span && token[r] < seg.n.qn && head0 + head_in[r] < p.heads_of_kv;
-                lo[r] = live[r] && p.window > 0 ? max(0, token[r] - p.window + 1) : 0;
-                hi[r] = !live[r] ? INT32_MAX : a.causal ? token[r] + 1 : seg.n.qn;
-            }
-            const PromptEdge edge = edge_of(seg);
+            // Of row r: its token, whether it is one, and the keys that it sees.
+            auto token_of = [&](int r) { return (seg.c * TILES + i) * p.span + (r ? tok[1] : tok[0]); };
+            auto is_live = [&](int r) {
+                return (r ? tok[1] : tok[0]) < p.span && token_of(r) < seg.n.qn &&
+                       (seg.h - p.by_parts(seg.h) * p.parts) * p.group + (r ? head_in[1] : head_in[0]) < p.heads_of_kv;
+            };
+            auto lo_of = [&](int r) { return is_live(r) && p.window > 0 ? max(0, token_of(r) - p.window + 1) : 0; };
+            auto hi_of = [&](int r) { return !is_live(r) ? INT32_MAX : a.causal ? token_of(r) + 1 : seg.n.qn; };
+            const int edge_from = edge_of(seg).from, edge_to = edge_of(seg).to, first_tile = seg.first_tile;
             // What a row's weights are taken against, in units of log2 (kNone: it has seen no key yet), and their sum.
             constexpr float kNone = -FLT_MAX;
             float top[2] = {kNone, kNone}, less[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // less: what is taken off scores
@@ -443,17 +442,18 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 ok = wait(s_full + 8 * i, n);
                 if (!ok) break;
                 tc_after_sync();
-                const int key0 = (seg.first_tile + tl) * kPromptKeys;
+                const int key0 = (first_tile + tl) * kPromptKeys;
                 uint32_t v[64];  // v[4 j + 2 r + e]: row r, key 8 j + 2 t + e
                 tc_ld_rows64(s_at, v);
                 tc_ld_rows64(s_at + 64, v + 32);
                 tc_wait_ld();
-                const bool masks = edge.masks(key0);
+                const bool masks = PromptEdge{edge_from, edge_to}.masks(key0);
                 if (masks || flips) {
                     if (flips)
 #pragma unroll
                         for (int k = 0; k < 64; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * p.flip);
                     // bit j of seen[2 r + e]: whether row r sees key 8 j + 2 t + e
+                    const int lo[2] = {lo_of(0), lo_of(1)}, hi[2] = {hi_of(0), hi_of(1)};
                     uint32_t seen[4];
                     bool whole = true;
 #pragma unroll
@@ -554,6 +554,10 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
                 l[r] *= Sh::kUnlift;  // O stays lifted until it is divided by its sum
             }
+            const int kv_head = p.by_parts(seg.h), head0 = (seg.h - kv_head * p.parts) * p.group;  // of the KV head's query heads
+            const PromptEdge edge = {edge_from, edge_to};
+            const int token[2] = {token_of(0), token_of(1)}, lo[2] = {lo_of(0), lo_of(1)}, hi[2] = {hi_of(0), hi_of(1)};
+            const bool live[2] = {is_live(0), is_live(1)};
             T* out[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
