@@ -46,6 +46,7 @@ constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 bef
 // row's sum counts them whole.  So they are taken 2^kPromptLift times as large: 2^(8 + 7) fits.  (131072 keys of one run, each
 // 2^-25.3 of the largest: without it their share, 0.3 % of the values' size, was missing.)
 constexpr float kPromptLift = 7.f, kPromptUnlift = 1.f / 128;
+constexpr float kPromptMost = 32768.f;  // 8-bit cache: what a block's weights of a row may add up to before the maximum moves
 
 template <typename F, int D, int TILES>
 struct PromptShape {
@@ -191,9 +192,9 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             const int t0 = first_of(seg), t1 = end_of(seg);
             const int all_rows = seg.n.qn * p.group, r = seg.c * Sh::kRows + i * kPromptRows + row;
             const bool live = r < all_rows;
-            constexpr float kNone = kEight ? -0x1p90f : -FLT_MAX;  // no key yet (8 bits: scores are below 2^58, and m enters times 2^32)
-            float m = kNone, limit = kNone, l = 0.f, factor = 1.f;
-            int x = 0;  // 8-bit cache: the exponent that goes with m
+            constexpr float kNone = -FLT_MAX;  // no key yet
+            // (8-bit cache: m is in units of log2, and O and l are 2^-m as large; l has no 2^v)
+            float m = kEight && !live ? 0.f : kNone, limit = kNone, l = 0.f, factor = 1.f;
             if (t0 < t1) {
                 // ---- the row's query, scaled, into shared memory; the keys that it sees ----
                 int lo = 0, hi = 0;
@@ -261,73 +262,66 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                     }
                     if constexpr (kEight) {
                         // As in serve_attn_rows8.cuh: a block of 16 keys has the exponents k and v; scores are v[] 2^k, weights
-                        // 2^((score - m) factor + v - x), their sum's parts 2^(x - v) as large.
+                        // 2^(score factor + v - m), the sum's parts 2^-v as large.  m (kNone: no key yet) is the largest such
+                        // exponent of the row's first tile, until weights get large, which their sum shows.
                         const int2* const ex = exponents[n & 3];
-                        float tops[8], best = 0.f, now = 0.f;  // scores; the largest weight's exponent, its score and x
-                        int at = 0;
+                        for (bool exact = __any_sync(0xffffffffu, m == kNone);; exact = true) {
+                            if (exact) {
+                                float now = -INFINITY;
 #pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            float top = fmaxf(__uint_as_float(v[16 * b]), __uint_as_float(v[16 * b + 1]));
+                                for (int b = 0; b < 8; ++b) {
+                                    float top = -INFINITY;
 #pragma unroll
-                            for (int k = 2; k < 16; ++k) top = fmaxf(top, __uint_as_float(v[16 * b + k]));
-                            tops[b] = top * two_to(ex[b].x);
-                        }
-                        auto find = [&]() {
-                            best = -INFINITY;
-#pragma unroll
-                            for (int b = 0; b < 8; ++b) {
-                                const float up = fmaf(tops[b] - m, factor, (float)(ex[b].y - x));
-                                if (up > best) best = up, now = tops[b], at = ex[b].y;
-                            }
-                        };
-                        find();
-                        if (__any_sync(0xffffffffu, best > kPromptSlack)) {
-                            if (m == kNone && best > kPromptSlack) {  // so far away all weights look alike: again from a key
+                                    for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(v[16 * b + k]));
+                                    now = fmaxf(now, fmaf(top, factor * two_to(ex[b].x), (float)ex[b].y));
+                                }
+                                now = fmaxf(m, now);
+                                const float by = exp2_fast(m - now);
                                 m = now;
-                                x = at;
-                                find();
-                            }
-                            const bool moves = best > kPromptSlack;
-                            const float by = moves ? exp2_fast(-best) : 1.f;
-                            if (moves) {
-                                l *= exp2_fast((m - now) * factor);
-                                m = now;
-                                x = at;
-                            }
-                            if (tl > t0) {
+                                l *= by;
+                                if (tl > t0 && __any_sync(0xffffffffu, by != 1.f)) {
 #pragma unroll 1
-                                for (int q = 0; q < D / 16; ++q) {
-                                    uint32_t o[16];
-                                    tc_ld16(o_at + 16 * q, o);
-                                    tc_wait_ld();
+                                    for (int q = 0; q < D / 16; ++q) {
+                                        uint32_t o[16];
+                                        tc_ld16(o_at + 16 * q, o);
+                                        tc_wait_ld();
 #pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
-                                    tc_st16(o_at + 16 * q, o);
+                                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                                        tc_st16(o_at + 16 * q, o);
+                                    }
                                 }
                             }
-                        }
+                            const float less = m == kNone ? 0.f : kPromptLift - m;
+                            float most = 0.f, all = 0.f;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t w[32];
 #pragma unroll
-                            for (int b = 4 * q; b < 4 * q + 4; ++b) {
-                                const int2 e = ex[b];
-                                const float by = factor * two_to(e.x), less = -m * two_to(-e.x), lift = kPromptLift + (float)(e.y - x);
-                                const uint64_t by2 = pair2(by, by), less2 = pair2(less, less), lifts = pair2(lift, lift);
-                                uint64_t sum = pair2(0.f, 0.f);
+                                for (int b = 4 * q; b < 4 * q + 4; ++b) {
+                                    const int2 e = ex[b];
+                                    const float by = factor * two_to(e.x), off = less + (float)e.y;
+                                    const uint64_t by2 = pair2(by, by), off2 = pair2(off, off);
+                                    uint64_t sum = pair2(0.f, 0.f);
 #pragma unroll
-                                for (int k = 16 * b; k < 16 * b + 16; k += 2) {
-                                    float e0, e1;
-                                    split2(fma2(add2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), less2), by2, lifts), e0, e1);
-                                    e0 = exp2_fast(e0);
-                                    e1 = exp2_fast(e1);
-                                    sum = add2(sum, pair2(e0, e1));
-                                    v[k / 2] = pack_half2(e0, e1);
+                                    for (int k = 16 * b; k < 16 * b + 16; k += 2) {
+                                        float e0, e1;
+                                        split2(fma2(pair2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), by2, off2), e0, e1);
+                                        e0 = exp2_fast(e0);
+                                        e1 = exp2_fast(e1);
+                                        sum = add2(sum, pair2(e0, e1));
+                                        w[k / 2 - 32 * q] = pack_half2(e0, e1);
+                                    }
+                                    float a0, a1;
+                                    split2(sum, a0, a1);
+                                    most = fmaxf(most, a0 + a1);
+                                    all = fmaf(a0 + a1, two_to(-e.y), all);
                                 }
-                                float a0, a1;
-                                split2(sum, a0, a1);
-                                l = fmaf(a0 + a1, two_to(x - e.y), l);
+                                tc_st32(s_at + 32 * q, w);
                             }
-                            tc_st32(s_at + 32 * q, v + 32 * q);
+                            if (exact || !__any_sync(0xffffffffu, most > kPromptMost)) {
+                                l += all;
+                                break;
+                            }
                         }
                         tc_wait_st();
                         tc_before_sync();
@@ -387,9 +381,8 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             }
             // ---- the segment's end in this run ----
             const bool starts = seg.begin >= r0, ends = seg.end <= r1;
-            const float top = m * factor;
+            const float top = kEight ? m : m * factor;
             l *= kPromptUnlift;  // O stays lifted until it is divided by its sum
-            const float up = kEight ? two_to(x) : 1.f;  // what O is too small by
             auto put = [&](__nv_bfloat16* to, const float* o, float inv) {  // 32 channels
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
@@ -407,7 +400,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                 float inv = 0.f;
                 __nv_bfloat16* const to = live ? attn_row(p, seg.n.q0, seg.h, r, top, l, true, inv) : nullptr;
                 inv *= kPromptUnlift;
-                if constexpr (kEight) inv *= up;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
@@ -437,9 +429,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                             uint32_t v[32];
                             tc_ld32(o_at + 32 * q, v);
                             tc_wait_ld();
-                            if constexpr (kEight)
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * up);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 to[(8 * q + k) * kPromptRows + row] =
@@ -488,9 +477,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                             if (x == mine) {
                                 tc_ld32(o_at + 32 * q, v);
                                 tc_wait_ld();
-                                if constexpr (kEight)
-#pragma unroll
-                                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * up);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) *(float4*)(v + 4 * k) = __ldcg(part_of(x) + (8 * q + k) * kPromptRows + row);
@@ -529,11 +515,111 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
         // =============================== unpacking: a thread has half a row of two keys, 64 apart ====
         // so that a half of V's keys is unpacked while products still read the other
         set_registers<Sh::kUnpackRegs, Sh::kLaunchRegs>();
+        int64_t left = 0;  // tiles of this run
+        for (PromptSegment s = seg;;) {
+            left += max(0, end_of(s) - first_of(s));
+            if (s.end >= r1) break;
+            prompt_next(work, s);
+        }
+        if constexpr (kEight) {
+            // Pieces of 16 codes: eight lanes read a row of 128 (four one of 64), the warps 16 rows (32) at a time.
+            constexpr int kLanes = D / 16, kStep = 128 / kLanes, kTurns = kPromptKeys / kStep;
+            const int thread = tid & 127, piece = thread % kLanes, key0 = thread / kLanes, unpacker = warp - Sh::kUnpack;
+            uint4 k[kTurns], v[kTurns];  // K of tile n, V of tile n - 1
+            uint32_t ex = 0u;            // lanes 0 and 1: exponents of blocks 2 unpacker, 2 unpacker + 1
+            uint32_t there = 0u;         // which keys of this warp's word are there
+            int32_t blocks[8], count = 0;
+            auto places_of = [&](uint32_t t) {
+                const volatile int32_t* const from = places[t & 3];
+                count = from[8];
+#pragma unroll
+                for (int b = 0; b < 8; ++b) blocks[b] = from[b];
+            };
+            auto load = [&](uint4* x, int codes) {
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int key = key0 + kStep * i, block = D == 128 ? blocks[i] : key0 >> 4 ? blocks[2 * i + 1] : blocks[2 * i];
+                    const bool here = block >= 0 && key < count;
+                    x[i] = here ? *(const uint4*)((const char*)a.cache.pages + (int64_t)block * B::kBytes + codes + B::at(key & 15, piece)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto look = [&]() {  // of the tile whose places are at hand
+                int low = -1, high = -1;
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    if (w == unpacker) low = blocks[2 * w], high = blocks[2 * w + 1];
+                const int keys = min(max(count - 32 * unpacker, 0), 32);
+                there = ((low >= 0 ? 0xffffu : 0u) | (high >= 0 ? 0xffff0000u : 0u)) & (keys == 32 ? 0xffffffffu : (1u << keys) - 1u);
+                const int block = lane == 0 ? low : high;
+                ex = 0u;
+                if (lane < 2 && block >= 0 && 16 * lane < keys) ex = *(const uint32_t*)((const char*)a.cache.pages + (int64_t)block * B::kBytes + B::kExponents);
+            };
+            auto unpack = [&](const uint4& c, int key, uint32_t to) {
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int e = x ^ (piece >> 2 & 1);  // panels are as far apart as all banks: their pieces take turns
+                    uint32_t h[4];
+                    from_e4m3x4(e ? w[2] : w[0], h[0], h[1]);
+                    from_e4m3x4(e ? w[3] : w[1], h[2], h[3]);
+                    sts_v4(to + (piece >> 2) * Sh::kPanel + key * 128 + ((((piece & 3) * 2 + e) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
+                }
+            };
+            uint32_t now_there = 0u, now_ex = 0u;
+            if (left > 0) {
+                ok = wait(place_full, 0);
+                if (ok) {
+                    places_of(0);
+                    load(k, 0);
+                    look();
+                }
+            }
+#pragma unroll 1
+            for (int64_t tile = 0; ok && tile <= left && left > 0; ++tile) {
+                const uint32_t t = (uint32_t)tile, stage = t & 1;
+                if (tile < left) {
+                    now_there = there, now_ex = ex;
+                    if (lane < 2) exponents[t & 3][2 * unpacker + lane] = make_int2(kv8_exponent(now_ex, 0), kv8_exponent(now_ex, 1));
+                    if (lane == 0) seen_words[t & 3][unpacker] = now_there;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(seen_full + 8 * (t & 3));
+                    if (tile >= 2) ok = wait(k_empty + 8 * stage, (t >> 1) - 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < kTurns; ++i) unpack(k[i], key0 + kStep * i, smem + Sh::kK + stage * Sh::kParts * Sh::kTile);
+                    fence_proxy_async_smem();
+                    mbar_arrive(k_full + 8 * stage);
+                    if (tile + 1 < left) {
+                        ok = wait(place_full + 8 * ((t + 1) & 3), (t + 1) >> 2);
+                        if (!ok) break;
+                        places_of(t + 1);
+                        load(k, 0);
+                        look();
+                    }
+                }
+                if (tile > 0) {  // V of the tile before
+#pragma unroll
+                    for (int i = 0; i < kTurns; ++i) {
+                        if (i % (kTurns / 2) == 0 && tile > 1) ok = ok && wait(v_empty + 8 * (i / (kTurns / 2)), t - 2);
+                        if (ok) unpack(v[i], key0 + kStep * i, smem + Sh::kV);
+                    }
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    for (int i = 0; i < TILES; ++i) mbar_arrive(pv_full + 8 * i);
+                }
+                if (tile < left) {
+                    places_of(t);
+                    load(v, B::kV);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(place_empty + 8 * (t & 3));
+                }
+            }
+        } else {
         const int unpacker = warp - Sh::kUnpack, side = unpacker >> 1, key_in = 32 * (unpacker & 1) + lane;
-        constexpr int kLoads = D * F::kBits / 256;  // 16-byte loads of half a row of codes
+        constexpr int kLoads = D / 64;  // 16-byte loads of half a row of codes
         struct Codes {  // of half a row, and the row's scales
             uint4 c[kLoads];
-            uint32_t s[kEight ? 1 : J / 2];
+            uint32_t s[J / 2];
         };
         struct Places {  // the keys' blocks; null if they are not there
             const char* block[2];
@@ -556,41 +642,18 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool here = at.block[i] != nullptr;
-                if constexpr (kEight) {
-#pragma unroll
-                    for (int k = 0; k < kLoads; ++k)
-                        x[i].c[k] = here ? *(const uint4*)(at.block[i] + codes + B::at(row, side * kLoads + k)) : make_uint4(0u, 0u, 0u, 0u);
-                    x[i].s[0] = 0u;
-                    if (codes == 0 && side == 0 && row == 0 && here) x[i].s[0] = *(const uint32_t*)(at.block[i] + scales);
-                } else {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k)
                     x[i].c[k] = here ? *((const uint4*)(at.block[i] + codes + row * B::kRow + side * (B::kRow / 2)) + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int k = 0; k < J / 2; ++k)
                     x[i].s[k] = here ? *((const uint32_t*)(at.block[i] + scales + row * B::kScaleRow) + k) : 0u;
-                }
             }
         };
         // Half a row's codes as binary16 into their place of a swizzled tile; with_rest twice as large, and the part that
         // rounding lost into `rest`.
         const uint32_t row_at = key_in * 128;
         auto unpack = [&](const Codes& x, uint32_t to, uint32_t rest, auto with_rest) {
-            if constexpr (kEight) {
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const int piece = side * kLoads + k;  // 16 channels: two 16-byte pieces of a row of 64
-                    const uint32_t w[4] = {x.c[k].x, x.c[k].y, x.c[k].z, x.c[k].w};
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t h[4];
-                        from_e4m3x4(w[2 * e], h[0], h[1]);
-                        from_e4m3x4(w[2 * e + 1], h[2], h[3]);
-                        sts_v4(to + (piece >> 2) * Sh::kPanel + row_at + ((((piece & 3) * 2 + e) ^ (key_in & 7)) << 4), h[0], h[1], h[2], h[3]);
-                    }
-                }
-                return;
-            } else {
             uint32_t wd[4 * kLoads];
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) wd[4 * k] = x.c[k].x, wd[4 * k + 1] = x.c[k].y, wd[4 * k + 2] = x.c[k].z, wd[4 * k + 3] = x.c[k].w;
@@ -620,23 +683,14 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                         }
                     }
                 }
-            }
         };
         constexpr uint32_t kHalf = 64 * 128;  // from a tile's first key to its 65th
-        int64_t left = 0;  // tiles of this run
-        for (PromptSegment s = seg;;) {
-            left += max(0, end_of(s) - first_of(s));
-            if (s.end >= r1) break;
-            prompt_next(work, s);
-        }
         // K is unpacked a tile ahead of V: its two stages are free before V's one
-        constexpr int kScalesK = [] { if constexpr (kEight) return B::kExponents; else return B::kScaleK; }();
-        constexpr int kScalesV = [] { if constexpr (kEight) return B::kExponents; else return B::kScaleV; }();
         Codes k[2], v[2];        // K of tile n, V of tile n - 1
         Places here = {{nullptr, nullptr}};  // of tile n
         if (left > 0) {
             here = places_of(0);
-            load(k, here, 0, kScalesK);
+            load(k, here, 0, B::kScaleK);
         }
 #pragma unroll 1
         for (int64_t tile = 0; ok && tile <= left && left > 0; ++tile) {
@@ -644,13 +698,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             const uint32_t t = (uint32_t)tile, stage = t & 1;
             if (tile < left) {
                 const uint32_t there = __ballot_sync(0xffffffffu, (side == 0 ? now.block[0] : now.block[1]) != nullptr);
-                if constexpr (kEight) {
-                    if (side == 0 && row == 0)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            exponents[t & 3][key_in / kKvBlockTokens + 4 * i] = make_int2(kv8_exponent(k[i].s[0], 0), kv8_exponent(k[i].s[0], 1));
-                    __syncwarp();
-                }
                 if (lane == 0) {
                     seen_words[t & 3][unpacker] = there;
                     mbar_arrive(seen_full + 8 * (t & 3));
@@ -665,7 +712,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                 if (tile + 1 < left) {
                     here = places_of(t + 1);
                     if (!ok) break;
-                    load(k, here, 0, kScalesK);
+                    load(k, here, 0, B::kScaleK);
                 }
             }
             if (tile > 0) {  // V of the tile before
@@ -679,7 +726,8 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                 fence_proxy_async_smem();
                 for (int i = 0; i < TILES; ++i) mbar_arrive(pv_full + 8 * i);
             }
-            if (tile < left) load(v, now, B::kV, kScalesV);
+            if (tile < left) load(v, now, B::kV, B::kScaleV);
+        }
         }
     } else {
         // =============================== products of tile i: one thread issues ====
