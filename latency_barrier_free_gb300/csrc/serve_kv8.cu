@@ -6,7 +6,7 @@
 // prompt: one in 16; a decode step: each), then its warps share runs x heads x 2.
 // A run's values stay in registers from their maximum to their codes.
 //
-// Read.  A warp's lanes take 8 channels each of a row.
+// Read.  A thread takes 8 channels of a row of K, and of V (16: 11.0 us against 7.9 for 8754 tokens of 8 heads of 128).
 #include <algorithm>
 
 #include "serve_common.cuh"
@@ -33,17 +33,55 @@ __device__ __forceinline__ char* kv8_block(const Kv8Params& p, int64_t slot, int
     return (char*)c.pages + ((int64_t)(page * c.kv_heads + h) * p.by_page.d + (at - page * p.by_page.d)) * B::kBytes;
 }
 
-// Eight channels as binary32.
-__device__ __forceinline__ void kv8_load(const float* from, float* x) {
-    const float4 a = __ldcs((const float4*)from), b = __ldcs((const float4*)from + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void kv8_load(const __nv_bfloat16* from, float* x) {
-    const uint4 v = __ldcs((const uint4*)from);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight channels as they are in memory.
+template <typename T>
+struct Kv8Raw;
+template <>
+struct Kv8Raw<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float* from) {
+        const float4 a = __ldcs((const float4*)from), b = __ldcs((const float4*)from + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-}
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    __device__ __forceinline__ float get(int i) const { return x[i]; }
+    __device__ __forceinline__ float most() const {  // NaN counts for nothing
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+        return m;
+    }
+    __device__ __forceinline__ bool odd() const {  // whether some may be NaN
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += x[i] * 0.f;
+        return sum != 0.f;  // NaN or infinity: 0 times it is NaN
+    }
+};
+template <>
+struct Kv8Raw<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* from) {
+        const uint4 v = __ldcs((const uint4*)from);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16); }
+    __device__ __forceinline__ float most() const {
+        const __nv_bfloat162* const h = (const __nv_bfloat162*)w;
+        const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+        return fmaxf(__low2float(m), __high2float(m));  // NaN counts for nothing
+    }
+    __device__ __forceinline__ bool odd() const {
+        uint32_t any = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= ((w[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        return any != 0u;
+    }
+};
 __device__ __forceinline__ void kv8_store(float* to, const float* x) {
     __stcs((float4*)to, make_float4(x[0], x[1], x[2], x[3]));
     __stcs((float4*)to + 1, make_float4(x[4], x[5], x[6], x[7]));
@@ -73,159 +111,191 @@ __device__ __forceinline__ int kv8_exponent_of(float most) {
     return min(max(e, kKv8Low), kKv8High);  // most = 0 and its neighbours end up at the lower one
 }
 
+// The next tokens of a run from `at` on, up to 16, into picks as token * 16 + row; skipped slots between them do not end it.
+// Where there are more (the same slots over and over), `at` becomes the next one's place and `more` true.  A whole warp.
+__device__ __forceinline__ int kv8_gather(const Kv8Params& p, int64_t& at, bool& more, int32_t* picks, const int64_t* slots, int64_t t0) {
+    const int lane = (int)threadIdx.x & 31;
+    int n = 0;
+    int64_t block = -1;
+    more = false;
+    for (;; at += 32) {
+        const int64_t t = at + lane, s = t - t0 < kKv8Span + kKvBlockTokens ? slots[t - t0] : t < p.a.tokens ? p.a.slots[t] : -1;
+        if (block < 0) block = __shfl_sync(0xffffffffu, s, 0) >> 4;  // the first is inside the cache
+        const bool valid = (uint64_t)s < (uint64_t)p.room, same = valid && s >> 4 == block;
+        const uint32_t ends = __ballot_sync(0xffffffffu, (valid && !same) || t >= p.a.tokens);
+        const uint32_t in = __ballot_sync(0xffffffffu, same) & ((ends & (0u - ends)) - 1u);
+        const int place = n + __popc(in & ((1u << lane) - 1u));
+        const bool mine = in >> lane & 1u;
+        if (mine && place < kKvBlockTokens) picks[place] = (int32_t)t * kKvBlockTokens + ((int32_t)s & (kKvBlockTokens - 1));
+        const uint32_t over = __ballot_sync(0xffffffffu, mine && place == kKvBlockTokens);
+        n += __popc(in);
+        if (over != 0u) {
+            at += __ffs((int)over) - 1;
+            more = true;
+            break;
+        }
+        if (ends != 0u) break;
+    }
+    __syncwarp();
+    return min(n, kKvBlockTokens);
+}
+
+// A run of a CTA: its slot, its first tokens, and where it goes on (-1: it does not).
+struct Kv8Run {
+    int64_t slot, more;
+    int32_t length;
+    uint32_t rows;  // which rows it writes
+    int32_t picks[kKvBlockTokens];
+};
+
+// The codes that are there, in a unit 2^k as large.
+__device__ __forceinline__ void kv8_round_again(char* codes, int vectors, int k) {
+    const float down = two_to(-k);
+    for (int i = (int)threadIdx.x & 31; i < vectors; i += 32) {
+        uint4 c = *((uint4*)codes + i);
+        uint32_t* const w = (uint32_t*)&c;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            uint32_t low, high;
+            from_e4m3x4(w[x], low, high);
+            const float2 y = __half22float2(*(const __half2*)&low), z = __half22float2(*(const __half2*)&high);
+            w[x] = to_e4m3x4(y.x * down, y.y * down, z.x * down, z.y * down);
+        }
+        *((uint4*)codes + i) = c;
+    }
+    __syncwarp();
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kKv8Threads) kv8_append_kernel(const __grid_constant__ Kv8Params p) {
+__global__ void __launch_bounds__(kKv8Threads, sizeof(T) == 2 ? 4 : 2) kv8_append_kernel(const __grid_constant__ Kv8Params p) {
     using B = Kv8Block<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows that a warp takes at once
     constexpr int kHeld = kKvBlockTokens / kRows;       // rows of a lane
     __shared__ int64_t slots[kKv8Span + kKvBlockTokens];
-    __shared__ int runs[kKv8Span], count;
-    __shared__ int32_t picks[kKv8Threads / 32][kKvBlockTokens];
+    __shared__ Kv8Run runs[kKv8Span];
+    __shared__ int firsts[kKv8Span], count;
+    __shared__ int32_t again[kKv8Threads / 32][kKvBlockTokens];  // tokens behind a run's first 16
     const rra_kv_tokens_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * p.span;
     const int h0 = (int)blockIdx.y * p.heads, heads = min(p.heads, a.cache.kv_heads - h0);
     pdl_release_early();
     pdl_wait();
-    // ---- the runs that begin among this CTA's tokens; the slots of those and of 16 more ----
+    // ---- the runs that begin among this CTA's tokens ----
     if (warp == 0) {
-        const bool mine = lane < p.span && t0 + lane < a.tokens;
         const int64_t slot = t0 + lane < a.tokens ? a.slots[t0 + lane] : -1;
+        int64_t s = t0 - 32 + lane >= 0 ? a.slots[t0 - 32 + lane] : -1;
         slots[lane] = slot;
         const bool inside = (uint64_t)slot < (uint64_t)p.room;
         // the slot before, not counting those that are skipped; -1: none
         const uint32_t valid = __ballot_sync(0xffffffffu, inside), lower = valid & ((1u << lane) - 1u);
         int64_t left = __shfl_sync(0xffffffffu, slot, 31 - __clz((int)(lower | 1u)));
         int64_t earlier = -1;
-        for (int64_t t = t0 - 32; valid != 0u && t > -32; t -= 32) {
-            const int64_t s = t + lane >= 0 ? a.slots[t + lane] : -1;
+        for (int64_t t = t0 - 32; valid != 0u; t -= 32) {
             const uint32_t there = __ballot_sync(0xffffffffu, (uint64_t)s < (uint64_t)p.room);
-            if (there == 0u) continue;
-            earlier = __shfl_sync(0xffffffffu, s, 31 - __clz((int)there));
-            break;
+            earlier = there != 0u ? __shfl_sync(0xffffffffu, s, 31 - __clz((int)there)) : -1;
+            if (there != 0u || t <= 0) break;
+            s = t - 32 + lane >= 0 ? a.slots[t - 32 + lane] : -1;
         }
         if (lower == 0u) left = earlier;
-        const bool begins = mine && inside && (left < 0 || left / kKvBlockTokens != slot / kKvBlockTokens);
+        const bool begins = lane < p.span && inside && (left < 0 || left >> 4 != slot >> 4);
         const uint32_t who = __ballot_sync(0xffffffffu, begins);
-        if (begins) runs[__popc(who & ((1u << lane) - 1u))] = lane;
+        if (begins) firsts[__popc(who & ((1u << lane) - 1u))] = lane;
         if (lane == 0) count = __popc(who);
     }
     __syncthreads();
-    const int items = count * heads * 2;
+    for (int r = warp; r < count; r += kKv8Threads / 32) {
+        Kv8Run& run = runs[r];
+        int64_t at = t0 + firsts[r];
+        bool more;
+        const int n = kv8_gather(p, at, more, run.picks, slots, t0);
+        const uint32_t row = lane < n ? 1u << (run.picks[lane] & (kKvBlockTokens - 1)) : 0u, rows = __reduce_or_sync(0xffffffffu, row);
+        if (lane == 0) run.slot = slots[firsts[r]], run.more = more ? at : -1, run.length = n, run.rows = rows;
+    }
+    __syncthreads();
     const int sub = lane / kLanes, m = lane % kLanes;  // this lane's row of those that the warp takes at once, and its eight channels
+    const int items = count * heads * 2;
     for (int item = warp; item < items; item += kKv8Threads / 32) {
         const int v = item & 1, r = (item >> 1) / heads, h = h0 + (item >> 1) - r * heads;
-        const int first = runs[r];
-        const int64_t in_block = slots[first] / kKvBlockTokens;
-        char* const block = kv8_block<B>(p, slots[first], h);
+        const Kv8Run& run = runs[r];
+        char* const block = kv8_block<B>(p, run.slot, h);
         char* const codes = block + v * B::kV;
-        const T* const from = v ? (const T*)a.v + h * a.v_head_stride : (const T*)a.k + h * a.k_head_stride;
+        const T* const from = (v ? (const T*)a.v + h * a.v_head_stride : (const T*)a.k + h * a.k_head_stride) + 8 * m;
         const int64_t stride = v ? a.v_token_stride : a.k_token_stride;
-        const uint32_t held = *(const uint32_t*)(block + B::kExponents);
-        // The next tokens of the run from `at` on, up to 16, into pick; skipped slots between them do not end it.  Where there
-        // are more (the same slots over and over), `at` becomes the next one's place and `more` true.
-        int32_t* const pick = picks[warp];
-        auto gather = [&](int64_t& at, bool& more) {
-            int n = 0;
-            more = false;
-            __syncwarp();
-            for (;; at += 32) {
-                const int64_t t = at + lane, s = t - t0 < kKv8Span + kKvBlockTokens ? slots[t - t0] : t < a.tokens ? a.slots[t] : -1;
-                const bool valid = (uint64_t)s < (uint64_t)p.room, same = valid && s / kKvBlockTokens == in_block;
-                const uint32_t ends = __ballot_sync(0xffffffffu, (valid && !same) || t >= a.tokens);
-                const uint32_t in = __ballot_sync(0xffffffffu, same) & ((ends & (0u - ends)) - 1u);
-                const int place = n + __popc(in & ((1u << lane) - 1u));
-                const bool mine = in >> lane & 1u;
-                if (mine && place < kKvBlockTokens) pick[place] = (int32_t)t;
-                const uint32_t over = __ballot_sync(0xffffffffu, mine && place == kKvBlockTokens);
-                n += __popc(in);
-                if (over != 0u) {
-                    at += __ffs((int)over) - 1;
-                    more = true;
-                    break;
-                }
-                if (ends != 0u) break;
-            }
-            __syncwarp();
-            return min(n, kKvBlockTokens);
-        };
-        const int64_t run = t0 + first;
-        int64_t next = run;
-        bool repeats;
-        const int length = gather(next, repeats);
-        float x[kHeld][8];
-        uint32_t rows = 0;      // where this lane's tokens go, 4 bits each
-        float most = 0.f;
-        uint32_t starts = 0;    // is the block's first token among them
-        auto take = [&](int n) {  // the tokens in pick: their values, what is largest of them
+        Kv8Raw<T> x[kHeld];
+        auto take = [&](const int32_t* picks, int n) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-                const int k = i * kRows + sub;
-                if (k < n) {
-                    const int64_t t = pick[k];
-                    kv8_load(from + t * stride + 8 * m, x[i]);
-                    const int row = (int)(t - t0 < kKv8Span + kKvBlockTokens ? slots[t - t0] : a.slots[t]) & (kKvBlockTokens - 1);
-                    rows = (rows & ~(15u << (4 * i))) | (uint32_t)row << (4 * i);
-                    starts |= row == 0 ? 1u : 0u;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) x[i][c] = 0.f;
-                }
+                if (i * kRows + sub < n) x[i].load(from + (picks[i * kRows + sub] >> 4) * stride);
+                else x[i].clear();
             }
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    x[i][c] = x[i][c] == x[i][c] ? x[i][c] : 0.f;  // NaN is stored as 0
-                    const float size = fabsf(x[i][c]);
-                    if (size < INFINITY) most = fmaxf(most, size);
-                }
         };
-        take(length);
-        if (repeats) {  // all others are looked at before any is written
-            int64_t at = next;
-            for (bool more = true; more;) take(gather(at, more));
-            at = run;
-            take(gather(at, repeats));
+        bool odd = false;  // NaN or infinity: rare
+        auto most_of = [&]() {
+            odd = false;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) odd |= x[i].odd();
+            float most = 0.f;
+            if (!odd) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) most = fmaxf(most, x[i].most());
+            } else {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float size = fabsf(x[i].get(c));
+                        if (size < INFINITY) most = fmaxf(most, size);
+                    }
+            }
+            return most;
+        };
+        take(run.picks, run.length);
+        const int old = kv8_exponent(*(const uint32_t*)(block + B::kExponents), v);
+        float most = most_of();
+        bool anew = (run.rows & 1u) != 0u;
+        if (run.more >= 0) {  // all others are looked at before any is written
+            int64_t at = run.more;
+            for (bool more = true; more;) {
+                const int n = kv8_gather(p, at, more, again[warp], slots, t0);
+                anew |= __any_sync(0xffffffffu, lane < n && (again[warp][lane & 15] & 15) == 0);
+                take(again[warp], n);
+                most = fmaxf(most, most_of());
+                __syncwarp();
+            }
+            take(run.picks, run.length);
+            most = fmaxf(most, most_of());
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const int old = kv8_exponent(held, v);
-        const bool anew = __any_sync(0xffffffffu, starts != 0u);
         int e = kv8_exponent_of(most);
         if (!anew) e = max(e, old);
-        if (!anew && e > old) {  // the codes that are there, in the new unit
-            const float down = two_to(old - e);
-            for (int i = lane; i < D; i += 32) {  // 16 bytes each
-                uint4 c = *((uint4*)codes + i);
-                uint32_t* const w = (uint32_t*)&c;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t low, high;
-                    from_e4m3x4(w[k], low, high);
-                    const float2 y = __half22float2(*(const __half2*)&low), z = __half22float2(*(const __half2*)&high);
-                    w[k] = to_e4m3x4(y.x * down, y.y * down, z.x * down, z.y * down);
-                }
-                *((uint4*)codes + i) = c;
-            }
-            __syncwarp();
-        }
+        if (!anew && e > old) kv8_round_again(codes, D, e - old);
         const float by = two_to(-e);
-        auto put = [&](int n) {
+        auto put = [&](const int32_t* picks, int n) {
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 if (i * kRows + sub >= n) continue;
-                const int row = (int)(rows >> (4 * i)) & 15;
-                *(uint2*)(codes + B::at(row, m >> 1) + 8 * (m & 1)) =
-                    make_uint2(to_e4m3x4(x[i][0] * by, x[i][1] * by, x[i][2] * by, x[i][3] * by),
-                               to_e4m3x4(x[i][4] * by, x[i][5] * by, x[i][6] * by, x[i][7] * by));
+                float y[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) y[c] = x[i].get(c) * by;
+                if (odd)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) y[c] = y[c] == y[c] ? y[c] : 0.f;  // NaN is stored as 0
+                *(uint2*)(codes + B::at(picks[i * kRows + sub] & (kKvBlockTokens - 1), m >> 1) + 8 * (m & 1)) =
+                    make_uint2(to_e4m3x4(y[0], y[1], y[2], y[3]), to_e4m3x4(y[4], y[5], y[6], y[7]));
             }
         };
-        put(length);
-        for (bool more = repeats; more;) {
-            const int n = gather(next, more);
-            take(n);
-            put(n);
+        put(run.picks, run.length);
+        if (run.more >= 0) {
+            int64_t at = run.more;
+            for (bool more = true; more;) {
+                const int n = kv8_gather(p, at, more, again[warp], slots, t0);
+                take(again[warp], n);
+                most_of();
+                put(again[warp], n);
+                __syncwarp();
+            }
         }
         if (lane == 0) *(int8_t*)(block + B::kExponents + v) = (int8_t)e;
     }
