@@ -377,6 +377,7 @@ rra_status_t rra_prompt_attention_plan(const rra_prompt_attention_args_t* args, 
  * same buffer; nothing else overlaps.  Each call is one kernel and moves no page:
  * fork and compact write lists for rra_pages_copy, which is called for the pages
  * of every layer.
+ * requests 0..RRA_SERVE_MAX_REQUESTS; num_pages up to 2^24.
  *
  * rra_pages_fork: for i < forks, row target[i] becomes a copy of row source[i]:
  *   its whole pages are shared (shared + 1 for each), and a page of its own is

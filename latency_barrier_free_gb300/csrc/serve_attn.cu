@@ -25,8 +25,8 @@ namespace rra {
 
 constexpr double kLog2E = 1.4426950408889634;
 constexpr int kAttnMinRun = 1;     // tiles a warp takes at least
-constexpr int kAttnSegmentCost = 4;  // what starting and ending a segment costs, in tiles
-
+constexpr int kAttnSegmentCost = 4;  // what starting and ending a segment costs, in tiles of 32 keys
+constexpr int segment_cost(int blocks) { return kAttnSegmentCost * 2 / blocks; }  // in tiles of so many blocks of 16
 
 // The queries and keys of request b, clamped to the buffers.
 struct AttnRequest {
@@ -36,14 +36,15 @@ struct AttnRequest {
     int32_t tiles;        // tiles of one segment, at least one
     int32_t chunks;       // segments of a KV head
 };
-template <int kRows>
+template <int kRows, int NB>
 __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, const AttnLengths& n) {
+    constexpr int kKeys = NB * kKvBlockTokens;
     AttnRequest r;
     r.q0 = n.q0;
     r.qn = n.qn;
     r.kv = n.kv;
-    r.first_tile = (p.window > 0 ? max(0, r.kv - r.qn - p.window + 1) : 0) / kAttnTile;
-    r.tiles = max(1, (r.kv + kAttnTile - 1) / kAttnTile - r.first_tile);
+    r.first_tile = (p.window > 0 ? max(0, r.kv - r.qn - p.window + 1) : 0) / kKeys;
+    r.tiles = max(1, (r.kv + kKeys - 1) / kKeys - r.first_tile);
     r.chunks = (r.qn * p.group + kRows - 1) / kRows;
     return r;
 }
@@ -56,7 +57,7 @@ struct AttnSegment {
     int64_t begin, end;
 };
 // `known`: the first requests' lengths, n of them, in shared memory.
-template <int kRows>
+template <int kRows, int NB>
 __device__ __noinline__ void attn_next(const AttnParams& p, const AttnLengths* known, int n, AttnSegment& s) {  // out of line: once a segment, in two places
     if (++s.c >= s.r.chunks) {
         s.c = 0;
@@ -67,12 +68,12 @@ __device__ __noinline__ void attn_next(const AttnParams& p, const AttnLengths* k
                     s.begin = s.end = INT64_MAX;
                     return;
                 }
-                s.r = attn_request<kRows>(p, s.b < n ? known[s.b] : attn_lengths(p, s.b));
+                s.r = attn_request<kRows, NB>(p, s.b < n ? known[s.b] : attn_lengths(p, s.b));
             } while (s.r.chunks == 0);
         }
     }
     s.begin = s.end;
-    s.end += s.r.tiles + kAttnSegmentCost;
+    s.end += s.r.tiles + segment_cost(NB);
 }
 
 // x / y, which fits 32 bits; mostly x does too, and then the division is a short one.
@@ -89,12 +90,13 @@ struct AttnPiece {
 };
 enum { kHas = 1, kStarts = 2, kEnds = 4 };
 
-template <typename F, int D, int NT, int kWarps, int kStages>
+// NB: blocks of 16 keys that a warp takes at a time, a stage of its ring.
+template <typename F, int D, int NT, int kWarps, int kStages, int NB>
 struct AttnShape {
     using B = typename F::template Block<D>;
     static constexpr int kRows = 8 * NT;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStage = 2 * B::kBytes;
+    static constexpr int kStage = NB * B::kBytes;
     static constexpr int kPartial = kRows * (D + 2);           // floats of a piece: maximum and sum of each row, rows
     static constexpr int kRing = kWarps * kStages * kStage;    // a warp's last piece goes where its ring was
     static constexpr int kHeads = kWarps * kPartial * 4;       // a warp's first piece
@@ -114,9 +116,9 @@ __device__ __forceinline__ void attn_add(float top, float& sum, float4& o, float
     o.w = fmaf(v.w, by, o.w);
 }
 
-template <typename F, int D, int NT, int kWarps, int kStages>
+template <typename F, int D, int NT, int kWarps, int kStages, int NB>
 __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = AttnShape<F, D, NT, kWarps, kStages>;
+    using Sh = AttnShape<F, D, NT, kWarps, kStages, NB>;
     using B = typename F::template Block<D>;
     constexpr int J = D / 32, kRows = Sh::kRows;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -158,8 +160,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
         if (b < a.requests) {
             const AttnLengths n = attn_lengths(p, b);
             if (b0 == 0) known[tid] = n;
-            const AttnRequest r = attn_request<kRows>(p, n);
-            v = (int64_t)(r.tiles + kAttnSegmentCost) * r.chunks * a.cache.kv_heads;
+            const AttnRequest r = attn_request<kRows, NB>(p, n);
+            v = (int64_t)(r.tiles + segment_cost(NB)) * r.chunks * a.cache.kv_heads;
         }
         int64_t inc = v;
 #pragma unroll
@@ -206,8 +208,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 else high = mid;
             }
             seg.b = low;
-            seg.r = attn_request<kRows>(p, low < Sh::kThreads ? known[low] : attn_lengths(p, low));
-            const int each = seg.r.tiles + kAttnSegmentCost;
+            seg.r = attn_request<kRows, NB>(p, low < Sh::kThreads ? known[low] : attn_lengths(p, low));
+            const int each = seg.r.tiles + segment_cost(NB);
             const int i = quotient(r0 - sums[low], each);
             seg.h = i / seg.r.chunks;
             seg.c = i - seg.h * seg.r.chunks;
@@ -215,11 +217,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             seg.end = seg.begin + each;
         }
         auto first_tile = [&](const AttnSegment& s) {
-            const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - kAttnSegmentCost;
+            const int64_t from = (s.begin > r0 ? s.begin : r0) - s.begin - segment_cost(NB);
             return (int)(from > 0 ? from : 0);
         };
         auto end_tile = [&](const AttnSegment& s) {
-            const int64_t to = (s.end < r1 ? s.end : r1) - s.begin - kAttnSegmentCost;
+            const int64_t to = (s.end < r1 ? s.end : r1) - s.begin - segment_cost(NB);
             return (int)(to > 0 ? to : 0);
         };
 
@@ -243,11 +245,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
             if (held >= held_end) {
                 while (next >= from_end) {
                     if (from.end >= r1) return;
-                    attn_next<kRows>(p, known, Sh::kThreads, from);
+                    attn_next<kRows, NB>(p, known, Sh::kThreads, from);
                     next = first_tile(from);
                     from_end = end_tile(from);
                 }
-                const int key = (from.r.first_tile + next + lane) * kAttnTile;
+                const int key = (from.r.first_tile + next + lane) * (NB * kKvBlockTokens);
                 const int32_t* const row = a.block_table + from.b * a.table_stride;
                 src0 = src1 = nullptr;
                 auto place = [&](int k) -> const char* {
@@ -258,9 +260,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                            (((int64_t)page * a.cache.kv_heads + from.h) * blocks + (k - i * ps) / kKvBlockTokens) * B::kBytes;
                 };
                 src0 = place(key);
-                src1 = place(key + kKvBlockTokens);
+                if (NB == 2) src1 = place(key + kKvBlockTokens);
                 ok0 = __ballot_sync(0xffffffffu, src0 != nullptr);
-                ok1 = __ballot_sync(0xffffffffu, src1 != nullptr);
+                if (NB == 2) ok1 = __ballot_sync(0xffffffffu, src1 != nullptr);
                 held = 0;
                 held_end = min(32, from_end - next);
                 next += held_end;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 const uint32_t bar = bars + 8 * put, dst = ring + put * Sh::kStage;
                 const bool h0 = src0 != nullptr, h1 = src1 != nullptr;
                 mbar_expect_tx(bar, ((h0 ? 1u : 0u) + (h1 ? 1u : 0u)) * (uint32_t)B::kBytes);
-                if (h0 && src1 == src0 + B::kBytes) {
+                if (NB == 2 && h0 && src1 == src0 + B::kBytes) {
                     bulk_g2s(dst, src0, 2 * B::kBytes, bar);
                 } else {
                     if (h0) bulk_g2s(dst, src0, B::kBytes, bar);
@@ -305,9 +307,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                 phase ^= 1u << take;
                 const uint32_t have = dead ? 0u : (valid >> (2 * take)) & 3u;
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < NB; ++i)
                     if (have >> i & 1u)
-                        att.block(tile + i * B::kBytes, (seg.r.first_tile + tl) * kAttnTile + kKvBlockTokens * i);
+                        att.block(tile + i * B::kBytes, ((seg.r.first_tile + tl) * NB + i) * kKvBlockTokens);
                 take = take + 1 == kStages ? 0 : take + 1;
                 __syncwarp();  // every lane has read the stage
                 if (!dead) copy_next();
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
                     }
                 }
             if (seg.end >= r1) break;
-            attn_next<kRows>(p, known, Sh::kThreads, seg);
+            attn_next<kRows, NB>(p, known, Sh::kThreads, seg);
             load_queries();
         }
         if (dead) drain();  // copies in flight at this point: none, or those that a wait gave up on
@@ -506,10 +508,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_kernel(const __gr
     }
 }
 
-template <typename F, int D, int NT, int kWarps, int kStages>
+template <typename F, int D, int NT, int kWarps, int kStages, int NB = 2>
 static rra_status_t attn_launch(const AttnParams& p, int ctas, rra_stream_t stream) {
-    using Sh = AttnShape<F, D, NT, kWarps, kStages>;
-    const void* k = (const void*)kv_attention_kernel<F, D, NT, kWarps, kStages>;
+    using Sh = AttnShape<F, D, NT, kWarps, kStages, NB>;
+    const void* k = (const void*)kv_attention_kernel<F, D, NT, kWarps, kStages, NB>;
     static_assert(Sh::kFixed + 8 * (RRA_SERVE_MAX_REQUESTS + 1) <= 227 * 1024 - 10240, "shared memory");
     if (configure_cluster_kernel(k, (int)Sh::smem(RRA_SERVE_MAX_REQUESTS)) != cudaSuccess) {
         cudaGetLastError();
@@ -624,7 +626,7 @@ static rra_status_t kv_attention(const rra_kv_attention_args_t* args, int bits, 
     const bool eight = kernel == rra::kRows8;
     if (bits == 8) {
         if (args->cache.head_dim == 128)
-            return eight ? rra::attn_launch<Cache8, 128, 1, 8, 2>(p, ctas, stream) : rra::attn_launch<Cache8, 128, 2, 6, 2>(p, ctas, stream);
+            return eight ? rra::attn_launch<Cache8, 128, 1, 12, 2, 1>(p, ctas, stream) : rra::attn_launch<Cache8, 128, 2, 6, 2>(p, ctas, stream);
         return eight ? rra::attn_launch<Cache8, 64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<Cache8, 64, 2, 8, 3>(p, ctas, stream);
     }
     if (args->cache.head_dim == 128)

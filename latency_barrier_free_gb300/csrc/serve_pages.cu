@@ -15,6 +15,7 @@ namespace rra {
 constexpr int kPagesThreads = 1024;
 constexpr int kPagesMaxCluster = 16;
 constexpr int kPagesMost = (1 << 30) - 1;  // tokens of a request
+constexpr int kPagesPool = 1 << 24;        // pages of a pool: a bit each in the cluster's shared memory
 
 __device__ __forceinline__ void pages_sync() {
     if (gridDim.x > 1) cluster_sync();
@@ -64,13 +65,24 @@ __device__ __forceinline__ void pages_meet(const int* mine, int& before, int& al
     }
 }
 
-// This CTA's share of n items: an equal run, in whole multiples of 4.
-__device__ __forceinline__ void pages_share(int n, int& begin, int& end) {
-    int64_t run = ((int64_t)n + gridDim.x - 1) / gridDim.x;
-    run = (run + 3) & ~(int64_t)3;
-    begin = (int)min((int64_t)n, run * blockIdx.x);
-    end = (int)min((int64_t)n, run * (blockIdx.x + 1));
-}
+// Pages as bits in the shared memory of the cluster: CTA x has the words of pages x * run .. (x + 1) * run.
+struct PageBits {
+    uint32_t* words;
+    int run, begin, end, count;  // pages of a CTA, this one's, its words
+    __device__ __forceinline__ PageBits(uint32_t* at, int n) : words(at) {
+        run = (int)(((int64_t)n + gridDim.x - 1) / gridDim.x + 31) & ~31;
+        begin = (int)min((int64_t)n, (int64_t)run * blockIdx.x);
+        end = min(n, begin + run);
+        count = (end - begin + 31) >> 5;
+        for (int i = (int)threadIdx.x; i < run >> 5; i += (int)blockDim.x) words[i] = 0u;
+    }
+    __device__ __forceinline__ void set(int page) const {
+        const uint32_t cta = (uint32_t)page / (uint32_t)run, in = (uint32_t)page - cta * (uint32_t)run;
+        const uint32_t at = smem_u32(words + (in >> 5)), bit = 1u << (in & 31);
+        if (gridDim.x == 1) atomicOr(words + (in >> 5), bit);
+        else asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" : : "r"(map_to_rank(at, cta)), "r"(bit) : "memory");
+    }
+};
 
 // ================================================================= fork ====
 struct ForkParams {
@@ -164,18 +176,20 @@ struct ReleaseParams {
 };
 
 __global__ void __launch_bounds__(kPagesThreads, 1) pages_release_kernel(const __grid_constant__ ReleaseParams p) {
+    extern __shared__ uint32_t bits_mem[];
     __shared__ int part[32], gone;
     const rra_pages_release_args_t& a = p.a;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, lane = tid & 31;
     const int me = (int)blockIdx.x * nt + tid, all = (int)gridDim.x * nt;
     pdl_release_early();
+    const PageBits bits(bits_mem, a.num_pages);  // pages that lose their last holder
     pdl_wait();
     const int count = min(max(a.free_count[0], 0), a.num_pages);
-    if (a.shared_out != a.shared) {
+    if (a.shared_out != a.shared)
         for (int i = me; i < a.num_pages; i += all) a.shared_out[i] = a.shared[i];
-        pages_sync();
-    }
-    // A holder less for every page of a request that ends; whoever takes the last one away leaves the count below 0.
+    pages_sync();
+    // A holder less for every page of a request that ends.  Whoever takes the last one away marks the page, and a page that is
+    // listed more often than held has its count put right at the end.
     for (int b = me >> 5; b < a.requests; b += all >> 5) {
         const int length = min(max(a.seq_len[b], 0), kPagesMost);
         const bool ends = a.new_len[b] < 0;
@@ -184,22 +198,20 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_release_kernel(const _
         if (!ends) continue;
         const int held = min(length > 0 ? p.by_page(length - 1) + 1 : 0, a.table_pages);
         const int32_t* const row = a.block_table + b * a.table_stride;
-        for (int j = lane; j < held; j += 32) {
-            const int page = row[j];
-            if (page >= 0 && page < a.num_pages) atomicSub(a.shared_out + page, 1);
+        constexpr int kAhead = 4;
+        for (int j0 = 0; j0 < held; j0 += 32 * kAhead) {
+            int page[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) page[k] = j0 + 32 * k + lane < held ? row[j0 + 32 * k + lane] : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (page[k] >= 0 && page[k] < a.num_pages && atomicSub(a.shared_out + page[k], 1) <= 0) bits.set(page[k]);
         }
     }
     pages_sync();
-    // Pages below 0 go back, in their order.  A thread has four neighbours.
-    int begin, end;
-    pages_share(a.num_pages, begin, end);
+    // Marked pages go back, in their order: a word a thread.
     int mine = 0;
-    for (int i0 = begin; i0 < end; i0 += nt * 4)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = i0 + 4 * tid + k;
-            if (i < end && __ldcg(a.shared_out + i) < 0) ++mine;
-        }
+    for (int i = tid; i < bits.count; i += nt) mine += __popc(bits.words[i]);
     int total, before, whole;
     pages_scan(mine, total, part);
     if (tid == 0) gone = total;
@@ -207,22 +219,14 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_release_kernel(const _
     pages_meet(&gone, before, whole);
     int at = count + before;
     if (total > 0)
-        for (int i0 = begin; i0 < end; i0 += nt * 4) {
-            uint32_t who = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = i0 + 4 * tid + k;
-                if (i < end && __ldcg(a.shared_out + i) < 0) who |= 1u << k;
-            }
+        for (int i0 = 0; i0 < bits.count; i0 += nt) {
+            uint32_t who = i0 + tid < bits.count ? bits.words[i0 + tid] : 0u;
             int some, rank = at + pages_scan(__popc(who), some, part);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (who >> k & 1u) {
-                    const int i = i0 + 4 * tid + k;
-                    if (rank < a.num_pages) a.free_pages[rank] = i;
-                    a.shared_out[i] = 0;
-                    ++rank;
-                }
+            for (; who != 0u; who &= who - 1u, ++rank) {
+                const int page = bits.begin + 32 * (i0 + tid) + __ffs((int)who) - 1;
+                if (rank < a.num_pages) a.free_pages[rank] = page;
+                a.shared_out[page] = 0;
+            }
             at += some;
         }
     pages_sync();  // `gone` has been read, and the count that free_left may be
@@ -236,60 +240,69 @@ struct CompactParams {
 };
 
 __global__ void __launch_bounds__(kPagesThreads, 1) pages_compact_kernel(const __grid_constant__ CompactParams p) {
-    __shared__ int part[32], holes, low_holes;
+    extern __shared__ uint32_t bits_mem[];
+    __shared__ int part[32], holes;
     const rra_pages_compact_args_t& a = p.a;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, lane = tid & 31;
     const int me = (int)blockIdx.x * nt + tid, all = (int)gridDim.x * nt;
     pdl_release_early();
-    pdl_wait();
-    const int n = a.num_pages, count = min(max(a.free_count[0], 0), n);
-    // ---- moved[] marks the free pages ----
-    for (int i = me; i < n; i += all) {
-        a.moved[i] = i;
-        if (a.shared_out != a.shared) a.shared_out[i] = a.shared[i];
-    }
-    for (int i = me; i < a.max_moves; i += all) a.move_from[i] = a.move_to[i] = -1;
+    const int n = a.num_pages;
+    const PageBits bits(bits_mem, n);  // pages that are free
     pages_sync();
+    pdl_wait();
+    const int count = min(max(a.free_count[0], 0), n);
     for (int i = me; i < count; i += all) {
         const int page = a.free_pages[i];
-        if (page >= 0 && page < n) a.moved[page] = -1;
+        if (page >= 0 && page < n) bits.set(page);
     }
+    if (a.shared_out != a.shared)
+        for (int i = me; i < n; i += all) a.shared_out[i] = a.shared[i];
+    for (int i = me; i < a.max_moves; i += all) a.move_from[i] = a.move_to[i] = -1;
     pages_sync();
     // ---- how many are free, and how many of those lie below the number in use ----
-    int begin, end, mine = 0, total, before, free_all;
-    pages_share(n, begin, end);
-    auto free_at = [&](int i) { return i < end && __ldcg(a.moved + i) < 0; };
-    for (int i0 = begin; i0 < end; i0 += nt * 4)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mine += free_at(i0 + 4 * tid + k);
+    int mine = 0, total, before, free_all;
+    for (int i = tid; i < bits.count; i += nt) mine += __popc(bits.words[i]);
     pages_scan(mine, total, part);
     if (tid == 0) holes = total;
     pages_sync();
     pages_meet(&holes, before, free_all);
     const int used = n - free_all;
-    mine = 0;
-    for (int i0 = begin; i0 < min(end, used); i0 += nt * 4)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mine += i0 + 4 * tid + k < used && free_at(i0 + 4 * tid + k);
-    pages_scan(mine, total, part);
-    if (tid == 0) low_holes = total;
-    pages_sync();
-    int low_before, low_all;
-    pages_meet(&low_holes, low_before, low_all);
-    const int moves = min(low_all, a.max_moves);
-    // ---- the lists.  Of page i: `lower` free pages and i - lower used ones lie below it. ----
+    int moves;
+    {
+        // those of the CTAs before the one that has page `used`, and of its words up to there
+        const int cta = used < n ? used / bits.run : (int)gridDim.x, in = used - cta * bits.run;
+        int low = 0;
+        if (gridDim.x == 1) {
+            for (int i = tid; i < in >> 5; i += nt) low += __popc(bits.words[i]);
+            if (cta == 0 && tid == 0 && (in & 31) != 0) low += __popc(bits.words[in >> 5] & ((1u << (in & 31)) - 1u));
+            if (cta == 1 && tid == 0) low = free_all;
+        } else {
+            if (tid < (int)gridDim.x && tid < cta) low += ld_peer_int(map_to_rank(smem_u32(&holes), (uint32_t)tid));
+            if (cta < (int)gridDim.x)
+                for (int i = tid; 32 * i < in; i += nt) {
+                    const uint32_t w = (uint32_t)ld_peer_int(map_to_rank(smem_u32(bits.words + i), (uint32_t)cta));
+                    low += __popc(in - 32 * i >= 32 ? w : w & ((1u << (in - 32 * i)) - 1u));
+                }
+        }
+        int low_all;
+        pages_scan(low, low_all, part);
+        moves = min(low_all, a.max_moves);
+    }
+    // ---- the lists.  Of page i: `lower` free pages and i - lower used ones lie below it.  moved[] of a page that leaves: the
+    // complement of 1 + the number of its move, until the move's other end is known ----
     int at = before;
-    for (int i0 = begin; i0 < end; i0 += nt * 4) {
-        uint32_t who = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) who |= free_at(i0 + 4 * tid + k) ? 1u << k : 0u;
+    for (int i0 = 0; i0 < bits.count; i0 += nt >> 3) {  // eight threads a word, four pages each
+        const int word = i0 + (tid >> 3);
+        const uint32_t whole_word = word < bits.count ? bits.words[word] : 0u, who = whole_word >> (4 * (tid & 7)) & 15u;
         int some, lower = at + pages_scan(__popc(who), some, part);
+        const int first = bits.begin + 32 * word + 4 * (tid & 7);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int i = i0 + 4 * tid + k;
-            if (i >= end) continue;
+            const int i = first + k;
+            if (word >= bits.count || i >= bits.end) continue;
             const int used_below = i - lower;
             bool now;  // free afterwards
+            int to = -1;
             if (who >> k & 1u) {
                 now = lower >= moves;  // its rank among the holes
                 if (!now) a.move_to[lower] = i;
@@ -297,7 +310,9 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_compact_kernel(const _
                 const int above = used - 1 - used_below;
                 now = above < moves;
                 if (now) a.move_from[above] = i;
+                to = now ? ~(1 + above) : i;
             }
+            a.moved[i] = to;
             if (now) {
                 const int rank = lower - min(lower, moves) + max(0, used_below - (used - moves));  // free afterwards and lower
                 a.free_out[free_all - 1 - rank] = i;
@@ -317,8 +332,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_compact_kernel(const _
         a.free_left[0] = free_all;
         a.move_count[0] = moves;
     }
-    pages_sync();
-    // ---- the tables: a warp a row ----
+    // ---- the tables: a warp a row.  What moved[] says may be either, the move's number or its end ----
     for (int b = me >> 5; b < a.requests; b += all >> 5) {
         const int length = min(max(a.seq_len[b], 0), kPagesMost);
         const int held = min(length > 0 ? p.by_page(length - 1) + 1 : 0, a.table_pages);
@@ -330,12 +344,18 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_compact_kernel(const _
             int page[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) page[k] = j0 + 32 * k + lane < entries ? row[j0 + 32 * k + lane] : -1;
+            int now[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                now[k] = page[k];
+                if (j0 + 32 * k + lane < held && page[k] >= 0 && page[k] < n) now[k] = __ldcg(a.moved + page[k]);
+            }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int j = j0 + 32 * k + lane;
                 if (j >= entries) continue;
-                if (j < held && page[k] >= 0 && page[k] < n) page[k] = __ldcg(a.moved + page[k]);
-                to[j] = page[k];
+                if (j < held && page[k] >= 0 && page[k] < n && now[k] < -1) now[k] = __ldcg(a.move_to + (~now[k] - 1));
+                to[j] = now[k];
             }
         }
     }
@@ -344,42 +364,71 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_compact_kernel(const _
 // ================================================================= copy ====
 constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 8;  // 16-byte loads of a thread in flight
+constexpr int kCopyCtas = 152 * 8;
 
 struct CopyParams {
     rra_pages_copy_args_t a;
-    int64_t vectors;   // of a page
-    int32_t pieces;    // CTAs of a page
+    Divisor by_pieces; // pieces of a page
+    int32_t total;     // pieces of all pages
+    int32_t vectors;   // of a piece, the last one's may be fewer
+    int64_t page;      // vectors of a page
 };
 
+// A CTA takes every gridDim'th piece; it looks at kCopyThreads pairs at once, so that lists that are mostly empty (the
+// moves of a pool that needs few) cost a round trip, not one a pair.
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
     const rra_pages_copy_args_t& a = p.a;
+    __shared__ const uint4* srcs[kCopyThreads];
+    __shared__ uint4* dsts[kCopyThreads];
+    __shared__ int32_t lengths[kCopyThreads];
     pdl_release_early();
-    const int i = (int)(blockIdx.x / (unsigned)p.pieces), piece = (int)(blockIdx.x - (unsigned)i * (unsigned)p.pieces);
     pdl_wait();
-    const int from = a.from[i], to = a.to[i];
-    if (from < 0 || to < 0 || from >= a.from_num || to >= a.to_num) return;
-    const uint4* const src = (const uint4*)((const char*)a.from_pages + (int64_t)from * a.page_bytes);
-    uint4* const dst = (uint4*)((char*)a.to_pages + (int64_t)to * a.page_bytes);
-    const int64_t at = (int64_t)piece * kCopyThreads * kCopyAhead + threadIdx.x;
-    uint4 x[kCopyAhead];
+    for (int64_t w0 = blockIdx.x; w0 < p.total; w0 += (int64_t)gridDim.x * kCopyThreads) {
+        const int64_t w = w0 + (int64_t)threadIdx.x * gridDim.x;
+        int length = 0;
+        if (w < p.total) {
+            const int i = p.by_pieces((int)w);
+            const int64_t piece = w - (int64_t)i * p.by_pieces.d;
+            const int from = a.from[i], to = a.to[i];
+            if (from >= 0 && to >= 0 && from < a.from_num && to < a.to_num) {
+                srcs[threadIdx.x] = (const uint4*)((const char*)a.from_pages + (int64_t)from * a.page_bytes) + piece * p.vectors;
+                dsts[threadIdx.x] = (uint4*)((char*)a.to_pages + (int64_t)to * a.page_bytes) + piece * p.vectors;
+                length = (int)min((int64_t)p.vectors, p.page - piece * p.vectors);
+            }
+        }
+        lengths[threadIdx.x] = length;
+        const int some = __syncthreads_or(length > 0);
+        if (some)
+            for (int k = 0; k < kCopyThreads && w0 + (int64_t)k * gridDim.x < p.total; ++k) {
+                const int n = lengths[k];
+                if (n == 0) continue;
+                const uint4* const src = srcs[k] + threadIdx.x;
+                uint4* const dst = dsts[k] + threadIdx.x;
+                uint4 x[kCopyAhead];
 #pragma unroll
-    for (int k = 0; k < kCopyAhead; ++k)
-        if (at + k * kCopyThreads < p.vectors) x[k] = __ldcs(src + at + k * kCopyThreads);
+                for (int v = 0; v < kCopyAhead; ++v)
+                    if ((int)threadIdx.x + v * kCopyThreads < n) x[v] = __ldcs(src + v * kCopyThreads);
 #pragma unroll
-    for (int k = 0; k < kCopyAhead; ++k)
-        if (at + k * kCopyThreads < p.vectors) __stcs(dst + at + k * kCopyThreads, x[k]);
+                for (int v = 0; v < kCopyAhead; ++v)
+                    if ((int)threadIdx.x + v * kCopyThreads < n) __stcs(dst + v * kCopyThreads, x[v]);
+            }
+        __syncthreads();
+    }
 }
 
 // CTAs for so many items of a thread's work.
 static int pages_ctas(int64_t items) {
     int ctas = 1;
-    while (ctas < kPagesMaxCluster && (int64_t)ctas * kPagesThreads * 2 < items) ctas *= 2;
+    while (ctas < kPagesMaxCluster && (int64_t)ctas * kPagesThreads < items) ctas *= 2;
     return ctas;
 }
 
+// Bytes of shared memory that so many pages take in each CTA.
+static size_t pages_bits(int pages, int ctas) { return ((size_t)pages / (size_t)ctas + 32) / 32 * 4 + 4; }
+
 static bool pages_ok(int requests, int table_pages, int64_t stride, int page_tokens, int num_pages, const void* table, const void* lengths) {
     if (requests < 0 || requests > RRA_SERVE_MAX_REQUESTS || table_pages < 0 || stride < table_pages || page_tokens < 1 ||
-        num_pages < 0 || num_pages > INT32_MAX - 65536)
+        num_pages < 0 || num_pages > kPagesPool)
         return false;
     return requests == 0 || (lengths != nullptr && (table_pages == 0 || table != nullptr));
 }
@@ -421,13 +470,13 @@ rra_status_t rra_pages_release(const rra_pages_release_args_t* args, rra_stream_
     p.a = a;
     p.by_page = rra::Divisor(a.page_tokens);
     const void* k = (const void*)rra::pages_release_kernel;
-    if (rra::configure_cluster_kernel(k, 0) != cudaSuccess) {
+    if (rra::configure_cluster_kernel(k, (int)rra::pages_bits(rra::kPagesPool, rra::kPagesMaxCluster)) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
     const int ctas = rra::pages_ctas(std::max<int64_t>((int64_t)a.requests * 32, a.num_pages / 4));
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, 0, ctas, stream, kargs);
+    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, rra::pages_bits(a.num_pages, ctas), ctas, stream, kargs);
 }
 
 rra_status_t rra_pages_compact(const rra_pages_compact_args_t* args, rra_stream_t stream) {
@@ -445,13 +494,13 @@ rra_status_t rra_pages_compact(const rra_pages_compact_args_t* args, rra_stream_
     p.a = a;
     p.by_page = rra::Divisor(a.page_tokens);
     const void* k = (const void*)rra::pages_compact_kernel;
-    if (rra::configure_cluster_kernel(k, 0) != cudaSuccess) {
+    if (rra::configure_cluster_kernel(k, (int)rra::pages_bits(rra::kPagesPool, rra::kPagesMaxCluster)) != cudaSuccess) {
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
     const int ctas = rra::pages_ctas(std::max<int64_t>((int64_t)a.requests * 64, a.num_pages / 4));
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, 0, ctas, stream, kargs);
+    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, rra::pages_bits(a.num_pages, ctas), ctas, stream, kargs);
 }
 
 rra_status_t rra_pages_copy(const rra_pages_copy_args_t* args, rra_stream_t stream) {
@@ -464,12 +513,15 @@ rra_status_t rra_pages_copy(const rra_pages_copy_args_t* args, rra_stream_t stre
     if (a.from_pages == nullptr || a.to_pages == nullptr || a.from == nullptr || a.to == nullptr) return RRA_ERR_INVALID_ARG;
     rra::CopyParams p;
     p.a = a;
-    p.vectors = a.page_bytes / 16;
-    const int64_t pieces = (p.vectors + rra::kCopyThreads * rra::kCopyAhead - 1) / (rra::kCopyThreads * rra::kCopyAhead);
-    if (pieces > INT32_MAX / a.count) return RRA_ERR_INVALID_ARG;  // CTAs are counted in 32 bits
-    p.pieces = (int)pieces;
+    p.page = a.page_bytes / 16;
+    constexpr int kMost = rra::kCopyThreads * rra::kCopyAhead;
+    const int64_t pieces = (p.page + kMost - 1) / kMost;
+    if (pieces > INT32_MAX / 2 / a.count) return RRA_ERR_INVALID_ARG;  // pieces are counted in 32 bits
+    p.by_pieces = rra::Divisor((int32_t)pieces);
+    p.total = (int32_t)(pieces * a.count);
+    p.vectors = (int32_t)((p.page + pieces - 1) / pieces);
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch((const void*)rra::pages_copy_kernel, dim3((unsigned)(pieces * a.count)), rra::kCopyThreads, 0, 1, stream, kargs);
+    return rra::serve_launch((const void*)rra::pages_copy_kernel, dim3((unsigned)std::min<int64_t>(p.total, rra::kCopyCtas)), rra::kCopyThreads, 0, 1, stream, kargs);
 }
 
 }  // extern "C"
