@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_compact_kernel(const _
 // ================================================================= copy ====
 constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 8;  // 16-byte loads of a thread in flight
-constexpr int kCopyCtas = 152 * 8;
+constexpr int kCopyCtas = 152 * 16;  // (5620 pages of 33 KB: 8 an SM 60.8 us, 16 59.1, 32 58.0, but of 8192 listed moves 626 9.1, 8.4 and 10.5)
 
 struct CopyParams {
     rra_pages_copy_args_t a;

@@ -707,11 +707,11 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
         }
         // A wait ran out: the results are lost, but the counters of the segments from here on have to be zero for the next
         // call.  So this CTA still counts itself, and whoever is last there clears them.
-        if (!ok && (tid & 255) == 0)
+        if (!ok && (warp & 7) == 0)  // a whole warp, which goes from segment to segment together
 #pragma unroll 1
             while (true) {
                 const int which = seg.begin >= r0 ? 1 : 0;
-                if (which == 0 || seg.end > r1) {
+                if (lane == 0 && (which == 0 || seg.end > r1)) {
                     const int i0 = (int)(seg.begin / run), i1 = (int)((seg.end - 1) / run);
                     uint32_t* const count = &ws->arrived[i0 * TILES + i];
                     const uint32_t before = added[which][i] != 0u ? arrived[which][i] : atomicAdd(count, 1u);
