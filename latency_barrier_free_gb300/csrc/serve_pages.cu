@@ -423,6 +423,9 @@ static int pages_ctas(int64_t items) {
     return ctas;
 }
 
+// Threads of a CTA: fewer warps meet sooner.
+static int pages_threads(int64_t items) { return items <= 1024 ? 256 : kPagesThreads; }
+
 // Bytes of shared memory that so many pages take in each CTA.
 static size_t pages_bits(int pages, int ctas) { return ((size_t)pages / (size_t)ctas + 32) / 32 * 4 + 4; }
 
@@ -454,9 +457,10 @@ rra_status_t rra_pages_fork(const rra_pages_fork_args_t* args, rra_stream_t stre
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
-    const int ctas = rra::pages_ctas(std::max<int64_t>((int64_t)a.forks * 64, a.shared == a.shared_out ? 0 : a.num_pages / 4));
+    const int64_t items = std::max<int64_t>((int64_t)a.forks * 64, a.shared == a.shared_out ? 0 : a.num_pages / 4);
+    const int ctas = rra::pages_ctas(items);
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, (size_t)a.forks * 4, ctas, stream, kargs);
+    return rra::serve_launch(k, dim3((unsigned)ctas), rra::pages_threads(items), (size_t)a.forks * 4, ctas, stream, kargs);
 }
 
 rra_status_t rra_pages_release(const rra_pages_release_args_t* args, rra_stream_t stream) {
@@ -474,9 +478,10 @@ rra_status_t rra_pages_release(const rra_pages_release_args_t* args, rra_stream_
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
-    const int ctas = rra::pages_ctas(std::max<int64_t>((int64_t)a.requests * 32, a.num_pages / 4));
+    const int64_t items = std::max<int64_t>((int64_t)a.requests * 32, a.num_pages / 4);
+    const int ctas = rra::pages_ctas(items);
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, rra::pages_bits(a.num_pages, ctas), ctas, stream, kargs);
+    return rra::serve_launch(k, dim3((unsigned)ctas), rra::pages_threads(items), rra::pages_bits(a.num_pages, ctas), ctas, stream, kargs);
 }
 
 rra_status_t rra_pages_compact(const rra_pages_compact_args_t* args, rra_stream_t stream) {
@@ -498,9 +503,10 @@ rra_status_t rra_pages_compact(const rra_pages_compact_args_t* args, rra_stream_
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
-    const int ctas = rra::pages_ctas(std::max<int64_t>((int64_t)a.requests * 64, a.num_pages / 4));
+    const int64_t items = std::max<int64_t>((int64_t)a.requests * 64, a.num_pages / 4);
+    const int ctas = rra::pages_ctas(items);
     void* kargs[] = {(void*)&p};
-    return rra::serve_launch(k, dim3((unsigned)ctas), rra::kPagesThreads, rra::pages_bits(a.num_pages, ctas), ctas, stream, kargs);
+    return rra::serve_launch(k, dim3((unsigned)ctas), rra::pages_threads(items), rra::pages_bits(a.num_pages, ctas), ctas, stream, kargs);
 }
 
 rra_status_t rra_pages_copy(const rra_pages_copy_args_t* args, rra_stream_t stream) {

@@ -321,6 +321,16 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                    drained = half_done + 8 * TILES;
     constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
+    // TMEM and the tensors' descriptions, while the work is dealt out
+    if (warp == Sh::kIssue) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 32) {
+        asm volatile("prefetch.tensormap [%0];" : : "l"(&p.q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" : : "l"(&p.k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" : : "l"(&p.v) : "memory");
+    }
     if (tid == 0) {
         for (int i = 0; i < TILES; ++i) {
             added[0][i] = added[1][i] = 0u;
@@ -352,16 +362,17 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     int64_t r0 = 0, r1 = INT64_MAX, run = 1;
     const int dealt = prompt_deal<Sh::kWarps>(work, chunk_sums, part, items);
     __syncthreads();
-    if (dealt == 0 || (dealt < 0 && !prompt_run<Sh::kWarps>(work, chunk_sums, part, start, r0, r1, run))) return;
-    if (warp == Sh::kIssue) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    const bool idle = dealt == 0 || (dealt < 0 && !prompt_run<Sh::kWarps>(work, chunk_sums, part, start, r0, r1, run));
     fence_proxy_async_smem();  // the sums were where copies go next
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = tmem_base;
+    if (idle) {
+        if (warp == Sh::kIssue)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" : : "r"(tmem), "r"(Sh::kColumns) : "memory");
+        return;
+    }
     // Segments: the first, and the next of one; those that are dealt out have a row of their own.
     auto load = [&](PromptSegment& s, int k) {
         const int4 it = items[k];
