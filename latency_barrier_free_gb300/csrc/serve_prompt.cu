@@ -101,6 +101,31 @@ struct WholeWork {
     }
 };
 
+// Exclusive sum over the block, and the total, in 32 bits; part: a word for each warp.
+template <int kWarps>
+__device__ __forceinline__ int short_sum(int v, int& total, int32_t* part) {
+    static_assert(kWarps <= 32, "a lane for each warp");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    int w = lane < kWarps ? part[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += up;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    __syncthreads();
+    return inc - v + (warp > 0 ? before : 0);
+}
+
 // Deals the segments out: this CTA's in items[] as (first token, tokens, chunk, head), their number; 0 if there is nothing to
 // do, -1 if the work is better cut into runs.  Segment i of all, by number of chunk from the last down, then by request, those
 // with most chunks first, then by head, goes to CTA i of the first round, to CTA gridDim - 1 - i of the second, and so on:
@@ -113,11 +138,12 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
     if (requests > kDealRequests) return -1;
     int32_t *const q0 = scratch, *const qn = q0 + kDealRequests, *const chunks = qn + kDealRequests, *const sorted = chunks + kDealRequests,
                    *const order = sorted + kDealRequests, *const levels = order + kDealRequests;
-    int mine = 0;
+    int mine = 0, longest = 0;
     for (int b = tid; b < requests; b += kThreads) {
         const AttnLengths n = work.lengths(b);
         q0[b] = n.q0, qn[b] = n.qn;
         mine = max(mine, chunks[b] = work.chunks(n));
+        longest = max(longest, n.qn);
     }
     if (__syncthreads_or(mine > kDealChunks)) return -1;
     for (int b = tid; b < requests; b += kThreads) {
@@ -127,7 +153,8 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
         sorted[rank] = c;
         order[rank] = b;
     }
-    __syncthreads();
+    // CTAs' shares differ by no more than the longest segment's cost
+    const bool uneven = __syncthreads_or(longest > (2 * kPromptJoinCost - kPromptSegmentCost) * kPromptKeys);
     // level i is the chunks sorted[0] - 1 - i: how many there are at lower levels
     const int most = requests > 0 ? sorted[0] : 0;
     int before = 0;
@@ -139,11 +166,11 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
             if (sorted[mid] > c) low = mid + 1;
             else high = mid;
         }
-        int64_t all;
-        const int64_t at = before + block_sum<kWarps>(i < most ? low : 0, all, sums);
-        if (before + all > INT32_MAX / 4) return -1;
-        if (i < most) levels[i] = (int)at;
-        before += (int)all;
+        int all;
+        const int at = before + short_sum<kWarps>(i < most ? low : 0, all, (int32_t*)sums);  // up to kDealRequests * kThreads
+        if (i < most) levels[i] = at;
+        before += all;
+        if (before > kDealItems * ctas) return -1;
     }
     if (tid == 0) levels[most] = before;
     __syncthreads();
@@ -166,13 +193,13 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
         to = make_int4(q0[b], qn[b], most - 1 - low, at - y * heads);
         return true;
     };
-    if (rounds <= kDealChecked) {
+    if (uneven && rounds <= kDealChecked) {
         int cost = 0;
         int4 it;
         for (int k = 0; tid < ctas && k < rounds; ++k)
             if (item(tid, k, it)) cost += work.item(AttnLengths{it.x, it.y, it.y}, it.z).tiles + kPromptSegmentCost;
-        int64_t all;
-        block_sum<kWarps>(cost, all, sums);
+        int all;
+        short_sum<kWarps>(cost, all, (int32_t*)sums);  // kDealChecked segments a CTA of up to kDealChunks * 2 tiles each
         if (__syncthreads_or(cost > all / ctas + 2 * kPromptJoinCost)) return -1;
     }
     for (int k = tid; k < rounds; k += kThreads) {
