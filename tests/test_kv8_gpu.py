@@ -328,3 +328,14 @@ def test_skipped_slots_do_not_come_between_neighbours(serve, gap):
         cache.append(x, x * 2, dev(np.array(slots, np.int64)))
         more.append8(pages, ps, hk, d, f64(x), f64(x * 2), slots)
         assert np.array_equal(cache.pages.cpu().numpy(), pages)
+
+
+def steps(span):
+    """Sizes that change from block to block by 2^span at most: prompts take a tile's blocks in one unit up to 2^15."""
+    return lambda rng, n, which: 2.0 ** np.repeat(rng.integers(0, span + 1, n // 16 + 1), 16)[:n, None, None]
+
+
+@pytest.mark.parametrize("span", [1, 14, 15, 16, 17])
+@pytest.mark.parametrize("case", ["prompts of odd lengths", "a chunk of a prompt", "a prompt in a window"])
+def test_attention_with_exponents_about_as_far_apart_as_a_tile_takes(serve, case, span):
+    check_all(case, *build(serve, case, span, steps(span)), scale=2.0 ** (-span - 3))
