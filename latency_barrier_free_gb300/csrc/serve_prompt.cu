@@ -348,11 +348,6 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                    drained = half_done + 8 * TILES;
     constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
-    // TMEM and the tensors' descriptions, while the work is dealt out
-    if (warp == Sh::kIssue) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
     if (tid == 32) {
         asm volatile("prefetch.tensormap [%0];" : : "l"(&p.q) : "memory");
         asm volatile("prefetch.tensormap [%0];" : : "l"(&p.k) : "memory");
@@ -384,6 +379,12 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
         fence_proxy_async_smem();
     }
     pdl_wait();
+    // TMEM, while the work is dealt out.  Not before the wait: the grid before this one may still have to get its own on this SM,
+    // and would wait for ours.
+    if (warp == Sh::kIssue) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" : : "r"(smem_u32(&tmem_base)), "r"(Sh::kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 
     const WholeWork<TILES> work{p};
     int64_t r0 = 0, r1 = INT64_MAX, run = 1;

@@ -104,6 +104,34 @@ def test_two_prompts_objects_on_two_streams(serve):
     assert all(torch.equal(o, want) for o in outs) and a.status() == 0 and b.status() == 0
 
 
+def test_kernels_that_need_tensor_memory_back_to_back(serve):
+    """A grid may be on its way while the one before it ends, on the same SM and with the same tensor memory to share."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    ps, hq, hk, d, n = 64, 8, 4, 64, 1500
+    q, k, v = torch.randn(n, hq + 2 * hk, d, generator=gen, device="cuda").bfloat16().split([hq, hk, hk], 1)
+    pages = -(-n // ps)
+    caches = [serve.KvCache(torch.zeros(pages, serve.kv_page_bytes(ps, hk, d), dtype=torch.uint8, device="cuda"), ps, hk, d),
+              serve.KvCache8(torch.zeros(pages, serve.kv8_page_bytes(ps, hk, d), dtype=torch.uint8, device="cuda"), ps, hk, d)]
+    table, cu, kv = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1), i32([0, n]), i32([n])
+    for cache in caches:
+        cache.append(k, v, torch.arange(n, device="cuda"))
+    prompts = serve.PromptAttention()
+    assert [prompts.plan_kernel(hq, hk, max_len=m) for m in (1, n)] == ["prompt_attention_kernel<128 rows>", "prompt_attention_kernel<256 rows>"]
+
+    def calls(out):
+        prompts.attention(q, k, v, out[0], cu, max_len=1)
+        prompts.attention(q, k, v, out[1], cu, max_len=n)
+        for o, cache in zip(out[2:], caches):
+            cache.attention(q, o, cu, kv, table, max_q=n, max_kv=n)
+
+    want = [torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    calls(want)
+    got = [torch.zeros_like(w) for w in want]
+    for _ in range(50):
+        calls(got)
+    assert prompts.status() == 0 and all(c.status() == 0 for c in caches) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_tensors_of_another_kind_are_refused(serve):
     q = torch.zeros(4, 4, 64, dtype=torch.bfloat16, device="cuda")
     cu, prompts = i32([0, 4]), serve.PromptAttention()

@@ -14,7 +14,7 @@ from test_serve_cpu import FAKE, ROOT, fields, refused, serve  # noqa: F401
 torch = pytest.importorskip("torch")
 
 STRUCTS = {"rra_pages_fork_args_t": "_FORK", "rra_pages_release_args_t": "_RELEASE", "rra_pages_compact_args_t": "_COMPACT",
-           "rra_pages_copy_args_t": "_COPY"}
+           "rra_pages_copy_args_t": "_COPY", "rra_prompt_attention_args_t": "_PROMPT"}
 
 
 def test_structures_have_the_headers_sizes(serve, tmp_path):  # noqa: F811
@@ -57,13 +57,39 @@ def test_cache_refusals(serve):  # noqa: F811
     assert serve._lib().rra_kv8_attention_plan(serve._ATTN.pack(*good), None) == rra.ERR_INVALID_ARG
 
 
+def test_prompt_refusals(serve):  # noqa: F811
+    names = fields("rra_prompt_attention_args_t")
+    good = [FAKE] * 7 + [1024, 128, 512, 128, 512, 128, 1024, 128, 100, 0.1, 3, 8, 4, 128, 0, 60, 1, 0]
+    assert len(names) == len(good)
+    refused(serve, "rra_prompt_attention", serve._PROMPT, good, [
+        ("q", 0), ("k", 0), ("v", 0), ("out", 0), ("cu", 0), ("workspace", 0), ("workspace", FAKE + 16), ("q", FAKE + 8),
+        ("k", FAKE + 2), ("q_token_stride", 0), ("k_head_stride", 100), ("v_token_stride", 516), ("out_head_stride", 4),
+        ("q_token_stride", 2 ** 39), ("tokens", -1), ("tokens", 2 ** 30), ("tokens", 2 ** 27), ("scale", float("inf")),
+        ("scale", float("nan")), ("scale", 3e38), ("requests", -1), ("requests", 4097), ("q_heads", 0), ("q_heads", 7),
+        ("kv_heads", 0), ("head_dim", 0), ("head_dim", 100), ("head_dim", 136), ("half", 2), ("half", -1), ("max_len", -1),
+        ("window", -1)], names)
+    for name in ("requests", "tokens"):  # nothing to do
+        args = list(good)
+        args[names.index(name)] = 0
+        assert serve._lib().rra_prompt_attention(serve._PROMPT.pack(*args), 0) == rra.OK
+    name = ctypes.c_char_p()
+    plan = serve._lib().rra_prompt_attention_plan
+    for longest, rows in ((0, 128), (64, 128), (65, 256), (2 ** 31 - 1, 256)):
+        args = list(good)
+        args[names.index("max_len")] = longest
+        assert plan(serve._PROMPT.pack(*args), ctypes.byref(name)) == rra.OK
+        assert name.value.decode() == "prompt_attention_kernel<%d rows>" % rows
+    assert plan(serve._PROMPT.pack(*good), None) == rra.ERR_INVALID_ARG
+    assert serve._lib().rra_prompt_attention_workspace_bytes() > 4096
+
+
 def test_fork_refusals(serve):  # noqa: F811
     names = fields("rra_pages_fork_args_t")
     good = [FAKE] * 13 + [8, 4, 3, 8, 16, 100, 0]
     assert len(names) == len(good)
     refused(serve, "rra_pages_fork", serve._FORK, good, [(n, 0) for n in names[:13]] + [
         ("table_stride", 7), ("requests", -1), ("requests", 4097), ("forks", -1), ("forks", 4097), ("table_pages", -1),
-        ("page_tokens", 0), ("num_pages", -1), ("num_pages", 2 ** 31 - 1), ("reserved", 1)], names)
+        ("page_tokens", 0), ("num_pages", -1), ("num_pages", 2 ** 24 + 1), ("num_pages", 2 ** 31 - 1), ("reserved", 1)], names)
 
 
 def test_release_refusals(serve):  # noqa: F811
@@ -72,7 +98,7 @@ def test_release_refusals(serve):  # noqa: F811
     assert len(names) == len(good)
     refused(serve, "rra_pages_release", serve._RELEASE, good, [(n, 0) for n in names[:9]] + [
         ("table_stride", 7), ("requests", -1), ("requests", 4097), ("table_pages", -1), ("page_tokens", 0), ("num_pages", -1),
-        ("num_pages", 2 ** 31 - 1)], names)
+        ("num_pages", 2 ** 24 + 1), ("num_pages", 2 ** 31 - 1)], names)
 
 
 def test_compact_refusals(serve):  # noqa: F811
@@ -81,7 +107,7 @@ def test_compact_refusals(serve):  # noqa: F811
     assert len(names) == len(good)
     refused(serve, "rra_pages_compact", serve._COMPACT, good, [(n, 0) for n in names[:13]] + [
         ("table_stride", 7), ("table_out_stride", 7), ("table_out_stride", 9), ("requests", -1), ("requests", 4097),
-        ("table_pages", -1), ("page_tokens", 0), ("num_pages", -1), ("num_pages", 2 ** 31 - 1), ("max_moves", -1),
+        ("table_pages", -1), ("page_tokens", 0), ("num_pages", -1), ("num_pages", 2 ** 24 + 1), ("num_pages", 2 ** 31 - 1), ("max_moves", -1),
         ("reserved", 1)], names)
 
 
