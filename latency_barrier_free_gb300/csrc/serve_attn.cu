@@ -550,27 +550,40 @@ static bool attn_args_ok(const rra_kv_attention_args_t* a) {
 // (64 heads over 8 of 128, 8 requests, 4096 keys: 4 queries 37.1, 32.7, 51.5, 56.1 us; 8: 64, 53, 52, 57; 32: 217, 172, 80,
 // 58; 32768 keys, 64 queries: 3207, 2376, 932, 525.  1 request and query, 500 keys: 8.1 us against 6.7, 5.6, 4.8, 5.0 in
 // clusters; 8000 keys: 13.8 against 57, 31, 17.8, 11.0; 32000: 19.6 against 31.5 in clusters of 8.)
+// Over the 8-bit cache, whose codes take fewer instructions and have no second product: 11.2 or 13.8 (10.2 or 12.1) + 0.138 or
+// 0.252 (0.078 or 0.133); 10.6 or 17.4 (8.8 or 12.7) + 2.2 or 2.6 (1.65 or 1.95), joins 1.9 (1.1) each; clusters 4.6 to 5.3
+// (4.2 to 5.3) + 0.76 (0.62), times 1.03 (0.78).  (Same heads and requests: 1 query, 8192 keys, 31.5, 40.0, 81.0, 97.8 us, in
+// clusters 59, 33, 25, 30; 4, 2048: 25.3, 28.5, 40, 48, and 22, 26, 35, 52; 2 requests, 32 queries, 512 keys, 20.0, 23.5, 15.0,
+// 20.6, and 17.5, 27.8.  Over 756 sizes of 1 to 32 requests, 1 to 256 queries, 512 to 32768 keys the choice takes 0.8 %
+// longer than the best on average, 27 % at most; by the 4-bit cache's numbers 3.2 %, 57 %.)
+struct AttnCosts {
+    double rows8[2], rows16[2], prompt128[2], prompt256[2], join, team[4], team_tile, team_share;  // what it starts with, and a tile
+};
+constexpr AttnCosts kAttnCosts[2][2] = {  // 4 bits, 8 bits; heads of 64, of 128
+    {{{9.5, 0.085}, {12, 0.135}, {8, 1.9}, {11, 2.0}, 1.1, {3.5, 4.0, 4.1, 4.4}, 0.64, 0.7},
+     {{11.5, 0.125}, {14, 0.2}, {8, 2.7}, {11, 3.2}, 2, {3.5, 4.0, 4.1, 4.4}, 0.83, 1.1}},
+    {{{10.2, 0.078}, {12.1, 0.133}, {8.76, 1.65}, {12.7, 1.96}, 1.1, {4.2, 5.2, 5.17, 5.29}, 0.62, 0.78},
+     {{11.18, 0.138}, {13.8, 0.252}, {10.6, 2.166}, {17.35, 2.573}, 1.87, {4.59, 4.87, 5.01, 5.27}, 0.762, 1.033}}};
 enum AttnKernel { kRows8, kRows16, kPrompt128, kPrompt256, kTeam1, kTeam2, kTeam4, kTeam8 };
-static AttnKernel attn_kernel_of(const rra_kv_attention_args_t& a) {
-    const bool big = a.cache.head_dim == 128;
+static AttnKernel attn_kernel_of(const rra_kv_attention_args_t& a, int bits) {
+    const AttnCosts& cost = kAttnCosts[bits == 8][a.cache.head_dim == 128];
     const double sms = 152;
     const double rows = (double)std::max(a.max_q, 1) * (a.q_heads / a.cache.kv_heads);
     const double seen = a.window > 0 ? std::min((double)a.max_kv, (double)a.window + a.max_q) : (double)a.max_kv;
     const double heads = (double)std::max(a.requests, 1) * a.cache.kv_heads, tiles = std::max(1.0, std::ceil(seen / kAttnTile));
     auto segments = [&](double n) { return heads * std::ceil(rows / n); };
-    auto few = [&](double n, double fixed, double tile) { return fixed + segments(n) * (tiles + kAttnSegmentCost) / sms * tile; };
-    auto many = [&](double n, double fixed, double tile) {
+    auto few = [&](double n, const double* by) { return by[0] + segments(n) * (tiles + kAttnSegmentCost) / sms * by[1]; };
+    auto many = [&](double n, const double* by) {
         const double of = std::ceil(seen / 128), run = std::max(6.0, segments(n) * (of + 2) / sms);
-        return fixed + (segments(n) <= sms ? std::min(of, run) : run) * tile + (of > run ? of / run * (big ? 2 : 1.1) : 0);
+        return by[0] + (segments(n) <= sms ? std::min(of, run) : run) * by[1] + (of > run ? of / run * cost.join : 0);
     };
     auto team = [&](double size, double fixed) {
         const double ctas = segments(8) * size;
         if (ctas > 16 * sms) return 1e30;
-        return fixed + std::ceil(tiles / (kTeamWarps * size)) * (big ? 0.83 : 0.64) * std::max(1.0, (big ? 1.1 : 0.7) * ctas / sms);
+        return fixed + std::ceil(tiles / (kTeamWarps * size)) * cost.team_tile * std::max(1.0, cost.team_share * ctas / sms);
     };
-    const double t[8] = {few(8, big ? 11.5 : 9.5, big ? 0.125 : 0.085), few(16, big ? 14 : 12, big ? 0.2 : 0.135), many(128, 8, big ? 2.7 : 1.9),
-                         many(256, 11, big ? 3.2 : 2.0),   team(1, 3.5),                   team(2, 4.0),
-                         team(4, 4.1),                     team(8, 4.4)};
+    const double t[8] = {few(8, cost.rows8),     few(16, cost.rows16),  many(128, cost.prompt128), many(256, cost.prompt256),
+                         team(1, cost.team[0]), team(2, cost.team[1]), team(4, cost.team[2]),     team(8, cost.team[3])};
     return (AttnKernel)(std::min_element(t, t + 8) - t);
 }
 
@@ -584,19 +597,19 @@ size_t rra_kv_attention_workspace_bytes(int head_dim) {
     return sizeof(rra::AttnWorkspace) + std::max(decode, rra::prefill_partial_bytes(head_dim));
 }
 
-rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
+static rra_status_t kv_attention_plan(const rra_kv_attention_args_t* args, int bits, const char** name) {
     if (name == nullptr || !rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
     static const char* const names[] = {"kv_attention_kernel<8 rows>", "kv_attention_kernel<16 rows>",
                                         "kv_attention_prompt_kernel<128 rows>", "kv_attention_prompt_kernel<256 rows>",
                                         "kv_attention_team_kernel<1 CTA>", "kv_attention_team_kernel<2 CTAs>",
                                         "kv_attention_team_kernel<4 CTAs>", "kv_attention_team_kernel<8 CTAs>"};
-    *name = names[rra::attn_kernel_of(*args)];
+    *name = names[rra::attn_kernel_of(*args, bits)];
     return RRA_OK;
 }
 
-rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const char** name) {
-    return rra_kv_attention_plan(args, name);
-}
+rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const char** name) { return kv_attention_plan(args, 4, name); }
+
+rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const char** name) { return kv_attention_plan(args, 8, name); }
 
 static rra_status_t kv_attention(const rra_kv_attention_args_t* args, int bits, rra_stream_t stream) {
     if (!rra::attn_args_ok(args)) return RRA_ERR_INVALID_ARG;
@@ -615,7 +628,7 @@ static rra_status_t kv_attention(const rra_kv_attention_args_t* args, int bits, 
     p.by_page = rra::Divisor(args->cache.page_tokens);
     p.room = args->table_pages * args->cache.page_tokens;
     p.window = std::min(args->window, 1 << 30);
-    const rra::AttnKernel kernel = rra::attn_kernel_of(*args);
+    const rra::AttnKernel kernel = rra::attn_kernel_of(*args, bits);
     if (kernel >= rra::kTeam1)
         return rra::launch_team(p, bits, (int)(((int64_t)std::max(args->max_q, 1) * p.group + 7) / 8), 1 << (kernel - rra::kTeam1), stream);
     if (kernel == rra::kPrompt128 || kernel == rra::kPrompt256)

@@ -37,11 +37,12 @@
 namespace rra {
 
 
-constexpr int kDealRequests = 1024;  // up to so many requests, and chunks of the longest, segments are dealt out: their order
-constexpr int kDealChunks = 8192;    // is found in shared memory
-constexpr int kDealItems = 1024;     // segments of a CTA
-constexpr int kDealChecked = 16;     // with more, the CTAs' shares differ by little
-constexpr int kPromptJoinCost = 8;   // what joining the parts of a segment costs, in key tiles
+constexpr int kDealRequests = 1024;  // up to so many requests segments are dealt out: their order is found in shared memory
+// And up to so many segments a CTA.  With more, runs are as even, and a CTA's next segment mostly reads the keys that the one
+// before it read (32 heads over 32: 16 requests of 1024 tokens, 14 segments a CTA, 215 us, in runs 206; 64 of 300, 27, 265 and 257.
+// 64 heads over 8: 64 of 512, 54, 503 and 481; 3 of 2000, 10, 184 and 193; one of 500, 1, 16.6 and 31.6).
+constexpr int kDealItems = 10, kDealChunks = kDealItems * kPromptMaxCtas;
+constexpr int kDealExcess = 10;  // key tiles that a CTA may have above the mean: about what finding runs and joining parts costs
 
 struct PromptParams {
     CUtensorMap q, k, v;  // [channels][heads][tokens]; boxes of 64 channels, q: group heads of `span` tokens, k, v: 128 tokens
@@ -138,14 +139,17 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
     if (requests > kDealRequests) return -1;
     int32_t *const q0 = scratch, *const qn = q0 + kDealRequests, *const chunks = qn + kDealRequests, *const sorted = chunks + kDealRequests,
                    *const order = sorted + kDealRequests, *const levels = order + kDealRequests;
-    int mine = 0, longest = 0;
+    int mine = 0, longest = 0, before;
     for (int b = tid; b < requests; b += kThreads) {
         const AttnLengths n = work.lengths(b);
         q0[b] = n.q0, qn[b] = n.qn;
-        mine = max(mine, chunks[b] = work.chunks(n));
+        mine += min(chunks[b] = work.chunks(n), kDealChunks + 1);
         longest = max(longest, n.qn);
     }
-    if (__syncthreads_or(mine > kDealChunks)) return -1;
+    short_sum<kWarps>(mine, before, (int32_t*)sums);
+    const int64_t total = (int64_t)before * heads;
+    if (total == 0) return 0;
+    if (total > (int64_t)kDealItems * ctas) return -1;
     for (int b = tid; b < requests; b += kThreads) {
         const int c = chunks[b];
         int rank = 0;
@@ -154,10 +158,10 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
         order[rank] = b;
     }
     // CTAs' shares differ by no more than the longest segment's cost
-    const bool uneven = __syncthreads_or(longest > (2 * kPromptJoinCost - kPromptSegmentCost) * kPromptKeys);
+    const bool uneven = __syncthreads_or(longest > (kDealExcess - kPromptSegmentCost) * kPromptKeys);
     // level i is the chunks sorted[0] - 1 - i: how many there are at lower levels
-    const int most = requests > 0 ? sorted[0] : 0;
-    int before = 0;
+    const int most = sorted[0];
+    before = 0;
     for (int i0 = 0; i0 < most; i0 += kThreads) {
         const int i = i0 + tid, c = most - 1 - i;
         int low = 0, high = requests;  // requests with more than c chunks
@@ -170,13 +174,9 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
         const int at = before + short_sum<kWarps>(i < most ? low : 0, all, (int32_t*)sums);  // up to kDealRequests * kThreads
         if (i < most) levels[i] = at;
         before += all;
-        if (before > kDealItems * ctas) return -1;
     }
     if (tid == 0) levels[most] = before;
     __syncthreads();
-    const int64_t total = (int64_t)before * heads;
-    if (total == 0) return 0;
-    if (total > (int64_t)kDealItems * ctas) return -1;
     const int rounds = (int)((total + ctas - 1) / ctas);
     // segment of CTA x in round k
     auto item = [&](int x, int k, int4& to) {
@@ -193,14 +193,14 @@ __device__ __forceinline__ int prompt_deal(const W& work, int32_t* scratch, int6
         to = make_int4(q0[b], qn[b], most - 1 - low, at - y * heads);
         return true;
     };
-    if (uneven && rounds <= kDealChecked) {
+    if (uneven) {
         int cost = 0;
         int4 it;
         for (int k = 0; tid < ctas && k < rounds; ++k)
             if (item(tid, k, it)) cost += work.item(AttnLengths{it.x, it.y, it.y}, it.z).tiles + kPromptSegmentCost;
         int all;
-        short_sum<kWarps>(cost, all, (int32_t*)sums);  // kDealChecked segments a CTA of up to kDealChunks * 2 tiles each
-        if (__syncthreads_or(cost > all / ctas + 2 * kPromptJoinCost)) return -1;
+        short_sum<kWarps>(cost, all, (int32_t*)sums);  // kDealItems segments a CTA of up to kDealChunks * 2 tiles each
+        if (__syncthreads_or(cost > all / ctas + kDealExcess)) return -1;
     }
     for (int k = tid; k < rounds; k += kThreads) {
         int4 it;
@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     __shared__ volatile int32_t dirty[8];              // of every eighth segment: its number + 1 if values were taken out
     __shared__ volatile uint32_t arrived[2][TILES];    // of the run's first and last segment
     __shared__ volatile uint32_t added[2][TILES];      // whether this CTA has counted itself there
+    __shared__ volatile int64_t of_run[3];
+    __shared__ volatile int32_t of_deal;
     __shared__ PromptSegment start;
     __shared__ PromptSegment segments[Sh::kWarps];  // each warp's: registers are for scores
     __shared__ int4 items[kDealItems];
@@ -387,10 +389,17 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     }
 
     const WholeWork<TILES> work{p};
-    int64_t r0 = 0, r1 = INT64_MAX, run = 1;
-    const int dealt = prompt_deal<Sh::kWarps>(work, chunk_sums, part, items);
-    __syncthreads();
-    const bool idle = dealt == 0 || (dealt < 0 && !prompt_run<Sh::kWarps>(work, chunk_sums, part, start, r0, r1, run));
+    // Its run, and all runs' length; or the segments that are dealt to it (-1: it has a run).  In shared memory, for registers.
+    volatile const int64_t &r0 = of_run[0], &r1 = of_run[1], &run = of_run[2];
+    volatile const int32_t& dealt = of_deal;
+    bool idle;
+    {
+        int64_t from = 0, to = INT64_MAX, length = 1;
+        const int given = prompt_deal<Sh::kWarps>(work, chunk_sums, part, items);
+        __syncthreads();
+        idle = given == 0 || (given < 0 && !prompt_run<Sh::kWarps>(work, chunk_sums, part, start, from, to, length));
+        if (tid == 0) of_run[0] = from, of_run[1] = to, of_run[2] = length, of_deal = given;
+    }
     fence_proxy_async_smem();  // the sums were where copies go next
     tc_before_sync();
     __syncthreads();
@@ -402,19 +411,17 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
         return;
     }
     // Segments: the first, and the next of one; those that are dealt out have a row of their own.
-    auto load = [&](PromptSegment& s, int k) {
+    auto given = [&](PromptSegment& s, int k) {
         const int4 it = items[k];
         s.n = AttnLengths{it.x, it.y, it.y};
-        s.b = k, s.c = it.z, s.h = it.w;
-        const PromptItem t = work.item(s.n, s.c);
-        s.first_tile = t.first_tile;
-        s.begin = 0, s.end = t.tiles + kPromptSegmentCost;
+        s.b = k, s.c = it.z, s.h = it.w, s.begin = 0;
     };
     auto next = [&](PromptSegment& at) {
         PromptSegment s = at;
         if (dealt >= 0 ? s.b + 1 == dealt : s.end >= r1) return false;
-        if (dealt >= 0) load(s, s.b + 1);
-        else prompt_next(work, s);
+        if (dealt >= 0) given(s, s.b + 1);
+        else prompt_step(work, s);
+        prompt_place(work, s);
         __syncwarp();  // all lanes have read it; they write the same
         at = s;
         __syncwarp();
@@ -423,8 +430,9 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
     PromptSegment& seg = segments[warp];
     {
         PromptSegment s = start;
-        if (dealt >= 0) load(s, 0);
-        else prompt_load(work, s);
+        if (dealt >= 0) given(s, 0);
+        else s.n = work.lengths(s.b);
+        prompt_place(work, s);
         seg = s;
         __syncwarp();
     }
@@ -1001,10 +1009,38 @@ static bool prompt_args_ok(const rra_prompt_attention_args_t* a) {
     return a->q != nullptr && a->k != nullptr && a->v != nullptr && a->out != nullptr && a->cu != nullptr && a->workspace != nullptr;
 }
 
-// Tiles of a CTA: two, if the longest prompt fills more than one.
-static int prompt_tiles(const rra_prompt_attention_args_t& a) {
-    const int64_t rows = (int64_t)std::max(a.max_len, 1) * (a.q_heads / a.kv_heads);
-    return rows > kPromptRows ? 2 : 1;
+// Tiles of a CTA, by what was measured of either, for lengths as they are on average and at most (every choice is right for
+// every call): a key tile takes 1.3 us for one tile and 1.7 for two (heads of 64: 1.15 and 1.35), a segment 2.8 and 5.8 (2.5
+// and 5) more; 20 us to find that they are better cut into runs, and to join those.  (64 heads over 8 of 128: 16 tokens, 64
+// requests, 21.9 and 31.6 us; 64 tokens 63.0 and 60.7; one request of 700 24.2 and 20.4, of 2000 94 and 68; 8192 and 3000
+// 1320 and 850.  32 over 32: 64 of 300 214 and 257, 32 of 600 227 and 242, 16 of 1024 234 and 206.  8 over 1: 2000 27 and 34,
+// 4000 48 and 55, 5000 67 and 66.)
+static int prompt_tiles(const PromptParams& p) {
+    const rra_prompt_attention_args_t& a = p.a;
+    const bool big = a.head_dim > 64;
+    const double sms = 152, most = std::max(a.max_len, 1), requests = std::max(a.requests, 1);
+    const double length = std::min(std::max(a.tokens / requests, most / requests), most);
+    auto time = [&](int tiles) {
+        const double step = tiles == 2 ? (big ? 1.7 : 1.35) : big ? 1.3 : 1.15, fixed = tiles == 2 ? (big ? 5.8 : 5) : big ? 2.8 : 2.5;
+        const double chunk = tiles * p.span, chunks = std::ceil(length / chunk), segments = chunks * a.kv_heads * p.parts * requests;
+        auto keys = [&](double n) {  // in tiles
+            return std::max(1.0, (a.window > 0 ? std::min(n, (double)a.window + chunk) : n) / kPromptKeys);
+        };
+        const double mean = keys(a.causal ? std::min((chunks + 1) * chunk, length + chunk) / 2 : length), longest = std::ceil(keys(most));
+        const bool alike = longest == 1 || !a.causal;  // CTAs have whole numbers of the same
+        const double load = (alike ? std::ceil(segments / sms) : segments / sms + 0.25) * (mean * step + fixed);
+        return std::min(std::max(load, longest * step + fixed), segments / sms * (mean * step + fixed) + 20);
+    };
+    return time(2) < time(1) ? 2 : 1;
+}
+
+// The rest of a call's parameters, but for the tensors' descriptions.
+static void prompt_sizes(PromptParams& p, const rra_prompt_attention_args_t& a) {
+    p.a = a;
+    p.heads_of_kv = a.q_heads / a.kv_heads;
+    p.parts = (p.heads_of_kv + kPromptRows - 1) / kPromptRows;
+    p.group = (p.heads_of_kv + p.parts - 1) / p.parts;
+    p.span = kPromptRows / p.group;
 }
 
 }  // namespace rra
@@ -1015,7 +1051,9 @@ size_t rra_prompt_attention_workspace_bytes(void) { return sizeof(rra::AttnWorks
 
 rra_status_t rra_prompt_attention_plan(const rra_prompt_attention_args_t* args, const char** name) {
     if (name == nullptr || !rra::prompt_args_ok(args)) return RRA_ERR_INVALID_ARG;
-    *name = rra::prompt_tiles(*args) == 2 ? "prompt_attention_kernel<256 rows>" : "prompt_attention_kernel<128 rows>";
+    rra::PromptParams p;
+    rra::prompt_sizes(p, *args);
+    *name = rra::prompt_tiles(p) == 2 ? "prompt_attention_kernel<256 rows>" : "prompt_attention_kernel<128 rows>";
     return RRA_OK;
 }
 
@@ -1028,13 +1066,9 @@ rra_status_t rra_prompt_attention(const rra_prompt_attention_args_t* args, rra_s
         cudaGetLastError();
         return RRA_ERR_CUDA;
     }
-    const int tiles = rra::prompt_tiles(a);
     rra::PromptParams p;
-    p.a = a;
-    p.heads_of_kv = a.q_heads / a.kv_heads;
-    p.parts = (p.heads_of_kv + rra::kPromptRows - 1) / rra::kPromptRows;
-    p.group = (p.heads_of_kv + p.parts - 1) / p.parts;
-    p.span = rra::kPromptRows / p.group;
+    rra::prompt_sizes(p, a);
+    const int tiles = rra::prompt_tiles(p);
     p.window = std::min(a.window, 1 << 30);
     p.by_group = rra::Divisor(p.group);
     p.by_parts = rra::Divisor(p.parts);

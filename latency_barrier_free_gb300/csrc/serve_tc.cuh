@@ -143,16 +143,22 @@ struct PromptSegment {
     int32_t b, c, h, chunks, first_tile;
     int64_t begin, end;
 };
+// Its place in the row, by its begin.
 template <typename W>
-__device__ __forceinline__ void prompt_load(const W& w, PromptSegment& s) {
-    s.n = w.lengths(s.b);
+__device__ __forceinline__ void prompt_place(const W& w, PromptSegment& s) {
     s.chunks = w.chunks(s.n);
     const PromptItem t = w.item(s.n, s.c);
     s.first_tile = t.first_tile;
     s.end = s.begin + t.tiles + kPromptSegmentCost;
 }
 template <typename W>
-__device__ __forceinline__ void prompt_next(const W& w, PromptSegment& s) {
+__device__ __forceinline__ void prompt_load(const W& w, PromptSegment& s) {
+    s.n = w.lengths(s.b);
+    prompt_place(w, s);
+}
+// To the next one, but for its place.
+template <typename W>
+__device__ __forceinline__ void prompt_step(const W& w, PromptSegment& s) {
     s.begin = s.end;
     if (++s.c >= s.chunks) {
         s.c = 0;
@@ -161,6 +167,10 @@ __device__ __forceinline__ void prompt_next(const W& w, PromptSegment& s) {
             s.n = w.lengths(s.b);
         } while (s.n.qn == 0 && s.h < w.heads());  // some request has queries: there is a segment
     }
+}
+template <typename W>
+__device__ __forceinline__ void prompt_next(const W& w, PromptSegment& s) {
+    prompt_step(w, s);
     prompt_load(w, s);
 }
 

@@ -221,11 +221,14 @@ class PromptAttention(_Workspace):
         if st:
             raise rra.RraError(st, "rra_prompt_attention")
 
-    def plan_kernel(self, q_heads: int, kv_heads: int, *, max_len: int) -> str:
-        """Name of the kernel that attention() launches for so many heads, planned for max_len."""
+    def plan_kernel(self, q_heads: int, kv_heads: int, requests: int, *, max_len: int, tokens=None, head_dim: int = 128,
+                    causal: bool = True, window: int = 0) -> str:
+        """Name of the kernel that attention() launches for so many requests of max_len
+        tokens at most, and `tokens` rows (requests * max_len, if not given)."""
         some = self._workspace.data_ptr()  # planning reads no memory
+        rows = requests * max_len if tokens is None else tokens
         args = _PROMPT.pack(some, some, some, some, 0, some, some, q_heads * 128, 128, kv_heads * 128, 128, kv_heads * 128, 128,
-                            q_heads * 128, 128, 1, 1.0, 1, q_heads, kv_heads, 128, 0, max_len, 1, 0)
+                            q_heads * 128, 128, rows, 1.0, requests, q_heads, kv_heads, head_dim, 0, max_len, int(causal), window)
         name = ctypes.c_char_p()
         st = _lib().rra_prompt_attention_plan(args, ctypes.byref(name))
         if st:
@@ -244,6 +247,7 @@ class KvCache(_Workspace):
     it has to outlive, and for graphs that hold calls."""
 
     _size = staticmethod(kv_page_bytes)
+    _plan = "rra_kv_attention_plan"
 
     def __init__(self, pages, page_tokens: int, kv_heads: int, head_dim: int):
         lib = _lib()
@@ -292,9 +296,9 @@ class KvCache(_Workspace):
         args = _ATTN.pack(*_CACHE.unpack(self._cache), some, some, 0, some, some, some, some, q_heads * d, d, q_heads * d, d, 1,
                           requests, self._scale, requests, 1, q_heads, max_q, max_kv, 1, window, 0)
         name = ctypes.c_char_p()
-        st = _lib().rra_kv_attention_plan(args, ctypes.byref(name))
+        st = getattr(_lib(), self._plan)(args, ctypes.byref(name))
         if st:
-            raise rra.RraError(st, "rra_kv_attention_plan")
+            raise rra.RraError(st, self._plan)
         return name.value.decode()
 
     def copy(self, source, target, to=None, stream=None) -> None:
@@ -315,6 +319,7 @@ class KvCache8(KvCache):
     rra_serve.h)."""
 
     _size = staticmethod(kv8_page_bytes)
+    _plan = "rra_kv8_attention_plan"
 
     def append(self, k, v, slots, stream=None) -> None:
         """Write k and v [tokens, kv_heads, head_dim] to the slots (int64; negative:

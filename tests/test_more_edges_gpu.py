@@ -25,7 +25,8 @@ def i32(x):
 
 # one prompt that is cut into runs (few segments, long), many that are dealt out, and short ones
 @pytest.mark.parametrize("lengths,hq,hk,d", [([4000], 8, 1, 128), ([700, 30, 900, 0, 5] * 6, 16, 4, 64), ([20, 9], 4, 2, 128)])
-def test_after_a_wait_ran_out_the_next_prompt_is_right(serve, impatient, lengths, hq, hk, d):  # noqa: F811
+@pytest.mark.parametrize("max_len", [1, 10 ** 6])  # either kernel
+def test_after_a_wait_ran_out_the_next_prompt_is_right(serve, impatient, lengths, hq, hk, d, max_len):  # noqa: F811
     gen = torch.Generator(device="cuda").manual_seed(4)
     t = sum(lengths)
     q, k, v = torch.randn(t, hq + 2 * hk, d, generator=gen, device="cuda").bfloat16().split([hq, hk, hk], 1)
@@ -33,12 +34,12 @@ def test_after_a_wait_ran_out_the_next_prompt_is_right(serve, impatient, lengths
     prompts = serve.PromptAttention()
     want, lse = torch.empty(t, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(t, hq, device="cuda")
     out, lse2 = torch.empty_like(want), torch.empty_like(lse)
-    prompts.attention(q, k, v, want, cu, max_len=max(lengths), lse=lse)
+    prompts.attention(q, k, v, want, cu, max_len=max_len, lse=lse)
     assert prompts.status() == 0
     tok = (hq + 2 * hk) * d
     args = serve._PROMPT.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse2.data_ptr(), cu.data_ptr(),
                               prompts._workspace.data_ptr(), tok, d, tok, d, tok, d, hq * d, d, t, d ** -0.5, len(lengths), hq, hk, d,
-                              0, max(lengths), 1, 0)
+                              0, max_len, 1, 0)
     impatient.rra_prompt_attention.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
     for _ in range(2):
@@ -48,7 +49,7 @@ def test_after_a_wait_ran_out_the_next_prompt_is_right(serve, impatient, lengths
         head = prompts._workspace[:4096].view(torch.int32)
         assert status == 5 and (head[1:] == 0).all()
         prompts.reset()
-        prompts.attention(q, k, v, out, cu, max_len=max(lengths), lse=lse2)
+        prompts.attention(q, k, v, out, cu, max_len=max_len, lse=lse2)
         assert prompts.status() == 0 and torch.equal(out, want) and torch.equal(lse, lse2)
 
 
@@ -116,11 +117,11 @@ def test_kernels_that_need_tensor_memory_back_to_back(serve):
     for cache in caches:
         cache.append(k, v, torch.arange(n, device="cuda"))
     prompts = serve.PromptAttention()
-    assert [prompts.plan_kernel(hq, hk, max_len=m) for m in (1, n)] == ["prompt_attention_kernel<128 rows>", "prompt_attention_kernel<256 rows>"]
+    assert [prompts.plan_kernel(hq, hk, 1, max_len=m, tokens=n, head_dim=d) for m in (1, 10 ** 6)] == ["prompt_attention_kernel<128 rows>", "prompt_attention_kernel<256 rows>"]
 
     def calls(out):
         prompts.attention(q, k, v, out[0], cu, max_len=1)
-        prompts.attention(q, k, v, out[1], cu, max_len=n)
+        prompts.attention(q, k, v, out[1], cu, max_len=10 ** 6)
         for o, cache in zip(out[2:], caches):
             cache.attention(q, o, cu, kv, table, max_q=n, max_kv=n)
 

@@ -74,7 +74,7 @@ def test_prompt_refusals(serve):  # noqa: F811
         assert serve._lib().rra_prompt_attention(serve._PROMPT.pack(*args), 0) == rra.OK
     name = ctypes.c_char_p()
     plan = serve._lib().rra_prompt_attention_plan
-    for longest, rows in ((0, 128), (64, 128), (65, 256), (2 ** 31 - 1, 256)):
+    for longest, rows in ((0, 128), (64, 128), (100000, 256), (2 ** 31 - 1, 256)):
         args = list(good)
         args[names.index("max_len")] = longest
         assert plan(serve._PROMPT.pack(*args), ctypes.byref(name)) == rra.OK

@@ -171,14 +171,15 @@ BAD = {"nan": float("nan"), "inf": float("inf"), "-inf": float("-inf")}
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("what", sorted(BAD))
+@pytest.mark.parametrize("max_len", [1, 10 ** 6])  # either kernel
 @pytest.mark.parametrize("hq,hk,d,causal,window", [(4, 2, 64, True, 0), (2, 2, 128, True, 0), (8, 1, 128, True, 40), (4, 1, 64, False, 0)])
-def test_values_that_are_not_finite_reach_only_rows_that_see_them(serve, hq, hk, d, causal, window, what, dtype):
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(serve, hq, hk, d, causal, window, max_len, what, dtype):
     lengths = [150, 300, 7]
     q, k, v = build(np.random.default_rng(5), hq, hk, d, lengths, dtype, packed=False)
     cu = [0, 150, 450, 457]
     prompts = serve.PromptAttention()
     out, lse = torch.empty_like(q), torch.empty(457, hq, device="cuda")
-    run = lambda: prompts.attention(q, k, v, out, dev(np.array(cu, np.int32)), max_len=300, causal=causal, window=window, lse=lse)  # noqa: E731
+    run = lambda: prompts.attention(q, k, v, out, dev(np.array(cu, np.int32)), max_len=max_len, causal=causal, window=window, lse=lse)  # noqa: E731
     run()
     want, want_lse = out.clone(), lse.clone()
     places = [(0, 0, 3), (149, hk - 1, d - 1), (150 + 131, 0, 5), (150 + 131, 0, 6), (450, 0, 0), (456, hk - 1, 9)]
@@ -200,16 +201,17 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(serve, hq, hk,
     assert np.array_equal(got[~hit], was[~hit])
 
 
-def test_keys_and_queries_that_are_not_finite(serve):
+@pytest.mark.parametrize("max_len", [1, 10 ** 6])
+def test_keys_and_queries_that_are_not_finite(serve, max_len):
     """They make the rows that see the key, or have the query, NaN or infinite; no others change."""
     q, k, v = build(np.random.default_rng(6), 2, 1, 64, [200, 140], torch.bfloat16, packed=False)
     cu = dev(np.array([0, 200, 340], np.int32))
     prompts = serve.PromptAttention()
     out = torch.empty_like(q)
-    prompts.attention(q, k, v, out, cu, max_len=200)
+    prompts.attention(q, k, v, out, cu, max_len=max_len)
     want = out.clone()
     k[150, 0, 3], q[20, 1, 5] = float("nan"), float("inf")
-    prompts.attention(q, k, v, out, cu, max_len=200)
+    prompts.attention(q, k, v, out, cu, max_len=max_len)
     hit = torch.zeros(340, 2, dtype=torch.bool, device="cuda")
     hit[150:200] = True
     hit[20, 1] = True
@@ -231,7 +233,7 @@ def test_graphs_streams_and_other_calls(serve):
     assert torch.equal(out, want)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        for max_len in (1, 400, 1, 400):
+        for max_len in (1, 10 ** 6, 1, 400):
             prompts.attention(q, k, v, out, cu, max_len=max_len)
     for _ in range(3):
         out.zero_()
