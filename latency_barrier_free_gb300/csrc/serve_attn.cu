@@ -1,5 +1,6 @@
-// serve_attn.cu -- attention over the 4-bit cache for single tokens and a few
-// drafted ones (rra_serve.h); the arithmetic is in serve_attn_rows.cuh.
+// serve_attn.cu -- attention over the 4-bit and the 8-bit cache for single tokens
+// and a few drafted ones (rra_serve.h); the arithmetic is in serve_attn_rows.cuh and
+// serve_attn_rows8.cuh.
 //
 // Work is split by keys.  A segment is the rows of one request and KV head
 // that fit the instructions (8 NT); its tiles are 32 keys each.  All
@@ -16,6 +17,9 @@
 // 25 us of stream at 6 TB/s, then the joins.  64 ragged requests, 175 MB:
 // 44.9 us (3.9 TB/s).  Half the instructions are the unpacking of codes, and the
 // ALU pipe is half busy; four schedulers need the three warps each.
+//
+// Over the 8-bit cache 64 ragged requests, 312 MB, take 59.4 us (5.3 TB/s): 5 us to the
+// first copy, 46 of stream at 6.8 TB/s, the copy's own rate, and 6 to 8 of joins.
 #include <algorithm>
 #include <cmath>
 
@@ -638,6 +642,7 @@ static rra_status_t kv_attention(const rra_kv_attention_args_t* args, int bits, 
     using rra::Cache8;
     const bool eight = kernel == rra::kRows8;
     if (bits == 8) {
+        // pages are twice as large: one block a stage where two take the room of warps (64 ragged requests: 60.3 us, with two 61.8)
         if (args->cache.head_dim == 128)
             return eight ? rra::attn_launch<Cache8, 128, 1, 12, 2, 1>(p, ctas, stream) : rra::attn_launch<Cache8, 128, 2, 6, 2>(p, ctas, stream);
         return eight ? rra::attn_launch<Cache8, 64, 1, 12, 3>(p, ctas, stream) : rra::attn_launch<Cache8, 64, 2, 8, 3>(p, ctas, stream);

@@ -7,6 +7,10 @@
 // A run's values stay in registers from their maximum to their codes.
 //
 // Read.  A thread takes 8 channels of a row of K, and of V (16: 11.0 us against 7.9 for 8754 tokens of 8 heads of 128).
+//
+// Four prompts, 8754 tokens of 8 heads of 128, bfloat16, 108 MB: 22.9 us for both, 4.7 TB/s; the write 13.3 and the read
+// 7.8 us alone.  The read is at HBM's rate.  The write is bound by the chain list of tokens, slots, values, maximum, codes:
+// a third of the warps wait for memory, a fifth for the list.  One token for each request, 16: 4.4 us, launches and round trips.
 #include <algorithm>
 
 #include "serve_common.cuh"
@@ -14,7 +18,7 @@
 namespace rra {
 
 constexpr int kKv8Threads = 256;
-constexpr int kKv8Span = 16;      // tokens of a CTA where there are many
+constexpr int kKv8Span = 16;      // tokens of a CTA, at most
 
 struct Kv8Params {
     rra_kv_tokens_args_t a;
@@ -361,9 +365,13 @@ static rra_status_t kv8_tokens(const rra_kv_tokens_args_t* a, rra_stream_t strea
     dim3 grid;
     const void* k;
     if (append) {
-        // a CTA a token and four heads, a warp a row: where tokens are few each may be a block of its own
-        p.span = a->tokens * c.kv_heads <= 4096 ? 1 : kKv8Span;
+        // A CTA takes four heads of a token, of more tokens only where there are more CTAs than run at once: a decode step's
+        // tokens are blocks of their own, which its warps take one after the other.  (8 heads of 128, single tokens of 1, 2, 4, 8
+        // and 16 a CTA: 256 tokens 5.0, 5.5, 7.6, 12.7, 23.7 us; 1024 13.2, 12.2, 13.0, 15.1, 23.6; 4096 47, 42, 40, 40, 47.  A
+        // prompt's: 256 4.3, 4.2, 4.0, 3.7, 3.8; 1024 6.7, 5.7, 5.2, 5.1, 3.9; 8192 29.4, 19.7, 14.9, 12.3, 10.3.)
         p.heads = std::min(4, c.kv_heads);
+        const int64_t ctas = a->tokens * ((c.kv_heads + p.heads - 1) / p.heads);
+        for (p.span = 1; p.span < kKv8Span && ctas > 4 * 152 * p.span;) p.span *= 2;
         grid = dim3((unsigned)((a->tokens + p.span - 1) / p.span), (unsigned)((c.kv_heads + p.heads - 1) / p.heads));
         k = elem == 4 ? (big ? (const void*)kv8_append_kernel<float, 128> : (const void*)kv8_append_kernel<float, 64>)
                       : (big ? (const void*)kv8_append_kernel<__nv_bfloat16, 128> : (const void*)kv8_append_kernel<__nv_bfloat16, 64>);

@@ -4,6 +4,9 @@
 // The first three are bookkeeping, bound by latency like the slot map: one
 // cluster, whose barriers separate what is read from what is written to the same
 // buffers, and whose CTAs share rows and pages.  The copies are bound by HBM.
+//
+// One prompt into 8 samples 4.5 us with its copies, 32 into 8 each 12.4 (63 MB).  After 500 requests over 8192 pages
+// release takes 12.0 us, compaction 13.0, the copies of 5620 pages of 33 KB 58 (6.4 TB/s); after 9 requests 3.8, 5.3 and 1.5.
 #include <algorithm>
 
 #include "cluster_prims.cuh"
@@ -423,8 +426,9 @@ static int pages_ctas(int64_t items) {
     return ctas;
 }
 
-// Threads of a CTA: fewer warps meet sooner.
-static int pages_threads(int64_t items) { return items <= 1024 ? 256 : kPagesThreads; }
+// Threads of a CTA: fewer warps meet sooner.  (256, 512 and 1024: release, compaction and copies after 9 requests 11.0, 10.7 and
+// 11.4 us, after 30 14.2, 12.5 and 11.9.)
+static int pages_threads(int64_t items) { return items <= 768 ? 512 : kPagesThreads; }
 
 // Bytes of shared memory that so many pages take in each CTA.
 static size_t pages_bits(int pages, int ctas) { return ((size_t)pages / (size_t)ctas + 32) / 32 * 4 + 4; }

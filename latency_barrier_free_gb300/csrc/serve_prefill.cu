@@ -1,4 +1,4 @@
-// serve_prefill.cu -- attention over the 4-bit cache for prompts: many queries
+// serve_prefill.cu -- attention over the 4-bit or 8-bit cache for prompts: many queries
 // of a request at once (rra_serve.h), on the tensor cores' own memory.
 //
 // A row is one query of one head.  A CTA takes a segment: TILES x 128 rows of
@@ -33,6 +33,11 @@
 // rest), a wait of 250, its softmax (2000: reading the scores, their maximum, and
 // 128 exponentials a thread take about as long each).  TMEM has no room for the
 // next scores beside the weights, so only the other tile fills the gap.
+//
+// Over the 8-bit cache K is one binary16 number, its code: 271 GFLOP (3 requests of up
+// to 1024 queries) in 280 us, 970 TFLOP/s.  The products have 2048 of the 4150 cycles
+// for 256 rows and 128 keys; the softmax, one thread a row and one warp a scheduler,
+// takes 2300 to 3000 of one tile's chain, the products behind it 1070 and 340.
 #include <algorithm>
 #include <type_traits>
 

@@ -23,10 +23,18 @@
 // shared memory before products may read them; such elements become 0 there, and
 // rows that see them get them at their end.
 //
-// Segments are dealt out whole, the longest first, to and fro over the CTAs.  Where
-// that leaves CTAs idle (few long segments) they are cut into equal runs of key
-// tiles, one per CTA (serve_tc.cuh); what a run has of a segment it shares goes to
-// the workspace, and the last CTA to arrive adds the parts in order.
+// Few segments are dealt out whole, the longest first, to and fro over the CTAs.
+// Many, or where that leaves CTAs idle (a few long ones), are cut into equal runs
+// of key tiles, one per CTA (serve_tc.cuh); what a run has of a segment it shares
+// goes to the workspace, and the last CTA to arrive adds the parts in order.
+//
+// 64 heads over 8 of 128, bfloat16, two prompts of up to 8192 tokens, 1.1 TFLOP:
+// 770 us among other calls, 1430 TFLOP/s, at the power limit; 8 over 1, one of 16384
+// 358 us, 1535 TFLOP/s (large library products reach 1937).  The products of 256 rows
+// and 128 keys take 2080 cycles at their full rate; the pipe is 55 to 70 % busy.  The
+// rest is the chain of one tile, scores to weights (about 1000 cycles) and its two
+// products, where the other tile's products do not cover it.  Few short ones are
+// latency: 5 prompts, 14 heads over 2 of 64, take 9.6 us.
 #include <algorithm>
 #include <cmath>
 
@@ -39,8 +47,8 @@ namespace rra {
 
 constexpr int kDealRequests = 1024;  // up to so many requests segments are dealt out: their order is found in shared memory
 // And up to so many segments a CTA.  With more, runs are as even, and a CTA's next segment mostly reads the keys that the one
-// before it read (32 heads over 32: 16 requests of 1024 tokens, 14 segments a CTA, 215 us, in runs 206; 64 of 300, 27, 265 and 257.
-// 64 heads over 8: 64 of 512, 54, 503 and 481; 3 of 2000, 10, 184 and 193; one of 500, 1, 16.6 and 31.6).
+// before it read (32 heads over 32: 16 requests of 1024 tokens, 14 segments a CTA, 228 us, in runs 206; 64 of 300, 27, 277 and 257.
+// 64 heads over 8: 64 of 512, 54, 541 and 481; 3 of 2000, 10, 184 and 193; one of 500, 1, 16.6 and 31.6).
 constexpr int kDealItems = 10, kDealChunks = kDealItems * kPromptMaxCtas;
 constexpr int kDealExcess = 10;  // key tiles that a CTA may have above the mean: about what finding runs and joining parts costs
 
