@@ -75,6 +75,27 @@ def test_append_and_read(serve, case):
     assert torch.equal(kb, k.bfloat16()) and torch.equal(vb, v.bfloat16())
 
 
+@pytest.mark.parametrize("tokens", [500, 700, 1300, 2500, 5000])
+def test_runs_that_end_anywhere_among_a_ctas_tokens(serve, tokens):
+    """Runs of 1 to 40 neighbours from anywhere in a page, with skipped slots between: a CTA takes more tokens the more there are."""
+    d, ps, hk, num = 64, 64, 1, 3000
+    rng = np.random.default_rng(tokens)
+    slots, pages_left = [], rng.permutation(num).tolist()
+    while len(slots) < tokens:
+        first = int(rng.integers(0, ps))
+        run = (pages_left.pop() * ps + np.arange(first, min(ps, first + int(rng.integers(1, 41))))).tolist()
+        if rng.integers(0, 4) == 0:
+            run.insert(int(rng.integers(0, len(run) + 1)), -1)
+        slots += run
+    slots = slots[:tokens]
+    cache = cache_of(serve, num, ps, hk, d)
+    pages = cache.pages.cpu().numpy().copy()
+    x = dev(rng.standard_normal((tokens, hk, 2 * d)) * 10.0 ** rng.uniform(-3, 3, (tokens, 1, 1)), torch.bfloat16)
+    cache.append(x[..., :d], x[..., d:], dev(np.array(slots, np.int64)))
+    more.append8(pages, ps, hk, d, f64(x[..., :d]), f64(x[..., d:]), slots)
+    assert np.array_equal(cache.pages.cpu().numpy(), pages)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_what_rounding_does(serve, dtype):
     """Ties, the largest and smallest exponents, infinities, NaN, zeros of both signs."""
