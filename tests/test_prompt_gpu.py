@@ -105,6 +105,8 @@ CASES = {
     "not causal, a window": (4, 1, 64, [300], False, 50),
     "longer": (8, 1, 128, [1500], True, 0),
     "longer, not causal": (2, 2, 64, [1111], False, 0),
+    "more segments than are dealt out": (16, 16, 64, [(11 * i) % 150 for i in range(120)], True, 0),
+    "many of them and a window": (20, 20, 128, [(7 * i) % 40 for i in range(100)], True, 9),
     "many short": (4, 1, 64, [(7 * i) % 23 for i in range(300)], True, 0),
 }
 
@@ -202,6 +204,28 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(serve, hq, hk,
 
 
 @pytest.mark.parametrize("max_len", [1, 10 ** 6])
+@pytest.mark.parametrize("what", sorted(BAD))
+def test_values_that_are_not_finite_in_parts_that_are_joined(serve, what, max_len):
+    """One prompt whose segments several CTAs share."""
+    t, hq = 1800, 8
+    q, k, v = build(np.random.default_rng(9), hq, 1, 128, [t], torch.bfloat16, packed=False)
+    cu = dev(np.array([0, t], np.int32))
+    prompts = serve.PromptAttention()
+    out, lse, lse2 = torch.empty_like(q), torch.empty(t, hq, device="cuda"), torch.empty(t, hq, device="cuda")
+    prompts.attention(q, k, v, out, cu, max_len=max_len, lse=lse)
+    want = out.clone()
+    places = [(1790, 3), (1660, 127), (900, 64), (897, 64), (130, 5)]  # in tiles that some rows see in part
+    for token, c in places:
+        v[token, 0, c] = BAD[what]
+    prompts.attention(q, k, v, out, cu, max_len=max_len, lse=lse2)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    for token, c in places:
+        hit[token:, :, c] = True
+    assert not torch.isfinite(out[hit]).any() and torch.equal(out[~hit], want[~hit])
+    assert torch.equal(lse, lse2) and prompts.status() == 0
+
+
+@pytest.mark.parametrize("max_len", [1, 10 ** 6])
 def test_keys_and_queries_that_are_not_finite(serve, max_len):
     """They make the rows that see the key, or have the query, NaN or infinite; no others change."""
     q, k, v = build(np.random.default_rng(6), 2, 1, 64, [200, 140], torch.bfloat16, packed=False)
@@ -248,14 +272,15 @@ def test_graphs_streams_and_other_calls(serve):
     assert prompts.status() == 0
 
 
-def test_a_long_prompt(serve):
+@pytest.mark.parametrize("max_len", [1, 9001])
+def test_a_long_prompt(serve, max_len):
     """More key tiles than CTAs, runs that end inside segments; against binary32 on the GPU, row by row."""
     rng = np.random.default_rng(8)
     t, hq, hk, d = 9001, 4, 1, 128
     q, k, v = build(rng, hq, hk, d, [t], torch.bfloat16)
     out, prompts = torch.empty(t, hq, d, dtype=torch.bfloat16, device="cuda"), serve.PromptAttention()
     lse = torch.empty(t, hq, device="cuda")
-    prompts.attention(q, k, v, out, dev(np.array([0, t], np.int32)), max_len=t, lse=lse)
+    prompts.attention(q, k, v, out, dev(np.array([0, t], np.int32)), max_len=max_len, lse=lse)
     assert prompts.status() == 0
     for i in [0, 1, 127, 128, 4999, 8191, 8192, 9000] + rng.integers(0, t, 40).tolist():
         s = q[i].double() @ k[:i + 1, 0].double().T * d ** -0.5
