@@ -490,8 +490,11 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             auto hi_of = [&](int r) { return !is_live(r) ? INT32_MAX : a.causal ? token_of(r) + 1 : seg.n.qn; };
             const int edge_from = edge_of(seg).from, edge_to = edge_of(seg).to, first_tile = seg.first_tile;
             // What a row's weights are taken against, in units of log2 (kNone: it has seen no key yet), and their sum.
+            // Rows that are no rows (behind the group's heads or the prompt's tokens: what memory or the next prompt has there) have
+            // no say in the votes below, which change the others' roundings.
             constexpr float kNone = -FLT_MAX;
-            float top[2] = {kNone, kNone}, less[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // less: what is taken off scores
+            const bool votes[2] = {is_live(0), is_live(1)};
+            float top[2] = {votes[0] ? kNone : 0.f, votes[1] ? kNone : 0.f}, less[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // less: what is taken off scores
             bool fresh = true;  // some row has none
 #pragma unroll 1
             for (int tl = t0; tl < t1; ++tl, ++n) {
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                             split2(sum[r], a0, a1);
                             all[r] = a0 + a1;
                         }
-                        if (exact || !__any_sync(0xffffffffu, all[0] > Sh::kMost || all[1] > Sh::kMost)) break;
+                        if (exact || !__any_sync(0xffffffffu, (votes[0] && all[0] > Sh::kMost) || (votes[1] && all[1] > Sh::kMost))) break;
                         exact = true;
                     }
                     l[0] += all[0];
