@@ -126,7 +126,7 @@ __device__ __forceinline__ AttnLengths attn_lengths(const AttnParams& p, int b) 
 __device__ __forceinline__ void attn_row_scale(const AttnParams& p, float most, float& down, float& factor) {
     int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 : 0;
     e = min(max(e, -120), 120);
-    factor = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23);
+    factor = fminf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), FLT_MAX);  // infinite, it would make NaN of scores of 0
     down = __uint_as_float((uint32_t)(127 - e) << 23);
     if (p.scale_log2 < 0.f) down = -down;
     if (factor == 0.f) factor = 1.f, down = 0.f;  // every score is 0
