@@ -51,6 +51,10 @@ constexpr float kPromptSlack = 8.f;    // log2 of how far weights may pass 1 bef
 // row's sum counts them whole.  So they are taken 2^kPromptLift times as large: 2^(8 + 7) fits.  (131072 keys of one run, each
 // 2^-25.3 of the largest: without it their share, 0.3 % of the values' size, was missing.)
 constexpr float kPromptLift = 7.f, kPromptUnlift = 1.f / 128;
+// 8-bit cache: what scores are multiplied with, times a block's 2^k, has to be a number of binary32, neither 0 nor infinite.  With
+// less than 2^-90 scores (at most 2^50 before) are as good as 0; with more than 2^95 those that are not 0 (at least 2^-65 before)
+// are larger than scores may be.
+constexpr float kPromptLeast = 0x1p-90f, kPromptBeyond = 0x1p95f;
 constexpr float kPromptMost = 32768.f;  // 8-bit cache: what a block's weights of a row may add up to before the maximum moves
 
 template <typename F, int D, int TILES>
@@ -227,7 +231,8 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                             most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
                     }
                     attn_row_scale(p, most, down, factor);
-                    if constexpr (!kEight) factor *= 0.5f;  // K is held twice as large
+                    if constexpr (kEight) factor = fminf(fmaxf(factor, kPromptLeast), kPromptBeyond);
+                    else factor *= 0.5f;  // K is held twice as large
 #pragma unroll
                     for (int k = 0; k < D / 8; ++k) {
                         const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};

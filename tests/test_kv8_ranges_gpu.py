@@ -82,8 +82,20 @@ def check(serve, kind, q, k, v, lengths, queries, scale, causal=True, window=0, 
 
 
 @pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
+@pytest.mark.parametrize("scale,by", [(1e-37, 1.0), (2.0 ** -60, 2.0 ** -60), (1.0, 2.0 ** -119), (-1e-38, 2.0 ** -10), (1e-30, 2.0 ** 20)])
+def test_scores_that_are_next_to_nothing(serve, scale, by, d, hq, hk):
+    """Keys of zero and of normal sizes: every score is about 0."""
+    rng = np.random.default_rng(2)
+    lengths, queries = [300, 20], [140, 20]
+    k, v = rng.standard_normal((2, sum(lengths), hk, d))
+    k[32:64] = 0
+    k[100:] = 0
+    check(serve, 8, rng.standard_normal((sum(queries), hq, d)) * by, k, v, lengths, queries, scale)
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
 @pytest.mark.parametrize("scale,by", [(2.0 ** 40, 2.0 ** 60), (-(2.0 ** 50), 2.0 ** 50), (2.0 ** 100, 1.0), (2.0 ** 70, 2.0 ** 60), (2.0 ** 120, 2.0 ** 90)])
-@pytest.mark.parametrize("kind", [4])
+@pytest.mark.parametrize("kind", [8, 4])
 def test_large_scales_over_scores_of_zero(serve, kind, scale, by, d, hq, hk):
     """Keys that are large where queries are 0: every score is 0, whatever it is scaled with."""
     rng = np.random.default_rng(3)
