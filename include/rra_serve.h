@@ -297,10 +297,10 @@ rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const ch
  * call, its codes and exponents may not belong together.  A slot that occurs
  * twice gets either token's values, channel by channel.
  * rra_kv8_read, rra_kv8_attention: as rra_kv_read, rra_kv_attention; every code
- * and exponent enters exactly.  Codes are binary16 in the products, weights
- * too, against a maximum of score and exponent together: 2^10 (for prompts 2^7)
- * times as large, against their underflow, times 2^exponent.  The workspace is
- * the same. */
+ * and exponent enters exactly.  Codes are binary16 in the products, weights too:
+ * off by 2^-11 of themselves, or where they are small by 2^-24 of the largest; so
+ * a key adds an error of 2^-24 of its value at most, whatever the exponents of other
+ * blocks, and of values that a row does not see.  The workspace is the same. */
 size_t rra_kv8_page_bytes(int page_tokens, int kv_heads, int head_dim);
 rra_status_t rra_kv8_append(const rra_kv_tokens_args_t* args, rra_stream_t stream);
 rra_status_t rra_kv8_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);

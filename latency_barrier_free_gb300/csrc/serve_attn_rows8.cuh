@@ -8,10 +8,12 @@
 // The first is a multiply of the finished score.  The second is not worth one for
 // every output and block; instead 2^xv goes into the weight's exponent,
 //     w = 2^((s - m) factor + xv - x),
-// against a maximum (m, x) of score and exponent together, so that weights stay
-// within binary16 whatever the blocks' exponents; the softmax's own sum gets
-// 2^(x - xv) of a block's weights, in binary32.  Nothing is lost that the result
-// would show: the largest w is near 2^lift, and errors are relative to it.
+// with m the maximum and x an exponent for the sums; the softmax's own sum gets
+// 2^(x - xv) of a block's weights, in binary32.  For w to be in binary16's range x
+// becomes xv where that is larger, and also where it is smaller by kKv8Apart or more:
+// a block's exponent may be that of values which a row does not see, or of other
+// channels, and must not cost what the row does see its bits.  The sums, in binary32,
+// have room for all exponents at once.
 //
 // A lane takes D / 4 channels in a row of a key (operands of the first product:
 // the sum's order is free) and D / 8 of four keys (the second's rows are channels,
@@ -21,6 +23,10 @@
 #include "serve_attn_rows.cuh"
 
 namespace rra {
+
+// How far a block's exponent may be below that of the sums.  A weight, near 2^lift where it counts most, is rounded by 2^-25 at
+// least: 2^(kKv8Apart - lift - 25) of what its key would count for alone, for prompts (lift 7) 2^-24.
+constexpr int kKv8Apart = 8;
 
 template <int D, int NT>
 struct AttnRows8 : AttnRange<NT> {
@@ -34,15 +40,15 @@ struct AttnRows8 : AttnRange<NT> {
     uint4 raw[NT][kWide];           // queries as they are, channels D / 4 t ..: loaded some time before start()
     uint32_t q[NT][kSteps][2];      // as B operands, each row scaled to [1, 2) by a power of two
     float factor[NT][2];            // of columns 2 t, 2 t + 1: |softmax scale| times that power, above 0
-    // The weights' maximum: score m (-FLT_MAX: no key yet) and exponent x; sum l, of 2^((s - m) factor + lift).
+    // Maximum m (-FLT_MAX: no key yet), exponent x of the sums; sum l, of 2^((s - m) factor + lift).
     float m[NT][2], l[NT][2];
-    int x[NT][2];
+    int x;                          // the same for all rows of the warp
     float acc[kSteps][NT][4];       // of 2^((s - m) factor + xv - x + lift) times codes; channels D / 8 g + 2 i, + 1
 
     __device__ __forceinline__ float top(int n, int k) const { return fmaxf(m[n][k] * factor[n][k], -FLT_MAX) - kAttnLift; }
     // Of column 2 t + k of n-tile n: channels channel(j, g) .. + 3 (not divided by the sum)
     __device__ __forceinline__ float4 output(int j, int n, int k) const {
-        const float up = two_to(x[n][k]);
+        const float up = two_to(x);
         return make_float4(acc[2 * j][n][k] * up, acc[2 * j][n][k + 2] * up, acc[2 * j + 1][n][k] * up, acc[2 * j + 1][n][k + 2] * up);
     }
 
@@ -83,9 +89,10 @@ struct AttnRows8 : AttnRange<NT> {
             for (int k = 0; k < 2; ++k) {
                 factor[n][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
                 this->add(p, n, k, c * kRows + 8 * n + 2 * t + k, rows, qn, kv);
-                m[n][k] = -FLT_MAX, l[n][k] = 0.f, x[n][k] = 0;
+                m[n][k] = -FLT_MAX, l[n][k] = 0.f;
             }
         }
+        x = kKv8Low;
         this->meet();
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
@@ -141,15 +148,16 @@ struct AttnRows8 : AttnRange<NT> {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) s[n][k] = this->sees(n, k & 1, key0 + g + 8 * (k >> 1)) ? s[n][k] : -INFINITY;
         }
-        // ---- does a weight pass the running maximum? ----
+        // ---- does a weight get large, or are all far from it? ----
         const int xv = kv8_exponent(exponents, 1);
-        bool moves = false;
+        bool moves = xv < x - kKv8Apart;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                moves |= fmaf(fmaxf(s[n][k], s[n][k + 2]) - m[n][k], factor[n][k], (float)(xv - x[n][k])) > kAttnSlack;
+                moves |= fmaf(fmaxf(s[n][k], s[n][k + 2]) - m[n][k], factor[n][k], (float)(xv - x)) > kAttnSlack;
         if (__any_sync(0xffffffffu, moves)) {
+            const int to = xv > x || xv < x - kKv8Apart ? xv : x;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -158,18 +166,17 @@ struct AttnRows8 : AttnRange<NT> {
                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 4));
                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
-                    const float up = fmaf(now - m[n][k], factor[n][k], (float)(xv - x[n][k]));
-                    if (!(up > 0.f)) continue;
-                    l[n][k] *= exp2_fast((m[n][k] - now) * factor[n][k]);
+                    now = fmaxf(now, m[n][k]);
+                    const float up = (m[n][k] - now) * factor[n][k], by = exp2_fast(up + (float)(x - to));
+                    l[n][k] *= exp2_fast(up);
                     m[n][k] = now;
-                    x[n][k] = xv;
-                    const float by = exp2_fast(-up);
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) {
                         acc[i][n][k] *= by;
                         acc[i][n][k + 2] *= by;
                     }
                 }
+            x = to;
         }
         // ---- weights, and their products with the values ----
         uint32_t b0[NT], b1[NT];
@@ -178,9 +185,9 @@ struct AttnRows8 : AttnRange<NT> {
             float e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                e[k] = exp2_fast(fmaf(s[n][k] - m[n][k & 1], factor[n][k & 1], kAttnLift + (float)(xv - x[n][k & 1])));
+                e[k] = exp2_fast(fmaf(s[n][k] - m[n][k & 1], factor[n][k & 1], kAttnLift + (float)(xv - x)));
 #pragma unroll
-            for (int k = 0; k < 2; ++k) l[n][k] = fmaf(e[k] + e[k + 2], two_to(x[n][k] - xv), l[n][k]);
+            for (int k = 0; k < 2; ++k) l[n][k] = fmaf(e[k] + e[k + 2], two_to(x - xv), l[n][k]);
             b0[n] = transpose8(pack_half2(e[0], e[1]));  // row g, keys 2 t and 2 t + 1
             b1[n] = transpose8(pack_half2(e[2], e[3]));  // row g, keys 2 t + 8 and + 9
         }

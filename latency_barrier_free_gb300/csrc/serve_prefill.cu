@@ -35,7 +35,7 @@
 // next scores beside the weights, so only the other tile fills the gap.
 //
 // Over the 8-bit cache K is one binary16 number, its code: 271 GFLOP (3 requests of up
-// to 1024 queries) in 280 us, 970 TFLOP/s.  The products have 2048 of the 4150 cycles
+// to 1024 queries) in 285 us, 950 TFLOP/s.  The products have 2048 of the 4150 cycles
 // for 256 rows and 128 keys; the softmax, one thread a row and one warp a scheduler,
 // takes 2300 to 3000 of one tile's chain, the products behind it 1070 and 340.
 #include <algorithm>
@@ -55,6 +55,12 @@ constexpr float kPromptLift = 7.f, kPromptUnlift = 1.f / 128;
 // less than 2^-90 scores (at most 2^50 before) are as good as 0; with more than 2^95 those that are not 0 (at least 2^-65 before)
 // are larger than scores may be.
 constexpr float kPromptLeast = 0x1p-90f, kPromptBeyond = 0x1p95f;
+// A tile's blocks whose units of values are far apart (kKv8Apart), or far below those that maxima are against, do not enter one
+// product: binary16 has no weights for both.  The blocks down to kKv8Apart below the highest unit come first, then those down to
+// kKv8Apart below the highest that is left, and so on, each time with weights against their own maximum, O and l being brought to
+// it: not below 2^-kPromptRange of the highest so far, so that they stay numbers of binary32.
+constexpr float kPromptAbsent = -100.f;  // unit of a block that is not there
+constexpr float kPromptRange = 56.f;
 constexpr float kPromptMost = 32768.f;  // 8-bit cache: what a block's weights of a row may add up to before the maximum moves
 
 template <typename F, int D, int TILES>
@@ -106,6 +112,14 @@ struct CacheWork {
     }
 };
 
+// The highest unit of a tile's values below those that a product takes; kPromptAbsent: none.
+__device__ __forceinline__ float next_unit(const float4* ex, float unit) {
+    float most = kPromptAbsent;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) most = ex[b].y < unit - kKv8Apart ? fmaxf(most, ex[b].y) : most;
+    return most;
+}
+
 template <typename F, int D, int TILES>
 __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_attention_prompt_kernel(const __grid_constant__ AttnParams p) {
     using Sh = PromptShape<F, D, TILES>;
@@ -113,11 +127,14 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
     constexpr int J = D / kKvGroup;
     constexpr bool kEight = F::kBits == 8;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ __align__(8) uint64_t bar_mem[5 * TILES + 4 + 2 + 4 + 1 + 8];
+    __shared__ __align__(8) uint64_t bar_mem[7 * TILES + 4 + 2 + 4 + 1 + 8];
     __shared__ int64_t part[Sh::kWarps];
     __shared__ volatile uint32_t seen_words[4][4];  // of the last four tiles, which keys are there
     __shared__ volatile int32_t places[4][9];  // of four tiles: the cache's blocks of its keys (-1: none), and how many keys there are
-    __shared__ int2 exponents[4][8];  // 8-bit cache: of K and V in the blocks of four tiles
+    // 8-bit cache, of eight tiles, of each block: 2^exponent of K, exponent of V, 2 to minus that, and infinity if the tile's units
+    // are far apart, else 0.  And of each row its highest maximum in such a tile.
+    __shared__ float4 exponents[8][8];
+    __shared__ float highest[kEight ? TILES * kPromptRows : 1];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t arrived[2][TILES];  // of the run's first and last segment
     __shared__ volatile uint32_t added[2][TILES];    // whether this CTA has counted itself there
@@ -133,7 +150,8 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
     // q_full[i], pv_full[i]: what the next products of tile i wait for, with their turn; s_full[i], o_full[i]: done
     const uint32_t q_full = bars, s_full = q_full + 8 * TILES, pv_full = s_full + 8 * TILES, o_full = pv_full + 8 * TILES,
                    joined = o_full + 8 * TILES, k_full = joined + 8 * TILES, k_empty = k_full + 16, v_empty = k_empty + 16,
-                   seen_full = v_empty + 16, drained = seen_full + 32, place_full = drained + 8, place_empty = place_full + 32;
+                   seen_full = v_empty + 16, drained = seen_full + 32, place_full = drained + 8, place_empty = place_full + 32,
+                   part_full = place_empty + 32, part_done = part_full + 8 * TILES;  // of a tile's further products
     constexpr uint32_t kTurn = TILES == 2 ? 1 : 0;
     pdl_release_early();
     if (tid == 0) {
@@ -144,6 +162,8 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             mbar_init(pv_full + 8 * i, kPromptRows + 128 + kTurn);
             mbar_init(o_full + 8 * i, 1);
             mbar_init(joined + 8 * i, kPromptRows);
+            mbar_init(part_full + 8 * i, kPromptRows);
+            mbar_init(part_done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(v_empty + 8 * i, TILES);
@@ -189,6 +209,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
 
     uint32_t n = 0;   // key tiles of this run so far
     uint32_t sn = 0;  // segments so far that had tiles
+    uint32_t pn = 0;  // further products of a tile so far
     bool ok = true;
     if (warp < Sh::kSoftmaxWarps) {
         // =============================== softmax: a thread has a row ====
@@ -203,6 +224,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             const bool live = r < all_rows;
             constexpr float kNone = -FLT_MAX;  // no key yet
             // (8-bit cache: m is in units of log2, and O and l are 2^-m as large; l has no 2^v)
+            if (kEight) highest[tid] = kNone;
             float m = kEight && !live ? 0.f : kNone, limit = kNone, l = 0.f, factor = 1.f;
             if (t0 < t1) {
                 // ---- the row's query, scaled, into shared memory; the keys that it sees ----
@@ -274,8 +296,69 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                         // As in serve_attn_rows8.cuh: a block of 16 keys has the exponents k and v; scores are v[] 2^k, weights
                         // 2^(score factor + v - m), the sum's parts 2^-v as large.  m (kNone: no key yet) is the largest such
                         // exponent of the row's first tile, until weights get large, which their sum shows.
-                        const int2* const ex = exponents[n & 3];
+                        const float4* const ex = exponents[n & 7];
                         for (bool exact = __any_sync(0xffffffffu, m == kNone);; exact = true) {
+                            if (exact && __any_sync(0xffffffffu, ex[0].w != 0.f)) {  // units that are far apart
+                                float unit = next_unit(ex, INFINITY);
+                                uint32_t to = pv_full;
+#pragma unroll 1
+                                while (true) {
+                                    auto takes = [&](int b) { return ex[b].y <= unit && ex[b].y >= unit - kKv8Apart; };
+                                    float now = -INFINITY;
+#pragma unroll
+                                    for (int b = 0; b < 8; ++b) {
+                                        float top = -INFINITY;
+#pragma unroll
+                                        for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(v[16 * b + k]));
+                                        if (takes(b)) now = fmaxf(now, fmaf(top, factor * ex[b].x, ex[b].y));
+                                    }
+                                    const float high = fmaxf(fmaxf(highest[tid], m), now);
+                                    highest[tid] = high;
+                                    now = fmaxf(now, high - kPromptRange);  // a row that sees none of the blocks is ready for any
+                                    const float by = exp2_fast(m - now);
+                                    m = now;
+                                    l *= by;
+                                    if (tl > t0 || to != pv_full)
+#pragma unroll 1
+                                        for (int q = 0; q < D / 16; ++q) {
+                                            uint32_t o[16];
+                                            tc_ld16(o_at + 16 * q, o);
+                                            tc_wait_ld();
+#pragma unroll
+                                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                                            tc_st16(o_at + 16 * q, o);
+                                        }
+                                    const float less = m == kNone ? 0.f : kPromptLift - m;
+#pragma unroll
+                                    for (int b = 0; b < 8; b += 2) {
+                                        uint32_t w[16];
+#pragma unroll
+                                        for (int c = b; c < b + 2; ++c) {
+                                            const float up = factor * ex[c].x, off = takes(c) ? less + ex[c].y : -INFINITY;
+                                            float sum = 0.f;
+#pragma unroll
+                                            for (int k = 0; k < 16; k += 2) {
+                                                const float e0 = exp2_fast(fmaf(__uint_as_float(v[16 * c + k]), up, off));
+                                                const float e1 = exp2_fast(fmaf(__uint_as_float(v[16 * c + k + 1]), up, off));
+                                                sum += e0 + e1;
+                                                w[8 * (c - b) + k / 2] = pack_half2(e0, e1);
+                                            }
+                                            l = fmaf(sum, ex[c].z, l);
+                                        }
+                                        tc_st16(s_at + 8 * b, w);
+                                    }
+                                    unit = next_unit(ex, unit);
+                                    tc_wait_st();
+                                    tc_before_sync();
+                                    mbar_arrive(to + 8 * i);
+                                    to = part_full;
+                                    if (unit == kPromptAbsent) break;
+                                    ok = wait(part_done + 8 * i, pn++);
+                                    if (!ok) break;
+                                    tc_after_sync();
+                                }
+                                goto given;
+                            }
                             if (exact) {
                                 float now = -INFINITY;
 #pragma unroll
@@ -283,7 +366,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                                     float top = -INFINITY;
 #pragma unroll
                                     for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(v[16 * b + k]));
-                                    now = fmaxf(now, fmaf(top, factor * two_to(ex[b].x), (float)ex[b].y));
+                                    now = fmaxf(now, fmaf(top, factor * ex[b].x, ex[b].y));
                                 }
                                 now = fmaxf(m, now);
                                 const float by = exp2_fast(m - now);
@@ -302,14 +385,14 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                                 }
                             }
                             const float less = m == kNone ? 0.f : kPromptLift - m;
-                            float most = 0.f, all = 0.f;
+                            float most = ex[0].w, all = 0.f;
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
                                 uint32_t w[32];
 #pragma unroll
                                 for (int b = 4 * q; b < 4 * q + 4; ++b) {
-                                    const int2 e = ex[b];
-                                    const float by = factor * two_to(e.x), off = less + (float)e.y;
+                                    const float4 e = ex[b];
+                                    const float by = factor * e.x, off = less + e.y;
                                     const uint64_t by2 = pair2(by, by), off2 = pair2(off, off);
                                     uint64_t sum = pair2(0.f, 0.f);
 #pragma unroll
@@ -324,7 +407,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                                     float a0, a1;
                                     split2(sum, a0, a1);
                                     most = fmaxf(most, a0 + a1);
-                                    all = fmaf(a0 + a1, two_to(-e.y), all);
+                                    all = fmaf(a0 + a1, e.z, all);
                                 }
                                 tc_st32(s_at + 32 * q, w);
                             }
@@ -336,6 +419,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                         tc_wait_st();
                         tc_before_sync();
                         mbar_arrive(pv_full + 8 * i);
+                    given:
                         continue;
                     }
                     float tops[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
@@ -536,7 +620,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             constexpr int kLanes = D / 16, kStep = 128 / kLanes, kTurns = kPromptKeys / kStep;
             const int thread = tid & 127, piece = thread % kLanes, key0 = thread / kLanes, unpacker = warp - Sh::kUnpack;
             uint4 k[kTurns], v[kTurns];  // K of tile n, V of tile n - 1
-            uint32_t ex = 0u;            // lanes 0 and 1: exponents of blocks 2 unpacker, 2 unpacker + 1
             uint32_t there = 0u;         // which keys of this warp's word are there
             int32_t blocks[8], count = 0;
             auto places_of = [&](uint32_t t) {
@@ -560,9 +643,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                     if (w == unpacker) low = blocks[2 * w], high = blocks[2 * w + 1];
                 const int keys = min(max(count - 32 * unpacker, 0), 32);
                 there = ((low >= 0 ? 0xffffu : 0u) | (high >= 0 ? 0xffff0000u : 0u)) & (keys == 32 ? 0xffffffffu : (1u << keys) - 1u);
-                const int block = lane == 0 ? low : high;
-                ex = 0u;
-                if (lane < 2 && block >= 0 && 16 * lane < keys) ex = *(const uint32_t*)((const char*)a.cache.pages + (int64_t)block * B::kBytes + B::kExponents);
             };
             auto unpack = [&](const uint4& c, int key, uint32_t to) {
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -575,7 +655,6 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                     sts_v4(to + (piece >> 2) * Sh::kPanel + key * 128 + ((((piece & 3) * 2 + e) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
                 }
             };
-            uint32_t now_there = 0u, now_ex = 0u;
             if (left > 0) {
                 ok = wait(place_full, 0);
                 if (ok) {
@@ -588,11 +667,10 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             for (int64_t tile = 0; ok && tile <= left && left > 0; ++tile) {
                 const uint32_t t = (uint32_t)tile, stage = t & 1;
                 if (tile < left) {
-                    now_there = there, now_ex = ex;
-                    if (lane < 2) exponents[t & 3][2 * unpacker + lane] = make_int2(kv8_exponent(now_ex, 0), kv8_exponent(now_ex, 1));
-                    if (lane == 0) seen_words[t & 3][unpacker] = now_there;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(seen_full + 8 * (t & 3));
+                    if (lane == 0) {
+                        seen_words[t & 3][unpacker] = there;
+                        mbar_arrive(seen_full + 8 * (t & 3));
+                    }
                     if (tile >= 2) ok = wait(k_empty + 8 * stage, (t >> 1) - 1);
                     if (!ok) break;
 #pragma unroll
@@ -747,22 +825,47 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
             // =============================== another warp looks up pages, up to four tiles ahead of the unpacking ====
             // (by the unpacking warps themselves, lookups and addresses took a quarter of a tile's time: 270 us against 259)
             const int ps = a.cache.page_tokens, blocks = ps / kKvBlockTokens;
+            constexpr int kAhead = kEight ? 4 : 1;  // tiles looked up at once: the exponents are another round trip
             uint32_t t = 0;
             for (PromptSegment s = seg; ok;) {
                 const int end = end_of(s);
-                for (int tl = first_of(s); ok && tl < end; ++tl, ++t) {
+                float unit = kPromptAbsent;  // of values, that maxima are against or about to be
+                for (int tl = first_of(s); ok && tl < end; tl += kAhead) {
                     const int key0 = (s.first_tile + tl) * kPromptKeys, key = key0 + kKvBlockTokens * lane;
                     int block = -1;
-                    if (lane < kPromptKeys / kKvBlockTokens && key < s.n.kv) {
+                    if (lane < kAhead * 8 && tl + (lane >> 3) < end && key < s.n.kv) {
                         const int at = p.by_page(key), page = a.block_table[s.b * a.table_stride + at];
                         if (page >= 0 && page < a.cache.num_pages) block = (page * a.cache.kv_heads + s.h) * blocks + (key - at * ps) / kKvBlockTokens;
                     }
-                    if (t >= 4) ok = wait(place_empty + 8 * (t & 3), (t >> 2) - 1);
-                    if (!ok) break;
-                    if (lane < kPromptKeys / kKvBlockTokens) places[t & 3][lane] = block;
-                    if (lane == 0) places[t & 3][8] = min(kPromptKeys, s.n.kv - key0);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(place_full + 8 * (t & 3));
+                    float4 ex = make_float4(1.f, kPromptAbsent, 1.f, 0.f);
+                    if constexpr (kEight) {
+                        if (block >= 0) {
+                            const uint32_t w = *(const uint32_t*)((const char*)a.cache.pages + (int64_t)block * B::kBytes + B::kExponents);
+                            ex = make_float4(two_to(kv8_exponent(w, 0)), (float)kv8_exponent(w, 1), two_to(-kv8_exponent(w, 1)), 0.f);
+                        }
+                    }
+                    for (int x = 0; x < kAhead && tl + x < end; ++x, ++t) {
+                        const bool mine = lane >> 3 == x;
+                        if (kEight) {
+                            const bool here = mine && ex.y != kPromptAbsent;
+                            auto highest_below = [&](float y) { return (float)__reduce_max_sync(0xffffffffu, here && ex.y < y ? (int)ex.y : (int)kPromptAbsent); };
+                            const float most = highest_below(INFINITY), least = (float)__reduce_min_sync(0xffffffffu, here ? (int)ex.y : -(int)kPromptAbsent);
+                            unit = fmaxf(unit, most);
+                            if (unit - least > kKv8Apart) {  // (no block: least is above all)
+                                ex.w = mine ? INFINITY : ex.w;
+                                for (float next = most; next != kPromptAbsent; next = highest_below(unit - kKv8Apart)) unit = next;
+                            }
+                        }
+                        if (t >= 4) ok = wait(place_empty + 8 * (t & 3), (t >> 2) - 1);
+                        if (!ok) break;
+                        if (mine) {
+                            places[t & 3][lane & 7] = block;
+                            if (kEight) exponents[t & 7][lane & 7] = ex;
+                        }
+                        if (lane == 0) places[t & 3][8] = min(kPromptKeys, s.n.kv - key0 - x * kPromptKeys);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(place_full + 8 * (t & 3));
+                    }
                 }
                 if (s.end >= r1) break;
                 prompt_next(work, s);
@@ -780,6 +883,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
         while (ok) {
             const int t0 = first_of(seg), t1 = end_of(seg);
             if (t0 < t1) {
+                bool far = false;  // whether the units of the tile whose products come next are far apart
 #pragma unroll 1
                 for (int tl = t0 - 1; tl < t1; ++tl) {  // products of tile tl, scores of the next
                     const bool values = tl >= t0, next = tl + 1 < t1;
@@ -789,11 +893,27 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                     if (!ok) break;
                     tc_after_sync();
                     const uint32_t k_at = k_desc + (then & 1) * Sh::kParts * kStep;
+                    bool sums = tl > t0;
+                    if (far) {  // all but the last of its products
+                        const float4* const ex = exponents[n & 7];
+                        for (float unit = next_unit(ex, next_unit(ex, INFINITY)); ok && unit != kPromptAbsent; unit = next_unit(ex, unit)) {
+                            if (elected()) {
+#pragma unroll 1
+                                for (int k = 0; k < kPromptKeys / 16; ++k) tc_mma_ts(o_at, s_at + 8 * k, v_desc + k * (2048 >> 4), kPv, sums || k > 0);
+                                tc_commit(part_done + 8 * i);
+                            }
+                            __syncwarp();
+                            ok = wait(part_full + 8 * i, pn++);
+                            tc_after_sync();
+                            sums = true;
+                        }
+                        if (!ok) break;
+                    }
                     if (elected()) {
                         if (values) {  // O_i += P_i V
 #pragma unroll
                             for (int k = 0; k < kPromptKeys / 16; ++k) {
-                                tc_mma_ts(o_at, s_at + 8 * k, v_desc + k * (2048 >> 4), kPv, tl > t0 || k > 0);
+                                tc_mma_ts(o_at, s_at + 8 * k, v_desc + k * (2048 >> 4), kPv, sums || k > 0);
                                 if (k == kPromptKeys / 32 - 1) tc_commit(v_empty);
                             }
                             tc_commit(v_empty + 8);
@@ -814,6 +934,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                     }
                     __syncwarp();
                     n = then;
+                    far = kEight && next && __any_sync(0xffffffffu, exponents[n & 7][0].w != 0.f);
                 }
                 ++sn;
             }

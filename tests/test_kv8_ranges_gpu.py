@@ -1,9 +1,13 @@
-"""The caches' attention where scales, queries and scores are very small or large."""
+"""The 8-bit cache at the ends of its ranges: exponents far apart, of values that a row does not see too, and scales and queries
+that are very small or large."""
+import ctypes
+
 import numpy as np
 import pytest
 
 import serve_ref as ref
 from test_kv8_gpu import U8, U16, U32, dev, f64, plans, score_error
+from test_serve_edges_gpu import arguments, impatient  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -79,6 +83,62 @@ def check(serve, kind, q, k, v, lengths, queries, scale, causal=True, window=0, 
             assert not bad.any(), (name, bad.sum(), np.argwhere(bad)[:4], np.max(np.abs(f64(out[a:b]) - want)[bad] / tol[bad]))
             tol = off + (n + 64) * U32 + 4 * U32 * np.abs(want_lse)
             assert (np.abs(f64(lse[a:b]) - want_lse) <= tol).all(), name
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (False, 0)])
+@pytest.mark.parametrize("gap", [7, 8, 9, 20, 28, 32, 36, 40, 60])
+def test_values_far_apart(serve, gap, causal, window, d, hq, hk):
+    """Single values 2^gap times as large as the others, in one channel: rows that do not see them, and other channels, keep what
+    they have."""
+    rng = np.random.default_rng(gap)
+    lengths, queries = [700, 33, 150], [230, 1, 150]
+    k, v = rng.standard_normal((2, sum(lengths), hk, d))
+    v *= 2.0 ** -20
+    for token, channel in [(95, 3), (480, d - 1), (515, 8), (693, 0), (700 + 2, 5), (733 + 17, 1), (733 + 149, 2)]:
+        v[token, :, channel] = 2.0 ** (gap - 20)
+    check(serve, 8, rng.standard_normal((sum(queries), hq, d)), k, v, lengths, queries, d ** -0.5, causal, window)
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
+def test_values_that_rise_and_fall(serve, d, hq, hk):
+    """Blocks' units go up and down by up to 2^60, and so does which of them counts most."""
+    rng = np.random.default_rng(1)
+    lengths, queries = [1000, 400], [260, 2]
+    k, v = rng.standard_normal((2, sum(lengths), hk, d))
+    blocks = np.arange(sum(lengths)) // 16
+    v *= (2.0 ** np.array([-20, 20, 0, -38, 22, -1, 21, -30, 7, 8, 0, 16, -16]))[blocks % 13][:, None, None]
+    v *= np.where(rng.random((sum(lengths), 1, d)) < 0.9, 1, 0)
+    check(serve, 8, rng.standard_normal((sum(queries), hq, d)), k, v, lengths, queries, 2.0)
+    k *= np.exp2(rng.integers(-6, 6, len(blocks)))[:, None, None]
+    check(serve, 8, rng.standard_normal((sum(queries), hq, d)), k, v, lengths, queries, 0.2, window=300)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_after_a_wait_ran_out_among_values_far_apart(serve, impatient, d):  # noqa: F811
+    rng = np.random.default_rng(5)
+    lengths, queries, hq, hk = [3000, 500], [400, 60], 8, 2
+    k, v = rng.standard_normal((2, sum(lengths), hk, d))
+    v *= (2.0 ** (np.arange(sum(lengths)) // 16 % 5 * 12 - 30))[:, None, None]
+    cache, table, _, _ = filled(serve, 8, k, v, 64, lengths)
+    cu, kv_len = dev(np.cumsum([0] + queries).astype(np.int32)), dev(np.array(lengths, np.int32))
+    q = dev(rng.standard_normal((sum(queries), hq, d)).astype(np.float32)).bfloat16()
+    impatient.rra_kv8_attention.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    flush, ran_out = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), 0
+    for max_q, max_kv in plans(cache, hq, len(lengths)).values():
+        want, lse = torch.empty_like(q), torch.empty(q.shape[0], hq, device="cuda")
+        out, lse2 = torch.empty_like(want), torch.empty_like(lse)
+        cache.attention(q, want, cu, kv_len, table, max_q=max_q, max_kv=max_kv, lse=lse)
+        assert cache.status() == 0
+        flush.zero_()
+        args = arguments(serve, cache, q, out, lse2, cu, kv_len, table, max_q, max_kv)
+        assert impatient.rra_kv8_attention(args, torch.cuda.current_stream().cuda_stream) == 0
+        ran_out += cache.status() == 5
+        assert (cache._workspace[:4096].view(torch.int32)[1:] == 0).all()
+        cache.reset()
+        cache.attention(q, out, cu, kv_len, table, max_q=max_q, max_kv=max_kv, lse=lse2)
+        assert cache.status() == 0 and torch.equal(out, want) and torch.equal(lse, lse2)
+    assert ran_out >= 5
 
 
 @pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1)])
