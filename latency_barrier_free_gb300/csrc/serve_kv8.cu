@@ -11,6 +11,7 @@
 // Four prompts, 8754 tokens of 8 heads of 128, bfloat16, 108 MB: 22.5 us for both, 4.8 TB/s; the write 13.3 and the read
 // 7.8 us alone.  The read is at HBM's rate.  The write is bound by the chain list of tokens, slots, values, maximum, codes:
 // a third of the warps wait for memory, a fifth for the list.  One token for each request, 16: 4.4 us, launches and round trips.
+// Of a step of 8192 slots 16 that are not padding: the write takes 25 us, two CTAs having them all (of 16 slots: 3.1).
 #include <algorithm>
 
 #include "serve_common.cuh"
@@ -115,13 +116,41 @@ __device__ __forceinline__ int kv8_exponent_of(float most) {
     return min(max(e, kKv8Low), kKv8High);  // most = 0 and its neighbours end up at the lower one
 }
 
-// The next tokens of a run from `at` on, up to 16, into picks as token * 16 + row; skipped slots between them do not end it.
-// Where there are more (the same slots over and over), `at` becomes the next one's place and `more` true.  A whole warp.
-__device__ __forceinline__ int kv8_gather(const Kv8Params& p, int64_t& at, bool& more, int32_t* picks, const int64_t* slots, int64_t t0) {
+// The place of the nearest slot inside the cache from `from` on, forwards (1) or backwards (-1); -1: there is none.  The whole CTA:
+// steps of fixed shape may be padding for the most part, which a warp would pass a round trip to memory for every 32.
+template <int kWay>
+__device__ __forceinline__ int64_t kv8_find(const Kv8Params& p, int64_t from, int* nearest) {
+    constexpr int kLook = 8;  // of a thread at once
+    for (; kWay > 0 ? from < p.a.tokens : from >= 0; from += kWay * kLook * kKv8Threads) {
+        if (threadIdx.x == 0) *nearest = INT32_MAX;
+        int64_t s[kLook];
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            const int64_t t = from + kWay * (i * kKv8Threads + (int)threadIdx.x);
+            s[i] = t >= 0 && t < p.a.tokens ? p.a.slots[t] : -1;
+        }
+        int mine = INT32_MAX;
+#pragma unroll
+        for (int i = kLook - 1; i >= 0; --i) mine = (uint64_t)s[i] < (uint64_t)p.room ? i * kKv8Threads + (int)threadIdx.x : mine;
+        __syncthreads();
+        if (mine != INT32_MAX) atomicMin(nearest, mine);
+        __syncthreads();
+        const int n = *nearest;
+        __syncthreads();
+        if (n != INT32_MAX) return from + kWay * n;
+    }
+    return -1;
+}
+
+// The next tokens of a run from `at` on, after the n that picks has, up to 16, as token * 16 + row; skipped slots between them do
+// not end it.  Where there are more (the same slots over and over), `at` becomes the next one's place; with kPause also where 32
+// skipped slots come next, the place behind them.  A whole warp.
+enum Kv8Left { kNothing, kMore, kPadding };
+template <bool kPause>
+__device__ __forceinline__ Kv8Left kv8_gather(const Kv8Params& p, int64_t& at, int& n, int32_t* picks, const int64_t* slots, int64_t t0) {
     const int lane = (int)threadIdx.x & 31;
-    int n = 0;
     int64_t block = -1;
-    more = false;
+    Kv8Left left = kNothing;
     for (;; at += 32) {
         const int64_t t = at + lane, s = t - t0 < kKv8Span + kKvBlockTokens ? slots[t - t0] : t < p.a.tokens ? p.a.slots[t] : -1;
         if (block < 0) block = __shfl_sync(0xffffffffu, s, 0) >> 4;  // the first is inside the cache
@@ -135,13 +164,19 @@ __device__ __forceinline__ int kv8_gather(const Kv8Params& p, int64_t& at, bool&
         n += __popc(in);
         if (over != 0u) {
             at += __ffs((int)over) - 1;
-            more = true;
+            left = kMore;
             break;
         }
         if (ends != 0u) break;
+        if (kPause && in == 0u) {
+            at += 32;
+            left = kPadding;
+            break;
+        }
     }
     __syncwarp();
-    return min(n, kKvBlockTokens);
+    n = min(n, kKvBlockTokens);
+    return left;
 }
 
 // A run of a CTA: its slot, its first tokens, and where it goes on (-1: it does not).
@@ -177,7 +212,8 @@ __global__ void __launch_bounds__(kKv8Threads, sizeof(T) == 2 ? 4 : 2) kv8_appen
     constexpr int kHeld = kKvBlockTokens / kRows;       // rows of a lane
     __shared__ int64_t slots[kKv8Span + kKvBlockTokens];
     __shared__ Kv8Run runs[kKv8Span];
-    __shared__ int firsts[kKv8Span], count;
+    __shared__ int firsts[kKv8Span], count, nearest;
+    __shared__ int64_t before, behind;  // where the whole CTA looks for the slot before its own, and for more of its last run; -1: nowhere
     __shared__ int32_t again[kKv8Threads / 32][kKvBlockTokens];  // tokens behind a run's first 16
     const rra_kv_tokens_args_t& a = p.a;
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -186,37 +222,60 @@ __global__ void __launch_bounds__(kKv8Threads, sizeof(T) == 2 ? 4 : 2) kv8_appen
     pdl_release_early();
     pdl_wait();
     // ---- the runs that begin among this CTA's tokens ----
-    if (warp == 0) {
-        const int64_t slot = t0 + lane < a.tokens ? a.slots[t0 + lane] : -1;
-        int64_t s = t0 - 32 + lane >= 0 ? a.slots[t0 - 32 + lane] : -1;
-        slots[lane] = slot;
+    auto begin = [&](int64_t earlier) {  // warp 0; earlier: the slot before them, not counting those that are skipped; -1: none
+        const int64_t slot = slots[lane];
         const bool inside = (uint64_t)slot < (uint64_t)p.room;
-        // the slot before, not counting those that are skipped; -1: none
-        const uint32_t valid = __ballot_sync(0xffffffffu, inside), lower = valid & ((1u << lane) - 1u);
+        const uint32_t lower = __ballot_sync(0xffffffffu, inside) & ((1u << lane) - 1u);
         int64_t left = __shfl_sync(0xffffffffu, slot, 31 - __clz((int)(lower | 1u)));
-        int64_t earlier = -1;
-        for (int64_t t = t0 - 32; valid != 0u; t -= 32) {
-            const uint32_t there = __ballot_sync(0xffffffffu, (uint64_t)s < (uint64_t)p.room);
-            earlier = there != 0u ? __shfl_sync(0xffffffffu, s, 31 - __clz((int)there)) : -1;
-            if (there != 0u || t <= 0) break;
-            s = t - 32 + lane >= 0 ? a.slots[t - 32 + lane] : -1;
-        }
         if (lower == 0u) left = earlier;
         const bool begins = lane < p.span && inside && (left < 0 || left >> 4 != slot >> 4);
         const uint32_t who = __ballot_sync(0xffffffffu, begins);
         if (begins) firsts[__popc(who & ((1u << lane) - 1u))] = lane;
         if (lane == 0) count = __popc(who);
+    };
+    if (warp == 0) {
+        const int64_t slot = t0 + lane < a.tokens ? a.slots[t0 + lane] : -1;
+        const int64_t s = t0 - 32 + lane >= 0 ? a.slots[t0 - 32 + lane] : -1;
+        slots[lane] = slot;
+        __syncwarp();
+        const bool inside = (uint64_t)slot < (uint64_t)p.room;
+        const uint32_t there = __ballot_sync(0xffffffffu, (uint64_t)s < (uint64_t)p.room);
+        const bool open = __any_sync(0xffffffffu, inside) && there == 0u && t0 > 32;  // what comes before is further back
+        if (!open) begin(there != 0u ? __shfl_sync(0xffffffffu, s, 31 - __clz((int)there)) : -1);
+        if (lane == 0) before = open ? t0 - 33 : -1, behind = -1;
     }
     __syncthreads();
-    for (int r = warp; r < count; r += kKv8Threads / 32) {
+    if (before >= 0) {
+        const int64_t at = kv8_find<-1>(p, before, &nearest);
+        if (warp == 0) begin(at >= 0 ? a.slots[at] : -1);
+        __syncthreads();
+    }
+    // Of run r, its tokens: those that it has, and those from `at` on.
+    auto gather = [&](int r, int64_t at) {
         Kv8Run& run = runs[r];
-        int64_t at = t0 + firsts[r];
-        bool more;
-        const int n = kv8_gather(p, at, more, run.picks, slots, t0);
+        int n = run.length;
+        const Kv8Left left = kv8_gather<true>(p, at, n, run.picks, slots, t0);
         const uint32_t row = lane < n ? 1u << (run.picks[lane] & (kKvBlockTokens - 1)) : 0u, rows = __reduce_or_sync(0xffffffffu, row);
-        if (lane == 0) run.slot = slots[firsts[r]], run.more = more ? at : -1, run.length = n, run.rows = rows;
+        if (lane == 0) {
+            run.more = left == kMore ? at : -1, run.length = n, run.rows = rows;
+            if (r == count - 1) behind = left == kPadding ? at : -1;  // others have ended
+        }
+    };
+    for (int r = warp; r < count; r += kKv8Threads / 32) {
+        if (lane == 0) runs[r].slot = slots[firsts[r]], runs[r].length = 0;
+        __syncwarp();
+        gather(r, t0 + firsts[r]);
     }
     __syncthreads();
+    while (behind >= 0) {
+        const int64_t at = kv8_find<1>(p, behind, &nearest);
+        __syncthreads();
+        if (warp == 0) {
+            if (at >= 0 && a.slots[at] >> 4 == runs[count - 1].slot >> 4) gather(count - 1, at);
+            else if (lane == 0) behind = -1;
+        }
+        __syncthreads();
+    }
     const int sub = lane / kLanes, m = lane % kLanes;  // this lane's row of those that the warp takes at once, and its eight channels
     const int items = count * heads * 2;
     for (int item = warp; item < items; item += kKv8Threads / 32) {
@@ -261,7 +320,8 @@ __global__ void __launch_bounds__(kKv8Threads, sizeof(T) == 2 ? 4 : 2) kv8_appen
         if (run.more >= 0) {  // all others are looked at before any is written
             int64_t at = run.more;
             for (bool more = true; more;) {
-                const int n = kv8_gather(p, at, more, again[warp], slots, t0);
+                int n = 0;
+                more = kv8_gather<false>(p, at, n, again[warp], slots, t0) == kMore;
                 anew |= __any_sync(0xffffffffu, lane < n && (again[warp][lane & 15] & 15) == 0);
                 take(again[warp], n);
                 most = fmaxf(most, most_of());
@@ -294,7 +354,8 @@ __global__ void __launch_bounds__(kKv8Threads, sizeof(T) == 2 ? 4 : 2) kv8_appen
         if (run.more >= 0) {
             int64_t at = run.more;
             for (bool more = true; more;) {
-                const int n = kv8_gather(p, at, more, again[warp], slots, t0);
+                int n = 0;
+                more = kv8_gather<false>(p, at, n, again[warp], slots, t0) == kMore;
                 take(again[warp], n);
                 most_of();
                 put(again[warp], n);
