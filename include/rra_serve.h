@@ -287,9 +287,10 @@ rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const ch
  * at a block's start begins it anew: what it held before goes.  Writing others
  * keeps what is there and can only raise the exponent; the codes that are there
  * are then rounded again, to the new unit (a power of two: only those that get
- * below 2^-6 of it lose bits, at most 2^-10 of it each time).  So a value is within
- * 2^-4 of itself, or 2^-10 * 2^e for each write that raised e.  NaN is stored as 0;
- * infinities as the largest code, and do not count for the exponent.
+ * below 2^-6 of it lose bits, at most 2^-10 of it each time).  So a value x, up to
+ * 448 * 2^32, is off by at most 2^-4 |x| + 2^-9 * 2^e, with the e that its block has
+ * now: half a step of its code, and 2^-10 of each unit that the block has had.  NaN
+ * is stored as 0; infinities as the largest code, and do not count for the exponent.
  *
  * rra_kv8_append: slots of one block are neighbours in the list, in any order, as
  * rra_slot_map gives them (slots outside the cache are skipped and do not come
