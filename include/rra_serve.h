@@ -319,7 +319,9 @@ rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const c
  * products, the softmax's maximum, sum and weights are binary32; for the sum over
  * values a weight is rounded to the values' type (bfloat16, 8 bits; binary16, 11 bits,
  * times 2^7 against its underflow), out to it once.  Results do not depend on timing.
- *   An infinity or NaN makes the rows that see its token infinite or NaN, no others.
+ *   A NaN, or an infinite value, makes the rows that see its token NaN or infinite, no
+ *   others.  Infinite queries and keys make infinite scores: +inf makes its row NaN or
+ *   infinite; -inf has weight 0, and a row with no other scores sees no key.
  *   q, out [tokens][q_heads][head_dim], k, v [tokens][kv_heads][head_dim], all
  *   bfloat16, or binary16 (`half`); strides in elements, multiples of 8, below 2^39;
  *   channels adjacent; pointers 16-byte aligned; out overlaps nothing.  They may be

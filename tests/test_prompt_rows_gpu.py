@@ -64,3 +64,31 @@ def test_a_neighbours_queries_change_no_bit(serve, hq, hk, d, window, max_len, d
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
     assert prompts.status() == 0
+
+
+@pytest.mark.parametrize("max_len", [1, 10 ** 6])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("token", [0, 150, 333])
+@pytest.mark.parametrize("what", ["key", "query"])
+def test_keys_and_queries_that_are_infinite(serve, what, token, sign, max_len):
+    """A score of +inf makes its row NaN or infinite; one of -inf has weight 0; a row with no other scores is one that sees no key."""
+    n, d = 400, 64
+    q, k, v = qkv(n, 2, 1, d, torch.bfloat16, 3)
+    prompts, cu = serve.PromptAttention(), i32([0, n])
+    (q if what == "query" else k)[token, :, 5] = sign * float("inf")
+    out, lse = torch.empty_like(q), torch.empty(n, 2, device="cuda")
+    prompts.attention(q, k, v, out, cu, max_len=max_len, lse=lse)
+    assert prompts.status() == 0
+    s = (q[:, :, None].double() * k[:, 0].double()).sum(-1).transpose(0, 1) / d ** 0.5  # [heads, queries, keys]
+    s = s.masked_fill(torch.ones(n, n, device="cuda", dtype=torch.bool).triu(1), float("-inf"))
+    high, none = (s == float("inf")).any(-1).T, (s == float("-inf")).all(-1).T
+    assert (high | none).any()
+    assert not torch.isfinite(out[high]).any() and not torch.isfinite(lse[high]).any()
+    assert (out[none] == 0).all() and (lse[none] == float("-inf")).all()
+    fine = ~(high | none)
+    want = torch.einsum("hij,jd->ihd", s.softmax(-1), v[:, 0].double())[fine]
+    mean = torch.einsum("hij,jd->ihd", s.softmax(-1), v[:, 0].double().abs())[fine]
+    # a weight, and the result, to bfloat16; a score is a sum of 64 products below 20 in binary32, times 1/8: off by
+    # 64 * 2 * 2^-24 * 64 * 20 / 8 = 1.2e-3 if all of them were, and were rounded the same way
+    assert ((out[fine].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1.01 * (2.0 ** -8 + 2.4e-3) * mean).all()
+    assert ((lse.double() - s.logsumexp(-1).T)[fine].abs() <= 1.3e-3).all()
