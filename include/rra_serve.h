@@ -301,7 +301,8 @@ rra_status_t rra_kv_attention_plan(const rra_kv_attention_args_t* args, const ch
  * and exponent enters exactly.  Codes are binary16 in the products, weights too:
  * off by 2^-11 of themselves, or where they are small by 2^-24 of the largest; so
  * a key adds an error of 2^-24 of its value at most, whatever the exponents of other
- * blocks, and of values that a row does not see.  The workspace is the same. */
+ * blocks, and of values that a row does not see.  Scores are below 2^26, as in
+ * rra_prompt_attention.  The workspace is the same. */
 size_t rra_kv8_page_bytes(int page_tokens, int kv_heads, int head_dim);
 rra_status_t rra_kv8_append(const rra_kv_tokens_args_t* args, rra_stream_t stream);
 rra_status_t rra_kv8_read(const rra_kv_tokens_args_t* args, rra_stream_t stream);
@@ -319,6 +320,8 @@ rra_status_t rra_kv8_attention_plan(const rra_kv_attention_args_t* args, const c
  * products, the softmax's maximum, sum and weights are binary32; for the sum over
  * values a weight is rounded to the values' type (bfloat16, 8 bits; binary16, 11 bits,
  * times 2^7 against its underflow), out to it once.  Results do not depend on timing.
+ * Scores, times log2(e), are below 2^26: where binary32 has no bits left for their
+ * differences, above that, rows may become NaN.
  *   A NaN, or an infinite value, makes the rows that see its token NaN or infinite, no
  *   others.  Infinite queries and keys make infinite scores: +inf makes its row NaN or
  *   infinite; -inf has weight 0, and a row with no other scores sees no key.
@@ -346,7 +349,7 @@ typedef struct {
     int64_t v_token_stride, v_head_stride;
     int64_t out_token_stride, out_head_stride;
     int64_t tokens;             /* rows of q, k, v and out */
-    double scale;               /* usually 1 / sqrt(head_dim); times log2(e) finite in binary32, as scores are */
+    double scale;               /* usually 1 / sqrt(head_dim); times log2(e) finite in binary32 */
     int32_t requests;
     int32_t q_heads, kv_heads;
     int32_t head_dim;

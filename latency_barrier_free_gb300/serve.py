@@ -214,7 +214,7 @@ class PromptAttention(_Workspace):
         b has the tokens cu[b]..cu[b+1] (int32) of all of them, each of which sees the
         prompt's tokens up to itself (all of them, unless `causal`), the last `window`
         of them if that is not 0.  max_len is what to plan for; scale defaults to
-        1/sqrt(head_dim).  lse: float32 [tokens, q_heads], optional.  Rows of out and lse
+        1/sqrt(head_dim); scores are below 2^26.  lse: float32 [tokens, q_heads], optional.  Rows of out and lse
         after cu[-1], a step's padding, stay as they are."""
         st = _native.prompt_attention(self._dev, self._workspace, q, k, v, out, cu, max_len, scale, causal, window, lse, stream,
                                       self._home)
@@ -338,7 +338,7 @@ class KvCache8(KvCache):
 
     def attention(self, q, out, cu_q, kv_len, block_table, *, max_q: int, max_kv: int, scale=None, causal: bool = True,
                   window: int = 0, lse=None, stream=None) -> None:
-        """As KvCache.attention, over this cache (rra_kv8_attention)."""
+        """As KvCache.attention, over this cache (rra_kv8_attention); scores are below 2^26."""
         st = _native.kv8_attention(self._cache, self._dev, self._workspace, q, out, cu_q, kv_len, block_table, max_q, max_kv,
                                    self._scale if scale is None else scale, causal, window, lse, stream, self._home)
         if st:
