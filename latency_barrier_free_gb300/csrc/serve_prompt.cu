@@ -28,9 +28,9 @@
 // of key tiles, one per CTA (serve_tc.cuh); what a run has of a segment it shares
 // goes to the workspace, and the last CTA to arrive adds the parts in order.
 //
-// 64 heads over 8 of 128, bfloat16, two prompts of up to 8192 tokens, 1.1 TFLOP:
-// 770 us among other calls, 1430 TFLOP/s, at the power limit; 8 over 1, one of 16384
-// 358 us, 1535 TFLOP/s (large library products reach 1937).  The products of 256 rows
+// 64 heads over 8 of 128, bfloat16, prompts of 8192 and 78 tokens, 1.1 TFLOP:
+// 775 us among other calls, 1420 TFLOP/s, at the power limit; 8 over 1, one of 16384
+// 359 us, 1530 TFLOP/s (large library products reach 1937).  The products of 256 rows
 // and 128 keys take 2080 cycles at their full rate; the pipe is 55 to 70 % busy.  The
 // rest is the chain of one tile, scores to weights (about 1000 cycles) and its two
 // products, where the other tile's products do not cover it.  Few short ones are
@@ -491,10 +491,11 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             const int edge_from = edge_of(seg).from, edge_to = edge_of(seg).to, first_tile = seg.first_tile;
             // What a row's weights are taken against, in units of log2 (kNone: it has seen no key yet), and their sum.
             // Rows that are no rows (behind the group's heads or the prompt's tokens: what memory or the next prompt has there) have
-            // no say in the votes below, which change the others' roundings.
+            // no say in the votes below, which change the others' roundings.  (28 heads over 4, one prompt of 2000: 39.6 us with,
+            // 36.2 without their maxima.)
             constexpr float kNone = -FLT_MAX;
-            const bool votes[2] = {is_live(0), is_live(1)};
-            float top[2] = {votes[0] ? kNone : 0.f, votes[1] ? kNone : 0.f}, less[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // less: what is taken off scores
+            const bool live[2] = {is_live(0), is_live(1)};
+            float top[2] = {kNone, kNone}, less[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // less: what is taken off scores
             bool fresh = true;  // some row has none
 #pragma unroll 1
             for (int tl = t0; tl < t1; ++tl, ++n) {
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                             split2(sum[r], a0, a1);
                             all[r] = a0 + a1;
                         }
-                        if (exact || !__any_sync(0xffffffffu, (votes[0] && all[0] > Sh::kMost) || (votes[1] && all[1] > Sh::kMost))) break;
+                        if (exact || !__any_sync(0xffffffffu, (live[0] ? all[0] : 0.f) > Sh::kMost || (live[1] ? all[1] : 0.f) > Sh::kMost)) break;
                         exact = true;
                     }
                     l[0] += all[0];
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
                     mbar_arrive((q == 0 ? pv_half : pv_full) + 8 * i);
                 }
                 if (!ok) break;
-                if (fresh) fresh = __any_sync(0xffffffffu, top[0] == kNone || top[1] == kNone);
+                if (fresh) fresh = __any_sync(0xffffffffu, (live[0] && top[0] == kNone) || (live[1] && top[1] == kNone));
             }
             bool lost = false;
             if (ok && t0 < t1) {
@@ -616,7 +617,6 @@ __global__ void __launch_bounds__(WholeShape<T, D, TILES>::kThreads, 1) prompt_a
             const int kv_head = p.by_parts(seg.h), head0 = (seg.h - kv_head * p.parts) * p.group;  // of the KV head's query heads
             const PromptEdge edge = {edge_from, edge_to};
             const int token[2] = {token_of(0), token_of(1)}, lo[2] = {lo_of(0), lo_of(1)}, hi[2] = {hi_of(0), hi_of(1)};
-            const bool live[2] = {is_live(0), is_live(1)};
             T* out[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
