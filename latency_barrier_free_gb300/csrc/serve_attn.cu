@@ -18,7 +18,7 @@
 // 44.9 us (3.9 TB/s).  Half the instructions are the unpacking of codes, and the
 // ALU pipe is half busy; four schedulers need the three warps each.
 //
-// Over the 8-bit cache 64 ragged requests, 312 MB, take 58.9 us (5.3 TB/s): 5 us to the
+// Over the 8-bit cache 64 ragged requests, 312 MB, take 59.4 us (5.3 TB/s): 5 us to the
 // first copy, 46 of stream at 6.8 TB/s, the copy's own rate, and 6 to 8 of joins.
 #include <algorithm>
 #include <cmath>

@@ -10,7 +10,7 @@
 //     w = 2^((s - m) factor + xv - x),
 // with m the maximum and x an exponent for the sums; the softmax's own sum gets
 // 2^(x - xv) of a block's weights, in binary32.  For w to be in binary16's range x
-// becomes xv where that is larger, and also where it is smaller by kKv8Apart or more:
+// becomes xv where that is larger, and also where it is smaller by more than kKv8Apart:
 // a block's exponent may be that of values which a row does not see, or of other
 // channels, and must not cost what the row does see its bits.  The sums, in binary32,
 // have room for all exponents at once.

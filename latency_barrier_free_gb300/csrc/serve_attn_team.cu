@@ -9,7 +9,7 @@
 // remains is lengths, page numbers, pages: three round trips, one after another.
 // 8 heads over 1 of 128: 2000 keys in 5.6 us (the other kernel: 9.7).  24
 // requests of up to 5 queries, 14 heads over 2 of 64, a window of 1000: 10.8 us.
-// Over the 8-bit cache: 8 heads over 1 of 128, 2000 keys, 5.5 us.
+// Over the 8-bit cache: 8 heads over 1 of 128, 2000 keys, 5.4 us.
 #include "serve_attn_rows8.cuh"
 
 namespace rra {

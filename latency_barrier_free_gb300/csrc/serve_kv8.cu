@@ -8,9 +8,10 @@
 //
 // Read.  A thread takes 8 channels of a row of K, and of V (16: 11.0 us against 7.9 for 8754 tokens of 8 heads of 128).
 //
-// Four prompts, 8754 tokens of 8 heads of 128, bfloat16, 108 MB: 22.5 us for both, 4.8 TB/s; the write 13.3 and the read
-// 7.8 us alone.  The read is at HBM's rate.  The write is bound by the chain list of tokens, slots, values, maximum, codes:
-// a third of the warps wait for memory, a fifth for the list.  One token for each request, 16: 4.4 us, launches and round trips.
+// Four prompts, 8754 tokens of 8 heads of 128, bfloat16, 108 MB: 23.1 us for both, 4.7 TB/s, over three sets of buffers in
+// turn; the write 13.9 and the read 11.1 us alone (7.8 where it finds the pages in L2).  The read waits for memory.  The write is
+// bound by the chain list of tokens, slots, values, maximum, codes: a third of the warps wait for memory, a fifth for the list.
+// One token for each request, 16: 4.5 us, launches and round trips.
 // Of a step of 8192 slots 16 that are not padding: the write takes 25 us, two CTAs having them all (of 16 slots: 3.1).
 #include <algorithm>
 

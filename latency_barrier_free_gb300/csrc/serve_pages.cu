@@ -5,7 +5,7 @@
 // cluster, whose barriers separate what is read from what is written to the same
 // buffers, and whose CTAs share rows and pages.  The copies are bound by HBM.
 //
-// One prompt into 8 samples 4.8 us with its copies, 32 into 8 each 12.3 (63 MB).  After 500 requests over 8192 pages
+// One prompt into 8 samples 4.8 us with its copies, 32 into 8 each 12.3 (63 MB).  After 500 requests over 22773 pages
 // release takes 12.0 us, compaction 13.0, the copies of 5620 pages of 33 KB 58 (6.4 TB/s); after 9 requests 3.8, 5.3 and 1.5.
 #include <algorithm>
 
