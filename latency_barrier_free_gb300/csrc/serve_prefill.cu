@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(PromptShape<F, D, TILES>::kThreads, 1) kv_atte
                             if (exact && __any_sync(0xffffffffu, ex[0].w != 0.f)) {  // units that are far apart
                                 float unit = next_unit(ex, INFINITY);
                                 uint32_t to = pv_full;
+                                tc_wait_st();  // of the weights that led here
 #pragma unroll 1
                                 while (true) {
                                     auto takes = [&](int b) { return ex[b].y <= unit && ex[b].y >= unit - kKv8Apart; };
